@@ -83,9 +83,10 @@ enum {
   DA_DEV_BAD_QPOS = 4,       /* q_pos[b] < 0: the row is written as empty (out 0, lse -inf)   */
   DA_DEV_SPLIT_OVERFLOW = 8, /* split_partial: keys past max_splits*split_tokens were dropped  */
   DA_DEV_BAD_TIER = 16,      /* tiered: hot_len > ring capacity or negative tier length        */
-  DA_DEV_TIMEOUT = 32        /* an internal pipeline wait ran past its time limit (never      */
+  DA_DEV_TIMEOUT = 32,       /* an internal pipeline wait ran past its time limit (never      */
                              /* expected; 2 s, or DA_WAIT_LIMIT_MS): the kernel then ends     */
                              /* without waiting further and its outputs are undefined          */
+  DA_DEV_BAD_SEQ = 64        /* append_paged_rope: token_seq[n] >= batch: the token is dropped */
 };
 
 typedef struct {
@@ -319,6 +320,127 @@ int decode_attn_append_tiered_f16(const da_params* p, int32_t hot_window, int32_
                                   const int32_t* block_table, int32_t* cold_lens,
                                   int32_t* hot_lens, int32_t* hot_starts, int32_t* dev_status,
                                   void* stream);
+
+/*
+ * Per-head RMS norm and position rotation of new queries and keys
+ * (decode_attn_qk_norm_rope, decode_attn_append_paged_rope).  For the row x
+ * (D values) of one token and head:
+ *   norm = 1:  y_d = x_d * (weight_d + weight_offset) / sqrt(mean(x^2) + eps)
+ *              (a NULL weight stands for ones, weight_offset then unused)
+ *   norm = 0:  y = x
+ *   rotation:  for pair i < rotary_dim / 2, with the angle a = position *
+ *              freqs[i] / 2^64 turns,
+ *                z_lo = y_lo cos a - y_hi sin a,  z_hi = y_lo sin a + y_hi cos a
+ *              where (lo, hi) = (i, i + rotary_dim / 2), or (2i, 2i + 1) when
+ *              interleaved; the values from rotary_dim on are not rotated.
+ * The frequencies are turns per position in 64-bit fixed point
+ * (decode_attn_rope_freqs): position * freqs[i] modulo 2^64 drops whole turns
+ * exactly, so the angle of a position of any size, also a negative one, is as
+ * good as that of a small one.  All arithmetic is f32; the only rounding to
+ * fewer bits is the last one, of keys and values to the cache's f16 (to
+ * nearest even, beyond its range to infinity).
+ * Rows may be slices of a larger tensor: token n, head h of q starts at
+ * element n * q_token_stride + h * q_head_stride (k and v alike); its D
+ * values are contiguous.  Every row must start on a 16-byte boundary.
+ */
+enum { DA_TYPE_F32 = 0, DA_TYPE_F16 = 1, DA_TYPE_BF16 = 2 };
+
+typedef struct {
+  int32_t type;           /* DA_TYPE_* of q, k and v                                     */
+  int32_t rotary_dim;     /* values of a head that are rotated: 0 (none) or a multiple of
+                             16 up to head_dim                                           */
+  int32_t interleaved;    /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1)     */
+  int32_t norm;           /* 1: RMS norm of every q and k head before the rotation       */
+  float eps;              /* >= 0                                                        */
+  float weight_offset;    /* added to the weights (1 for weights kept around zero)       */
+  int64_t q_token_stride, q_head_stride; /* elements, >= 0                               */
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride; /* append only                                  */
+  const uint64_t* freqs;  /* [rotary_dim / 2] device; may be NULL when rotary_dim is 0   */
+  const float* q_weight;  /* [head_dim] device or NULL; read when norm is 1              */
+  const float* k_weight;  /* [head_dim] device or NULL; read when norm is 1              */
+} da_rope_params;
+
+/*
+ * decode_attn_rope_freqs — host function: fills freqs[0 .. rotary_dim/2) with
+ * inv_freq[i] / (2 pi) turns in units of 2^-64, rounded to nearest; inv_freq
+ * (HOST, radians per position, finite) or, when NULL, theta^(-2i/rotary_dim)
+ * with theta > 0.  The caller copies them to the device.
+ */
+int decode_attn_rope_freqs(int32_t rotary_dim, double theta, const double* inv_freq,
+                           uint64_t* freqs);
+
+/*
+ * decode_attn_qk_norm_rope — norm and rotation of the queries and keys of
+ * num_tokens tokens in one pass, to the types the decode and append calls
+ * take:
+ *   q [N, Hq, D], k [N, Hkv, D] of r->type (strided rows; either may be NULL)
+ *   positions i32 [N] (may be NULL when rotary_dim is 0)
+ *   q_out f32 [N, Hq, D], k_out f16 [N, Hkv, D] (contiguous)
+ * q_out may be q and k_out may be k when type and layout agree; other
+ * overlaps are not allowed.  head_dim in {64, 128, 256}.
+ */
+int decode_attn_qk_norm_rope(const da_rope_params* r, int32_t num_tokens, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, const void* q, const void* k,
+                             const int32_t* positions, float* q_out, uint16_t* k_out,
+                             void* stream);
+
+/*
+ * decode_attn_append_paged_rope — appends the keys and values of num_tokens
+ * tokens to the paged cache, the keys normed and rotated on the way, and
+ * norms and rotates the tokens' queries in the same launch when q is given.
+ * The tokens may belong to any sequences, any number to each (a decode step,
+ * drafted tokens, a ragged prefill):
+ *   token_seq i32 [N]: the sequence (row of block_table) of each token; a
+ *              negative entry is a padding token, for which nothing is written.
+ *              NULL: token n is sequence n (num_tokens must equal p->batch).
+ *   positions i32 [N]: the angle's position, and the cache slot: page
+ *              block_table[seq][pos / block_size], row pos % block_size
+ *   k_new, v_new [N, Hkv, D], q [N, Hq, D] (or NULL) of r->type
+ *   q_out f32 [N, Hq, D] contiguous (NULL exactly when q is)
+ * A position outside [0, max_blocks_per_seq * block_size) sets
+ * DA_DEV_BAD_SEQ_LEN, a page id outside [0, num_blocks) DA_DEV_BAD_BLOCK, a
+ * token_seq >= batch DA_DEV_BAD_SEQ: such a token writes no cache row (its
+ * query is still written).  No two tokens of a call may name the same slot.
+ * Uses batch, num_q_heads (with q), num_kv_heads, head_dim, block_size,
+ * max_blocks_per_seq and num_blocks of p.
+ */
+int decode_attn_append_paged_rope(const da_params* p, const da_rope_params* r, int32_t num_tokens,
+                                  const void* q, const void* k_new, const void* v_new,
+                                  const int32_t* positions, const int32_t* token_seq,
+                                  const int32_t* block_table, float* q_out, uint16_t* k_pool,
+                                  uint16_t* v_pool, int32_t* dev_status, void* stream);
+
+/*
+ * decode_attn_paged_prefix — decode_attn_paged / decode_attn_paged_multi for a
+ * batch whose sequences share the pages of a common prefix: the shared keys
+ * are read once for the whole batch instead of once per sequence.
+ *   prefix_len: keys of the common prefix, 0 <= prefix_len <=
+ *               max_blocks_per_seq * block_size.  Sharing is by whole pages: the first
+ *               prefix_len / block_size columns of every block_table row are
+ *               not read, their pages come from prefix_table.
+ *   prefix_table i32 [prefix_len / block_size] device (row 0 of block_table
+ *               when that row holds the prefix); may be NULL when it is empty
+ *   q_len = T >= 1 query tokens per sequence: q f32 [B, T, Hq, D], out f32
+ *               [B, T, Hq, D], lse f32 [B, T, Hq] or NULL
+ * seq_lens and q_pos count from the start of the prefix, as for the calls
+ * above, and every mask applies over the whole sequence: a sequence may be
+ * shorter than the prefix, or empty, and a sliding window may cut into the
+ * prefix or end after it.  The result is that of decode_attn_paged_multi on
+ * a table whose rows all start with prefix_table.
+ * workspace: device scratch of at least
+ * decode_attn_paged_prefix_workspace_size(p, q_len, prefix_len) bytes, 256-byte
+ * aligned, of any content; calls that overlap on the GPU must not share it.
+ * Everything else as for decode_attn_paged.
+ */
+size_t decode_attn_paged_prefix_workspace_size(const da_params* p, int32_t q_len,
+                                               int32_t prefix_len);
+int decode_attn_paged_prefix(const da_params* p, int32_t q_len, int32_t prefix_len,
+                             const int32_t* prefix_table, const float* q, const uint16_t* k_pool,
+                             const uint16_t* v_pool, const int32_t* block_table,
+                             const int32_t* seq_lens, const int32_t* q_pos, float* out,
+                             float* lse, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream);
 
 /*
  * decode_attn_split_partial — first half of flash-decoding: split s covers

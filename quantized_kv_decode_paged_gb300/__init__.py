@@ -25,9 +25,11 @@ __all__ = [
     "decode_attn_tiered_int8", "decode_attn_tiered_f16", "decode_attn_split_partial",
     "decode_attn_split_merge", "decode_attn_workspace_size", "decode_attn_status_string",
     "decode_attn_paged_static_ws", "decode_attn_append_paged", "decode_attn_append_tiered_int8",
-    "decode_attn_append_tiered_f16", "DecodeAttnError", "DaTuning", "get_tuning", "set_tuning",
-    "tuning", "DEV_BAD_BLOCK", "DEV_BAD_SEQ_LEN",
-    "DEV_BAD_QPOS", "DEV_SPLIT_OVERFLOW", "DEV_BAD_TIER", "DEV_TIMEOUT",
+    "decode_attn_append_tiered_f16", "decode_attn_rope_freqs", "decode_attn_qk_norm_rope",
+    "decode_attn_append_paged_rope", "decode_attn_paged_prefix",
+    "decode_attn_paged_prefix_workspace_size", "DecodeAttnError", "DaTuning", "get_tuning",
+    "set_tuning", "tuning", "DEV_BAD_BLOCK", "DEV_BAD_SEQ_LEN",
+    "DEV_BAD_QPOS", "DEV_SPLIT_OVERFLOW", "DEV_BAD_TIER", "DEV_TIMEOUT", "DEV_BAD_SEQ",
 ]
 
 DEV_BAD_BLOCK = 1
@@ -36,6 +38,7 @@ DEV_BAD_QPOS = 4
 DEV_SPLIT_OVERFLOW = 8
 DEV_BAD_TIER = 16
 DEV_TIMEOUT = 32
+DEV_BAD_SEQ = 64
 
 DA_OK = 0
 DA_ERR_INVALID = -1
@@ -48,8 +51,9 @@ _EXPORTS = (
     "decode_attn_split_partial",
     "decode_attn_split_merge", "decode_attn_workspace_size", "decode_attn_workspace_init",
     "decode_attn_status_string", "decode_attn_paged_static_ws", "decode_attn_append_paged",
-    "decode_attn_append_tiered_int8", "decode_attn_append_tiered_f16", "decode_attn_get_tuning",
-    "decode_attn_set_tuning", "decode_attn_testing_skip_first_arm",
+    "decode_attn_append_tiered_int8", "decode_attn_append_tiered_f16", "decode_attn_rope_freqs",
+    "decode_attn_qk_norm_rope", "decode_attn_append_paged_rope", "decode_attn_paged_prefix",
+    "decode_attn_paged_prefix_workspace_size", "decode_attn_get_tuning", "decode_attn_set_tuning", "decode_attn_testing_skip_first_arm",
 )
 
 
@@ -85,6 +89,18 @@ class DaSparseLayout(ctypes.Structure):
         ("sparse_block", ctypes.c_int32), ("num_layouts", ctypes.c_int32),
         ("num_rows", ctypes.c_int32), ("max_nnz", ctypes.c_int32),
         ("row_ptr", ctypes.c_void_p), ("col_idx", ctypes.c_void_p),
+    ]
+
+
+class DaRopeParams(ctypes.Structure):
+    _fields_ = [
+        ("type", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("norm", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+        ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("freqs", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
     ]
 
 
@@ -161,6 +177,20 @@ def load_library():
         lib.decode_attn_append_tiered_f16.restype = ctypes.c_int
         lib.decode_attn_append_tiered_f16.argtypes = ([ctypes.POINTER(DaParams), i32, i32]
                                                       + [P] * 12)
+        lib.decode_attn_rope_freqs.restype = ctypes.c_int
+        lib.decode_attn_rope_freqs.argtypes = [i32, ctypes.c_double, P, P]
+        lib.decode_attn_qk_norm_rope.restype = ctypes.c_int
+        lib.decode_attn_qk_norm_rope.argtypes = ([ctypes.POINTER(DaRopeParams)] + [i32] * 4
+                                                 + [P] * 6)
+        lib.decode_attn_append_paged_rope.restype = ctypes.c_int
+        lib.decode_attn_append_paged_rope.argtypes = ([ctypes.POINTER(DaParams),
+                                                       ctypes.POINTER(DaRopeParams), i32]
+                                                      + [P] * 11)
+        lib.decode_attn_paged_prefix_workspace_size.restype = ctypes.c_size_t
+        lib.decode_attn_paged_prefix_workspace_size.argtypes = [ctypes.POINTER(DaParams), i32, i32]
+        lib.decode_attn_paged_prefix.restype = ctypes.c_int
+        lib.decode_attn_paged_prefix.argtypes = ([ctypes.POINTER(DaParams), i32, i32] + [P] * 10
+                                                 + [ctypes.c_size_t, P, P])
         lib.decode_attn_get_tuning.restype = ctypes.c_int
         lib.decode_attn_get_tuning.argtypes = [ctypes.POINTER(DaTuning)]
         lib.decode_attn_set_tuning.restype = ctypes.c_int
@@ -703,3 +733,307 @@ def decode_attn_append_tiered_f16(k_new, v_new, k_hot, v_hot, k_cold, v_cold, bl
         _ptr(k_hot), _ptr(v_hot), _ptr(k_cold), _ptr(v_cold), _ptr(block_table),
         _ptr(cold_lens), _ptr(hot_lens), _ptr(hot_starts), _ptr(dev_status), _stream(dev, stream))
     _check("decode_attn_append_tiered_f16", st)
+
+
+# ---------------------------------------------------------------------------
+# norm, rotation and append of a step's new rows
+# ---------------------------------------------------------------------------
+
+def _check_cuda(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
+
+
+class _on_device:
+    """Makes ``dev`` the current CUDA device for a call when it is not."""
+
+    def __init__(self, dev):
+        self.guard = None
+        torch = _torch()
+        if dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def decode_attn_rope_freqs(rotary_dim, theta=10000.0, *, inv_freq=None, device="cuda"):
+    """Rotation frequencies for the calls below: int64 [rotary_dim / 2], turns
+    per position in units of 2^-64, of inv_freq (radians per position, any
+    sequence of numbers) or theta^(-2i / rotary_dim)."""
+    torch = _torch()
+    n = int(rotary_dim) // 2
+    host = torch.zeros(n, dtype=torch.int64)
+    inv = None
+    if inv_freq is not None:
+        inv = torch.as_tensor(inv_freq, dtype=torch.float64).detach().cpu().contiguous()
+        if inv.shape != (n,):
+            raise ValueError(f"inv_freq must have {n} values, got shape {tuple(inv.shape)}")
+    st = load_library().decode_attn_rope_freqs(int(rotary_dim), float(theta), _ptr(inv),
+                                               _ptr(host))
+    _check("decode_attn_rope_freqs", st)
+    return host.to(device)
+
+
+def _rope_types(torch):
+    return {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _req_rows(t, name, dtype, device):
+    """A [tokens, heads, D] view whose rows are contiguous; returns its token
+    and head strides (a dimension of one has none)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
+    n, h, d = t.shape
+    ts, hs, ds = t.stride()
+    if ds != 1 and d != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return (ts if n > 1 else 0), (hs if h > 1 else 0)
+
+
+def _rope_params(x, freqs, norm, q_weight, k_weight, weight_offset, eps, interleaved):
+    torch = _torch()
+    types = _rope_types(torch)
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("q and k must be torch.Tensors")
+    if x.dtype not in types:
+        raise TypeError(f"q, k and v must be float32, float16 or bfloat16, got {x.dtype}")
+    dev = x.device
+    r = DaRopeParams()
+    r.type = types[x.dtype]
+    r.interleaved = int(bool(interleaved))
+    r.norm = int(bool(norm))
+    r.eps = float(eps)
+    r.weight_offset = float(weight_offset)
+    if freqs is not None:
+        _req(freqs, "freqs", torch.int64, dev, 1)
+        r.rotary_dim = 2 * freqs.shape[0]
+        r.freqs = freqs.data_ptr()
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if not norm:
+            raise ValueError(f"{name} is given but norm is off")
+        _req(w, name, torch.float32, dev, 1)
+        if w.shape[0] != x.shape[-1]:
+            raise ValueError(f"{name} must have {x.shape[-1]} values, got {w.shape[0]}")
+    r.q_weight = _ptr(q_weight)
+    r.k_weight = _ptr(k_weight)
+    return r
+
+
+def decode_attn_qk_norm_rope(q, k, positions, freqs, *, norm=True, q_weight=None, k_weight=None,
+                             weight_offset=0.0, eps=1e-6, interleaved=False, q_out=None,
+                             k_out=None, stream=None):
+    """RMS norm of every query and key head and the position rotation, in one
+    pass.  q [N, Hq, D], k [N, Hkv, D] (float32, float16 or bfloat16, the same
+    type; slices of a fused projection are fine; either may be None);
+    positions i32 [N]; freqs from decode_attn_rope_freqs, or None for no
+    rotation (positions may then be None).  q_weight / k_weight f32 [D] with
+    ``norm``.  Returns (q_out f32 [N, Hq, D], k_out f16 [N, Hkv, D]): the types
+    that the decode and the append calls take."""
+    torch = _torch()
+    lib = load_library()
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k are both None")
+    r = _rope_params(x, freqs, norm, q_weight, k_weight, weight_offset, eps, interleaved)
+    dev = x.device
+    Hq = Hkv = 0
+    if q is not None:
+        r.q_token_stride, r.q_head_stride = _req_rows(q, "q", x.dtype, dev)
+        Hq = q.shape[1]
+    if k is not None:
+        r.k_token_stride, r.k_head_stride = _req_rows(k, "k", x.dtype, dev)
+        Hkv = k.shape[1]
+    N, _, D = x.shape
+    if k is not None and (k.shape[0] != N or k.shape[2] != D):
+        raise ValueError("inconsistent shapes")
+    if positions is not None:
+        _req(positions, "positions", torch.int32, dev, 1)
+        if positions.shape[0] != N:
+            raise ValueError("inconsistent shapes")
+    elif freqs is not None:
+        raise ValueError("positions are needed for the rotation")
+    for name, t, dt, shape in (("q_out", q_out, torch.float32, (N, Hq, D)),
+                               ("k_out", k_out, torch.float16, (N, Hkv, D))):
+        if t is not None:
+            _req(t, name, dt, dev, 3)
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    _check_cuda("q and k", x)
+    with _on_device(dev):
+        if q is not None and q_out is None:
+            q_out = torch.empty((N, Hq, D), dtype=torch.float32, device=dev)
+        if k is not None and k_out is None:
+            k_out = torch.empty((N, Hkv, D), dtype=torch.float16, device=dev)
+        if N == 0:
+            return q_out, k_out
+        st = lib.decode_attn_qk_norm_rope(ctypes.byref(r), N, Hq, Hkv, D, _ptr(q), _ptr(k),
+                                          _ptr(positions), _ptr(q_out), _ptr(k_out),
+                                          _stream(dev, stream))
+    _check("decode_attn_qk_norm_rope", st)
+    return q_out, k_out
+
+
+def decode_attn_append_paged_rope(k_new, v_new, positions, block_table, k_pool, v_pool, freqs, *,
+                                  token_seq=None, q=None, norm=False, q_weight=None,
+                                  k_weight=None, weight_offset=0.0, eps=1e-6, interleaved=False,
+                                  q_out=None, dev_status=None, stream=None):
+    """Appends k_new / v_new [N, Hkv, D] (float32, float16 or bfloat16, strided
+    rows) to the f16 paged pools in place, the keys normed (with ``norm``) and
+    rotated on the way.  positions i32 [N]; token_seq i32 [N] names each
+    token's row of block_table (negative: padding, nothing is written; None:
+    token n is sequence n).  With q [N, Hq, D] the queries are normed and rotated
+    in the same launch.  Returns q_out f32 [N, Hq, D], or None without q."""
+    torch = _torch()
+    lib = load_library()
+    r = _rope_params(k_new, freqs, norm, q_weight, k_weight, weight_offset, eps, interleaved)
+    dev = k_new.device
+    r.k_token_stride, r.k_head_stride = _req_rows(k_new, "k_new", k_new.dtype, dev)
+    r.v_token_stride, r.v_head_stride = _req_rows(v_new, "v_new", k_new.dtype, dev)
+    _req(positions, "positions", torch.int32, dev, 1)
+    _req(block_table, "block_table", torch.int32, dev, 2)
+    _req(k_pool, "k_pool", torch.float16, dev, 4)
+    _req(v_pool, "v_pool", torch.float16, dev, 4)
+    N, Hkv, D = k_new.shape
+    NB, bs = k_pool.shape[:2]
+    if (v_new.shape != k_new.shape or v_pool.shape != k_pool.shape
+            or k_pool.shape[2:] != k_new.shape[1:] or positions.shape[0] != N):
+        raise ValueError("inconsistent shapes")
+    if token_seq is not None:
+        _req(token_seq, "token_seq", torch.int32, dev, 1)
+        if token_seq.shape[0] != N:
+            raise ValueError("inconsistent shapes")
+    Hq = Hkv
+    if q is not None:
+        r.q_token_stride, r.q_head_stride = _req_rows(q, "q", k_new.dtype, dev)
+        Hq = q.shape[1]
+        if q.shape[0] != N or q.shape[2] != D:
+            raise ValueError("inconsistent shapes")
+        if q_out is not None:
+            _req(q_out, "q_out", torch.float32, dev, 3)
+            if q_out.shape != q.shape:
+                raise ValueError("inconsistent shapes")
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    if dev_status is not None:
+        _req(dev_status, "dev_status", torch.int32, dev)
+    _check_cuda("k_new", k_new)
+    p = DaParams(block_table.shape[0], Hq, Hkv, D, bs, block_table.shape[1], NB, 0, 0.0, 0.0, 0, 1)
+    with _on_device(dev):
+        if q is not None and q_out is None:
+            q_out = torch.empty((N, Hq, D), dtype=torch.float32, device=dev)
+        if N == 0:
+            return q_out
+        st = lib.decode_attn_append_paged_rope(
+            ctypes.byref(p), ctypes.byref(r), N, _ptr(q), _ptr(k_new), _ptr(v_new),
+            _ptr(positions), _ptr(token_seq), _ptr(block_table), _ptr(q_out), _ptr(k_pool),
+            _ptr(v_pool), _ptr(dev_status), _stream(dev, stream))
+    _check("decode_attn_append_paged_rope", st)
+    return q_out
+
+
+# ---------------------------------------------------------------------------
+# a batch that shares a prefix
+# ---------------------------------------------------------------------------
+
+def decode_attn_paged_prefix_workspace_size(params: DaParams, q_len: int, prefix_len: int) -> int:
+    return int(load_library().decode_attn_paged_prefix_workspace_size(ctypes.byref(params),
+                                                                      int(q_len), int(prefix_len)))
+
+
+def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_len,
+                             prefix_table=None, q_pos=None, *, scale=0.0, softcap=0.0,
+                             sliding_window=0, causal=True, max_seq_len=0, out=None, lse=None,
+                             workspace="auto", dev_status=None, stream=None):
+    """decode_attn_paged (q [B, Hq, D]) or decode_attn_paged_multi (q [B, T, Hq,
+    D]) for a batch whose sequences all start with the same prefix_len keys:
+    the shared pages are read once for the batch.  The whole pages of the
+    prefix come from prefix_table (i32 [prefix_len // block_size]; None: the
+    first columns of block_table's row 0); those columns of block_table are not
+    read.  seq_lens and q_pos include the prefix.  Returns (out, lse).
+
+    ``workspace``: "auto" (allocated for the call) or a caller-owned uint8
+    tensor of decode_attn_paged_prefix_workspace_size bytes (any content)."""
+    torch = _torch()
+    lib = load_library()
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be a tensor of 3 or 4 dims")
+    dev = q.device
+    _req(q, "q", torch.float32, dev)
+    _req(k_pool, "k_pool", torch.float16, dev, 4)
+    _req(v_pool, "v_pool", torch.float16, dev, 4)
+    _req(block_table, "block_table", torch.int32, dev, 2)
+    _req(seq_lens, "seq_lens", torch.int32, dev, 1)
+    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
+    T = q.shape[1] if q.dim() == 4 else 1
+    NB, bs, Hkv, D2 = k_pool.shape
+    if (k_pool.shape != v_pool.shape or D2 != D or block_table.shape[0] != B
+            or seq_lens.shape[0] != B):
+        raise ValueError("inconsistent shapes")
+    if q_pos is not None:
+        _req(q_pos, "q_pos", torch.int32, dev, 1)
+        if q_pos.shape[0] != B:
+            raise ValueError("inconsistent shapes")
+    prefix_len = int(prefix_len)
+    pages = prefix_len // bs
+    if prefix_table is None:
+        # row 0 starts the table: its address serves as the prefix's
+        pt = block_table.data_ptr()
+    else:
+        _req(prefix_table, "prefix_table", torch.int32, dev, 1)
+        if prefix_table.shape[0] < pages:
+            raise ValueError(f"prefix_table must have {pages} entries, got "
+                             f"{prefix_table.shape[0]}")
+        pt = prefix_table.data_ptr()
+    if out is not None:
+        _req(out, "out", torch.float32, dev)
+        if out.shape != q.shape:
+            raise ValueError("inconsistent shapes")
+    if lse is not None:
+        _req(lse, "lse", torch.float32, dev)
+        if lse.shape != q.shape[:-1]:
+            raise ValueError("inconsistent shapes")
+    if dev_status is not None:
+        _req(dev_status, "dev_status", torch.int32, dev)
+    if isinstance(workspace, torch.Tensor):
+        _req(workspace, "workspace", torch.uint8, dev)
+    elif not (isinstance(workspace, str) and workspace == "auto"):
+        raise ValueError("workspace must be \"auto\" or a uint8 tensor")
+    _check_cuda("q", q)
+    params = DaParams(B, Hq, Hkv, D, bs, block_table.shape[1], NB, int(max_seq_len), float(scale),
+                      float(softcap), int(sliding_window), int(bool(causal)))
+    with _on_device(dev):
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+        if B == 0:
+            return out, lse
+        if isinstance(workspace, str):
+            nbytes = lib.decode_attn_paged_prefix_workspace_size(ctypes.byref(params), T,
+                                                                 prefix_len)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            if stream is not None:
+                workspace.record_stream(stream)
+        st = lib.decode_attn_paged_prefix(ctypes.byref(params), T, prefix_len, pt, _ptr(q),
+                                          _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
+                                          _ptr(seq_lens), _ptr(q_pos), _ptr(out), _ptr(lse),
+                                          _ptr(workspace), workspace.numel(), _ptr(dev_status),
+                                          _stream(dev, stream))
+    _check("decode_attn_paged_prefix", st)
+    return out, lse

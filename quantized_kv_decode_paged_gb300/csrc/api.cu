@@ -662,6 +662,67 @@ int sparse_impl(const da_params* p, const da_sparse_layout* sl, const float* q,
   return run_batched(k, lc, off, static_cast<cudaStream_t>(stream));
 }
 
+// Sizes of a shared-prefix call: check_params and the ones that only it has.
+int check_prefix(const da_params* p, int T, int prefix_len) {
+  int st = check_params(p, false);
+  if (st != DA_OK) return st;
+  if (T < 1 || prefix_len < 0) return DA_ERR_INVALID;
+  if ((long long)prefix_len > (long long)p->max_blocks_per_seq * p->block_size)
+    return DA_ERR_INVALID;
+  if ((long long)T * p->num_q_heads > 0x7fffffffLL / 64) return DA_ERR_UNSUPPORTED;
+  return DA_OK;
+}
+
+// Decode over a shared prefix, T query tokens per sequence.
+int prefix_impl(const da_params* p, int T, int prefix_len, const int32_t* prefix_table,
+                const float* q, const uint16_t* k_pool, const uint16_t* v_pool,
+                const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_pos,
+                float* out, float* lse, void* workspace, size_t workspace_bytes,
+                int32_t* dev_status, void* stream) {
+  int st = check_prefix(p, T, prefix_len);
+  if (st != DA_OK) return st;
+  if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !out) return DA_ERR_INVALID;
+  if (!prefix_table && prefix_len >= p->block_size) return DA_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || (q_pos && !aligned(q_pos, 4)) ||
+      !aligned(prefix_table, 4) || (lse && !aligned(lse, 4)) ||
+      (dev_status && !aligned(dev_status, 4)) || !aligned(workspace, 256))
+    return DA_ERR_INVALID;
+  if (!workspace && workspace_bytes) return DA_ERR_INVALID;
+  if (p->batch == 0) return DA_OK;
+  if (workspace_bytes < decode_attn_paged_prefix_workspace_size(p, T, prefix_len))
+    return DA_ERR_WORKSPACE;
+  da::PrefixParams k = {};
+  k.B = p->batch;
+  k.T = T;
+  k.Hq = p->num_q_heads;
+  k.Hkv = p->num_kv_heads;
+  k.D = p->head_dim;
+  k.G = p->num_q_heads / p->num_kv_heads;
+  k.bs = p->block_size;
+  k.log2_bs = ilog2(p->block_size);
+  k.max_blocks = p->max_blocks_per_seq;
+  k.num_blocks = p->num_blocks;
+  k.prefix_pages = prefix_len / p->block_size;
+  k.window = p->sliding_window;
+  k.causal = p->causal;
+  k.qscale = effective_qscale(p);
+  k.softcap2 = p->softcap > 0.f ? p->softcap * 1.4426950408889634f : 0.f;
+  k.softcap_inv = k.softcap2 > 0.f ? (float)(1.0 / (double)k.softcap2) : 0.f;
+  k.q = q;
+  k.k_pool = k_pool;
+  k.v_pool = v_pool;
+  k.prefix_table = prefix_table;
+  k.block_table = block_table;
+  k.seq_lens = seq_lens;
+  k.q_pos = q_pos;
+  k.out = out;
+  k.lse = lse;
+  k.dev_status = dev_status;
+  return da::launch_prefix(k, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK
+                                                                               : DA_ERR_CUDA;
+}
+
 }  // namespace
 
 namespace da {
@@ -761,6 +822,22 @@ int decode_attn_paged_multi(const da_params* p, int32_t q_len, const float* q,
                             size_t workspace_bytes, int32_t* dev_status, void* stream) {
   return paged_impl(p, q_len, q, k_pool, v_pool, block_table, seq_lens, q_pos, out, lse,
                     workspace, workspace_bytes, dev_status, stream);
+}
+
+size_t decode_attn_paged_prefix_workspace_size(const da_params* p, int32_t q_len,
+                                               int32_t prefix_len) {
+  if (check_prefix(p, q_len, prefix_len) != DA_OK) return 0;
+  return 256;
+}
+
+int decode_attn_paged_prefix(const da_params* p, int32_t q_len, int32_t prefix_len,
+                             const int32_t* prefix_table, const float* q, const uint16_t* k_pool,
+                             const uint16_t* v_pool, const int32_t* block_table,
+                             const int32_t* seq_lens, const int32_t* q_pos, float* out,
+                             float* lse, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream) {
+  return prefix_impl(p, q_len, prefix_len, prefix_table, q, k_pool, v_pool, block_table, seq_lens,
+                     q_pos, out, lse, workspace, workspace_bytes, dev_status, stream);
 }
 
 int decode_attn_split_partial(const da_params* p, int32_t split_tokens, int32_t max_splits,

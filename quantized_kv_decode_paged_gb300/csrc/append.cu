@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "../../include/decode_attn.h"
+#include "launch.h"
 
 namespace {
 
@@ -154,26 +155,13 @@ __global__ void __launch_bounds__(kThreads) append_tiered_kernel(
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Geometry shared by the append entry points.
-int check_append(const da_params* p) {
-  if (!p) return DA_ERR_INVALID;
-  if (p->batch < 0 || p->num_kv_heads <= 0 || p->head_dim <= 0) return DA_ERR_INVALID;
-  if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256) return DA_ERR_UNSUPPORTED;
-  if (p->block_size <= 0 || p->max_blocks_per_seq <= 0 || p->num_blocks <= 0)
-    return DA_ERR_INVALID;
-  if ((long long)p->num_blocks * p->block_size > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
-  if ((long long)p->max_blocks_per_seq * p->block_size > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
-  if ((long long)p->num_kv_heads * p->head_dim * 2 > (1LL << 30)) return DA_ERR_UNSUPPORTED;
-  return DA_OK;
-}
-
 template <bool F16>
 int append_tiered(const da_params* p, int32_t hot_window, int32_t hot_capacity,
                   const uint16_t* k_new, const uint16_t* v_new, uint16_t* k_hot, uint16_t* v_hot,
                   void* k_cold, void* v_cold, uint16_t* k_scale, uint16_t* v_scale,
                   const int32_t* block_table, int32_t* cold_lens, int32_t* hot_lens,
                   int32_t* hot_starts, int32_t* dev_status, void* stream) {
-  int st = check_append(p);
+  int st = da::check_append_params(p);
   if (st != DA_OK) return st;
   if (hot_window <= 0 || hot_capacity < hot_window) return DA_ERR_INVALID;
   if (!k_new || !v_new || !k_hot || !v_hot || !k_cold || !v_cold || !block_table ||
@@ -194,13 +182,30 @@ int append_tiered(const da_params* p, int32_t hot_window, int32_t hot_capacity,
 
 }  // namespace
 
+namespace da {
+
+// Geometry shared by the append entry points.
+int check_append_params(const da_params* p) {
+  if (!p) return DA_ERR_INVALID;
+  if (p->batch < 0 || p->num_kv_heads <= 0 || p->head_dim <= 0) return DA_ERR_INVALID;
+  if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256) return DA_ERR_UNSUPPORTED;
+  if (p->block_size <= 0 || p->max_blocks_per_seq <= 0 || p->num_blocks <= 0)
+    return DA_ERR_INVALID;
+  if ((long long)p->num_blocks * p->block_size > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+  if ((long long)p->max_blocks_per_seq * p->block_size > 0x7fffffffLL) return DA_ERR_UNSUPPORTED;
+  if ((long long)p->num_kv_heads * p->head_dim * 2 > (1LL << 30)) return DA_ERR_UNSUPPORTED;
+  return DA_OK;
+}
+
+}  // namespace da
+
 extern "C" {
 
 int decode_attn_append_paged(const da_params* p, const uint16_t* k_new, const uint16_t* v_new,
                              const int32_t* positions, const int32_t* block_table,
                              uint16_t* k_pool, uint16_t* v_pool, int32_t* dev_status,
                              void* stream) {
-  int st = check_append(p);
+  int st = da::check_append_params(p);
   if (st != DA_OK) return st;
   if (!k_new || !v_new || !positions || !block_table || !k_pool || !v_pool) return DA_ERR_INVALID;
   if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) || !aligned16(v_pool))

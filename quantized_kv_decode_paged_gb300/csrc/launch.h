@@ -3,9 +3,13 @@
 
 #include <cuda_runtime.h>
 
+#include "../../include/decode_attn.h"
 #include "kernel_params.h"
 
 namespace da {
+
+// Validation of the geometry an append uses (append.cu).
+int check_append_params(const da_params* p);
 
 // kv heads per work unit for a cache of `kind` with head dimension D and
 // Hkv kv heads: enough that one token row of the block is >= 512
@@ -38,5 +42,29 @@ size_t workspace_ticket_bytes();
 cudaError_t launch_split_merge(int rows, int max_splits, int D, const float* o_part,
                                const float* lse_part, float* out, float* lse,
                                cudaStream_t stream);
+
+// Shared-prefix decode (prefix_attn.cu).  Rows are (sequence, query token,
+// query head of the kv head); keys below prefix_pages * bs are read through
+// prefix_table, the others through block_table.
+struct PrefixParams {
+  int B, T, Hq, Hkv, D, G;
+  int bs, log2_bs, max_blocks, num_blocks;
+  int prefix_pages;
+  int window, causal;
+  float qscale;       // scale * log2(e): scores are kept in base-2 units
+  float softcap2;     // softcap * log2(e) (0 = off)
+  float softcap_inv;  // 1 / softcap2
+  const float* q;
+  const uint16_t* k_pool;
+  const uint16_t* v_pool;
+  const int* prefix_table;
+  const int* block_table;
+  const int* seq_lens;
+  const int* q_pos;
+  float* out;
+  float* lse;
+  int* dev_status;
+};
+cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t stream);
 
 }  // namespace da

@@ -1,0 +1,387 @@
+// rope.cu — what a step does to its new rows before the attention: RMS norm
+// of every query and key head, position rotation, and the append of rotated
+// keys and plain values to the paged cache.
+//
+// Mathematics.  A head's row x has D values.  Norm: y_d = x_d r w_d with
+// r = 1/sqrt(mean(x^2) + eps).  Rotation of a pair by the angle a:
+// (y0 cos a - y1 sin a, y0 sin a + y1 cos a).  a = pos * f turns with f in
+// 64-bit fixed point: the low 64 bits of the integer product are the angle
+// modulo one turn, exact up to f's own 2^-65 turns a position.  The top 32 bits
+// as a signed number times 2^-31 are a / pi in [-1, 1), what sincospif takes.
+//
+// One CTA per token: its rd/2 cosines and sines are computed once into shared memory
+// and serve all the token's heads.  D/16 threads take a row, each
+// two 8-value chunks that hold both halves of its 8 pairs: (8c, rd/2 + 8c) or, interleaved,
+// (16c, 16c + 8); the chunks past the rotated part pair up without rotation.
+// So no value crosses threads but the norm's sum of squares.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/decode_attn.h"
+#include "launch.h"
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;  // element strides of tokens and heads
+  const float* qw;
+  const float* kw;
+  const uint64_t* freqs;
+  const int32_t* positions;
+  int Hq, Hkv, rd, norm;
+  float eps, woff;
+  float* q_out;
+  uint16_t* k_out;  // norm_rope: [N, Hkv, D]
+  // append
+  const int32_t* token_seq;
+  const int32_t* block_table;
+  uint16_t* k_pool;
+  uint16_t* v_pool;
+  int batch, bs, max_blocks, num_blocks;
+  int32_t* dev_status;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8], const __half*) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8], const __nv_bfloat16*) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// Eight values at a 16-byte boundary (32 bytes of f32).
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  if constexpr (std::is_same<T, float>::value) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    unpack8(*reinterpret_cast<const uint4*>(p), x, static_cast<const T*>(nullptr));
+  }
+}
+
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Row n's place in the cache, in rows of the pool; negative: not written
+// (padding, or a flag is set).
+__device__ __forceinline__ long long cache_row(const RopeArgs& a, int n, int& flag, bool& pad) {
+  const int seq = a.token_seq ? a.token_seq[n] : n;
+  pad = seq < 0;
+  flag = 0;
+  if (pad) return -1;
+  if (seq >= a.batch) {
+    flag = DA_DEV_BAD_SEQ;
+    return -1;
+  }
+  const long long pos = a.positions[n];
+  if (pos < 0 || pos >= (long long)a.max_blocks * a.bs) {
+    flag = DA_DEV_BAD_SEQ_LEN;
+    return -1;
+  }
+  const int blk = a.block_table[(long long)seq * a.max_blocks + pos / a.bs];
+  if (blk < 0 || blk >= a.num_blocks) {
+    flag = DA_DEV_BAD_BLOCK;
+    return -1;
+  }
+  return (long long)blk * a.bs + pos % a.bs;
+}
+
+template <typename T, int D, bool IL, bool APPEND>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+  constexpr int TPR = D / 16;  // threads of a row
+  __shared__ float2 cs[D / 2];
+  const int n = blockIdx.x;
+  for (int i = threadIdx.x; i < a.rd / 2; i += kRopeThreads) {
+    const uint64_t turns = (uint64_t)(long long)a.positions[n] * a.freqs[i];
+    const float half_turns = (float)(int32_t)(turns >> 32) * 0x1p-31f;
+    sincospif(half_turns, &cs[i].y, &cs[i].x);
+  }
+  long long row = -1;
+  if constexpr (APPEND) {
+    int flag;
+    bool pad;
+    row = cache_row(a, n, flag, pad);
+    if (pad) return;
+    if (flag && threadIdx.x == 0 && a.dev_status) atomicOr(a.dev_status, flag);
+  }
+  __syncthreads();
+  const int c = threadIdx.x % TPR;
+  const int nrot = a.rd / 16;  // chunk pairs that are rotated
+  const bool rot = c < nrot;
+  const int lo = IL ? 16 * c : rot ? 8 * c : a.rd + 16 * (c - nrot);
+  const int hi = (IL || !rot) ? lo + 8 : a.rd / 2 + 8 * c;
+  const int Hk = a.k ? a.Hkv : 0, Hq = a.q ? a.Hq : 0;
+  const int heads = Hq + Hk + (APPEND ? a.Hkv : 0);
+  // a warp's threads run the same number of rounds: the norm's sum is taken across them
+  for (int h0 = 0; h0 < heads; h0 += kRopeThreads / TPR) {
+    const int h = h0 + threadIdx.x / TPR;
+    const bool on = h < heads;
+    const bool is_q = h < Hq, is_v = h >= Hq + Hk;
+    const int hh = is_q ? h : is_v ? h - Hq - Hk : h - Hq;
+    float x[2][8];
+    if (on) {
+      const T* src = is_q   ? static_cast<const T*>(a.q) + n * a.q_ts + hh * a.q_hs
+                     : is_v ? static_cast<const T*>(a.v) + n * a.v_ts + hh * a.v_hs
+                            : static_cast<const T*>(a.k) + n * a.k_ts + hh * a.k_hs;
+      load8(src + lo, x[0]);
+      load8(src + hi, x[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[0][i] = x[1][i] = 0.f;
+    }
+    if (a.norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[0][i], x[0][i], fmaf(x[1][i], x[1][i], ss));
+#pragma unroll
+      for (int o = TPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (on && !is_v) {
+        const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+        const float* w = is_q ? a.qw : a.kw;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[0][i] *= r * (w ? w[lo + i] + a.woff : 1.f);
+          x[1][i] *= r * (w ? w[hi + i] + a.woff : 1.f);
+        }
+      }
+    }
+    if (!on) continue;
+    if (rot && !is_v) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 t = cs[8 * c + i];
+        float& y0 = IL ? x[i / 4][2 * (i % 4)] : x[0][i];
+        float& y1 = IL ? x[i / 4][2 * (i % 4) + 1] : x[1][i];
+        const float z0 = y0 * t.x - y1 * t.y;
+        y1 = y0 * t.y + y1 * t.x;
+        y0 = z0;
+      }
+    }
+    if (is_q) {
+      float* dst = a.q_out + ((long long)n * a.Hq + hh) * D;
+      store8(dst + lo, x[0]);
+      store8(dst + hi, x[1]);
+    } else {
+      uint16_t* dst;
+      if constexpr (APPEND) {
+        if (row < 0) continue;
+        dst = (is_v ? a.v_pool : a.k_pool) + (row * a.Hkv + hh) * D;
+      } else {
+        dst = a.k_out + ((long long)n * a.Hkv + hh) * D;
+      }
+      store8(dst + lo, x[0]);
+      store8(dst + hi, x[1]);
+    }
+  }
+}
+
+template <typename T, int D, bool APPEND>
+void launch_rope_d(const RopeArgs& a, int il, int num_tokens, cudaStream_t s) {
+  if (il)
+    rope_kernel<T, D, true, APPEND><<<num_tokens, kRopeThreads, 0, s>>>(a);
+  else
+    rope_kernel<T, D, false, APPEND><<<num_tokens, kRopeThreads, 0, s>>>(a);
+}
+
+template <typename T, bool APPEND>
+void launch_rope_t(const RopeArgs& a, int D, int il, int num_tokens, cudaStream_t s) {
+  if (D == 64)
+    launch_rope_d<T, 64, APPEND>(a, il, num_tokens, s);
+  else if (D == 128)
+    launch_rope_d<T, 128, APPEND>(a, il, num_tokens, s);
+  else
+    launch_rope_d<T, 256, APPEND>(a, il, num_tokens, s);
+}
+
+template <bool APPEND>
+int launch_rope(const RopeArgs& a, const da_rope_params* r, int D, int num_tokens, void* stream) {
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (r->type == DA_TYPE_F32)
+    launch_rope_t<float, APPEND>(a, D, r->interleaved, num_tokens, s);
+  else if (r->type == DA_TYPE_F16)
+    launch_rope_t<__half, APPEND>(a, D, r->interleaved, num_tokens, s);
+  else
+    launch_rope_t<__nv_bfloat16, APPEND>(a, D, r->interleaved, num_tokens, s);
+  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// A strided input: every row on a 16-byte boundary, offsets within 63 bits.
+int check_rows(const void* p, long long ts, long long hs, int esize, int tokens, int heads) {
+  if (!aligned(p, 16) || ts < 0 || hs < 0) return DA_ERR_INVALID;
+  if ((ts * esize) % 16 != 0 || (hs * esize) % 16 != 0) return DA_ERR_INVALID;
+  const long long lim = 1LL << 40;  // elements between rows: far past any device's memory
+  if (ts > lim || hs > lim || tokens < 0 || heads <= 0) return DA_ERR_INVALID;
+  return DA_OK;
+}
+
+int check_rope(const da_rope_params* r, int D) {
+  if (!r) return DA_ERR_INVALID;
+  if (r->type != DA_TYPE_F32 && r->type != DA_TYPE_F16 && r->type != DA_TYPE_BF16)
+    return DA_ERR_INVALID;
+  if (D <= 0) return DA_ERR_INVALID;
+  if (D != 64 && D != 128 && D != 256) return DA_ERR_UNSUPPORTED;
+  if (r->rotary_dim < 0 || r->rotary_dim > D || r->rotary_dim % 2 != 0) return DA_ERR_INVALID;
+  if (r->rotary_dim % 16 != 0) return DA_ERR_UNSUPPORTED;
+  if ((r->interleaved != 0 && r->interleaved != 1) || (r->norm != 0 && r->norm != 1))
+    return DA_ERR_INVALID;
+  if (r->norm && (!(r->eps >= 0.f) || isinf(r->eps) || !isfinite(r->weight_offset)))
+    return DA_ERR_INVALID;
+  if (r->rotary_dim > 0 && (!r->freqs || !aligned(r->freqs, 8))) return DA_ERR_INVALID;
+  if (r->norm && ((r->q_weight && !aligned(r->q_weight, 16)) ||
+                  (r->k_weight && !aligned(r->k_weight, 16))))
+    return DA_ERR_INVALID;
+  return DA_OK;
+}
+
+void fill_args(RopeArgs& a, const da_rope_params* r, const void* q, const void* k,
+               const int32_t* positions, int Hq, int Hkv, float* q_out) {
+  a.q = q;
+  a.k = k;
+  a.q_ts = r->q_token_stride;
+  a.q_hs = r->q_head_stride;
+  a.k_ts = r->k_token_stride;
+  a.k_hs = r->k_head_stride;
+  a.v_ts = r->v_token_stride;
+  a.v_hs = r->v_head_stride;
+  a.qw = r->norm ? r->q_weight : nullptr;
+  a.kw = r->norm ? r->k_weight : nullptr;
+  a.freqs = r->freqs;
+  a.positions = positions;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.rd = r->rotary_dim;
+  a.norm = r->norm;
+  a.eps = r->eps;
+  a.woff = r->weight_offset;
+  a.q_out = q_out;
+}
+
+}  // namespace
+
+extern "C" {
+
+int decode_attn_rope_freqs(int32_t rotary_dim, double theta, const double* inv_freq,
+                           uint64_t* freqs) {
+  if (rotary_dim < 0 || rotary_dim % 2 != 0 || (rotary_dim > 0 && !freqs)) return DA_ERR_INVALID;
+  if (!inv_freq && !(theta > 0.0 && isfinite(theta))) return DA_ERR_INVALID;
+  for (int i = 0; inv_freq && i < rotary_dim / 2; ++i)
+    if (!isfinite(inv_freq[i])) return DA_ERR_INVALID;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double w = inv_freq ? inv_freq[i] : pow(theta, -2.0 * i / rotary_dim);
+    // the fraction of a turn, in [0, 1); whole turns a position drop out
+    double t = w / 6.283185307179586476925286766559;
+    t -= floor(t);
+    const double u = rint(t * 18446744073709551616.0);
+    freqs[i] = u >= 18446744073709551616.0 ? 0 : (uint64_t)u;
+  }
+  return DA_OK;
+}
+
+int decode_attn_qk_norm_rope(const da_rope_params* r, int32_t num_tokens, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, const void* q, const void* k,
+                             const int32_t* positions, float* q_out, uint16_t* k_out,
+                             void* stream) {
+  int st = check_rope(r, head_dim);
+  if (st != DA_OK) return st;
+  if (num_tokens < 0 || (!q && !k)) return DA_ERR_INVALID;
+  const int esize = r->type == DA_TYPE_F32 ? 4 : 2;
+  if (q) {
+    if (!q_out || !aligned(q_out, 16)) return DA_ERR_INVALID;
+    st = check_rows(q, r->q_token_stride, r->q_head_stride, esize, num_tokens, num_q_heads);
+    if (st != DA_OK) return st;
+  }
+  if (k) {
+    if (!k_out || !aligned(k_out, 16)) return DA_ERR_INVALID;
+    st = check_rows(k, r->k_token_stride, r->k_head_stride, esize, num_tokens, num_kv_heads);
+    if (st != DA_OK) return st;
+  }
+  if ((long long)(q ? num_q_heads : 0) + (k ? num_kv_heads : 0) > 65536) return DA_ERR_UNSUPPORTED;
+  if (r->rotary_dim > 0 && !positions) return DA_ERR_INVALID;
+  if (positions && !aligned(positions, 4)) return DA_ERR_INVALID;
+  if (num_tokens == 0) return DA_OK;
+  RopeArgs a = {};
+  fill_args(a, r, q, k, positions, num_q_heads, num_kv_heads, q_out);
+  a.k_out = k_out;
+  return launch_rope<false>(a, r, head_dim, num_tokens, stream);
+}
+
+int decode_attn_append_paged_rope(const da_params* p, const da_rope_params* r, int32_t num_tokens,
+                                  const void* q, const void* k_new, const void* v_new,
+                                  const int32_t* positions, const int32_t* token_seq,
+                                  const int32_t* block_table, float* q_out, uint16_t* k_pool,
+                                  uint16_t* v_pool, int32_t* dev_status, void* stream) {
+  int st = da::check_append_params(p);
+  if (st != DA_OK) return st;
+  st = check_rope(r, p->head_dim);
+  if (st != DA_OK) return st;
+  if (num_tokens < 0 || (!token_seq && num_tokens != p->batch)) return DA_ERR_INVALID;
+  if (!k_new || !v_new || !positions || !block_table || !k_pool || !v_pool) return DA_ERR_INVALID;
+  if ((q == nullptr) != (q_out == nullptr)) return DA_ERR_INVALID;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(positions, 4) ||
+      !aligned(block_table, 4) || (token_seq && !aligned(token_seq, 4)) ||
+      (dev_status && !aligned(dev_status, 4)) || (q_out && !aligned(q_out, 16)))
+    return DA_ERR_INVALID;
+  const int esize = r->type == DA_TYPE_F32 ? 4 : 2;
+  st = check_rows(k_new, r->k_token_stride, r->k_head_stride, esize, num_tokens, p->num_kv_heads);
+  if (st != DA_OK) return st;
+  st = check_rows(v_new, r->v_token_stride, r->v_head_stride, esize, num_tokens, p->num_kv_heads);
+  if (st != DA_OK) return st;
+  if (q) {
+    st = check_rows(q, r->q_token_stride, r->q_head_stride, esize, num_tokens, p->num_q_heads);
+    if (st != DA_OK) return st;
+  }
+  if ((long long)(q ? p->num_q_heads : 0) + 2LL * p->num_kv_heads > 65536)
+    return DA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return DA_OK;
+  RopeArgs a = {};
+  fill_args(a, r, q, k_new, positions, p->num_q_heads, p->num_kv_heads, q_out);
+  a.v = v_new;
+  a.token_seq = token_seq;
+  a.block_table = block_table;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.batch = p->batch;
+  a.bs = p->block_size;
+  a.max_blocks = p->max_blocks_per_seq;
+  a.num_blocks = p->num_blocks;
+  a.dev_status = dev_status;
+  return launch_rope<true>(a, r, p->head_dim, num_tokens, stream);
+}
+
+}  // extern "C"
