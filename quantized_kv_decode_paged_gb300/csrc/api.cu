@@ -669,7 +669,41 @@ int check_prefix(const da_params* p, int T, int prefix_len) {
   if (T < 1 || prefix_len < 0) return DA_ERR_INVALID;
   if ((long long)prefix_len > (long long)p->max_blocks_per_seq * p->block_size)
     return DA_ERR_INVALID;
-  if ((long long)T * p->num_q_heads > 0x7fffffffLL / 64) return DA_ERR_UNSUPPORTED;
+  // row indices of a launch have 32 bits
+  if ((long long)T * p->num_q_heads * da::prefix_max_batch(p->head_dim) > 0x7fffffffLL - 1024)
+    return DA_ERR_UNSUPPORTED;
+  // a tile past the last key still has 32-bit key indices
+  if ((long long)p->max_blocks_per_seq * p->block_size > 0x7fffffffLL - 1024)
+    return DA_ERR_UNSUPPORTED;
+  return DA_OK;
+}
+
+// Sequences of one launch: the batch split evenly over the fewest launches.
+int prefix_chunk(int batch, int D) {
+  const int most = da::prefix_max_batch(D), n = (batch + most - 1) / most;
+  return n > 0 ? (batch + n - 1) / n : 0;
+}
+
+// Pool maps of the shared-prefix kernel: the 4-D view of encode_pool_map
+// with boxes of one kv head, min(block_size, tile) keys, and every 128-byte
+// slice of the row when one box is a whole tile (a tile is laid out [slice][key]).
+int encode_prefix_maps(da::PrefixParams& k, const da_params* p, const void* kp, const void* vp) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return DA_ERR_CUDA;
+  const int D = p->head_dim, tile = da::prefix_tile_keys(D);
+  k.box_rows = p->block_size < tile ? p->block_size : tile;
+  k.box_slices = k.box_rows == tile ? D / 64 : 1;
+  cuuint64_t dims[4] = {64, (cuuint64_t)p->num_blocks * p->block_size, (cuuint64_t)(D / 64),
+                        (cuuint64_t)p->num_kv_heads};
+  cuuint64_t strides[3] = {(cuuint64_t)p->num_kv_heads * D * 2, 128, (cuuint64_t)D * 2};
+  cuuint32_t box[4] = {64u, (cuuint32_t)k.box_rows, (cuuint32_t)k.box_slices, 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  for (int i = 0; i < 2; ++i)
+    if (fn(i ? &k.tm_v : &k.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
+           const_cast<void*>(i ? vp : kp), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return DA_ERR_CUDA;
   return DA_OK;
 }
 
@@ -690,15 +724,20 @@ int prefix_impl(const da_params* p, int T, int prefix_len, const int32_t* prefix
     return DA_ERR_INVALID;
   if (!workspace && workspace_bytes) return DA_ERR_INVALID;
   if (p->batch == 0) return DA_OK;
-  if (workspace_bytes < decode_attn_paged_prefix_workspace_size(p, T, prefix_len))
-    return DA_ERR_WORKSPACE;
-  da::PrefixParams k = {};
-  k.B = p->batch;
+  int sms = 0;
+  st = device_sms(&sms);
+  if (st != DA_OK) return st;
+  da::PrefixParams k;
+  memset(&k, 0, sizeof(k));
+  st = encode_prefix_maps(k, p, k_pool, v_pool);
+  if (st != DA_OK) return st;
   k.T = T;
   k.Hq = p->num_q_heads;
   k.Hkv = p->num_kv_heads;
   k.D = p->head_dim;
   k.G = p->num_q_heads / p->num_kv_heads;
+  k.R1 = T * k.G;
+  k.own_tiles = (k.R1 + da::kPrefixRows - 1) / da::kPrefixRows;
   k.bs = p->block_size;
   k.log2_bs = ilog2(p->block_size);
   k.max_blocks = p->max_blocks_per_seq;
@@ -709,18 +748,36 @@ int prefix_impl(const da_params* p, int T, int prefix_len, const int32_t* prefix
   k.qscale = effective_qscale(p);
   k.softcap2 = p->softcap > 0.f ? p->softcap * 1.4426950408889634f : 0.f;
   k.softcap_inv = k.softcap2 > 0.f ? (float)(1.0 / (double)k.softcap2) : 0.f;
-  k.q = q;
+  k.grid = sms;
+  k.wait_ns = wait_limit_ns();
+  k.test_skip_arm = test_skip_arm();
   k.k_pool = k_pool;
   k.v_pool = v_pool;
   k.prefix_table = prefix_table;
-  k.block_table = block_table;
-  k.seq_lens = seq_lens;
-  k.q_pos = q_pos;
-  k.out = out;
-  k.lse = lse;
   k.dev_status = dev_status;
-  return da::launch_prefix(k, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK
-                                                                               : DA_ERR_CUDA;
+  const int chunk = prefix_chunk(p->batch, k.D);
+  const da::PrefixWs w = da::prefix_ws(sms, k.D, (long long)chunk * T * p->num_q_heads);
+  if (!workspace || workspace_bytes < w.total) return DA_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  k.ws_plan = reinterpret_cast<int*>(ws + w.plan);
+  k.ws_cut_ml = reinterpret_cast<float2*>(ws + w.cut_ml);
+  k.ws_pre_ml = reinterpret_cast<float2*>(ws + w.pre_ml);
+  k.ws_own_ml = reinterpret_cast<float2*>(ws + w.own_ml);
+  k.ws_cut_o = reinterpret_cast<float*>(ws + w.cut_o);
+  k.ws_pre_o = reinterpret_cast<float*>(ws + w.pre_o);
+  const long long row = (long long)T * p->num_q_heads;
+  for (int b0 = 0; b0 < p->batch; b0 += chunk) {
+    k.B = p->batch - b0 < chunk ? p->batch - b0 : chunk;
+    k.row_tiles = (int)(((long long)k.B * k.R1 + da::kPrefixRows - 1) / da::kPrefixRows);
+    k.q = q + b0 * row * k.D;
+    k.block_table = block_table + (long long)b0 * k.max_blocks;
+    k.seq_lens = seq_lens + b0;
+    k.q_pos = q_pos ? q_pos + b0 : nullptr;
+    k.out = out + b0 * row * k.D;
+    k.lse = lse ? lse + b0 * row : nullptr;
+    if (da::launch_prefix(k, static_cast<cudaStream_t>(stream)) != cudaSuccess) return DA_ERR_CUDA;
+  }
+  return DA_OK;
 }
 
 }  // namespace
@@ -827,7 +884,11 @@ int decode_attn_paged_multi(const da_params* p, int32_t q_len, const float* q,
 size_t decode_attn_paged_prefix_workspace_size(const da_params* p, int32_t q_len,
                                                int32_t prefix_len) {
   if (check_prefix(p, q_len, prefix_len) != DA_OK) return 0;
-  return 256;
+  int sms = 0;
+  if (device_sms(&sms) != DA_OK) return 0;
+  return da::prefix_ws(sms, p->head_dim,
+                       (long long)prefix_chunk(p->batch, p->head_dim) * q_len * p->num_q_heads)
+      .total;
 }
 
 int decode_attn_paged_prefix(const da_params* p, int32_t q_len, int32_t prefix_len,

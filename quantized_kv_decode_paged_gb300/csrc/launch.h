@@ -46,14 +46,29 @@ cudaError_t launch_split_merge(int rows, int max_splits, int D, const float* o_p
 // Shared-prefix decode (prefix_attn.cu).  Rows are (sequence, query token,
 // query head of the kv head); keys below prefix_pages * bs are read through
 // prefix_table, the others through block_table.
-struct PrefixParams {
+constexpr int kPrefixRows = 128;      // rows of a tile (the MMA's M)
+// sequences of a launch: their lengths sit in shared memory beside the tiles
+__host__ __device__ constexpr int prefix_max_batch(int D) { return D >= 256 ? 184 : 256; }
+// keys of a tile
+__host__ __device__ constexpr int prefix_tile_keys(int D) { return D >= 256 ? 64 : 128; }
+
+struct alignas(128) PrefixParams {
+  CUtensorMap tm_k;  // boxes of box_rows keys, one kv head, box_slices 128-byte slices
+  CUtensorMap tm_v;
+  int box_rows, box_slices;
   int B, T, Hq, Hkv, D, G;
+  int R1;             // rows of a sequence and kv head: T * G
+  int row_tiles;      // tiles of the batch's rows of a kv head
+  int own_tiles;      // tiles of one sequence's rows of a kv head
   int bs, log2_bs, max_blocks, num_blocks;
   int prefix_pages;
   int window, causal;
   float qscale;       // scale * log2(e): scores are kept in base-2 units
   float softcap2;     // softcap * log2(e) (0 = off)
   float softcap_inv;  // 1 / softcap2
+  int grid;
+  unsigned long long wait_ns;  // time limit of every wait (abort mode after it)
+  int test_skip_arm;           // test hook: CTA 0's first copy is left out
   const float* q;
   const uint16_t* k_pool;
   const uint16_t* v_pool;
@@ -64,7 +79,32 @@ struct PrefixParams {
   float* out;
   float* lse;
   int* dev_status;
+  // workspace (PrefixWs).  A state is o (not divided by l), and (m, l): the
+  // reference the weights were taken against, base 2, and their sum, negative when
+  // some key of its tiles was masked for the row.
+  int* ws_plan;       // tiles of a prefix unit, CTAs, [B + 1] tiles of own keys before b
+  float2* ws_cut_ml;  // [grid][2][128] of a unit's part
+  float2* ws_pre_ml;  // [B * T * Hq] of the prefix, units that no CTA boundary cuts
+  float2* ws_own_ml;  // [B * T * Hq] of own keys; their o goes to out
+  float* ws_cut_o;    // [grid][2][128][D]
+  float* ws_pre_o;    // [B * T * Hq][D]
 };
+
+struct PrefixWs {
+  size_t plan, cut_ml, pre_ml, own_ml, cut_o, pre_o, total;
+};
+inline PrefixWs prefix_ws(int grid, int D, long long rows) {
+  auto al = [](size_t x) { return (x + 255) / 256 * 256; };
+  PrefixWs w;
+  w.plan = 0;
+  w.cut_ml = al((prefix_max_batch(D) + 3) * 4);
+  w.pre_ml = w.cut_ml + al((size_t)grid * 2 * kPrefixRows * 8);
+  w.own_ml = w.pre_ml + al((size_t)rows * 8);
+  w.cut_o = w.own_ml + al((size_t)rows * 8);
+  w.pre_o = w.cut_o + al((size_t)grid * 2 * kPrefixRows * D * 4);
+  w.total = w.pre_o + al((size_t)rows * D * 4);
+  return w;
+}
 cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t stream);
 
 }  // namespace da

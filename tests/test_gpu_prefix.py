@@ -477,3 +477,18 @@ def test_a_serving_step(T):
     vmax = vp.abs().max().item()
     assert np.abs(out.cpu().numpy() - ro.reshape(shape)).max() <= vmax * (2 * eps + (n / 8 + 40) * 2.0 ** -23)
     assert np.abs(lse.cpu().numpy() - rl.reshape(shape[:-1])).max() <= 2 * eps + (n / 8 + 40) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_wait_that_runs_out_is_reported(D):
+    """CTA 0's first copy left out: its consumers' waits run out after 50 ms,
+    the kernel ends with DEV_TIMEOUT, and the next call is right again."""
+    lib = qk.load_library()
+    c = Case(23, 4, 8, 2, D, 16, 2048, [2100, 2049, 2300, 2060])
+    with qk.tuning(wait_limit_ms=50):
+        lib.decode_attn_testing_skip_first_arm(1)
+        try:
+            assert c.run()[2] == qk.DEV_TIMEOUT
+        finally:
+            lib.decode_attn_testing_skip_first_arm(0)
+    c.check()
