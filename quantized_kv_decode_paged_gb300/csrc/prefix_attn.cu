@@ -541,6 +541,7 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s, long long 
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
   const int row = w * 32 + lane;
   const uint32_t lanes = s.tmem + ((uint32_t)(w * 32) << 16);
+  const int box_shift = __ffs(p.box_rows) - 1;
   int x = 0;  // tiles so far
   for (Cursor<D> c(p, s, tp, g0, g1); !c.done(); c.next()) {
     const int k = c.k;
@@ -575,32 +576,41 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s, long long 
       if (any) {
         tc5_fence_after();
         const uint32_t sa = lanes + G::S0 + buf * KT;
-        float v[KT];
-#pragma unroll
-        for (int i = 0; i < KT; i += 32) tmem_ld32(sa + i, v + i);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < KT; i += 32) tmem_loaded32(v + i);
         const int k0 = c.base + (c.i0 + j) * KT;
         const int bad = s.bad[x & 7];
-        if (CAP) {
+        const bool masked =
+            !__all_sync(0xffffffffu, (!on || (lo <= k0 && hi >= k0 + KT)) && bad == 0);
+        partial |= masked;
+        // Two passes over the scores, 32 columns at a time: a loop that stays in the
+        // instruction cache and needs few registers.
+        float top = m;
+#pragma unroll 1
+        for (int i0 = 0; i0 < KT; i0 += 32) {
+          float v[32];
+          tmem_ld32(sa + i0, v);
+          tmem_wait_ld();
+          tmem_loaded32(v);
+          if (CAP || masked) {
+            if (CAP) {
 #pragma unroll
-          for (int i = 0; i < KT; ++i) v[i] = capped(v[i] * scale, p.softcap2, p.softcap_inv);
+              for (int i = 0; i < 32; ++i) v[i] = capped(v[i] * scale, p.softcap2, p.softcap_inv);
+            }
+            if (masked) {
+              const int a = lo - k0 - i0, z = hi - k0 - i0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < a || i >= z || ((bad >> ((i0 + i) >> box_shift)) & 1)) v[i] = -kInf;
+            }
+            tmem_st32(sa + i0, v);
+          }
+          float mx[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = v[i];
+#pragma unroll
+          for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+          top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (CAP ? 1.f : scale));
         }
-        if (!__all_sync(0xffffffffu, (!on || (lo <= k0 && hi >= k0 + KT)) && bad == 0)) {
-          partial = true;
-          const int a = lo - k0, z = hi - k0, sh = __ffs(p.box_rows) - 1;
-#pragma unroll
-          for (int i = 0; i < KT; ++i)
-            if (i < a || i >= z || ((bad >> (i >> sh)) & 1)) v[i] = -kInf;
-        }
-        float mx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = v[i];
-#pragma unroll
-        for (int i = 4; i < KT; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
-        const float cc = CAP ? 1.f : scale;
-        const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cc);
+        if (CAP || masked) tmem_wait_st();
         // no key so far: any finite reference does
         const float ref = top == -kInf ? 0.f : top;
         const float f = ex2_ftz(m - ref);
@@ -609,21 +619,26 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s, long long 
           tmem_st1(lanes + G::F0 + buf, f);
         else
           s.fac[buf * kPrefixRows + row] = f;
-        const float base = ref - kShift;
+        const float cc = CAP ? 1.f : scale, base = ref - kShift;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
         for (int i0 = 0; i0 < KT; i0 += 32) {
+          float v[32];
           uint32_t ph[16], pl[16];
+          tmem_ld32(sa + i0, v);
+          tmem_wait_ld();
+          tmem_loaded32(v);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float p0 = ex2_ftz(fmaf(v[i0 + i], cc, -base));
-            const float p1 = ex2_ftz(fmaf(v[i0 + i + 1], cc, -base));
+            const float p0 = ex2_ftz(fmaf(v[i], cc, -base));
+            const float p1 = ex2_ftz(fmaf(v[i + 1], cc, -base));
             sum[i & 2] += p0;
             sum[(i & 2) + 1] += p1;
             split_half2(p0, p1, ph[i / 2], pl[i / 2]);
           }
-          tmem_st16(sa + i0 / 2, ph);
-          tmem_st16(sa + KT / 2 + i0 / 2, pl);
+          // the weights of 32 keys take the columns of their scores: 16 of high terms, 16 of low
+          tmem_st16(sa + i0, ph);
+          tmem_st16(sa + i0 + 16, pl);
         }
         l = fmaf(l, f, (sum[0] + sum[1]) + (sum[2] + sum[3]));
         tmem_wait_st();
@@ -759,7 +774,7 @@ __device__ void mma_loop(const PrefixParams& p, PrefixSmem<D>& s, long long tp, 
     for (int term = 1; term >= 0; --term)
 #pragma unroll
       for (int k = 0; k < KT; k += 16)
-        mma_ts(tm, tm + G::S0 + buf * KT + term * (KT / 2) + k / 2,
+        mma_ts(tm, tm + G::S0 + buf * KT + k / 32 * 32 + term * 16 + k % 32 / 2,
                smem_desc(v + k * 128, KT * 128, 1024), id_pv, term == 0 || k > 0);
     mma_commit(&s.empty[slot]);
     mma_commit(&s.pv_done[buf]);
