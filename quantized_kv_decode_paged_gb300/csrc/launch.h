@@ -48,7 +48,7 @@ cudaError_t launch_split_merge(int rows, int max_splits, int D, const float* o_p
 // prefix_table, the others through block_table.
 constexpr int kPrefixRows = 128;      // rows of a tile (the MMA's M)
 // sequences of a launch: their lengths sit in shared memory beside the tiles
-__host__ __device__ constexpr int prefix_max_batch(int D) { return D >= 256 ? 184 : 256; }
+__host__ __device__ constexpr int prefix_max_batch(int D) { return D >= 256 ? 172 : 256; }
 // keys of a tile
 __host__ __device__ constexpr int prefix_tile_keys(int D) { return D >= 256 ? 64 : 128; }
 
@@ -82,7 +82,7 @@ struct alignas(128) PrefixParams {
   // workspace (PrefixWs).  A state is o (not divided by l), and (m, l): the
   // reference the weights were taken against, base 2, and their sum, negative when
   // some key of its tiles was masked for the row.
-  int* ws_plan;       // tiles of a prefix unit, CTAs, [B + 1] tiles of own keys before b
+  int* ws_plan;       // tiles of a prefix unit, [B + 1] tiles of own keys before b
   float2* ws_cut_ml;  // [grid][2][128] of a unit's part
   float2* ws_pre_ml;  // [B * T * Hq] of the prefix, units that no CTA boundary cuts
   float2* ws_own_ml;  // [B * T * Hq] of own keys; their o goes to out
@@ -97,7 +97,7 @@ inline PrefixWs prefix_ws(int grid, int D, long long rows) {
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   PrefixWs w;
   w.plan = 0;
-  w.cut_ml = al((prefix_max_batch(D) + 3) * 4);
+  w.cut_ml = al((prefix_max_batch(D) + 2) * 4);
   w.pre_ml = w.cut_ml + al((size_t)grid * 2 * kPrefixRows * 8);
   w.own_ml = w.pre_ml + al((size_t)rows * 8);
   w.cut_o = w.own_ml + al((size_t)rows * 8);

@@ -29,12 +29,13 @@
 // (their steps truncate at their own size), and the sums over tiles are ordinary f32 adds in
 // registers.
 //
-// Warps.  0: TMA of K and V pages into a ring of tiles.  1: one thread issues
-// the products, QK(x + 2) behind PV(x), so that the tensor pipe works on later
-// tiles' scores while the softmax of one runs (S and P share three buffers).  2, 3: the next
-// unit's Q, when its rows are few.  4-7, softmax: one thread a row, scores to weights, running
-// maximum and sum.  8-11 (and 12-15 for D = 256, 128 columns each), sums:
-// one thread a row, acc = acc * 2^(m_old - m_new) + O_tile, and the state's store.
+// Warps.  0: TMA of K and V pages into a ring of tiles.  1 and 2: one thread
+// issues the scores' products, one the values' (S and P share three buffers, so scores run
+// ahead while the softmax of a tile runs).  3: the next unit's Q, when its rows are few.
+// Then one or two warpgroups of softmax, a thread a row: scores to weights, running maximum
+// and sum; two groups take turns at the tiles and hand the maximum on.  Then
+// one (D = 256: two, 128 columns each) of sums, a thread a row:
+// acc = acc * 2^(m_old - m_new) + O_tile, and the state's store.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -170,15 +171,17 @@ struct PGeo {
   static constexpr bool FAC_TMEM = F0 + NS <= 512;
   static constexpr int AC = D < 128 ? D : 128;    // columns a sum thread holds
   static constexpr int SUMG = D / AC;             // sum warpgroups
-  static constexpr int THREADS = 256 + 128 * SUMG;
+  static constexpr int SOFTG = D >= 256 ? 1 : 2;  // softmax warpgroups, taking turns at the tiles
+  static constexpr int GROUPS = 1 + SOFTG + SUMG;
+  static constexpr int THREADS = 128 * GROUPS;
   // Registers a thread: at launch, then by role (setmaxnreg); the roles'
   // sum over the warpgroups stays within the launch's.
-  static constexpr int REG_LAUNCH = SUMG == 1 ? 168 : 128;
-  static constexpr int REG_LOAD = SUMG == 1 ? 72 : 64;
-  static constexpr int REG_SOFT = SUMG == 1 ? 232 : 128;
-  static constexpr int REG_SUM = SUMG == 1 ? 200 : 160;
+  static constexpr int REG_LAUNCH = 128;
+  static constexpr int REG_LOAD = 64;
+  static constexpr int REG_SOFT = SOFTG == 1 ? 96 : 136;
+  static constexpr int REG_SUM = 176;
   static_assert(F0 <= 512, "tensor memory");
-  static_assert(REG_LOAD + REG_SOFT + SUMG * REG_SUM <= (2 + SUMG) * REG_LAUNCH, "registers");
+  static_assert(REG_LOAD + SOFTG * REG_SOFT + SUMG * REG_SUM <= GROUPS * REG_LAUNCH, "registers");
   static_assert(THREADS * REG_LAUNCH <= 65536, "registers");
 };
 
@@ -194,15 +197,22 @@ struct PrefixSmem {
   uint8_t q[2 * G::QTERM];
   uint8_t ring[G::RING * G::TILE];
   uint64_t full[G::RING], empty[G::RING];
-  uint64_t s_full[G::NS], p_full[G::NS], pv_done[G::NS];
-  uint64_t o_free, q_full[2], q_free[2], drain;
+  uint64_t s_full[G::NS], p_full[G::NS], pv_done[G::NS], o_free[G::NS];
+  uint64_t q_full[2], q_free[2], drain[2];
+  uint64_t m_ready[4], l_ready[2][4];                    // by warp of a warpgroup
   float row_scale[kPrefixRows];                          // qscale * 2^e, by row of the Q buffer
   float fac[G::FAC_TMEM ? 1 : G::NS * kPrefixRows];      // 2^(m_old - m_new) of a tile's rows
+  // two softmax warpgroups: the running maximum from one tile to the next, and
+  // the sum of the one that does not end the part
+  float m[G::SOFTG == 1 ? 1 : kPrefixRows], l[G::SOFTG == 1 ? 1 : 2 * kPrefixRows],
+      m_last[G::SOFTG == 1 ? 1 : 2 * kPrefixRows];
   int cum[MAXB + 1];                                     // own-key tiles before sequence b
   int len[MAXB], qp[MAXB];                               // seq_info
   int bad[8];                                            // per tile (mod 8): masked boxes of keys
   int warp_sum[16];
   int lo, hi;                                            // prefix keys some row sees
+  int first[4];                                          // where the CTA's run starts: b, h, rt, i0
+  int run;                                               // its tiles
   int abort;
   uint32_t tmem;
 };
@@ -210,13 +220,22 @@ static_assert(sizeof(PrefixSmem<64>) <= kSmemLimit && sizeof(PrefixSmem<128>) <=
                   sizeof(PrefixSmem<256>) <= kSmemLimit,
               "shared memory");
 
-__device__ __forceinline__ long long part_start(int c, long long total, int ctas) {
-  return (long long)c * total / ctas;
+// a / b, without the long division where 32 bits hold a.
+__device__ __forceinline__ long long div_small(long long a, int b) {
+  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
-// The CTA whose run holds tile g.
-__device__ __forceinline__ int part_cta(long long g, long long total, int ctas) {
-  return (int)(((g + 1) * ctas - 1) / total);
-}
+// The list of tiles is cut into runs of share + 1 tiles (the first rem CTAs) and share.
+struct Split {
+  long long share;
+  int rem;
+  __device__ __forceinline__ long long start(int c) const { return c * share + min(c, rem); }
+  // The CTA whose run holds tile g.
+  __device__ __forceinline__ int cta(long long g) const {
+    const long long longer = rem * (share + 1);
+    return g < longer ? (int)div_small(g, (int)share + 1)
+                      : rem + (int)div_small(g - longer, (int)share);
+  }
+};
 
 // The parts of units that a CTA's run [g0, g1) of the tile list is made of,
 // one after the other.  Part: rows [r0, r0 + nr) of kv head h (r0 counts the
@@ -227,47 +246,21 @@ struct Cursor {
   static constexpr int KT = PGeo<D>::KT;
   const PrefixParams& p;
   const PrefixSmem<D>& s;
-  long long left;        // tiles of the run from this part on
-  int P, pn;             // prefix keys; tiles of a prefix unit
+  int left;              // tiles of the run from this part on
+  int P;                 // prefix keys
   int k = 0;             // parts so far
   int h, b, rt;          // b < 0: prefix; rt: tile of rows
   int r0, nr;
   int base, klo, khi;    // keys [klo, khi) may be seen
   int unit_n, i0, n;
 
-  __device__ __forceinline__ Cursor(const PrefixParams& p_, const PrefixSmem<D>& s_, long long tp,
-                                    long long g0, long long g1)
-      : p(p_), s(s_), left(g1 - g0), P(p_.prefix_pages << p_.log2_bs) {
-    const int pt0 = s.lo / KT;
-    pn = s.hi > s.lo ? (s.hi + KT - 1) / KT - pt0 : 0;
-    h = b = rt = r0 = nr = base = klo = khi = unit_n = i0 = n = 0;
-    if (left <= 0) return;
-    if (g0 < tp) {
-      const int u = (int)(g0 / pn);
-      i0 = (int)(g0 - (long long)u * pn);
-      h = u / p.row_tiles;
-      rt = u - h * p.row_tiles;
-      b = -1;
-    } else {
-      const int units1 = p.Hkv * p.own_tiles;
-      const long long x = (g0 - tp) / units1;  // sequence b holds it: cum[b] <= x < cum[b + 1]
-      int lo = 0, hi = p.B;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s.cum[mid] <= x)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      b = lo;
-      const long long in = g0 - tp - (long long)s.cum[lo] * units1;
-      const int each = s.cum[lo + 1] - s.cum[lo];
-      const int u = (int)(in / each);
-      i0 = (int)(in - (long long)u * each);
-      h = u / p.own_tiles;
-      rt = u - h * p.own_tiles;
-    }
-    enter();
+  __device__ __forceinline__ Cursor(const PrefixParams& p_, const PrefixSmem<D>& s_)
+      : p(p_), s(s_), left(s_.run), P(p_.prefix_pages << p_.log2_bs) {
+    b = s.first[0];
+    h = s.first[1];
+    rt = s.first[2];
+    i0 = s.first[3];
+    if (left > 0) enter();
   }
   __device__ __forceinline__ bool done() const { return left <= 0; }
   __device__ __forceinline__ bool whole() const { return n == unit_n; }
@@ -279,7 +272,7 @@ struct Cursor {
       klo = s.lo;
       khi = s.hi;
       base = klo / KT * KT;
-      unit_n = pn;
+      unit_n = (khi + KT - 1) / KT - klo / KT;
     } else {
       nr = min(kPrefixRows, p.R1 - r0);
       key_range(p, s.len[b], s.qp[b], 0, p.T - 1, klo, khi);
@@ -287,7 +280,7 @@ struct Cursor {
       base = P + (klo - P) / KT * KT;
       unit_n = s.cum[b + 1] - s.cum[b];
     }
-    n = (int)min((long long)(unit_n - i0), left);
+    n = min(unit_n - i0, left);
   }
   __device__ __forceinline__ void next() {
     left -= n;
@@ -358,6 +351,44 @@ __device__ int make_plan(const PrefixParams& p, PrefixSmem<D>& s) {
   return flags;
 }
 
+// Where the run that starts at tile g begins: sequence (-1: the prefix), kv
+// head, tile of rows, tile of the unit.  pn: tiles of a prefix unit, tp: of the
+// whole prefix.
+template <int D>
+__device__ void find_first(const PrefixParams& p, PrefixSmem<D>& s, long long g, int pn,
+                           long long tp) {
+  int b, each, u, tiles;
+  if (g < tp) {
+    b = -1;
+    each = pn;
+    tiles = p.row_tiles;
+    u = (int)div_small(g, pn);
+    g -= (long long)u * pn;
+  } else {
+    g -= tp;
+    const int units1 = p.Hkv * p.own_tiles;
+    const long long x = div_small(g, units1);  // sequence b holds it: cum[b] <= x < cum[b + 1]
+    int hi = p.B;
+    b = 0;
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
+      if (s.cum[mid] <= x)
+        b = mid;
+      else
+        hi = mid;
+    }
+    each = s.cum[b + 1] - s.cum[b];
+    tiles = p.own_tiles;
+    g -= (long long)s.cum[b] * units1;
+    u = (int)div_small(g, each);
+    g -= (long long)u * each;
+  }
+  s.first[0] = b;
+  s.first[1] = u / tiles;
+  s.first[2] = u % tiles;
+  s.first[3] = (int)g;
+}
+
 // A wait that gives up sets the abort flag; every role then leaves its loop.
 template <int D>
 __device__ __forceinline__ bool wait_or_abort(const PrefixParams& p, PrefixSmem<D>& s,
@@ -406,11 +437,11 @@ struct Loader {
                             : p.block_table[(long long)c.b * p.max_blocks + col];
     return blk == p.num_blocks ? -1 : blk;
   }
-  // x: the tile's number in the CTA's run.
-  __device__ __forceinline__ bool issue(const Cursor<D>& c, int j, int x, int blk, bool is_v) {
+  // The tile of kv head h whose first key is k0, number x of the CTA's run.
+  __device__ __forceinline__ bool issue(int h, int k0, int x, int blk, bool is_v) {
     const int lane = threadIdx.x & 31, slot = r % G::RING;
     if (r >= G::RING && !warp_wait<D>(p, s, &s.empty[slot], (r / G::RING - 1) & 1)) return false;
-    const int k0 = c.base + (c.i0 + j) * G::KT + sub * p.box_rows;
+    k0 += sub * p.box_rows;
     int row = p.num_blocks << p.log2_bs;
     const bool bad = blk < 0 || blk > p.num_blocks;
     if (!bad && blk < p.num_blocks) row = (blk << p.log2_bs) + (k0 & (p.bs - 1));
@@ -425,29 +456,27 @@ struct Loader {
     __syncwarp();
     if (sub >= 0 && !skip)
       tma_load_4d(s.ring + slot * G::TILE + slice * (G::KT * 128) + sub * p.box_rows * 128,
-                  is_v ? &p.tm_v : &p.tm_k, &s.full[slot], 0, row, slice, c.h);
+                  is_v ? &p.tm_v : &p.tm_k, &s.full[slot], 0, row, slice, h);
     ++r;
     return true;
   }
-  __device__ __forceinline__ void run(long long tp, long long g0, long long g1) {
-    Cursor<D> ck(p, s, tp, g0, g1), cv = ck;
-    const int tiles = (int)(g1 - g0);
+  __device__ __forceinline__ void run() {
+    Cursor<D> ck(p, s), cv = ck;
+    const int tiles = s.run;
     int jk = 0, jv = 0, blk = ck.done() ? 0 : block(ck, 0);
     auto next_k = [&](int x) {  // K of tile x; its block id was fetched a step ago
       if (x >= tiles) return true;
-      const int now = blk;
-      const Cursor<D> c = ck;
-      const int j = jk;
+      const int now = blk, h = ck.h, k0 = ck.base + (ck.i0 + jk) * G::KT;
       if (++jk == ck.n) {
         jk = 0;
         ck.next();
       }
       if (!ck.done()) blk = block(ck, jk);
-      return issue(c, j, x, now, false);
+      return issue(h, k0, x, now, false);
     };
     if (!next_k(0) || !next_k(1)) return;
     for (int x = 0; x < tiles; ++x) {
-      if (!issue(cv, jv, x, block(cv, jv), true)) return;
+      if (!issue(cv.h, cv.base + (cv.i0 + jv) * G::KT, x, block(cv, jv), true)) return;
       if (++jv == cv.n) {
         jv = 0;
         cv.next();
@@ -460,95 +489,123 @@ struct Loader {
 // ------------------------------------------------------------------ Q
 // Rows [first, last) of a part's Q into shared memory by one warp: the power
 // of two that brings a row's largest value to [2^9, 2^10), then two f16 terms.
+// A lane takes 8 values, D / 8 lanes a row: 16-byte stores.
 template <int D>
 __device__ void load_q_rows(const PrefixParams& p, PrefixSmem<D>& s, const Cursor<D>& c, int first,
                             int last) {
-  constexpr int V = D / 32;  // values of a lane
-  constexpr int BATCH = D >= 256 ? 4 : 8;
-  const int lane = threadIdx.x & 31;
-  for (int i0 = first; i0 < last; i0 += 32) {
-    int seq, tok;
-    const int mine = i0 + lane < last ? c.out_row(i0 + lane, seq, tok) : 0;
-    for (int u0 = 0; u0 < min(32, last - i0); u0 += BATCH) {
-      float x[BATCH][V];
+  constexpr int LR = D / 8;        // lanes of a row
+  constexpr int RW = 32 / LR;      // rows of a step
+  constexpr int BATCH = 4;         // steps in flight
+  const int lane = threadIdx.x & 31, sub = lane / LR, d = lane % LR * 8;
+  if (first >= last) return;
+  int seq, tok;
+  // the row each lane addresses for the warp: first + lane, past the last one the last
+  const int mine = c.out_row(min(first + lane, last - 1), seq, tok);
+  const int n = last - first;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += RW * BATCH) {
+    float4 x[BATCH][2];
 #pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        // rows past the last one repeat it
-        const int at = __shfl_sync(0xffffffffu, mine, min(u0 + u, last - i0 - 1));
-        const float* src = p.q + (long long)at * D + lane * V;
+    for (int u = 0; u < BATCH; ++u) {
+      const int at = __shfl_sync(0xffffffffu, mine, min(i0 + u * RW + sub, 31));
+      const float4* src = reinterpret_cast<const float4*>(p.q + (long long)at * D + d);
+      x[u][0] = src[0];
+      x[u][1] = src[1];
+    }
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          const float2 f = *reinterpret_cast<const float2*>(src + i);
-          x[u][i] = f.x;
-          x[u][i + 1] = f.y;
-        }
-      }
+    for (int u = 0; u < BATCH; ++u) {
+      const int row = c.q_row() + first + min(i0 + u * RW + sub, n - 1);
+      const float v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w,
+                          x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+      float m = 0.f;
 #pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        const int row = c.q_row() + min(i0 + u0 + u, last - 1);
-        float m = 0.f;
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
 #pragma unroll
-        for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(x[u][i]));
-        m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-        // exponent of the largest value, clamped so that both powers are normal
-        int e = (int)(__float_as_uint(m) >> 23) - 127;
-        e = min(max(e, -100), 120);
-        const float f = __uint_as_float((uint32_t)(9 - e + 127) << 23);
-        if (lane == 0) s.row_scale[row] = p.qscale * __uint_as_float((uint32_t)(e - 9 + 127) << 23);
+      for (int o = LR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // exponent of the largest value, clamped so that both powers are normal
+      int e = (int)(__float_as_uint(m) >> 23) - 127;
+      e = min(max(e, -100), 120);
+      const float f = __uint_as_float((uint32_t)(9 - e + 127) << 23);
+      if (d == 0) s.row_scale[row] = p.qscale * __uint_as_float((uint32_t)(e - 9 + 127) << 23);
+      uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          uint32_t hi, lo;
-          split_half2(x[u][i] * f, x[u][i + 1] * f, hi, lo);
-          const int d = lane * V + i;
-          const int at = (d >> 6) * (kPrefixRows * 128) + row * 128 +
-                         ((((d & 63) >> 3) ^ (row & 7)) << 4) + (d & 7) * 2;
-          *reinterpret_cast<uint32_t*>(s.q + at) = hi;
-          *reinterpret_cast<uint32_t*>(s.q + PGeo<D>::QTERM + at) = lo;
-        }
-      }
+      for (int i = 0; i < 4; ++i) split_half2(v[2 * i] * f, v[2 * i + 1] * f, hi[i], lo[i]);
+      const int at = (d >> 6) * (kPrefixRows * 128) + row * 128 + ((((d & 63) >> 3) ^ (row & 7)) << 4);
+      *reinterpret_cast<uint4*>(s.q + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(s.q + PGeo<D>::QTERM + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
   fence_proxy_async_smem();
   __syncwarp();
 }
 
-// Warps 2 and 3: Q of the parts with few rows, one part ahead of the products.
+// Warp 3: Q of the parts with few rows, one part ahead of the products.  The
+// softmax warps load the others; this warp waits for and passes those too: a
+// barrier's parity names a phase only to a warp that no phase can leave behind.
 template <int D>
-__device__ void q_loop(const PrefixParams& p, PrefixSmem<D>& s, long long tp, long long g0,
-                       long long g1) {
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 2;
+__device__ void q_loop(const PrefixParams& p, PrefixSmem<D>& s) {
+  const int lane = threadIdx.x & 31;
   bool prev_small = true;
-  for (Cursor<D> c(p, s, tp, g0, g1); !c.done(); c.next()) {
+  for (Cursor<D> c(p, s); !c.done(); c.next()) {
     const int k = c.k;
-    if (c.small()) {
-      // the half's last user, and a part of many rows just before
-      if (k >= 2 && !warp_wait<D>(p, s, &s.q_free[k & 1], ((k - 2) >> 1) & 1)) return;
-      if (!prev_small && !warp_wait<D>(p, s, &s.q_free[(k - 1) & 1], ((k - 1) >> 1) & 1)) return;
-      const int half = (c.nr + 1) / 2;
-      load_q_rows<D>(p, s, c, w * half, min(c.nr, (w + 1) * half));
-      if (lane < 2) mbar_arrive(&s.q_full[k & 1]);  // two of the barrier's four
+    const bool small = c.small();
+    // a part of many rows takes the whole buffer, one of few the half of part k - 2
+    if (k >= 2 && !warp_wait<D>(p, s, &s.q_free[k & 1], ((k - 2) >> 1) & 1)) return;
+    if (k >= 1 && !(small && prev_small) &&
+        !warp_wait<D>(p, s, &s.q_free[(k - 1) & 1], ((k - 1) >> 1) & 1))
+      return;
+    if (small) {
+      load_q_rows<D>(p, s, c, 0, min(c.nr, 32));
+      load_q_rows<D>(p, s, c, 32, c.nr);
     }
-    prev_small = c.small();
+    // its own arrival, and for few rows those of the softmax warps
+    if (lane < 1 + (small ? 4 * PGeo<D>::SOFTG : 0)) mbar_arrive(&s.q_full[k & 1]);
+    prev_small = small;
   }
 }
 
 // ------------------------------------------------------------------ softmax warps
+// Largest of 32 scores a lane, four chains.
+__device__ __forceinline__ float max32(const float* v) {
+  float mx[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mx[i] = v[i];
+#pragma unroll
+  for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+// N columns of this warp's lanes, a multiple of 32, waited for.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, float* v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 32) tmem_ld32(addr + i, v + i);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; i += 32) tmem_loaded32(v + i);
+}
+
 template <int D, bool CAP>
-__device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s, long long tp, long long g0,
-                             long long g1) {
+__device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   using G = PGeo<D>;
   constexpr int KT = G::KT;
+  constexpr bool TWO = G::SOFTG == 2;
+  constexpr int CH = TWO ? 64 : 32;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+  const int group = TWO ? (threadIdx.x >> 7) - 1 : 0;  // takes the tiles x = group mod 2
   const int row = w * 32 + lane;
   const uint32_t lanes = s.tmem + ((uint32_t)(w * 32) << 16);
   const int box_shift = __ffs(p.box_rows) - 1;
-  int x = 0;  // tiles so far
-  for (Cursor<D> c(p, s, tp, g0, g1); !c.done(); c.next()) {
+  int x0 = 0;                // tiles of the parts before
+  int shared_sums[2] = {0, 0};  // parts so far, by parity, whose sum took both groups
+  for (Cursor<D> c(p, s); !c.done(); x0 += c.n, c.next()) {
     const int k = c.k;
     if (!c.small()) {
       // many rows: they take the whole buffer
       if (k >= 1 && !warp_wait<D>(p, s, &s.q_free[(k - 1) & 1], ((k - 1) >> 1) & 1)) return;
-      load_q_rows<D>(p, s, c, min(c.nr, w * 32), min(c.nr, w * 32 + 32));
+      constexpr int ROWS = kPrefixRows / (4 * G::SOFTG);
+      const int first = (group * 4 + w) * ROWS;
+      load_q_rows<D>(p, s, c, min(c.nr, first), min(c.nr, first + ROWS));
       if (lane == 0) mbar_arrive(&s.q_full[k & 1]);
     }
     const bool any = w * 32 < c.nr;  // rows of this warp
@@ -565,32 +622,37 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s, long long 
     }
     float scale = 0.f, m = -kInf, l = 0.f;
     bool partial = false;
-    for (int j = 0; j < c.n; ++j, ++x) {
-      const int buf = x % G::NS;
+    const int j0 = TWO ? (x0 ^ group) & 1 : 0;  // this group's first tile of the part
+    if (j0 >= c.n) {
+      // it has none; the part's Q is there once all have left part k - 2
+      if (!warp_wait<D>(p, s, &s.q_full[k & 1], (k >> 1) & 1)) return;
+      if (lane == 0) mbar_arrive(&s.q_free[k & 1]);
+    }
+    for (int j = j0; j < c.n; j += G::SOFTG) {
+      const int x = x0 + j, buf = x % G::NS;
       if (!warp_wait<D>(p, s, &s.s_full[buf], (x / G::NS) & 1)) return;
-      if (j == 0) {
+      if (j == j0) {
         if (on) scale = s.row_scale[c.q_row() + row];
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.q_free[k & 1]);
       }
+      const uint32_t sa = lanes + G::S0 + buf * KT;
+      const int k0 = c.base + (c.i0 + j) * KT;
+      const float cc = CAP ? 1.f : scale;
+      bool masked = false;
+      float top = -kInf;
       if (any) {
         tc5_fence_after();
-        const uint32_t sa = lanes + G::S0 + buf * KT;
-        const int k0 = c.base + (c.i0 + j) * KT;
         const int bad = s.bad[x & 7];
-        const bool masked =
-            !__all_sync(0xffffffffu, (!on || (lo <= k0 && hi >= k0 + KT)) && bad == 0);
+        masked = !__all_sync(0xffffffffu, (!on || (lo <= k0 && hi >= k0 + KT)) && bad == 0);
         partial |= masked;
-        // Two passes over the scores, 32 columns at a time: a loop that stays in the
-        // instruction cache and needs few registers.
-        float top = m;
+        // Two passes over the scores, CH columns a step: loops that stay in the
+        // instruction cache and need few registers.
+        if (CAP || masked) {
 #pragma unroll 1
-        for (int i0 = 0; i0 < KT; i0 += 32) {
-          float v[32];
-          tmem_ld32(sa + i0, v);
-          tmem_wait_ld();
-          tmem_loaded32(v);
-          if (CAP || masked) {
+          for (int i0 = 0; i0 < KT; i0 += 32) {
+            float v[32];
+            tmem_load<32>(sa + i0, v);
             if (CAP) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = capped(v[i] * scale, p.softcap2, p.softcap_inv);
@@ -602,50 +664,100 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s, long long 
                 if (i < a || i >= z || ((bad >> ((i0 + i) >> box_shift)) & 1)) v[i] = -kInf;
             }
             tmem_st32(sa + i0, v);
+            top = fmaxf(top, max32(v));
           }
-          float mx[4];
+          tmem_wait_st();
+        } else {
+#pragma unroll 1
+          for (int i0 = 0; i0 < KT; i0 += CH) {
+            float v[CH];
+            tmem_load<CH>(sa + i0, v);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = v[i];
-#pragma unroll
-          for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
-          top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (CAP ? 1.f : scale));
+            for (int h = 0; h < CH; h += 32) top = fmaxf(top, max32(v + h));
+          }
         }
-        if (CAP || masked) tmem_wait_st();
+      }
+      // the maximum up to the tile before, from the other group; then this one's to it
+      float before = m;
+      if (TWO) {
+        if (x > 0 && !warp_wait<D>(p, s, &s.m_ready[w], (x - 1) & 1)) return;
+        before = j > 0 ? s.m[row] : -kInf;
+      }
+      const float now = fmaxf(before, top * cc);
+      if (TWO) {
+        s.m[row] = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.m_ready[w]);
+      }
+      if (any) {
         // no key so far: any finite reference does
-        const float ref = top == -kInf ? 0.f : top;
-        const float f = ex2_ftz(m - ref);
-        m = top;
+        const float ref = now == -kInf ? 0.f : now;
+        const float f = ex2_ftz(before - ref);  // for the sums up to the tile before
         if constexpr (G::FAC_TMEM)
           tmem_st1(lanes + G::F0 + buf, f);
         else
           s.fac[buf * kPrefixRows + row] = f;
-        const float cc = CAP ? 1.f : scale, base = ref - kShift;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float base = ref - kShift;
+        const float2 cc2 = make_float2(cc, cc), base2 = make_float2(-base, -base);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll 1
-        for (int i0 = 0; i0 < KT; i0 += 32) {
-          float v[32];
-          uint32_t ph[16], pl[16];
-          tmem_ld32(sa + i0, v);
-          tmem_wait_ld();
-          tmem_loaded32(v);
+        for (int i0 = 0; i0 < KT; i0 += CH) {
+          float v[CH];
+          tmem_load<CH>(sa + i0, v);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float p0 = ex2_ftz(fmaf(v[i], cc, -base));
-            const float p1 = ex2_ftz(fmaf(v[i + 1], cc, -base));
-            sum[i & 2] += p0;
-            sum[(i & 2) + 1] += p1;
-            split_half2(p0, p1, ph[i / 2], pl[i / 2]);
+          for (int h = 0; h < CH; h += 32) {
+            uint32_t ph[16], pl[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float2 e = fma2(make_float2(v[h + i], v[h + i + 1]), cc2, base2);
+              e.x = ex2_ftz(e.x);
+              e.y = ex2_ftz(e.y);
+              if (i & 2)
+                sum1 = add2(sum1, e);
+              else
+                sum0 = add2(sum0, e);
+              const __half2 hh = __floats2half2_rn(e.x, e.y);
+              const float2 hf = __half22float2(hh);
+              const float2 r = add2(e, make_float2(-hf.x, -hf.y));
+              const __half2 hl = __floats2half2_rn(r.x, r.y);
+              ph[i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+              pl[i / 2] = *reinterpret_cast<const uint32_t*>(&hl);
+            }
+            // the weights of 32 keys take the columns of their scores: 16 of high terms,
+            // 16 of low
+            tmem_st16(sa + i0 + h, ph);
+            tmem_st16(sa + i0 + h + 16, pl);
           }
-          // the weights of 32 keys take the columns of their scores: 16 of high terms, 16 of low
-          tmem_st16(sa + i0, ph);
-          tmem_st16(sa + i0 + 16, pl);
         }
-        l = fmaf(l, f, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        // l counts against `now`, so far against this group's last maximum m
+        l = fmaf(l, ex2_ftz(m - ref), (sum0.x + sum0.y) + (sum1.x + sum1.y));
         tmem_wait_st();
         tc5_fence_before();
       }
+      m = now;
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.p_full[buf]);
+    }
+    if (TWO && c.n > 1) {
+      // the group of the part's last tile adds the other's sum to its own
+      const int q = k & 1;
+      float* slot = s.l + q * kPrefixRows + row;
+      if (((x0 + c.n - 1) & 1) != group) {
+        *slot = partial ? -l : l;
+        // its reference: the maximum it saw last, which s.m may have passed
+        s.m_last[q * kPrefixRows + row] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.l_ready[q][w]);
+        ++shared_sums[q];
+        continue;
+      }
+      if (!warp_wait<D>(p, s, &s.l_ready[q][w], shared_sums[q] & 1)) return;
+      ++shared_sums[q];
+      const float lx = *slot, mx = s.m_last[q * kPrefixRows + row];
+      partial |= signbit(lx) != 0;
+      l = fmaf(fabsf(lx), ex2_ftz(mx - (m == -kInf ? 0.f : m)), l);
+    } else if (TWO && j0 != 0) {
+      continue;  // the one tile was the other group's
     }
     if (on) {
       float2* dst;
@@ -662,15 +774,14 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s, long long 
 
 // ------------------------------------------------------------------ sum warps
 template <int D>
-__device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s, long long tp, long long g0,
-                         long long g1) {
+__device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   using G = PGeo<D>;
   constexpr int C = G::AC;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
-  const int row = w * 32 + lane, col = ((int)(threadIdx.x >> 7) - 2) * C;
+  const int row = w * 32 + lane, col = ((int)(threadIdx.x >> 7) - 1 - G::SOFTG) * C;
   const uint32_t lanes = s.tmem + ((uint32_t)(w * 32) << 16);
   int x = 0;
-  for (Cursor<D> c(p, s, tp, g0, g1); !c.done(); c.next()) {
+  for (Cursor<D> c(p, s); !c.done(); c.next()) {
     const bool any = w * 32 < c.nr, on = row < c.nr;
     float acc[C];
 #pragma unroll
@@ -705,7 +816,7 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s, long long tp, 
         tc5_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.o_free);
+      if (lane == 0) mbar_arrive(&s.o_free[buf]);
     }
     if (on) {
       float* dst;
@@ -723,63 +834,75 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s, long long tp, 
   }
 }
 
-// ------------------------------------------------------------------ MMA thread
+// ------------------------------------------------------------------ MMA threads
+// One thread issues the scores' products and another the values', so that
+// one's waits do not hold up the other's.  The low terms go first: their
+// steps truncate at their own size.  Place of a tile's K and V in the ring's order:
+// K(0) K(1) V(0) K(2) V(1) ... K(n - 1) V(n - 2) V(n - 1).
+__device__ __forceinline__ int k_place(int x) { return x < 2 ? x : 2 * x - 1; }
+__device__ __forceinline__ int v_place(int x, int tiles) {
+  return x < tiles - 1 ? 2 * x + 2 : 2 * x + 1;
+}
+
 template <int D>
-__device__ void mma_loop(const PrefixParams& p, PrefixSmem<D>& s, long long tp, long long g0,
-                         long long g1) {
+__device__ void qk_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   using G = PGeo<D>;
   constexpr int KT = G::KT;
-  constexpr uint32_t id_qk = f16_idesc(KT, false), id_pv = f16_idesc(D, true);
-  const uint32_t tm = s.tmem, q0 = smem_u32(s.q), ring = smem_u32(s.ring);
-  Cursor<D> c(p, s, tp, g0, g1);  // of the scores
-  const int tiles = (int)(g1 - g0);
-  int r = 0;  // ring tiles taken
-  int jq = 0;
-  auto qk = [&](int y) {  // scores of tile y; the low term first: its steps truncate at its size
-    if (y >= tiles) return true;
-    const int slot = r % G::RING, buf = y % G::NS;
-    if (jq == 0 && !wait_or_abort<D>(p, s, &s.q_full[c.k & 1], (c.k >> 1) & 1)) return false;
-    if (y >= G::NS && !wait_or_abort<D>(p, s, &s.pv_done[buf], (y / G::NS - 1) & 1)) return false;
-    if (!wait_or_abort<D>(p, s, &s.full[slot], (r / G::RING) & 1)) return false;
-    tc5_fence_after();
-    const uint32_t k = ring + slot * G::TILE, q = q0 + c.q_row() * 128;
+  constexpr uint32_t idesc = f16_idesc(KT, false);
+  const uint32_t tm = s.tmem + G::S0;
+  const uint64_t q0 = smem_desc(smem_u32(s.q), 16, 1024);
+  const uint64_t k0 = smem_desc(smem_u32(s.ring), 16, 1024);
+  int x = 0;
+  for (Cursor<D> c(p, s); !c.done(); c.next()) {
+    if (!wait_or_abort<D>(p, s, &s.q_full[c.k & 1], (c.k >> 1) & 1)) return;
+    const uint64_t q = q0 + c.q_row() * 8;  // 128 bytes a row
+    for (int j = 0; j < c.n; ++j, ++x) {
+      const int place = k_place(x), slot = place % G::RING, buf = x % G::NS;
+      if (!wait_or_abort<D>(p, s, &s.full[slot], (place / G::RING) & 1)) return;
+      // the buffer's last tile is summed up: its weights and its factor are read
+      if (x >= G::NS && !wait_or_abort<D>(p, s, &s.o_free[buf], (x / G::NS - 1) & 1)) return;
+      tc5_fence_after();
+      const uint64_t k = k0 + slot * (G::TILE / 16);
+      // a loop over 128-byte slices: unrolled further, its descriptors would spill
+#pragma unroll 1
+      for (int i = 0; i < 2 * G::SL; ++i) {
+        const int term = i < G::SL ? 1 : 0, slice = i < G::SL ? i : i - G::SL;
+        const uint64_t qd = q + (term * G::QTERM + slice * (kPrefixRows * 128)) / 16;
+        const uint64_t kd = k + slice * (KT * 128 / 16);
 #pragma unroll
-    for (int term = 1; term >= 0; --term)
-#pragma unroll
-      for (int d = 0; d < D; d += 16)
-        mma_ss(tm + G::S0 + buf * KT,
-               smem_desc(q + term * G::QTERM + (d >> 6) * (kPrefixRows * 128) + (d & 63) * 2, 16,
-                         1024),
-               smem_desc(k + (d >> 6) * (KT * 128) + (d & 63) * 2, 16, 1024), id_qk,
-               term == 0 || d > 0);
-    mma_commit(&s.empty[slot]);
-    mma_commit(&s.s_full[buf]);
-    ++r;
-    if (++jq == c.n) {
-      jq = 0;
-      mma_commit(&s.q_free[c.k & 1]);
-      c.next();
+        for (int u = 0; u < 4; ++u)  // 16 values: 32 bytes
+          mma_ss(tm + buf * KT, qd + u * 2, kd + u * 2, idesc, i + u > 0);
+      }
+      mma_commit(&s.s_full[buf]);
+      mma_commit(&s.empty[slot]);
     }
-    return true;
-  };
-  if (!qk(0) || !qk(1)) return;
+    mma_commit(&s.q_free[c.k & 1]);
+  }
+}
+
+template <int D>
+__device__ void pv_loop(const PrefixParams& p, PrefixSmem<D>& s) {
+  using G = PGeo<D>;
+  constexpr int KT = G::KT;
+  constexpr uint32_t idesc = f16_idesc(D, true);
+  const uint32_t tm = s.tmem;
+  const uint64_t v0 = smem_desc(smem_u32(s.ring), KT * 128, 1024);
+  const int tiles = s.run;
   for (int x = 0; x < tiles; ++x) {
-    const int buf = x % G::NS, slot = r % G::RING;
-    if (!wait_or_abort<D>(p, s, &s.full[slot], (r / G::RING) & 1)) return;
+    const int place = v_place(x, tiles), slot = place % G::RING, buf = x % G::NS;
+    if (!wait_or_abort<D>(p, s, &s.full[slot], (place / G::RING) & 1)) return;
+    if (x > 0 && !wait_or_abort<D>(p, s, &s.o_free[(x - 1) % G::NS], ((x - 1) / G::NS) & 1)) return;
     if (!wait_or_abort<D>(p, s, &s.p_full[buf], (x / G::NS) & 1)) return;
-    if (x > 0 && !wait_or_abort<D>(p, s, &s.o_free, (x - 1) & 1)) return;
     tc5_fence_after();
-    const uint32_t v = ring + slot * G::TILE;
+    const uint64_t v = v0 + slot * (G::TILE / 16);
 #pragma unroll
     for (int term = 1; term >= 0; --term)
 #pragma unroll
       for (int k = 0; k < KT; k += 16)
-        mma_ts(tm, tm + G::S0 + buf * KT + k / 32 * 32 + term * 16 + k % 32 / 2,
-               smem_desc(v + k * 128, KT * 128, 1024), id_pv, term == 0 || k > 0);
-    mma_commit(&s.empty[slot]);
+        mma_ts(tm, tm + G::S0 + buf * KT + k / 32 * 32 + term * 16 + k % 32 / 2, v + k * 8, idesc,
+               term == 0 || k > 0);
     mma_commit(&s.pv_done[buf]);
-    ++r;
-    if (!qk(x + 2)) return;
+    mma_commit(&s.empty[slot]);
   }
 }
 
@@ -799,19 +922,22 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 4);
       mbar_init(&s.pv_done[i], 1);
+      mbar_init(&s.o_free[i], 4 * G::SUMG);
     }
-    mbar_init(&s.o_free, 4 * G::SUMG);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.q_full[i], 4);
-      mbar_init(&s.q_free[i], 5);  // the products with it, and the softmax warps' row scales
+      mbar_init(&s.q_full[i], 1 + 4 * G::SOFTG);
+      mbar_init(&s.q_free[i], 1 + 4 * G::SOFTG);  // the products, and the readers of row_scale
+      mbar_init(&s.drain[i], 1);
     }
-    mbar_init(&s.drain, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s.m_ready[i], 1);
+      mbar_init(&s.l_ready[0][i], 1);
+      mbar_init(&s.l_ready[1][i], 1);
+    }
     fence_mbarrier_init();
     s.lo = 0x7fffffff;
     s.hi = 0;
     s.abort = 0;
-  }
-  if (warp == 0 && lane == 0) {
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
   }
@@ -820,28 +946,27 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
   __syncthreads();
   tc5_fence_after();
   const int flags = make_plan<D>(p, s);
-  const int pn = s.hi > s.lo ? (s.hi + G::KT - 1) / G::KT - s.lo / G::KT : 0;
-  const long long tp = (long long)pn * p.Hkv * p.row_tiles;
-  const long long total = tp + (long long)s.cum[p.B] * (p.Hkv * p.own_tiles);
-  const int ctas = (int)min(total, (long long)p.grid);
-  if (blockIdx.x == 0) {
-    if (flags && p.dev_status) atomicOr(p.dev_status, flags);
-    if (tid == 0) {
-      p.ws_plan[0] = pn;
-      p.ws_plan[1] = ctas;
-    }
-    for (int i = tid; i <= p.B; i += G::THREADS) p.ws_plan[2 + i] = s.cum[i];
+  if (blockIdx.x == 0 && flags && p.dev_status) atomicOr(p.dev_status, flags);
+  if (tid == 0) {
+    const int pn = s.hi > s.lo ? (s.hi + G::KT - 1) / G::KT - s.lo / G::KT : 0;
+    const long long tp = (long long)pn * (p.Hkv * p.row_tiles);
+    const long long total = tp + (long long)s.cum[p.B] * (p.Hkv * p.own_tiles);
+    Split sp;
+    sp.share = div_small(total, p.grid);
+    sp.rem = (int)(total - sp.share * p.grid);
+    const long long g0 = sp.start(blockIdx.x);
+    s.run = (int)(sp.share + ((int)blockIdx.x < sp.rem));
+    if (s.run > 0) find_first<D>(p, s, g0, pn, tp);
+    if (blockIdx.x == 0) p.ws_plan[0] = pn;
   }
-  long long g0 = 0, g1 = 0;
-  if ((int)blockIdx.x < ctas) {
-    g0 = part_start(blockIdx.x, total, ctas);
-    g1 = part_start(blockIdx.x + 1, total, ctas);
-  }
+  if (blockIdx.x == 0)
+    for (int i = tid; i <= p.B; i += G::THREADS) p.ws_plan[1 + i] = s.cum[i];
+  __syncthreads();
   if (warp < 4) {
     setmaxnreg_dec<G::REG_LOAD>();
     if (warp == 0) {
       Loader<D> ld(p, s);
-      ld.run(tp, g0, g1);
+      ld.run();
       const int bad = __reduce_or_sync(0xffffffffu, ld.flags);
       if (bad && lane == 0 && p.dev_status) atomicOr(p.dev_status, bad);
       if (*(volatile int*)&s.abort) {
@@ -849,24 +974,30 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
         for (int r = max(0, ld.r - G::RING); r < ld.r; ++r)
           mbar_wait(&s.full[r % G::RING], (r / G::RING) & 1, nullptr, p.wait_ns);
       }
-    } else if (warp == 1) {
+    } else if (warp < 3) {
       if (lane == 0) {
-        mma_loop<D>(p, s, tp, g0, g1);
+        if (warp == 1)
+          qk_loop<D>(p, s);
+        else
+          pv_loop<D>(p, s);
         if (*(volatile int*)&s.abort) {
           // so do the products
-          mma_commit(&s.drain);
-          mbar_wait(&s.drain, 0, nullptr, p.wait_ns);
+          mma_commit(&s.drain[warp - 1]);
+          mbar_wait(&s.drain[warp - 1], 0, nullptr, p.wait_ns);
         }
       }
     } else {
-      q_loop<D>(p, s, tp, g0, g1);
+      q_loop<D>(p, s);
     }
-  } else if (warp < 8) {
-    if constexpr (G::REG_SOFT > G::REG_LAUNCH) setmaxnreg_inc<G::REG_SOFT>();
-    softmax_loop<D, CAP>(p, s, tp, g0, g1);
+  } else if (warp < 4 + 4 * G::SOFTG) {
+    if constexpr (G::REG_SOFT > G::REG_LAUNCH)
+      setmaxnreg_inc<G::REG_SOFT>();
+    else
+      setmaxnreg_dec<G::REG_SOFT>();
+    softmax_loop<D, CAP>(p, s);
   } else {
     setmaxnreg_inc<G::REG_SUM>();
-    sum_loop<D>(p, s, tp, g0, g1);
+    sum_loop<D>(p, s);
   }
   __syncwarp();
   tc5_fence_before();
@@ -891,11 +1022,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int b = bt / p.T, tok = bt - b * p.T;
   const int r1 = tok * p.G + hq - h * p.G;
   const int rb = b * p.R1 + r1;
-  const int pn = p.ws_plan[0], ctas = p.ws_plan[1];
-  const int* cum = p.ws_plan + 2;
+  const int pn = p.ws_plan[0];
+  const int* cum = p.ws_plan + 1;
   const int units1 = p.Hkv * p.own_tiles;
   const long long tp = (long long)pn * p.Hkv * p.row_tiles;
   const long long total = tp + (long long)cum[p.B] * units1;
+  Split sp;
+  sp.share = div_small(total, p.grid);
+  sp.rem = (int)(total - sp.share * p.grid);
   float M = -kInf, L = 0.f, o[V];
   bool partial = false;
 #pragma unroll
@@ -924,7 +1058,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       in_tile = r1 % kPrefixRows;
     }
     if (n == 0) continue;
-    const int c0 = part_cta(g0, total, ctas), c1 = part_cta(g0 + n - 1, total, ctas);
+    const int c0 = sp.cta(g0), c1 = sp.cta(g0 + n - 1);
     if (c0 == c1) {
       if (u == 0)
         add(p.ws_pre_ml[row], p.ws_pre_o + (long long)row * D);
@@ -933,7 +1067,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       continue;
     }
     for (int c = c0; c <= c1; ++c) {
-      const int slot = 2 * c + (c == c0 && part_start(c, total, ctas) != g0 ? 1 : 0);
+      const int slot = 2 * c + (c == c0 && sp.start(c) != g0 ? 1 : 0);
       const long long i = (long long)slot * kPrefixRows + in_tile;
       add(p.ws_cut_ml[i], p.ws_cut_o + i * D);
     }

@@ -144,6 +144,15 @@ def test_batches(B):
     Case(4, B, 15, 3, 64, 16, 320, _lens(r, B, 320, 70)).check()
 
 
+@pytest.mark.parametrize("D,T", [(64, 1), (128, 1), (128, 3), (256, 1)])
+@pytest.mark.parametrize("prefix,most", [(16, 40), (16, 700), (300, 20), (0, 300)])
+def test_many_parts_a_processor(D, T, prefix, most):
+    """So many units that every CTA goes through runs of parts with many rows,
+    of parts with few, and from the ones to the others."""
+    r = np.random.default_rng(prefix + most + D)
+    Case(24, 160, 64, 8, D, 16, prefix, _lens(r, 160, prefix, most) + T - 1, T=T).check()
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("prefix,longest", [(4096, 40), (64, 3000), (0, 5000), (2048, 2048)])
 def test_long_axes(D, prefix, longest):
