@@ -409,10 +409,16 @@ __device__ __forceinline__ bool warp_wait(const PrefixParams& p, PrefixSmem<D>& 
 // K and V tiles into the ring in the order the products take them:
 // K(0) K(1) V(0) K(2) V(1) ...  Each lane copies one box.  Boxes without a
 // visible key and pages outside the pool are filled with zeros by a copy that
-// starts past the pool's last row.
+// starts past the pool's last row.  A tile's block ids are fetched a step before its K is
+// issued and kept until its V is: no copy waits for them.
 template <int D>
 struct Loader {
   using G = PGeo<D>;
+  struct Tile {
+    int h, k0;     // kv head; first key of this lane's box
+    int blk;       // its page, where a key of it may be seen
+    bool seen;
+  };
   const PrefixParams& p;
   PrefixSmem<D>& s;
   int nsl, sub, slice, boxes;
@@ -425,26 +431,32 @@ struct Loader {
     boxes = G::KT / p.box_rows * nsl;
     sub = lane / nsl;
     slice = lane - sub * nsl;
-    if (lane >= boxes) sub = -1;
   }
-  // Block id of this lane's box in tile j of the cursor's part (the load may
-  // run ahead of its use); num_blocks: no key of it is seen.
-  __device__ __forceinline__ int block(const Cursor<D>& c, int j) const {
-    const int k0 = c.base + (c.i0 + j) * G::KT + sub * p.box_rows;
-    if (sub < 0 || k0 >= c.khi || k0 + p.box_rows <= c.klo) return p.num_blocks;
-    const int col = k0 >> p.log2_bs;
-    const int blk = c.b < 0 ? p.prefix_table[col]
-                            : p.block_table[(long long)c.b * p.max_blocks + col];
-    return blk == p.num_blocks ? -1 : blk;
+  __device__ __forceinline__ bool copies() const { return (threadIdx.x & 31) < boxes; }
+  // The cursor's tile j, and the cursor moved on.
+  __device__ __forceinline__ Tile fetch(Cursor<D>& c, int& j) const {
+    Tile t = {0, 0, 0, false};
+    if (c.done()) return t;
+    t.h = c.h;
+    t.k0 = c.base + (c.i0 + j) * G::KT + sub * p.box_rows;
+    t.seen = copies() && t.k0 < c.khi && t.k0 + p.box_rows > c.klo;
+    if (t.seen) {
+      const int* table = c.b < 0 ? p.prefix_table : p.block_table + (long long)c.b * p.max_blocks;
+      t.blk = table[t.k0 >> p.log2_bs];
+    }
+    if (++j == c.n) {
+      j = 0;
+      c.next();
+    }
+    return t;
   }
-  // The tile of kv head h whose first key is k0, number x of the CTA's run.
-  __device__ __forceinline__ bool issue(int h, int k0, int x, int blk, bool is_v) {
+  // K or V of tile number x of the CTA's run.
+  __device__ __forceinline__ bool issue(const Tile& t, int x, bool is_v) {
     const int lane = threadIdx.x & 31, slot = r % G::RING;
     if (r >= G::RING && !warp_wait<D>(p, s, &s.empty[slot], (r / G::RING - 1) & 1)) return false;
-    k0 += sub * p.box_rows;
     int row = p.num_blocks << p.log2_bs;
-    const bool bad = blk < 0 || blk > p.num_blocks;
-    if (!bad && blk < p.num_blocks) row = (blk << p.log2_bs) + (k0 & (p.bs - 1));
+    const bool bad = t.seen && (t.blk < 0 || t.blk >= p.num_blocks);
+    if (t.seen && !bad) row = (t.blk << p.log2_bs) + (t.k0 & (p.bs - 1));
     if (!is_v) {
       const int mask = __reduce_or_sync(0xffffffffu, bad ? 1 << sub : 0);
       if (lane == 0) s.bad[x & 7] = mask;
@@ -454,34 +466,24 @@ struct Loader {
     const bool skip = p.test_skip_arm && blockIdx.x == 0 && r == 0;
     if (lane == 0 && !skip) mbar_arrive_expect_tx(&s.full[slot], G::TILE);
     __syncwarp();
-    if (sub >= 0 && !skip)
+    if (copies() && !skip)
       tma_load_4d(s.ring + slot * G::TILE + slice * (G::KT * 128) + sub * p.box_rows * 128,
-                  is_v ? &p.tm_v : &p.tm_k, &s.full[slot], 0, row, slice, h);
+                  is_v ? &p.tm_v : &p.tm_k, &s.full[slot], 0, row, slice, t.h);
     ++r;
     return true;
   }
   __device__ __forceinline__ void run() {
-    Cursor<D> ck(p, s), cv = ck;
+    Cursor<D> c(p, s);
     const int tiles = s.run;
-    int jk = 0, jv = 0, blk = ck.done() ? 0 : block(ck, 0);
-    auto next_k = [&](int x) {  // K of tile x; its block id was fetched a step ago
-      if (x >= tiles) return true;
-      const int now = blk, h = ck.h, k0 = ck.base + (ck.i0 + jk) * G::KT;
-      if (++jk == ck.n) {
-        jk = 0;
-        ck.next();
-      }
-      if (!ck.done()) blk = block(ck, jk);
-      return issue(h, k0, x, now, false);
-    };
-    if (!next_k(0) || !next_k(1)) return;
+    if (tiles == 0) return;
+    int j = 0;
+    Tile t0 = fetch(c, j), t1 = fetch(c, j), t2 = fetch(c, j);
+    if (!issue(t0, 0, false) || (tiles > 1 && !issue(t1, 1, false))) return;
     for (int x = 0; x < tiles; ++x) {
-      if (!issue(cv.h, cv.base + (cv.i0 + jv) * G::KT, x, block(cv, jv), true)) return;
-      if (++jv == cv.n) {
-        jv = 0;
-        cv.next();
-      }
-      if (!next_k(x + 2)) return;
+      if (!issue(t0, x, true) || (x + 2 < tiles && !issue(t2, x + 2, false))) return;
+      t0 = t1;
+      t1 = t2;
+      t2 = fetch(c, j);
     }
   }
 };
