@@ -431,7 +431,9 @@ int decode_attn_append_paged_rope(const da_params* p, const da_rope_params* r, i
  * workspace: device scratch of at least
  * decode_attn_paged_prefix_workspace_size(p, q_len, prefix_len) bytes, 256-byte
  * aligned, of any content; calls that overlap on the GPU must not share it.
- * Everything else as for decode_attn_paged.
+ * Everything else as for decode_attn_paged.  DA_ERR_UNSUPPORTED also where a
+ * launch's work would not count in 31 bits: q_len * num_q_heads * 256 rows, or
+ * the table's keys / 128 (64 for head_dim 256) * num_kv_heads * 256 tiles.
  */
 size_t decode_attn_paged_prefix_workspace_size(const da_params* p, int32_t q_len,
                                                int32_t prefix_len);

@@ -672,12 +672,12 @@ int check_prefix(const da_params* p, int T, int prefix_len) {
   // row indices of a launch have 32 bits
   if ((long long)T * p->num_q_heads * da::prefix_max_batch(p->head_dim) > 0x7fffffffLL - 1024)
     return DA_ERR_UNSUPPORTED;
-  // so do the tiles of one CTA
+  // so do a launch's tiles, by the table's width
   const int tile = da::prefix_tile_keys(p->head_dim), most = da::prefix_max_batch(p->head_dim);
   const int G = p->num_q_heads / p->num_kv_heads;
   const long long units = (long long)p->num_kv_heads * most *
                           (((long long)T * G + da::kPrefixRows - 1) / da::kPrefixRows + 1);
-  if (((long long)p->max_blocks_per_seq * p->block_size / tile + 1) * units > (1LL << 37))
+  if (((long long)p->max_blocks_per_seq * p->block_size / tile + 2) * units > 0x7fffffffLL)
     return DA_ERR_UNSUPPORTED;
   // a tile past the last key still has 32-bit key indices
   if ((long long)p->max_blocks_per_seq * p->block_size > 0x7fffffffLL - 1024)

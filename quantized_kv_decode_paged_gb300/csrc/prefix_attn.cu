@@ -97,17 +97,18 @@ __device__ __forceinline__ int seq_info(const PrefixParams& p, int b, int& len, 
 }
 
 // Keys [lo, hi) that the query tokens t0 .. t1 see between them: token t0's
-// lower bound, token t1's upper bound.
+// lower bound, token t1's upper bound.  qp is at least -T, and only then negative;
+// otherwise the sums fit in 32 unsigned bits.
 __device__ __forceinline__ void key_range(const PrefixParams& p, int len, int qp, int t0, int t1,
                                           int& lo, int& hi) {
-  const long long a = (long long)qp + t0, z = (long long)qp + t1 + 1;
-  const long long l = (p.window > 0 && a >= p.window) ? a - p.window + 1 : 0;
-  const long long h = p.causal && z < len ? z : len;
-  lo = hi = 0;
-  if (h > l) {
-    lo = (int)l;
-    hi = (int)h;
-  }
+  const uint32_t a = (uint32_t)qp + t0, z = (uint32_t)qp + t1 + 1;
+  const bool before = qp < 0 && (int)a < 0, none = qp < 0 && (int)z <= 0;
+  const uint32_t W = p.window;
+  const uint32_t l = (W > 0 && !before && a >= W) ? a - W + 1 : 0;
+  const uint32_t h = !p.causal ? len : none ? 0 : min(z, (uint32_t)len);
+  const bool some = h > l;
+  lo = some ? (int)l : 0;
+  hi = some ? (int)h : 0;
 }
 
 // Page of key k of sequence b (not checked against num_blocks).
@@ -120,7 +121,7 @@ __device__ __forceinline__ int page_of(const PrefixParams& p, int b, int k) {
 // One warp's state of a row over keys [k0, k1), key by key: lane i holds the
 // values [i * D/32, (i + 1) * D/32) of q and o.  Pages outside the pool are masked.
 template <int D>
-__device__ void attend_row(const PrefixParams& p, int b, int kv, const float (&q)[D / 32], int k0,
+__device__ __noinline__ void attend_row(const PrefixParams& p, int b, int kv, const float (&q)[D / 32], int k0,
                            int k1, float& m, float& l, float (&o)[D / 32]) {
   constexpr int V = D / 32;
   const int lane = threadIdx.x & 31;
@@ -220,20 +221,18 @@ static_assert(sizeof(PrefixSmem<64>) <= kSmemLimit && sizeof(PrefixSmem<128>) <=
                   sizeof(PrefixSmem<256>) <= kSmemLimit,
               "shared memory");
 
-// a / b, without the long division where 32 bits hold a.
-__device__ __forceinline__ long long div_small(long long a, int b) {
-  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
-// The list of tiles is cut into runs of share + 1 tiles (the first rem CTAs) and share.
+// The list of tiles (fewer than 2^31: the host refuses more) is cut into runs
+// of share + 1 tiles (the first rem CTAs) and share.
 struct Split {
-  long long share;
-  int rem;
-  __device__ __forceinline__ long long start(int c) const { return c * share + min(c, rem); }
+  int share, rem;
+  __device__ __forceinline__ Split(int total, int ctas)
+      : share((uint32_t)total / (uint32_t)ctas), rem(total - share * ctas) {}
+  __device__ __forceinline__ int start(int c) const { return c * share + min(c, rem); }
   // The CTA whose run holds tile g.
-  __device__ __forceinline__ int cta(long long g) const {
-    const long long longer = rem * (share + 1);
-    return g < longer ? (int)div_small(g, (int)share + 1)
-                      : rem + (int)div_small(g - longer, (int)share);
+  __device__ __forceinline__ int cta(int g) const {
+    const int longer = rem * (share + 1);
+    return g < longer ? (uint32_t)g / (uint32_t)(share + 1)
+                      : rem + (uint32_t)(g - longer) / (uint32_t)share;
   }
 };
 
@@ -355,19 +354,18 @@ __device__ int make_plan(const PrefixParams& p, PrefixSmem<D>& s) {
 // head, tile of rows, tile of the unit.  pn: tiles of a prefix unit, tp: of the
 // whole prefix.
 template <int D>
-__device__ void find_first(const PrefixParams& p, PrefixSmem<D>& s, long long g, int pn,
-                           long long tp) {
+__device__ void find_first(const PrefixParams& p, PrefixSmem<D>& s, int g, int pn, int tp) {
   int b, each, u, tiles;
   if (g < tp) {
     b = -1;
     each = pn;
     tiles = p.row_tiles;
-    u = (int)div_small(g, pn);
-    g -= (long long)u * pn;
+    u = (uint32_t)g / (uint32_t)pn;
+    g -= u * pn;
   } else {
     g -= tp;
     const int units1 = p.Hkv * p.own_tiles;
-    const long long x = div_small(g, units1);  // sequence b holds it: cum[b] <= x < cum[b + 1]
+    const int x = (uint32_t)g / (uint32_t)units1;  // sequence b holds it: cum[b] <= x < cum[b + 1]
     int hi = p.B;
     b = 0;
     while (hi - b > 1) {
@@ -379,24 +377,33 @@ __device__ void find_first(const PrefixParams& p, PrefixSmem<D>& s, long long g,
     }
     each = s.cum[b + 1] - s.cum[b];
     tiles = p.own_tiles;
-    g -= (long long)s.cum[b] * units1;
-    u = (int)div_small(g, each);
-    g -= (long long)u * each;
+    g -= s.cum[b] * units1;
+    u = (uint32_t)g / (uint32_t)each;
+    g -= u * each;
   }
   s.first[0] = b;
   s.first[1] = u / tiles;
   s.first[2] = u % tiles;
-  s.first[3] = (int)g;
+  s.first[3] = g;
 }
 
-// A wait that gives up sets the abort flag; every role then leaves its loop.
+// Waits for the phase of `bar` with the given parity.  A wait that runs past
+// the limit sets the abort flag; every role then leaves its loop, and the kernel reports it
+// at its end.  Short, because it is inlined at every wait: the kernel's code has to stay in the
+// instruction cache (117 KB of it, most in these waits, cost 3 of 6 us a tile).
 template <int D>
 __device__ __forceinline__ bool wait_or_abort(const PrefixParams& p, PrefixSmem<D>& s,
                                               uint64_t* bar, uint32_t parity) {
-  if (mbar_wait(bar, parity, &s.abort, p.wait_ns)) return true;
-  *(volatile int*)&s.abort = 1;
-  if (p.dev_status) atomicOr(p.dev_status, DEV_TIMEOUT);
-  return false;
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*(volatile int*)&s.abort) return false;
+    if (globaltimer_ns() - t0 > p.wait_ns) {
+      *(volatile int*)&s.abort = 1;
+      return false;
+    }
+  }
+  return true;
 }
 // The same for all lanes of a warp, which go on or leave together.
 template <int D>
@@ -477,10 +484,12 @@ struct Loader {
     const int tiles = s.run;
     if (tiles == 0) return;
     int j = 0;
-    Tile t0 = fetch(c, j), t1 = fetch(c, j), t2 = fetch(c, j);
-    if (!issue(t0, 0, false) || (tiles > 1 && !issue(t1, 1, false))) return;
-    for (int x = 0; x < tiles; ++x) {
-      if (!issue(t0, x, true) || (x + 2 < tiles && !issue(t2, x + 2, false))) return;
+    Tile t0 = {0, 0, 0, false}, t1 = t0, t2 = fetch(c, j);  // tiles x, x + 1, x + 2
+#pragma unroll 1
+    for (int x = -2; x < tiles; ++x) {
+#pragma unroll 1
+      for (int u = x < 0 ? 1 : 0; u < (x + 2 < tiles ? 2 : 1); ++u)
+        if (!issue(u ? t2 : t0, u ? x + 2 : x, u == 0)) return;
       t0 = t1;
       t1 = t2;
       t2 = fetch(c, j);
@@ -489,34 +498,30 @@ struct Loader {
 };
 
 // ------------------------------------------------------------------ Q
-// Rows [first, last) of a part's Q into shared memory by one warp: the power
+// n <= 32 rows of Q into rows row0 .. of the Q buffer by one warp; lane i names
+// row i (`mine`, its place in [B, T, Hq]; lanes past the last name the last).  The power
 // of two that brings a row's largest value to [2^9, 2^10), then two f16 terms.
 // A lane takes 8 values, D / 8 lanes a row: 16-byte stores.
 template <int D>
-__device__ void load_q_rows(const PrefixParams& p, PrefixSmem<D>& s, const Cursor<D>& c, int first,
-                            int last) {
+__device__ __forceinline__ void load_q_rows(const float* src, float qscale, PrefixSmem<D>& s, int mine,
+                                         int row0, int n) {
   constexpr int LR = D / 8;        // lanes of a row
   constexpr int RW = 32 / LR;      // rows of a step
   constexpr int BATCH = 4;         // steps in flight
   const int lane = threadIdx.x & 31, sub = lane / LR, d = lane % LR * 8;
-  if (first >= last) return;
-  int seq, tok;
-  // the row each lane addresses for the warp: first + lane, past the last one the last
-  const int mine = c.out_row(min(first + lane, last - 1), seq, tok);
-  const int n = last - first;
 #pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += RW * BATCH) {
     float4 x[BATCH][2];
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
       const int at = __shfl_sync(0xffffffffu, mine, min(i0 + u * RW + sub, 31));
-      const float4* src = reinterpret_cast<const float4*>(p.q + (long long)at * D + d);
-      x[u][0] = src[0];
-      x[u][1] = src[1];
+      const float4* q = reinterpret_cast<const float4*>(src + (long long)at * D + d);
+      x[u][0] = q[0];
+      x[u][1] = q[1];
     }
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
-      const int row = c.q_row() + first + min(i0 + u * RW + sub, n - 1);
+      const int row = row0 + min(i0 + u * RW + sub, n - 1);
       const float v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w,
                           x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
       float m = 0.f;
@@ -528,7 +533,7 @@ __device__ void load_q_rows(const PrefixParams& p, PrefixSmem<D>& s, const Curso
       int e = (int)(__float_as_uint(m) >> 23) - 127;
       e = min(max(e, -100), 120);
       const float f = __uint_as_float((uint32_t)(9 - e + 127) << 23);
-      if (d == 0) s.row_scale[row] = p.qscale * __uint_as_float((uint32_t)(e - 9 + 127) << 23);
+      if (d == 0) s.row_scale[row] = qscale * __uint_as_float((uint32_t)(e - 9 + 127) << 23);
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) split_half2(v[2 * i] * f, v[2 * i + 1] * f, hi[i], lo[i]);
@@ -539,6 +544,17 @@ __device__ void load_q_rows(const PrefixParams& p, PrefixSmem<D>& s, const Curso
   }
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// Rows [first, first + 32) of the cursor's part, as far as `last`.
+template <int D>
+__device__ __forceinline__ void load_q(const PrefixParams& p, PrefixSmem<D>& s,
+                                       const Cursor<D>& c, int first, int last) {
+  const int n = min(32, min(last, c.nr) - first);
+  if (n <= 0) return;
+  int seq, tok;
+  const int mine = c.out_row(first + min((int)(threadIdx.x & 31), n - 1), seq, tok);
+  load_q_rows<D>(p.q, p.qscale, s, mine, c.q_row() + first, n);
 }
 
 // Warp 3: Q of the parts with few rows, one part ahead of the products.  The
@@ -557,8 +573,8 @@ __device__ void q_loop(const PrefixParams& p, PrefixSmem<D>& s) {
         !warp_wait<D>(p, s, &s.q_free[(k - 1) & 1], ((k - 1) >> 1) & 1))
       return;
     if (small) {
-      load_q_rows<D>(p, s, c, 0, min(c.nr, 32));
-      load_q_rows<D>(p, s, c, 32, c.nr);
+#pragma unroll 1
+      for (int i = 0; i < c.nr; i += 32) load_q<D>(p, s, c, i, c.nr);
     }
     // its own arrival, and for few rows those of the softmax warps
     if (lane < 1 + (small ? 4 * PGeo<D>::SOFTG : 0)) mbar_arrive(&s.q_full[k & 1]);
@@ -607,7 +623,7 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s) {
       if (k >= 1 && !warp_wait<D>(p, s, &s.q_free[(k - 1) & 1], ((k - 1) >> 1) & 1)) return;
       constexpr int ROWS = kPrefixRows / (4 * G::SOFTG);
       const int first = (group * 4 + w) * ROWS;
-      load_q_rows<D>(p, s, c, min(c.nr, first), min(c.nr, first + ROWS));
+      load_q<D>(p, s, c, first, first + ROWS);
       if (lane == 0) mbar_arrive(&s.q_full[k & 1]);
     }
     const bool any = w * 32 < c.nr;  // rows of this warp
@@ -660,10 +676,15 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s) {
               for (int i = 0; i < 32; ++i) v[i] = capped(v[i] * scale, p.softcap2, p.softcap_inv);
             }
             if (masked) {
-              const int a = lo - k0 - i0, z = hi - k0 - i0;
+              // bit i: key k0 + i0 + i is seen
+              const int a = min(max(lo - k0 - i0, 0), 32), z = min(max(hi - k0 - i0, 0), 32);
+              uint32_t seen = (uint32_t)(0xffffffffull << a) & ~(uint32_t)(0xffffffffull << z);
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                if ((bad >> ((i0 + i) >> box_shift)) & 1) seen &= ~(0xffu << i);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (i < a || i >= z || ((bad >> ((i0 + i) >> box_shift)) & 1)) v[i] = -kInf;
+                if (!(seen >> i & 1)) v[i] = -kInf;
             }
             tmem_st32(sa + i0, v);
             top = fmaxf(top, max32(v));
@@ -951,14 +972,10 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
   if (blockIdx.x == 0 && flags && p.dev_status) atomicOr(p.dev_status, flags);
   if (tid == 0) {
     const int pn = s.hi > s.lo ? (s.hi + G::KT - 1) / G::KT - s.lo / G::KT : 0;
-    const long long tp = (long long)pn * (p.Hkv * p.row_tiles);
-    const long long total = tp + (long long)s.cum[p.B] * (p.Hkv * p.own_tiles);
-    Split sp;
-    sp.share = div_small(total, p.grid);
-    sp.rem = (int)(total - sp.share * p.grid);
-    const long long g0 = sp.start(blockIdx.x);
-    s.run = (int)(sp.share + ((int)blockIdx.x < sp.rem));
-    if (s.run > 0) find_first<D>(p, s, g0, pn, tp);
+    const int tp = pn * (p.Hkv * p.row_tiles);
+    const Split sp(tp + s.cum[p.B] * (p.Hkv * p.own_tiles), p.grid);
+    s.run = sp.share + ((int)blockIdx.x < sp.rem);
+    if (s.run > 0) find_first<D>(p, s, sp.start(blockIdx.x), pn, tp);
     if (blockIdx.x == 0) p.ws_plan[0] = pn;
   }
   if (blockIdx.x == 0)
@@ -1005,6 +1022,7 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
   tc5_fence_before();
   __syncthreads();
   tc5_fence_after();
+  if (tid == 0 && s.abort && p.dev_status) atomicOr(p.dev_status, DEV_TIMEOUT);
   if (warp == 1) tmem_free(s.tmem, 512);
 }
 
@@ -1027,11 +1045,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int pn = p.ws_plan[0];
   const int* cum = p.ws_plan + 1;
   const int units1 = p.Hkv * p.own_tiles;
-  const long long tp = (long long)pn * p.Hkv * p.row_tiles;
-  const long long total = tp + (long long)cum[p.B] * units1;
-  Split sp;
-  sp.share = div_small(total, p.grid);
-  sp.rem = (int)(total - sp.share * p.grid);
+  const int tp = pn * (p.Hkv * p.row_tiles);
+  const Split sp(tp + cum[p.B] * units1, p.grid);
   float M = -kInf, L = 0.f, o[V];
   bool partial = false;
 #pragma unroll
@@ -1047,16 +1062,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     for (int i = 0; i < V; ++i) o[i] = fmaf(o[i], f, w * src[lane * V + i]);
   };
   for (int u = 0; u < 2; ++u) {  // the prefix's states, then the own keys'
-    long long g0;
-    int n, in_tile;
+    int g0, n, in_tile;
     if (u == 0) {
       n = pn;
-      g0 = (h * (long long)p.row_tiles + rb / kPrefixRows) * pn;
+      g0 = (h * p.row_tiles + rb / kPrefixRows) * pn;
       in_tile = rb % kPrefixRows;
     } else {
       n = cum[b + 1] - cum[b];
-      g0 = tp + (long long)cum[b] * units1 +
-           ((long long)h * p.own_tiles + r1 / kPrefixRows) * n;
+      g0 = tp + cum[b] * units1 + (h * p.own_tiles + r1 / kPrefixRows) * n;
       in_tile = r1 % kPrefixRows;
     }
     if (n == 0) continue;
