@@ -12,6 +12,7 @@ seq_lens i32 [B]; out f32 [B, Hq, D]; lse f32 [B, Hq].
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -745,22 +746,37 @@ def _check_cuda(name, t):
 
 
 class _on_device:
-    """Makes ``dev`` the current CUDA device for a call when it is not."""
+    """Makes ``dev`` the current CUDA device for a call."""
 
     def __init__(self, dev):
-        self.guard = None
-        torch = _torch()
-        if dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(dev)
+        self.guard = _torch().cuda.device(dev)
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+        self.guard.__enter__()
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        self.guard.__exit__(*exc)
         return False
+
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _device_guard(torch, dev):
+    return _NO_GUARD if torch.cuda.current_device() == dev.index else _on_device(dev)
+
+
+def _raw_stream(torch, dev, stream):
+    """The stream's handle as an integer (its current stream's by default)."""
+    if stream is not None:
+        return stream.cuda_stream
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(dev.index) if get is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _plain(t, dtype, device, ndim):
+    """Whether _req accepts t: asked first, because it costs a tenth of it."""
+    return t.dtype is dtype and t.device == device and t.dim() == ndim and t.is_contiguous()
 
 
 def decode_attn_rope_freqs(rotary_dim, theta=10000.0, *, inv_freq=None, device="cuda"):
@@ -781,8 +797,7 @@ def decode_attn_rope_freqs(rotary_dim, theta=10000.0, *, inv_freq=None, device="
     return host.to(device)
 
 
-def _rope_types(torch):
-    return {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_ROPE_TYPES: dict = {}  # torch dtype -> DA_TYPE_*
 
 
 def _req_rows(t, name, dtype, device):
@@ -804,35 +819,35 @@ def _req_rows(t, name, dtype, device):
     return (ts if n > 1 else 0), (hs if h > 1 else 0)
 
 
-def _rope_params(x, freqs, norm, q_weight, k_weight, weight_offset, eps, interleaved):
-    torch = _torch()
-    types = _rope_types(torch)
+def _rope_params(torch, x, freqs, norm, q_weight, k_weight, weight_offset, eps, interleaved,
+                 q_rows, k_rows, v_rows):
     if not isinstance(x, torch.Tensor):
         raise TypeError("q and k must be torch.Tensors")
-    if x.dtype not in types:
+    if not _ROPE_TYPES:
+        _ROPE_TYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    kind = _ROPE_TYPES.get(x.dtype)
+    if kind is None:
         raise TypeError(f"q, k and v must be float32, float16 or bfloat16, got {x.dtype}")
     dev = x.device
-    r = DaRopeParams()
-    r.type = types[x.dtype]
-    r.interleaved = int(bool(interleaved))
-    r.norm = int(bool(norm))
-    r.eps = float(eps)
-    r.weight_offset = float(weight_offset)
+    rd, fp = 0, None
     if freqs is not None:
-        _req(freqs, "freqs", torch.int64, dev, 1)
-        r.rotary_dim = 2 * freqs.shape[0]
-        r.freqs = freqs.data_ptr()
+        if not _plain(freqs, torch.int64, dev, 1):
+            _req(freqs, "freqs", torch.int64, dev, 1)
+        rd, fp = 2 * freqs.shape[0], freqs.data_ptr()
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is None:
             continue
         if not norm:
             raise ValueError(f"{name} is given but norm is off")
-        _req(w, name, torch.float32, dev, 1)
+        if not _plain(w, torch.float32, dev, 1):
+            _req(w, name, torch.float32, dev, 1)
         if w.shape[0] != x.shape[-1]:
             raise ValueError(f"{name} must have {x.shape[-1]} values, got {w.shape[0]}")
-    r.q_weight = _ptr(q_weight)
-    r.k_weight = _ptr(k_weight)
-    return r
+    return DaRopeParams(kind, rd, 1 if interleaved else 0, 1 if norm else 0, eps, weight_offset,
+                        *q_rows, *k_rows, *v_rows, fp, _ptr(q_weight), _ptr(k_weight))
+
+
+_NO_ROWS = (0, 0)
 
 
 def decode_attn_qk_norm_rope(q, k, positions, freqs, *, norm=True, q_weight=None, k_weight=None,
@@ -846,24 +861,27 @@ def decode_attn_qk_norm_rope(q, k, positions, freqs, *, norm=True, q_weight=None
     ``norm``.  Returns (q_out f32 [N, Hq, D], k_out f16 [N, Hkv, D]): the types
     that the decode and the append calls take."""
     torch = _torch()
-    lib = load_library()
+    lib = _lib or load_library()
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
-    r = _rope_params(x, freqs, norm, q_weight, k_weight, weight_offset, eps, interleaved)
-    dev = x.device
+    dtype, dev = x.dtype, x.device
     Hq = Hkv = 0
+    q_rows = k_rows = _NO_ROWS
     if q is not None:
-        r.q_token_stride, r.q_head_stride = _req_rows(q, "q", x.dtype, dev)
+        q_rows = _req_rows(q, "q", dtype, dev)
         Hq = q.shape[1]
     if k is not None:
-        r.k_token_stride, r.k_head_stride = _req_rows(k, "k", x.dtype, dev)
+        k_rows = _req_rows(k, "k", dtype, dev)
         Hkv = k.shape[1]
+    r = _rope_params(torch, x, freqs, norm, q_weight, k_weight, weight_offset, eps, interleaved,
+                     q_rows, k_rows, _NO_ROWS)
     N, _, D = x.shape
     if k is not None and (k.shape[0] != N or k.shape[2] != D):
         raise ValueError("inconsistent shapes")
     if positions is not None:
-        _req(positions, "positions", torch.int32, dev, 1)
+        if not _plain(positions, torch.int32, dev, 1):
+            _req(positions, "positions", torch.int32, dev, 1)
         if positions.shape[0] != N:
             raise ValueError("inconsistent shapes")
     elif freqs is not None:
@@ -875,7 +893,7 @@ def decode_attn_qk_norm_rope(q, k, positions, freqs, *, norm=True, q_weight=None
             if t.shape != shape:
                 raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     _check_cuda("q and k", x)
-    with _on_device(dev):
+    with _device_guard(torch, dev):
         if q is not None and q_out is None:
             q_out = torch.empty((N, Hq, D), dtype=torch.float32, device=dev)
         if k is not None and k_out is None:
@@ -884,7 +902,7 @@ def decode_attn_qk_norm_rope(q, k, positions, freqs, *, norm=True, q_weight=None
             return q_out, k_out
         st = lib.decode_attn_qk_norm_rope(ctypes.byref(r), N, Hq, Hkv, D, _ptr(q), _ptr(k),
                                           _ptr(positions), _ptr(q_out), _ptr(k_out),
-                                          _stream(dev, stream))
+                                          _raw_stream(torch, dev, stream))
     _check("decode_attn_qk_norm_rope", st)
     return q_out, k_out
 
@@ -900,27 +918,31 @@ def decode_attn_append_paged_rope(k_new, v_new, positions, block_table, k_pool, 
     token n is sequence n).  With q [N, Hq, D] the queries are normed and rotated
     in the same launch.  Returns q_out f32 [N, Hq, D], or None without q."""
     torch = _torch()
-    lib = load_library()
-    r = _rope_params(k_new, freqs, norm, q_weight, k_weight, weight_offset, eps, interleaved)
-    dev = k_new.device
-    r.k_token_stride, r.k_head_stride = _req_rows(k_new, "k_new", k_new.dtype, dev)
-    r.v_token_stride, r.v_head_stride = _req_rows(v_new, "v_new", k_new.dtype, dev)
-    _req(positions, "positions", torch.int32, dev, 1)
-    _req(block_table, "block_table", torch.int32, dev, 2)
-    _req(k_pool, "k_pool", torch.float16, dev, 4)
-    _req(v_pool, "v_pool", torch.float16, dev, 4)
+    lib = _lib or load_library()
+    dtype, dev, i32 = k_new.dtype, k_new.device, torch.int32
+    k_rows = _req_rows(k_new, "k_new", dtype, dev)
+    v_rows = _req_rows(v_new, "v_new", dtype, dev)
+    q_rows = _NO_ROWS if q is None else _req_rows(q, "q", dtype, dev)
+    r = _rope_params(torch, k_new, freqs, norm, q_weight, k_weight, weight_offset, eps,
+                     interleaved, q_rows, k_rows, v_rows)
+    if not (_plain(positions, i32, dev, 1) and _plain(block_table, i32, dev, 2)
+            and _plain(k_pool, torch.float16, dev, 4) and _plain(v_pool, torch.float16, dev, 4)):
+        _req(positions, "positions", i32, dev, 1)
+        _req(block_table, "block_table", i32, dev, 2)
+        _req(k_pool, "k_pool", torch.float16, dev, 4)
+        _req(v_pool, "v_pool", torch.float16, dev, 4)
     N, Hkv, D = k_new.shape
-    NB, bs = k_pool.shape[:2]
-    if (v_new.shape != k_new.shape or v_pool.shape != k_pool.shape
-            or k_pool.shape[2:] != k_new.shape[1:] or positions.shape[0] != N):
+    NB, bs, Hp, Dp = k_pool.shape
+    if (v_new.shape != k_new.shape or v_pool.shape != k_pool.shape or Hp != Hkv or Dp != D
+            or positions.shape[0] != N):
         raise ValueError("inconsistent shapes")
     if token_seq is not None:
-        _req(token_seq, "token_seq", torch.int32, dev, 1)
+        if not _plain(token_seq, i32, dev, 1):
+            _req(token_seq, "token_seq", i32, dev, 1)
         if token_seq.shape[0] != N:
             raise ValueError("inconsistent shapes")
     Hq = Hkv
     if q is not None:
-        r.q_token_stride, r.q_head_stride = _req_rows(q, "q", k_new.dtype, dev)
         Hq = q.shape[1]
         if q.shape[0] != N or q.shape[2] != D:
             raise ValueError("inconsistent shapes")
@@ -931,18 +953,19 @@ def decode_attn_append_paged_rope(k_new, v_new, positions, block_table, k_pool, 
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need q")
     if dev_status is not None:
-        _req(dev_status, "dev_status", torch.int32, dev)
+        _req(dev_status, "dev_status", i32, dev)
     _check_cuda("k_new", k_new)
     p = DaParams(block_table.shape[0], Hq, Hkv, D, bs, block_table.shape[1], NB, 0, 0.0, 0.0, 0, 1)
-    with _on_device(dev):
+    with _device_guard(torch, dev):
         if q is not None and q_out is None:
             q_out = torch.empty((N, Hq, D), dtype=torch.float32, device=dev)
         if N == 0:
             return q_out
         st = lib.decode_attn_append_paged_rope(
-            ctypes.byref(p), ctypes.byref(r), N, _ptr(q), _ptr(k_new), _ptr(v_new),
-            _ptr(positions), _ptr(token_seq), _ptr(block_table), _ptr(q_out), _ptr(k_pool),
-            _ptr(v_pool), _ptr(dev_status), _stream(dev, stream))
+            ctypes.byref(p), ctypes.byref(r), N, _ptr(q), k_new.data_ptr(), v_new.data_ptr(),
+            positions.data_ptr(), _ptr(token_seq), block_table.data_ptr(), _ptr(q_out),
+            k_pool.data_ptr(), v_pool.data_ptr(), _ptr(dev_status),
+            _raw_stream(torch, dev, stream))
     _check("decode_attn_append_paged_rope", st)
     return q_out
 
@@ -956,6 +979,25 @@ def decode_attn_paged_prefix_workspace_size(params: DaParams, q_len: int, prefix
                                                                       int(q_len), int(prefix_len)))
 
 
+_prefix_ws: dict = {}  # (device, stream) -> workspace
+
+
+def _prefix_workspace(torch, dev, stream, raw, nbytes):
+    """The stream's workspace, grown as needed.  Calls of one stream follow one
+    another; a call that is being captured gets its own, which lives in its
+    graph's memory: graphs may be replayed side by side."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    key = (dev.index, raw)
+    ws = _prefix_ws.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            ws.record_stream(stream)
+        _prefix_ws[key] = ws
+    return ws
+
+
 def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_len,
                              prefix_table=None, q_pos=None, *, scale=0.0, softcap=0.0,
                              sliding_window=0, causal=True, max_seq_len=0, out=None, lse=None,
@@ -967,73 +1009,76 @@ def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_le
     first columns of block_table's row 0); those columns of block_table are not
     read.  seq_lens and q_pos include the prefix.  Returns (out, lse).
 
-    ``workspace``: "auto" (allocated for the call) or a caller-owned uint8
-    tensor of decode_attn_paged_prefix_workspace_size bytes (any content)."""
+    ``workspace``: "auto" (kept per stream; a captured call's own) or a
+    caller-owned uint8 tensor of decode_attn_paged_prefix_workspace_size bytes
+    (any content)."""
     torch = _torch()
-    lib = load_library()
+    lib = _lib or load_library()
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be a tensor of 3 or 4 dims")
-    dev = q.device
-    _req(q, "q", torch.float32, dev)
-    _req(k_pool, "k_pool", torch.float16, dev, 4)
-    _req(v_pool, "v_pool", torch.float16, dev, 4)
-    _req(block_table, "block_table", torch.int32, dev, 2)
-    _req(seq_lens, "seq_lens", torch.int32, dev, 1)
-    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
-    T = q.shape[1] if q.dim() == 4 else 1
+    dev, i32, f16 = q.device, torch.int32, torch.float16
+    shape = q.shape
+    if not (_plain(q, torch.float32, dev, len(shape)) and _plain(k_pool, f16, dev, 4)
+            and _plain(v_pool, f16, dev, 4) and _plain(block_table, i32, dev, 2)
+            and _plain(seq_lens, i32, dev, 1)):
+        _req(q, "q", torch.float32, dev)
+        _req(k_pool, "k_pool", f16, dev, 4)
+        _req(v_pool, "v_pool", f16, dev, 4)
+        _req(block_table, "block_table", i32, dev, 2)
+        _req(seq_lens, "seq_lens", i32, dev, 1)
+    B, Hq, D = shape[0], shape[-2], shape[-1]
+    T = shape[1] if len(shape) == 4 else 1
     NB, bs, Hkv, D2 = k_pool.shape
-    if (k_pool.shape != v_pool.shape or D2 != D or block_table.shape[0] != B
-            or seq_lens.shape[0] != B):
+    rows, columns = block_table.shape
+    if v_pool.shape != k_pool.shape or D2 != D or rows != B or seq_lens.shape[0] != B:
         raise ValueError("inconsistent shapes")
     if q_pos is not None:
-        _req(q_pos, "q_pos", torch.int32, dev, 1)
+        _req(q_pos, "q_pos", i32, dev, 1)
         if q_pos.shape[0] != B:
             raise ValueError("inconsistent shapes")
     prefix_len = int(prefix_len)
     pages = prefix_len // bs
     if prefix_table is None:
-        # row 0 starts the table: its address serves as the prefix's
-        pt = block_table.data_ptr()
+        prefix_table = block_table  # its first row
     else:
-        _req(prefix_table, "prefix_table", torch.int32, dev, 1)
+        _req(prefix_table, "prefix_table", i32, dev, 1)
         if prefix_table.shape[0] < pages:
             raise ValueError(f"prefix_table must have {pages} entries, got "
                              f"{prefix_table.shape[0]}")
-        pt = prefix_table.data_ptr()
     if out is not None:
         _req(out, "out", torch.float32, dev)
-        if out.shape != q.shape:
+        if out.shape != shape:
             raise ValueError("inconsistent shapes")
     if lse is not None:
         _req(lse, "lse", torch.float32, dev)
-        if lse.shape != q.shape[:-1]:
+        if lse.shape != shape[:-1]:
             raise ValueError("inconsistent shapes")
     if dev_status is not None:
-        _req(dev_status, "dev_status", torch.int32, dev)
-    if isinstance(workspace, torch.Tensor):
+        _req(dev_status, "dev_status", i32, dev)
+    auto = isinstance(workspace, str) and workspace == "auto"
+    if not auto:
+        if not isinstance(workspace, torch.Tensor):
+            raise ValueError("workspace must be \"auto\" or a uint8 tensor")
         _req(workspace, "workspace", torch.uint8, dev)
-    elif not (isinstance(workspace, str) and workspace == "auto"):
-        raise ValueError("workspace must be \"auto\" or a uint8 tensor")
     _check_cuda("q", q)
-    params = DaParams(B, Hq, Hkv, D, bs, block_table.shape[1], NB, int(max_seq_len), float(scale),
-                      float(softcap), int(sliding_window), int(bool(causal)))
-    with _on_device(dev):
+    params = DaParams(B, Hq, Hkv, D, bs, columns, NB, max_seq_len, scale, softcap, sliding_window,
+                      1 if causal else 0)
+    ref = ctypes.byref(params)
+    with _device_guard(torch, dev):
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+            out = torch.empty(shape, dtype=torch.float32, device=dev)
         if lse is None:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+            lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         if B == 0:
             return out, lse
-        if isinstance(workspace, str):
-            nbytes = lib.decode_attn_paged_prefix_workspace_size(ctypes.byref(params), T,
-                                                                 prefix_len)
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            if stream is not None:
-                workspace.record_stream(stream)
-        st = lib.decode_attn_paged_prefix(ctypes.byref(params), T, prefix_len, pt, _ptr(q),
-                                          _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
-                                          _ptr(seq_lens), _ptr(q_pos), _ptr(out), _ptr(lse),
-                                          _ptr(workspace), workspace.numel(), _ptr(dev_status),
-                                          _stream(dev, stream))
+        raw = _raw_stream(torch, dev, stream)
+        if auto:
+            nbytes = lib.decode_attn_paged_prefix_workspace_size(ref, T, prefix_len)
+            workspace = _prefix_workspace(torch, dev, stream, raw, nbytes)
+        st = lib.decode_attn_paged_prefix(
+            ref, T, prefix_len, prefix_table.data_ptr(), q.data_ptr(), k_pool.data_ptr(),
+            v_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), _ptr(q_pos),
+            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _ptr(dev_status), raw)
     _check("decode_attn_paged_prefix", st)
     return out, lse
