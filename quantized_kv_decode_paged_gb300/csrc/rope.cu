@@ -9,11 +9,12 @@
 // modulo one turn, exact up to f's own 2^-65 turns a position.  The top 32 bits
 // as a signed number times 2^-31 are a / pi in [-1, 1), what sincospif takes.
 //
-// One CTA per token: its rd/2 cosines and sines are computed once into shared memory
-// and serve all the token's heads.  D/16 threads take a row, each
+// A CTA takes up to kMaxTokens tokens: their rd/2 cosines and sines are computed once
+// into shared memory and serve all the tokens' heads.  D/16 threads take a row, each
 // two 8-value chunks that hold both halves of its 8 pairs: (8c, rd/2 + 8c) or, interleaved,
 // (16c, 16c + 8); the chunks past the rotated part pair up without rotation.
-// So no value crosses threads but the norm's sum of squares.
+// So no value crosses threads but the norm's sum of squares.  A thread's next row is
+// loaded before its last one is worked on.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -28,6 +29,8 @@
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kMaxTokens = 8;  // of a CTA
+constexpr int kManyCtas = 1216;  // eight for each of 152 SMs
 
 struct RopeArgs {
   const void* q;
@@ -38,7 +41,10 @@ struct RopeArgs {
   const float* kw;
   const uint64_t* freqs;
   const int32_t* positions;
-  int Hq, Hkv, rd, norm;
+  int N, tokens;            // tokens; tokens of a CTA
+  int heads;                // rows of a token: q, k and (append) v heads
+  uint64_t inv_heads;       // ceil(2^32 / heads): r / heads = r * inv_heads >> 32, r < 2^16
+  int Hq, Hk, Hkv, rd, norm;  // Hq, Hk: 0 where q or k is not given
   float eps, woff;
   float* q_out;
   uint16_t* k_out;  // norm_rope: [N, Hkv, D]
@@ -49,6 +55,12 @@ struct RopeArgs {
   uint16_t* v_pool;
   int batch, bs, max_blocks, num_blocks;
   int32_t* dev_status;
+};
+
+// Eight values of type T as they lie in memory.
+template <typename T>
+struct Raw {
+  uint4 w[sizeof(T) / 2];
 };
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8], const __half*) {
@@ -69,15 +81,22 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8], const __n
   }
 }
 
-// Eight values at a 16-byte boundary (32 bytes of f32).
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+__device__ __forceinline__ Raw<T> load8(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void values8(const Raw<T>& r, float (&x)[8]) {
   if constexpr (std::is_same<T, float>::value) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    x[0] = __uint_as_float(r.w[0].x), x[1] = __uint_as_float(r.w[0].y);
+    x[2] = __uint_as_float(r.w[0].z), x[3] = __uint_as_float(r.w[0].w);
+    x[4] = __uint_as_float(r.w[1].x), x[5] = __uint_as_float(r.w[1].y);
+    x[6] = __uint_as_float(r.w[1].z), x[7] = __uint_as_float(r.w[1].w);
   } else {
-    unpack8(*reinterpret_cast<const uint4*>(p), x, static_cast<const T*>(nullptr));
+    unpack8(r.w[0], x, static_cast<const T*>(nullptr));
   }
 }
 
@@ -122,68 +141,90 @@ __device__ __forceinline__ long long cache_row(const RopeArgs& a, int n, int& fl
 
 template <typename T, int D, bool IL, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
-  constexpr int TPR = D / 16;  // threads of a row
-  __shared__ float2 cs[D / 2];
-  const int n = blockIdx.x;
-  for (int i = threadIdx.x; i < a.rd / 2; i += kRopeThreads) {
-    const uint64_t turns = (uint64_t)(long long)a.positions[n] * a.freqs[i];
-    const float half_turns = (float)(int32_t)(turns >> 32) * 0x1p-31f;
-    sincospif(half_turns, &cs[i].y, &cs[i].x);
-  }
-  long long row = -1;
-  if constexpr (APPEND) {
-    int flag;
-    bool pad;
-    row = cache_row(a, n, flag, pad);
-    if (pad) return;
-    if (flag && threadIdx.x == 0 && a.dev_status) atomicOr(a.dev_status, flag);
-  }
-  __syncthreads();
+  constexpr int TPR = D / 16;                 // threads of a row
+  constexpr int RPI = kRopeThreads / TPR;     // rows of a round
+  __shared__ float2 cs[kMaxTokens][D / 2];
+  __shared__ long long place[kMaxTokens];     // append: row of the pool, or one of:
+  constexpr long long kDropped = -1, kPadding = -2;
+  const int n0 = blockIdx.x * a.tokens, tokens = min(a.tokens, a.N - n0);
   const int c = threadIdx.x % TPR;
   const int nrot = a.rd / 16;  // chunk pairs that are rotated
   const bool rot = c < nrot;
   const int lo = IL ? 16 * c : rot ? 8 * c : a.rd + 16 * (c - nrot);
   const int hi = (IL || !rot) ? lo + 8 : a.rd / 2 + 8 * c;
-  const int Hk = a.k ? a.Hkv : 0, Hq = a.q ? a.Hq : 0;
-  const int heads = Hq + Hk + (APPEND ? a.Hkv : 0);
-  // a warp's threads run the same number of rounds: the norm's sum is taken across them
-  for (int h0 = 0; h0 < heads; h0 += kRopeThreads / TPR) {
-    const int h = h0 + threadIdx.x / TPR;
-    const bool on = h < heads;
-    const bool is_q = h < Hq, is_v = h >= Hq + Hk;
-    const int hh = is_q ? h : is_v ? h - Hq - Hk : h - Hq;
-    float x[2][8];
-    if (on) {
-      const T* src = is_q   ? static_cast<const T*>(a.q) + n * a.q_ts + hh * a.q_hs
-                     : is_v ? static_cast<const T*>(a.v) + n * a.v_ts + hh * a.v_hs
-                            : static_cast<const T*>(a.k) + n * a.k_ts + hh * a.k_hs;
-      load8(src + lo, x[0]);
-      load8(src + hi, x[1]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[0][i] = x[1][i] = 0.f;
+  const int rows = tokens * a.heads;
+
+  struct Row {
+    int t, h, kind;  // token of the CTA, head, 0 q / 1 k / 2 v
+    Raw<T> lo, hi;
+  };
+  auto fetch = [&](int r) {
+    Row x;
+    x.t = (int)(((uint64_t)r * a.inv_heads) >> 32);
+    x.h = r - x.t * a.heads;
+    x.kind = x.h < a.Hq ? 0 : x.h < a.Hq + a.Hk ? 1 : 2;
+    x.h -= x.kind == 0 ? 0 : x.kind == 1 ? a.Hq : a.Hq + a.Hk;
+    const long long n = n0 + x.t;
+    const T* src = x.kind == 0   ? static_cast<const T*>(a.q) + n * a.q_ts + x.h * a.q_hs
+                   : x.kind == 1 ? static_cast<const T*>(a.k) + n * a.k_ts + x.h * a.k_hs
+                                 : static_cast<const T*>(a.v) + n * a.v_ts + x.h * a.v_hs;
+    x.lo = load8(src + lo);
+    x.hi = load8(src + hi);
+    return x;
+  };
+  int r = threadIdx.x / TPR;
+  Row next = fetch(min(r, rows - 1));  // rows past the last are loaded, not stored
+
+  for (int i = threadIdx.x; i < tokens * (a.rd / 2); i += kRopeThreads) {
+    const int t = i / (a.rd / 2), f = i - t * (a.rd / 2);
+    const uint64_t turns = (uint64_t)(long long)a.positions[n0 + t] * a.freqs[f];
+    const float half_turns = (float)(int32_t)(turns >> 32) * 0x1p-31f;
+    sincospif(half_turns, &cs[t][f].y, &cs[t][f].x);
+  }
+  if constexpr (APPEND) {
+    if ((int)threadIdx.x < tokens) {
+      int flag;
+      bool pad;
+      const long long row = cache_row(a, n0 + threadIdx.x, flag, pad);
+      place[threadIdx.x] = pad ? kPadding : flag ? kDropped : row;
+      if (flag && a.dev_status) atomicOr(a.dev_status, flag);
     }
+  }
+  __syncthreads();
+
+  // a warp's threads run the same number of rounds: the norm's sum is taken across them
+  for (int r0 = 0; r0 < rows; r0 += RPI, r += RPI) {
+    const Row cur = next;
+    if (r0 + RPI < rows) next = fetch(min(r + RPI, rows - 1));
+    float x[2][8];
+    values8(cur.lo, x[0]);
+    values8(cur.hi, x[1]);
     if (a.norm) {
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(x[0][i], x[0][i], fmaf(x[1][i], x[1][i], ss));
 #pragma unroll
       for (int o = TPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (on && !is_v) {
-        const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-        const float* w = is_q ? a.qw : a.kw;
+      if (cur.kind < 2) {
+        const float m = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+        const float* w = cur.kind == 0 ? a.qw : a.kw;
+        float g[2][8];
+        if (w) {
+          values8(load8(w + lo), g[0]);
+          values8(load8(w + hi), g[1]);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[0][i] *= r * (w ? w[lo + i] + a.woff : 1.f);
-          x[1][i] *= r * (w ? w[hi + i] + a.woff : 1.f);
+          x[0][i] *= w ? m * (g[0][i] + a.woff) : m;
+          x[1][i] *= w ? m * (g[1][i] + a.woff) : m;
         }
       }
     }
-    if (!on) continue;
-    if (rot && !is_v) {
+    if (r >= rows) continue;
+    if (rot && cur.kind < 2) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float2 t = cs[8 * c + i];
+        const float2 t = cs[cur.t][8 * c + i];
         float& y0 = IL ? x[i / 4][2 * (i % 4)] : x[0][i];
         float& y1 = IL ? x[i / 4][2 * (i % 4) + 1] : x[1][i];
         const float z0 = y0 * t.x - y1 * t.y;
@@ -191,17 +232,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
         y0 = z0;
       }
     }
-    if (is_q) {
-      float* dst = a.q_out + ((long long)n * a.Hq + hh) * D;
+    long long row = 0;
+    if constexpr (APPEND) row = place[cur.t];
+    if (cur.kind == 0) {
+      if (APPEND && row == kPadding) continue;
+      float* dst = a.q_out + ((long long)(n0 + cur.t) * a.Hq + cur.h) * D;
       store8(dst + lo, x[0]);
       store8(dst + hi, x[1]);
     } else {
       uint16_t* dst;
       if constexpr (APPEND) {
         if (row < 0) continue;
-        dst = (is_v ? a.v_pool : a.k_pool) + (row * a.Hkv + hh) * D;
+        dst = (cur.kind == 2 ? a.v_pool : a.k_pool) + (row * a.Hkv + cur.h) * D;
       } else {
-        dst = a.k_out + ((long long)n * a.Hkv + hh) * D;
+        dst = a.k_out + ((long long)(n0 + cur.t) * a.Hkv + cur.h) * D;
       }
       store8(dst + lo, x[0]);
       store8(dst + hi, x[1]);
@@ -210,32 +254,39 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
 }
 
 template <typename T, int D, bool APPEND>
-void launch_rope_d(const RopeArgs& a, int il, int num_tokens, cudaStream_t s) {
+void launch_rope_d(const RopeArgs& a, int il, cudaStream_t s) {
+  const int grid = (a.N + a.tokens - 1) / a.tokens;
   if (il)
-    rope_kernel<T, D, true, APPEND><<<num_tokens, kRopeThreads, 0, s>>>(a);
+    rope_kernel<T, D, true, APPEND><<<grid, kRopeThreads, 0, s>>>(a);
   else
-    rope_kernel<T, D, false, APPEND><<<num_tokens, kRopeThreads, 0, s>>>(a);
+    rope_kernel<T, D, false, APPEND><<<grid, kRopeThreads, 0, s>>>(a);
 }
 
 template <typename T, bool APPEND>
-void launch_rope_t(const RopeArgs& a, int D, int il, int num_tokens, cudaStream_t s) {
+void launch_rope_t(const RopeArgs& a, int D, int il, cudaStream_t s) {
   if (D == 64)
-    launch_rope_d<T, 64, APPEND>(a, il, num_tokens, s);
+    launch_rope_d<T, 64, APPEND>(a, il, s);
   else if (D == 128)
-    launch_rope_d<T, 128, APPEND>(a, il, num_tokens, s);
+    launch_rope_d<T, 128, APPEND>(a, il, s);
   else
-    launch_rope_d<T, 256, APPEND>(a, il, num_tokens, s);
+    launch_rope_d<T, 256, APPEND>(a, il, s);
 }
 
 template <bool APPEND>
-int launch_rope(const RopeArgs& a, const da_rope_params* r, int D, int num_tokens, void* stream) {
+int launch_rope(RopeArgs& a, const da_rope_params* r, int D, int num_tokens, void* stream) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  a.N = num_tokens;
+  a.heads = a.Hq + a.Hk + (APPEND ? a.Hkv : 0);
+  a.inv_heads = (0x100000000ULL + a.heads - 1) / a.heads;
+  // tokens of a CTA: several where that still leaves CTAs for every SM
+  a.tokens = 1;
+  while (a.tokens < kMaxTokens && num_tokens >= 2 * a.tokens * kManyCtas) a.tokens *= 2;
   if (r->type == DA_TYPE_F32)
-    launch_rope_t<float, APPEND>(a, D, r->interleaved, num_tokens, s);
+    launch_rope_t<float, APPEND>(a, D, r->interleaved, s);
   else if (r->type == DA_TYPE_F16)
-    launch_rope_t<__half, APPEND>(a, D, r->interleaved, num_tokens, s);
+    launch_rope_t<__half, APPEND>(a, D, r->interleaved, s);
   else
-    launch_rope_t<__nv_bfloat16, APPEND>(a, D, r->interleaved, num_tokens, s);
+    launch_rope_t<__nv_bfloat16, APPEND>(a, D, r->interleaved, s);
   return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
@@ -283,7 +334,8 @@ void fill_args(RopeArgs& a, const da_rope_params* r, const void* q, const void* 
   a.kw = r->norm ? r->k_weight : nullptr;
   a.freqs = r->freqs;
   a.positions = positions;
-  a.Hq = Hq;
+  a.Hq = q ? Hq : 0;
+  a.Hk = k ? Hkv : 0;
   a.Hkv = Hkv;
   a.rd = r->rotary_dim;
   a.norm = r->norm;
@@ -331,7 +383,7 @@ int decode_attn_qk_norm_rope(const da_rope_params* r, int32_t num_tokens, int32_
     st = check_rows(k, r->k_token_stride, r->k_head_stride, esize, num_tokens, num_kv_heads);
     if (st != DA_OK) return st;
   }
-  if ((long long)(q ? num_q_heads : 0) + (k ? num_kv_heads : 0) > 65536) return DA_ERR_UNSUPPORTED;
+  if ((long long)(q ? num_q_heads : 0) + (k ? num_kv_heads : 0) > 8191) return DA_ERR_UNSUPPORTED;
   if (r->rotary_dim > 0 && !positions) return DA_ERR_INVALID;
   if (positions && !aligned(positions, 4)) return DA_ERR_INVALID;
   if (num_tokens == 0) return DA_OK;
@@ -366,7 +418,7 @@ int decode_attn_append_paged_rope(const da_params* p, const da_rope_params* r, i
     st = check_rows(q, r->q_token_stride, r->q_head_stride, esize, num_tokens, p->num_q_heads);
     if (st != DA_OK) return st;
   }
-  if ((long long)(q ? p->num_q_heads : 0) + 2LL * p->num_kv_heads > 65536)
+  if ((long long)(q ? p->num_q_heads : 0) + 2LL * p->num_kv_heads > 8191)
     return DA_ERR_UNSUPPORTED;
   if (num_tokens == 0) return DA_OK;
   RopeArgs a = {};

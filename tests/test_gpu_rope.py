@@ -64,7 +64,8 @@ def test_norm_rope_matches_64_bits(dtype, D, rd, interleaved):
         _close(k, y, half_bound(y, b), "k")
 
 
-@pytest.mark.parametrize("N,Hq,Hkv", [(1, 1, 1), (1, 64, 8), (3, 33, 1), (513, 7, 2), (2, 200, 100)])
+@pytest.mark.parametrize("N,Hq,Hkv", [(1, 1, 1), (1, 64, 8), (3, 33, 1), (513, 7, 2), (2, 200, 100),
+                                       (2433, 5, 1), (4871, 1, 2), (9999, 3, 3)])
 def test_norm_rope_sizes_and_offset_weight(N, Hq, Hkv):
     rng = np.random.default_rng(N + Hq)
     D = 128
@@ -78,6 +79,17 @@ def test_norm_rope_sizes_and_offset_weight(N, Hq, Hkv):
     _close(qo, y, b, "q")
     y, b = norm_rope(_np(k), pos, fh, norm=True)
     _close(ko, y, half_bound(y, b), "k")
+
+
+def test_norm_rope_one_head_many_tokens():
+    rng = np.random.default_rng(6)
+    N, D = 12001, 64
+    pos = rng.integers(0, 4096, N).astype(np.int32)
+    f, fh = _freqs(D)
+    q = _t(rng.standard_normal((N, 1, D)).astype(np.float32), "float16")
+    y, b = norm_rope(_np(q), pos, fh, norm=True)
+    out, _ = qk.decode_attn_qk_norm_rope(q, None, _t(pos), f)
+    _close(out, y, b, "q")
 
 
 def test_norm_rope_strides_one_side_and_in_place():
@@ -207,6 +219,28 @@ def test_append_matches_64_bits(dtype, D, rd, bs, il, with_q):
         assert (out[torch.from_numpy(pad).cuda()] == 7.0).all()
     else:
         assert out is None
+
+
+def test_append_of_a_long_ragged_prefill():
+    """Many tokens, so that a CTA takes several at once, of three prompts and
+    with padding between them."""
+    rng = np.random.default_rng(13)
+    B, H, D, bs = 3, 2, 64, 16
+    lens = [7001, 1, 2444]
+    npg = -(-max(lens) // bs)
+    table, kp, vp = _cache(rng, B, npg, bs, H, D)
+    seq = np.concatenate([np.full(n, b) for b, n in enumerate(lens)] + [np.full(555, -1)])
+    pos = np.concatenate([np.arange(n) for n in lens] + [np.zeros(555)])
+    order = rng.permutation(len(seq))
+    seq, pos = seq[order].astype(np.int32), pos[order].astype(np.int32)
+    x = _t(rng.standard_normal((len(seq), 2 * H, D)).astype(np.float32), "bfloat16")
+    f, fh = _freqs(D)
+    K, bk, V, bv = _append_ref(_np(x[:, :H]), _np(x[:, H:]), pos, seq, table, kp, vp, bs, fh)
+    tk, tv = _t(kp), _t(vp)
+    qk.decode_attn_append_paged_rope(x[:, :H], x[:, H:], _t(pos), _t(table), tk, tv, f,
+                                     token_seq=_t(seq))
+    _close(tk, K, bk, "k pool")
+    _close(tv, V, bv, "v pool")
 
 
 def test_append_without_rotation_equals_the_plain_append():
