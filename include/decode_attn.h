@@ -339,7 +339,7 @@ int decode_attn_append_tiered_f16(const da_params* p, int32_t hot_window, int32_
  * good as that of a small one.  All arithmetic is f32; the only rounding to
  * fewer bits is the last one, of keys and values to the cache's f16 (to
  * nearest even, beyond its range to infinity).
- * At most 8191 heads a token (q, k and v together).
+ * At most 4096 heads a token (q, k and v together).
  * Rows may be slices of a larger tensor: token n, head h of q starts at
  * element n * q_token_stride + h * q_head_stride (k and v alike); its D
  * values are contiguous.  Every row must start on a 16-byte boundary.

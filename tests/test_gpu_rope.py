@@ -65,7 +65,7 @@ def test_norm_rope_matches_64_bits(dtype, D, rd, interleaved):
 
 
 @pytest.mark.parametrize("N,Hq,Hkv", [(1, 1, 1), (1, 64, 8), (3, 33, 1), (513, 7, 2), (2, 200, 100),
-                                       (2433, 5, 1), (4871, 1, 2), (9999, 3, 3)])
+                                       (2433, 5, 1), (4871, 1, 2), (9999, 3, 3), (16381, 2, 1)])
 def test_norm_rope_sizes_and_offset_weight(N, Hq, Hkv):
     rng = np.random.default_rng(N + Hq)
     D = 128

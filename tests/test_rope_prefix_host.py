@@ -98,7 +98,7 @@ def test_norm_rope_rejects_bad_arguments(lib):
                 dict(ko=ODD), dict(pos=None), dict(pos=ctypes.c_void_p(0x10002))):
         assert call(**bad) == qk.DA_ERR_INVALID, bad
     assert call(d=96) == qk.DA_ERR_UNSUPPORTED
-    assert call(hq=8190) == qk.DA_ERR_UNSUPPORTED
+    assert call(hq=4095) == qk.DA_ERR_UNSUPPORTED
     assert call(n=0) == qk.DA_OK
     assert lib.decode_attn_qk_norm_rope(None, 4, 8, 2, 64, FAKE, FAKE, FAKE, FAKE, FAKE,
                                         None) == qk.DA_ERR_INVALID
