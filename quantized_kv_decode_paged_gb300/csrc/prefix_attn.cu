@@ -965,6 +965,7 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
     prefetch_tensormap(&p.tm_v);
   }
   if (warp == 1) tmem_alloc(&s.tmem, 512);
+  let_next_grid_start();
   tc5_fence_before();
   __syncthreads();
   tc5_fence_after();
@@ -1029,6 +1030,16 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
 // ------------------------------------------------------------------ joining the states
 constexpr int kMergeWarps = 8;
 
+template <int V>
+__device__ __forceinline__ void load_row(const float* p, float* x) {
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    const float2 f = *reinterpret_cast<const float2*>(p + i);
+    x[i] = f.x;
+    x[i + 1] = f.y;
+  }
+}
+
 // One warp a row.
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
@@ -1036,6 +1047,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   constexpr int V = D / 32;
   const int lane = threadIdx.x & 31;
   const long long at = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  wait_for_grid_before();
   if (at >= (long long)p.B * p.T * p.Hq) return;
   const int row = (int)at;
   const int bt = row / p.Hq, hq = row - bt * p.Hq, h = hq / p.G;
@@ -1047,44 +1059,64 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int units1 = p.Hkv * p.own_tiles;
   const int tp = pn * (p.Hkv * p.row_tiles);
   const Split sp(tp + cum[p.B] * units1, p.grid);
+  // the CTAs that hold the row's prefix unit, then its own one
+  const int n0 = pn, n1 = cum[b + 1] - cum[b];
+  const int g0 = (h * p.row_tiles + rb / kPrefixRows) * n0;
+  const int g1 = tp + cum[b] * units1 + (h * p.own_tiles + r1 / kPrefixRows) * n1;
+  const int c0 = n0 ? sp.cta(g0) : 0, c1 = n1 ? sp.cta(g1) : 0;
+  const int s0 = n0 ? sp.cta(g0 + n0 - 1) - c0 + 1 : 0;  // its states
+  const int s1 = n1 ? sp.cta(g1 + n1 - 1) - c1 + 1 : 0;
   float M = -kInf, L = 0.f, o[V];
   bool partial = false;
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.f;
-  auto add = [&](float2 ml, const float* src) {
-    partial |= signbit(ml.y) != 0;
-    if (ml.y == 0.f) return;  // no key
-    const float mn = fmaxf(M, ml.x);
-    const float f = ex2_ftz(M - mn), w = ex2_ftz(ml.x - mn);
-    M = mn;
-    L = fmaf(L, f, w * fabsf(ml.y));
+  for (int j0 = 0; j0 < s0 + s1; j0 += 32) {
+    // a lane finds and weighs one state
+    const int j = j0 + lane;
+    const float2* ml = nullptr;
+    const float* src = nullptr;
+    if (j < s0 + s1) {
+      const bool own = j >= s0;
+      const int states = own ? s1 : s0, jj = own ? j - s0 : j, first = own ? c1 : c0;
+      if (states == 1) {
+        ml = (own ? p.ws_own_ml : p.ws_pre_ml) + row;
+        src = (own ? p.out : p.ws_pre_o) + (long long)row * D;
+      } else {
+        const int c = first + jj;
+        const int slot = 2 * c + (jj == 0 && sp.start(c) != (own ? g1 : g0) ? 1 : 0);
+        const long long at = (long long)slot * kPrefixRows + (own ? r1 : rb) % kPrefixRows;
+        ml = p.ws_cut_ml + at;
+        src = p.ws_cut_o + at * D;
+      }
+    }
+    const float2 v = ml ? *ml : make_float2(-kInf, 0.f);
+    partial |= __any_sync(0xffffffffu, signbit(v.y) != 0);
+    const bool some = v.y != 0.f;  // has a key
+    float top = some ? v.x : -kInf;
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = fmaf(o[i], f, w * src[lane * V + i]);
-  };
-  for (int u = 0; u < 2; ++u) {  // the prefix's states, then the own keys'
-    int g0, n, in_tile;
-    if (u == 0) {
-      n = pn;
-      g0 = (h * p.row_tiles + rb / kPrefixRows) * pn;
-      in_tile = rb % kPrefixRows;
-    } else {
-      n = cum[b + 1] - cum[b];
-      g0 = tp + cum[b] * units1 + (h * p.own_tiles + r1 / kPrefixRows) * n;
-      in_tile = r1 % kPrefixRows;
-    }
-    if (n == 0) continue;
-    const int c0 = sp.cta(g0), c1 = sp.cta(g0 + n - 1);
-    if (c0 == c1) {
-      if (u == 0)
-        add(p.ws_pre_ml[row], p.ws_pre_o + (long long)row * D);
-      else
-        add(p.ws_own_ml[row], p.out + (long long)row * D);
-      continue;
-    }
-    for (int c = c0; c <= c1; ++c) {
-      const int slot = 2 * c + (c == c0 && sp.start(c) != g0 ? 1 : 0);
-      const long long i = (long long)slot * kPrefixRows + in_tile;
-      add(p.ws_cut_ml[i], p.ws_cut_o + i * D);
+    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float mn = fmaxf(M, top);
+    if (mn == -kInf && !__any_sync(0xffffffffu, some)) continue;
+    const float f = ex2_ftz(M - mn), w = some ? ex2_ftz(v.x - mn) : 0.f;
+    float l = w * fabsf(v.y);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    L = fmaf(L, f, l);
+    M = mn;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] *= f;
+    const int n = min(32, s0 + s1 - j0);
+    const uint32_t have = __ballot_sync(0xffffffffu, some);
+#pragma unroll 4
+    for (int u = 0; u < n; ++u) {
+      const float wu = __shfl_sync(0xffffffffu, w, u);
+      const float* su = reinterpret_cast<const float*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), u));
+      if (!(have >> u & 1)) continue;
+      float x[V];
+      load_row<V>(su + lane * V, x);
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = fmaf(wu, x[i], o[i]);
     }
   }
   // A zero weight does not silence a value that is not finite: a row that met masked keys
@@ -1125,8 +1157,17 @@ cudaError_t launch_prefix_impl(const PrefixParams& p, cudaStream_t stream) {
   prefix_attn_kernel<D, CAP><<<p.grid, PGeo<D>::THREADS, smem, stream>>>(p);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  prefix_merge_kernel<D><<<(int)blocks, kMergeWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  // launched while the first kernel still runs; it waits for that one's end itself
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D>, p);
 }
 
 }  // namespace
