@@ -247,7 +247,7 @@ struct Cursor {
   const PrefixSmem<D>& s;
   int left;              // tiles of the run from this part on
   int P;                 // prefix keys
-  int k = 0;             // parts so far
+  int k = -1;            // number of the part
   int h, b, rt;          // b < 0: prefix; rt: tile of rows
   int r0, nr;
   int base, klo, khi;    // keys [klo, khi) may be seen
@@ -259,12 +259,24 @@ struct Cursor {
     h = s.first[1];
     rt = s.first[2];
     i0 = s.first[3];
-    if (left > 0) enter();
+    n = 0;
   }
-  __device__ __forceinline__ bool done() const { return left <= 0; }
   __device__ __forceinline__ bool whole() const { return n == unit_n; }
-  // Geometry of the part at (b, h, rt), its first tile i0.
-  __device__ __forceinline__ void enter() {
+  // On to the run's first or next part; false behind the last one.
+  __device__ __forceinline__ bool step() {
+    left -= n;
+    if (left <= 0) return false;
+    if (++k > 0) {
+      i0 = 0;
+      if (++rt == (b < 0 ? p.row_tiles : p.own_tiles)) {
+        rt = 0;
+        if (++h == p.Hkv) {
+          h = 0;
+          b = max(b, -1) + 1;
+          while (s.cum[b + 1] == s.cum[b]) ++b;
+        }
+      }
+    }
     r0 = rt * kPrefixRows;
     if (b < 0) {
       nr = min(kPrefixRows, p.B * p.R1 - r0);
@@ -280,21 +292,7 @@ struct Cursor {
       unit_n = s.cum[b + 1] - s.cum[b];
     }
     n = min(unit_n - i0, left);
-  }
-  __device__ __forceinline__ void next() {
-    left -= n;
-    ++k;
-    i0 = 0;
-    if (left <= 0) return;
-    if (++rt == (b < 0 ? p.row_tiles : p.own_tiles)) {
-      rt = 0;
-      if (++h == p.Hkv) {
-        h = 0;
-        b = max(b, -1) + 1;
-        while (s.cum[b + 1] == s.cum[b]) ++b;
-      }
-    }
-    enter();
+    return true;
   }
   __device__ __forceinline__ bool small() const { return nr <= kSmallRows; }
   // First row of the Q buffer that the part's rows take.
@@ -443,7 +441,10 @@ struct Loader {
   // The cursor's tile j, and the cursor moved on.
   __device__ __forceinline__ Tile fetch(Cursor<D>& c, int& j) const {
     Tile t = {0, 0, 0, false};
-    if (c.done()) return t;
+    if (j == c.n) {
+      j = 0;
+      if (!c.step()) return t;
+    }
     t.h = c.h;
     t.k0 = c.base + (c.i0 + j) * G::KT + sub * p.box_rows;
     t.seen = copies() && t.k0 < c.khi && t.k0 + p.box_rows > c.klo;
@@ -451,10 +452,7 @@ struct Loader {
       const int* table = c.b < 0 ? p.prefix_table : p.block_table + (long long)c.b * p.max_blocks;
       t.blk = table[t.k0 >> p.log2_bs];
     }
-    if (++j == c.n) {
-      j = 0;
-      c.next();
-    }
+    ++j;
     return t;
   }
   // K or V of tile number x of the CTA's run.
@@ -484,11 +482,11 @@ struct Loader {
     const int tiles = s.run;
     if (tiles == 0) return;
     int j = 0;
-    Tile t0 = {0, 0, 0, false}, t1 = t0, t2 = fetch(c, j);  // tiles x, x + 1, x + 2
+    Tile t0 = {0, 0, 0, false}, t1 = t0, t2 = t0;  // tiles x, x + 1, x + 2
 #pragma unroll 1
-    for (int x = -2; x < tiles; ++x) {
+    for (int x = -3; x < tiles; ++x) {
 #pragma unroll 1
-      for (int u = x < 0 ? 1 : 0; u < (x + 2 < tiles ? 2 : 1); ++u)
+      for (int u = x < 0 ? 1 : 0; u < (x > -3 && x + 2 < tiles ? 2 : 1); ++u)
         if (!issue(u ? t2 : t0, u ? x + 2 : x, u == 0)) return;
       t0 = t1;
       t1 = t2;
@@ -501,46 +499,46 @@ struct Loader {
 // n <= 32 rows of Q into rows row0 .. of the Q buffer by one warp; lane i names
 // row i (`mine`, its place in [B, T, Hq]; lanes past the last name the last).  The power
 // of two that brings a row's largest value to [2^9, 2^10), then two f16 terms.
-// A lane takes 8 values, D / 8 lanes a row: 16-byte stores.
+// A lane takes 8 values, D / 8 lanes a row: 16-byte stores.  All rows are touched first, so
+// that the loop over them, kept small, finds them in L1.
 template <int D>
-__device__ __forceinline__ void load_q_rows(const float* src, float qscale, PrefixSmem<D>& s, int mine,
-                                         int row0, int n) {
+__device__ __forceinline__ void load_q_rows(const float* src, float qscale, PrefixSmem<D>& s,
+                                            int mine, int row0, int n) {
   constexpr int LR = D / 8;        // lanes of a row
   constexpr int RW = 32 / LR;      // rows of a step
-  constexpr int BATCH = 4;         // steps in flight
+  constexpr int LINES = D / 32;    // 128-byte lines of a row
   const int lane = threadIdx.x & 31, sub = lane / LR, d = lane % LR * 8;
 #pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += RW * BATCH) {
-    float4 x[BATCH][2];
+  for (int i = 0; i < n; i += 32 / LINES) {
+    const int at = __shfl_sync(0xffffffffu, mine, min(i + lane / LINES, 31));
+    uint32_t unused;
+    asm volatile("ld.global.b32 %0, [%1];"
+                 : "=r"(unused)
+                 : "l"(src + (long long)at * D + lane % LINES * 32));
+  }
+#pragma unroll 1
+  for (int i = 0; i < n; i += RW) {
+    const int at = __shfl_sync(0xffffffffu, mine, min(i + sub, 31));
+    const float4* q = reinterpret_cast<const float4*>(src + (long long)at * D + d);
+    const float4 x = q[0], y = q[1];
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    const int row = row0 + min(i + sub, n - 1);
+    float m = 0.f;
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const int at = __shfl_sync(0xffffffffu, mine, min(i0 + u * RW + sub, 31));
-      const float4* q = reinterpret_cast<const float4*>(src + (long long)at * D + d);
-      x[u][0] = q[0];
-      x[u][1] = q[1];
-    }
+    for (int u = 0; u < 8; ++u) m = fmaxf(m, fabsf(v[u]));
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const int row = row0 + min(i0 + u * RW + sub, n - 1);
-      const float v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w,
-                          x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
-      float m = 0.f;
+    for (int o = LR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // exponent of the largest value, clamped so that both powers are normal
+    int e = (int)(__float_as_uint(m) >> 23) - 127;
+    e = min(max(e, -100), 120);
+    const float f = __uint_as_float((uint32_t)(9 - e + 127) << 23);
+    if (d == 0) s.row_scale[row] = qscale * __uint_as_float((uint32_t)(e - 9 + 127) << 23);
+    uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-#pragma unroll
-      for (int o = LR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      // exponent of the largest value, clamped so that both powers are normal
-      int e = (int)(__float_as_uint(m) >> 23) - 127;
-      e = min(max(e, -100), 120);
-      const float f = __uint_as_float((uint32_t)(9 - e + 127) << 23);
-      if (d == 0) s.row_scale[row] = qscale * __uint_as_float((uint32_t)(e - 9 + 127) << 23);
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) split_half2(v[2 * i] * f, v[2 * i + 1] * f, hi[i], lo[i]);
-      const int at = (d >> 6) * (kPrefixRows * 128) + row * 128 + ((((d & 63) >> 3) ^ (row & 7)) << 4);
-      *reinterpret_cast<uint4*>(s.q + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(s.q + PGeo<D>::QTERM + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
+    for (int u = 0; u < 4; ++u) split_half2(v[2 * u] * f, v[2 * u + 1] * f, hi[u], lo[u]);
+    const int to = (d >> 6) * (kPrefixRows * 128) + row * 128 + ((((d & 63) >> 3) ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(s.q + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(s.q + PGeo<D>::QTERM + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -564,7 +562,7 @@ template <int D>
 __device__ void q_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   const int lane = threadIdx.x & 31;
   bool prev_small = true;
-  for (Cursor<D> c(p, s); !c.done(); c.next()) {
+  for (Cursor<D> c(p, s); c.step();) {
     const int k = c.k;
     const bool small = c.small();
     // a part of many rows takes the whole buffer, one of few the half of part k - 2
@@ -583,13 +581,14 @@ __device__ void q_loop(const PrefixParams& p, PrefixSmem<D>& s) {
 }
 
 // ------------------------------------------------------------------ softmax warps
-// Largest of 32 scores a lane, four chains.
-__device__ __forceinline__ float max32(const float* v) {
+// Largest of N scores, four chains.
+template <int N>
+__device__ __forceinline__ float largest(const float* v) {
   float mx[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) mx[i] = v[i];
 #pragma unroll
-  for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+  for (int i = 4; i < N; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
   return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
 
@@ -608,7 +607,7 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   using G = PGeo<D>;
   constexpr int KT = G::KT;
   constexpr bool TWO = G::SOFTG == 2;
-  constexpr int CH = TWO ? 64 : 32;
+  constexpr int W = CAP ? 16 : 32;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
   const int group = TWO ? (threadIdx.x >> 7) - 1 : 0;  // takes the tiles x = group mod 2
   const int row = w * 32 + lane;
@@ -616,7 +615,7 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   const int box_shift = __ffs(p.box_rows) - 1;
   int x0 = 0;                // tiles of the parts before
   int shared_sums[2] = {0, 0};  // parts so far, by parity, whose sum took both groups
-  for (Cursor<D> c(p, s); !c.done(); x0 += c.n, c.next()) {
+  for (Cursor<D> c(p, s); c.step(); x0 += c.n) {
     const int k = c.k;
     if (!c.small()) {
       // many rows: they take the whole buffer
@@ -664,41 +663,38 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s) {
         const int bad = s.bad[x & 7];
         masked = !__all_sync(0xffffffffu, (!on || (lo <= k0 && hi >= k0 + KT)) && bad == 0);
         partial |= masked;
-        // Two passes over the scores, CH columns a step: loops that stay in the
+        // Two passes over the scores, W or 32 columns a step: loops that stay in the
         // instruction cache and need few registers.
-        if (CAP || masked) {
 #pragma unroll 1
-          for (int i0 = 0; i0 < KT; i0 += 32) {
-            float v[32];
-            tmem_load<32>(sa + i0, v);
-            if (CAP) {
+        for (int i0 = 0; i0 < KT; i0 += W) {
+          float v[W];
+          if constexpr (CAP)
+            tmem_load16(sa + i0, v);
+          else
+            tmem_load<W>(sa + i0, v);
+          if (CAP) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = capped(v[i] * scale, p.softcap2, p.softcap_inv);
-            }
-            if (masked) {
-              // bit i: key k0 + i0 + i is seen
-              const int a = min(max(lo - k0 - i0, 0), 32), z = min(max(hi - k0 - i0, 0), 32);
-              uint32_t seen = (uint32_t)(0xffffffffull << a) & ~(uint32_t)(0xffffffffull << z);
-#pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                if ((bad >> ((i0 + i) >> box_shift)) & 1) seen &= ~(0xffu << i);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(seen >> i & 1)) v[i] = -kInf;
-            }
-            tmem_st32(sa + i0, v);
-            top = fmaxf(top, max32(v));
+            for (int i = 0; i < W; ++i) v[i] = capped(v[i] * scale, p.softcap2, p.softcap_inv);
           }
-          tmem_wait_st();
-        } else {
-#pragma unroll 1
-          for (int i0 = 0; i0 < KT; i0 += CH) {
-            float v[CH];
-            tmem_load<CH>(sa + i0, v);
+          if (masked) {
+            // bit i: key k0 + i0 + i is seen
+            const int a = min(max(lo - k0 - i0, 0), 32), z = min(max(hi - k0 - i0, 0), 32);
+            uint32_t seen = (uint32_t)(0xffffffffull << a) & ~(uint32_t)(0xffffffffull << z);
 #pragma unroll
-            for (int h = 0; h < CH; h += 32) top = fmaxf(top, max32(v + h));
+            for (int i = 0; i < W; i += 8)
+              if ((bad >> ((i0 + i) >> box_shift)) & 1) seen &= ~(0xffu << i);
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+              if (!(seen >> i & 1)) v[i] = -kInf;
           }
+          if (CAP || masked) {
+#pragma unroll
+            for (int i = 0; i < W; i += 16)
+              tmem_st16(sa + i0 + i, reinterpret_cast<const uint32_t*>(v + i));
+          }
+          top = fmaxf(top, largest<W>(v));
         }
+        if (CAP || masked) tmem_wait_st();
       }
       // the maximum up to the tile before, from the other group; then this one's to it
       float before = m;
@@ -724,33 +720,29 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s) {
         const float2 cc2 = make_float2(cc, cc), base2 = make_float2(-base, -base);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll 1
-        for (int i0 = 0; i0 < KT; i0 += CH) {
-          float v[CH];
-          tmem_load<CH>(sa + i0, v);
+        for (int i0 = 0; i0 < KT; i0 += 32) {
+          float v[32];
+          uint32_t ph[16], pl[16];
+          tmem_load<32>(sa + i0, v);
 #pragma unroll
-          for (int h = 0; h < CH; h += 32) {
-            uint32_t ph[16], pl[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float2 e = fma2(make_float2(v[h + i], v[h + i + 1]), cc2, base2);
-              e.x = ex2_ftz(e.x);
-              e.y = ex2_ftz(e.y);
-              if (i & 2)
-                sum1 = add2(sum1, e);
-              else
-                sum0 = add2(sum0, e);
-              const __half2 hh = __floats2half2_rn(e.x, e.y);
-              const float2 hf = __half22float2(hh);
-              const float2 r = add2(e, make_float2(-hf.x, -hf.y));
-              const __half2 hl = __floats2half2_rn(r.x, r.y);
-              ph[i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
-              pl[i / 2] = *reinterpret_cast<const uint32_t*>(&hl);
-            }
-            // the weights of 32 keys take the columns of their scores: 16 of high terms,
-            // 16 of low
-            tmem_st16(sa + i0 + h, ph);
-            tmem_st16(sa + i0 + h + 16, pl);
+          for (int i = 0; i < 32; i += 2) {
+            float2 e = fma2(make_float2(v[i], v[i + 1]), cc2, base2);
+            e.x = ex2_ftz(e.x);
+            e.y = ex2_ftz(e.y);
+            if (i & 2)
+              sum1 = add2(sum1, e);
+            else
+              sum0 = add2(sum0, e);
+            const __half2 hh = __floats2half2_rn(e.x, e.y);
+            const float2 hf = __half22float2(hh);
+            const float2 r = add2(e, make_float2(-hf.x, -hf.y));
+            const __half2 hl = __floats2half2_rn(r.x, r.y);
+            ph[i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+            pl[i / 2] = *reinterpret_cast<const uint32_t*>(&hl);
           }
+          // the weights of 32 keys take the columns of their scores: 16 of high terms, 16 of low
+          tmem_st16(sa + i0, ph);
+          tmem_st16(sa + i0 + 16, pl);
         }
         // l counts against `now`, so far against this group's last maximum m
         l = fmaf(l, ex2_ftz(m - ref), (sum0.x + sum0.y) + (sum1.x + sum1.y));
@@ -804,11 +796,11 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   const int row = w * 32 + lane, col = ((int)(threadIdx.x >> 7) - 1 - G::SOFTG) * C;
   const uint32_t lanes = s.tmem + ((uint32_t)(w * 32) << 16);
   int x = 0;
-  for (Cursor<D> c(p, s); !c.done(); c.next()) {
+  for (Cursor<D> c(p, s); c.step();) {
     const bool any = w * 32 < c.nr, on = row < c.nr;
-    float acc[C];
+    float2 acc[C / 2];
 #pragma unroll
-    for (int i = 0; i < C; ++i) acc[i] = 0.f;
+    for (int i = 0; i < C / 2; ++i) acc[i] = make_float2(0.f, 0.f);
     for (int j = 0; j < c.n; ++j, ++x) {
       const int buf = x % G::NS;
       const uint32_t parity = (x / G::NS) & 1;
@@ -825,16 +817,14 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
       if (!warp_wait<D>(p, s, &s.pv_done[buf], parity)) return;
       if (any) {
         tc5_fence_after();
-        if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
-          for (int i = 0; i < C; ++i) acc[i] *= f;
-        }
+        const float2 f2 = make_float2(f, f);
 #pragma unroll
         for (int i = 0; i < C; i += 16) {
           float o[16];
           tmem_load16(lanes + col + i, o);
 #pragma unroll
-          for (int u = 0; u < 16; ++u) acc[i + u] += o[u];
+          for (int u = 0; u < 16; u += 2)
+            acc[(i + u) / 2] = fma2(acc[(i + u) / 2], f2, make_float2(o[u], o[u + 1]));
         }
         tc5_fence_before();
       }
@@ -852,7 +842,7 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
 #pragma unroll
       for (int i = 0; i < C; i += 4)
         *reinterpret_cast<float4*>(dst + col + i) =
-            make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+            make_float4(acc[i / 2].x, acc[i / 2].y, acc[i / 2 + 1].x, acc[i / 2 + 1].y);
     }
   }
 }
@@ -876,7 +866,7 @@ __device__ void qk_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   const uint64_t q0 = smem_desc(smem_u32(s.q), 16, 1024);
   const uint64_t k0 = smem_desc(smem_u32(s.ring), 16, 1024);
   int x = 0;
-  for (Cursor<D> c(p, s); !c.done(); c.next()) {
+  for (Cursor<D> c(p, s); c.step();) {
     if (!wait_or_abort<D>(p, s, &s.q_full[c.k & 1], (c.k >> 1) & 1)) return;
     const uint64_t q = q0 + c.q_row() * 8;  // 128 bytes a row
     for (int j = 0; j < c.n; ++j, ++x) {
@@ -918,12 +908,14 @@ __device__ void pv_loop(const PrefixParams& p, PrefixSmem<D>& s) {
     if (!wait_or_abort<D>(p, s, &s.p_full[buf], (x / G::NS) & 1)) return;
     tc5_fence_after();
     const uint64_t v = v0 + slot * (G::TILE / 16);
+#pragma unroll 1
+    for (int i = 0; i < 2 * KT; i += 32) {
+      const int term = i < KT ? 1 : 0, k = i < KT ? i : i - KT;
 #pragma unroll
-    for (int term = 1; term >= 0; --term)
-#pragma unroll
-      for (int k = 0; k < KT; k += 16)
-        mma_ts(tm, tm + G::S0 + buf * KT + k / 32 * 32 + term * 16 + k % 32 / 2, v + k * 8, idesc,
-               term == 0 || k > 0);
+      for (int u = 0; u < 2; ++u)
+        mma_ts(tm, tm + G::S0 + buf * KT + k + term * 16 + u * 8, v + (k + u * 16) * 8, idesc,
+               i + u > 0);
+    }
     mma_commit(&s.pv_done[buf]);
     mma_commit(&s.empty[slot]);
   }
