@@ -48,9 +48,9 @@ cudaError_t launch_split_merge(int rows, int max_splits, int D, const float* o_p
 // prefix_table, the others through block_table.
 constexpr int kPrefixRows = 128;      // rows of a tile (the MMA's M)
 // sequences of a launch: their lengths sit in shared memory beside the tiles
-__host__ __device__ constexpr int prefix_max_batch(int D) { return D >= 256 ? 172 : 256; }
+__host__ __device__ constexpr int prefix_max_batch(int D) { return D >= 256 ? 160 : 256; }
 // keys of a tile
-__host__ __device__ constexpr int prefix_tile_keys(int D) { return D >= 256 ? 64 : 128; }
+__host__ __device__ constexpr int prefix_tile_keys(int D) { return D == 64 ? 128 : 64; }
 
 struct alignas(128) PrefixParams {
   CUtensorMap tm_k;  // boxes of box_rows keys, one kv head, box_slices 128-byte slices

@@ -29,13 +29,13 @@
 // (their steps truncate at their own size), and the sums over tiles are ordinary f32 adds in
 // registers.
 //
-// Warps.  0: TMA of K and V pages into a ring of tiles.  1 and 2: one thread
+// Warps.  0: TMA of K pages into a ring of tiles, 3: of V pages (D = 256: 0
+// both, 3 the Q of units with few rows).  1 and 2: one thread
 // issues the scores' products, one the values' (S and P share three buffers, so scores run
-// ahead while the softmax of a tile runs).  3: the next unit's Q, when its rows are few.
-// Then one or two warpgroups of softmax, a thread a row: scores to weights, running maximum
-// and sum; two groups take turns at the tiles and hand the maximum on.  Then
-// one (D = 256: two, 128 columns each) of sums, a thread a row:
-// acc = acc * 2^(m_old - m_new) + O_tile, and the state's store.
+// ahead while the softmax of a tile runs).  Then two warpgroups (D = 256: one) of softmax, a
+// thread a row: scores to weights, running maximum and sum; they take turns at the tiles and hand
+// the maximum on, and convert Q.  Then one (D = 256: two, 128 columns each) of sums, a thread a
+// row: acc = acc * 2^(m_old - m_new) + O_tile, and the state's store.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -55,22 +55,25 @@ namespace {
 constexpr float kInf = INFINITY;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// tanh by its identity in 2^x; below 1/2, where the identity's rounding next
-// to 1 would cost relative accuracy, by the Taylor series through y^13
-// (coefficients 2^2n (2^2n - 1) B_2n / (2n)!): a score keeps f32's relative
-// accuracy whatever the cap.
-__device__ __forceinline__ float capped(float x, float cap2, float inv_cap2) {
-  const float y = x * inv_cap2;
-  const float y2 = y * y;
-  float t = 21844.f / 6081075.f;
-  t = fmaf(t, y2, -1382.f / 155925.f);
-  t = fmaf(t, y2, 62.f / 2835.f);
-  t = fmaf(t, y2, -17.f / 315.f);
-  t = fmaf(t, y2, 2.f / 15.f);
-  t = fmaf(t, y2, -1.f / 3.f);
-  t = fmaf(t * y2, y, y);
-  const float big = 1.f - __fdividef(2.f, ex2_ftz(y * 2.8853900817779268f) + 1.f);
-  return cap2 * (fabsf(y) <= 0.5f ? t : big);
+// cap * tanh(y) in base-2 units.  Below |y| = 1/2 by tanh's Taylor series
+// through y^13 (coefficients 2^2n (2^2n - 1) B_2n / (2n)!), whose error is relative: a score
+// keeps f32's accuracy whatever the cap.  Above, by the identity in 2^x, whose rounding
+// next to 1 costs 3e-7 of a tanh that is near 1.
+__device__ __forceinline__ float2 cap_series(float2 y, float cap2) {
+  auto two = [](float c) { return make_float2(c, c); };
+  const float2 y2 = mul2(y, y);
+  float2 t = two(21844.f / 6081075.f);
+  t = fma2(t, y2, two(-1382.f / 155925.f));
+  t = fma2(t, y2, two(62.f / 2835.f));
+  t = fma2(t, y2, two(-17.f / 315.f));
+  t = fma2(t, y2, two(2.f / 15.f));
+  t = fma2(t, y2, two(-1.f / 3.f));
+  return mul2(fma2(mul2(t, y2), y, y), two(cap2));
+}
+__device__ __forceinline__ float cap_any(float y, float cap2) {
+  const float small = cap_series(make_float2(y, y), cap2).x;
+  const float big = cap2 * (1.f - __fdividef(2.f, ex2_ftz(y * 2.8853900817779268f) + 1.f));
+  return fabsf(y) <= 0.5f ? small : big;
 }
 
 // ------------------------------------------------------------------ what a row sees
@@ -143,7 +146,7 @@ __device__ __noinline__ void attend_row(const PrefixParams& p, int b, int kv, co
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     s *= p.qscale;
-    if (p.softcap2 > 0.f) s = capped(s, p.softcap2, p.softcap_inv);
+    if (p.softcap2 > 0.f) s = cap_any(s * p.softcap_inv, p.softcap2);
     const float mn = fmaxf(m, s);
     const float base = mn == -kInf ? 0.f : mn;
     const float f = exp2f(m - base), w = exp2f(s - base);
@@ -165,11 +168,19 @@ struct PGeo {
   static constexpr int SL = D / 64;               // 128-byte slices of a row
   static constexpr int TILE = KT * D * 2;         // bytes of a K or V tile
   static constexpr int QTERM = kPrefixRows * D * 2;  // bytes of one term of Q
-  static constexpr int RING = D == 64 ? 8 : D == 128 ? 4 : 3;  // K and V tiles in flight
   static constexpr int NS = 3;                    // S / P buffers
-  static constexpr int S0 = D;                    // tensor-memory columns: O, then S / P
-  static constexpr int F0 = S0 + NS * KT;         // then, if any are left, the factors
+  // Tensor-memory columns: O, then (D < 256) the two terms of Q, then S / P, then, if any are
+  // left, the factors.  With Q there the score products read only K from shared memory (with both
+  // operands in it they ran at two thirds of their rate), and 64 KB more of it hold tiles in
+  // flight.  D = 256 has no room for Q beside O.
+  static constexpr bool QT = D < 256;
+  static constexpr int Q0 = QT ? D : 0;
+  static constexpr int S0 = QT ? 2 * D : D;
+  static constexpr int F0 = S0 + NS * KT;
   static constexpr bool FAC_TMEM = F0 + NS <= 512;
+  // Tiles in flight: with Q in tensor memory K and V have a ring and a loading
+  // warp each; else three tiles are shared, in the products' order.
+  static constexpr int RK = QT ? 7 : 3, RV = QT ? 6 : 0, RING = RK + RV;
   static constexpr int AC = D < 128 ? D : 128;    // columns a sum thread holds
   static constexpr int SUMG = D / AC;             // sum warpgroups
   static constexpr int SOFTG = D >= 256 ? 1 : 2;  // softmax warpgroups, taking turns at the tiles
@@ -179,14 +190,20 @@ struct PGeo {
   // sum over the warpgroups stays within the launch's.
   static constexpr int REG_LAUNCH = 128;
   static constexpr int REG_LOAD = 64;
-  static constexpr int REG_SOFT = SOFTG == 1 ? 96 : 136;
-  static constexpr int REG_SUM = 176;
+  static constexpr int REG_SOFT = SOFTG == 1 ? 112 : 136;
+  static constexpr int REG_SUM = SOFTG == 1 ? 168 : 176;
   static_assert(F0 <= 512, "tensor memory");
   static_assert(REG_LOAD + SOFTG * REG_SOFT + SUMG * REG_SUM <= GROUPS * REG_LAUNCH, "registers");
   static_assert(THREADS * REG_LAUNCH <= 65536, "registers");
 };
 
-constexpr int kSmallRows = 64;  // parts of at most this many rows share the Q buffer in halves
+// Parts of at most this many rows leave room for the next part's Q: a quarter of the lanes
+// each in tensor memory, half of the buffer in shared memory.
+template <int D>
+constexpr int kSmallRows = PGeo<D>::QT ? 32 : 64;
+// Units cost more than their tiles: Q, the first tile's latencies, the state's store.  The list
+// counts so many tiles for it (fitted to 1 to 16 tiles a unit, 8 to 128 rows).
+constexpr int kPrefixExtra = 4, kOwnExtra = 1;
 // Weights are kept times 2^10: those down to 2^-24 of a row's largest stay normal f16
 // numbers, and the largest is far from f16's limit.
 constexpr float kShift = 10.f;
@@ -195,25 +212,25 @@ template <int D>
 struct PrefixSmem {
   using G = PGeo<D>;
   static constexpr int MAXB = prefix_max_batch(D);
-  uint8_t q[2 * G::QTERM];
   uint8_t ring[G::RING * G::TILE];
+  uint8_t q[G::QT ? 16 : 2 * G::QTERM];
   uint64_t full[G::RING], empty[G::RING];
   uint64_t s_full[G::NS], p_full[G::NS], pv_done[G::NS], o_free[G::NS];
   uint64_t q_full[2], q_free[2], drain[2];
-  uint64_t m_ready[4], l_ready[2][4];                    // by warp of a warpgroup
-  float row_scale[kPrefixRows];                          // qscale * 2^e, by row of the Q buffer
+  uint64_t m_ready[4], l_ready[2][4], q_half[4];         // by warp of a warpgroup
+  float row_scale[G::QT ? 1 : kPrefixRows];              // qscale * 2^e, by row of the Q buffer
   float fac[G::FAC_TMEM ? 1 : G::NS * kPrefixRows];      // 2^(m_old - m_new) of a tile's rows
-  // two softmax warpgroups: the running maximum from one tile to the next, and
-  // the sum of the one that does not end the part
+  // two softmax warpgroups: the running maximum from one tile to the next, the sum of the one
+  // that does not end the part, the largest value of their halves of a Q row
   float m[G::SOFTG == 1 ? 1 : kPrefixRows], l[G::SOFTG == 1 ? 1 : 2 * kPrefixRows],
-      m_last[G::SOFTG == 1 ? 1 : 2 * kPrefixRows];
-  int cum[MAXB + 1];                                     // own-key tiles before sequence b
+      m_last[G::SOFTG == 1 ? 1 : 2 * kPrefixRows], q_max[G::SOFTG == 1 ? 1 : 2 * kPrefixRows];
+  int cum[MAXB + 1];                                     // the list's tiles a unit before sequence b
   int len[MAXB], qp[MAXB];                               // seq_info
-  int bad[8];                                            // per tile (mod 8): masked boxes of keys
+  int bad[16];                                           // per tile (mod 16): masked boxes of keys
   int warp_sum[16];
   int lo, hi;                                            // prefix keys some row sees
-  int first[4];                                          // where the CTA's run starts: b, h, rt, i0
-  int run;                                               // its tiles
+  int first[4];                                          // where the CTA's run starts: b, h, rt, tile
+  int run;                                               // its length in the list
   int abort;
   uint32_t tmem;
 };
@@ -236,16 +253,18 @@ struct Split {
   }
 };
 
-// The parts of units that a CTA's run [g0, g1) of the tile list is made of,
-// one after the other.  Part: rows [r0, r0 + nr) of kv head h (r0 counts the
-// batch's rows in the prefix, the sequence's in its own keys), key tiles
-// [i0, i0 + n), tile i's keys starting at base + i * KT.
+// The parts of units that a CTA's run of the list is made of, one after the
+// other.  Part: rows [r0, r0 + nr) of kv head h (r0 counts the batch's rows in the prefix, the
+// sequence's in its own keys), key tiles [i0, i0 + n), tile i's keys starting at base + i * KT.
+// A unit's first `extra` entries of the list stand for its fixed cost; runs that hold only
+// such entries of a unit have no part of it.
 template <int D>
 struct Cursor {
   static constexpr int KT = PGeo<D>::KT;
   const PrefixParams& p;
   const PrefixSmem<D>& s;
-  int left;              // tiles of the run from this part on
+  int left;              // entries of the run from this part on
+  int at, len;           // the part's first entry of its unit, its entries
   int P;                 // prefix keys
   int k = -1;            // number of the part
   int h, b, rt;          // b < 0: prefix; rt: tile of rows
@@ -254,49 +273,57 @@ struct Cursor {
   int unit_n, i0, n;
 
   __device__ __forceinline__ Cursor(const PrefixParams& p_, const PrefixSmem<D>& s_)
-      : p(p_), s(s_), left(s_.run), P(p_.prefix_pages << p_.log2_bs) {
+      : p(p_), s(s_), left(s_.run), at(s_.first[3]), len(-1), P(p_.prefix_pages << p_.log2_bs) {
     b = s.first[0];
     h = s.first[1];
     rt = s.first[2];
-    i0 = s.first[3];
     n = 0;
   }
   __device__ __forceinline__ bool whole() const { return n == unit_n; }
   // On to the run's first or next part; false behind the last one.
   __device__ __forceinline__ bool step() {
-    left -= n;
-    if (left <= 0) return false;
-    if (++k > 0) {
-      i0 = 0;
-      if (++rt == (b < 0 ? p.row_tiles : p.own_tiles)) {
-        rt = 0;
-        if (++h == p.Hkv) {
-          h = 0;
-          b = max(b, -1) + 1;
-          while (s.cum[b + 1] == s.cum[b]) ++b;
+    do {
+      if (len >= 0) {
+        left -= len;
+        at = 0;
+        if (left > 0 && ++rt == (b < 0 ? p.row_tiles : p.own_tiles)) {
+          rt = 0;
+          if (++h == p.Hkv) {
+            h = 0;
+            b = max(b, -1) + 1;
+            while (s.cum[b + 1] == s.cum[b]) ++b;
+          }
         }
       }
-    }
+      if (left <= 0) return false;
+      int extra = kOwnExtra;
+      if (b < 0) {
+        extra = kPrefixExtra;
+        klo = s.lo;
+        khi = s.hi;
+        base = klo / KT * KT;
+        unit_n = (khi + KT - 1) / KT - klo / KT;
+      } else {
+        key_range(p, s.len[b], s.qp[b], 0, p.T - 1, klo, khi);
+        klo = max(klo, P);
+        base = P + (klo - P) / KT * KT;
+        unit_n = s.cum[b + 1] - s.cum[b] - extra;
+      }
+      len = min(unit_n + extra - at, left);
+      i0 = max(0, at - extra);
+      n = at + len - extra - i0;
+    } while (n <= 0);
+    ++k;
     r0 = rt * kPrefixRows;
-    if (b < 0) {
-      nr = min(kPrefixRows, p.B * p.R1 - r0);
-      klo = s.lo;
-      khi = s.hi;
-      base = klo / KT * KT;
-      unit_n = (khi + KT - 1) / KT - klo / KT;
-    } else {
-      nr = min(kPrefixRows, p.R1 - r0);
-      key_range(p, s.len[b], s.qp[b], 0, p.T - 1, klo, khi);
-      klo = max(klo, P);
-      base = P + (klo - P) / KT * KT;
-      unit_n = s.cum[b + 1] - s.cum[b];
-    }
-    n = min(unit_n - i0, left);
+    nr = min(kPrefixRows, (b < 0 ? p.B * p.R1 : p.R1) - r0);
     return true;
   }
-  __device__ __forceinline__ bool small() const { return nr <= kSmallRows; }
-  // First row of the Q buffer that the part's rows take.
-  __device__ __forceinline__ int q_row() const { return small() ? (k & 1) * kSmallRows : 0; }
+  __device__ __forceinline__ bool small() const { return nr <= kSmallRows<D>; }
+  // Lane of tensor memory (row of the Q buffer) of the part's first row.
+  __device__ __forceinline__ int lane0() const {
+    constexpr int parts = kPrefixRows / kSmallRows<D>;
+    return small() ? k % parts * kSmallRows<D> : 0;
+  }
   // Sequence, query token and place in [B, T, Hq] of the part's row i.
   __device__ __forceinline__ int out_row(int i, int& seq, int& tok) const {
     int r = r0 + i;
@@ -330,7 +357,7 @@ __device__ int make_plan(const PrefixParams& p, PrefixSmem<D>& s) {
       atomicMax(&s.hi, min(hi, P));
     }
     const int l = max(lo, P);
-    if (hi > l) n = (hi - P + KT - 1) / KT - (l - P) / KT;
+    if (hi > l) n = (hi - P + KT - 1) / KT - (l - P) / KT + kOwnExtra;
   }
   int sum = n;
 #pragma unroll
@@ -348,8 +375,8 @@ __device__ int make_plan(const PrefixParams& p, PrefixSmem<D>& s) {
   return flags;
 }
 
-// Where the run that starts at tile g begins: sequence (-1: the prefix), kv
-// head, tile of rows, tile of the unit.  pn: tiles of a prefix unit, tp: of the
+// Where the run that starts at entry g of the list begins: sequence (-1: the
+// prefix), kv head, tile of rows, entry of the unit.  pn: entries of a prefix unit, tp: of the
 // whole prefix.
 template <int D>
 __device__ void find_first(const PrefixParams& p, PrefixSmem<D>& s, int g, int pn, int tp) {
@@ -410,12 +437,30 @@ __device__ __forceinline__ bool warp_wait(const PrefixParams& p, PrefixSmem<D>& 
   return __all_sync(0xffffffffu, wait_or_abort<D>(p, s, bar, parity));
 }
 
-// ------------------------------------------------------------------ TMA warp
-// K and V tiles into the ring in the order the products take them:
-// K(0) K(1) V(0) K(2) V(1) ...  Each lane copies one box.  Boxes without a
+// ------------------------------------------------------------------ the ring
+// Slot of tile x's K or V and how often the slot was used before.  A shared
+// ring takes them in the products' order K(0) K(1) V(0) K(2) V(1) ...
+template <int D>
+struct Place {
+  using G = PGeo<D>;
+  int slot, use;
+  __device__ __forceinline__ static Place k(int x) {
+    if (G::QT) return {x % G::RK, x / G::RK};
+    const int at = x < 2 ? x : 2 * x - 1;
+    return {at % G::RING, at / G::RING};
+  }
+  __device__ __forceinline__ static Place v(int x) {
+    if constexpr (G::QT) return {G::RK + x % G::RV, x / G::RV};
+    const int at = 2 * x + 2;
+    return {at % G::RING, at / G::RING};
+  }
+};
+
+// ------------------------------------------------------------------ TMA warps
+// K and V tiles into the ring.  Each lane copies one box.  Boxes without a
 // visible key and pages outside the pool are filled with zeros by a copy that
-// starts past the pool's last row.  A tile's block ids are fetched a step before its K is
-// issued and kept until its V is: no copy waits for them.
+// starts past the pool's last row.  A tile's block ids are fetched a step before its copy is
+// issued: no copy waits for them.
 template <int D>
 struct Loader {
   using G = PGeo<D>;
@@ -423,11 +468,12 @@ struct Loader {
     int h, k0;     // kv head; first key of this lane's box
     int blk;       // its page, where a key of it may be seen
     bool seen;
+    bool there;    // false behind the last tile
   };
   const PrefixParams& p;
   PrefixSmem<D>& s;
   int nsl, sub, slice, boxes;
-  int r = 0;  // ring tiles issued
+  uint32_t used = 0;  // bit per slot: parity of its last copy, shifted by 16 if there was one
   int flags = 0;
 
   __device__ __forceinline__ Loader(const PrefixParams& p_, PrefixSmem<D>& s_) : p(p_), s(s_) {
@@ -438,13 +484,17 @@ struct Loader {
     slice = lane - sub * nsl;
   }
   __device__ __forceinline__ bool copies() const { return (threadIdx.x & 31) < boxes; }
-  // The cursor's tile j, and the cursor moved on.
+  // Tile j of the cursor's part, or the next part's first.
   __device__ __forceinline__ Tile fetch(Cursor<D>& c, int& j) const {
-    Tile t = {0, 0, 0, false};
+    Tile t = {0, 0, 0, false, false};
     if (j == c.n) {
       j = 0;
-      if (!c.step()) return t;
+      if (!c.step()) {
+        c.n = 0;
+        return t;
+      }
     }
+    t.there = true;
     t.h = c.h;
     t.k0 = c.base + (c.i0 + j) * G::KT + sub * p.box_rows;
     t.seen = copies() && t.k0 < c.khi && t.k0 + p.box_rows > c.klo;
@@ -457,48 +507,128 @@ struct Loader {
   }
   // K or V of tile number x of the CTA's run.
   __device__ __forceinline__ bool issue(const Tile& t, int x, bool is_v) {
-    const int lane = threadIdx.x & 31, slot = r % G::RING;
-    if (r >= G::RING && !warp_wait<D>(p, s, &s.empty[slot], (r / G::RING - 1) & 1)) return false;
+    const int lane = threadIdx.x & 31;
+    const Place<D> at = is_v ? Place<D>::v(x) : Place<D>::k(x);
+    if (at.use > 0 && !warp_wait<D>(p, s, &s.empty[at.slot], (at.use - 1) & 1)) return false;
     int row = p.num_blocks << p.log2_bs;
     const bool bad = t.seen && (t.blk < 0 || t.blk >= p.num_blocks);
     if (t.seen && !bad) row = (t.blk << p.log2_bs) + (t.k0 & (p.bs - 1));
     if (!is_v) {
       const int mask = __reduce_or_sync(0xffffffffu, bad ? 1 << sub : 0);
-      if (lane == 0) s.bad[x & 7] = mask;
+      if (lane == 0) s.bad[x & 15] = mask;
       if (bad) flags |= DEV_BAD_BLOCK;
     }
     // test hook: the first tile of CTA 0 never arrives and its consumer's wait runs out
-    const bool skip = p.test_skip_arm && blockIdx.x == 0 && r == 0;
-    if (lane == 0 && !skip) mbar_arrive_expect_tx(&s.full[slot], G::TILE);
-    __syncwarp();
-    if (copies() && !skip)
-      tma_load_4d(s.ring + slot * G::TILE + slice * (G::KT * 128) + sub * p.box_rows * 128,
-                  is_v ? &p.tm_v : &p.tm_k, &s.full[slot], 0, row, slice, t.h);
-    ++r;
+    const bool skip = p.test_skip_arm && blockIdx.x == 0 && x == 0 && !is_v;
+    if (!skip) {
+      used = (used & ~(1u << at.slot)) | (uint32_t)(at.use & 1) << at.slot | 0x10000u << at.slot;
+      if (lane == 0) mbar_arrive_expect_tx(&s.full[at.slot], G::TILE);
+      __syncwarp();
+      if (copies())
+        tma_load_4d(s.ring + at.slot * G::TILE + slice * (G::KT * 128) + sub * p.box_rows * 128,
+                    is_v ? &p.tm_v : &p.tm_k, &s.full[at.slot], 0, row, slice, t.h);
+    }
     return true;
   }
-  __device__ __forceinline__ void run() {
+  // One warp loads K or V (its own ring), or both.
+  __device__ __forceinline__ void run(bool values) {
     Cursor<D> c(p, s);
-    const int tiles = s.run;
-    if (tiles == 0) return;
     int j = 0;
-    Tile t0 = {0, 0, 0, false}, t1 = t0, t2 = t0;  // tiles x, x + 1, x + 2
+    if constexpr (G::QT) {
+      Tile now = {0, 0, 0, false, false};
 #pragma unroll 1
-    for (int x = -3; x < tiles; ++x) {
+      for (int x = -1;; ++x) {
+        const Tile next = fetch(c, j);
+        if (x >= 0 && !issue(now, x, values)) return;
+        now = next;
+        if (!now.there) return;
+      }
+    } else {
+      Tile t0 = {0, 0, 0, false, false}, t1 = t0, t2 = t0;  // tiles x, x + 1, x + 2
 #pragma unroll 1
-      for (int u = x < 0 ? 1 : 0; u < (x > -3 && x + 2 < tiles ? 2 : 1); ++u)
-        if (!issue(u ? t2 : t0, u ? x + 2 : x, u == 0)) return;
-      t0 = t1;
-      t1 = t2;
-      t2 = fetch(c, j);
+      for (int x = -3; x < 0 || t0.there; ++x) {
+#pragma unroll 1
+        for (int u = x < 0 ? 1 : 0; u < (t2.there ? 2 : 1); ++u)
+          if (!issue(u ? t2 : t0, u ? x + 2 : x, u == 0)) return;
+        t0 = t1;
+        t1 = t2;
+        t2 = fetch(c, j);
+      }
     }
+  }
+  // After an abort: the copies in flight end before their memory is given back.
+  __device__ __forceinline__ void drain() {
+    for (int i = 0; i < G::RING; ++i)
+      if (used >> (16 + i) & 1) mbar_wait(&s.full[i], used >> i & 1, nullptr, p.wait_ns);
   }
 };
 
 // ------------------------------------------------------------------ Q
-// n <= 32 rows of Q into rows row0 .. of the Q buffer by one warp; lane i names
-// row i (`mine`, its place in [B, T, Hq]; lanes past the last name the last).  The power
-// of two that brings a row's largest value to [2^9, 2^10), then two f16 terms.
+// A row of Q is divided by the power of two that brings its largest value to [2^9, 2^10) and
+// held as two f16 terms.  Powers for a row whose largest value is m (the exponent
+// clamped so that both are normal): what it is multiplied by, and what undoes it.
+__device__ __forceinline__ void q_powers(float m, float& by, float& undo) {
+  int e = (int)(__float_as_uint(m) >> 23) - 127;
+  e = min(max(e, -100), 120);
+  by = __uint_as_float((uint32_t)(9 - e + 127) << 23);
+  undo = __uint_as_float((uint32_t)(e - 9 + 127) << 23);
+}
+
+// Q in tensor memory: warp w of softmax group g converts half g of the rows of
+// the part that lie in lanes [32 w, 32 w + 32), a thread a row.  The groups tell each other
+// their halves' largest values; `uses` counts that.  Gives qscale * 2^e of the thread's row.
+template <int D>
+__device__ __forceinline__ bool load_q_lanes(const PrefixParams& p, PrefixSmem<D>& s,
+                                             const Cursor<D>& c, int group, int w, uint32_t lanes,
+                                             int uses, float& scale) {
+  constexpr int H = D / 2;
+  const int lane = threadIdx.x & 31, row = w * 32 + lane;
+  int seq, tok;
+  const int at = c.out_row(min(max(row - c.lane0(), 0), c.nr - 1), seq, tok);
+  const float* src = p.q + (long long)at * D + group * H;
+#pragma unroll
+  for (int i = 0; i < H; i += 32) {  // the lines are under way before the first is waited for
+    uint32_t unused;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(unused) : "l"(src + i));
+  }
+  float m = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < H; i += 16)
+#pragma unroll
+    for (int u = 0; u < 16; u += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src + i + u);
+      m = fmaxf(fmaxf(fmaxf(m, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(x.z))), fabsf(x.w));
+    }
+  s.q_max[group * kPrefixRows + row] = m;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&s.q_half[w]);
+  if (!warp_wait<D>(p, s, &s.q_half[w], uses & 1)) return false;
+  float by;
+  q_powers(fmaxf(m, s.q_max[(group ^ 1) * kPrefixRows + row]), by, scale);
+  scale *= p.qscale;
+#pragma unroll 1
+  for (int i = 0; i < H; i += 16) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float4 x = *reinterpret_cast<const float4*>(src + i + 4 * u);
+      split_half2(x.x * by, x.y * by, hi[2 * u], lo[2 * u]);
+      split_half2(x.z * by, x.w * by, hi[2 * u + 1], lo[2 * u + 1]);
+    }
+    const uint32_t to = lanes + PGeo<D>::Q0 + (group * H + i) / 2;
+    tmem_st8(to, hi);
+    tmem_st8(to + D / 2, lo);
+  }
+  tmem_wait_st();
+  tc5_fence_before();
+  __syncwarp();
+  // the barrier counts eight: every warp for many rows, these two for few
+  if (lane < (c.small() ? 4 : 1)) mbar_arrive(&s.q_full[c.k & 1]);
+  return true;
+}
+
+// Q in shared memory: n <= 32 rows into rows row0 .. of the buffer by one warp;
+// lane i names row i (`mine`, its place in [B, T, Hq]; lanes past the last name the last).
 // A lane takes 8 values, D / 8 lanes a row: 16-byte stores.  All rows are touched first, so
 // that the loop over them, kept small, finds them in L1.
 template <int D>
@@ -528,11 +658,9 @@ __device__ __forceinline__ void load_q_rows(const float* src, float qscale, Pref
     for (int u = 0; u < 8; ++u) m = fmaxf(m, fabsf(v[u]));
 #pragma unroll
     for (int o = LR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    // exponent of the largest value, clamped so that both powers are normal
-    int e = (int)(__float_as_uint(m) >> 23) - 127;
-    e = min(max(e, -100), 120);
-    const float f = __uint_as_float((uint32_t)(9 - e + 127) << 23);
-    if (d == 0) s.row_scale[row] = qscale * __uint_as_float((uint32_t)(e - 9 + 127) << 23);
+    float f, undo;
+    q_powers(m, f, undo);
+    if (d == 0) s.row_scale[row] = qscale * undo;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) split_half2(v[2 * u] * f, v[2 * u + 1] * f, hi[u], lo[u]);
@@ -552,7 +680,7 @@ __device__ __forceinline__ void load_q(const PrefixParams& p, PrefixSmem<D>& s,
   if (n <= 0) return;
   int seq, tok;
   const int mine = c.out_row(first + min((int)(threadIdx.x & 31), n - 1), seq, tok);
-  load_q_rows<D>(p.q, p.qscale, s, mine, c.q_row() + first, n);
+  load_q_rows<D>(p.q, p.qscale, s, mine, c.lane0() + first, n);
 }
 
 // Warp 3: Q of the parts with few rows, one part ahead of the products.  The
@@ -602,165 +730,254 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float* v) {
   for (int i = 0; i < N; i += 32) tmem_loaded32(v + i);
 }
 
+// What a softmax thread knows of its row in a part.
+struct Row {
+  bool any, on;       // the warp has rows, the thread has one
+  int lo, hi;         // keys it sees among the part's
+  int place;          // in [B, T, Hq]
+  float scale;        // of its scores, base 2
+  float m, l;         // running maximum, and the sum of the weights against it
+  bool partial;       // it met a tile some key of which was masked (for a row of its warp)
+};
+template <int D>
+__device__ __forceinline__ Row row_of(const PrefixParams& p, const PrefixSmem<D>& s,
+                                      const Cursor<D>& c, int w) {
+  Row r = {false, false, 0, 0, 0, 0.f, -kInf, 0.f, false};
+  const int first = c.lane0(), row = w * 32 + (int)(threadIdx.x & 31);
+  r.any = w * 32 + 32 > first && w * 32 < first + c.nr;
+  r.on = row >= first && row < first + c.nr;
+  if (r.on) {
+    int b, tok;
+    r.place = c.out_row(row - first, b, tok);
+    key_range(p, s.len[b], s.qp[b], tok, tok, r.lo, r.hi);
+    if (c.b < 0)
+      r.hi = min(r.hi, c.P);
+    else
+      r.lo = max(r.lo, c.P);
+  }
+  return r;
+}
+
+// Scores of tile x (number j of the part) to weights.  `chain`: the running
+// maximum comes from the tile before and goes on to the next (two groups take turns).
 template <int D, bool CAP>
-__device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s) {
+__device__ __forceinline__ bool softmax_tile(const PrefixParams& p, PrefixSmem<D>& s,
+                                             const Cursor<D>& c, Row& r, int j, int x, int w,
+                                             uint32_t lanes, int box_shift) {
   using G = PGeo<D>;
   constexpr int KT = G::KT;
   constexpr bool TWO = G::SOFTG == 2;
-  constexpr int W = CAP ? 16 : 32;
+  const int buf = x % G::NS, lane = threadIdx.x & 31, row = w * 32 + lane;
+  const uint32_t sa = lanes + G::S0 + buf * KT;
+  const float cc = CAP ? 1.f : r.scale;
+  float top = -kInf;
+  if (r.any) {
+    tc5_fence_after();
+    const int k0 = c.base + (c.i0 + j) * KT;
+    const int bad = s.bad[x & 15];
+    const bool masked =
+        !__all_sync(0xffffffffu, (!r.on || (r.lo <= k0 && r.hi >= k0 + KT)) && bad == 0);
+    r.partial |= masked;
+    const float to_y = r.scale * p.softcap_inv;
+    // Two passes over the scores, W or 32 columns a step: loops that stay in the
+    // instruction cache and need few registers.
+    constexpr int W = CAP ? 16 : 32;
+#pragma unroll 1
+    for (int i0 = 0; i0 < KT; i0 += W) {
+      float v[W];
+      if constexpr (CAP) {
+        tmem_load16(sa + i0, v);
+        float far = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          v[i] *= to_y;
+          far = fmaxf(far, fabsf(v[i]));
+        }
+        if (__any_sync(0xffffffffu, far > 0.5f)) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) v[i] = cap_any(v[i], p.softcap2);
+        } else {  // NaN stays NaN
+#pragma unroll
+          for (int i = 0; i < W; i += 2) {
+            const float2 y = cap_series(make_float2(v[i], v[i + 1]), p.softcap2);
+            v[i] = y.x;
+            v[i + 1] = y.y;
+          }
+        }
+      } else {
+        tmem_load<W>(sa + i0, v);
+      }
+      if (masked) {
+        // bit i: key k0 + i0 + i is seen
+        const int a = min(max(r.lo - k0 - i0, 0), 32), z = min(max(r.hi - k0 - i0, 0), 32);
+        uint32_t seen = (uint32_t)(0xffffffffull << a) & ~(uint32_t)(0xffffffffull << z);
+#pragma unroll
+        for (int i = 0; i < W; i += 8)
+          if ((bad >> ((i0 + i) >> box_shift)) & 1) seen &= ~(0xffu << i);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (!(seen >> i & 1)) v[i] = -kInf;
+      }
+      if (CAP || masked) {
+#pragma unroll
+        for (int i = 0; i < W; i += 16)
+          tmem_st16(sa + i0 + i, reinterpret_cast<const uint32_t*>(v + i));
+      }
+      top = fmaxf(top, largest<W>(v));
+    }
+    if (CAP || masked) tmem_wait_st();
+  }
+  float before = r.m;
+  if (TWO) {
+    if (x > 0 && !warp_wait<D>(p, s, &s.m_ready[w], (x - 1) & 1)) return false;
+    before = j > 0 ? s.m[row] : -kInf;
+  }
+  const float now = fmaxf(before, top * cc);
+  if (TWO) {
+    s.m[row] = now;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.m_ready[w]);
+  }
+  if (r.any) {
+    // no key so far: any finite reference does
+    const float ref = now == -kInf ? 0.f : now;
+    const float f = ex2_ftz(before - ref);  // for the sums up to the tile before
+    if constexpr (G::FAC_TMEM)
+      tmem_st1(lanes + G::F0 + buf, f);
+    else
+      s.fac[buf * kPrefixRows + row] = f;
+    const float base = ref - kShift;
+    const float2 cc2 = make_float2(cc, cc), base2 = make_float2(-base, -base);
+    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < KT; i0 += 32) {
+      float v[32];
+      uint32_t ph[16], pl[16];
+      tmem_load<32>(sa + i0, v);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        float2 e = fma2(make_float2(v[i], v[i + 1]), cc2, base2);
+        e.x = ex2_ftz(e.x);
+        e.y = ex2_ftz(e.y);
+        if (i & 2)
+          sum1 = add2(sum1, e);
+        else
+          sum0 = add2(sum0, e);
+        const __half2 hh = __floats2half2_rn(e.x, e.y);
+        const float2 hf = __half22float2(hh);
+        const float2 rest = add2(e, make_float2(-hf.x, -hf.y));
+        const __half2 hl = __floats2half2_rn(rest.x, rest.y);
+        ph[i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+        pl[i / 2] = *reinterpret_cast<const uint32_t*>(&hl);
+      }
+      // the weights of 32 keys take the columns of their scores: 16 of high terms, 16 of low
+      tmem_st16(sa + i0, ph);
+      tmem_st16(sa + i0 + 16, pl);
+    }
+    // l counts against `now`, so far against the maximum this thread saw last
+    r.l = fmaf(r.l, ex2_ftz(r.m - ref), (sum0.x + sum0.y) + (sum1.x + sum1.y));
+    tmem_wait_st();
+    tc5_fence_before();
+  }
+  r.m = now;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&s.p_full[buf]);
+  return true;
+}
+
+template <int D>
+__device__ __forceinline__ void store_ml(const PrefixParams& p, const Cursor<D>& c, const Row& r,
+                                         int w) {
+  if (!r.on) return;
+  float2* dst;
+  if (!c.whole())
+    dst = p.ws_cut_ml + (blockIdx.x * 2 + (c.k == 0 ? 0 : 1)) * kPrefixRows + w * 32 +
+          (int)(threadIdx.x & 31) - c.lane0();
+  else
+    dst = (c.b < 0 ? p.ws_pre_ml : p.ws_own_ml) + r.place;
+  *dst = make_float2(r.m - kShift, r.partial ? -r.l : r.l);
+}
+
+// One group, Q in shared memory (D = 256).
+template <int D, bool CAP>
+__device__ void softmax_loop_one(const PrefixParams& p, PrefixSmem<D>& s) {
+  using G = PGeo<D>;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
-  const int group = TWO ? (threadIdx.x >> 7) - 1 : 0;  // takes the tiles x = group mod 2
-  const int row = w * 32 + lane;
   const uint32_t lanes = s.tmem + ((uint32_t)(w * 32) << 16);
   const int box_shift = __ffs(p.box_rows) - 1;
-  int x0 = 0;                // tiles of the parts before
-  int shared_sums[2] = {0, 0};  // parts so far, by parity, whose sum took both groups
-  for (Cursor<D> c(p, s); c.step(); x0 += c.n) {
+  int x = 0;
+  for (Cursor<D> c(p, s); c.step();) {
     const int k = c.k;
     if (!c.small()) {
       // many rows: they take the whole buffer
       if (k >= 1 && !warp_wait<D>(p, s, &s.q_free[(k - 1) & 1], ((k - 1) >> 1) & 1)) return;
-      constexpr int ROWS = kPrefixRows / (4 * G::SOFTG);
-      const int first = (group * 4 + w) * ROWS;
-      load_q<D>(p, s, c, first, first + ROWS);
+      load_q<D>(p, s, c, w * 32, w * 32 + 32);
       if (lane == 0) mbar_arrive(&s.q_full[k & 1]);
     }
-    const bool any = w * 32 < c.nr;  // rows of this warp
-    const bool on = row < c.nr;
-    int lo = 0, hi = 0, orow = 0;
-    if (on) {
-      int b, tok;
-      orow = c.out_row(row, b, tok);
-      key_range(p, s.len[b], s.qp[b], tok, tok, lo, hi);
-      if (c.b < 0)
-        hi = min(hi, c.P);
-      else
-        lo = max(lo, c.P);
-    }
-    float scale = 0.f, m = -kInf, l = 0.f;
-    bool partial = false;
-    const int j0 = TWO ? (x0 ^ group) & 1 : 0;  // this group's first tile of the part
-    if (j0 >= c.n) {
-      // it has none; the part's Q is there once all have left part k - 2
-      if (!warp_wait<D>(p, s, &s.q_full[k & 1], (k >> 1) & 1)) return;
-      if (lane == 0) mbar_arrive(&s.q_free[k & 1]);
-    }
-    for (int j = j0; j < c.n; j += G::SOFTG) {
-      const int x = x0 + j, buf = x % G::NS;
-      if (!warp_wait<D>(p, s, &s.s_full[buf], (x / G::NS) & 1)) return;
-      if (j == j0) {
-        if (on) scale = s.row_scale[c.q_row() + row];
+    Row r = row_of<D>(p, s, c, w);
+    for (int j = 0; j < c.n; ++j, ++x) {
+      if (!warp_wait<D>(p, s, &s.s_full[x % G::NS], (x / G::NS) & 1)) return;
+      if (j == 0) {
+        if (r.on) r.scale = s.row_scale[w * 32 + lane];
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.q_free[k & 1]);
       }
-      const uint32_t sa = lanes + G::S0 + buf * KT;
-      const int k0 = c.base + (c.i0 + j) * KT;
-      const float cc = CAP ? 1.f : scale;
-      bool masked = false;
-      float top = -kInf;
-      if (any) {
-        tc5_fence_after();
-        const int bad = s.bad[x & 7];
-        masked = !__all_sync(0xffffffffu, (!on || (lo <= k0 && hi >= k0 + KT)) && bad == 0);
-        partial |= masked;
-        // Two passes over the scores, W or 32 columns a step: loops that stay in the
-        // instruction cache and need few registers.
-#pragma unroll 1
-        for (int i0 = 0; i0 < KT; i0 += W) {
-          float v[W];
-          if constexpr (CAP)
-            tmem_load16(sa + i0, v);
-          else
-            tmem_load<W>(sa + i0, v);
-          if (CAP) {
-#pragma unroll
-            for (int i = 0; i < W; ++i) v[i] = capped(v[i] * scale, p.softcap2, p.softcap_inv);
-          }
-          if (masked) {
-            // bit i: key k0 + i0 + i is seen
-            const int a = min(max(lo - k0 - i0, 0), 32), z = min(max(hi - k0 - i0, 0), 32);
-            uint32_t seen = (uint32_t)(0xffffffffull << a) & ~(uint32_t)(0xffffffffull << z);
-#pragma unroll
-            for (int i = 0; i < W; i += 8)
-              if ((bad >> ((i0 + i) >> box_shift)) & 1) seen &= ~(0xffu << i);
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-              if (!(seen >> i & 1)) v[i] = -kInf;
-          }
-          if (CAP || masked) {
-#pragma unroll
-            for (int i = 0; i < W; i += 16)
-              tmem_st16(sa + i0 + i, reinterpret_cast<const uint32_t*>(v + i));
-          }
-          top = fmaxf(top, largest<W>(v));
-        }
-        if (CAP || masked) tmem_wait_st();
-      }
-      // the maximum up to the tile before, from the other group; then this one's to it
-      float before = m;
-      if (TWO) {
-        if (x > 0 && !warp_wait<D>(p, s, &s.m_ready[w], (x - 1) & 1)) return;
-        before = j > 0 ? s.m[row] : -kInf;
-      }
-      const float now = fmaxf(before, top * cc);
-      if (TWO) {
-        s.m[row] = now;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.m_ready[w]);
-      }
-      if (any) {
-        // no key so far: any finite reference does
-        const float ref = now == -kInf ? 0.f : now;
-        const float f = ex2_ftz(before - ref);  // for the sums up to the tile before
-        if constexpr (G::FAC_TMEM)
-          tmem_st1(lanes + G::F0 + buf, f);
-        else
-          s.fac[buf * kPrefixRows + row] = f;
-        const float base = ref - kShift;
-        const float2 cc2 = make_float2(cc, cc), base2 = make_float2(-base, -base);
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll 1
-        for (int i0 = 0; i0 < KT; i0 += 32) {
-          float v[32];
-          uint32_t ph[16], pl[16];
-          tmem_load<32>(sa + i0, v);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float2 e = fma2(make_float2(v[i], v[i + 1]), cc2, base2);
-            e.x = ex2_ftz(e.x);
-            e.y = ex2_ftz(e.y);
-            if (i & 2)
-              sum1 = add2(sum1, e);
-            else
-              sum0 = add2(sum0, e);
-            const __half2 hh = __floats2half2_rn(e.x, e.y);
-            const float2 hf = __half22float2(hh);
-            const float2 r = add2(e, make_float2(-hf.x, -hf.y));
-            const __half2 hl = __floats2half2_rn(r.x, r.y);
-            ph[i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
-            pl[i / 2] = *reinterpret_cast<const uint32_t*>(&hl);
-          }
-          // the weights of 32 keys take the columns of their scores: 16 of high terms, 16 of low
-          tmem_st16(sa + i0, ph);
-          tmem_st16(sa + i0 + 16, pl);
-        }
-        // l counts against `now`, so far against this group's last maximum m
-        l = fmaf(l, ex2_ftz(m - ref), (sum0.x + sum0.y) + (sum1.x + sum1.y));
-        tmem_wait_st();
-        tc5_fence_before();
-      }
-      m = now;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.p_full[buf]);
+      if (!softmax_tile<D, CAP>(p, s, c, r, j, x, w, lanes, box_shift)) return;
     }
-    if (TWO && c.n > 1) {
+    store_ml<D>(p, c, r, w);
+  }
+}
+
+// Two groups that take turns at the tiles, Q in tensor memory.
+template <int D, bool CAP>
+__device__ void softmax_loop_two(const PrefixParams& p, PrefixSmem<D>& s) {
+  using G = PGeo<D>;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+  const int group = (threadIdx.x >> 7) - 1;  // takes the tiles x = group mod 2
+  const int row = w * 32 + lane;
+  const uint32_t lanes = s.tmem + ((uint32_t)(w * 32) << 16);
+  const int box_shift = __ffs(p.box_rows) - 1;
+  int x0 = 0;                   // tiles of the parts before
+  int shared_sums[2] = {0, 0};  // parts so far, by parity, whose sum took both groups
+  int loads = 0;                // of Q by this warp
+  float next_scale = 0.f;
+  Cursor<D> c(p, s), next(p, s);
+  bool more = next.step();
+  // Whether this warp loads the next part's Q: rows of it lie in its lanes, or all warps do.
+  auto mine = [&] { return !next.small() || w == next.lane0() / 32; };
+  if (more && mine() && !load_q_lanes<D>(p, s, next, group, w, lanes, loads++, next_scale)) return;
+  while (more) {
+    c.step();
+    more = next.step();
+    const int k = c.k;
+    Row r = row_of<D>(p, s, c, w);
+    r.scale = next_scale;
+    // The next part's Q goes into lanes that this part does not use while this part is worked on:
+    // the products of the parts before are done with them.
+    const bool early = more && c.small() && next.small();
+    bool load = more && mine();
+    for (int pass = 0; pass < 2; ++pass) {
+      if (load && early == (pass == 0)) {
+        const int last = pass == 0 ? k - 1 : k;
+        if (last >= 0 && !warp_wait<D>(p, s, &s.q_free[last & 1], (last >> 1) & 1)) return;
+        if (!load_q_lanes<D>(p, s, next, group, w, lanes, loads++, next_scale)) return;
+      }
+      if (pass == 1) break;
+      for (int j = (x0 ^ group) & 1; j < c.n; j += 2) {
+        const int x = x0 + j;
+        if (!warp_wait<D>(p, s, &s.s_full[x % G::NS], (x / G::NS) & 1)) return;
+        if (!softmax_tile<D, CAP>(p, s, c, r, j, x, w, lanes, box_shift)) return;
+      }
+    }
+    const int last = x0 + c.n - 1;
+    x0 += c.n;
+    if (c.n > 1) {
       // the group of the part's last tile adds the other's sum to its own
       const int q = k & 1;
       float* slot = s.l + q * kPrefixRows + row;
-      if (((x0 + c.n - 1) & 1) != group) {
-        *slot = partial ? -l : l;
-        // its reference: the maximum it saw last, which s.m may have passed
-        s.m_last[q * kPrefixRows + row] = m;
+      if ((last & 1) != group) {
+        *slot = r.partial ? -r.l : r.l;
+        s.m_last[q * kPrefixRows + row] = r.m;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.l_ready[q][w]);
         ++shared_sums[q];
@@ -769,21 +986,12 @@ __device__ void softmax_loop(const PrefixParams& p, PrefixSmem<D>& s) {
       if (!warp_wait<D>(p, s, &s.l_ready[q][w], shared_sums[q] & 1)) return;
       ++shared_sums[q];
       const float lx = *slot, mx = s.m_last[q * kPrefixRows + row];
-      partial |= signbit(lx) != 0;
-      l = fmaf(fabsf(lx), ex2_ftz(mx - (m == -kInf ? 0.f : m)), l);
-    } else if (TWO && j0 != 0) {
+      r.partial |= signbit(lx) != 0;
+      r.l = fmaf(fabsf(lx), ex2_ftz(mx - (r.m == -kInf ? 0.f : r.m)), r.l);
+    } else if ((last & 1) != group) {
       continue;  // the one tile was the other group's
     }
-    if (on) {
-      float2* dst;
-      if (!c.whole())
-        dst = p.ws_cut_ml + (blockIdx.x * 2 + (k == 0 ? 0 : 1)) * kPrefixRows + row;
-      else if (c.b < 0)
-        dst = p.ws_pre_ml + orow;
-      else
-        dst = p.ws_own_ml + orow;
-      *dst = make_float2(m - kShift, partial ? -l : l);
-    }
+    store_ml<D>(p, c, r, w);
   }
 }
 
@@ -797,7 +1005,9 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   const uint32_t lanes = s.tmem + ((uint32_t)(w * 32) << 16);
   int x = 0;
   for (Cursor<D> c(p, s); c.step();) {
-    const bool any = w * 32 < c.nr, on = row < c.nr;
+    const int first = c.lane0();
+    const bool any = w * 32 + 32 > first && w * 32 < first + c.nr;
+    const bool on = row >= first && row < first + c.nr;
     float2 acc[C / 2];
 #pragma unroll
     for (int i = 0; i < C / 2; ++i) acc[i] = make_float2(0.f, 0.f);
@@ -834,10 +1044,11 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
     if (on) {
       float* dst;
       if (!c.whole()) {
-        dst = p.ws_cut_o + ((long long)(blockIdx.x * 2 + (c.k == 0 ? 0 : 1)) * kPrefixRows + row) * D;
+        dst = p.ws_cut_o +
+              ((long long)(blockIdx.x * 2 + (c.k == 0 ? 0 : 1)) * kPrefixRows + row - first) * D;
       } else {
         int b, tok;
-        dst = (c.b < 0 ? p.ws_pre_o : p.out) + (long long)c.out_row(row, b, tok) * D;
+        dst = (c.b < 0 ? p.ws_pre_o : p.out) + (long long)c.out_row(row - first, b, tok) * D;
       }
 #pragma unroll
       for (int i = 0; i < C; i += 4)
@@ -850,44 +1061,46 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
 // ------------------------------------------------------------------ MMA threads
 // One thread issues the scores' products and another the values', so that
 // one's waits do not hold up the other's.  The low terms go first: their
-// steps truncate at their own size.  Place of a tile's K and V in the ring's order:
-// K(0) K(1) V(0) K(2) V(1) ... K(n - 1) V(n - 2) V(n - 1).
-__device__ __forceinline__ int k_place(int x) { return x < 2 ? x : 2 * x - 1; }
-__device__ __forceinline__ int v_place(int x, int tiles) {
-  return x < tiles - 1 ? 2 * x + 2 : 2 * x + 1;
-}
-
+// steps truncate at their own size.
 template <int D>
 __device__ void qk_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   using G = PGeo<D>;
   constexpr int KT = G::KT;
   constexpr uint32_t idesc = f16_idesc(KT, false);
-  const uint32_t tm = s.tmem + G::S0;
-  const uint64_t q0 = smem_desc(smem_u32(s.q), 16, 1024);
+  const uint32_t tm = s.tmem;
+  const uint64_t q0 = smem_desc(smem_u32(s.q), 16, 1024);  // all 128 rows, whoever's they are
   const uint64_t k0 = smem_desc(smem_u32(s.ring), 16, 1024);
   int x = 0;
   for (Cursor<D> c(p, s); c.step();) {
     if (!wait_or_abort<D>(p, s, &s.q_full[c.k & 1], (c.k >> 1) & 1)) return;
-    const uint64_t q = q0 + c.q_row() * 8;  // 128 bytes a row
     for (int j = 0; j < c.n; ++j, ++x) {
-      const int place = k_place(x), slot = place % G::RING, buf = x % G::NS;
-      if (!wait_or_abort<D>(p, s, &s.full[slot], (place / G::RING) & 1)) return;
-      // the buffer's last tile is summed up: its weights and its factor are read
+      const Place<D> at = Place<D>::k(x);
+      const int buf = x % G::NS;
+      // the buffer's last tile is summed up: its weights and its factor are read.  Before the wait
+      // for K: in a shared ring of three the slot held that tile's V, and only then has its phase
+      // passed that the next one's parity is told from
       if (x >= G::NS && !wait_or_abort<D>(p, s, &s.o_free[buf], (x / G::NS - 1) & 1)) return;
+      if (!wait_or_abort<D>(p, s, &s.full[at.slot], at.use & 1)) return;
       tc5_fence_after();
-      const uint64_t k = k0 + slot * (G::TILE / 16);
+      const uint64_t k = k0 + at.slot * (G::TILE / 16);
+      const uint32_t d = tm + G::S0 + buf * KT;
       // a loop over 128-byte slices: unrolled further, its descriptors would spill
 #pragma unroll 1
       for (int i = 0; i < 2 * G::SL; ++i) {
         const int term = i < G::SL ? 1 : 0, slice = i < G::SL ? i : i - G::SL;
-        const uint64_t qd = q + (term * G::QTERM + slice * (kPrefixRows * 128)) / 16;
         const uint64_t kd = k + slice * (KT * 128 / 16);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)  // 16 values: 32 bytes
-          mma_ss(tm + buf * KT, qd + u * 2, kd + u * 2, idesc, i + u > 0);
+        for (int u = 0; u < 4; ++u) {  // 16 values: 32 bytes, 8 columns
+          if constexpr (G::QT)
+            mma_ts(d, tm + G::Q0 + term * (D / 2) + slice * 32 + u * 8, kd + u * 2, idesc,
+                   i + u > 0);
+          else
+            mma_ss(d, q0 + (term * G::QTERM + slice * (kPrefixRows * 128)) / 16 + u * 2, kd + u * 2,
+                   idesc, i + u > 0);
+        }
       }
       mma_commit(&s.s_full[buf]);
-      mma_commit(&s.empty[slot]);
+      mma_commit(&s.empty[at.slot]);
     }
     mma_commit(&s.q_free[c.k & 1]);
   }
@@ -900,25 +1113,29 @@ __device__ void pv_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   constexpr uint32_t idesc = f16_idesc(D, true);
   const uint32_t tm = s.tmem;
   const uint64_t v0 = smem_desc(smem_u32(s.ring), KT * 128, 1024);
-  const int tiles = s.run;
-  for (int x = 0; x < tiles; ++x) {
-    const int place = v_place(x, tiles), slot = place % G::RING, buf = x % G::NS;
-    if (!wait_or_abort<D>(p, s, &s.full[slot], (place / G::RING) & 1)) return;
-    if (x > 0 && !wait_or_abort<D>(p, s, &s.o_free[(x - 1) % G::NS], ((x - 1) / G::NS) & 1)) return;
-    if (!wait_or_abort<D>(p, s, &s.p_full[buf], (x / G::NS) & 1)) return;
-    tc5_fence_after();
-    const uint64_t v = v0 + slot * (G::TILE / 16);
+  int x = 0;
+  for (Cursor<D> c(p, s); c.step();)
+    for (int j = 0; j < c.n; ++j, ++x) {
+      const Place<D> at = Place<D>::v(x);
+      const int buf = x % G::NS;
+      if (!wait_or_abort<D>(p, s, &s.p_full[buf], (x / G::NS) & 1)) return;
+      if (x > 0 && !wait_or_abort<D>(p, s, &s.o_free[(x - 1) % G::NS], ((x - 1) / G::NS) & 1))
+        return;
+      // last: in a shared ring of three the slot held this tile's K
+      if (!wait_or_abort<D>(p, s, &s.full[at.slot], at.use & 1)) return;
+      tc5_fence_after();
+      const uint64_t v = v0 + at.slot * (G::TILE / 16);
 #pragma unroll 1
-    for (int i = 0; i < 2 * KT; i += 32) {
-      const int term = i < KT ? 1 : 0, k = i < KT ? i : i - KT;
+      for (int i = 0; i < 2 * KT; i += 32) {
+        const int term = i < KT ? 1 : 0, k = i < KT ? i : i - KT;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-        mma_ts(tm, tm + G::S0 + buf * KT + k + term * 16 + u * 8, v + (k + u * 16) * 8, idesc,
-               i + u > 0);
+        for (int u = 0; u < 2; ++u)
+          mma_ts(tm, tm + G::S0 + buf * KT + k + term * 16 + u * 8, v + (k + u * 16) * 8, idesc,
+                 i + u > 0);
+      }
+      mma_commit(&s.pv_done[buf]);
+      mma_commit(&s.empty[at.slot]);
     }
-    mma_commit(&s.pv_done[buf]);
-    mma_commit(&s.empty[slot]);
-  }
 }
 
 template <int D, bool CAP>
@@ -940,14 +1157,17 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
       mbar_init(&s.o_free[i], 4 * G::SUMG);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.q_full[i], 1 + 4 * G::SOFTG);
-      mbar_init(&s.q_free[i], 1 + 4 * G::SOFTG);  // the products, and the readers of row_scale
+      // Q in tensor memory: eight warps load it, the products use it; else one group's four
+      // warps and warp 3 load it, the products use it and the group reads its row_scale
+      mbar_init(&s.q_full[i], G::QT ? 8 : 5);
+      mbar_init(&s.q_free[i], G::QT ? 1 : 5);
       mbar_init(&s.drain[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s.m_ready[i], 1);
       mbar_init(&s.l_ready[0][i], 1);
       mbar_init(&s.l_ready[1][i], 1);
+      mbar_init(&s.q_half[i], 2);
     }
     fence_mbarrier_init();
     s.lo = 0x7fffffff;
@@ -964,7 +1184,8 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
   const int flags = make_plan<D>(p, s);
   if (blockIdx.x == 0 && flags && p.dev_status) atomicOr(p.dev_status, flags);
   if (tid == 0) {
-    const int pn = s.hi > s.lo ? (s.hi + G::KT - 1) / G::KT - s.lo / G::KT : 0;
+    const int pn =
+        s.hi > s.lo ? (s.hi + G::KT - 1) / G::KT - s.lo / G::KT + kPrefixExtra : 0;
     const int tp = pn * (p.Hkv * p.row_tiles);
     const Split sp(tp + s.cum[p.B] * (p.Hkv * p.own_tiles), p.grid);
     s.run = sp.share + ((int)blockIdx.x < sp.rem);
@@ -976,16 +1197,12 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
   __syncthreads();
   if (warp < 4) {
     setmaxnreg_dec<G::REG_LOAD>();
-    if (warp == 0) {
+    if (warp == 0 || (warp == 3 && G::QT)) {
       Loader<D> ld(p, s);
-      ld.run();
+      ld.run(warp == 3);
       const int bad = __reduce_or_sync(0xffffffffu, ld.flags);
       if (bad && lane == 0 && p.dev_status) atomicOr(p.dev_status, bad);
-      if (*(volatile int*)&s.abort) {
-        // the copies in flight end before their memory is given back
-        for (int r = max(0, ld.r - G::RING); r < ld.r; ++r)
-          mbar_wait(&s.full[r % G::RING], (r / G::RING) & 1, nullptr, p.wait_ns);
-      }
+      if (*(volatile int*)&s.abort) ld.drain();
     } else if (warp < 3) {
       if (lane == 0) {
         if (warp == 1)
@@ -993,20 +1210,23 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
         else
           pv_loop<D>(p, s);
         if (*(volatile int*)&s.abort) {
-          // so do the products
+          // the products in flight end before their memory is given back
           mma_commit(&s.drain[warp - 1]);
           mbar_wait(&s.drain[warp - 1], 0, nullptr, p.wait_ns);
         }
       }
     } else {
-      q_loop<D>(p, s);
+      if constexpr (!G::QT) q_loop<D>(p, s);
     }
   } else if (warp < 4 + 4 * G::SOFTG) {
     if constexpr (G::REG_SOFT > G::REG_LAUNCH)
       setmaxnreg_inc<G::REG_SOFT>();
     else
       setmaxnreg_dec<G::REG_SOFT>();
-    softmax_loop<D, CAP>(p, s);
+    if constexpr (G::QT)
+      softmax_loop_two<D, CAP>(p, s);
+    else
+      softmax_loop_one<D, CAP>(p, s);
   } else {
     setmaxnreg_inc<G::REG_SUM>();
     sum_loop<D>(p, s);
@@ -1055,7 +1275,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int n0 = pn, n1 = cum[b + 1] - cum[b];
   const int g0 = (h * p.row_tiles + rb / kPrefixRows) * n0;
   const int g1 = tp + cum[b] * units1 + (h * p.own_tiles + r1 / kPrefixRows) * n1;
-  const int c0 = n0 ? sp.cta(g0) : 0, c1 = n1 ? sp.cta(g1) : 0;
+  const int c0 = n0 ? sp.cta(g0 + kPrefixExtra) : 0, c1 = n1 ? sp.cta(g1 + kOwnExtra) : 0;
   const int s0 = n0 ? sp.cta(g0 + n0 - 1) - c0 + 1 : 0;  // its states
   const int s1 = n1 ? sp.cta(g1 + n1 - 1) - c1 + 1 : 0;
   float M = -kInf, L = 0.f, o[V];
@@ -1075,7 +1295,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         src = (own ? p.out : p.ws_pre_o) + (long long)row * D;
       } else {
         const int c = first + jj;
-        const int slot = 2 * c + (jj == 0 && sp.start(c) != (own ? g1 : g0) ? 1 : 0);
+        const int slot = 2 * c + (jj == 0 && sp.start(c) < (own ? g1 : g0) ? 1 : 0);
         const long long at = (long long)slot * kPrefixRows + (own ? r1 : rb) % kPrefixRows;
         ml = p.ws_cut_ml + at;
         src = p.ws_cut_o + at * D;

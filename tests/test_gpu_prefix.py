@@ -493,7 +493,8 @@ def test_a_wait_that_runs_out_is_reported(D):
     """CTA 0's first copy left out: its consumers' waits run out after 50 ms,
     the kernel ends with DEV_TIMEOUT, and the next call is right again."""
     lib = qk.load_library()
-    c = Case(23, 4, 8, 2, D, 16, 2048, [2100, 2049, 2300, 2060])
+    # long enough for CTA 0 to hold tiles beside the entries of the list that stand for a unit's cost
+    c = Case(23, 2, 8, 8, D, 64, 16384, [16385, 16450])
     with qk.tuning(wait_limit_ms=50):
         lib.decode_attn_testing_skip_first_arm(1)
         try:
