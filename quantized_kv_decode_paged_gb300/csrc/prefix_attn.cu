@@ -1058,51 +1058,58 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   }
 }
 
-// ------------------------------------------------------------------ MMA threads
-// One thread issues the scores' products and another the values', so that
-// one's waits do not hold up the other's.  The low terms go first: their
+// ------------------------------------------------------------------ MMA warps
+// One warp issues the scores' products and another the values', so that
+// one's waits do not hold up the other's.  All lanes walk the tiles, with values the compiler can
+// see to be the same in all of them, and one issues: the operands then live in uniform
+// registers (moved there one by one by a single lane, an MMA took 100 cycles
+// to issue, three times what a 128 x 64 x 16 one takes to run).  The low terms go first: their
 // steps truncate at their own size.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 template <int D>
 __device__ void qk_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   using G = PGeo<D>;
   constexpr int KT = G::KT;
   constexpr uint32_t idesc = f16_idesc(KT, false);
-  const uint32_t tm = s.tmem;
-  const uint64_t q0 = smem_desc(smem_u32(s.q), 16, 1024);  // all 128 rows, whoever's they are
+  const uint32_t tm = uniform(s.tmem);
+  const uint64_t q = smem_desc(smem_u32(s.q), 16, 1024);  // all 128 rows, whoever's they are
   const uint64_t k0 = smem_desc(smem_u32(s.ring), 16, 1024);
   int x = 0;
   for (Cursor<D> c(p, s); c.step();) {
-    if (!wait_or_abort<D>(p, s, &s.q_full[c.k & 1], (c.k >> 1) & 1)) return;
-    for (int j = 0; j < c.n; ++j, ++x) {
+    const int n = uniform(c.n), part = uniform(c.k);
+    if (!warp_wait<D>(p, s, &s.q_full[part & 1], (part >> 1) & 1)) return;
+    for (int j = 0; j < n; ++j, ++x) {
       const Place<D> at = Place<D>::k(x);
       const int buf = x % G::NS;
       // the buffer's last tile is summed up: its weights and its factor are read.  Before the wait
       // for K: in a shared ring of three the slot held that tile's V, and only then has its phase
       // passed that the next one's parity is told from
-      if (x >= G::NS && !wait_or_abort<D>(p, s, &s.o_free[buf], (x / G::NS - 1) & 1)) return;
-      if (!wait_or_abort<D>(p, s, &s.full[at.slot], at.use & 1)) return;
+      if (x >= G::NS && !warp_wait<D>(p, s, &s.o_free[buf], (x / G::NS - 1) & 1)) return;
+      if (!warp_wait<D>(p, s, &s.full[at.slot], at.use & 1)) return;
       tc5_fence_after();
       const uint64_t k = k0 + at.slot * (G::TILE / 16);
       const uint32_t d = tm + G::S0 + buf * KT;
-      // a loop over 128-byte slices: unrolled further, its descriptors would spill
-#pragma unroll 1
-      for (int i = 0; i < 2 * G::SL; ++i) {
-        const int term = i < G::SL ? 1 : 0, slice = i < G::SL ? i : i - G::SL;
-        const uint64_t kd = k + slice * (KT * 128 / 16);
+      if (elect_one()) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {  // 16 values: 32 bytes, 8 columns
-          if constexpr (G::QT)
-            mma_ts(d, tm + G::Q0 + term * (D / 2) + slice * 32 + u * 8, kd + u * 2, idesc,
-                   i + u > 0);
-          else
-            mma_ss(d, q0 + (term * G::QTERM + slice * (kPrefixRows * 128)) / 16 + u * 2, kd + u * 2,
-                   idesc, i + u > 0);
+        for (int i = 0; i < 2 * G::SL; ++i) {
+          const int term = i < G::SL ? 1 : 0, slice = i < G::SL ? i : i - G::SL;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {  // 16 values: 32 bytes, 8 columns
+            const uint64_t kd = k + slice * (KT * 128 / 16) + u * 2;
+            if constexpr (G::QT)
+              mma_ts(d, tm + G::Q0 + term * (D / 2) + slice * 32 + u * 8, kd, idesc, i + u > 0);
+            else
+              mma_ss(d, q + (term * G::QTERM + slice * (kPrefixRows * 128)) / 16 + u * 2, kd, idesc,
+                     i + u > 0);
+          }
         }
+        mma_commit(&s.s_full[buf]);
+        mma_commit(&s.empty[at.slot]);
+        if (j == n - 1) mma_commit(&s.q_free[part & 1]);
       }
-      mma_commit(&s.s_full[buf]);
-      mma_commit(&s.empty[at.slot]);
+      __syncwarp();
     }
-    mma_commit(&s.q_free[c.k & 1]);
   }
 }
 
@@ -1111,31 +1118,34 @@ __device__ void pv_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   using G = PGeo<D>;
   constexpr int KT = G::KT;
   constexpr uint32_t idesc = f16_idesc(D, true);
-  const uint32_t tm = s.tmem;
+  const uint32_t tm = uniform(s.tmem);
   const uint64_t v0 = smem_desc(smem_u32(s.ring), KT * 128, 1024);
   int x = 0;
-  for (Cursor<D> c(p, s); c.step();)
-    for (int j = 0; j < c.n; ++j, ++x) {
+  for (Cursor<D> c(p, s); c.step();) {
+    const int n = uniform(c.n);
+    for (int j = 0; j < n; ++j, ++x) {
       const Place<D> at = Place<D>::v(x);
       const int buf = x % G::NS;
-      if (!wait_or_abort<D>(p, s, &s.p_full[buf], (x / G::NS) & 1)) return;
-      if (x > 0 && !wait_or_abort<D>(p, s, &s.o_free[(x - 1) % G::NS], ((x - 1) / G::NS) & 1))
-        return;
+      if (!warp_wait<D>(p, s, &s.p_full[buf], (x / G::NS) & 1)) return;
+      if (x > 0 && !warp_wait<D>(p, s, &s.o_free[(x - 1) % G::NS], ((x - 1) / G::NS) & 1)) return;
       // last: in a shared ring of three the slot held this tile's K
-      if (!wait_or_abort<D>(p, s, &s.full[at.slot], at.use & 1)) return;
+      if (!warp_wait<D>(p, s, &s.full[at.slot], at.use & 1)) return;
       tc5_fence_after();
       const uint64_t v = v0 + at.slot * (G::TILE / 16);
-#pragma unroll 1
-      for (int i = 0; i < 2 * KT; i += 32) {
-        const int term = i < KT ? 1 : 0, k = i < KT ? i : i - KT;
+      const uint32_t a = tm + G::S0 + buf * KT;
+      if (elect_one()) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          mma_ts(tm, tm + G::S0 + buf * KT + k + term * 16 + u * 8, v + (k + u * 16) * 8, idesc,
-                 i + u > 0);
+        for (int term = 1; term >= 0; --term)
+#pragma unroll
+          for (int k = 0; k < KT; k += 16)
+            mma_ts(tm, a + k / 32 * 32 + term * 16 + k % 32 / 2, v + k * 8, idesc,
+                   term == 0 || k > 0);
+        mma_commit(&s.pv_done[buf]);
+        mma_commit(&s.empty[at.slot]);
       }
-      mma_commit(&s.pv_done[buf]);
-      mma_commit(&s.empty[at.slot]);
+      __syncwarp();
     }
+  }
 }
 
 template <int D, bool CAP>
@@ -1204,16 +1214,14 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
       if (bad && lane == 0 && p.dev_status) atomicOr(p.dev_status, bad);
       if (*(volatile int*)&s.abort) ld.drain();
     } else if (warp < 3) {
-      if (lane == 0) {
-        if (warp == 1)
-          qk_loop<D>(p, s);
-        else
-          pv_loop<D>(p, s);
-        if (*(volatile int*)&s.abort) {
-          // the products in flight end before their memory is given back
-          mma_commit(&s.drain[warp - 1]);
-          mbar_wait(&s.drain[warp - 1], 0, nullptr, p.wait_ns);
-        }
+      if (warp == 1)
+        qk_loop<D>(p, s);
+      else
+        pv_loop<D>(p, s);
+      if (lane == 0 && *(volatile int*)&s.abort) {
+        // the products in flight end before their memory is given back
+        mma_commit(&s.drain[warp - 1]);
+        mbar_wait(&s.drain[warp - 1], 0, nullptr, p.wait_ns);
       }
     } else {
       if constexpr (!G::QT) q_loop<D>(p, s);

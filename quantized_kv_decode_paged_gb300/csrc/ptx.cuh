@@ -185,6 +185,14 @@ __device__ __forceinline__ void wait_for_grid_before() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(one));
+  return one != 0;
+}
+
 // Named barrier over a subset of warps.
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
