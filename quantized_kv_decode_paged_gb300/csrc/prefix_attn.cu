@@ -168,7 +168,7 @@ struct PGeo {
   static constexpr int SL = D / 64;               // 128-byte slices of a row
   static constexpr int TILE = KT * D * 2;         // bytes of a K or V tile
   static constexpr int QTERM = kPrefixRows * D * 2;  // bytes of one term of Q
-  static constexpr int NS = 3;                    // S / P buffers
+  static constexpr int NS = D == 128 ? 4 : 3;     // S / P buffers
   // Tensor-memory columns: O, then (D < 256) the two terms of Q, then S / P, then, if any are
   // left, the factors.  With Q there the score products read only K from shared memory (with both
   // operands in it they ran at two thirds of their rate), and 64 KB more of it hold tiles in
@@ -204,9 +204,13 @@ constexpr int kSmallRows = PGeo<D>::QT ? 32 : 64;
 // Units cost more than their tiles: Q, the first tile's latencies, the state's store.  The list
 // counts so many tiles for it (fitted to 1 to 16 tiles a unit, 8 to 128 rows).
 constexpr int kPrefixExtra = 4, kOwnExtra = 1;
-// Weights are kept times 2^10: those down to 2^-24 of a row's largest stay normal f16
-// numbers, and the largest is far from f16's limit.
-constexpr float kShift = 10.f;
+// The maximum that a tile's weights are taken against moves at the first tile of a group of
+// kGroup, whose products add up in tensor memory before the sum warps take them, and where a row
+// outgrows it by 2^kGrow (that tile then starts a group).  Weights are kept times 2^kShift:
+// those down to 2^-22 of the largest stay normal f16 numbers, and none passes 2^15.
+constexpr int kGroup = 2;
+constexpr float kGrow = 7.f;
+constexpr float kShift = 8.f;
 
 template <int D>
 struct PrefixSmem {
@@ -215,7 +219,7 @@ struct PrefixSmem {
   uint8_t ring[G::RING * G::TILE];
   uint8_t q[G::QT ? 16 : 2 * G::QTERM];
   uint64_t full[G::RING], empty[G::RING];
-  uint64_t s_full[G::NS], p_full[G::NS], pv_done[G::NS], o_free[G::NS];
+  uint64_t s_full[G::NS], p_full[G::NS], pv_done[G::NS], b_free[G::NS], o_free;
   uint64_t q_full[2], q_free[2], drain[2];
   uint64_t m_ready[4], l_ready[2][4], q_half[4];         // by warp of a warpgroup
   float row_scale[G::QT ? 1 : kPrefixRows];              // qscale * 2^e, by row of the Q buffer
@@ -227,6 +231,7 @@ struct PrefixSmem {
   int cum[MAXB + 1];                                     // the list's tiles a unit before sequence b
   int len[MAXB], qp[MAXB];                               // seq_info
   int bad[16];                                           // per tile (mod 16): masked boxes of keys
+  uint8_t grew[G::NS][4];                                // by tile's buffer and warp: a row outgrew
   int warp_sum[16];
   int lo, hi;                                            // prefix keys some row sees
   int first[4];                                          // where the CTA's run starts: b, h, rt, tile
@@ -832,7 +837,10 @@ __device__ __forceinline__ bool softmax_tile(const PrefixParams& p, PrefixSmem<D
     if (x > 0 && !warp_wait<D>(p, s, &s.m_ready[w], (x - 1) & 1)) return false;
     before = j > 0 ? s.m[row] : -kInf;
   }
-  const float now = fmaxf(before, top * cc);
+  const float most = fmaxf(before, top * cc);
+  const bool grew = __any_sync(0xffffffffu, r.on && most > before + kGrow);
+  const float now = grew || j % kGroup == 0 ? most : before;
+  if (lane == 0) s.grew[buf][w] = grew;
   if (TWO) {
     s.m[row] = now;
     __syncwarp();
@@ -1011,35 +1019,49 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
     float2 acc[C / 2];
 #pragma unroll
     for (int i = 0; i < C / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-    for (int j = 0; j < c.n; ++j, ++x) {
-      const int buf = x % G::NS;
-      const uint32_t parity = (x / G::NS) & 1;
-      if (!warp_wait<D>(p, s, &s.p_full[buf], parity)) return;
+    float fac = 0.f;  // the group's
+    for (int j = 0; j <= c.n; ++j) {
+      bool start = true;  // of a group, or the part's end
       float f = 0.f;
-      if (any) {
-        if constexpr (G::FAC_TMEM) {
+      if (j < c.n) {
+        const int buf = x % G::NS;
+        if (!warp_wait<D>(p, s, &s.p_full[buf], (x / G::NS) & 1)) return;
+        start = j % kGroup == 0 || *reinterpret_cast<const uint32_t*>(s.grew[buf]) != 0;
+        if (any) {
+          if constexpr (G::FAC_TMEM) {
+            tc5_fence_after();
+            f = tmem_ld1(lanes + G::F0 + buf);
+            tc5_fence_before();
+          } else {
+            f = s.fac[buf * kPrefixRows + row];
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.b_free[buf]);
+        ++x;
+      }
+      if (!start) continue;
+      if (j > 0) {
+        // the group before: its last tile is number y
+        const int y = j < c.n ? x - 2 : x - 1;
+        if (!warp_wait<D>(p, s, &s.pv_done[y % G::NS], (y / G::NS) & 1)) return;
+        if (any) {
           tc5_fence_after();
-          f = tmem_ld1(lanes + G::F0 + buf);
-        } else {
-          f = s.fac[buf * kPrefixRows + row];
-        }
-      }
-      if (!warp_wait<D>(p, s, &s.pv_done[buf], parity)) return;
-      if (any) {
-        tc5_fence_after();
-        const float2 f2 = make_float2(f, f);
+          const float2 f2 = make_float2(fac, fac);
 #pragma unroll
-        for (int i = 0; i < C; i += 16) {
-          float o[16];
-          tmem_load16(lanes + col + i, o);
+          for (int i = 0; i < C; i += 16) {
+            float o[16];
+            tmem_load16(lanes + col + i, o);
 #pragma unroll
-          for (int u = 0; u < 16; u += 2)
-            acc[(i + u) / 2] = fma2(acc[(i + u) / 2], f2, make_float2(o[u], o[u + 1]));
+            for (int u = 0; u < 16; u += 2)
+              acc[(i + u) / 2] = fma2(acc[(i + u) / 2], f2, make_float2(o[u], o[u + 1]));
+          }
+          tc5_fence_before();
         }
-        tc5_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.o_free);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.o_free[buf]);
+      fac = f;
     }
     if (on) {
       float* dst;
@@ -1082,16 +1104,16 @@ __device__ void qk_loop(const PrefixParams& p, PrefixSmem<D>& s) {
     for (int j = 0; j < n; ++j, ++x) {
       const Place<D> at = Place<D>::k(x);
       const int buf = x % G::NS;
-      // the buffer's last tile is summed up: its weights and its factor are read.  Before the wait
+      // the buffer's last tile: its products are done and its factor is read.  Before the wait
       // for K: in a shared ring of three the slot held that tile's V, and only then has its phase
       // passed that the next one's parity is told from
-      if (x >= G::NS && !warp_wait<D>(p, s, &s.o_free[buf], (x / G::NS - 1) & 1)) return;
+      if (x >= G::NS && !warp_wait<D>(p, s, &s.b_free[buf], (x / G::NS - 1) & 1)) return;
       if (!warp_wait<D>(p, s, &s.full[at.slot], at.use & 1)) return;
       tc5_fence_after();
       const uint64_t k = k0 + at.slot * (G::TILE / 16);
       const uint32_t d = tm + G::S0 + buf * KT;
       if (elect_one()) {
-#pragma unroll
+#pragma unroll G::QT ? 2 * G::SL : 1  // D = 256: its descriptors would spill
         for (int i = 0; i < 2 * G::SL; ++i) {
           const int term = i < G::SL ? 1 : 0, slice = i < G::SL ? i : i - G::SL;
 #pragma unroll
@@ -1120,14 +1142,17 @@ __device__ void pv_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   constexpr uint32_t idesc = f16_idesc(D, true);
   const uint32_t tm = uniform(s.tmem);
   const uint64_t v0 = smem_desc(smem_u32(s.ring), KT * 128, 1024);
-  int x = 0;
+  int x = 0, groups = 0;
   for (Cursor<D> c(p, s); c.step();) {
     const int n = uniform(c.n);
     for (int j = 0; j < n; ++j, ++x) {
       const Place<D> at = Place<D>::v(x);
       const int buf = x % G::NS;
       if (!warp_wait<D>(p, s, &s.p_full[buf], (x / G::NS) & 1)) return;
-      if (x > 0 && !warp_wait<D>(p, s, &s.o_free[(x - 1) % G::NS], ((x - 1) / G::NS) & 1)) return;
+      const bool start =
+          j % kGroup == 0 || uniform(*reinterpret_cast<const int*>(s.grew[buf])) != 0;
+      if (start && groups > 0 && !warp_wait<D>(p, s, &s.o_free, (groups - 1) & 1)) return;
+      groups += start;
       // last: in a shared ring of three the slot held this tile's K
       if (!warp_wait<D>(p, s, &s.full[at.slot], at.use & 1)) return;
       tc5_fence_after();
@@ -1139,8 +1164,9 @@ __device__ void pv_loop(const PrefixParams& p, PrefixSmem<D>& s) {
 #pragma unroll
           for (int k = 0; k < KT; k += 16)
             mma_ts(tm, a + k / 32 * 32 + term * 16 + k % 32 / 2, v + k * 8, idesc,
-                   term == 0 || k > 0);
+                   term == 0 || k > 0 || !start);
         mma_commit(&s.pv_done[buf]);
+        mma_commit(&s.b_free[buf]);
         mma_commit(&s.empty[at.slot]);
       }
       __syncwarp();
@@ -1164,8 +1190,9 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 4);
       mbar_init(&s.pv_done[i], 1);
-      mbar_init(&s.o_free[i], 4 * G::SUMG);
+      mbar_init(&s.b_free[i], 1 + 4 * G::SUMG);
     }
+    mbar_init(&s.o_free, 4 * G::SUMG);
     for (int i = 0; i < 2; ++i) {
       // Q in tensor memory: eight warps load it, the products use it; else one group's four
       // warps and warp 3 load it, the products use it and the group reads its row_scale
