@@ -464,8 +464,9 @@ struct Place {
 // ------------------------------------------------------------------ TMA warps
 // K and V tiles into the ring.  Each lane copies one box.  Boxes without a
 // visible key and pages outside the pool are filled with zeros by a copy that
-// starts past the pool's last row.  A tile's block ids are fetched a step before its copy is
-// issued: no copy waits for them.
+// starts past the pool's last row.  No copy waits for its block ids.  One warp that loads K
+// or V alone has about 1000 cycles a tile (D = 128): it reads 32 ids at once, two windows ahead,
+// and does little else (with the general form's cursor and divisions, 1700).
 template <int D>
 struct Loader {
   using G = PGeo<D>;
@@ -535,30 +536,76 @@ struct Loader {
     }
     return true;
   }
-  // One warp loads K or V (its own ring), or both.
-  __device__ __forceinline__ void run(bool values) {
+  // K or V into a ring of its own: slots [first, first + ring).
+  template <int RING>
+  __device__ __forceinline__ void run_one(bool is_v, int first) {
+    const int lane = threadIdx.x & 31;
+    const bool copy = copies();
+    const int none = p.num_blocks << p.log2_bs, mask = p.bs - 1;
+    const CUtensorMap* map = is_v ? &p.tm_v : &p.tm_k;
+    uint8_t* to = s.ring + first * G::TILE + slice * (G::KT * 128) + sub * p.box_rows * 128;
+    int slot = 0, x = 0;
+    uint32_t parity = 1;  // of the slot's last release: none to wait for the first time round
+    bool skip = p.test_skip_arm && blockIdx.x == 0 && !is_v;
+    for (Cursor<D> c(p, s); c.step();) {
+      const int* table = c.b < 0 ? p.prefix_table : p.block_table + (long long)c.b * p.max_blocks;
+      const int end = (c.khi + mask) >> p.log2_bs;  // columns that hold a key
+      int k0 = c.base + c.i0 * G::KT + sub * p.box_rows;  // this lane's box
+      int w0 = (c.base + c.i0 * G::KT) >> p.log2_bs;
+      auto window = [&](int w) { return w + lane < end ? table[w + lane] : -1; };
+      int ids = window(w0), more = window(w0 + 32);
+#pragma unroll 1
+      for (int j = 0; j < c.n; ++j, ++x, k0 += G::KT) {
+        const int col = (k0 >> p.log2_bs) - w0;
+        const int a = __shfl_sync(0xffffffffu, ids, col), b = __shfl_sync(0xffffffffu, more, col);
+        const int blk = col < 32 ? a : b;
+        const bool seen = copy && k0 < c.khi && k0 + p.box_rows > c.klo;
+        const bool ok = (uint32_t)blk < (uint32_t)p.num_blocks;
+        const int row = seen && ok ? (blk << p.log2_bs) + (k0 & mask) : none;
+        if (x >= RING && !warp_wait<D>(p, s, &s.empty[first + slot], parity)) return;
+        if (!is_v) {
+          int bad = 0;
+          if (__any_sync(0xffffffffu, seen && !ok)) {
+            bad = __reduce_or_sync(0xffffffffu, seen && !ok ? 1 << sub : 0);
+            flags = DEV_BAD_BLOCK;
+          }
+          if (lane == 0) s.bad[x & 15] = bad;
+        }
+        // test hook: the first tile of CTA 0 never arrives and its consumer's wait runs out
+        if (!skip) {
+          const int at = first + slot;
+          used = (used & ~(1u << at)) | (parity ^ 1) << at | 0x10000u << at;
+          if (lane == 0) mbar_arrive_expect_tx(&s.full[at], G::TILE);
+          __syncwarp();
+          if (copy) tma_load_4d(to + slot * G::TILE, map, &s.full[at], 0, row, slice, c.h);
+        }
+        skip = false;
+        if (++slot == RING) {
+          slot = 0;
+          parity ^= 1;
+        }
+        // all boxes of the next tile lie in the second window
+        if (__shfl_sync(0xffffffffu, ((k0 + G::KT) >> p.log2_bs) - w0, 0) >= 32) {
+          w0 += 32;
+          ids = more;
+          more = window(w0 + 32);
+        }
+      }
+    }
+  }
+  // One warp loads both, in the order of the shared ring.
+  __device__ __forceinline__ void run_both() {
     Cursor<D> c(p, s);
     int j = 0;
-    if constexpr (G::QT) {
-      Tile now = {0, 0, 0, false, false};
+    Tile t0 = {0, 0, 0, false, false}, t1 = t0, t2 = t0;  // tiles x, x + 1, x + 2
 #pragma unroll 1
-      for (int x = -1;; ++x) {
-        const Tile next = fetch(c, j);
-        if (x >= 0 && !issue(now, x, values)) return;
-        now = next;
-        if (!now.there) return;
-      }
-    } else {
-      Tile t0 = {0, 0, 0, false, false}, t1 = t0, t2 = t0;  // tiles x, x + 1, x + 2
+    for (int x = -3; x < 0 || t0.there; ++x) {
 #pragma unroll 1
-      for (int x = -3; x < 0 || t0.there; ++x) {
-#pragma unroll 1
-        for (int u = x < 0 ? 1 : 0; u < (t2.there ? 2 : 1); ++u)
-          if (!issue(u ? t2 : t0, u ? x + 2 : x, u == 0)) return;
-        t0 = t1;
-        t1 = t2;
-        t2 = fetch(c, j);
-      }
+      for (int u = x < 0 ? 1 : 0; u < (t2.there ? 2 : 1); ++u)
+        if (!issue(u ? t2 : t0, u ? x + 2 : x, u == 0)) return;
+      t0 = t1;
+      t1 = t2;
+      t2 = fetch(c, j);
     }
   }
   // After an abort: the copies in flight end before their memory is given back.
@@ -1089,6 +1136,26 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
 // steps truncate at their own size.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
+// A place that goes round `n` of them, and how often it went round, modulo 2.
+struct Round {
+  int at = 0;
+  uint32_t odd = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++at == n) {
+      at = 0;
+      odd ^= 1;
+    }
+  }
+};
+// Both waits; asked for together, so that where both are over they cost one's latency.
+template <int D>
+__device__ __forceinline__ bool warp_wait2(const PrefixParams& p, PrefixSmem<D>& s, uint64_t* a,
+                                           uint32_t pa, uint64_t* b, uint32_t pb) {
+  const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
+  if (__all_sync(0xffffffffu, x && y)) return true;
+  return warp_wait<D>(p, s, a, pa) && warp_wait<D>(p, s, b, pb);
+}
+
 template <int D>
 __device__ void qk_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   using G = PGeo<D>;
@@ -1098,20 +1165,31 @@ __device__ void qk_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   const uint64_t q = smem_desc(smem_u32(s.q), 16, 1024);  // all 128 rows, whoever's they are
   const uint64_t k0 = smem_desc(smem_u32(s.ring), 16, 1024);
   int x = 0;
+  Round buf, ring;
   for (Cursor<D> c(p, s); c.step();) {
     const int n = uniform(c.n), part = uniform(c.k);
     if (!warp_wait<D>(p, s, &s.q_full[part & 1], (part >> 1) & 1)) return;
     for (int j = 0; j < n; ++j, ++x) {
-      const Place<D> at = Place<D>::k(x);
-      const int buf = x % G::NS;
-      // the buffer's last tile: its products are done and its factor is read.  Before the wait
-      // for K: in a shared ring of three the slot held that tile's V, and only then has its phase
-      // passed that the next one's parity is told from
-      if (x >= G::NS && !warp_wait<D>(p, s, &s.b_free[buf], (x / G::NS - 1) & 1)) return;
-      if (!warp_wait<D>(p, s, &s.full[at.slot], at.use & 1)) return;
+      int slot = ring.at;
+      uint32_t use = ring.odd;
+      if constexpr (!G::QT) {
+        const Place<D> at = Place<D>::k(x);
+        slot = at.slot;
+        use = at.use & 1;
+      }
+      // the buffer's last tile: its products are done and its factor is read
+      if constexpr (G::QT) {
+        // (the first time round the other parity, which has always passed)
+        if (!warp_wait2<D>(p, s, &s.b_free[buf.at], buf.odd ^ 1, &s.full[slot], use)) return;
+      } else {
+        // before the wait for K: in a shared ring of three the slot held that tile's V, and only
+        // then has its phase passed that the next one's parity is told from
+        if (!warp_wait<D>(p, s, &s.b_free[buf.at], buf.odd ^ 1)) return;
+        if (!warp_wait<D>(p, s, &s.full[slot], use)) return;
+      }
       tc5_fence_after();
-      const uint64_t k = k0 + at.slot * (G::TILE / 16);
-      const uint32_t d = tm + G::S0 + buf * KT;
+      const uint64_t k = k0 + slot * (G::TILE / 16);
+      const uint32_t d = tm + G::S0 + buf.at * KT;
       if (elect_one()) {
 #pragma unroll G::QT ? 2 * G::SL : 1  // D = 256: its descriptors would spill
         for (int i = 0; i < 2 * G::SL; ++i) {
@@ -1126,11 +1204,13 @@ __device__ void qk_loop(const PrefixParams& p, PrefixSmem<D>& s) {
                      i + u > 0);
           }
         }
-        mma_commit(&s.s_full[buf]);
-        mma_commit(&s.empty[at.slot]);
+        mma_commit(&s.s_full[buf.at]);
+        mma_commit(&s.empty[slot]);
         if (j == n - 1) mma_commit(&s.q_free[part & 1]);
       }
       __syncwarp();
+      buf.next(G::NS);
+      ring.next(G::RK);
     }
   }
 }
@@ -1142,22 +1222,31 @@ __device__ void pv_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   constexpr uint32_t idesc = f16_idesc(D, true);
   const uint32_t tm = uniform(s.tmem);
   const uint64_t v0 = smem_desc(smem_u32(s.ring), KT * 128, 1024);
-  int x = 0, groups = 0;
+  int x = 0;
+  uint32_t groups = 0;
+  Round buf, ring;
   for (Cursor<D> c(p, s); c.step();) {
     const int n = uniform(c.n);
     for (int j = 0; j < n; ++j, ++x) {
-      const Place<D> at = Place<D>::v(x);
-      const int buf = x % G::NS;
-      if (!warp_wait<D>(p, s, &s.p_full[buf], (x / G::NS) & 1)) return;
+      int slot = G::RK + ring.at;
+      uint32_t use = ring.odd;
+      if constexpr (G::QT) {
+        if (!warp_wait2<D>(p, s, &s.full[slot], use, &s.p_full[buf.at], buf.odd)) return;
+      } else {
+        // V last: in a shared ring of three the slot held this tile's K
+        const Place<D> at = Place<D>::v(x);
+        slot = at.slot;
+        use = at.use & 1;
+        if (!warp_wait<D>(p, s, &s.p_full[buf.at], buf.odd)) return;
+        if (!warp_wait<D>(p, s, &s.full[slot], use)) return;
+      }
       const bool start =
-          j % kGroup == 0 || uniform(*reinterpret_cast<const int*>(s.grew[buf])) != 0;
+          j % kGroup == 0 || uniform(*reinterpret_cast<const int*>(s.grew[buf.at])) != 0;
       if (start && groups > 0 && !warp_wait<D>(p, s, &s.o_free, (groups - 1) & 1)) return;
       groups += start;
-      // last: in a shared ring of three the slot held this tile's K
-      if (!warp_wait<D>(p, s, &s.full[at.slot], at.use & 1)) return;
       tc5_fence_after();
-      const uint64_t v = v0 + at.slot * (G::TILE / 16);
-      const uint32_t a = tm + G::S0 + buf * KT;
+      const uint64_t v = v0 + slot * (G::TILE / 16);
+      const uint32_t a = tm + G::S0 + buf.at * KT;
       if (elect_one()) {
 #pragma unroll
         for (int term = 1; term >= 0; --term)
@@ -1165,11 +1254,13 @@ __device__ void pv_loop(const PrefixParams& p, PrefixSmem<D>& s) {
           for (int k = 0; k < KT; k += 16)
             mma_ts(tm, a + k / 32 * 32 + term * 16 + k % 32 / 2, v + k * 8, idesc,
                    term == 0 || k > 0 || !start);
-        mma_commit(&s.pv_done[buf]);
-        mma_commit(&s.b_free[buf]);
-        mma_commit(&s.empty[at.slot]);
+        mma_commit(&s.pv_done[buf.at]);
+        mma_commit(&s.b_free[buf.at]);
+        mma_commit(&s.empty[slot]);
       }
       __syncwarp();
+      buf.next(G::NS);
+      ring.next(G::QT ? G::RV : 1);
     }
   }
 }
@@ -1236,7 +1327,12 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
     setmaxnreg_dec<G::REG_LOAD>();
     if (warp == 0 || (warp == 3 && G::QT)) {
       Loader<D> ld(p, s);
-      ld.run(warp == 3);
+      if constexpr (!G::QT)
+        ld.run_both();
+      else if (warp == 0)
+        ld.template run_one<G::RK>(false, 0);
+      else
+        ld.template run_one<G::RV>(true, G::RK);
       const int bad = __reduce_or_sync(0xffffffffu, ld.flags);
       if (bad && lane == 0 && p.dev_status) atomicOr(p.dev_status, bad);
       if (*(volatile int*)&s.abort) ld.drain();
