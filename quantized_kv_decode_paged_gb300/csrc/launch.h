@@ -68,7 +68,7 @@ struct alignas(128) PrefixParams {
   float softcap_inv;  // 1 / softcap2
   int grid;
   unsigned long long wait_ns;  // time limit of every wait (abort mode after it)
-  int test_skip_arm;           // test hook: CTA 0's first copy is left out
+  int test_skip_arm;           // test hook: the first copy is left out
   const float* q;
   const uint16_t* k_pool;
   const uint16_t* v_pool;

@@ -203,7 +203,10 @@ template <int D>
 constexpr int kSmallRows = PGeo<D>::QT ? 32 : 64;
 // Units cost more than their tiles: Q, the first tile's latencies, the state's store.  The list
 // counts so many tiles for it (fitted to 1 to 16 tiles a unit, 8 to 128 rows).
-constexpr int kPrefixExtra = 4, kOwnExtra = 1;
+template <int D>
+constexpr int kPrefixExtra = D >= 256 ? 24 : 8;
+template <int D>
+constexpr int kOwnExtra = D >= 256 ? 2 : 4;
 // The maximum that a tile's weights are taken against moves at the first tile of a group of
 // kGroup, whose products add up in tensor memory before the sum warps take them, and where a row
 // outgrows it by 2^kGrow (that tile then starts a group).  Weights are kept times 2^kShift:
@@ -236,6 +239,7 @@ struct PrefixSmem {
   int lo, hi;                                            // prefix keys some row sees
   int first[4];                                          // where the CTA's run starts: b, h, rt, tile
   int run;                                               // its length in the list
+  int skip;                                              // test hook: the first copy is left out
   int abort;
   uint32_t tmem;
 };
@@ -301,9 +305,9 @@ struct Cursor {
         }
       }
       if (left <= 0) return false;
-      int extra = kOwnExtra;
+      int extra = kOwnExtra<D>;
       if (b < 0) {
-        extra = kPrefixExtra;
+        extra = kPrefixExtra<D>;
         klo = s.lo;
         khi = s.hi;
         base = klo / KT * KT;
@@ -362,7 +366,7 @@ __device__ int make_plan(const PrefixParams& p, PrefixSmem<D>& s) {
       atomicMax(&s.hi, min(hi, P));
     }
     const int l = max(lo, P);
-    if (hi > l) n = (hi - P + KT - 1) / KT - (l - P) / KT + kOwnExtra;
+    if (hi > l) n = (hi - P + KT - 1) / KT - (l - P) / KT + kOwnExtra<D>;
   }
   int sum = n;
 #pragma unroll
@@ -524,8 +528,8 @@ struct Loader {
       if (lane == 0) s.bad[x & 15] = mask;
       if (bad) flags |= DEV_BAD_BLOCK;
     }
-    // test hook: the first tile of CTA 0 never arrives and its consumer's wait runs out
-    const bool skip = p.test_skip_arm && blockIdx.x == 0 && x == 0 && !is_v;
+    // test hook: a tile that never arrives; its consumer's wait runs out
+    const bool skip = s.skip && x == 0 && !is_v;
     if (!skip) {
       used = (used & ~(1u << at.slot)) | (uint32_t)(at.use & 1) << at.slot | 0x10000u << at.slot;
       if (lane == 0) mbar_arrive_expect_tx(&s.full[at.slot], G::TILE);
@@ -546,7 +550,7 @@ struct Loader {
     uint8_t* to = s.ring + first * G::TILE + slice * (G::KT * 128) + sub * p.box_rows * 128;
     int slot = 0, x = 0;
     uint32_t parity = 1;  // of the slot's last release: none to wait for the first time round
-    bool skip = p.test_skip_arm && blockIdx.x == 0 && !is_v;
+    bool skip = s.skip && !is_v;  // test hook
     for (Cursor<D> c(p, s); c.step();) {
       const int* table = c.b < 0 ? p.prefix_table : p.block_table + (long long)c.b * p.max_blocks;
       const int end = (c.khi + mask) >> p.log2_bs;  // columns that hold a key
@@ -571,7 +575,6 @@ struct Loader {
           }
           if (lane == 0) s.bad[x & 15] = bad;
         }
-        // test hook: the first tile of CTA 0 never arrives and its consumer's wait runs out
         if (!skip) {
           const int at = first + slot;
           used = (used & ~(1u << at)) | (parity ^ 1) << at | 0x10000u << at;
@@ -638,19 +641,23 @@ __device__ __forceinline__ bool load_q_lanes(const PrefixParams& p, PrefixSmem<D
   int seq, tok;
   const int at = c.out_row(min(max(row - c.lane0(), 0), c.nr - 1), seq, tok);
   const float* src = p.q + (long long)at * D + group * H;
+  // Every lane reads lines of its own, which is what the L1's rate bounds: each line once,
+  // in the widest pieces the address allows (read twice in 16-byte ones, 128 rows took
+  // 8000 cycles more).
+  float v[H];
+  if (reinterpret_cast<uintptr_t>(p.q) % 32 == 0) {
 #pragma unroll
-  for (int i = 0; i < H; i += 32) {  // the lines are under way before the first is waited for
-    uint32_t unused;
-    asm volatile("ld.global.b32 %0, [%1];" : "=r"(unused) : "l"(src + i));
+    for (int i = 0; i < H; i += 8) load_f32x8(src + i, v + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < H; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src + i);
+      v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+    }
   }
   float m = 0.f;
-#pragma unroll 1
-  for (int i = 0; i < H; i += 16)
 #pragma unroll
-    for (int u = 0; u < 16; u += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(src + i + u);
-      m = fmaxf(fmaxf(fmaxf(m, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(x.z))), fabsf(x.w));
-    }
+  for (int i = 0; i < H; ++i) m = fmaxf(m, fabsf(v[i]));
   s.q_max[group * kPrefixRows + row] = m;
   __syncwarp();
   if (lane == 0) mbar_arrive(&s.q_half[w]);
@@ -658,15 +665,12 @@ __device__ __forceinline__ bool load_q_lanes(const PrefixParams& p, PrefixSmem<D
   float by;
   q_powers(fmaxf(m, s.q_max[(group ^ 1) * kPrefixRows + row]), by, scale);
   scale *= p.qscale;
-#pragma unroll 1
+#pragma unroll
   for (int i = 0; i < H; i += 16) {
     uint32_t hi[8], lo[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float4 x = *reinterpret_cast<const float4*>(src + i + 4 * u);
-      split_half2(x.x * by, x.y * by, hi[2 * u], lo[2 * u]);
-      split_half2(x.z * by, x.w * by, hi[2 * u + 1], lo[2 * u + 1]);
-    }
+    for (int u = 0; u < 8; ++u)
+      split_half2(v[i + 2 * u] * by, v[i + 2 * u + 1] * by, hi[u], lo[u]);
     const uint32_t to = lanes + PGeo<D>::Q0 + (group * H + i) / 2;
     tmem_st8(to, hi);
     tmem_st8(to + D / 2, lo);
@@ -1313,11 +1317,15 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
   if (blockIdx.x == 0 && flags && p.dev_status) atomicOr(p.dev_status, flags);
   if (tid == 0) {
     const int pn =
-        s.hi > s.lo ? (s.hi + G::KT - 1) / G::KT - s.lo / G::KT + kPrefixExtra : 0;
+        s.hi > s.lo ? (s.hi + G::KT - 1) / G::KT - s.lo / G::KT + kPrefixExtra<D> : 0;
     const int tp = pn * (p.Hkv * p.row_tiles);
     const Split sp(tp + s.cum[p.B] * (p.Hkv * p.own_tiles), p.grid);
     s.run = sp.share + ((int)blockIdx.x < sp.rem);
-    if (s.run > 0) find_first<D>(p, s, sp.start(blockIdx.x), pn, tp);
+    const int g = sp.start(blockIdx.x);
+    if (s.run > 0) find_first<D>(p, s, g, pn, tp);
+    // test hook: in the first CTA that has a tile
+    const int tile = pn ? kPrefixExtra<D> : kOwnExtra<D>;
+    s.skip = p.test_skip_arm && g <= tile && tile < g + s.run;
     if (blockIdx.x == 0) p.ws_plan[0] = pn;
   }
   if (blockIdx.x == 0)
@@ -1406,7 +1414,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int n0 = pn, n1 = cum[b + 1] - cum[b];
   const int g0 = (h * p.row_tiles + rb / kPrefixRows) * n0;
   const int g1 = tp + cum[b] * units1 + (h * p.own_tiles + r1 / kPrefixRows) * n1;
-  const int c0 = n0 ? sp.cta(g0 + kPrefixExtra) : 0, c1 = n1 ? sp.cta(g1 + kOwnExtra) : 0;
+  const int c0 = n0 ? sp.cta(g0 + kPrefixExtra<D>) : 0, c1 = n1 ? sp.cta(g1 + kOwnExtra<D>) : 0;
   const int s0 = n0 ? sp.cta(g0 + n0 - 1) - c0 + 1 : 0;  // its states
   const int s1 = n1 ? sp.cta(g1 + n1 - 1) - c1 + 1 : 0;
   float M = -kInf, L = 0.f, o[V];
