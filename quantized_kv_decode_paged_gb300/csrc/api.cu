@@ -677,7 +677,7 @@ int check_prefix(const da_params* p, int T, int prefix_len) {
   const int G = p->num_q_heads / p->num_kv_heads;
   const long long units = (long long)p->num_kv_heads * most *
                           (((long long)T * G + da::kPrefixRows - 1) / da::kPrefixRows + 1);
-  if (((long long)p->max_blocks_per_seq * p->block_size / tile + 32) * units > 0x7fffffffLL)
+  if (((long long)p->max_blocks_per_seq * p->block_size / tile + 64) * units > 0x7fffffffLL)
     return DA_ERR_UNSUPPORTED;
   // a tile past the last key still has 32-bit key indices
   if ((long long)p->max_blocks_per_seq * p->block_size > 0x7fffffffLL - 1024)

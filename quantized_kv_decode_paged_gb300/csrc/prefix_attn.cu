@@ -8,11 +8,11 @@
 //
 // Work.  The rows of one kv head (sequences x query tokens x its query
 // heads) that share keys are cut into tiles of 128 rows, the keys into tiles
-// of 128 (64 for D = 256).  A prefix unit is a (kv head, tile of the batch's
+// of 64 (128 for D = 64).  A prefix unit is a (kv head, tile of the batch's
 // rows) over the prefix, an own unit a (sequence, kv head, tile of its rows)
-// over its own keys.  All units' key tiles form one list; every CTA takes an
-// equal run of it (tiles cost the same: the MMA's M is 128 whether a tile has
-// 4 rows or 128).  A unit that lies in one CTA leaves its state in
+// over its own keys.  All units' key tiles, and entries that stand for a unit's
+// fixed cost, form one list; every CTA takes an equal run of it (tiles cost about the same:
+// the MMA's M is 128 whether a tile has 4 rows or 128).  A unit that lies in one CTA leaves its state in
 // the row's place; the parts of a unit that CTA boundaries cut go to the
 // CTAs' slots.  prefix_merge_kernel joins a row's states:
 // M = max m_s, w_s = 2^(m_s - M), out = sum w_s o_s / sum w_s l_s.
@@ -21,11 +21,11 @@
 // operands and f32 accumulators in tensor memory.  Q (f32) is held as
 // two f16 terms of q / 2^e, e the row's exponent, P as two f16 terms: 22 bits
 // each, so out keeps f32's accuracy (one term would leave 2^-12).  That doubles
-// the products: 8 * 128 * D flops a key; a 128-key tile of D = 128 is 2048
-// cycles of the tensor pipe for 64 KB of K and V, about the rate at which
+// the products: 8 * 128 * D flops a key; a 64-key tile of D = 128 is 1024
+// cycles of the tensor pipe for 32 KB of K and V, about the rate at which
 // HBM delivers them.  The tensor cores' f32 sums truncate: a long chain of
 // them drifts (2^-24 of the sum a step on average; 3.6e-5 of the result after 145 tiles
-// in one accumulator).  So every tile starts a new accumulator, the low terms go first
+// in one accumulator).  So every second tile starts a new accumulator, the low terms go first
 // (their steps truncate at their own size), and the sums over tiles are ordinary f32 adds in
 // registers.
 //
@@ -175,7 +175,7 @@ struct PGeo {
   // flight.  D = 256 has no room for Q beside O.
   static constexpr bool QT = D < 256;
   static constexpr int Q0 = QT ? D : 0;
-  static constexpr int S0 = QT ? 2 * D : D;
+  static constexpr int S0 = Q0 + D;
   static constexpr int F0 = S0 + NS * KT;
   static constexpr bool FAC_TMEM = F0 + NS <= 512;
   // Tiles in flight: with Q in tensor memory K and V have a ring and a loading
@@ -424,7 +424,8 @@ __device__ void find_first(const PrefixParams& p, PrefixSmem<D>& s, int g, int p
 // Waits for the phase of `bar` with the given parity.  A wait that runs past
 // the limit sets the abort flag; every role then leaves its loop, and the kernel reports it
 // at its end.  Short, because it is inlined at every wait: the kernel's code has to stay in the
-// instruction cache (117 KB of it, most in these waits, cost 3 of 6 us a tile).
+// instruction cache (123 KB of it, most in these waits, took 566 us where 61 KB took 322: 128
+// sequences of 64 heads over 32,768 shared keys).
 template <int D>
 __device__ __forceinline__ bool wait_or_abort(const PrefixParams& p, PrefixSmem<D>& s,
                                               uint64_t* bar, uint32_t parity) {
@@ -447,22 +448,15 @@ __device__ __forceinline__ bool warp_wait(const PrefixParams& p, PrefixSmem<D>& 
 }
 
 // ------------------------------------------------------------------ the ring
-// Slot of tile x's K or V and how often the slot was used before.  A shared
-// ring takes them in the products' order K(0) K(1) V(0) K(2) V(1) ...
+// The shared ring (D = 256) takes K and V in the products' order K(0) K(1) V(0) K(2) V(1) ...:
+// slot of tile x's, and how often the slot was used before.
 template <int D>
 struct Place {
-  using G = PGeo<D>;
   int slot, use;
-  __device__ __forceinline__ static Place k(int x) {
-    if (G::QT) return {x % G::RK, x / G::RK};
-    const int at = x < 2 ? x : 2 * x - 1;
-    return {at % G::RING, at / G::RING};
-  }
-  __device__ __forceinline__ static Place v(int x) {
-    if constexpr (G::QT) return {G::RK + x % G::RV, x / G::RV};
-    const int at = 2 * x + 2;
-    return {at % G::RING, at / G::RING};
-  }
+  __device__ __forceinline__ explicit Place(int at)
+      : slot(at % PGeo<D>::RING), use(at / PGeo<D>::RING) {}
+  __device__ __forceinline__ static Place k(int x) { return Place(x < 2 ? x : 2 * x - 1); }
+  __device__ __forceinline__ static Place v(int x) { return Place(2 * x + 2); }
 };
 
 // ------------------------------------------------------------------ TMA warps
@@ -1004,17 +998,19 @@ __device__ void softmax_loop_two(const PrefixParams& p, PrefixSmem<D>& s) {
   bool more = next.step();
   // Whether this warp loads the next part's Q: rows of it lie in its lanes, or all warps do.
   auto mine = [&] { return !next.small() || w == next.lane0() / 32; };
-  if (more && mine() && !load_q_lanes<D>(p, s, next, group, w, lanes, loads++, next_scale)) return;
-  while (more) {
-    c.step();
-    more = next.step();
-    const int k = c.k;
-    Row r = row_of<D>(p, s, c, w);
-    r.scale = next_scale;
+  // k = -1: no part yet, the first one's Q alone
+  for (int k = -1; k < 0 || more; ++k) {
+    Row r;
+    if (k >= 0) {
+      c.step();
+      more = next.step();
+      r = row_of<D>(p, s, c, w);
+      r.scale = next_scale;
+    }
     // The next part's Q goes into lanes that this part does not use while this part is worked on:
     // the products of the parts before are done with them.
-    const bool early = more && c.small() && next.small();
-    bool load = more && mine();
+    const bool early = k >= 0 && more && c.small() && next.small();
+    const bool load = more && mine();
     for (int pass = 0; pass < 2; ++pass) {
       if (load && early == (pass == 0)) {
         const int last = pass == 0 ? k - 1 : k;
@@ -1028,6 +1024,7 @@ __device__ void softmax_loop_two(const PrefixParams& p, PrefixSmem<D>& s) {
         if (!softmax_tile<D, CAP>(p, s, c, r, j, x, w, lanes, box_shift)) return;
       }
     }
+    if (k < 0) continue;
     const int last = x0 + c.n - 1;
     x0 += c.n;
     if (c.n > 1) {
