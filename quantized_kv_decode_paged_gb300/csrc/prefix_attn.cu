@@ -42,6 +42,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/decode_attn.h"
 #include "launch.h"
@@ -184,6 +185,7 @@ struct PGeo {
   static constexpr int AC = D < 128 ? D : 128;    // columns a sum thread holds
   static constexpr int SUMG = D / AC;             // sum warpgroups
   static constexpr int SOFTG = D >= 256 ? 1 : 2;  // softmax warpgroups, taking turns at the tiles
+  static constexpr int SETS = QT ? 5 : 1;         // of barriers, by which warps take a part
   static constexpr int GROUPS = 1 + SOFTG + SUMG;
   static constexpr int THREADS = 128 * GROUPS;
   // Registers a thread: at launch, then by role (setmaxnreg); the roles'
@@ -202,11 +204,15 @@ struct PGeo {
 template <int D>
 constexpr int kSmallRows = PGeo<D>::QT ? 32 : 64;
 // Units cost more than their tiles: Q, the first tile's latencies, the state's store.  The list
-// counts so many tiles for it (fitted to 1 to 16 tiles a unit, 8 to 128 rows).
+// counts so many tiles for it.  D = 128, without it (0, 0) and with (12, 2): 376 and 259 us for 128
+// sequences of 64 heads over 32,768 shared and 64 to 2048 own keys, 61 and 45 for 24 x 4 tokens of
+// 32 heads over 8192 and 64 to 1400, 419 and 79 for the first over 16 shared keys.  Own units of one
+// tile want 2, long ones 1 (1 alone: 225 for 210 us with 1 or 2 own keys, 76 for 79 with 64 to 2048).
+// D = 256: 170 and 140 us for 64 sequences of 16 heads, a window of 4096 and 256 to 2048 own keys.
 template <int D>
-constexpr int kPrefixExtra = D >= 256 ? 24 : 8;
+constexpr int kPrefixExtra = D >= 256 ? 24 : 12;
 template <int D>
-constexpr int kOwnExtra = D >= 256 ? 2 : 4;
+constexpr int kOwnExtra = 2;
 // The maximum that a tile's weights are taken against moves at the first tile of a group of
 // kGroup, whose products add up in tensor memory before the sum warps take them, and where a row
 // outgrows it by 2^kGrow (that tile then starts a group).  Weights are kept times 2^kShift:
@@ -215,6 +221,18 @@ constexpr int kGroup = 2;
 constexpr float kGrow = 7.f;
 constexpr float kShift = 8.f;
 
+// A part of a unit (Part) as the list's run names it.
+struct alignas(16) PartInfo {
+  int b, h;              // b < 0: prefix
+  int r0, nr;
+  int base, klo, khi;    // keys [klo, khi) may be seen
+  int i0, n;
+  int unit_n;            // tiles of the whole unit
+};
+// How many a CTA keeps: a part is read by every warp before the loads are so many ahead of it (they
+// are at most 13 tiles ahead of the sums, and a warp takes at least every fourth part).
+constexpr int kParts = 32;
+
 template <int D>
 struct PrefixSmem {
   using G = PGeo<D>;
@@ -222,9 +240,12 @@ struct PrefixSmem {
   uint8_t ring[G::RING * G::TILE];
   uint8_t q[G::QT ? 16 : 2 * G::QTERM];
   uint64_t full[G::RING], empty[G::RING];
-  uint64_t s_full[G::NS], p_full[G::NS], pv_done[G::NS], b_free[G::NS], o_free;
-  uint64_t q_full[2], q_free[2], drain[2];
+  uint64_t s_full[G::SETS * G::NS], p_full[G::SETS * G::NS], pv_done[G::SETS * G::NS];
+  uint64_t b_free[G::NS], o_free;
+  uint64_t q_full[G::QT ? G::SETS : 2], q_free[G::QT ? G::SETS : 2], drain[2];
   uint64_t m_ready[4], l_ready[2][4], q_half[4];         // by warp of a warpgroup
+  uint64_t part_ready[G::QT ? kParts : 1];
+  PartInfo parts[G::QT ? kParts : 1];
   float row_scale[G::QT ? 1 : kPrefixRows];              // qscale * 2^e, by row of the Q buffer
   float fac[G::FAC_TMEM ? 1 : G::NS * kPrefixRows];      // 2^(m_old - m_new) of a tile's rows
   // two softmax warpgroups: the running maximum from one tile to the next, the sum of the one
@@ -262,35 +283,90 @@ struct Split {
   }
 };
 
-// The parts of units that a CTA's run of the list is made of, one after the
-// other.  Part: rows [r0, r0 + nr) of kv head h (r0 counts the batch's rows in the prefix, the
-// sequence's in its own keys), key tiles [i0, i0 + n), tile i's keys starting at base + i * KT.
-// A unit's first `extra` entries of the list stand for its fixed cost; runs that hold only
-// such entries of a unit have no part of it.
+// Waits for the phase of `bar` with the given parity.  A wait that runs past
+// the limit sets the abort flag; every role then leaves its loop, and the kernel reports it
+// at its end.  Short, because it is inlined at every wait: the kernel's code has to stay in the
+// instruction cache (123 KB of it, most in these waits, took 566 us where 61 KB took 322: 128
+// sequences of 64 heads over 32,768 shared keys).
 template <int D>
-struct Cursor {
+__device__ __forceinline__ bool wait_or_abort(const PrefixParams& p, PrefixSmem<D>& s,
+                                              uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*(volatile int*)&s.abort) return false;
+    if (globaltimer_ns() - t0 > p.wait_ns) {
+      *(volatile int*)&s.abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// The same for all lanes of a warp, which go on or leave together.
+template <int D>
+__device__ __forceinline__ bool warp_wait(const PrefixParams& p, PrefixSmem<D>& s, uint64_t* bar,
+                                          uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_or_abort<D>(p, s, bar, parity));
+}
+
+// A part of a unit: rows [r0, r0 + nr) of kv head h (r0 counts the batch's rows in the prefix,
+// the sequence's in its own keys), key tiles [i0, i0 + n), tile i's keys starting at base + i * KT.
+template <int D>
+struct Part : PartInfo {
+  using G = PGeo<D>;
+  int k = -1;            // number of the part
+  __device__ __forceinline__ bool whole() const { return n == unit_n; }
+  __device__ __forceinline__ bool small() const { return nr <= kSmallRows<D>; }
+  // Q in tensor memory: the rows of a small part lie in the lanes of one warp of each warpgroup,
+  // and only these warps take part in it, so that four such parts are under way at once.  Barriers
+  // that not every warp waits for come in sets, one of each of those warps' and one of all's (a
+  // warp then waits for every phase of the barriers it knows).
+  __device__ __forceinline__ bool apart() const { return G::QT && small(); }
+  __device__ __forceinline__ int set() const { return apart() ? k % 4 : G::SETS - 1; }
+  __device__ __forceinline__ bool takes(int w) const { return !apart() || k % 4 == w; }
+  // Lane of tensor memory (row of the Q buffer) of the part's first row.
+  __device__ __forceinline__ int lane0() const {
+    constexpr int parts = kPrefixRows / kSmallRows<D>;
+    return small() ? k % parts * kSmallRows<D> : 0;
+  }
+  // Sequence, query token and place in [B, T, Hq] of the part's row i.
+  __device__ __forceinline__ int out_row(const PrefixParams& p, int i, int& seq, int& tok) const {
+    int r = r0 + i;
+    seq = b;
+    if (b < 0) {
+      seq = (uint32_t)r / (uint32_t)p.R1;
+      r -= seq * p.R1;
+    }
+    tok = (uint32_t)r / (uint32_t)p.G;
+    return (seq * p.T + tok) * p.Hq + h * p.G + (r - tok * p.G);
+  }
+};
+
+// The parts that a CTA's run of the list is made of, one after the other.  A unit's first `extra`
+// entries of the list stand for its fixed cost; runs that hold only such entries of a unit have no
+// part of it.  TELL: each is announced to the warps that read them with a Reader.
+template <int D, bool TELL>
+struct Lister : Part<D> {
+  using Part<D>::b, Part<D>::h, Part<D>::r0, Part<D>::nr, Part<D>::base, Part<D>::klo,
+      Part<D>::khi, Part<D>::i0, Part<D>::n, Part<D>::unit_n, Part<D>::k;
   static constexpr int KT = PGeo<D>::KT;
   const PrefixParams& p;
-  const PrefixSmem<D>& s;
+  PrefixSmem<D>& s;
   int left;              // entries of the run from this part on
   int at, len;           // the part's first entry of its unit, its entries
-  int P;                 // prefix keys
-  int k = -1;            // number of the part
-  int h, b, rt;          // b < 0: prefix; rt: tile of rows
-  int r0, nr;
-  int base, klo, khi;    // keys [klo, khi) may be seen
-  int unit_n, i0, n;
+  int rt;                // tile of rows
 
-  __device__ __forceinline__ Cursor(const PrefixParams& p_, const PrefixSmem<D>& s_)
-      : p(p_), s(s_), left(s_.run), at(s_.first[3]), len(-1), P(p_.prefix_pages << p_.log2_bs) {
+  __device__ __forceinline__ Lister(const PrefixParams& p_, PrefixSmem<D>& s_)
+      : p(p_), s(s_), left(s_.run), at(s_.first[3]), len(-1) {
     b = s.first[0];
     h = s.first[1];
     rt = s.first[2];
     n = 0;
   }
-  __device__ __forceinline__ bool whole() const { return n == unit_n; }
-  // On to the run's first or next part; false behind the last one.
+  // On to the run's first or next part; false, and n = 0, behind the last one.
   __device__ __forceinline__ bool step() {
+    if (k >= 0 && n == 0) return false;
+    n = 0;
     do {
       if (len >= 0) {
         left -= len;
@@ -304,7 +380,7 @@ struct Cursor {
           }
         }
       }
-      if (left <= 0) return false;
+      if (left <= 0) break;
       int extra = kOwnExtra<D>;
       if (b < 0) {
         extra = kPrefixExtra<D>;
@@ -313,6 +389,7 @@ struct Cursor {
         base = klo / KT * KT;
         unit_n = (khi + KT - 1) / KT - klo / KT;
       } else {
+        const int P = p.prefix_pages << p.log2_bs;
         key_range(p, s.len[b], s.qp[b], 0, p.T - 1, klo, khi);
         klo = max(klo, P);
         base = P + (klo - P) / KT * KT;
@@ -322,29 +399,37 @@ struct Cursor {
       i0 = max(0, at - extra);
       n = at + len - extra - i0;
     } while (n <= 0);
+    n = max(n, 0);
     ++k;
     r0 = rt * kPrefixRows;
     nr = min(kPrefixRows, (b < 0 ? p.B * p.R1 : p.R1) - r0);
-    return true;
-  }
-  __device__ __forceinline__ bool small() const { return nr <= kSmallRows<D>; }
-  // Lane of tensor memory (row of the Q buffer) of the part's first row.
-  __device__ __forceinline__ int lane0() const {
-    constexpr int parts = kPrefixRows / kSmallRows<D>;
-    return small() ? k % parts * kSmallRows<D> : 0;
-  }
-  // Sequence, query token and place in [B, T, Hq] of the part's row i.
-  __device__ __forceinline__ int out_row(int i, int& seq, int& tok) const {
-    int r = r0 + i;
-    seq = b;
-    if (b < 0) {
-      seq = r / p.R1;
-      r -= seq * p.R1;
+    if (TELL && (threadIdx.x & 31) == 0) {
+      s.parts[k % kParts] = *this;
+      mbar_arrive(&s.part_ready[k % kParts]);
     }
-    tok = r / p.G;
-    return (seq * p.T + tok) * p.Hq + h * p.G + (r - tok * p.G);
+    return n > 0;
   }
 };
+
+template <int D>
+struct Reader : Part<D> {
+  using Part<D>::k, Part<D>::n;
+  const PrefixParams& p;
+  PrefixSmem<D>& s;
+  __device__ __forceinline__ Reader(const PrefixParams& p_, PrefixSmem<D>& s_) : p(p_), s(s_) {}
+  __device__ __forceinline__ bool step() {
+    const int next = k + 1, at = next % kParts;
+    if (!warp_wait<D>(p, s, &s.part_ready[at], next / kParts & 1)) return false;
+    static_cast<PartInfo&>(*this) = s.parts[at];
+    k = next;
+    return n > 0;
+  }
+};
+
+// How a warp other than the one that loads K walks its CTA's parts: to find one takes 1000 cycles, as
+// much as a tile, to read it 100; D = 256, whose parts are longer, has no room to keep them.
+template <int D>
+using Cursor = std::conditional_t<PGeo<D>::QT, Reader<D>, Lister<D, false>>;
 
 // Lengths and positions into shared memory, the tiles of every sequence's own
 // keys (running sums) and the prefix keys that some row sees.  All threads
@@ -421,31 +506,24 @@ __device__ void find_first(const PrefixParams& p, PrefixSmem<D>& s, int g, int p
   s.first[3] = g;
 }
 
-// Waits for the phase of `bar` with the given parity.  A wait that runs past
-// the limit sets the abort flag; every role then leaves its loop, and the kernel reports it
-// at its end.  Short, because it is inlined at every wait: the kernel's code has to stay in the
-// instruction cache (123 KB of it, most in these waits, took 566 us where 61 KB took 322: 128
-// sequences of 64 heads over 32,768 shared keys).
+// Parity of the phases of a tile's barriers (by set and buffer) as one warp comes to them: with
+// one set it follows from the tile's number, else each barrier's uses so far are counted.
 template <int D>
-__device__ __forceinline__ bool wait_or_abort(const PrefixParams& p, PrefixSmem<D>& s,
-                                              uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*(volatile int*)&s.abort) return false;
-    if (globaltimer_ns() - t0 > p.wait_ns) {
-      *(volatile int*)&s.abort = 1;
-      return false;
-    }
+struct Phases {
+  uint32_t odd = 0;
+  // of barrier `at`'s next use, for tile x
+  __device__ __forceinline__ uint32_t next(int at, int x) {
+    if constexpr (PGeo<D>::SETS == 1) return x / PGeo<D>::NS & 1;
+    const uint32_t parity = odd >> at & 1;
+    odd ^= 1u << at;
+    return parity;
   }
-  return true;
-}
-// The same for all lanes of a warp, which go on or leave together.
-template <int D>
-__device__ __forceinline__ bool warp_wait(const PrefixParams& p, PrefixSmem<D>& s, uint64_t* bar,
-                                          uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_or_abort<D>(p, s, bar, parity));
-}
+  // of its last use, for tile x
+  __device__ __forceinline__ uint32_t last(int at, int x) const {
+    if constexpr (PGeo<D>::SETS == 1) return x / PGeo<D>::NS & 1;
+    return odd >> at & 1 ^ 1;
+  }
+};
 
 // ------------------------------------------------------------------ the ring
 // The shared ring (D = 256) takes K and V in the products' order K(0) K(1) V(0) K(2) V(1) ...:
@@ -493,10 +571,7 @@ struct Loader {
     Tile t = {0, 0, 0, false, false};
     if (j == c.n) {
       j = 0;
-      if (!c.step()) {
-        c.n = 0;
-        return t;
-      }
+      if (!c.step()) return t;
     }
     t.there = true;
     t.h = c.h;
@@ -535,7 +610,7 @@ struct Loader {
     return true;
   }
   // K or V into a ring of its own: slots [first, first + ring).
-  template <int RING>
+  template <int RING, class Parts>
   __device__ __forceinline__ void run_one(bool is_v, int first) {
     const int lane = threadIdx.x & 31;
     const bool copy = copies();
@@ -545,7 +620,7 @@ struct Loader {
     int slot = 0, x = 0;
     uint32_t parity = 1;  // of the slot's last release: none to wait for the first time round
     bool skip = s.skip && !is_v;  // test hook
-    for (Cursor<D> c(p, s); c.step();) {
+    for (Parts c(p, s); c.step();) {
       const int* table = c.b < 0 ? p.prefix_table : p.block_table + (long long)c.b * p.max_blocks;
       const int end = (c.khi + mask) >> p.log2_bs;  // columns that hold a key
       int k0 = c.base + c.i0 * G::KT + sub * p.box_rows;  // this lane's box
@@ -628,12 +703,12 @@ __device__ __forceinline__ void q_powers(float m, float& by, float& undo) {
 // their halves' largest values; `uses` counts that.  Gives qscale * 2^e of the thread's row.
 template <int D>
 __device__ __forceinline__ bool load_q_lanes(const PrefixParams& p, PrefixSmem<D>& s,
-                                             const Cursor<D>& c, int group, int w, uint32_t lanes,
+                                             const Part<D>& c, int group, int w, uint32_t lanes,
                                              int uses, float& scale) {
   constexpr int H = D / 2;
   const int lane = threadIdx.x & 31, row = w * 32 + lane;
   int seq, tok;
-  const int at = c.out_row(min(max(row - c.lane0(), 0), c.nr - 1), seq, tok);
+  const int at = c.out_row(p, min(max(row - c.lane0(), 0), c.nr - 1), seq, tok);
   const float* src = p.q + (long long)at * D + group * H;
   // Every lane reads lines of its own, which is what the L1's rate bounds: each line once,
   // in the widest pieces the address allows (read twice in 16-byte ones, 128 rows took
@@ -672,8 +747,7 @@ __device__ __forceinline__ bool load_q_lanes(const PrefixParams& p, PrefixSmem<D
   tmem_wait_st();
   tc5_fence_before();
   __syncwarp();
-  // the barrier counts eight: every warp for many rows, these two for few
-  if (lane < (c.small() ? 4 : 1)) mbar_arrive(&s.q_full[c.k & 1]);
+  if (lane == 0) mbar_arrive(&s.q_full[c.set()]);
   return true;
 }
 
@@ -725,11 +799,11 @@ __device__ __forceinline__ void load_q_rows(const float* src, float qscale, Pref
 // Rows [first, first + 32) of the cursor's part, as far as `last`.
 template <int D>
 __device__ __forceinline__ void load_q(const PrefixParams& p, PrefixSmem<D>& s,
-                                       const Cursor<D>& c, int first, int last) {
+                                       const Part<D>& c, int first, int last) {
   const int n = min(32, min(last, c.nr) - first);
   if (n <= 0) return;
   int seq, tok;
-  const int mine = c.out_row(first + min((int)(threadIdx.x & 31), n - 1), seq, tok);
+  const int mine = c.out_row(p, first + min((int)(threadIdx.x & 31), n - 1), seq, tok);
   load_q_rows<D>(p.q, p.qscale, s, mine, c.lane0() + first, n);
 }
 
@@ -791,29 +865,31 @@ struct Row {
 };
 template <int D>
 __device__ __forceinline__ Row row_of(const PrefixParams& p, const PrefixSmem<D>& s,
-                                      const Cursor<D>& c, int w) {
+                                      const Part<D>& c, int w) {
   Row r = {false, false, 0, 0, 0, 0.f, -kInf, 0.f, false};
   const int first = c.lane0(), row = w * 32 + (int)(threadIdx.x & 31);
   r.any = w * 32 + 32 > first && w * 32 < first + c.nr;
   r.on = row >= first && row < first + c.nr;
   if (r.on) {
     int b, tok;
-    r.place = c.out_row(row - first, b, tok);
+    r.place = c.out_row(p, row - first, b, tok);
     key_range(p, s.len[b], s.qp[b], tok, tok, r.lo, r.hi);
+    const int P = p.prefix_pages << p.log2_bs;
     if (c.b < 0)
-      r.hi = min(r.hi, c.P);
+      r.hi = min(r.hi, P);
     else
-      r.lo = max(r.lo, c.P);
+      r.lo = max(r.lo, P);
   }
   return r;
 }
 
-// Scores of tile x (number j of the part) to weights.  `chain`: the running
-// maximum comes from the tile before and goes on to the next (two groups take turns).
+// Scores of tile x (number j of the part) to weights.  Where two groups take turns the
+// running maximum comes from the tile before and goes on to the next; `turn` counts the tiles
+// that this warp's lanes took part in.
 template <int D, bool CAP>
 __device__ __forceinline__ bool softmax_tile(const PrefixParams& p, PrefixSmem<D>& s,
-                                             const Cursor<D>& c, Row& r, int j, int x, int w,
-                                             uint32_t lanes, int box_shift) {
+                                             const Part<D>& c, Row& r, int j, int x, int turn,
+                                             int w, uint32_t lanes, int box_shift) {
   using G = PGeo<D>;
   constexpr int KT = G::KT;
   constexpr bool TWO = G::SOFTG == 2;
@@ -879,13 +955,16 @@ __device__ __forceinline__ bool softmax_tile(const PrefixParams& p, PrefixSmem<D
   }
   float before = r.m;
   if (TWO) {
-    if (x > 0 && !warp_wait<D>(p, s, &s.m_ready[w], (x - 1) & 1)) return false;
+    if (turn > 0 && !warp_wait<D>(p, s, &s.m_ready[w], (turn - 1) & 1)) return false;
     before = j > 0 ? s.m[row] : -kInf;
   }
   const float most = fmaxf(before, top * cc);
   const bool grew = __any_sync(0xffffffffu, r.on && most > before + kGrow);
   const float now = grew || j % kGroup == 0 ? most : before;
-  if (lane == 0) s.grew[buf][w] = grew;
+  if (c.apart())
+    *reinterpret_cast<uint32_t*>(s.grew[buf]) = grew;
+  else if (lane == 0)
+    s.grew[buf][w] = grew;
   if (TWO) {
     s.m[row] = now;
     __syncwarp();
@@ -934,12 +1013,12 @@ __device__ __forceinline__ bool softmax_tile(const PrefixParams& p, PrefixSmem<D
   }
   r.m = now;
   __syncwarp();
-  if (lane == 0) mbar_arrive(&s.p_full[buf]);
+  if (lane == 0) mbar_arrive(&s.p_full[c.set() * G::NS + buf]);
   return true;
 }
 
 template <int D>
-__device__ __forceinline__ void store_ml(const PrefixParams& p, const Cursor<D>& c, const Row& r,
+__device__ __forceinline__ void store_ml(const PrefixParams& p, const Part<D>& c, const Row& r,
                                          int w) {
   if (!r.on) return;
   float2* dst;
@@ -975,13 +1054,15 @@ __device__ void softmax_loop_one(const PrefixParams& p, PrefixSmem<D>& s) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.q_free[k & 1]);
       }
-      if (!softmax_tile<D, CAP>(p, s, c, r, j, x, w, lanes, box_shift)) return;
+      if (!softmax_tile<D, CAP>(p, s, c, r, j, x, x, w, lanes, box_shift)) return;
     }
     store_ml<D>(p, c, r, w);
   }
 }
 
-// Two groups that take turns at the tiles, Q in tensor memory.
+// Two groups that take turns at the tiles, Q in tensor memory.  Warp w of both loads its
+// rows of a part's Q when the products of the part it took before are done with theirs; the two
+// meet there, so that neither is a part ahead of the other.
 template <int D, bool CAP>
 __device__ void softmax_loop_two(const PrefixParams& p, PrefixSmem<D>& s) {
   using G = PGeo<D>;
@@ -990,48 +1071,39 @@ __device__ void softmax_loop_two(const PrefixParams& p, PrefixSmem<D>& s) {
   const int row = w * 32 + lane;
   const uint32_t lanes = s.tmem + ((uint32_t)(w * 32) << 16);
   const int box_shift = __ffs(p.box_rows) - 1;
-  int x0 = 0;                   // tiles of the parts before
-  int shared_sums[2] = {0, 0};  // parts so far, by parity, whose sum took both groups
-  int loads = 0;                // of Q by this warp
-  float next_scale = 0.f;
-  Cursor<D> c(p, s), next(p, s);
-  bool more = next.step();
-  // Whether this warp loads the next part's Q: rows of it lie in its lanes, or all warps do.
-  auto mine = [&] { return !next.small() || w == next.lane0() / 32; };
-  // k = -1: no part yet, the first one's Q alone
-  for (int k = -1; k < 0 || more; ++k) {
-    Row r;
-    if (k >= 0) {
-      c.step();
-      more = next.step();
-      r = row_of<D>(p, s, c, w);
-      r.scale = next_scale;
+  int x = 0;                    // tiles so far, of all parts
+  int turn = 0;                 // of this warp's parts
+  int taken = 0;                // its parts
+  int shared_sums[2] = {0, 0};  // those, by parity, whose sum took both groups
+  Phases<D> phases;             // of s_full
+  uint32_t q_odd = 0;           // by set: parity of the releases waited for
+  int before = 0;               // the set of this warp's last part
+  for (Cursor<D> c(p, s); c.step();) {
+    if (!c.takes(w)) {
+      x += c.n;
+      continue;
     }
-    // The next part's Q goes into lanes that this part does not use while this part is worked on:
-    // the products of the parts before are done with them.
-    const bool early = k >= 0 && more && c.small() && next.small();
-    const bool load = more && mine();
-    for (int pass = 0; pass < 2; ++pass) {
-      if (load && early == (pass == 0)) {
-        const int last = pass == 0 ? k - 1 : k;
-        if (last >= 0 && !warp_wait<D>(p, s, &s.q_free[last & 1], (last >> 1) & 1)) return;
-        if (!load_q_lanes<D>(p, s, next, group, w, lanes, loads++, next_scale)) return;
-      }
-      if (pass == 1) break;
-      for (int j = (x0 ^ group) & 1; j < c.n; j += 2) {
-        const int x = x0 + j;
-        if (!warp_wait<D>(p, s, &s.s_full[x % G::NS], (x / G::NS) & 1)) return;
-        if (!softmax_tile<D, CAP>(p, s, c, r, j, x, w, lanes, box_shift)) return;
-      }
+    const int set = c.set();
+    if (taken > 0) {
+      if (!warp_wait<D>(p, s, &s.q_free[before], q_odd >> before & 1)) return;
+      q_odd ^= 1u << before;
     }
-    if (k < 0) continue;
-    const int last = x0 + c.n - 1;
-    x0 += c.n;
+    before = set;
+    Row r = row_of<D>(p, s, c, w);
+    if (!load_q_lanes<D>(p, s, c, group, w, lanes, taken, r.scale)) return;
+    for (int j = 0; j < c.n; ++j, ++x, ++turn) {
+      const int at = set * G::NS + x % G::NS;
+      const uint32_t parity = phases.next(at, x);
+      if ((x & 1) != group) continue;
+      if (!warp_wait<D>(p, s, &s.s_full[at], parity)) return;
+      if (!softmax_tile<D, CAP>(p, s, c, r, j, x, turn, w, lanes, box_shift)) return;
+    }
+    const int q = taken++ & 1;
+    const bool last = ((x - 1) & 1) == group;
     if (c.n > 1) {
       // the group of the part's last tile adds the other's sum to its own
-      const int q = k & 1;
       float* slot = s.l + q * kPrefixRows + row;
-      if ((last & 1) != group) {
+      if (!last) {
         *slot = r.partial ? -r.l : r.l;
         s.m_last[q * kPrefixRows + row] = r.m;
         __syncwarp();
@@ -1044,7 +1116,7 @@ __device__ void softmax_loop_two(const PrefixParams& p, PrefixSmem<D>& s) {
       const float lx = *slot, mx = s.m_last[q * kPrefixRows + row];
       r.partial |= signbit(lx) != 0;
       r.l = fmaf(fabsf(lx), ex2_ftz(mx - (r.m == -kInf ? 0.f : r.m)), r.l);
-    } else if ((last & 1) != group) {
+    } else if (!last) {
       continue;  // the one tile was the other group's
     }
     store_ml<D>(p, c, r, w);
@@ -1060,7 +1132,13 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   const int row = w * 32 + lane, col = ((int)(threadIdx.x >> 7) - 1 - G::SOFTG) * C;
   const uint32_t lanes = s.tmem + ((uint32_t)(w * 32) << 16);
   int x = 0;
+  Phases<D> phases;  // of p_full and pv_done
   for (Cursor<D> c(p, s); c.step();) {
+    if (!c.takes(w)) {
+      x += c.n;
+      continue;
+    }
+    const int set = c.set() * G::NS, arrivals = c.apart() ? 4 : 1;
     const int first = c.lane0();
     const bool any = w * 32 + 32 > first && w * 32 < first + c.nr;
     const bool on = row >= first && row < first + c.nr;
@@ -1073,7 +1151,7 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
       float f = 0.f;
       if (j < c.n) {
         const int buf = x % G::NS;
-        if (!warp_wait<D>(p, s, &s.p_full[buf], (x / G::NS) & 1)) return;
+        if (!warp_wait<D>(p, s, &s.p_full[set + buf], phases.next(set + buf, x))) return;
         start = j % kGroup == 0 || *reinterpret_cast<const uint32_t*>(s.grew[buf]) != 0;
         if (any) {
           if constexpr (G::FAC_TMEM) {
@@ -1085,14 +1163,14 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.b_free[buf]);
+        if (lane < arrivals) mbar_arrive(&s.b_free[buf]);
         ++x;
       }
       if (!start) continue;
       if (j > 0) {
         // the group before: its last tile is number y
-        const int y = j < c.n ? x - 2 : x - 1;
-        if (!warp_wait<D>(p, s, &s.pv_done[y % G::NS], (y / G::NS) & 1)) return;
+        const int y = j < c.n ? x - 2 : x - 1, at = set + y % G::NS;
+        if (!warp_wait<D>(p, s, &s.pv_done[at], phases.last(at, y))) return;
         if (any) {
           tc5_fence_after();
           const float2 f2 = make_float2(fac, fac);
@@ -1107,7 +1185,7 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
           tc5_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.o_free);
+        if (lane < arrivals) mbar_arrive(&s.o_free);
       }
       fac = f;
     }
@@ -1118,7 +1196,7 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
               ((long long)(blockIdx.x * 2 + (c.k == 0 ? 0 : 1)) * kPrefixRows + row - first) * D;
       } else {
         int b, tok;
-        dst = (c.b < 0 ? p.ws_pre_o : p.out) + (long long)c.out_row(row - first, b, tok) * D;
+        dst = (c.b < 0 ? p.ws_pre_o : p.out) + (long long)c.out_row(p, row - first, b, tok) * D;
       }
 #pragma unroll
       for (int i = 0; i < C; i += 4)
@@ -1166,10 +1244,13 @@ __device__ void qk_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   const uint64_t q = smem_desc(smem_u32(s.q), 16, 1024);  // all 128 rows, whoever's they are
   const uint64_t k0 = smem_desc(smem_u32(s.ring), 16, 1024);
   int x = 0;
+  uint32_t odd = 0;  // by barrier of q_full: parity of the uses so far
   Round buf, ring;
   for (Cursor<D> c(p, s); c.step();) {
-    const int n = uniform(c.n), part = uniform(c.k);
-    if (!warp_wait<D>(p, s, &s.q_full[part & 1], (part >> 1) & 1)) return;
+    const int n = uniform(c.n), set = uniform(c.set());
+    const int part = G::QT ? set : uniform(c.k) & 1;
+    if (!warp_wait<D>(p, s, &s.q_full[part], (G::QT ? odd >> part : c.k >> 1) & 1)) return;
+    odd ^= 1u << part;
     for (int j = 0; j < n; ++j, ++x) {
       int slot = ring.at;
       uint32_t use = ring.odd;
@@ -1205,9 +1286,9 @@ __device__ void qk_loop(const PrefixParams& p, PrefixSmem<D>& s) {
                      i + u > 0);
           }
         }
-        mma_commit(&s.s_full[buf.at]);
+        mma_commit(&s.s_full[set * G::NS + buf.at]);
         mma_commit(&s.empty[slot]);
-        if (j == n - 1) mma_commit(&s.q_free[part & 1]);
+        if (j == n - 1) mma_commit(&s.q_free[part]);
       }
       __syncwarp();
       buf.next(G::NS);
@@ -1225,20 +1306,23 @@ __device__ void pv_loop(const PrefixParams& p, PrefixSmem<D>& s) {
   const uint64_t v0 = smem_desc(smem_u32(s.ring), KT * 128, 1024);
   int x = 0;
   uint32_t groups = 0;
+  Phases<D> phases;  // of p_full
   Round buf, ring;
   for (Cursor<D> c(p, s); c.step();) {
-    const int n = uniform(c.n);
+    const int n = uniform(c.n), set = uniform(c.set() * G::NS);
     for (int j = 0; j < n; ++j, ++x) {
+      const int at_p = set + buf.at;
+      const uint32_t parity = G::QT ? phases.next(at_p, x) : buf.odd;
       int slot = G::RK + ring.at;
       uint32_t use = ring.odd;
       if constexpr (G::QT) {
-        if (!warp_wait2<D>(p, s, &s.full[slot], use, &s.p_full[buf.at], buf.odd)) return;
+        if (!warp_wait2<D>(p, s, &s.full[slot], use, &s.p_full[at_p], parity)) return;
       } else {
         // V last: in a shared ring of three the slot held this tile's K
         const Place<D> at = Place<D>::v(x);
         slot = at.slot;
         use = at.use & 1;
-        if (!warp_wait<D>(p, s, &s.p_full[buf.at], buf.odd)) return;
+        if (!warp_wait<D>(p, s, &s.p_full[at_p], parity)) return;
         if (!warp_wait<D>(p, s, &s.full[slot], use)) return;
       }
       const bool start =
@@ -1255,7 +1339,7 @@ __device__ void pv_loop(const PrefixParams& p, PrefixSmem<D>& s) {
           for (int k = 0; k < KT; k += 16)
             mma_ts(tm, a + k / 32 * 32 + term * 16 + k % 32 / 2, v + k * 8, idesc,
                    term == 0 || k > 0 || !start);
-        mma_commit(&s.pv_done[buf.at]);
+        mma_commit(&s.pv_done[at_p]);
         mma_commit(&s.b_free[buf.at]);
         mma_commit(&s.empty[slot]);
       }
@@ -1279,19 +1363,23 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
       mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < G::NS; ++i) {
-      mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[i], 4);
-      mbar_init(&s.pv_done[i], 1);
       mbar_init(&s.b_free[i], 1 + 4 * G::SUMG);
     }
-    mbar_init(&s.o_free, 4 * G::SUMG);
-    for (int i = 0; i < 2; ++i) {
-      // Q in tensor memory: eight warps load it, the products use it; else one group's four
-      // warps and warp 3 load it, the products use it and the group reads its row_scale
-      mbar_init(&s.q_full[i], G::QT ? 8 : 5);
-      mbar_init(&s.q_free[i], G::QT ? 1 : 5);
-      mbar_init(&s.drain[i], 1);
+    for (int i = 0; i < G::SETS * G::NS; ++i) {
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_full[i], i < (G::SETS - 1) * G::NS ? 1 : 4);
+      mbar_init(&s.pv_done[i], 1);
     }
+    mbar_init(&s.o_free, 4 * G::SUMG);
+    for (int i = 0; i < (G::QT ? G::SETS : 2); ++i) {
+      // Q in tensor memory: two or eight warps load it, the products use it; else one group's
+      // four warps and warp 3 load it, the products use it and the group reads its row_scale
+      mbar_init(&s.q_full[i], !G::QT ? 5 : i < 4 ? 2 : 8);
+      mbar_init(&s.q_free[i], G::QT ? 1 : 5);
+    }
+    mbar_init(&s.drain[0], 1);
+    mbar_init(&s.drain[1], 1);
+    for (int i = 0; i < (G::QT ? kParts : 0); ++i) mbar_init(&s.part_ready[i], 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s.m_ready[i], 1);
       mbar_init(&s.l_ready[0][i], 1);
@@ -1335,9 +1423,9 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
       if constexpr (!G::QT)
         ld.run_both();
       else if (warp == 0)
-        ld.template run_one<G::RK>(false, 0);
+        ld.template run_one<G::RK, Lister<D, true>>(false, 0);
       else
-        ld.template run_one<G::RV>(true, G::RK);
+        ld.template run_one<G::RV, Cursor<D>>(true, G::RK);
       const int bad = __reduce_or_sync(0xffffffffu, ld.flags);
       if (bad && lane == 0 && p.dev_status) atomicOr(p.dev_status, bad);
       if (*(volatile int*)&s.abort) ld.drain();
