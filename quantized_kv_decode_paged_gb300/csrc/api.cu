@@ -691,6 +691,17 @@ int prefix_chunk(int batch, int D) {
   return n > 0 ? (batch + n - 1) / n : 0;
 }
 
+int prefix_own_rows(const da_params* p, int T) {
+  const long long rows = (long long)T * (p->num_q_heads / p->num_kv_heads);
+  return rows < da::kPrefixRows ? (int)rows : da::kPrefixRows;
+}
+
+da::PrefixWs prefix_workspace(const da_params* p, int T, int sms) {
+  return da::prefix_ws(sms, p->head_dim,
+                       (long long)prefix_chunk(p->batch, p->head_dim) * T * p->num_q_heads,
+                       prefix_own_rows(p, T));
+}
+
 // Pool maps of the shared-prefix kernel: the 4-D view of encode_pool_map
 // with boxes of one kv head, min(block_size, tile) keys, and every 128-byte
 // slice of the row when one box is a whole tile (a tile is laid out [slice][key]).
@@ -745,6 +756,7 @@ int prefix_impl(const da_params* p, int T, int prefix_len, const int32_t* prefix
   k.G = p->num_q_heads / p->num_kv_heads;
   k.R1 = T * k.G;
   k.own_tiles = (k.R1 + da::kPrefixRows - 1) / da::kPrefixRows;
+  k.own_rows = prefix_own_rows(p, T);
   k.bs = p->block_size;
   k.log2_bs = ilog2(p->block_size);
   k.max_blocks = p->max_blocks_per_seq;
@@ -763,7 +775,7 @@ int prefix_impl(const da_params* p, int T, int prefix_len, const int32_t* prefix
   k.prefix_table = prefix_table;
   k.dev_status = dev_status;
   const int chunk = prefix_chunk(p->batch, k.D);
-  const da::PrefixWs w = da::prefix_ws(sms, k.D, (long long)chunk * T * p->num_q_heads);
+  const da::PrefixWs w = prefix_workspace(p, T, sms);
   if (!workspace || workspace_bytes < w.total) return DA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   k.ws_plan = reinterpret_cast<int*>(ws + w.plan);
@@ -893,9 +905,7 @@ size_t decode_attn_paged_prefix_workspace_size(const da_params* p, int32_t q_len
   if (check_prefix(p, q_len, prefix_len) != DA_OK) return 0;
   int sms = 0;
   if (device_sms(&sms) != DA_OK) return 0;
-  return da::prefix_ws(sms, p->head_dim,
-                       (long long)prefix_chunk(p->batch, p->head_dim) * q_len * p->num_q_heads)
-      .total;
+  return prefix_workspace(p, q_len, sms).total;
 }
 
 int decode_attn_paged_prefix(const da_params* p, int32_t q_len, int32_t prefix_len,

@@ -48,7 +48,7 @@ cudaError_t launch_split_merge(int rows, int max_splits, int D, const float* o_p
 // prefix_table, the others through block_table.
 constexpr int kPrefixRows = 128;      // rows of a tile (the MMA's M)
 // sequences of a launch: their lengths sit in shared memory beside the tiles
-__host__ __device__ constexpr int prefix_max_batch(int D) { return D >= 256 ? 160 : 256; }
+__host__ __device__ constexpr int prefix_max_batch(int D) { return D >= 256 ? 144 : 256; }
 // keys of a tile
 __host__ __device__ constexpr int prefix_tile_keys(int D) { return D == 64 ? 128 : 64; }
 
@@ -60,6 +60,7 @@ struct alignas(128) PrefixParams {
   int R1;             // rows of a sequence and kv head: T * G
   int row_tiles;      // tiles of the batch's rows of a kv head
   int own_tiles;      // tiles of one sequence's rows of a kv head
+  int own_rows;       // most rows of such a tile
   int bs, log2_bs, max_blocks, num_blocks;
   int prefix_pages;
   int window, causal;
@@ -82,26 +83,38 @@ struct alignas(128) PrefixParams {
   // workspace (PrefixWs).  A state is o (not divided by l), and (m, l): the
   // reference the weights were taken against, base 2, and their sum, negative when
   // some key of its tiles was masked for the row.
-  int* ws_plan;       // tiles of a prefix unit, [B + 1] tiles of own keys before b
-  float2* ws_cut_ml;  // [grid][2][128] of a unit's part
+  int* ws_plan;       // PrefixPlan, then [B + 1] entries of the own list before b's
+  float2* ws_cut_ml;  // [grid][2][128] of a prefix unit's part, [grid][2][own_rows] of an own one's
   float2* ws_pre_ml;  // [B * T * Hq] of the prefix, units that no CTA boundary cuts
   float2* ws_own_ml;  // [B * T * Hq] of own keys; their o goes to out
-  float* ws_cut_o;    // [grid][2][128][D]
+  float* ws_cut_o;    // as ws_cut_ml, [D]
   float* ws_pre_o;    // [B * T * Hq][D]
+};
+
+// How the work is shared out, as prefix_attn_kernel decides it and prefix_merge_kernel reads it.
+struct PrefixPlan {
+  int pn;                     // entries of a prefix unit
+  int width, blocks;          // tiles of rows that CTAs work on side by side; blocks of so many
+  int pre_share, pre_rem;     // of the groups of `width` CTAs: the prefix's Split
+  int members, others;        // CTAs of the groups; those behind them, which take the own
+  int before;                 // list's first entries
+  int first_share, first_rem;  // the Split of these
+  int rest_share, rest_rem;   // and of the others, among the members
 };
 
 struct PrefixWs {
   size_t plan, cut_ml, pre_ml, own_ml, cut_o, pre_o, total;
 };
-inline PrefixWs prefix_ws(int grid, int D, long long rows) {
+inline PrefixWs prefix_ws(int grid, int D, long long rows, int own_rows) {
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   PrefixWs w;
   w.plan = 0;
-  w.cut_ml = al((prefix_max_batch(D) + 2) * 4);
-  w.pre_ml = w.cut_ml + al((size_t)grid * 2 * kPrefixRows * 8);
+  const size_t cut_rows = (size_t)grid * 2 * (kPrefixRows + own_rows);
+  w.cut_ml = al(sizeof(PrefixPlan) + (prefix_max_batch(D) + 1) * 4);
+  w.pre_ml = w.cut_ml + al(cut_rows * 8);
   w.own_ml = w.pre_ml + al((size_t)rows * 8);
   w.cut_o = w.own_ml + al((size_t)rows * 8);
-  w.pre_o = w.cut_o + al((size_t)grid * 2 * kPrefixRows * D * 4);
+  w.pre_o = w.cut_o + al(cut_rows * D * 4);
   w.total = w.pre_o + al((size_t)rows * D * 4);
   return w;
 }

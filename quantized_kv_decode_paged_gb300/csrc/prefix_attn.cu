@@ -54,6 +54,7 @@ namespace da {
 namespace {
 
 constexpr float kInf = INFINITY;
+constexpr int kPlanInts = sizeof(PrefixPlan) / 4;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // cap * tanh(y) in base-2 units.  Below |y| = 1/2 by tanh's Taylor series
@@ -227,7 +228,7 @@ struct alignas(16) PartInfo {
   int r0, nr;
   int base, klo, khi;    // keys [klo, khi) may be seen
   int i0, n;
-  int unit_n;            // tiles of the whole unit
+  int slot;              // its rows' place among the parts of units that are cut, or -1: all of one
 };
 // How many a CTA keeps: a part is read by every warp before the loads are so many ahead of it (they
 // are at most 13 tiles ahead of the sums, and a warp takes at least every fourth part).
@@ -258,8 +259,10 @@ struct PrefixSmem {
   uint8_t grew[G::NS][4];                                // by tile's buffer and warp: a row outgrew
   int warp_sum[16];
   int lo, hi;                                            // prefix keys some row sees
-  int first[4];                                          // where the CTA's run starts: b, h, rt, tile
-  int run;                                               // its length in the list
+  // the CTA's runs of the prefix's list and the own one: where they start (sequence, kv head,
+  // tile of rows or block of them, entry of the unit) and how long they are
+  int first[2][4], run[2];
+  PrefixPlan plan;
   int skip;                                              // test hook: the first copy is left out
   int abort;
   uint32_t tmem;
@@ -268,12 +271,16 @@ static_assert(sizeof(PrefixSmem<64>) <= kSmemLimit && sizeof(PrefixSmem<128>) <=
                   sizeof(PrefixSmem<256>) <= kSmemLimit,
               "shared memory");
 
-// The list of tiles (fewer than 2^31: the host refuses more) is cut into runs
+// A list of tiles (fewer than 2^31: the host refuses more) is cut into runs
 // of share + 1 tiles (the first rem CTAs) and share.
 struct Split {
   int share, rem;
-  __device__ __forceinline__ Split(int total, int ctas)
-      : share((uint32_t)total / (uint32_t)ctas), rem(total - share * ctas) {}
+  __device__ __forceinline__ Split(int share_, int rem_) : share(share_), rem(rem_) {}
+  __device__ __forceinline__ static Split of(int total, int ctas) {
+    const int share = (uint32_t)total / (uint32_t)ctas;
+    return {share, total - share * ctas};
+  }
+  __device__ __forceinline__ int longest() const { return share + (rem > 0); }
   __device__ __forceinline__ int start(int c) const { return c * share + min(c, rem); }
   // The CTA whose run holds tile g.
   __device__ __forceinline__ int cta(int g) const {
@@ -315,7 +322,7 @@ template <int D>
 struct Part : PartInfo {
   using G = PGeo<D>;
   int k = -1;            // number of the part
-  __device__ __forceinline__ bool whole() const { return n == unit_n; }
+  __device__ __forceinline__ bool whole() const { return slot < 0; }
   __device__ __forceinline__ bool small() const { return nr <= kSmallRows<D>; }
   // Q in tensor memory: the rows of a small part lie in the lanes of one warp of each warpgroup,
   // and only these warps take part in it, so that four such parts are under way at once.  Barriers
@@ -342,28 +349,35 @@ struct Part : PartInfo {
   }
 };
 
-// The parts that a CTA's run of the list is made of, one after the other.  A unit's first `extra`
-// entries of the list stand for its fixed cost; runs that hold only such entries of a unit have no
-// part of it.  TELL: each is announced to the warps that read them with a Reader.
+// The parts that a CTA's runs are made of, one after the other, the prefix's first.  A unit's first
+// `extra` entries of its list stand for its fixed cost; runs that hold only such entries of a unit have
+// no part of it.  TELL: each is announced to the warps that read them with a Reader.
 template <int D, bool TELL>
 struct Lister : Part<D> {
   using Part<D>::b, Part<D>::h, Part<D>::r0, Part<D>::nr, Part<D>::base, Part<D>::klo,
-      Part<D>::khi, Part<D>::i0, Part<D>::n, Part<D>::unit_n, Part<D>::k;
+      Part<D>::khi, Part<D>::i0, Part<D>::n, Part<D>::slot, Part<D>::k;
   static constexpr int KT = PGeo<D>::KT;
   const PrefixParams& p;
   PrefixSmem<D>& s;
   int left;              // entries of the run from this part on
   int at, len;           // the part's first entry of its unit, its entries
-  int rt;                // tile of rows
+  int rt;                // tile of rows; prefix: block of them
+  int moved;             // the run's first unit is behind
 
-  __device__ __forceinline__ Lister(const PrefixParams& p_, PrefixSmem<D>& s_)
-      : p(p_), s(s_), left(s_.run), at(s_.first[3]), len(-1) {
-    b = s.first[0];
-    h = s.first[1];
-    rt = s.first[2];
+  __device__ __forceinline__ Lister(const PrefixParams& p_, PrefixSmem<D>& s_) : p(p_), s(s_) {
+    enter(0);
     n = 0;
   }
-  // On to the run's first or next part; false, and n = 0, behind the last one.
+  __device__ __forceinline__ void enter(int list) {
+    b = s.first[list][0];
+    h = s.first[list][1];
+    rt = s.first[list][2];
+    at = s.first[list][3];
+    left = s.run[list];
+    len = -1;
+    moved = 0;
+  }
+  // On to the first or next part; false, and n = 0, behind the last one.
   __device__ __forceinline__ bool step() {
     if (k >= 0 && n == 0) return false;
     n = 0;
@@ -371,19 +385,28 @@ struct Lister : Part<D> {
       if (len >= 0) {
         left -= len;
         at = 0;
-        if (left > 0 && ++rt == (b < 0 ? p.row_tiles : p.own_tiles)) {
+        moved = 1;
+        if (left > 0 && ++rt == (b < 0 ? s.plan.blocks : p.own_tiles)) {
           rt = 0;
           if (++h == p.Hkv) {
             h = 0;
-            b = max(b, -1) + 1;
-            while (s.cum[b + 1] == s.cum[b]) ++b;
+            if (b >= 0) {
+              ++b;
+              while (s.cum[b + 1] == s.cum[b]) ++b;
+            }
           }
         }
       }
+      if (left <= 0 && b < 0) enter(1);
       if (left <= 0) break;
-      int extra = kOwnExtra<D>;
+      int extra = kOwnExtra<D>, unit_n, rows = p.R1;
+      slot = (blockIdx.x * 2 + moved) * p.own_rows + p.grid * (2 * kPrefixRows);
+      r0 = rt * kPrefixRows;
       if (b < 0) {
         extra = kPrefixExtra<D>;
+        rows = p.B * p.R1;
+        r0 = (rt * s.plan.width + (int)blockIdx.x % s.plan.width) * kPrefixRows;
+        slot = (blockIdx.x * 2 + moved) * kPrefixRows;
         klo = s.lo;
         khi = s.hi;
         base = klo / KT * KT;
@@ -397,12 +420,12 @@ struct Lister : Part<D> {
       }
       len = min(unit_n + extra - at, left);
       i0 = max(0, at - extra);
-      n = at + len - extra - i0;
+      nr = min(kPrefixRows, rows - r0);
+      n = nr > 0 ? at + len - extra - i0 : 0;  // the last block may have fewer tiles
+      if (n == unit_n) slot = -1;
     } while (n <= 0);
     n = max(n, 0);
     ++k;
-    r0 = rt * kPrefixRows;
-    nr = min(kPrefixRows, (b < 0 ? p.B * p.R1 : p.R1) - r0);
     if (TELL && (threadIdx.x & 31) == 0) {
       s.parts[k % kParts] = *this;
       mbar_arrive(&s.part_ready[k % kParts]);
@@ -469,24 +492,74 @@ __device__ int make_plan(const PrefixParams& p, PrefixSmem<D>& s) {
   return flags;
 }
 
-// Where the run that starts at entry g of the list begins: sequence (-1: the
-// prefix), kv head, tile of rows, entry of the unit.  pn: entries of a prefix unit, tp: of the
-// whole prefix.
+// Shares the work out.  All units' entries, `total` with the own ones, make `grid` runs of equal length.
+// CTAs that work on the same keys for different tiles of rows should do so at the same
+// time, or each reads them from HBM: `width` neighbours form a group that goes through a
+// list of (kv head, block of `width` tiles of rows) together, a tile of rows each.  The widest
+// groups are taken that cost no more than 1/24 in balance (they leave grid % width CTAs without
+// prefix, and places of the last block empty); the own list fills the runs up.  128 sequences of 64 heads (8 tiles of rows) over 32,768 shared
+// keys read @@ MB of HBM for @@ with single CTAs, and take @@ us for @@.
+// All threads call it, one a width.
 template <int D>
-__device__ void find_first(const PrefixParams& p, PrefixSmem<D>& s, int g, int pn, int tp) {
-  int b, each, u, tiles;
-  if (g < tp) {
-    b = -1;
-    each = pn;
-    tiles = p.row_tiles;
-    u = (uint32_t)g / (uint32_t)pn;
-    g -= u * pn;
-  } else {
-    g -= tp;
-    const int units1 = p.Hkv * p.own_tiles;
+__device__ void share_out(const PrefixParams& p, PrefixSmem<D>& s) {
+  const int tid = threadIdx.x;
+  const int pn = s.hi > s.lo ? (s.hi + PGeo<D>::KT - 1) / PGeo<D>::KT - s.lo / PGeo<D>::KT +
+                                   kPrefixExtra<D>
+                             : 0;
+  const int units1 = p.Hkv * p.own_tiles, own = s.cum[p.B] * units1;
+  // entries of a run where tiles of rows are worked on `width` at a time
+  auto mean = [&](int width, int blocks) {
+    return (int)(((uint32_t)pn * (p.Hkv * blocks) * width + own + p.grid - 1) / (uint32_t)p.grid);
+  };
+  if (tid < (pn ? min(p.row_tiles, p.grid) : 0)) {
+    const int width = tid + 1, blocks = (uint32_t)(p.row_tiles + tid) / (uint32_t)width;
+    const Split pre = Split::of(pn * (p.Hkv * blocks), (uint32_t)p.grid / (uint32_t)width);
+    const int longest = max(pre.longest(), mean(width, blocks));
+    if ((long long)longest * 24 <= (long long)mean(1, p.row_tiles) * 25)
+      atomicMax(&s.plan.width, width);
+  }
+  __syncthreads();
+  if (tid != 0 && tid != 32) return;
+  const int c = blockIdx.x, width = s.plan.width;
+  const int blocks = (uint32_t)(p.row_tiles + width - 1) / (uint32_t)width;
+  const int tp = pn * (p.Hkv * blocks), each = mean(width, blocks);
+  // as few groups as the mean allows: a run that turns to own keys pays for its units twice
+  int groups = (uint32_t)p.grid / (uint32_t)width;
+  if (pn) {
+    int few = max(1, (uint32_t)tp / (uint32_t)each);
+    if ((long long)Split::of(tp, few).longest() * 24 > (long long)each * 25) ++few;
+    groups = min(groups, few);
+  }
+  const Split pre = Split::of(tp, groups);
+  const int members = groups * width, others = p.grid - members;
+  // all own entries where that fits (a few for each member would cut units for little)
+  const int room = others * each, before = (long long)own * 24 <= (long long)room * 25 ? own : room;
+  const Split front = Split::of(before, max(others, 1)), rest = Split::of(own - before, members);
+  if (tid == 0) {
+    s.plan = {pn,     width,  blocks,      pre.share, pre.rem,    members,
+              others, before, front.share, front.rem, rest.share, rest.rem};
+    const int group = (uint32_t)c / (uint32_t)width, g = pre.start(group);
+    s.run[0] = group < groups ? pre.share + (group < pre.rem) : 0;
+    s.first[0][0] = -1;
+    if (s.run[0] > 0) {
+      const int u = (uint32_t)g / (uint32_t)pn;
+      s.first[0][1] = (uint32_t)u / (uint32_t)blocks;
+      s.first[0][2] = u - s.first[0][1] * blocks;
+      s.first[0][3] = g - u * pn;
+    }
+    // test hook: the first tile of the first CTA that has one
+    if (pn > 0)
+      s.skip = p.test_skip_arm && c == group * width && g <= kPrefixExtra<D> &&
+               kPrefixExtra<D> < g + s.run[0];
+    return;
+  }
+  const int o = c < members ? c : c - members;
+  int g = c < members ? before + rest.start(o) : front.start(o);
+  s.run[1] = c < members ? rest.share + (o < rest.rem) : front.share + (o < front.rem);
+  if (pn == 0) s.skip = p.test_skip_arm && g <= kOwnExtra<D> && kOwnExtra<D> < g + s.run[1];
+  if (s.run[1] > 0) {
     const int x = (uint32_t)g / (uint32_t)units1;  // sequence b holds it: cum[b] <= x < cum[b + 1]
-    int hi = p.B;
-    b = 0;
+    int b = 0, hi = p.B;
     while (hi - b > 1) {
       const int mid = (b + hi) >> 1;
       if (s.cum[mid] <= x)
@@ -494,16 +567,13 @@ __device__ void find_first(const PrefixParams& p, PrefixSmem<D>& s, int g, int p
       else
         hi = mid;
     }
-    each = s.cum[b + 1] - s.cum[b];
-    tiles = p.own_tiles;
     g -= s.cum[b] * units1;
-    u = (uint32_t)g / (uint32_t)each;
-    g -= u * each;
+    const int u = (uint32_t)g / (uint32_t)(s.cum[b + 1] - s.cum[b]);
+    s.first[1][0] = b;
+    s.first[1][1] = (uint32_t)u / (uint32_t)p.own_tiles;
+    s.first[1][2] = u - s.first[1][1] * p.own_tiles;
+    s.first[1][3] = g - u * (s.cum[b + 1] - s.cum[b]);
   }
-  s.first[0] = b;
-  s.first[1] = u / tiles;
-  s.first[2] = u % tiles;
-  s.first[3] = g;
 }
 
 // Parity of the phases of a tile's barriers (by set and buffer) as one warp comes to them: with
@@ -1023,8 +1093,7 @@ __device__ __forceinline__ void store_ml(const PrefixParams& p, const Part<D>& c
   if (!r.on) return;
   float2* dst;
   if (!c.whole())
-    dst = p.ws_cut_ml + (blockIdx.x * 2 + (c.k == 0 ? 0 : 1)) * kPrefixRows + w * 32 +
-          (int)(threadIdx.x & 31) - c.lane0();
+    dst = p.ws_cut_ml + c.slot + w * 32 + (int)(threadIdx.x & 31) - c.lane0();
   else
     dst = (c.b < 0 ? p.ws_pre_ml : p.ws_own_ml) + r.place;
   *dst = make_float2(r.m - kShift, r.partial ? -r.l : r.l);
@@ -1192,8 +1261,7 @@ __device__ void sum_loop(const PrefixParams& p, PrefixSmem<D>& s) {
     if (on) {
       float* dst;
       if (!c.whole()) {
-        dst = p.ws_cut_o +
-              ((long long)(blockIdx.x * 2 + (c.k == 0 ? 0 : 1)) * kPrefixRows + row - first) * D;
+        dst = p.ws_cut_o + (long long)(c.slot + row - first) * D;
       } else {
         int b, tok;
         dst = (c.b < 0 ? p.ws_pre_o : p.out) + (long long)c.out_row(p, row - first, b, tok) * D;
@@ -1389,6 +1457,7 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
     fence_mbarrier_init();
     s.lo = 0x7fffffff;
     s.hi = 0;
+    s.plan.width = 1;
     s.abort = 0;
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
@@ -1400,22 +1469,12 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
   tc5_fence_after();
   const int flags = make_plan<D>(p, s);
   if (blockIdx.x == 0 && flags && p.dev_status) atomicOr(p.dev_status, flags);
-  if (tid == 0) {
-    const int pn =
-        s.hi > s.lo ? (s.hi + G::KT - 1) / G::KT - s.lo / G::KT + kPrefixExtra<D> : 0;
-    const int tp = pn * (p.Hkv * p.row_tiles);
-    const Split sp(tp + s.cum[p.B] * (p.Hkv * p.own_tiles), p.grid);
-    s.run = sp.share + ((int)blockIdx.x < sp.rem);
-    const int g = sp.start(blockIdx.x);
-    if (s.run > 0) find_first<D>(p, s, g, pn, tp);
-    // test hook: in the first CTA that has a tile
-    const int tile = pn ? kPrefixExtra<D> : kOwnExtra<D>;
-    s.skip = p.test_skip_arm && g <= tile && tile < g + s.run;
-    if (blockIdx.x == 0) p.ws_plan[0] = pn;
-  }
-  if (blockIdx.x == 0)
-    for (int i = tid; i <= p.B; i += G::THREADS) p.ws_plan[1 + i] = s.cum[i];
+  share_out<D>(p, s);
   __syncthreads();
+  if (blockIdx.x == 0) {
+    if (tid == 0) *reinterpret_cast<PrefixPlan*>(p.ws_plan) = s.plan;
+    for (int i = tid; i <= p.B; i += G::THREADS) p.ws_plan[kPlanInts + i] = s.cum[i];
+  }
   if (warp < 4) {
     setmaxnreg_dec<G::REG_LOAD>();
     if (warp == 0 || (warp == 3 && G::QT)) {
@@ -1490,18 +1549,23 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int b = bt / p.T, tok = bt - b * p.T;
   const int r1 = tok * p.G + hq - h * p.G;
   const int rb = b * p.R1 + r1;
-  const int pn = p.ws_plan[0];
-  const int* cum = p.ws_plan + 1;
-  const int units1 = p.Hkv * p.own_tiles;
-  const int tp = pn * (p.Hkv * p.row_tiles);
-  const Split sp(tp + cum[p.B] * units1, p.grid);
-  // the CTAs that hold the row's prefix unit, then its own one
-  const int n0 = pn, n1 = cum[b + 1] - cum[b];
-  const int g0 = (h * p.row_tiles + rb / kPrefixRows) * n0;
-  const int g1 = tp + cum[b] * units1 + (h * p.own_tiles + r1 / kPrefixRows) * n1;
-  const int c0 = n0 ? sp.cta(g0 + kPrefixExtra<D>) : 0, c1 = n1 ? sp.cta(g1 + kOwnExtra<D>) : 0;
-  const int s0 = n0 ? sp.cta(g0 + n0 - 1) - c0 + 1 : 0;  // its states
-  const int s1 = n1 ? sp.cta(g1 + n1 - 1) - c1 + 1 : 0;
+  const PrefixPlan plan = *reinterpret_cast<const PrefixPlan*>(p.ws_plan);
+  const int* cum = p.ws_plan + kPlanInts;
+  const Split pre(plan.pre_share, plan.pre_rem), front(plan.first_share, plan.first_rem),
+              rest(plan.rest_share, plan.rest_rem);
+  // the groups of CTAs that hold the row's prefix unit
+  const int n0 = plan.pn, rt = rb / kPrefixRows, block = (uint32_t)rt / (uint32_t)plan.width;
+  const int g0 = (h * plan.blocks + block) * n0;
+  const int c0 = n0 ? pre.cta(g0 + kPrefixExtra<D>) : 0;
+  const int s0 = n0 ? pre.cta(g0 + n0 - 1) - c0 + 1 : 0;  // its states
+  // the CTAs that hold its own unit
+  auto own_at = [&](int g) {  // place among them of the one that holds entry g
+    return g < plan.before ? front.cta(g) : plan.others + rest.cta(g - plan.before);
+  };
+  const int n1 = cum[b + 1] - cum[b];
+  const int g1 = cum[b] * (p.Hkv * p.own_tiles) + (h * p.own_tiles + r1 / kPrefixRows) * n1;
+  const int c1 = n1 ? own_at(g1 + kOwnExtra<D>) : 0;
+  const int s1 = n1 ? own_at(g1 + n1 - 1) - c1 + 1 : 0;
   float M = -kInf, L = 0.f, o[V];
   bool partial = false;
 #pragma unroll
@@ -1518,9 +1582,21 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         ml = (own ? p.ws_own_ml : p.ws_pre_ml) + row;
         src = (own ? p.out : p.ws_pre_o) + (long long)row * D;
       } else {
-        const int c = first + jj;
-        const int slot = 2 * c + (jj == 0 && sp.start(c) < (own ? g1 : g0) ? 1 : 0);
-        const long long at = (long long)slot * kPrefixRows + (own ? r1 : rb) % kPrefixRows;
+        // in the first CTA's second place if its run began before the unit
+        int c = first + jj;
+        long long at;
+        if (own) {
+          const int start =
+              c < plan.others ? front.start(c) : plan.before + rest.start(c - plan.others);
+          c = c < plan.others ? plan.members + c : c - plan.others;
+          at = (long long)p.grid * (2 * kPrefixRows) +
+               (2 * c + (jj == 0 && start < g1 ? 1 : 0)) * p.own_rows + r1 % kPrefixRows;
+        } else {
+          at = (long long)(2 * (c * plan.width + rt - block * plan.width) +
+                           (jj == 0 && pre.start(c) < g0 ? 1 : 0)) *
+                   kPrefixRows +
+               rb % kPrefixRows;
+        }
         ml = p.ws_cut_ml + at;
         src = p.ws_cut_o + at * D;
       }
