@@ -433,8 +433,12 @@ int decode_attn_append_paged_rope(const da_params* p, const da_rope_params* r, i
  * decode_attn_paged_prefix_workspace_size(p, q_len, prefix_len) bytes, 256-byte
  * aligned, of any content; calls that overlap on the GPU must not share it.
  * Everything else as for decode_attn_paged.  DA_ERR_UNSUPPORTED also where a
- * launch's work would not count in 31 bits: q_len * num_q_heads * 256 rows, or
- * the table's keys / 128 (64 for head_dim 256) * num_kv_heads * 256 tiles.
+ * launch's work would not count in 31 bits: rows, q_len * num_q_heads * 256
+ * (144 for head_dim 256), or entries of its list of tiles,
+ *   (max_blocks_per_seq * block_size / tile + 64) * num_kv_heads * 256 *
+ *   (ceil(q_len * num_q_heads / num_kv_heads / 128) + 1),
+ * tile 64 keys (128 for head_dim 64), again 144 in place of 256; or keys,
+ * max_blocks_per_seq * block_size.
  */
 size_t decode_attn_paged_prefix_workspace_size(const da_params* p, int32_t q_len,
                                                int32_t prefix_len);

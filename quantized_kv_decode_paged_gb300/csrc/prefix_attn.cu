@@ -10,9 +10,9 @@
 // heads) that share keys are cut into tiles of 128 rows, the keys into tiles
 // of 64 (128 for D = 64).  A prefix unit is a (kv head, tile of the batch's
 // rows) over the prefix, an own unit a (sequence, kv head, tile of its rows)
-// over its own keys.  All units' key tiles, and entries that stand for a unit's
-// fixed cost, form one list; every CTA takes an equal run of it (tiles cost about the same:
-// the MMA's M is 128 whether a tile has 4 rows or 128).  A unit that lies in one CTA leaves its state in
+// over its own keys.  A unit's key tiles, and entries that stand for its fixed cost, form a run of
+// a list; every CTA takes an equal share of entries (tiles cost about the same: the MMA's M is 128
+// whether a tile has 4 rows or 128).  A unit that lies in one CTA leaves its state in
 // the row's place; the parts of a unit that CTA boundaries cut go to the
 // CTAs' slots.  prefix_merge_kernel joins a row's states:
 // M = max m_s, w_s = 2^(m_s - M), out = sum w_s o_s / sum w_s l_s.
@@ -30,12 +30,19 @@
 // registers.
 //
 // Warps.  0: TMA of K pages into a ring of tiles, 3: of V pages (D = 256: 0
-// both, 3 the Q of units with few rows).  1 and 2: one thread
-// issues the scores' products, one the values' (S and P share three buffers, so scores run
+// both, 3 the Q of units with few rows).  1 issues the scores' products, 2
+// the values' (S and P share three or four buffers, so scores run
 // ahead while the softmax of a tile runs).  Then two warpgroups (D = 256: one) of softmax, a
 // thread a row: scores to weights, running maximum and sum; they take turns at the tiles and hand
 // the maximum on, and convert Q.  Then one (D = 256: two, 128 columns each) of sums, a thread a
-// row: acc = acc * 2^(m_old - m_new) + O_tile, and the state's store.
+// row: acc = acc * 2^(m_old - m_new) + O, and the state's store.  A unit of few rows lies in the
+// lanes of one warp of each of these groups, and four such units run at once.
+//
+// Measured (GB300), 128 sequences x 64 heads, 8 kv heads, D = 128, 32,768 shared and 64 to 2048 own
+// keys: 255 us, 235 of them in prefix_attn_kernel, which issues 352 GFLOP of products (140 before
+// the second terms and the empty rows of own tiles): 1.5 PFLOP/s, 79% of the tensor cores' measured
+// rate, at the card's power limit; 452 MB read, 1.9 TB/s.  A tile takes 0.8 us for 0.55 of products:
+// the softmax's and the sums' traffic with tensor memory; an own unit's chain of latencies 2 to 3 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -205,15 +212,14 @@ struct PGeo {
 template <int D>
 constexpr int kSmallRows = PGeo<D>::QT ? 32 : 64;
 // Units cost more than their tiles: Q, the first tile's latencies, the state's store.  The list
-// counts so many tiles for it.  D = 128, without it (0, 0) and with (12, 2): 376 and 259 us for 128
-// sequences of 64 heads over 32,768 shared and 64 to 2048 own keys, 61 and 45 for 24 x 4 tokens of
-// 32 heads over 8192 and 64 to 1400, 419 and 79 for the first over 16 shared keys.  Own units of one
-// tile want 2, long ones 1 (1 alone: 225 for 210 us with 1 or 2 own keys, 76 for 79 with 64 to 2048).
-// D = 256: 170 and 140 us for 64 sequences of 16 heads, a window of 4096 and 256 to 2048 own keys.
+// counts so many tiles for it.  D = 128, 32 to 64 heads and 64 to 2048 own keys, without it (0, 0) and
+// with (10, 1): 376 and 255 us over 32,768 shared keys, 61 and 45 over 8192, 419 and 84 over 16.  From
+// there it is flat: (8, 2) took 253, 47, 82, (14, 1) 251, 47, 81, (16, 3) 267, 47, 86.  D = 256: 170
+// and 140 us for 64 sequences of 16 heads, a window of 4096 and 256 to 2048 own keys.
 template <int D>
-constexpr int kPrefixExtra = D >= 256 ? 24 : 12;
+constexpr int kPrefixExtra = D >= 256 ? 24 : 10;
 template <int D>
-constexpr int kOwnExtra = 2;
+constexpr int kOwnExtra = D >= 256 ? 2 : 1;
 // The maximum that a tile's weights are taken against moves at the first tile of a group of
 // kGroup, whose products add up in tensor memory before the sum warps take them, and where a row
 // outgrows it by 2^kGrow (that tile then starts a group).  Weights are kept times 2^kShift:
@@ -222,7 +228,7 @@ constexpr int kGroup = 2;
 constexpr float kGrow = 7.f;
 constexpr float kShift = 8.f;
 
-// A part of a unit (Part) as the list's run names it.
+// A part of a unit (Part) as the CTA's run names it.
 struct alignas(16) PartInfo {
   int b, h;              // b < 0: prefix
   int r0, nr;
@@ -492,13 +498,15 @@ __device__ int make_plan(const PrefixParams& p, PrefixSmem<D>& s) {
   return flags;
 }
 
-// Shares the work out.  All units' entries, `total` with the own ones, make `grid` runs of equal length.
+// Shares the work out: runs of equal length, the prefix's entries and the own ones together.
 // CTAs that work on the same keys for different tiles of rows should do so at the same
 // time, or each reads them from HBM: `width` neighbours form a group that goes through a
 // list of (kv head, block of `width` tiles of rows) together, a tile of rows each.  The widest
-// groups are taken that cost no more than 1/24 in balance (they leave grid % width CTAs without
-// prefix, and places of the last block empty); the own list fills the runs up.  128 sequences of 64 heads (8 tiles of rows) over 32,768 shared
-// keys read @@ MB of HBM for @@ with single CTAs, and take @@ us for @@.
+// groups are taken that cost no more than 1/24 in balance (they leave places of the last block
+// empty and grid % width CTAs out).  The CTAs behind the groups take the own list, the groups' what
+// is left of it.  128 sequences of 64 heads, 8 tiles of rows, over 32,768 shared keys: single
+// CTAs read 787 MB of HBM in 235 us, groups 151 in 203; with 64 to 2048 own keys besides 862 MB and 262
+// us, 452 and 252.
 // All threads call it, one a width.
 template <int D>
 __device__ void share_out(const PrefixParams& p, PrefixSmem<D>& s) {

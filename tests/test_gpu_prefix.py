@@ -502,3 +502,82 @@ def test_a_wait_that_runs_out_is_reported(D):
         finally:
             lib.decode_attn_testing_skip_first_arm(0)
     c.check()
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,D", [(130, 1, 8, 4, 128), (65, 1, 16, 2, 64), (90, 2, 14, 2, 128),
+                                          (60, 3, 8, 1, 128), (140, 4, 8, 2, 64), (100, 1, 16, 8, 256),
+                                          (144, 2, 12, 2, 256), (130, 1, 64, 64, 64)])
+@pytest.mark.parametrize("prefix,most", [(80, 2), (600, 2), (600, 400), (3000, 60)])
+def test_row_tiles_side_by_side(B, T, Hq, Hkv, D, prefix, most):
+    """2 to 18 tiles of the batch's rows, with next to no own keys and with as
+    many as the prefix has: groups of several widths, that leave CTAs out or places of their
+    last block empty, and own keys that fill runs up."""
+    r = np.random.default_rng(B + prefix)
+    lens = prefix + T - 1 + r.integers(1, most, B)
+    lens[::7] = prefix // 2  # shorter than the prefix
+    Case(50, B, Hq, Hkv, D, 16, prefix, lens, T=T).check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_one_sequence_holds_all_own_keys(D):
+    lens = np.full(70, 320)
+    lens[69] = 9000
+    Case(51, 70, 8, 2, D, 16, 320, lens).check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_on_16_byte_boundaries(D):
+    """q and out 16 bytes past a 32-byte boundary: the same bits."""
+    import torch
+    c = Case(52, 9, 16, 2, D, 16, 512, 512 + np.arange(9) * 31 + 1)
+    want = c.run()
+    c.check(want)
+    args = [_t(x) for x in (c.k, c.v, c.table, c.lens)]
+    buf = torch.zeros(2 * c.q.size + 64, device="cuda")
+    q = buf[4:4 + c.q.size].view(c.q.shape)
+    out = buf[c.q.size + 12:2 * c.q.size + 12].view(c.q.shape)
+    assert q.data_ptr() % 32 == 16 and out.data_ptr() % 32 == 16
+    q.copy_(_t(c.q))
+    _, lse = qk.decode_attn_paged_prefix(q, *args, 512, _t(c.prefix_table), out=out)
+    assert np.array_equal(out.cpu().numpy(), want[0]) and np.array_equal(lse.cpu().numpy(), want[1])
+
+
+def test_two_threads_on_streams_of_their_own():
+    import threading
+    import torch
+    cases = [Case(60 + i, 20 + i, 8, 2, 128, 16, 1024, 1024 + np.arange(20 + i) * 13 + 1)
+             for i in range(2)]
+    got = [None, None]
+
+    def work(i):
+        c, s = cases[i], torch.cuda.Stream()
+        args = [_t(x) for x in (c.q, c.k, c.v, c.table, c.lens)]
+        t = _t(c.prefix_table)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                out, lse = qk.decode_attn_paged_prefix(*args, 1024, t)
+        s.synchronize()
+        got[i] = (out.cpu().numpy(), lse.cpu().numpy(), 0)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for c, g in zip(cases, got):
+        c.check(g)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_wait_that_runs_out_among_own_keys(D):
+    """As above, with no prefix."""
+    lib = qk.load_library()
+    c = Case(53, 2, 8, 8, D, 64, 0, [16385, 9000])
+    with qk.tuning(wait_limit_ms=50):
+        lib.decode_attn_testing_skip_first_arm(1)
+        try:
+            assert c.run()[2] == qk.DEV_TIMEOUT
+        finally:
+            lib.decode_attn_testing_skip_first_arm(0)
+    c.check()

@@ -329,3 +329,26 @@ def test_append_side_stream_and_graph_replay():
         _close(tk, K, bk, f"k replay {i}")
         _close(tv, V, bv, f"v replay {i}")
         _close(q[:5], y, b, f"q replay {i}")
+
+
+@pytest.mark.parametrize("dtype", ["float16", "float32"])
+def test_outputs_on_16_byte_boundaries(dtype):
+    """q_out 16 bytes past a 32-byte boundary, from both entry points: the same bits."""
+    import torch
+    rng = np.random.default_rng(17)
+    N, Hq, H, D = 37, 6, 2, 128
+    f, fh = _freqs(D)
+    pos = _t(rng.integers(0, 4096, N).astype(np.int32))
+    q, k, v = (_t(rng.standard_normal((N, h, D)).astype(np.float32), dtype) for h in (Hq, H, H))
+    want, _ = qk.decode_attn_qk_norm_rope(q, k, pos, f)
+    buf = torch.zeros(N * Hq * D + 8, device="cuda")
+    out = buf[4:-4].view(N, Hq, D)
+    assert out.data_ptr() % 32 == 16
+    qk.decode_attn_qk_norm_rope(q, k, pos, f, q_out=out)
+    assert torch.equal(out, want)
+    table = torch.arange(N, dtype=torch.int32, device="cuda").repeat_interleave(1)[:, None].repeat(1, 256)
+    kp, vp = (torch.zeros((N, 16, H, D), dtype=torch.float16, device="cuda") for _ in range(2))
+    out.zero_()
+    qk.decode_attn_append_paged_rope(k, v, pos, table, kp, vp, f, q=q, norm=True, q_out=out)
+    assert torch.equal(out, want)
+    assert (buf[:4] == 0).all() and (buf[-4:] == 0).all()
