@@ -762,7 +762,12 @@ class _on_device:
 _NO_GUARD = contextlib.nullcontext()
 
 
-def _device_guard(torch, dev):
+def _call_guard(torch, dev, stream):
+    """The tensor's device, and the call's stream where it is named: what the call
+    allocates then belongs to that stream, and no memory is taken that another
+    stream's pending work still uses."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
     return _NO_GUARD if torch.cuda.current_device() == dev.index else _on_device(dev)
 
 
@@ -893,7 +898,7 @@ def decode_attn_qk_norm_rope(q, k, positions, freqs, *, norm=True, q_weight=None
             if t.shape != shape:
                 raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     _check_cuda("q and k", x)
-    with _device_guard(torch, dev):
+    with _call_guard(torch, dev, stream):
         if q is not None and q_out is None:
             q_out = torch.empty((N, Hq, D), dtype=torch.float32, device=dev)
         if k is not None and k_out is None:
@@ -956,7 +961,7 @@ def decode_attn_append_paged_rope(k_new, v_new, positions, block_table, k_pool, 
         _req(dev_status, "dev_status", i32, dev)
     _check_cuda("k_new", k_new)
     p = DaParams(block_table.shape[0], Hq, Hkv, D, bs, block_table.shape[1], NB, 0, 0.0, 0.0, 0, 1)
-    with _device_guard(torch, dev):
+    with _call_guard(torch, dev, stream):
         if q is not None and q_out is None:
             q_out = torch.empty((N, Hq, D), dtype=torch.float32, device=dev)
         if N == 0:
@@ -982,8 +987,8 @@ def decode_attn_paged_prefix_workspace_size(params: DaParams, q_len: int, prefix
 _prefix_ws: dict = {}  # (device, stream) -> workspace
 
 
-def _prefix_workspace(torch, dev, stream, raw, nbytes):
-    """The stream's workspace, grown as needed.  Calls of one stream follow one
+def _prefix_workspace(torch, dev, raw, nbytes):
+    """The current stream's workspace, grown as needed.  Calls of one stream follow one
     another; a call that is being captured gets its own, which lives in its
     graph's memory: graphs may be replayed side by side."""
     if torch.cuda.is_current_stream_capturing():
@@ -992,8 +997,6 @@ def _prefix_workspace(torch, dev, stream, raw, nbytes):
     ws = _prefix_ws.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            ws.record_stream(stream)
         _prefix_ws[key] = ws
     return ws
 
@@ -1064,7 +1067,7 @@ def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_le
     params = DaParams(B, Hq, Hkv, D, bs, columns, NB, max_seq_len, scale, softcap, sliding_window,
                       1 if causal else 0)
     ref = ctypes.byref(params)
-    with _device_guard(torch, dev):
+    with _call_guard(torch, dev, stream):
         if out is None:
             out = torch.empty(shape, dtype=torch.float32, device=dev)
         if lse is None:
@@ -1074,7 +1077,7 @@ def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_le
         raw = _raw_stream(torch, dev, stream)
         if auto:
             nbytes = lib.decode_attn_paged_prefix_workspace_size(ref, T, prefix_len)
-            workspace = _prefix_workspace(torch, dev, stream, raw, nbytes)
+            workspace = _prefix_workspace(torch, dev, raw, nbytes)
         st = lib.decode_attn_paged_prefix(
             ref, T, prefix_len, prefix_table.data_ptr(), q.data_ptr(), k_pool.data_ptr(),
             v_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), _ptr(q_pos),

@@ -581,3 +581,21 @@ def test_a_wait_that_runs_out_among_own_keys(D):
         finally:
             lib.decode_attn_testing_skip_first_arm(0)
     c.check()
+
+
+def test_a_named_stream_takes_no_memory_in_use():
+    """What a call with a stream of its own allocates is not memory whose last
+    reader, on the current stream, is still to come."""
+    import torch
+    c = Case(54, 64, 8, 2, 128, 16, 256, 256 + np.arange(64) + 1)
+    args = [_t(x) for x in (c.q, c.k, c.v, c.table, c.lens)]
+    pt, side = _t(c.prefix_table), torch.cuda.Stream()
+    x = torch.full(c.q.shape, 7.0, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    y = x.clone()
+    del x
+    out, lse = qk.decode_attn_paged_prefix(*args, 256, pt, stream=side)
+    torch.cuda.synchronize()
+    assert (y == 7).all()
+    c.check((out.cpu().numpy(), lse.cpu().numpy(), 0))

@@ -352,3 +352,28 @@ def test_outputs_on_16_byte_boundaries(dtype):
     qk.decode_attn_append_paged_rope(k, v, pos, table, kp, vp, f, q=q, norm=True, q_out=out)
     assert torch.equal(out, want)
     assert (buf[:4] == 0).all() and (buf[-4:] == 0).all()
+
+
+def test_a_named_stream_takes_no_memory_in_use():
+    """What a call with a stream of its own allocates is not memory whose last
+    reader, on the current stream, is still to come."""
+    import torch
+    N, H, D = 64, 8, 128
+    f, _ = _freqs(D)
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    q, side = torch.ones((N, H, D), device="cuda"), torch.cuda.Stream()
+    kp, vp = (torch.zeros((N, 16, H, D), dtype=torch.float16, device="cuda") for _ in range(2))
+    table = torch.arange(N, dtype=torch.int32, device="cuda")[:, None].repeat(1, 8)
+    want, _ = qk.decode_attn_qk_norm_rope(q, None, pos, f)
+    for call in (lambda: qk.decode_attn_qk_norm_rope(q, None, pos, f, stream=side)[0],
+                 lambda: qk.decode_attn_append_paged_rope(q, q, pos, table, kp, vp, f, q=q,
+                                                          norm=True, stream=side)):
+        x = torch.full((N, H, D), 7.0, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)
+        y = x.clone()
+        del x
+        out = call()
+        torch.cuda.synchronize()
+        assert (y == 7).all()
+        assert torch.equal(out, want)
