@@ -745,20 +745,6 @@ def _check_cuda(name, t):
         raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
 
 
-class _on_device:
-    """Makes ``dev`` the current CUDA device for a call."""
-
-    def __init__(self, dev):
-        self.guard = _torch().cuda.device(dev)
-
-    def __enter__(self):
-        self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        self.guard.__exit__(*exc)
-        return False
-
-
 _NO_GUARD = contextlib.nullcontext()
 
 
@@ -768,7 +754,7 @@ def _call_guard(torch, dev, stream):
     stream's pending work still uses."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    return _NO_GUARD if torch.cuda.current_device() == dev.index else _on_device(dev)
+    return _NO_GUARD if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _raw_stream(torch, dev, stream):
@@ -806,53 +792,46 @@ _ROPE_TYPES: dict = {}  # torch dtype -> DA_TYPE_*
 
 
 def _req_rows(t, name, dtype, device):
-    """A [tokens, heads, D] view whose rows are contiguous; returns its token
-    and head strides (a dimension of one has none)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    """A [tokens, heads, D] view whose rows are contiguous; returns its shape and
+    its token and head strides (a dimension of one has none)."""
+    if getattr(t, "dtype", None) is not dtype:
+        raise TypeError(f"{name} must be a tensor of {dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
-    n, h, d = t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have 3 dims, got {len(shape)}")
     ts, hs, ds = t.stride()
-    if ds != 1 and d != 1:
+    if ds != 1 and shape[2] != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return (ts if n > 1 else 0), (hs if h > 1 else 0)
+    return shape, (ts if shape[0] > 1 else 0), (hs if shape[1] > 1 else 0)
 
 
-def _rope_params(torch, x, freqs, norm, q_weight, k_weight, weight_offset, eps, interleaved,
-                 q_rows, k_rows, v_rows):
+def _rope_kind(torch, x):
+    """DA_TYPE_* of the rows."""
     if not isinstance(x, torch.Tensor):
-        raise TypeError("q and k must be torch.Tensors")
+        raise TypeError("q, k and v must be torch.Tensors")
     if not _ROPE_TYPES:
         _ROPE_TYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
     kind = _ROPE_TYPES.get(x.dtype)
     if kind is None:
         raise TypeError(f"q, k and v must be float32, float16 or bfloat16, got {x.dtype}")
-    dev = x.device
-    rd, fp = 0, None
-    if freqs is not None:
-        if not _plain(freqs, torch.int64, dev, 1):
-            _req(freqs, "freqs", torch.int64, dev, 1)
-        rd, fp = 2 * freqs.shape[0], freqs.data_ptr()
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if not norm:
-            raise ValueError(f"{name} is given but norm is off")
-        if not _plain(w, torch.float32, dev, 1):
-            _req(w, name, torch.float32, dev, 1)
-        if w.shape[0] != x.shape[-1]:
-            raise ValueError(f"{name} must have {x.shape[-1]} values, got {w.shape[0]}")
-    return DaRopeParams(kind, rd, 1 if interleaved else 0, 1 if norm else 0, eps, weight_offset,
-                        *q_rows, *k_rows, *v_rows, fp, _ptr(q_weight), _ptr(k_weight))
+    return kind
 
 
-_NO_ROWS = (0, 0)
+def _weight_ptr(torch, w, name, norm, D, dev):
+    if w is None:
+        return None
+    if not norm:
+        raise ValueError(f"{name} is given but norm is off")
+    if not _plain(w, torch.float32, dev, 1):
+        _req(w, name, torch.float32, dev, 1)
+    if w.shape[0] != D:
+        raise ValueError(f"{name} must have {D} values, got {w.shape[0]}")
+    return w.data_ptr()
+
+
+_NO_ROWS = ((0, 0, 0), 0, 0)
 
 
 def decode_attn_qk_norm_rope(q, k, positions, freqs, *, norm=True, q_weight=None, k_weight=None,
@@ -870,27 +849,31 @@ def decode_attn_qk_norm_rope(q, k, positions, freqs, *, norm=True, q_weight=None
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
+    kind = _rope_kind(torch, x)
     dtype, dev = x.dtype, x.device
-    Hq = Hkv = 0
-    q_rows = k_rows = _NO_ROWS
-    if q is not None:
-        q_rows = _req_rows(q, "q", dtype, dev)
-        Hq = q.shape[1]
-    if k is not None:
-        k_rows = _req_rows(k, "k", dtype, dev)
-        Hkv = k.shape[1]
-    r = _rope_params(torch, x, freqs, norm, q_weight, k_weight, weight_offset, eps, interleaved,
-                     q_rows, k_rows, _NO_ROWS)
-    N, _, D = x.shape
-    if k is not None and (k.shape[0] != N or k.shape[2] != D):
+    qs, qt, qh = _NO_ROWS if q is None else _req_rows(q, "q", dtype, dev)
+    ks, kt, kh = _NO_ROWS if k is None else _req_rows(k, "k", dtype, dev)
+    N, _, D = ks if q is None else qs
+    Hq, Hkv = qs[1], ks[1]
+    if k is not None and (ks[0] != N or ks[2] != D):
         raise ValueError("inconsistent shapes")
+    rd, fp, pos = 0, None, None
+    if freqs is not None:
+        if not _plain(freqs, torch.int64, dev, 1):
+            _req(freqs, "freqs", torch.int64, dev, 1)
+        if positions is None:
+            raise ValueError("positions are needed for the rotation")
+        rd, fp = 2 * freqs.shape[0], freqs.data_ptr()
     if positions is not None:
         if not _plain(positions, torch.int32, dev, 1):
             _req(positions, "positions", torch.int32, dev, 1)
         if positions.shape[0] != N:
             raise ValueError("inconsistent shapes")
-    elif freqs is not None:
-        raise ValueError("positions are needed for the rotation")
+        pos = positions.data_ptr()
+    r = DaRopeParams(kind, rd, 1 if interleaved else 0, 1 if norm else 0, eps, weight_offset,
+                     qt, qh, kt, kh, 0, 0, fp,
+                     _weight_ptr(torch, q_weight, "q_weight", norm, D, dev),
+                     _weight_ptr(torch, k_weight, "k_weight", norm, D, dev))
     for name, t, dt, shape in (("q_out", q_out, torch.float32, (N, Hq, D)),
                                ("k_out", k_out, torch.float16, (N, Hkv, D))):
         if t is not None:
@@ -905,8 +888,8 @@ def decode_attn_qk_norm_rope(q, k, positions, freqs, *, norm=True, q_weight=None
             k_out = torch.empty((N, Hkv, D), dtype=torch.float16, device=dev)
         if N == 0:
             return q_out, k_out
-        st = lib.decode_attn_qk_norm_rope(ctypes.byref(r), N, Hq, Hkv, D, _ptr(q), _ptr(k),
-                                          _ptr(positions), _ptr(q_out), _ptr(k_out),
+        st = lib.decode_attn_qk_norm_rope(ctypes.byref(r), N, Hq, Hkv, D, _ptr(q), _ptr(k), pos,
+                                          _ptr(q_out), _ptr(k_out),
                                           _raw_stream(torch, dev, stream))
     _check("decode_attn_qk_norm_rope", st)
     return q_out, k_out
@@ -924,22 +907,30 @@ def decode_attn_append_paged_rope(k_new, v_new, positions, block_table, k_pool, 
     in the same launch.  Returns q_out f32 [N, Hq, D], or None without q."""
     torch = _torch()
     lib = _lib or load_library()
-    dtype, dev, i32 = k_new.dtype, k_new.device, torch.int32
-    k_rows = _req_rows(k_new, "k_new", dtype, dev)
-    v_rows = _req_rows(v_new, "v_new", dtype, dev)
-    q_rows = _NO_ROWS if q is None else _req_rows(q, "q", dtype, dev)
-    r = _rope_params(torch, k_new, freqs, norm, q_weight, k_weight, weight_offset, eps,
-                     interleaved, q_rows, k_rows, v_rows)
+    kind = _rope_kind(torch, k_new)
+    dtype, dev, i32, f16 = k_new.dtype, k_new.device, torch.int32, torch.float16
+    ks, kt, kh = _req_rows(k_new, "k_new", dtype, dev)
+    vs, vt, vh = _req_rows(v_new, "v_new", dtype, dev)
+    qs, qt, qh = _NO_ROWS if q is None else _req_rows(q, "q", dtype, dev)
+    N, Hkv, D = ks
+    rd, fp = 0, None
+    if freqs is not None:
+        if not _plain(freqs, torch.int64, dev, 1):
+            _req(freqs, "freqs", torch.int64, dev, 1)
+        rd, fp = 2 * freqs.shape[0], freqs.data_ptr()
+    r = DaRopeParams(kind, rd, 1 if interleaved else 0, 1 if norm else 0, eps, weight_offset,
+                     qt, qh, kt, kh, vt, vh, fp,
+                     _weight_ptr(torch, q_weight, "q_weight", norm, D, dev),
+                     _weight_ptr(torch, k_weight, "k_weight", norm, D, dev))
     if not (_plain(positions, i32, dev, 1) and _plain(block_table, i32, dev, 2)
-            and _plain(k_pool, torch.float16, dev, 4) and _plain(v_pool, torch.float16, dev, 4)):
+            and _plain(k_pool, f16, dev, 4) and _plain(v_pool, f16, dev, 4)):
         _req(positions, "positions", i32, dev, 1)
         _req(block_table, "block_table", i32, dev, 2)
-        _req(k_pool, "k_pool", torch.float16, dev, 4)
-        _req(v_pool, "v_pool", torch.float16, dev, 4)
-    N, Hkv, D = k_new.shape
-    NB, bs, Hp, Dp = k_pool.shape
-    if (v_new.shape != k_new.shape or v_pool.shape != k_pool.shape or Hp != Hkv or Dp != D
-            or positions.shape[0] != N):
+        _req(k_pool, "k_pool", f16, dev, 4)
+        _req(v_pool, "v_pool", f16, dev, 4)
+    pool = k_pool.shape
+    NB, bs, Hp, Dp = pool
+    if (vs != ks or v_pool.shape != pool or Hp != Hkv or Dp != D or positions.shape[0] != N):
         raise ValueError("inconsistent shapes")
     if token_seq is not None:
         if not _plain(token_seq, i32, dev, 1):
@@ -948,19 +939,20 @@ def decode_attn_append_paged_rope(k_new, v_new, positions, block_table, k_pool, 
             raise ValueError("inconsistent shapes")
     Hq = Hkv
     if q is not None:
-        Hq = q.shape[1]
-        if q.shape[0] != N or q.shape[2] != D:
+        Hq = qs[1]
+        if qs[0] != N or qs[2] != D:
             raise ValueError("inconsistent shapes")
         if q_out is not None:
             _req(q_out, "q_out", torch.float32, dev, 3)
-            if q_out.shape != q.shape:
+            if q_out.shape != qs:
                 raise ValueError("inconsistent shapes")
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need q")
     if dev_status is not None:
         _req(dev_status, "dev_status", i32, dev)
     _check_cuda("k_new", k_new)
-    p = DaParams(block_table.shape[0], Hq, Hkv, D, bs, block_table.shape[1], NB, 0, 0.0, 0.0, 0, 1)
+    rows, columns = block_table.shape
+    p = DaParams(rows, Hq, Hkv, D, bs, columns, NB, 0, 0.0, 0.0, 0, 1)
     with _call_guard(torch, dev, stream):
         if q is not None and q_out is None:
             q_out = torch.empty((N, Hq, D), dtype=torch.float32, device=dev)
@@ -985,6 +977,7 @@ def decode_attn_paged_prefix_workspace_size(params: DaParams, q_len: int, prefix
 
 
 _prefix_ws: dict = {}  # (device, stream) -> workspace
+_prefix_ws_bytes: dict = {}  # (device, B, T, Hq, Hkv, D), all that it depends on -> its size
 
 
 def _prefix_workspace(torch, dev, raw, nbytes):
@@ -1076,7 +1069,12 @@ def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_le
             return out, lse
         raw = _raw_stream(torch, dev, stream)
         if auto:
-            nbytes = lib.decode_attn_paged_prefix_workspace_size(ref, T, prefix_len)
+            key = (dev.index, B, T, Hq, Hkv, D)
+            nbytes = _prefix_ws_bytes.get(key)
+            if nbytes is None:
+                nbytes = lib.decode_attn_paged_prefix_workspace_size(ref, T, prefix_len)
+                if nbytes:  # the sizes are sound
+                    _prefix_ws_bytes[key] = nbytes
             workspace = _prefix_workspace(torch, dev, raw, nbytes)
         st = lib.decode_attn_paged_prefix(
             ref, T, prefix_len, prefix_table.data_ptr(), q.data_ptr(), k_pool.data_ptr(),
