@@ -43,6 +43,24 @@ cudaError_t launch_split_merge(int rows, int max_splits, int D, const float* o_p
                                const float* lse_part, float* out, float* lse,
                                cudaStream_t stream);
 
+// Launches a kernel that may be set up while the kernel before it in the stream still runs, and
+// that waits for that one's end itself (wait_for_grid_before) before it touches memory.
+template <typename P>
+inline cudaError_t launch_early(void (*kernel)(const P), unsigned grid, unsigned threads,
+                                size_t smem, cudaStream_t stream, const P& p) {
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // Shared-prefix decode (prefix_attn.cu).  Rows are (sequence, query token,
 // query head of the kv head); keys below prefix_pages * bs are read through
 // prefix_table, the others through block_table.

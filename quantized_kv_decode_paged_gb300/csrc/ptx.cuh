@@ -158,6 +158,12 @@ __device__ __forceinline__ void load_f32x8(const float* p, float* v) {
                : "l"(p));
 }
 
+__device__ __forceinline__ void store_f32x8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // Fetches the 128-byte line holding addr into L2 (a hint; nothing waits).
 __device__ __forceinline__ void prefetch_l2(const void* addr) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(addr));

@@ -25,6 +25,7 @@
 
 #include "../../include/decode_attn.h"
 #include "launch.h"
+#include "ptx.cuh"
 
 namespace {
 
@@ -109,9 +110,7 @@ __device__ __forceinline__ void values8(const Raw<T>& r, float (&x)[8]) {
 // against 92 for the 470 MB of 16,381 tokens x 40 heads x 128).
 __device__ __forceinline__ void store8(float* p, const float (&x)[8], bool wide) {
   if (wide) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]),
-                 "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
+    da::store_f32x8(p, x);
     return;
   }
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -169,6 +168,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
   const int lo = IL ? 16 * c : rot ? 8 * c : a.rd + 16 * (c - nrot);
   const int hi = (IL || !rot) ? lo + 8 : a.rd / 2 + 8 * c;
   const int rows = tokens * a.heads;
+  da::let_next_grid_start();
+  da::wait_for_grid_before();
 
   struct Row {
     int t, h, kind;  // token of the CTA, head, 0 q / 1 k / 2 v
@@ -274,22 +275,17 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
 }
 
 template <typename T, int D, bool APPEND>
-void launch_rope_d(const RopeArgs& a, int il, cudaStream_t s) {
+cudaError_t launch_rope_d(const RopeArgs& a, int il, cudaStream_t s) {
   const int grid = (a.N + a.tokens - 1) / a.tokens;
-  if (il)
-    rope_kernel<T, D, true, APPEND><<<grid, kRopeThreads, 0, s>>>(a);
-  else
-    rope_kernel<T, D, false, APPEND><<<grid, kRopeThreads, 0, s>>>(a);
+  return da::launch_early(il ? rope_kernel<T, D, true, APPEND> : rope_kernel<T, D, false, APPEND>,
+                          grid, kRopeThreads, 0, s, a);
 }
 
 template <typename T, bool APPEND>
-void launch_rope_t(const RopeArgs& a, int D, int il, cudaStream_t s) {
-  if (D == 64)
-    launch_rope_d<T, 64, APPEND>(a, il, s);
-  else if (D == 128)
-    launch_rope_d<T, 128, APPEND>(a, il, s);
-  else
-    launch_rope_d<T, 256, APPEND>(a, il, s);
+cudaError_t launch_rope_t(const RopeArgs& a, int D, int il, cudaStream_t s) {
+  if (D == 64) return launch_rope_d<T, 64, APPEND>(a, il, s);
+  if (D == 128) return launch_rope_d<T, 128, APPEND>(a, il, s);
+  return launch_rope_d<T, 256, APPEND>(a, il, s);
 }
 
 template <bool APPEND>
@@ -301,13 +297,11 @@ int launch_rope(RopeArgs& a, const da_rope_params* r, int D, int num_tokens, voi
   // tokens of a CTA: few enough for whole waves of CTAs
   const int waves = (num_tokens - 1) / (kWave * kMaxTokens) + 1;
   a.tokens = (num_tokens - 1) / (kWave * waves) + 1;
-  if (r->type == DA_TYPE_F32)
-    launch_rope_t<float, APPEND>(a, D, r->interleaved, s);
-  else if (r->type == DA_TYPE_F16)
-    launch_rope_t<__half, APPEND>(a, D, r->interleaved, s);
-  else
-    launch_rope_t<__nv_bfloat16, APPEND>(a, D, r->interleaved, s);
-  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  const cudaError_t err =
+      r->type == DA_TYPE_F32   ? launch_rope_t<float, APPEND>(a, D, r->interleaved, s)
+      : r->type == DA_TYPE_F16 ? launch_rope_t<__half, APPEND>(a, D, r->interleaved, s)
+                               : launch_rope_t<__nv_bfloat16, APPEND>(a, D, r->interleaved, s);
+  return err == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

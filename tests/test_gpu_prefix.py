@@ -599,3 +599,55 @@ def test_a_named_stream_takes_no_memory_in_use():
     torch.cuda.synchronize()
     assert (y == 7).all()
     c.check((out.cpu().numpy(), lse.cpu().numpy(), 0))
+
+
+def test_order_with_what_runs_before_and_after():
+    """The kernels may be set up before the work ahead of them in the stream is
+    done: copies, other kernels, each other and work joined from another stream, eager and
+    captured, each with results that follow from the order alone."""
+    import torch
+    B, Hq, Hkv, D, bs, P = 40, 8, 2, 128, 16, 512
+    r = np.random.default_rng(70)
+    c = Case(71, B, Hq, Hkv, D, bs, P, P + r.integers(1, 60, B))
+    src = [_t(r.standard_normal((B, Hq, D)).astype(np.float32)) for _ in range(2)]
+    k, v, table, lens, pt = (_t(x) for x in (c.k, c.v, c.table, c.lens, c.prefix_table))
+    want = [qk.decode_attn_paged_prefix(s, k, v, table, lens, P, pt) for s in src]
+    q, lens2 = torch.zeros_like(src[0]), torch.zeros_like(lens)
+    freqs = qk.decode_attn_rope_freqs(D)
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    got = [[torch.empty_like(t) for t in w] for w in want]
+
+    def step():
+        cur = torch.cuda.current_stream()
+        for i in range(2):
+            side.wait_stream(cur)
+            with torch.cuda.stream(side):
+                lens2.zero_()
+                torch.cuda._sleep(20_000)
+                lens2.add_(lens)
+            q.copy_(src[1 - i])  # overwritten by the next, which has to come after it
+            q.zero_()
+            qk.decode_attn_qk_norm_rope(src[i], None, zero, freqs, norm=False, q_out=q)
+            cur.wait_stream(side)
+            qk.decode_attn_paged_prefix(q, k, v, table, lens2, P, pt, out=got[i][0], lse=got[i][1])
+            q.zero_()
+
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for _ in range(20):
+            step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    for replay in range(2):
+        for w, g in zip(want, got):
+            assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1])
+            g[0].zero_()
+            g[1].zero_()
+        if replay == 0:
+            with torch.cuda.graph(graph, stream=stream):
+                step()
+            for _ in range(20):
+                graph.replay()
+            torch.cuda.synchronize()
