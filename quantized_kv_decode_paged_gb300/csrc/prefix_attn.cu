@@ -519,7 +519,7 @@ __device__ void share_out(const PrefixParams& p, PrefixSmem<D>& s) {
   auto mean = [&](int width, int blocks) {
     return (int)(((uint32_t)pn * (p.Hkv * blocks) * width + own + p.grid - 1) / (uint32_t)p.grid);
   };
-  if (tid < (pn ? min(p.row_tiles, p.grid) : 0)) {
+  if (p.row_tiles > 1 && tid < (pn ? min(p.row_tiles, p.grid) : 0)) {
     const int width = tid + 1, blocks = (uint32_t)(p.row_tiles + tid) / (uint32_t)width;
     const Split pre = Split::of(pn * (p.Hkv * blocks), (uint32_t)p.grid / (uint32_t)width);
     const int longest = max(pre.longest(), mean(width, blocks));
@@ -765,6 +765,40 @@ struct Loader {
   }
 };
 
+// What a softmax thread knows of its row in a part.
+struct Row {
+  bool any, on;       // the warp has rows, the thread has one
+  int lo, hi;         // keys it sees among the part's
+  int place;          // in [B, T, Hq]; of the part's nearest row where the thread has none
+  float scale;        // of its scores, base 2
+  float m, l;         // running maximum, and the sum of the weights against it
+  bool partial;       // it met a tile some key of which was masked (for a row of its warp)
+};
+// Its place (of sequence b, query token tok).
+template <int D>
+__device__ __forceinline__ int row_place(const PrefixParams& p, const Part<D>& c, int w, int& b,
+                                         int& tok) {
+  const int row = w * 32 + (int)(threadIdx.x & 31);
+  return c.out_row(p, min(max(row - c.lane0(), 0), c.nr - 1), b, tok);
+}
+template <int D>
+__device__ __forceinline__ Row row_of(const PrefixParams& p, const PrefixSmem<D>& s,
+                                      const Part<D>& c, int w, int place, int b, int tok) {
+  Row r = {false, false, 0, 0, place, 0.f, -kInf, 0.f, false};
+  const int first = c.lane0(), row = w * 32 + (int)(threadIdx.x & 31);
+  r.any = w * 32 + 32 > first && w * 32 < first + c.nr;
+  r.on = row >= first && row < first + c.nr;
+  if (r.on) {
+    key_range(p, s.len[b], s.qp[b], tok, tok, r.lo, r.hi);
+    const int P = p.prefix_pages << p.log2_bs;
+    if (c.b < 0)
+      r.hi = min(r.hi, P);
+    else
+      r.lo = max(r.lo, P);
+  }
+  return r;
+}
+
 // ------------------------------------------------------------------ Q
 // A row of Q is divided by the power of two that brings its largest value to [2^9, 2^10) and
 // held as two f16 terms.  Powers for a row whose largest value is m (the exponent
@@ -778,15 +812,15 @@ __device__ __forceinline__ void q_powers(float m, float& by, float& undo) {
 
 // Q in tensor memory: warp w of softmax group g converts half g of the rows of
 // the part that lie in lanes [32 w, 32 w + 32), a thread a row.  The groups tell each other
-// their halves' largest values; `uses` counts that.  Gives qscale * 2^e of the thread's row.
+// their halves' largest values; `uses` counts that.  Gives the thread's row, with qscale * 2^e.
 template <int D>
 __device__ __forceinline__ bool load_q_lanes(const PrefixParams& p, PrefixSmem<D>& s,
                                              const Part<D>& c, int group, int w, uint32_t lanes,
-                                             int uses, float& scale) {
+                                             int uses, Row& r) {
   constexpr int H = D / 2;
   const int lane = threadIdx.x & 31, row = w * 32 + lane;
   int seq, tok;
-  const int at = c.out_row(p, min(max(row - c.lane0(), 0), c.nr - 1), seq, tok);
+  const int at = row_place<D>(p, c, w, seq, tok);
   const float* src = p.q + (long long)at * D + group * H;
   // Every lane reads lines of its own, which is what the L1's rate bounds: each line once,
   // in the widest pieces the address allows (read twice in 16-byte ones, 128 rows took
@@ -802,6 +836,7 @@ __device__ __forceinline__ bool load_q_lanes(const PrefixParams& p, PrefixSmem<D
       v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
     }
   }
+  r = row_of<D>(p, s, c, w, at, seq, tok);  // while they are on their way
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < H; ++i) m = fmaxf(m, fabsf(v[i]));
@@ -810,8 +845,8 @@ __device__ __forceinline__ bool load_q_lanes(const PrefixParams& p, PrefixSmem<D
   if (lane == 0) mbar_arrive(&s.q_half[w]);
   if (!warp_wait<D>(p, s, &s.q_half[w], uses & 1)) return false;
   float by;
-  q_powers(fmaxf(m, s.q_max[(group ^ 1) * kPrefixRows + row]), by, scale);
-  scale *= p.qscale;
+  q_powers(fmaxf(m, s.q_max[(group ^ 1) * kPrefixRows + row]), by, r.scale);
+  r.scale *= p.qscale;
 #pragma unroll
   for (int i = 0; i < H; i += 16) {
     uint32_t hi[8], lo[8];
@@ -930,35 +965,6 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float* v) {
   tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < N; i += 32) tmem_loaded32(v + i);
-}
-
-// What a softmax thread knows of its row in a part.
-struct Row {
-  bool any, on;       // the warp has rows, the thread has one
-  int lo, hi;         // keys it sees among the part's
-  int place;          // in [B, T, Hq]
-  float scale;        // of its scores, base 2
-  float m, l;         // running maximum, and the sum of the weights against it
-  bool partial;       // it met a tile some key of which was masked (for a row of its warp)
-};
-template <int D>
-__device__ __forceinline__ Row row_of(const PrefixParams& p, const PrefixSmem<D>& s,
-                                      const Part<D>& c, int w) {
-  Row r = {false, false, 0, 0, 0, 0.f, -kInf, 0.f, false};
-  const int first = c.lane0(), row = w * 32 + (int)(threadIdx.x & 31);
-  r.any = w * 32 + 32 > first && w * 32 < first + c.nr;
-  r.on = row >= first && row < first + c.nr;
-  if (r.on) {
-    int b, tok;
-    r.place = c.out_row(p, row - first, b, tok);
-    key_range(p, s.len[b], s.qp[b], tok, tok, r.lo, r.hi);
-    const int P = p.prefix_pages << p.log2_bs;
-    if (c.b < 0)
-      r.hi = min(r.hi, P);
-    else
-      r.lo = max(r.lo, P);
-  }
-  return r;
 }
 
 // Scores of tile x (number j of the part) to weights.  Where two groups take turns the
@@ -1123,7 +1129,9 @@ __device__ void softmax_loop_one(const PrefixParams& p, PrefixSmem<D>& s) {
       load_q<D>(p, s, c, w * 32, w * 32 + 32);
       if (lane == 0) mbar_arrive(&s.q_full[k & 1]);
     }
-    Row r = row_of<D>(p, s, c, w);
+    int b, tok;
+    const int place = row_place<D>(p, c, w, b, tok);
+    Row r = row_of<D>(p, s, c, w, place, b, tok);
     for (int j = 0; j < c.n; ++j, ++x) {
       if (!warp_wait<D>(p, s, &s.s_full[x % G::NS], (x / G::NS) & 1)) return;
       if (j == 0) {
@@ -1166,8 +1174,8 @@ __device__ void softmax_loop_two(const PrefixParams& p, PrefixSmem<D>& s) {
       q_odd ^= 1u << before;
     }
     before = set;
-    Row r = row_of<D>(p, s, c, w);
-    if (!load_q_lanes<D>(p, s, c, group, w, lanes, taken, r.scale)) return;
+    Row r;
+    if (!load_q_lanes<D>(p, s, c, group, w, lanes, taken, r)) return;
     for (int j = 0; j < c.n; ++j, ++x, ++turn) {
       const int at = set * G::NS + x % G::NS;
       const uint32_t parity = phases.next(at, x);
