@@ -213,13 +213,12 @@ template <int D>
 constexpr int kSmallRows = PGeo<D>::QT ? 32 : 64;
 // Units cost more than their tiles: Q, the first tile's latencies, the state's store.  The list
 // counts so many tiles for it.  D = 128, 32 to 64 heads and 64 to 2048 own keys, without it (0, 0) and
-// with (10, 1): 376 and 255 us over 32,768 shared keys, 61 and 45 over 8192, 419 and 84 over 16.  From
-// there it is flat: (8, 2) took 253, 47, 82, (14, 1) 251, 47, 81, (16, 3) 267, 47, 86.  D = 256: 170
-// and 140 us for 64 sequences of 16 heads, a window of 4096 and 256 to 2048 own keys.
+// with (8, 1): 376 and 250 us over 32,768 shared keys, 61 and 43 over 8192, 419 and 78 over 16.  From
+// there it is flat: (14, 1) took 252, 44, 79, (16, 2) 252, 44, 81.  D = 256: 170 without and 136 us
+// with it for 64 sequences of 16 heads, a window of 4096 and 256 to 2048 own keys.
 template <int D>
-constexpr int kPrefixExtra = D >= 256 ? 24 : 10;
-template <int D>
-constexpr int kOwnExtra = D >= 256 ? 2 : 1;
+constexpr int kPrefixExtra = D >= 256 ? 20 : 8;
+constexpr int kOwnExtra = 1;
 // The maximum that a tile's weights are taken against moves at the first tile of a group of
 // kGroup, whose products add up in tensor memory before the sum warps take them, and where a row
 // outgrows it by 2^kGrow (that tile then starts a group).  Weights are kept times 2^kShift:
@@ -405,7 +404,7 @@ struct Lister : Part<D> {
       }
       if (left <= 0 && b < 0) enter(1);
       if (left <= 0) break;
-      int extra = kOwnExtra<D>, unit_n, rows = p.R1;
+      int extra = kOwnExtra, unit_n, rows = p.R1;
       slot = (blockIdx.x * 2 + moved) * p.own_rows + p.grid * (2 * kPrefixRows);
       r0 = rt * kPrefixRows;
       if (b < 0) {
@@ -480,7 +479,7 @@ __device__ int make_plan(const PrefixParams& p, PrefixSmem<D>& s) {
       atomicMax(&s.hi, min(hi, P));
     }
     const int l = max(lo, P);
-    if (hi > l) n = (hi - P + KT - 1) / KT - (l - P) / KT + kOwnExtra<D>;
+    if (hi > l) n = (hi - P + KT - 1) / KT - (l - P) / KT + kOwnExtra;
   }
   int sum = n;
 #pragma unroll
@@ -564,7 +563,7 @@ __device__ void share_out(const PrefixParams& p, PrefixSmem<D>& s) {
   const int o = c < members ? c : c - members;
   int g = c < members ? before + rest.start(o) : front.start(o);
   s.run[1] = c < members ? rest.share + (o < rest.rem) : front.share + (o < front.rem);
-  if (pn == 0) s.skip = p.test_skip_arm && g <= kOwnExtra<D> && kOwnExtra<D> < g + s.run[1];
+  if (pn == 0) s.skip = p.test_skip_arm && g <= kOwnExtra && kOwnExtra < g + s.run[1];
   if (s.run[1] > 0) {
     const int x = (uint32_t)g / (uint32_t)units1;  // sequence b holds it: cum[b] <= x < cum[b + 1]
     int b = 0, hi = p.B;
@@ -1589,7 +1588,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   };
   const int n1 = cum[b + 1] - cum[b];
   const int g1 = cum[b] * (p.Hkv * p.own_tiles) + (h * p.own_tiles + r1 / kPrefixRows) * n1;
-  const int c1 = n1 ? own_at(g1 + kOwnExtra<D>) : 0;
+  const int c1 = n1 ? own_at(g1 + kOwnExtra) : 0;
   const int s1 = n1 ? own_at(g1 + n1 - 1) - c1 + 1 : 0;
   float M = -kInf, L = 0.f, o[V];
   bool partial = false;
