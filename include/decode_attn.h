@@ -428,7 +428,8 @@ int decode_attn_append_paged_rope(const da_params* p, const da_rope_params* r, i
  * above, and every mask applies over the whole sequence: a sequence may be
  * shorter than the prefix, or empty, and a sliding window may cut into the
  * prefix or end after it.  The result is that of decode_attn_paged_multi on
- * a table whose rows all start with prefix_table.
+ * a table whose rows all start with prefix_table.  out must not overlap q
+ * (DA_ERR_INVALID).
  * workspace: device scratch of at least
  * decode_attn_paged_prefix_workspace_size(p, q_len, prefix_len) bytes, 256-byte
  * aligned, of any content; calls that overlap on the GPU must not share it.

@@ -741,6 +741,10 @@ int prefix_impl(const da_params* p, int T, int prefix_len, const int32_t* prefix
       (dev_status && !aligned(dev_status, 4)) || !aligned(workspace, 256))
     return DA_ERR_INVALID;
   if (!workspace && workspace_bytes) return DA_ERR_INVALID;
+  // rows of out are written while others' q is still to be read
+  const long long values = (long long)p->batch * T * p->num_q_heads * p->head_dim;
+  const uintptr_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(out);
+  if ((qa < oa ? oa - qa : qa - oa) < (unsigned long long)values * 4) return DA_ERR_INVALID;
   if (p->batch == 0) return DA_OK;
   int sms = 0;
   st = device_sms(&sms);

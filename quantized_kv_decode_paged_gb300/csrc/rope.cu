@@ -6,7 +6,7 @@
 // r = 1/sqrt(mean(x^2) + eps).  Rotation of a pair by the angle a:
 // (y0 cos a - y1 sin a, y0 sin a + y1 cos a).  a = pos * f turns with f in
 // 64-bit fixed point: the low 64 bits of the integer product are the angle
-// modulo one turn, exact up to f's own 2^-65 turns a position.  The top 32 bits
+// modulo one turn, exact up to f's own 2^-56 turns a position (a double's).  The top 32 bits
 // as a signed number times 2^-31 are a / pi in [-1, 1), what sincospif takes.
 //
 // A CTA takes up to kMaxTokens tokens: their rd/2 cosines and sines are computed once

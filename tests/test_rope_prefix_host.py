@@ -167,6 +167,22 @@ def test_prefix_rejects_bad_arguments(lib):
     assert qk.decode_attn_paged_prefix_workspace_size(qk.DaParams(**base), 1, 65) == 0
 
 
+def test_prefix_refuses_an_output_over_its_queries(lib):
+    p = qk.DaParams(2, 8, 2, 128, 16, 4, 8, 64, 0.0, 0.0, 0, 1)
+    n = 2 * 3 * 8 * 128 * 4  # bytes of q and of out, three tokens a sequence
+
+    def call(q, out):
+        return lib.decode_attn_paged_prefix(ctypes.byref(p), 3, 32, FAKE, q, FAKE, FAKE, FAKE, FAKE,
+                                            None, out, None, FAKE, 0, None, None)
+
+    at = FAKE.value
+    for d in (0, 16, n - 16):
+        for a, b in ((at, at + d), (at + d, at)):
+            assert call(ctypes.c_void_p(a), ctypes.c_void_p(b)) == qk.DA_ERR_INVALID
+    for a, b in ((at, at + n), (at + n, at)):  # side by side: not for this reason
+        assert call(ctypes.c_void_p(a), ctypes.c_void_p(b)) != qk.DA_ERR_INVALID
+
+
 # ------------------------------------------------------------------ the binding
 def _cpu_prefix(**kw):
     a = dict(q=torch.zeros(2, 8, 64), k_pool=torch.zeros(8, 16, 2, 64, dtype=torch.float16),
