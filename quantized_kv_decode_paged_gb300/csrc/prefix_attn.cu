@@ -39,7 +39,7 @@
 // lanes of one warp of each of these groups, and four such units run at once.
 //
 // Measured (GB300), 128 sequences x 64 heads, 8 kv heads, D = 128, 32,768 shared and 64 to 2048 own
-// keys: 255 us, 235 of them in prefix_attn_kernel, which issues 352 GFLOP of products (140 before
+// keys: 246 to 268 us by the card, 235 of them in prefix_attn_kernel, which issues 352 GFLOP of products (140 before
 // the second terms and the empty rows of own tiles): 1.5 PFLOP/s, 79% of the tensor cores' measured
 // rate, at the card's power limit; 452 MB read, 1.9 TB/s.  A tile takes 0.8 us for 0.55 of products:
 // the softmax's and the sums' traffic with tensor memory; an own unit's chain of latencies 2 to 3 us.
@@ -1557,7 +1557,8 @@ __device__ __forceinline__ void load_row(const float* p, float* x) {
   }
 }
 
-// One warp a row.
+// One warp a row: a lane finds and weighs a state, the warp adds their rows up.  Bound by a chain
+// of loads (plan, (m, l), o): 5 us behind the first kernel's end for 1024 rows, 10 for 8192.
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     prefix_merge_kernel(const __grid_constant__ PrefixParams p) {

@@ -14,7 +14,11 @@
 // two 8-value chunks that hold both halves of its 8 pairs: (8c, rd/2 + 8c) or, interleaved,
 // (16c, 16c + 8); the chunks past the rotated part pair up without rotation.
 // So no value crosses threads but the norm's sum of squares.  A thread's next row is
-// loaded before its last one is worked on.
+// loaded before its last one is worked on.  HBM bounds long calls, the host short ones.
+//
+// Measured (GB300): 16,381 tokens x (32 + 8) heads x 128 from bf16, 470 MB in 73 us, 6.4 TB/s (77.5 us a
+// call in a loop); an append of 12,287 tokens x 8 heads x 128 of keys and values, 101 MB in 17 us;
+// 128 tokens x 72 heads 7 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
