@@ -904,7 +904,8 @@ def decode_attn_append_paged_rope(k_new, v_new, positions, block_table, k_pool, 
     rotated on the way.  positions i32 [N]; token_seq i32 [N] names each
     token's row of block_table (negative: padding, nothing is written; None:
     token n is sequence n).  With q [N, Hq, D] the queries are normed and rotated
-    in the same launch.  Returns q_out f32 [N, Hq, D], or None without q."""
+    in the same launch (without q, q_weight is not read).  Returns q_out f32 [N, Hq, D],
+    or None without q."""
     torch = _torch()
     lib = _lib or load_library()
     kind = _rope_kind(torch, k_new)
@@ -946,8 +947,8 @@ def decode_attn_append_paged_rope(k_new, v_new, positions, block_table, k_pool, 
             _req(q_out, "q_out", torch.float32, dev, 3)
             if q_out.shape != qs:
                 raise ValueError("inconsistent shapes")
-    elif q_out is not None or q_weight is not None:
-        raise ValueError("q_out and q_weight need q")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
     if dev_status is not None:
         _req(dev_status, "dev_status", i32, dev)
     _check_cuda("k_new", k_new)

@@ -377,3 +377,27 @@ def test_a_named_stream_takes_no_memory_in_use():
         torch.cuda.synchronize()
         assert (y == 7).all()
         assert torch.equal(out, want)
+
+
+def test_weights_of_a_side_that_is_not_given_are_not_read():
+    """A program that keeps both weights passes both, whichever rows a call has."""
+    import torch
+    rng = np.random.default_rng(21)
+    N, H, D = 5, 2, 64
+    f, _ = _freqs(D)
+    pos = _t(rng.integers(0, 128, N).astype(np.int32))
+    x = _t(rng.standard_normal((N, H, D)).astype(np.float32))
+    w = _t(1 + 0.1 * rng.standard_normal(D).astype(np.float32))
+    bad = torch.full((D,), float("nan"), device="cuda")
+    table = torch.arange(N, dtype=torch.int32, device="cuda")[:, None].repeat(1, 8)
+    pools = [[torch.zeros((N, 16, H, D), dtype=torch.float16, device="cuda") for _ in range(2)]
+             for _ in range(2)]
+    for (kp, vp), qw in zip(pools, (None, bad)):
+        out = qk.decode_attn_append_paged_rope(x, x, pos, table, kp, vp, f, norm=True, q_weight=qw,
+                                               k_weight=w)
+        assert out is None
+    assert torch.equal(pools[0][0], pools[1][0]) and torch.equal(pools[0][1], pools[1][1])
+    q, none = qk.decode_attn_qk_norm_rope(x, None, pos, f, q_weight=w, k_weight=bad)
+    assert none is None and torch.isfinite(q).all()
+    none, k = qk.decode_attn_qk_norm_rope(None, x, pos, f, q_weight=bad, k_weight=w)
+    assert none is None and torch.isfinite(k).all()
