@@ -534,7 +534,10 @@ __device__ void share_out(const PrefixParams& p, PrefixSmem<D>& s) {
   if (pn) {
     int few = max(1, (uint32_t)tp / (uint32_t)each);
     if ((long long)Split::of(tp, few).longest() * 24 > (long long)each * 25) ++few;
-    groups = min(groups, few);
+    // nor more parts of a unit than the merge weighs at once: a prefix in 76 parts of a tile or two took
+    // 29 us where 32 parts take 25 (18 sequences of 2 heads, 6487 keys, D = 128), 51 where they take 44
+    // (15 sequences, 2 kv heads, a window of 4096, D = 256)
+    groups = min(min(groups, few), p.Hkv * blocks * 32);
   }
   const Split pre = Split::of(tp, groups);
   const int members = groups * width, others = p.grid - members;
@@ -1549,11 +1552,15 @@ constexpr int kMergeWarps = 8;
 
 template <int V>
 __device__ __forceinline__ void load_row(const float* p, float* x) {
+  if constexpr (V == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    x[0] = f.x, x[1] = f.y;
+  } else {
 #pragma unroll
-  for (int i = 0; i < V; i += 2) {
-    const float2 f = *reinterpret_cast<const float2*>(p + i);
-    x[i] = f.x;
-    x[i + 1] = f.y;
+    for (int i = 0; i < V; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p + i);
+      x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
+    }
   }
 }
 
@@ -1641,19 +1648,30 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     M = mn;
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] *= f;
+    // their rows, several in flight (places behind the last name the last one)
     const int n = min(32, s0 + s1 - j0);
     const uint32_t have = __ballot_sync(0xffffffffu, some);
-#pragma unroll 4
-    for (int u = 0; u < n; ++u) {
-      const float wu = __shfl_sync(0xffffffffu, w, u);
-      const float* su = reinterpret_cast<const float*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), u));
-      if (!(have >> u & 1)) continue;
-      float x[V];
-      load_row<V>(su + lane * V, x);
+    auto add = [&](int u0, auto batch) {
+      constexpr int N = decltype(batch)::value;
+      float x[N][V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = fmaf(wu, x[i], o[i]);
-    }
+      for (int u = 0; u < N; ++u)
+        load_row<V>(reinterpret_cast<const float*>(__shfl_sync(
+                        0xffffffffu, reinterpret_cast<unsigned long long>(src),
+                        min(u0 + u, n - 1))) + lane * V, x[u]);
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const float wu = __shfl_sync(0xffffffffu, w, (u0 + u) & 31);
+        if (u0 + u < n && (have >> (u0 + u) & 1)) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] = fmaf(wu, x[u][i], o[i]);
+        }
+      }
+    };
+    int u0 = 0;
+#pragma unroll 1
+    for (; n - u0 > 4; u0 += 8) add(u0, std::integral_constant<int, 8>());
+    if (u0 < n) add(u0, std::integral_constant<int, 4>());
   }
   // A zero weight does not silence a value that is not finite: a row that met masked keys
   // and came out non-finite is done again, key by key.
