@@ -14,6 +14,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import Optional
@@ -740,6 +742,31 @@ def decode_attn_append_tiered_f16(k_new, v_new, k_hot, v_hot, k_cold, v_cold, bl
 # norm, rotation and append of a step's new rows
 # ---------------------------------------------------------------------------
 
+_call = None
+
+
+def _load_call():
+    """The C++ module that takes the common case of the calls below (csrc/call.cpp)."""
+    global _call
+    lib = load_library()
+    with _lock:
+        if _call is None:
+            _torch()  # its libraries are the module's
+            path = _build.CALL_PATH
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing: build it first "
+                                   "(quantized_kv_decode_paged_gb300.build())")
+            loader = importlib.machinery.ExtensionFileLoader("decode_attn_call", path)
+            spec = importlib.util.spec_from_file_location("decode_attn_call", path, loader=loader)
+            module = importlib.util.module_from_spec(spec)
+            loader.exec_module(module)
+            module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.decode_attn_qk_norm_rope, lib.decode_attn_append_paged_rope,
+                lib.decode_attn_paged_prefix, lib.decode_attn_paged_prefix_workspace_size)))
+            _call = module
+    return _call
+
+
 def _check_cuda(name, t):
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
@@ -844,6 +871,13 @@ def decode_attn_qk_norm_rope(q, k, positions, freqs, *, norm=True, q_weight=None
     rotation (positions may then be None).  q_weight / k_weight f32 [D] with
     ``norm``.  Returns (q_out f32 [N, Hq, D], k_out f16 [N, Hkv, D]): the types
     that the decode and the append calls take."""
+    if stream is None:
+        y = (_call or _load_call()).norm_rope(q, k, positions, freqs, norm, q_weight, k_weight,
+                                              weight_offset, eps, interleaved, q_out, k_out)
+        if type(y) is tuple:
+            return y
+        if y is not NotImplemented:
+            _check("decode_attn_qk_norm_rope", y)
     torch = _torch()
     lib = _lib or load_library()
     x = q if q is not None else k
@@ -906,6 +940,14 @@ def decode_attn_append_paged_rope(k_new, v_new, positions, block_table, k_pool, 
     token n is sequence n).  With q [N, Hq, D] the queries are normed and rotated
     in the same launch (without q, q_weight is not read).  Returns q_out f32 [N, Hq, D],
     or None without q."""
+    if stream is None:
+        y = (_call or _load_call()).append(k_new, v_new, positions, block_table, k_pool, v_pool,
+                                           freqs, token_seq, q, norm, q_weight, k_weight,
+                                           weight_offset, eps, interleaved, q_out, dev_status)
+        if type(y) is int:
+            _check("decode_attn_append_paged_rope", y)
+        if y is not NotImplemented:
+            return y
     torch = _torch()
     lib = _lib or load_library()
     kind = _rope_kind(torch, k_new)
@@ -1009,6 +1051,14 @@ def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_le
     ``workspace``: "auto" (kept per stream; a captured call's own) or a
     caller-owned uint8 tensor of decode_attn_paged_prefix_workspace_size bytes
     (any content)."""
+    if stream is None and isinstance(workspace, str) and workspace == "auto":
+        y = (_call or _load_call()).prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_len,
+                                           prefix_table, q_pos, scale, softcap, sliding_window,
+                                           causal, max_seq_len, out, lse, dev_status)
+        if type(y) is tuple:
+            return y
+        if y is not NotImplemented:
+            _check("decode_attn_paged_prefix", y)
     torch = _torch()
     lib = _lib or load_library()
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):

@@ -1,8 +1,10 @@
 """Builds libdecode_attn.so in-tree with nvcc for sm_103a.
 
 The translation units are compiled in parallel and linked into one shared
-library next to this file (``_lib/libdecode_attn.so``).  A rebuild happens
-only when a source or header is newer than the library.
+library next to this file (``_lib/libdecode_attn.so``).  Beside it the host
+compiler makes ``_lib/decode_attn_call.so``, the Python module that marshals
+the calls that take torch tensors in C++.  A rebuild happens only when a source
+or header is newer than what it makes.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libdecode_attn.so")
+CALL_SRC = os.path.join(CSRC, "call.cpp")
+CALL_PATH = os.path.join(LIB_DIR, "decode_attn_call.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -39,19 +44,53 @@ def _deps():
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _newer(path, deps) -> bool:
+    if not os.path.exists(path):
         return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(f) <= t for f in deps)
+
+
+def _call_up_to_date() -> bool:
+    return _newer(CALL_PATH, [CALL_SRC, os.path.join(INCLUDE, "decode_attn.h"),
+                              os.path.abspath(__file__)])
+
+
+def up_to_date() -> bool:
+    return _newer(LIB_PATH, _deps()) and _call_up_to_date()
+
+
+def _build_call() -> None:
+    """The marshalling module, against this interpreter's torch."""
+    import torch
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    top = os.path.dirname(os.path.abspath(torch.__file__))
+    include = [sysconfig.get_paths()["include"], os.path.join(top, "include"),
+               os.path.join(top, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), INCLUDE]
+    tmp = CALL_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for d in include for x in ("-I", d)], CALL_SRC, "-o", tmp,
+           "-L" + os.path.join(top, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {CALL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile every CUDA translation unit and link libdecode_attn.so."""
+    """Compile every CUDA translation unit and link libdecode_attn.so; make the
+    marshalling module."""
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(OBJ_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
+    stale = force or not _call_up_to_date()
+    if not force and _newer(LIB_PATH, _deps()):
+        _build_call()
+        return LIB_PATH
     nvcc = _nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
 
@@ -64,8 +103,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, r.stderr
 
     srcs = _sources()
-    with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        call = ex.submit(_build_call) if stale else None
         results = list(ex.map(compile_one, srcs))
+        if call:
+            call.result()
     if verbose or ptxas_verbose:
         for _, log in results:
             if log:
