@@ -9,6 +9,7 @@ or header is newer than what it makes.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -52,8 +53,9 @@ def _newer(path, deps) -> bool:
 
 
 def _call_up_to_date() -> bool:
+    torch = importlib.util.find_spec("torch")  # another torch, another module
     return _newer(CALL_PATH, [CALL_SRC, os.path.join(INCLUDE, "decode_attn.h"),
-                              os.path.abspath(__file__)])
+                              os.path.abspath(__file__)] + ([torch.origin] if torch else []))
 
 
 def up_to_date() -> bool:

@@ -8,6 +8,7 @@ import quantized_kv_decode_paged_gb300 as qk
 
 @pytest.fixture(scope="module")
 def call():
+    qk.build()
     return qk._load_call()
 
 
