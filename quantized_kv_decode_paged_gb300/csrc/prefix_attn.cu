@@ -222,6 +222,8 @@ constexpr int kOwnExtra = 1;
 // kGroup, whose products add up in tensor memory before the sum warps take them, and where a row
 // outgrows it by 2^kGrow (that tile then starts a group).  Weights are kept times 2^kShift:
 // those down to 2^-22 of the largest stay normal f16 numbers, and none passes 2^15.
+// (Groups of 4 and of 8 take 1 and 2% less time, 249, 247 and 245 us for the long case above, with
+// twice and four times the truncating steps in a chain.)
 constexpr int kGroup = 2;
 constexpr float kGrow = 7.f;
 constexpr float kShift = 8.f;
