@@ -218,6 +218,11 @@ constexpr int kSmallRows = PGeo<D>::QT ? 32 : 64;
 template <int D>
 constexpr int kPrefixExtra = D >= 256 ? 20 : 8;
 constexpr int kOwnExtra = 1;
+// And so does a CTA's run of the prefix, wherever in a unit it begins: it decides how many CTAs the
+// prefix gets.  0 and these: 134 and 114 us for the D = 256 case, 42 and 41 over 8192 shared keys,
+// 27.2 and 26.2 for 32 sequences over 4096.
+template <int D>
+constexpr int kPartExtra = D >= 256 ? 14 : 4;
 // The maximum that a tile's weights are taken against moves at the first tile of a group of
 // kGroup, whose products add up in tensor memory before the sum warps take them, and where a row
 // outgrows it by 2^kGrow (that tile then starts a group).  Weights are kept times 2^kShift:
@@ -269,6 +274,7 @@ struct PrefixSmem {
   // tile of rows or block of them, entry of the unit) and how long they are
   int first[2][4], run[2];
   PrefixPlan plan;
+  unsigned long long best;                               // cost and number of groups
   int skip;                                              // test hook: the first copy is left out
   int abort;
   uint32_t tmem;
@@ -527,20 +533,23 @@ __device__ void share_out(const PrefixParams& p, PrefixSmem<D>& s) {
       atomicMax(&s.plan.width, width);
   }
   __syncthreads();
-  if (tid != 0 && tid != 32) return;
   const int c = blockIdx.x, width = s.plan.width;
   const int blocks = (uint32_t)(p.row_tiles + width - 1) / (uint32_t)width;
-  const int tp = pn * (p.Hkv * blocks), each = mean(width, blocks);
-  // as few groups as the mean allows: a run that turns to own keys pays for its units twice
-  int groups = (uint32_t)p.grid / (uint32_t)width;
-  if (pn) {
-    int few = max(1, (uint32_t)tp / (uint32_t)each);
-    if ((long long)Split::of(tp, few).longest() * 24 > (long long)each * 25) ++few;
-    // nor more parts of a unit than the merge weighs at once: a prefix in 76 parts of a tile or two took
-    // 29 us where 32 parts take 25 (18 sequences of 2 heads, 6487 keys, D = 128), 51 where they take 44
-    // (15 sequences, 2 kv heads, a window of 4096, D = 256)
-    groups = min(min(groups, few), p.Hkv * blocks * 32);
+  const int tp = pn * (p.Hkv * blocks);
+  // How many groups: a run of the prefix costs its CTA kPartExtra more than its entries (Q of 128 rows,
+  // their state), whatever unit it is of.  One thread a number.
+  const int most = min((uint32_t)p.grid / (uint32_t)width, (uint32_t)(p.Hkv * blocks * 32));
+  if (tid < (pn ? most : 0)) {
+    const int n = tid + 1;
+    const uint32_t all =
+        (uint32_t)tp * width + (uint32_t)(n * width * kPartExtra<D>) + own + p.grid - 1;
+    const int cost = max(Split::of(tp, n).longest() + kPartExtra<D>, (int)(all / (uint32_t)p.grid));
+    atomicMin(&s.best, (unsigned long long)cost << 32 | (unsigned)n);
   }
+  __syncthreads();
+  if (tid != 0 && tid != 32) return;
+  const int groups = pn ? (int)(uint32_t)s.best : p.grid;
+  const int each = pn ? (int)(s.best >> 32) : mean(1, 1);
   const Split pre = Split::of(tp, groups);
   const int members = groups * width, others = p.grid - members;
   // all own entries where that fits (a few for each member would cut units for little)
@@ -1484,6 +1493,7 @@ __global__ void __launch_bounds__(PGeo<D>::THREADS, 1)
     s.lo = 0x7fffffff;
     s.hi = 0;
     s.plan.width = 1;
+    s.best = ~0ull;
     s.abort = 0;
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
