@@ -39,6 +39,19 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// Encodes a tensor map.  The driver's call wants a current context.  A host thread has one from its
+// first runtime call that needs it, a launch or an allocation; where this is the first, setting the
+// thread's device to what it is makes the device's context current.
+template <typename... Args>
+int encode_map(Args... args) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return DA_ERR_CUDA;
+  if (fn(args...) == CUDA_SUCCESS) return DA_OK;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return DA_ERR_CUDA;
+  return fn(args...) == CUDA_SUCCESS ? DA_OK : DA_ERR_CUDA;
+}
+
 constexpr int kMaxDevices = 128;
 
 // SM count of the current device, queried once per device.  Entries are
@@ -274,8 +287,6 @@ int encode_paged_maps(KParams& k, int kind, const void* kp, const void* vp, cons
 // [head][slice][key][128 bytes] with the 128-byte swizzle.
 int encode_pool_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize,
                     long long D, long long heads, long long rows, int box_rows, int kvb) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return DA_ERR_CUDA;
   const long long row_bytes = D * esize;
   cuuint64_t dims[4] = {(cuuint64_t)(128 / esize), (cuuint64_t)rows, (cuuint64_t)(row_bytes / 128),
                         (cuuint64_t)heads};
@@ -283,28 +294,24 @@ int encode_pool_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, in
   cuuint32_t box[4] = {(cuuint32_t)(128 / esize), (cuuint32_t)box_rows,
                        (cuuint32_t)(row_bytes / 128), (cuuint32_t)kvb};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  CUresult r = fn(m, dt, 4, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? DA_OK : DA_ERR_CUDA;
+  return encode_map(m, dt, 4u, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // 5-D map over the hot ring [B, cap, Hkv, D] f16, token dimension inside:
 //   dims {64, cap, D/64, Hkv, B}, box {64, box_rows, D/64, kvb, 1}.
 int encode_ring_map(CUtensorMap* m, const void* base, long long D, long long heads, long long cap,
                     long long B, int box_rows, int kvb) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return DA_ERR_CUDA;
   cuuint64_t dims[5] = {64, (cuuint64_t)cap, (cuuint64_t)(D / 64), (cuuint64_t)heads,
                         (cuuint64_t)B};
   cuuint64_t strides[4] = {(cuuint64_t)(heads * D * 2), 128, (cuuint64_t)(D * 2),
                            (cuuint64_t)(cap * heads * D * 2)};
   cuuint32_t box[5] = {64u, (cuuint32_t)box_rows, (cuuint32_t)(D / 64), (cuuint32_t)kvb, 1u};
   cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, const_cast<void*>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? DA_OK : DA_ERR_CUDA;
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5u, const_cast<void*>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Upper bound on pipeline stages: kMaxStages, or the tuning state's
@@ -706,8 +713,6 @@ da::PrefixWs prefix_workspace(const da_params* p, int T, int sms) {
 // with boxes of one kv head, min(block_size, tile) keys, and every 128-byte
 // slice of the row when one box is a whole tile (a tile is laid out [slice][key]).
 int encode_prefix_maps(da::PrefixParams& k, const da_params* p, const void* kp, const void* vp) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return DA_ERR_CUDA;
   const int D = p->head_dim, tile = da::prefix_tile_keys(D);
   k.box_rows = p->block_size < tile ? p->block_size : tile;
   k.box_slices = k.box_rows == tile ? D / 64 : 1;
@@ -716,13 +721,13 @@ int encode_prefix_maps(da::PrefixParams& k, const da_params* p, const void* kp, 
   cuuint64_t strides[3] = {(cuuint64_t)p->num_kv_heads * D * 2, 128, (cuuint64_t)D * 2};
   cuuint32_t box[4] = {64u, (cuuint32_t)k.box_rows, (cuuint32_t)k.box_slices, 1u};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  for (int i = 0; i < 2; ++i)
-    if (fn(i ? &k.tm_v : &k.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
-           const_cast<void*>(i ? vp : kp), dims, strides, box, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return DA_ERR_CUDA;
-  return DA_OK;
+  int st = DA_OK;
+  for (int i = 0; i < 2 && st == DA_OK; ++i)
+    st = encode_map(i ? &k.tm_v : &k.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4u,
+                    const_cast<void*>(i ? vp : kp), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return st;
 }
 
 // Decode over a shared prefix, T query tokens per sequence.

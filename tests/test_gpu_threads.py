@@ -105,3 +105,45 @@ def test_first_calls_from_four_threads_at_once(cuda_lib, tmp_path):
         assert flags == 0
         assert_parity(got[name + "_out"].reshape(-1, case.D), got[name + "_lse"].reshape(-1),
                       ref_out, ref_lse, name)
+
+
+@pytest.mark.parametrize("name", [*CASES, "prefix"])
+def test_a_threads_first_call_allocates_nothing(cuda_lib, name):
+    """A thread without a CUDA context of its own so far, every tensor of the
+    call made by another."""
+    import threading
+
+    import torch
+    import quantized_kv_decode_paged_gb300 as qk
+    case = CASES["paged" if name == "prefix" else name]()
+    t = case.device_tensors("cuda")
+    kw = dict(out=torch.zeros_like(t["q"]), lse=torch.zeros(t["q"].shape[:-1], device="cuda"),
+              workspace=torch.zeros(1 << 26, dtype=torch.uint8, device="cuda"),
+              max_seq_len=case.max_seq_len, stream=torch.cuda.current_stream())
+    if name.startswith("tiered"):
+        kw.update(hot_window=case.hot_window, cold_len=int(case.cold_lens[0]),
+                  hot_len=int(case.hot_lens[0]), hot_start=int(case.hot_starts[0]))
+        keys = ["q", "k_hot", "v_hot", "k_cold", "v_cold", "k_scale", "v_scale", "block_table"]
+        fn, keys = ((qk.decode_attn_tiered_f16, keys[:5] + keys[7:]) if case.cold_f16
+                    else (qk.decode_attn_tiered_int8, keys))
+    else:
+        fn, keys = qk.decode_attn_paged, ["q", "k_pool", "v_pool", "block_table", "seq_lens"]
+        if name == "prefix":
+            fn = lambda *a, **k: qk.decode_attn_paged_prefix(*a, 0, **k)  # noqa: E731
+    torch.cuda.synchronize()
+    errors = []
+
+    def work():
+        try:
+            fn(*(t[k] for k in keys), **kw)
+        except Exception as e:
+            errors.append(e)
+
+    thread = threading.Thread(target=work)
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert not errors
+    ref_out, ref_lse, _ = (oracle_tiered if name.startswith("tiered") else oracle_paged)(case)
+    assert_parity(kw["out"].cpu().numpy().reshape(-1, case.D), kw["lse"].cpu().numpy().reshape(-1),
+                  ref_out, ref_lse, name)
