@@ -433,6 +433,8 @@ int decode_attn_append_paged_rope(const da_params* p, const da_rope_params* r, i
  * workspace: device scratch of at least
  * decode_attn_paged_prefix_workspace_size(p, q_len, prefix_len) bytes, 256-byte
  * aligned, of any content; calls that overlap on the GPU must not share it.
+ * Calls of one stream may, also from several threads (a call's kernels are
+ * enqueued without another's between them).
  * Everything else as for decode_attn_paged.  DA_ERR_UNSUPPORTED also where a
  * launch's work would not count in 31 bits: rows, q_len * num_q_heads * 256
  * (144 for head_dim 256), or entries of its list of tiles,

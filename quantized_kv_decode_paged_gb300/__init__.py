@@ -1019,22 +1019,7 @@ def decode_attn_paged_prefix_workspace_size(params: DaParams, q_len: int, prefix
                                                                       int(q_len), int(prefix_len)))
 
 
-_prefix_ws: dict = {}  # (device, stream) -> workspace
 _prefix_ws_bytes: dict = {}  # (device, B, T, Hq, Hkv, D), all that it depends on -> its size
-
-
-def _prefix_workspace(torch, dev, raw, nbytes):
-    """The current stream's workspace, grown as needed.  Calls of one stream follow one
-    another; a call that is being captured gets its own, which lives in its
-    graph's memory: graphs may be replayed side by side."""
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    key = (dev.index, raw)
-    ws = _prefix_ws.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _prefix_ws[key] = ws
-    return ws
 
 
 def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_len,
@@ -1048,9 +1033,9 @@ def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_le
     first columns of block_table's row 0); those columns of block_table are not
     read.  seq_lens and q_pos include the prefix.  Returns (out, lse).
 
-    ``workspace``: "auto" (kept per stream; a captured call's own) or a
-    caller-owned uint8 tensor of decode_attn_paged_prefix_workspace_size bytes
-    (any content)."""
+    ``workspace``: "auto" (the call's own, from torch's allocator on the call's
+    stream; a captured call's in its graph's memory) or a caller-owned uint8
+    tensor of decode_attn_paged_prefix_workspace_size bytes (any content)."""
     if stream is None and isinstance(workspace, str) and workspace == "auto":
         y = (_call or _load_call()).prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_len,
                                            prefix_table, q_pos, scale, softcap, sliding_window,
@@ -1126,7 +1111,9 @@ def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_le
                 nbytes = lib.decode_attn_paged_prefix_workspace_size(ref, T, prefix_len)
                 if nbytes:  # the sizes are sound
                     _prefix_ws_bytes[key] = nbytes
-            workspace = _prefix_workspace(torch, dev, raw, nbytes)
+            # this call's alone: its kernels hand over through it, and other threads' calls may
+            # come between them in the stream
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         st = lib.decode_attn_paged_prefix(
             ref, T, prefix_len, prefix_table.data_ptr(), q.data_ptr(), k_pool.data_ptr(),
             v_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), _ptr(q_pos),

@@ -730,6 +730,14 @@ int encode_prefix_maps(da::PrefixParams& k, const da_params* p, const void* kp, 
   return st;
 }
 
+// A shared-prefix call is two kernels a launch, which hand over through the workspace: between them
+// in a stream no other call's may come that uses it.  Held while a call enqueues them (a lock a
+// workspace, or a few of them).
+std::mutex& workspace_mutex(const void* workspace) {
+  static std::mutex held[64];
+  return held[reinterpret_cast<uintptr_t>(workspace) * 0x9e3779b97f4a7c15ull >> 58];
+}
+
 // Decode over a shared prefix, T query tokens per sequence.
 int prefix_impl(const da_params* p, int T, int prefix_len, const int32_t* prefix_table,
                 const float* q, const uint16_t* k_pool, const uint16_t* v_pool,
@@ -794,6 +802,7 @@ int prefix_impl(const da_params* p, int T, int prefix_len, const int32_t* prefix
   k.ws_cut_o = reinterpret_cast<float*>(ws + w.cut_o);
   k.ws_pre_o = reinterpret_cast<float*>(ws + w.pre_o);
   const long long row = (long long)T * p->num_q_heads;
+  const std::lock_guard<std::mutex> unbroken(workspace_mutex(workspace));
   for (int b0 = 0; b0 < p->batch; b0 += chunk) {
     k.B = p->batch - b0 < chunk ? p->batch - b0 : chunk;
     k.row_tiles = (int)(((long long)k.B * k.R1 + da::kPrefixRows - 1) / da::kPrefixRows);

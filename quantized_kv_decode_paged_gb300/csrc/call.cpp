@@ -19,7 +19,6 @@
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 
-#include <map>
 #include <utility>
 
 #include "../../include/decode_attn.h"
@@ -231,21 +230,12 @@ PyObject* append(PyObject* const* a) {
   return qo.object();
 }
 
-// The workspace of a stream's calls, which follow one another.  Never freed: the device may be
-// gone when the process ends.
-void* workspace(int dev, void* stream, size_t bytes) {
-  static auto* kept = new std::map<std::pair<int, void*>, at::Tensor>();
-  at::Tensor& t = (*kept)[{dev, stream}];
-  if (!t.defined() || (size_t)t.numel() < bytes) t = empty({(int64_t)bytes}, at::kByte, dev);
-  return t.data_ptr();
-}
-
 // q, k_pool, v_pool, block_table, seq_lens, prefix_len, prefix_table, q_pos, scale, softcap,
 // sliding_window, causal, max_seq_len, out, lse, dev_status
 PyObject* prefix(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0]);
   const int dev = device(q);
-  // a captured call's workspace is its graph's
+  // captured calls go through Python
   need(c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None);
   need(q.dim() == 3 || q.dim() == 4);
   const at::Tensor &kp = tensor(a[1]), &vp = tensor(a[2]), &table = tensor(a[3]),
@@ -283,11 +273,11 @@ PyObject* prefix(PyObject* const* a) {
   need(bytes > 0);
   Output out(a[13], q.sizes(), at::kFloat, dev);
   Output lse(a[14], q.sizes().slice(0, q.dim() - 1), at::kFloat, dev);
-  void* stream = stream_of(dev);
-  void* ws = workspace(dev, stream, bytes);
+  // the call's own, as in Python; its memory goes to the stream's later calls
+  const at::Tensor ws = empty({(int64_t)bytes}, at::kByte, dev);
   const int st = prefix_fn(&p, i32(T), i32(len), pt, qp, kpp, vpp, tp, lp, pos,
-                           static_cast<float*>(out.p), static_cast<float*>(lse.p), ws, bytes, status,
-                           stream);
+                           static_cast<float*>(out.p), static_cast<float*>(lse.p), ws.data_ptr(),
+                           bytes, status, stream_of(dev));
   if (st != DA_OK) return PyLong_FromLong(st);
   return pair(out.object(), lse.object());
 }

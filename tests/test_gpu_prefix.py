@@ -651,3 +651,40 @@ def test_order_with_what_runs_before_and_after():
             for _ in range(20):
                 graph.replay()
             torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("path", ["C++", "Python", "own workspace"])
+def test_two_threads_on_one_stream(path):
+    """Calls of other sizes and inputs that go into the same stream at the same
+    time: each gets its own result, bit for bit."""
+    import threading
+    import torch
+    cases = [Case(64 + i, 7 + 30 * i, 8, 2, 128, 16, 1024 * (i + 1),
+                  1024 * (i + 1) + np.arange(7 + 30 * i) * 13 + 1) for i in range(2)]
+    stream = torch.cuda.Stream()
+    args = [[_t(x) for x in (c.q, c.k, c.v, c.table, c.lens)] + [c.prefix_len, _t(c.prefix_table)]
+            for c in cases]
+    kw = {}
+    if path != "C++":
+        kw["stream"] = stream
+    if path == "own workspace":
+        kw["workspace"] = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    got, start = [[], []], threading.Barrier(2)
+
+    def work(i):
+        with torch.cuda.stream(stream):
+            start.wait(60)
+            for _ in range(300):
+                got[i].append(qk.decode_attn_paged_prefix(*args[i], **kw))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    stream.synchronize()
+    for c, g in zip(cases, got):
+        assert len(g) == 300
+        c.check((g[0][0].cpu().numpy(), g[0][1].cpu().numpy(), 0))
+        assert all(torch.equal(a, g[0][0]) and torch.equal(b, g[0][1]) for a, b in g)

@@ -239,3 +239,50 @@ def test_binding_refuses_before_the_device(lib):
                           ((k, k, pos, table, pool, pool, f), {}, ValueError)):
         with pytest.raises(exc):
             qk.decode_attn_append_paged_rope(*args, **kw)
+
+
+# ------------------------------------------------------------------ the binding, up to the library
+class _Entry:
+    """Stands for an entry point of the library: keeps the calls' arguments."""
+
+    def __init__(self, then=lambda: None):
+        self.calls, self.then = [], then
+
+    def __call__(self, *args):
+        self.calls.append(args)
+        self.then()
+        return qk.DA_OK
+
+
+@pytest.fixture
+def on_host(lib, monkeypatch):
+    """The calls' Python path on CPU tensors, as far as a stand-in for the library."""
+    class Library:
+        decode_attn_paged_prefix = _Entry()
+
+        @staticmethod
+        def decode_attn_paged_prefix_workspace_size(*args):
+            return 4096
+
+    qk._load_call()  # leaves CPU tensors to Python
+    monkeypatch.setattr(qk, "_lib", Library)
+    monkeypatch.setattr(qk, "_check_cuda", lambda name, t: None)
+    monkeypatch.setattr(qk, "_call_guard", lambda *args: qk._NO_GUARD)
+    monkeypatch.setattr(qk, "_raw_stream", lambda *args: 0)
+    monkeypatch.setattr(qk, "_prefix_ws_bytes", {})
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return Library
+
+
+def test_calls_at_once_have_workspaces_of_their_own(on_host):
+    """Two threads inside the entry point at the same time, on one stream."""
+    import threading
+    both = threading.Barrier(2)
+    on_host.decode_attn_paged_prefix = entry = _Entry(lambda: both.wait(30))
+    threads = [threading.Thread(target=_cpu_prefix) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    a, b = [c[12] for c in entry.calls]
+    assert abs(a - b) >= 4096 and [c[13] for c in entry.calls] == [4096, 4096]
