@@ -6,8 +6,10 @@
 // r = 1/sqrt(mean(x^2) + eps).  Rotation of a pair by the angle a:
 // (y0 cos a - y1 sin a, y0 sin a + y1 cos a).  a = pos * f turns with f in
 // 64-bit fixed point: the low 64 bits of the integer product are the angle
-// modulo one turn, exact up to f's own 2^-56 turns a position (a double's).  The top 32 bits
-// as a signed number times 2^-31 are a / pi in [-1, 1), what sincospif takes.
+// modulo one turn, exact up to f's own 2^-56 turns a position (a double's).  Its distance from
+// the nearest quarter turn is rounded to f32, 2^-24 of a number of at most an eighth, and goes to
+// sincospif; the quarter turns swap and negate what comes back.  (The whole angle rounded to
+// f32 is off by 2^-25 of half a turn, 9.4e-8, which the small one of sine and cosine shows.)
 //
 // A CTA takes up to kMaxTokens tokens: their rd/2 cosines and sines are computed once
 // into shared memory and serve all the tokens' heads.  D/16 threads take a row, each
@@ -199,9 +201,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
   for (int i = threadIdx.x; i < tokens * (a.rd / 2); i += kRopeThreads) {
     const int t = i / (a.rd / 2), f = i - t * (a.rd / 2);
     const uint64_t turns = (uint64_t)(long long)a.positions[n0 + t] * a.freqs[f];
-    const float half_turns = (float)(int32_t)(turns >> 32) * 0x1p-31f;
+    // quarter turns, and the rest in [-1/8, 1/8) turns: rounded to f32 as a small number
+    const uint64_t quarter = (turns + (1ull << 61)) >> 62;
+    const float half_turns = __ll2float_rn((long long)(turns - (quarter << 62))) * 0x1p-63f;
+    float sn, cn;
+    sincospif(half_turns, &sn, &cn);
+    const float x = quarter & 1 ? -sn : cn, y = quarter & 1 ? cn : sn;
     float2* at = reinterpret_cast<float2*>(&cs[t][f % 8 / 2][f / 8]) + f % 2;
-    sincospif(half_turns, &at->y, &at->x);
+    *at = quarter & 2 ? make_float2(-x, -y) : make_float2(x, y);
   }
   if constexpr (APPEND) {
     if ((int)threadIdx.x < tokens) {

@@ -401,3 +401,39 @@ def test_weights_of_a_side_that_is_not_given_are_not_read():
     assert none is None and torch.isfinite(q).all()
     none, k = qk.decode_attn_qk_norm_rope(None, x, pos, f, q_weight=bad, k_weight=w)
     assert none is None and torch.isfinite(k).all()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_next_to_quarter_turns(interleaved):
+    """Sines and cosines as the rotation of (1, 0), to their own size: the smaller
+    one too, of angles at and next to every quarter of a turn and of any others.
+
+    a, the angle's distance from the nearest quarter turn, is rounded to f32
+    (2^-24 |a|), and sincospif's two results are within 2^-23 of themselves."""
+    import torch
+    rng = np.random.default_rng(31)
+    D = 256
+    near = [(k << 62) + s * (1 << e) for k in range(4) for e in (8, 30, 40, 52, 60) for s in (1, -1)]
+    some = [int(x) for x in rng.integers(0, 1 << 63, D // 2 - len(near) - 4) * 2]
+    turns = np.array([x % (1 << 64) for x in near + some + [k << 62 for k in range(4)]], np.uint64)
+    pos = np.array([1, 2, 3, -1, 5, 4097, 131071, 2 ** 31 - 1], np.int32)
+    q = torch.zeros(len(pos), 1, D, device="cuda")
+    lo, hi = ((slice(0, D, 2), slice(1, D, 2)) if interleaved
+              else (slice(0, D // 2), slice(D // 2, D)))
+    q[..., lo] = 1
+    out, _ = qk.decode_attn_qk_norm_rope(q, None, _t(pos), _t(turns.view(np.int64)), norm=False,
+                                         interleaved=interleaved)
+    with np.errstate(over="ignore"):
+        t = pos.astype(np.int64).view(np.uint64)[:, None] * turns
+        quarter = (t + np.uint64(1 << 61)) >> np.uint64(62)
+        a = (t - (quarter << np.uint64(62))).view(np.int64) * (2 * np.pi / 2.0 ** 64)
+    quarter = quarter.astype(int)
+    sin, cos, u = np.sin(a), np.cos(a), 2.0 ** -24
+    bs, bc = u * (np.abs(a) + 2 * np.abs(sin)), u * (np.abs(a * sin) + 2 * cos)
+    swap = quarter % 2 == 1
+    c, s = np.where(swap, -sin, cos), np.where(swap, cos, sin)
+    sign = np.where(quarter >= 2, -1, 1)
+    got = _np(out)[:, 0]
+    for what, have, want, bound in (("cos", got[:, lo], sign * c, np.where(swap, bs, bc)),
+                                    ("sin", got[:, hi], sign * s, np.where(swap, bc, bs))):
+        assert not (~(np.abs(have - want) <= bound)).any(), what
