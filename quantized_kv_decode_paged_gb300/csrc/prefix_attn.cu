@@ -813,11 +813,12 @@ __device__ __forceinline__ Row row_of(const PrefixParams& p, const PrefixSmem<D>
 
 // ------------------------------------------------------------------ Q
 // A row of Q is divided by the power of two that brings its largest value to [2^9, 2^10) and
-// held as two f16 terms.  Powers for a row whose largest value is m (the exponent
-// clamped so that both are normal): what it is multiplied by, and what undoes it.
+// held as two f16 terms.  Powers for a row whose largest value is m: what it is multiplied by,
+// and what undoes it.  The exponent is kept in [-100, 127], where both are normal: below, a row's
+// scores are next to nothing, above it is infinite.
 __device__ __forceinline__ void q_powers(float m, float& by, float& undo) {
   int e = (int)(__float_as_uint(m) >> 23) - 127;
-  e = min(max(e, -100), 120);
+  e = min(max(e, -100), 127);
   by = __uint_as_float((uint32_t)(9 - e + 127) << 23);
   undo = __uint_as_float((uint32_t)(e - 9 + 127) << 23);
 }

@@ -688,3 +688,14 @@ def test_two_threads_on_one_stream(path):
         assert len(g) == 300
         c.check((g[0][0].cpu().numpy(), g[0][1].cpu().numpy(), 0))
         assert all(torch.equal(a, g[0][0]) and torch.equal(b, g[0][1]) for a, b in g)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_queries_next_to_the_largest_f32(D):
+    """Rows whose largest value is past 2^127; every key is seen by every row."""
+    c = Case(72, 3, 8, 2, D, 16, 256, [384, 384, 384])
+    c.q *= 1e37
+    c.q[..., 5] = np.where(c.q[..., 5] < 0, -3e38, 3e38)
+    c.k = (c.k.astype(np.float32) / 64).astype(np.float16)
+    c.kw = dict(scale=2e-38)
+    c.check()
