@@ -129,41 +129,62 @@ __device__ __forceinline__ int page_of(const PrefixParams& p, int b, int k) {
                             : p.block_table[(long long)b * p.max_blocks + c];
 }
 
-// One warp's state of a row over keys [k0, k1), key by key: lane i holds the
-// values [i * D/32, (i + 1) * D/32) of q and o.  Pages outside the pool are masked.
+// One warp's state of a row over keys [k0, k1), four keys a step: lane i holds the values
+// [i * D/32, (i + 1) * D/32) of q and o.  Pages outside the pool are masked: neither their keys nor
+// their values count.  Ends early where the sum is NaN (a query that is not finite, a NaN key):
+// nothing behind changes the row any more.
 template <int D>
 __device__ __noinline__ void attend_row(const PrefixParams& p, int b, int kv, const float (&q)[D / 32], int k0,
                            int k1, float& m, float& l, float (&o)[D / 32]) {
-  constexpr int V = D / 32;
+  constexpr int V = D / 32, N = 4;
   const int lane = threadIdx.x & 31;
   m = -kInf;
   l = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.f;
-  for (int k = k0; k < k1; ++k) {
-    const int blk = page_of(p, b, k);
-    if (blk < 0 || blk >= p.num_blocks) continue;
-    const long long at =
-        ((((long long)blk << p.log2_bs) + (k & (p.bs - 1))) * p.Hkv + kv) * D + lane * V;
-    float s = 0.f;
+#pragma unroll 1
+  for (int k = k0; k < k1 && !isnan(l); k += N) {
+    long long at[N];
+    bool ok[N];
+    float s[N];
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(p.k_pool + at + i));
-      s = fmaf(q[i], x.x, fmaf(q[i + 1], x.y, s));
+    for (int u = 0; u < N; ++u) {
+      const int key = min(k + u, k1 - 1), blk = page_of(p, b, key);
+      ok[u] = k + u < k1 && (uint32_t)blk < (uint32_t)p.num_blocks;
+      at[u] = ((((long long)(ok[u] ? blk : 0) << p.log2_bs) + (key & (p.bs - 1))) * p.Hkv + kv) * D +
+              lane * V;
+      s[u] = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(p.k_pool + at[u] + i));
+        s[u] = fmaf(q[i], x.x, fmaf(q[i + 1], x.y, s[u]));
+      }
     }
+    float mn = m;
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= p.qscale;
-    if (p.softcap2 > 0.f) s = cap_any(s * p.softcap_inv, p.softcap2);
-    const float mn = fmaxf(m, s);
+    for (int u = 0; u < N; ++u) {
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], off);
+      s[u] *= p.qscale;
+      if (p.softcap2 > 0.f) s[u] = cap_any(s[u] * p.softcap_inv, p.softcap2);
+      if (!ok[u]) s[u] = -kInf;
+      mn = fmaxf(mn, s[u]);
+    }
     const float base = mn == -kInf ? 0.f : mn;
-    const float f = exp2f(m - base), w = exp2f(s - base);
-    l = fmaf(l, f, w);
+    const float f = exp2f(m - base);
+    l *= f;
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(p.v_pool + at + i));
-      o[i] = fmaf(o[i], f, w * x.x);
-      o[i + 1] = fmaf(o[i + 1], f, w * x.y);
+    for (int i = 0; i < V; ++i) o[i] *= f;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const float w = exp2f(s[u] - base);
+      l += w;
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(p.v_pool + at[u] + i));
+        o[i] = ok[u] ? fmaf(w, x.x, o[i]) : o[i];
+        o[i + 1] = ok[u] ? fmaf(w, x.y, o[i + 1]) : o[i + 1];
+      }
     }
     m = mn;
   }
