@@ -99,8 +99,7 @@ struct alignas(128) PrefixParams {
   float* lse;
   int* dev_status;
   // workspace (PrefixWs).  A state is o (not divided by l), and (m, l): the
-  // reference the weights were taken against, base 2, and their sum, negative when
-  // some key of its tiles was masked for the row.
+  // reference the weights were taken against, base 2, and their sum.
   int* ws_plan;       // PrefixPlan, then [B + 1] entries of the own list before b's
   float2* ws_cut_ml;  // [grid][2][128] of a prefix unit's part, [grid][2][own_rows] of an own one's
   float2* ws_pre_ml;  // [B * T * Hq] of the prefix, units that no CTA boundary cuts

@@ -805,7 +805,6 @@ struct Row {
   int place;          // in [B, T, Hq]; of the part's nearest row where the thread has none
   float scale;        // of its scores, base 2
   float m, l;         // running maximum, and the sum of the weights against it
-  bool partial;       // it met a tile some key of which was masked (for a row of its warp)
 };
 // Its place (of sequence b, query token tok).
 template <int D>
@@ -817,7 +816,7 @@ __device__ __forceinline__ int row_place(const PrefixParams& p, const Part<D>& c
 template <int D>
 __device__ __forceinline__ Row row_of(const PrefixParams& p, const PrefixSmem<D>& s,
                                       const Part<D>& c, int w, int place, int b, int tok) {
-  Row r = {false, false, 0, 0, place, 0.f, -kInf, 0.f, false};
+  Row r = {false, false, 0, 0, place, 0.f, -kInf, 0.f};
   const int first = c.lane0(), row = w * 32 + (int)(threadIdx.x & 31);
   r.any = w * 32 + 32 > first && w * 32 < first + c.nr;
   r.on = row >= first && row < first + c.nr;
@@ -1021,7 +1020,6 @@ __device__ __forceinline__ bool softmax_tile(const PrefixParams& p, PrefixSmem<D
     const int bad = s.bad[x & 15];
     const bool masked =
         !__all_sync(0xffffffffu, (!r.on || (r.lo <= k0 && r.hi >= k0 + KT)) && bad == 0);
-    r.partial |= masked;
     const float to_y = r.scale * p.softcap_inv;
     // Two passes over the scores, W or 32 columns a step: loops that stay in the
     // instruction cache and need few registers.
@@ -1144,7 +1142,7 @@ __device__ __forceinline__ void store_ml(const PrefixParams& p, const Part<D>& c
     dst = p.ws_cut_ml + c.slot + w * 32 + (int)(threadIdx.x & 31) - c.lane0();
   else
     dst = (c.b < 0 ? p.ws_pre_ml : p.ws_own_ml) + r.place;
-  *dst = make_float2(r.m - kShift, r.partial ? -r.l : r.l);
+  *dst = make_float2(r.m - kShift, r.l);
 }
 
 // One group, Q in shared memory (D = 256).
@@ -1223,7 +1221,7 @@ __device__ void softmax_loop_two(const PrefixParams& p, PrefixSmem<D>& s) {
       // the group of the part's last tile adds the other's sum to its own
       float* slot = s.l + q * kPrefixRows + row;
       if (!last) {
-        *slot = r.partial ? -r.l : r.l;
+        *slot = r.l;
         s.m_last[q * kPrefixRows + row] = r.m;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.l_ready[q][w]);
@@ -1233,8 +1231,7 @@ __device__ void softmax_loop_two(const PrefixParams& p, PrefixSmem<D>& s) {
       if (!warp_wait<D>(p, s, &s.l_ready[q][w], shared_sums[q] & 1)) return;
       ++shared_sums[q];
       const float lx = *slot, mx = s.m_last[q * kPrefixRows + row];
-      r.partial |= signbit(lx) != 0;
-      r.l = fmaf(fabsf(lx), ex2_ftz(mx - (r.m == -kInf ? 0.f : r.m)), r.l);
+      r.l = fmaf(lx, ex2_ftz(mx - (r.m == -kInf ? 0.f : r.m)), r.l);
     } else if (!last) {
       continue;  // the one tile was the other group's
     }
@@ -1632,7 +1629,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int c1 = n1 ? own_at(g1 + kOwnExtra) : 0;
   const int s1 = n1 ? own_at(g1 + n1 - 1) - c1 + 1 : 0;
   float M = -kInf, L = 0.f, o[V];
-  bool partial = false;
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.f;
   for (int j0 = 0; j0 < s0 + s1; j0 += 32) {
@@ -1667,7 +1663,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       }
     }
     const float2 v = ml ? *ml : make_float2(-kInf, 0.f);
-    partial |= __any_sync(0xffffffffu, signbit(v.y) != 0);
     const bool some = v.y != 0.f;  // has a key
     float top = some ? v.x : -kInf;
 #pragma unroll
@@ -1675,7 +1670,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const float mn = fmaxf(M, top);
     if (mn == -kInf && !__any_sync(0xffffffffu, some)) continue;
     const float f = ex2_ftz(M - mn), w = some ? ex2_ftz(v.x - mn) : 0.f;
-    float l = w * fabsf(v.y);
+    float l = w * v.y;
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
     L = fmaf(L, f, l);
@@ -1707,12 +1702,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     for (; n - u0 > 4; u0 += 8) add(u0, std::integral_constant<int, 8>());
     if (u0 < n) add(u0, std::integral_constant<int, 4>());
   }
-  // A zero weight does not silence a value that is not finite: a row that met masked keys
-  // and came out non-finite is done again, key by key.
+  // A masked key's weight of zero does not silence a value that is not finite, and two terms make NaN
+  // of an infinite product that one would leave infinite: a row that came out non-finite is done
+  // again, key by key.
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < V; ++i) bad |= !isfinite(o[i]);
-  if (__any_sync(0xffffffffu, partial && bad)) {
+  if (__any_sync(0xffffffffu, bad)) {
     int len, qp, lo, hi;
     seq_info(p, b, len, qp);
     key_range(p, len, qp, tok, tok, lo, hi);

@@ -728,3 +728,39 @@ def test_a_query_that_is_not_finite_takes_no_longer():
     assert torch.isnan(out[1]).all() and torch.isnan(out[2, 3]).any()
     assert torch.equal(out[[0, 3]], want[[0, 3]])
     assert tb <= 10 * t, f"{tb:.0f} us against {t:.0f}"
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens", [(384, 384, 384), (384, 380, 300)])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_visible_infinities(D, lens, softcap):
+    """Keys whose scores are -inf have weight 0 (with a softcap that of the cap),
+    infinite values are infinite in their column alone, whether or not the row
+    meets tiles with masked keys."""
+    def case():
+        c = Case(74, 3, 8, 2, D, 16, 256, lens)
+        c.kw = dict(softcap=softcap)
+        c.q[..., 5] = np.abs(c.q[..., 5]) + 0.5
+        return c
+
+    c, d = case(), case()
+    bounds = d.bounds()
+    for b, t in ((0, 3), (0, 200), (0, 300), (1, 299)):
+        at = c.full[b, t // 16], t % 16
+        c.k[at][..., 5] = -np.inf
+        # of the oracle: scores of -0.5 * 60000 / 16 and less, their weight e^-1800 of the others', and
+        # a tanh that rounds to -1
+        d.k[at][..., 5] = -60000
+    for b, t, col, x in ((0, 7, 9, np.inf), (0, 310, 11, -np.inf)):
+        at = c.full[b, t // 16], t % 16
+        c.v[at][..., col] = x
+        d.v[at][..., col] = 0
+    out, lse, fl = c.run()
+    ro, rl, rf = d.want()
+    assert fl == rf == 0
+    assert (out[..., 9] == np.inf).all()
+    assert (out[0, :, 11] == -np.inf).all()
+    keep = np.ones(out.shape, bool)
+    keep[..., 9] = keep[0, :, 11] = False
+    assert not (~(np.abs(out - ro.reshape(out.shape)) <= bounds[0]))[keep].any()
+    assert not (~(np.abs(lse - rl.reshape(lse.shape)) <= bounds[1] + 1e-6)).any()
