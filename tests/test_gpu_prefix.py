@@ -764,3 +764,81 @@ def test_visible_infinities(D, lens, softcap):
     keep[..., 9] = keep[0, :, 11] = False
     assert not (~(np.abs(out - ro.reshape(out.shape)) <= bounds[0]))[keep].any()
     assert not (~(np.abs(lse - rl.reshape(lse.shape)) <= bounds[1] + 1e-6)).any()
+
+
+# rows of a kv head: few enough for one warp's lanes in the prefix and own keys; two tiles of the
+# prefix, one of them full
+ROWS = [(2, 2), (40, 4)]
+
+
+@pytest.mark.parametrize("B,Hq", ROWS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_low_terms_of_queries(D, B, Hq):
+    """Scores that live in the low bits of q: neighbouring values of every key
+    cancel, k = +-64, and q_d = 1 + s_d 2^-12, so a score is scale * 2^-12 *
+    sum s_d k_d, at most sqrt(D) / 64.  f16 alone sees no difference between keys."""
+    r = np.random.default_rng(75)
+    c = Case(75, B, Hq, 1, D, 16, 128, 128 + r.integers(1, 14, B))
+    k = np.where(r.random(c.k.shape) < 0.5, 1, -1)
+    k[..., 1::2] = -k[..., ::2]
+    c.k = (64 * k).astype(np.float16)
+    c.q = (1 + np.where(r.random(c.q.shape) < 0.5, 1, -1) * 2.0 ** -12).astype(np.float32)
+    out, _, _ = c.run()
+    ro = c.want()[0].reshape(out.shape)
+    # the products of q's high term cancel within each sum of 16; those of its low one stay below
+    # D / 64: D / 16 truncating adds of 2^-23 of that a term, and the products with the scale
+    eps = (D / 64) * (D / 8 + 4) * 2.0 ** -23 / np.sqrt(D)
+    tol = np.abs(c.v.astype(np.float64)).max() * (2 * eps + (142 / 8 + 40) * 2.0 ** -23)
+    assert np.abs(out - ro).max() <= tol
+    # what scores of zero would give
+    flat = np.stack([c.v[c.full[b]].reshape(-1, D)[:c.lens[b]].astype(np.float64).mean(0)
+                     for b in range(B)])[:, None]
+    assert np.abs(ro - flat).max((1, 2)).min() > 20 * tol
+
+
+@pytest.mark.parametrize("B,Hq", ROWS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("own", [False, True])
+def test_low_terms_of_weights(D, B, Hq, own):
+    """Weights next to each other against opposite values, in the prefix's keys
+    or in own ones: 31 keys of weight w = e^(-2^-9 / sqrt(D)) and value 1, one
+    of weight 1 and value -31, and a key of weight w and value 0 beside them."""
+    c = Case(76, B, Hq, 1, D, 16, 32, np.full(B, 33 if not own else 64 + 32), junk=False)
+    c.q[:] = 0
+    c.q[..., 0] = 1
+    c.k[:], c.v[:] = 0, 0
+    for b in range(B):
+        at = c.full[b, :2] if not own else c.full[b, 2:4]
+        c.v[at] = 1
+        c.v[at[0], 3] = -31
+        c.k[at[0], 3, :, 0] = np.float16(2.0 ** -9)
+    out, _, _ = c.run()
+    ro = c.want()[0].reshape(out.shape)
+    n = int(c.lens[0])
+    # a weight is 2^x, good to 2^-22, in two terms, 2^-22: 62 of them times 2^-21 over n, and n / 8
+    # + 32 adds of 2^-23 of partial sums of at most 31 / n
+    tol = 62 / n * 2.0 ** -21 + (n / 8 + 32) * 2.0 ** -23 * 31 / n
+    assert np.abs(out - ro).max() <= tol
+    # one f16 term: every weight is 1, and the sum 0
+    assert np.abs(ro).min() > 10 * tol
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,prefix,most", [(1, 1000, 60), (1, 96, 900), (4, 4096, 40)])
+def test_errors_are_those_of_f32(D, T, prefix, most):
+    """The root mean square of the error against that of the result, for
+    normal inputs.
+
+    A score: q's terms leave 2^-23 of the row's largest value, 4.5 of its
+    deviation at most, in each of D products of deviation 1 / sqrt(D): 5.4e-7; its 2 D / 16
+    truncating adds leave half of 2^-23 of a sum of order 1 each, D / 8 * 6e-8, up to 1.9e-6
+    for D = 256.  Values: up to 16 such adds of 2^-23 in a group of two tiles, 1e-6 (D = 64:
+    32 and 1.9e-6).  Together 4.5e-6 at most, counted as 2^-17 = 7.6e-6.  One f16 term of q or of
+    the weights leaves 2^-12 or more: 30 times that."""
+    r = np.random.default_rng(77)
+    c = Case(77, 6, 16, 2, D, 16, prefix, _lens(r, 6, prefix, most) + T - 1, T=T)
+    out, lse, _ = c.run()
+    ro, rl, _ = c.want()
+    rms = lambda x: np.sqrt(np.mean(np.square(x.astype(np.float64))))  # noqa: E731
+    assert rms(out - ro.reshape(out.shape)) <= 2.0 ** -17 * rms(ro)
+    assert rms(lse - rl.reshape(lse.shape)) <= 2.0 ** -17 * max(1.0, rms(rl))
