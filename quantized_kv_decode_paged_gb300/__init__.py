@@ -18,6 +18,7 @@ import importlib.machinery
 import importlib.util
 import os
 import threading
+import warnings
 from typing import Optional
 
 from . import _build
@@ -745,6 +746,16 @@ def decode_attn_append_tiered_f16(k_new, v_new, k_hot, v_hot, k_cold, v_cold, bl
 _call = None
 
 
+class _NoCall:
+    """Stands for the C++ module where there is none: every call is left to Python."""
+
+    @staticmethod
+    def norm_rope(*args):
+        return NotImplemented
+
+    append = prefix = norm_rope
+
+
 def _load_call():
     """The C++ module that takes the common case of the calls below (csrc/call.cpp)."""
     global _call
@@ -752,17 +763,21 @@ def _load_call():
     with _lock:
         if _call is None:
             _torch()  # its libraries are the module's
-            path = _build.CALL_PATH
-            if not os.path.exists(path):
-                raise RuntimeError(f"{path} is missing: build it first "
-                                   "(quantized_kv_decode_paged_gb300.build())")
-            loader = importlib.machinery.ExtensionFileLoader("decode_attn_call", path)
-            spec = importlib.util.spec_from_file_location("decode_attn_call", path, loader=loader)
-            module = importlib.util.module_from_spec(spec)
-            loader.exec_module(module)
-            module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-                lib.decode_attn_qk_norm_rope, lib.decode_attn_append_paged_rope,
-                lib.decode_attn_paged_prefix, lib.decode_attn_paged_prefix_workspace_size)))
+            path = _build.call_path()
+            try:
+                loader = importlib.machinery.ExtensionFileLoader("decode_attn_call", path)
+                spec = importlib.util.spec_from_file_location("decode_attn_call", path,
+                                                              loader=loader)
+                module = importlib.util.module_from_spec(spec)
+                loader.exec_module(module)
+                module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                    lib.decode_attn_qk_norm_rope, lib.decode_attn_append_paged_rope,
+                    lib.decode_attn_paged_prefix, lib.decode_attn_paged_prefix_workspace_size)))
+            except ImportError as e:
+                warnings.warn("the norm, append and shared-prefix calls go through Python, slower: "
+                              f"no {path} (quantized_kv_decode_paged_gb300.build() makes it): {e}",
+                              RuntimeWarning)
+                module = _NoCall
             _call = module
     return _call
 

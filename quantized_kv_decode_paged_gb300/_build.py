@@ -2,18 +2,21 @@
 
 The translation units are compiled in parallel and linked into one shared
 library next to this file (``_lib/libdecode_attn.so``).  Beside it the host
-compiler makes ``_lib/decode_attn_call.so``, the Python module that marshals
-the calls that take torch tensors in C++.  A rebuild happens only when a source
-or header is newer than what it makes.
+compiler makes ``_lib/decode_attn_call.torch<version><ABI tag>.so``, the Python
+module that marshals the calls that take torch tensors in C++.  Only it needs
+torch: the library is there without it, and the calls then go through Python.
+A rebuild happens only when a source or header is newer than what it makes.
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -24,7 +27,6 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libdecode_attn.so")
 CALL_SRC = os.path.join(CSRC, "call.cpp")
-CALL_PATH = os.path.join(LIB_DIR, "decode_attn_call.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -52,10 +54,24 @@ def _newer(path, deps) -> bool:
     return all(os.path.getmtime(f) <= t for f in deps)
 
 
+def call_path():
+    """Where the marshalling module for this interpreter and its torch is, or
+    belongs; None without torch."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        import torch
+        version = torch.__version__
+    return os.path.join(LIB_DIR, f"decode_attn_call.torch{version}"
+                                 + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
 def _call_up_to_date() -> bool:
-    torch = importlib.util.find_spec("torch")  # another torch, another module
-    return _newer(CALL_PATH, [CALL_SRC, os.path.join(INCLUDE, "decode_attn.h"),
-                              os.path.abspath(__file__)] + ([torch.origin] if torch else []))
+    path = call_path()
+    return path is None or _newer(path, [CALL_SRC, os.path.join(INCLUDE, "decode_attn.h"),
+                                         os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
@@ -63,14 +79,23 @@ def up_to_date() -> bool:
 
 
 def _build_call() -> None:
-    """The marshalling module, against this interpreter's torch."""
+    """The marshalling module, against this interpreter's torch.  Where it
+    cannot be made, the calls do without it: a warning says why."""
+    try:
+        _compile_call(call_path())
+    except Exception as e:
+        warnings.warn(f"the norm, append and shared-prefix calls go through Python, slower: {e}",
+                      RuntimeWarning)
+
+
+def _compile_call(path) -> None:
     import torch
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     top = os.path.dirname(os.path.abspath(torch.__file__))
     include = [sysconfig.get_paths()["include"], os.path.join(top, "include"),
                os.path.join(top, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), INCLUDE]
-    tmp = CALL_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[x for d in include for x in ("-I", d)], CALL_SRC, "-o", tmp,
@@ -79,17 +104,17 @@ def _build_call() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for {CALL_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALL_PATH)
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile every CUDA translation unit and link libdecode_attn.so; make the
-    marshalling module."""
+    marshalling module if there is a torch."""
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(OBJ_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
-    stale = force or not _call_up_to_date()
+    stale = call_path() is not None and (force or not _call_up_to_date())
     if not force and _newer(LIB_PATH, _deps()):
         _build_call()
         return LIB_PATH
