@@ -809,7 +809,8 @@ def _raw_stream(torch, dev, stream):
 
 def _plain(t, dtype, device, ndim):
     """Whether _req accepts t: asked first, because it costs a tenth of it."""
-    return t.dtype is dtype and t.device == device and t.dim() == ndim and t.is_contiguous()
+    return (getattr(t, "dtype", None) is dtype and t.device == device and t.dim() == ndim
+            and t.is_contiguous())
 
 
 def decode_attn_rope_freqs(rotary_dim, theta=10000.0, *, inv_freq=None, device="cuda"):

@@ -286,3 +286,24 @@ def test_calls_at_once_have_workspaces_of_their_own(on_host):
         t.join()
     a, b = [c[12] for c in entry.calls]
     assert abs(a - b) >= 4096 and [c[13] for c in entry.calls] == [4096, 4096]
+
+
+def test_binding_names_arguments_that_are_no_tensors(lib):
+    q, k = torch.zeros(3, 8, 64), torch.zeros(3, 2, 64)
+    pos, f = torch.zeros(3, dtype=torch.int32), qk.decode_attn_rope_freqs(64, device="cpu")
+    pool, table = torch.zeros(8, 16, 2, 64, dtype=torch.float16), torch.zeros(3, 4, dtype=torch.int32)
+    for name in ("positions", "freqs", "q_weight", "k_weight", "q_out"):
+        args = dict(q=q, k=k, positions=pos, freqs=f)
+        args[name] = [0, 1, 2]
+        with pytest.raises(TypeError, match=name):
+            qk.decode_attn_qk_norm_rope(**args)
+    for name in ("v_new", "positions", "block_table", "k_pool", "v_pool", "freqs", "token_seq",
+                 "dev_status"):
+        args = dict(k_new=k, v_new=k, positions=pos, block_table=table, k_pool=pool, v_pool=pool,
+                    freqs=f)
+        args[name] = [0, 1, 2]
+        with pytest.raises(TypeError, match=name):
+            qk.decode_attn_append_paged_rope(**args)
+    for name in ("k_pool", "v_pool", "block_table", "seq_lens", "prefix_table", "q_pos", "out"):
+        with pytest.raises(TypeError, match=name):
+            _cpu_prefix(**{name: [0, 1]})
