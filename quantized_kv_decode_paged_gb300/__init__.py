@@ -1085,7 +1085,7 @@ def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_le
         if q_pos.shape[0] != B:
             raise ValueError("inconsistent shapes")
     prefix_len = int(prefix_len)
-    pages = prefix_len // bs
+    pages = prefix_len // bs if bs else 0  # pools without rows: refused below
     if prefix_table is None:
         prefix_table = block_table  # its first row
     else:

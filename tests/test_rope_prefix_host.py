@@ -264,6 +264,8 @@ def on_host(lib, monkeypatch):
         def decode_attn_paged_prefix_workspace_size(*args):
             return 4096
 
+        decode_attn_status_string = lib.decode_attn_status_string
+
     qk._load_call()  # leaves CPU tensors to Python
     monkeypatch.setattr(qk, "_lib", Library)
     monkeypatch.setattr(qk, "_check_cuda", lambda name, t: None)
@@ -307,3 +309,10 @@ def test_binding_names_arguments_that_are_no_tensors(lib):
     for name in ("k_pool", "v_pool", "block_table", "seq_lens", "prefix_table", "q_pos", "out"):
         with pytest.raises(TypeError, match=name):
             _cpu_prefix(**{name: [0, 1]})
+
+
+def test_pools_without_rows_are_refused(on_host):
+    on_host.decode_attn_paged_prefix = lambda *args: qk.DA_ERR_INVALID
+    pool = torch.zeros(8, 0, 2, 64, dtype=torch.float16)
+    with pytest.raises(qk.DecodeAttnError):
+        _cpu_prefix(k_pool=pool, v_pool=pool)
