@@ -365,8 +365,8 @@ typedef struct {
 /*
  * decode_attn_rope_freqs — host function: fills freqs[0 .. rotary_dim/2) with
  * inv_freq[i] / (2 pi) turns in units of 2^-64, rounded to nearest; inv_freq
- * (HOST, radians per position, finite) or, when NULL, theta^(-2i/rotary_dim)
- * with theta > 0.  The caller copies them to the device.
+ * (HOST, radians per position) or, when NULL, theta^(-2i/rotary_dim) with
+ * theta > 0, every one of them finite.  The caller copies them to the device.
  */
 int decode_attn_rope_freqs(int32_t rotary_dim, double theta, const double* inv_freq,
                            uint64_t* freqs);

@@ -378,10 +378,11 @@ int decode_attn_rope_freqs(int32_t rotary_dim, double theta, const double* inv_f
                            uint64_t* freqs) {
   if (rotary_dim < 0 || rotary_dim % 2 != 0 || (rotary_dim > 0 && !freqs)) return DA_ERR_INVALID;
   if (!inv_freq && !(theta > 0.0 && isfinite(theta))) return DA_ERR_INVALID;
-  for (int i = 0; inv_freq && i < rotary_dim / 2; ++i)
-    if (!isfinite(inv_freq[i])) return DA_ERR_INVALID;
+  auto radians = [&](int i) { return inv_freq ? inv_freq[i] : pow(theta, -2.0 * i / rotary_dim); };
+  for (int i = 0; i < rotary_dim / 2; ++i)
+    if (!isfinite(radians(i))) return DA_ERR_INVALID;  // a power may overflow too
   for (int i = 0; i < rotary_dim / 2; ++i) {
-    const double w = inv_freq ? inv_freq[i] : pow(theta, -2.0 * i / rotary_dim);
+    const double w = radians(i);
     // the fraction of a turn, in [0, 1); whole turns a position drop out
     double t = w / 6.283185307179586476925286766559;
     t -= floor(t);

@@ -316,3 +316,9 @@ def test_pools_without_rows_are_refused(on_host):
     pool = torch.zeros(8, 0, 2, 64, dtype=torch.float16)
     with pytest.raises(qk.DecodeAttnError):
         _cpu_prefix(k_pool=pool, v_pool=pool)
+
+
+def test_rope_freqs_refuse_a_power_that_overflows(lib):
+    with pytest.raises(qk.DecodeAttnError):
+        qk.decode_attn_rope_freqs(128, 5e-324, device="cpu")
+    assert qk.decode_attn_rope_freqs(128, 1e-300, device="cpu").numel() == 64
