@@ -795,6 +795,8 @@ def _call_guard(torch, dev, stream):
     allocates then belongs to that stream, and no memory is taken that another
     stream's pending work still uses."""
     if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream must be on {dev}, got {stream.device}")
         return torch.cuda.stream(stream)
     return _NO_GUARD if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 

@@ -322,3 +322,12 @@ def test_rope_freqs_refuse_a_power_that_overflows(lib):
     with pytest.raises(qk.DecodeAttnError):
         qk.decode_attn_rope_freqs(128, 5e-324, device="cpu")
     assert qk.decode_attn_rope_freqs(128, 1e-300, device="cpu").numel() == 64
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Its kernels would get pointers of a device that is not theirs."""
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="cuda:1"):
+        qk._call_guard(torch, torch.device("cuda", 0), Stream())
