@@ -1047,9 +1047,13 @@ def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_le
     """decode_attn_paged (q [B, Hq, D]) or decode_attn_paged_multi (q [B, T, Hq,
     D]) for a batch whose sequences all start with the same prefix_len keys:
     the shared pages are read once for the batch.  The whole pages of the
-    prefix come from prefix_table (i32 [prefix_len // block_size]; None: the
-    first columns of block_table's row 0); those columns of block_table are not
-    read.  seq_lens and q_pos include the prefix.  Returns (out, lse).
+    prefix come from prefix_table (i32 [prefix_len // block_size]); those columns
+    of block_table are not read.  None: the pages are the first columns of
+    block_table's row 0, which then holds all of them whatever sequence 0 is, also
+    where its slot is empty or it is shorter than the prefix (name a prefix_table
+    where it does not: a page outside the pool is masked for every sequence, and
+    only dev_status tells).  seq_lens and q_pos include the prefix.  Returns (out,
+    lse).
 
     ``workspace``: "auto" (the call's own, from torch's allocator on the call's
     stream; a captured call's in its graph's memory) or a caller-owned uint8

@@ -842,3 +842,20 @@ def test_errors_are_those_of_f32(D, T, prefix, most):
     rms = lambda x: np.sqrt(np.mean(np.square(x.astype(np.float64))))  # noqa: E731
     assert rms(out - ro.reshape(out.shape)) <= 2.0 ** -17 * rms(ro)
     assert rms(lse - rl.reshape(lse.shape)) <= 2.0 ** -17 * max(1.0, rms(rl))
+
+
+def test_prefix_of_row_0_whatever_its_sequence_is():
+    """Without a prefix_table row 0 holds the prefix's pages, its slot empty or its
+    sequence short; pages that it lacks are masked for all and flagged."""
+    import torch
+    for first in (0, 3, 100):
+        c = Case(78, 4, 8, 2, 128, 16, 320, [first, 400, 321, 350], junk=False)
+        c.table[1:, :20] = -1  # not read
+        args = [_t(x) for x in (c.q, c.k, c.v, c.table, c.lens)]
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = qk.decode_attn_paged_prefix(*args, 320, dev_status=status)
+        c.check((out.cpu().numpy(), lse.cpu().numpy(), int(status.item())))
+        args[3][0, 7] = -1
+        c.full[:, 7] = -1
+        out, lse = qk.decode_attn_paged_prefix(*args, 320, dev_status=status)
+        c.check((out.cpu().numpy(), lse.cpu().numpy(), int(status.item())), flags=qk.DEV_BAD_BLOCK)
