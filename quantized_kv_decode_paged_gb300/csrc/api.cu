@@ -15,6 +15,29 @@
 #include "kernel_params.h"
 #include "launch.h"
 
+namespace da {
+
+constexpr int kMaxDevices = 128;
+
+// SM count of the current device, queried once per device.  Entries are
+// atomics: host threads making their first call together each store the same
+// value.
+int device_sms(int* sms_out) {
+  static std::atomic<int> sms[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DA_ERR_CUDA;
+  int v = sms[dev].load(std::memory_order_relaxed);
+  if (v == 0) {
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+      return DA_ERR_CUDA;
+    sms[dev].store(v, std::memory_order_relaxed);
+  }
+  *sms_out = v;
+  return DA_OK;
+}
+
+}  // namespace da
+
 namespace {
 
 using da::KParams;
@@ -50,25 +73,6 @@ int encode_map(Args... args) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return DA_ERR_CUDA;
   return fn(args...) == CUDA_SUCCESS ? DA_OK : DA_ERR_CUDA;
-}
-
-constexpr int kMaxDevices = 128;
-
-// SM count of the current device, queried once per device.  Entries are
-// atomics: host threads making their first call together each store the same
-// value.
-int device_sms(int* sms_out) {
-  static std::atomic<int> sms[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DA_ERR_CUDA;
-  int v = sms[dev].load(std::memory_order_relaxed);
-  if (v == 0) {
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
-      return DA_ERR_CUDA;
-    sms[dev].store(v, std::memory_order_relaxed);
-  }
-  *sms_out = v;
-  return DA_OK;
 }
 
 // Process-wide tuning state.  Its initial values are read from the
@@ -413,7 +417,7 @@ template <typename OffsetFn>
 int run_batched(KParams& base, const Launch& lc, OffsetFn offset_chunk, cudaStream_t stream) {
   const da_params* p = lc.p;
   int sms = 0;
-  int st = device_sms(&sms);
+  int st = da::device_sms(&sms);
   if (st != DA_OK) return st;
   const bool use_ws = lc.workspace != nullptr;
   if (use_ws) {
@@ -760,7 +764,7 @@ int prefix_impl(const da_params* p, int T, int prefix_len, const int32_t* prefix
   if ((qa < oa ? oa - qa : qa - oa) < (unsigned long long)values * 4) return DA_ERR_INVALID;
   if (p->batch == 0) return DA_OK;
   int sms = 0;
-  st = device_sms(&sms);
+  st = da::device_sms(&sms);
   if (st != DA_OK) return st;
   da::PrefixParams k;
   memset(&k, 0, sizeof(k));
@@ -823,7 +827,7 @@ namespace da {
 
 size_t workspace_ticket_bytes() {
   int sms = 0;
-  if (device_sms(&sms) != DA_OK) return 0;
+  if (da::device_sms(&sms) != DA_OK) return 0;
   return ws_layout(sms, 64, 1).lse_off;
 }
 
@@ -845,7 +849,7 @@ const char* decode_attn_status_string(int status) {
 size_t decode_attn_workspace_size(const da_params* p) {
   if (check_params(p, false) != DA_OK && check_params(p, true) != DA_OK) return 0;
   int sms = 0;
-  if (device_sms(&sms) != DA_OK) return 0;
+  if (da::device_sms(&sms) != DA_OK) return 0;
   return ws_layout(sms, p->head_dim, ws_kvb(p)).total;
 }
 
@@ -922,7 +926,7 @@ size_t decode_attn_paged_prefix_workspace_size(const da_params* p, int32_t q_len
                                                int32_t prefix_len) {
   if (check_prefix(p, q_len, prefix_len) != DA_OK) return 0;
   int sms = 0;
-  if (device_sms(&sms) != DA_OK) return 0;
+  if (da::device_sms(&sms) != DA_OK) return 0;
   return prefix_workspace(p, q_len, sms).total;
 }
 

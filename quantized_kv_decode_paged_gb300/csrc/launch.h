@@ -11,6 +11,9 @@ namespace da {
 // Validation of the geometry an append uses (append.cu).
 int check_append_params(const da_params* p);
 
+// SM count of the current device (api.cu); a status.
+int device_sms(int* sms_out);
+
 // kv heads per work unit for a cache of `kind` with head dimension D and
 // Hkv kv heads: enough that one token row of the block is >= 512
 // contiguous bytes, and a divisor of Hkv.
