@@ -6,7 +6,7 @@
 // Python and here: norm and rotation of one token 20 and 7, the append of one 13 and 3, of 32 with
 // their queries 27 and 7, a shared-prefix decode of 2 sequences 29 and 12.  A call is
 // taken when everything is as the kernels need it: plain tensors of one device, the
-// current one, sizes that fit together, no capture in progress that needs a workspace.  Anything
+// current one, sizes that fit together, for the shared prefix no capture.  Anything
 // else is answered with NotImplemented, and the caller's checks in Python name what is wrong or do
 // the rest.  An error status of the entry point comes back as an int.
 #include <Python.h>

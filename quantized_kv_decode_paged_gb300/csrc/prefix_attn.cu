@@ -19,8 +19,11 @@
 //
 // A tile.  S = Q K^T and O_tile = P V run on the tensor cores (tcgen05), f16
 // operands and f32 accumulators in tensor memory.  Q (f32) is held as
-// two f16 terms of q / 2^e, e the row's exponent, P as two f16 terms: 22 bits
-// each, so out keeps f32's accuracy (one term would leave 2^-12).  That doubles
+// two f16 terms of q / 2^e, e the row's exponent, P as two f16 terms of the weight times 2^8: 22 bits
+// each, so out keeps f32's accuracy (one term would leave 2^-12).  Weights below 2^-22 of the
+// part's largest lose bits, each off by up to 2^-33 of that: as much as an f32 sum that holds the
+// largest drops of them (2^-25 of it a step), n 2^-33 of the result for n equal ones below one
+// largest.  The two terms double
 // the products: 8 * 128 * D flops a key; a 64-key tile of D = 128 is 1024
 // cycles of the tensor pipe for 32 KB of K and V, about the rate at which
 // HBM delivers them.  The tensor cores' f32 sums truncate: a long chain of
@@ -39,7 +42,7 @@
 // lanes of one warp of each of these groups, and four such units run at once.
 //
 // Measured (GB300), 128 sequences x 64 heads, 8 kv heads, D = 128, 32,768 shared and 64 to 2048 own
-// keys: 246 to 268 us by the card, 235 of them in prefix_attn_kernel, which issues 352 GFLOP of products (140 before
+// keys: 245 to 272 us by the card, 235 of them in prefix_attn_kernel, which issues 352 GFLOP of products (140 before
 // the second terms and the empty rows of own tiles): 1.5 PFLOP/s, 79% of the tensor cores' measured
 // rate, at the card's power limit; 452 MB read, 1.9 TB/s.  A tile takes 0.8 us for 0.55 of products:
 // the softmax's and the sums' traffic with tensor memory; an own unit's chain of latencies 2 to 3 us.
@@ -69,7 +72,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // tanh, with its roundings by 2.2 of 2^-24, relative, so a score keeps f32's accuracy whatever
 // the cap.  (tanh's series needs y^13 for that, two more products: 382 us against 353 for 128 sequences of 64 heads over
 // 32,768 shared keys.)  Above, by
-// the identity in 2^x, whose rounding next to 1 costs 3e-7 of a tanh that is near 1.
+// the identity in 2^x, whose rounding next to 1 costs 3e-7 of a tanh that is near 1: 1.5e-5 of a
+// score at a cap of 50, as in the unshared kernels.  Where one score of 16 columns is past 1/2 both
+// forms are worked out: 32,768 shared keys with a cap of 30 take 377 us for scores near 1, 389 and
+// 511 for a spread of 4 and 8.
 __device__ __forceinline__ float2 cap_near(float2 y, float cap2) {
   auto two = [](float c) { return make_float2(c, c); };
   const float2 t = mul2(y, y), z = mul2(y, two(cap2));
@@ -235,7 +241,8 @@ constexpr int kSmallRows = PGeo<D>::QT ? 32 : 64;
 // counts so many tiles for it.  D = 128, 32 to 64 heads and 64 to 2048 own keys, without it (0, 0) and
 // with (8, 1): 376 and 250 us over 32,768 shared keys, 61 and 43 over 8192, 419 and 78 over 16.  From
 // there it is flat: (14, 1) took 252, 44, 79, (16, 2) 252, 44, 81.  D = 256: 170 without and 136 us
-// with it for 64 sequences of 16 heads, a window of 4096 and 256 to 2048 own keys.
+// with it for 64 sequences of 16 heads, a window of 4096 and 256 to 2048 own keys (nearly all of its
+// tiles are own ones of two rows; full tiles of D = 256, and D = 64, were not fitted by themselves).
 template <int D>
 constexpr int kPrefixExtra = D >= 256 ? 20 : 8;
 constexpr int kOwnExtra = 1;

@@ -18,9 +18,10 @@
 // So no value crosses threads but the norm's sum of squares.  A thread's next row is
 // loaded before its last one is worked on.  HBM bounds long calls, the host short ones.
 //
-// Measured (GB300): 16,381 tokens x (32 + 8) heads x 128 from bf16, 470 MB in 73 us, 6.4 TB/s (77.5 us a
-// call in a loop); an append of 12,287 tokens x 8 heads x 128 of keys and values, 101 MB in 17 us;
-// 128 tokens x 72 heads 7 us.
+// Measured (GB300): 16,381 tokens x (32 + 8) heads x 128 from bf16, 470 MB in 74 us, 6.3 TB/s (77.5 to
+// 78.3 us a call in a loop); an append of 12,287 tokens x 8 heads x 128 of keys and values, 101 MB in
+// 17.8 us a call over the same inputs, 21.6 over changing ones; 128 tokens x 72 heads 4.7 us a call in
+// a graph.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
