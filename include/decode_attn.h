@@ -86,7 +86,12 @@ enum {
   DA_DEV_TIMEOUT = 32,       /* an internal pipeline wait ran past its time limit (never      */
                              /* expected; 2 s, or DA_WAIT_LIMIT_MS): the kernel then ends     */
                              /* without waiting further and its outputs are undefined          */
-  DA_DEV_BAD_SEQ = 64        /* append_paged_rope: token_seq[n] >= batch: the token is dropped */
+  DA_DEV_BAD_SEQ = 64,       /* append_paged_rope, append / gather_paged_q4: token_seq[n] >= batch: */
+                             /* the token is dropped (gather: its rows are zero)               */
+  DA_DEV_NO_BLOCKS = 128,    /* plan_blocks: too few free pages                               */
+  DA_DEV_TOKEN_OVERFLOW = 256, /* plan_blocks: more new tokens than max_tokens                */
+  DA_DEV_BAD_FREE_LIST = 512 /* plan_blocks: a count outside the free list, or an entry of it */
+                             /* that is no page                                               */
 };
 
 typedef struct {
@@ -457,6 +462,116 @@ int decode_attn_paged_prefix(const da_params* p, int32_t q_len, int32_t prefix_l
                              const int32_t* seq_lens, const int32_t* q_pos, float* out,
                              float* lse, void* workspace, size_t workspace_bytes,
                              int32_t* dev_status, void* stream);
+
+/*
+ * decode_attn_plan_blocks — pages and places for requests whose lengths
+ * change, worked out on the device.  For request b, with po = ceil(old_lens[b]
+ * / block_size) and pn = ceil(new_lens[b] / block_size):
+ *   pn > po: it takes pn - po free pages, columns po .. pn of its row of block_table;
+ *   pn < po: it gives pages pn .. po of its row back, whose entries become -1
+ *            (drafted tokens that were rejected; new_lens[b] = 0 ends it);
+ *   new_lens[b] > old_lens[b]: its new tokens are listed.
+ *   old_lens, new_lens i32 [B]; block_table i32 [B, max_blocks_per_seq], in place
+ *   free_list  i32 [free_capacity], free_count i32 [1], in place: the first
+ *              free_count entries are the free pages, a stack.  Pages given
+ *              back go on top in the order of requests and pages; then the
+ *              top ones are taken, the lowest of them first.  Old and new
+ *              lengths exchanged, the call undoes itself.  Entries from the
+ *              new count on are left as they were.
+ *   positions, token_seq i32 [max_tokens], slots i64 [max_tokens]: of every new token,
+ *              requests in order, its position, request and place page *
+ *              block_size + row: what the append and gather calls take.  Behind
+ *              the last token: 0, -1 and -1, padding to those calls.
+ *   cu_tokens  i32 [B + 1]: the new tokens before each request, and all
+ * All or nothing: where the free pages do not suffice (DA_DEV_NO_BLOCKS), a length
+ * is outside [0, max_blocks_per_seq * block_size] (DA_DEV_BAD_SEQ_LEN), the new
+ * tokens are more than max_tokens (DA_DEV_TOKEN_OVERFLOW), a page that would
+ * be given back or that a request goes on filling is outside [0, num_blocks)
+ * (DA_DEV_BAD_BLOCK), or the free list does not hold what its count says
+ * (DA_DEV_BAD_FREE_LIST), table, list and count stay as they are, every token is
+ * padding and cu_tokens is zero.  A caller sees that without dev_status by
+ * cu_tokens[B].
+ * The buffers must not overlap.  batch <= 16384; block_size a power of two in
+ * [8, 256].  max_tokens may be 0 (the three token arrays may then be NULL), but
+ * a request that gains tokens then overflows.
+ */
+int decode_attn_plan_blocks(int32_t batch, int32_t block_size, int32_t max_blocks_per_seq,
+                            int32_t num_blocks, int32_t max_tokens, int32_t free_capacity,
+                            const int32_t* old_lens, const int32_t* new_lens,
+                            int32_t* block_table, int32_t* free_list, int32_t* free_count,
+                            int32_t* positions, int32_t* token_seq, int64_t* slots,
+                            int32_t* cu_tokens, int32_t* dev_status, void* stream);
+
+/*
+ * A paged cache held in 4 bits (decode_attn_append_paged_q4,
+ * decode_attn_gather_paged_q4, decode_attn_paged_q4).  The D values of a row
+ * (token, kv head; keys and values apart) form D / group groups of
+ * neighbours, group in {32, 64, 128} and at most D.  A group has
+ *   zero  = f16(min),  scale = f16((max - min) / 15)   (min and max first taken to
+ *           [-65504, 65504])
+ *   code  = round((x - zero) / scale) in 0 .. 15  (f32 difference and division, ties
+ *           to even, values outside go to the ends; 0 where scale is 0)
+ * and stands for scale * code + zero.  A NaN makes its group's zero and scale
+ * NaN: whatever reads the group sees NaN.  Infinities go to the ends, +-65504.
+ *   pool u8 [num_blocks, Hkv, decode_attn_q4_page_bytes(block_size, D, group)],
+ *        16-byte aligned: a page of one kv head is, one behind the other,
+ *          key codes [block_size][D / 2], value codes [block_size][D / 2],
+ *          key and value params [2][block_size][D / group] of {f16 scale, f16 zero}
+ *        Value d of a row is half d % 2 (0: the low one) of byte d / 2, and the
+ *        16-byte pieces of row t are permuted: piece c lies at place
+ *        c ^ ((t / (256 / D)) % (D / 32)).
+ * A page's records move and copy as a whole.
+ */
+size_t decode_attn_q4_page_bytes(int32_t block_size, int32_t head_dim, int32_t group);
+
+/*
+ * decode_attn_append_paged_q4 — decode_attn_append_paged_rope into a cache in 4
+ * bits: the keys normed and rotated on the way (r: as there; rotary_dim 0 and
+ * norm 0 leave them as they are), quantised from their f32 values, and the
+ * tokens' queries normed and rotated in the same launch when q is given.
+ * block_size is a power of two in [8, 256].  Everything else as there.
+ */
+int decode_attn_append_paged_q4(const da_params* p, const da_rope_params* r, int32_t group,
+                                int32_t num_tokens, const void* q, const void* k_new,
+                                const void* v_new, const int32_t* positions,
+                                const int32_t* token_seq, const int32_t* block_table,
+                                float* q_out, uint8_t* pool, int32_t* dev_status, void* stream);
+
+/*
+ * decode_attn_gather_paged_q4 — the cached keys and values of num_tokens tokens
+ * as rows of `type` (DA_TYPE_*): k_out, v_out [N, Hkv, D], contiguous, 16-byte
+ * aligned.  positions, token_seq, block_table and the flags as for the append;
+ * rows of padding tokens and of flagged ones are zero.  f16 rows saturate at
+ * +-65504.  Uses batch, num_kv_heads (<= 4096), head_dim, block_size,
+ * max_blocks_per_seq and num_blocks of p.
+ */
+int decode_attn_gather_paged_q4(const da_params* p, int32_t group, int32_t num_tokens,
+                                int32_t type, const int32_t* positions, const int32_t* token_seq,
+                                const int32_t* block_table, const uint8_t* pool, void* k_out,
+                                void* v_out, int32_t* dev_status, void* stream);
+
+/*
+ * decode_attn_paged_q4 — decode_attn_paged (q_len 1) and decode_attn_paged_multi
+ * over a cache in 4 bits: q_len query tokens a sequence, q f32 [B, q_len, Hq, D],
+ * out f32 [B, q_len, Hq, D], lse f32 [B, q_len, Hq] or NULL; masks, softcap, q_pos
+ * and empty rows as there.  The products see Q and the softmax weights to 22
+ * bits and sum in f32.  A query row with a value that is not finite comes out
+ * as NaN (where it sees a key).  out must not overlap q (DA_ERR_INVALID).
+ * workspace: device scratch of decode_attn_paged_q4_workspace_size(p, q_len)
+ * bytes, 256-byte aligned, of any content, for long sequences to be split across
+ * CTAs; NULL with 0 bytes runs whole units per CTA.  Calls that overlap on the GPU
+ * must not share it; calls of one stream may, also from several threads.
+ * Everything else as for decode_attn_paged.  DA_ERR_UNSUPPORTED also where a
+ * launch's query rows (q_len * num_q_heads * 1024) or its key tiles
+ * (ceil(max_blocks_per_seq * block_size / 64) * num_kv_heads * 1024 *
+ * ceil(q_len * num_q_heads / num_kv_heads / 8)) would not count in 31 bits.
+ */
+size_t decode_attn_paged_q4_workspace_size(const da_params* p, int32_t q_len);
+int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const float* q,
+                         const uint8_t* pool, const int32_t* block_table,
+                         const int32_t* seq_lens, const int32_t* q_pos, float* out, float* lse,
+                         void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                         void* stream);
 
 /*
  * decode_attn_split_partial — first half of flash-decoding: split s covers

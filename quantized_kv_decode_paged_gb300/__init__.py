@@ -31,9 +31,12 @@ __all__ = [
     "decode_attn_paged_static_ws", "decode_attn_append_paged", "decode_attn_append_tiered_int8",
     "decode_attn_append_tiered_f16", "decode_attn_rope_freqs", "decode_attn_qk_norm_rope",
     "decode_attn_append_paged_rope", "decode_attn_paged_prefix",
-    "decode_attn_paged_prefix_workspace_size", "DecodeAttnError", "DaTuning", "get_tuning",
+    "decode_attn_paged_prefix_workspace_size", "decode_attn_plan_blocks",
+    "decode_attn_q4_page_bytes", "decode_attn_append_paged_q4", "decode_attn_gather_paged_q4",
+    "decode_attn_paged_q4", "decode_attn_paged_q4_workspace_size", "DecodeAttnError", "DaTuning", "get_tuning",
     "set_tuning", "tuning", "DEV_BAD_BLOCK", "DEV_BAD_SEQ_LEN",
     "DEV_BAD_QPOS", "DEV_SPLIT_OVERFLOW", "DEV_BAD_TIER", "DEV_TIMEOUT", "DEV_BAD_SEQ",
+    "DEV_NO_BLOCKS", "DEV_TOKEN_OVERFLOW", "DEV_BAD_FREE_LIST",
 ]
 
 DEV_BAD_BLOCK = 1
@@ -43,6 +46,9 @@ DEV_SPLIT_OVERFLOW = 8
 DEV_BAD_TIER = 16
 DEV_TIMEOUT = 32
 DEV_BAD_SEQ = 64
+DEV_NO_BLOCKS = 128
+DEV_TOKEN_OVERFLOW = 256
+DEV_BAD_FREE_LIST = 512
 
 DA_OK = 0
 DA_ERR_INVALID = -1
@@ -57,7 +63,9 @@ _EXPORTS = (
     "decode_attn_status_string", "decode_attn_paged_static_ws", "decode_attn_append_paged",
     "decode_attn_append_tiered_int8", "decode_attn_append_tiered_f16", "decode_attn_rope_freqs",
     "decode_attn_qk_norm_rope", "decode_attn_append_paged_rope", "decode_attn_paged_prefix",
-    "decode_attn_paged_prefix_workspace_size", "decode_attn_get_tuning", "decode_attn_set_tuning", "decode_attn_testing_skip_first_arm",
+    "decode_attn_paged_prefix_workspace_size", "decode_attn_plan_blocks",
+    "decode_attn_q4_page_bytes", "decode_attn_append_paged_q4", "decode_attn_gather_paged_q4",
+    "decode_attn_paged_q4", "decode_attn_paged_q4_workspace_size", "decode_attn_get_tuning", "decode_attn_set_tuning", "decode_attn_testing_skip_first_arm",
 )
 
 
@@ -195,6 +203,22 @@ def load_library():
         lib.decode_attn_paged_prefix.restype = ctypes.c_int
         lib.decode_attn_paged_prefix.argtypes = ([ctypes.POINTER(DaParams), i32, i32] + [P] * 10
                                                  + [ctypes.c_size_t, P, P])
+        lib.decode_attn_plan_blocks.restype = ctypes.c_int
+        lib.decode_attn_plan_blocks.argtypes = [i32] * 6 + [P] * 11
+        lib.decode_attn_q4_page_bytes.restype = ctypes.c_size_t
+        lib.decode_attn_q4_page_bytes.argtypes = [i32] * 3
+        lib.decode_attn_append_paged_q4.restype = ctypes.c_int
+        lib.decode_attn_append_paged_q4.argtypes = ([ctypes.POINTER(DaParams),
+                                                     ctypes.POINTER(DaRopeParams), i32, i32]
+                                                    + [P] * 10)
+        lib.decode_attn_gather_paged_q4.restype = ctypes.c_int
+        lib.decode_attn_gather_paged_q4.argtypes = ([ctypes.POINTER(DaParams), i32, i32, i32]
+                                                    + [P] * 8)
+        lib.decode_attn_paged_q4_workspace_size.restype = ctypes.c_size_t
+        lib.decode_attn_paged_q4_workspace_size.argtypes = [ctypes.POINTER(DaParams), i32]
+        lib.decode_attn_paged_q4.restype = ctypes.c_int
+        lib.decode_attn_paged_q4.argtypes = ([ctypes.POINTER(DaParams), i32, i32] + [P] * 8
+                                             + [ctypes.c_size_t, P, P])
         lib.decode_attn_get_tuning.restype = ctypes.c_int
         lib.decode_attn_get_tuning.argtypes = [ctypes.POINTER(DaTuning)]
         lib.decode_attn_set_tuning.restype = ctypes.c_int
@@ -1142,4 +1166,289 @@ def decode_attn_paged_prefix(q, k_pool, v_pool, block_table, seq_lens, prefix_le
             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
             _ptr(dev_status), raw)
     _check("decode_attn_paged_prefix", st)
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# a paged cache held in 4 bits, and the pages of requests
+# ---------------------------------------------------------------------------
+
+def _ints(torch, name, t, dev, ndim, dtype=None):
+    """t's address; an error that names it unless it is a contiguous int32 tensor (or one of dtype)."""
+    dtype = dtype or torch.int32
+    if not _plain(t, dtype, dev, ndim):
+        _req(t, name, dtype, dev, ndim)
+    return t.data_ptr()
+
+
+def decode_attn_plan_blocks(old_lens, new_lens, block_table, free_list, free_count, *, block_size,
+                            num_blocks, max_tokens, positions=None, token_seq=None, slots=None,
+                            cu_tokens=None, dev_status=None, stream=None):
+    """Pages and places for requests whose lengths change from old_lens to
+    new_lens (i32 [B]), on the device.  A request that grows takes free pages into
+    its row of block_table i32 [B, max_blocks]; one that shrinks (rejected
+    drafts) or ends (new length 0) gives its pages back, whose entries become
+    -1.  free_list i32 [capacity] and free_count i32 [1] are a stack of free
+    pages; table, list and count change in place.  Returns (positions i32
+    [max_tokens], token_seq i32 [max_tokens], slots i64 [max_tokens], cu_tokens
+    i32 [B + 1]): every new token's position, request and page * block_size + row, requests
+    in order, padding (0, -1, -1) behind them, and the tokens before each request.
+
+    All or nothing: where free pages or max_tokens do not suffice, or a
+    length, page or count is out of range, nothing is changed, every token is
+    padding, cu_tokens is zero and dev_status says why (DEV_NO_BLOCKS,
+    DEV_TOKEN_OVERFLOW, DEV_BAD_SEQ_LEN, DEV_BAD_BLOCK, DEV_BAD_FREE_LIST)."""
+    torch = _torch()
+    lib = _lib or load_library()
+    if not isinstance(old_lens, torch.Tensor):
+        raise TypeError("old_lens must be a torch.Tensor")
+    dev, i32 = old_lens.device, torch.int32
+    old_p = _ints(torch, "old_lens", old_lens, dev, 1)
+    new_p = _ints(torch, "new_lens", new_lens, dev, 1)
+    table_p = _ints(torch, "block_table", block_table, dev, 2)
+    list_p = _ints(torch, "free_list", free_list, dev, 1)
+    count_p = _ints(torch, "free_count", free_count, dev, 1)
+    B, N = old_lens.shape[0], int(max_tokens)
+    if new_lens.shape[0] != B or block_table.shape[0] != B or free_count.shape[0] != 1:
+        raise ValueError("inconsistent shapes")
+    if N < 0:
+        raise ValueError(f"max_tokens must not be negative, got {N}")
+    outs = (("positions", positions, i32, N), ("token_seq", token_seq, i32, N),
+            ("slots", slots, torch.int64, N), ("cu_tokens", cu_tokens, i32, B + 1))
+    for name, t, dtype, n in outs:
+        if t is not None:
+            _ints(torch, name, t, dev, 1, dtype)
+            if t.shape[0] != n:
+                raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    if dev_status is not None:
+        _req(dev_status, "dev_status", i32, dev)
+    _check_cuda("old_lens", old_lens)
+    with _call_guard(torch, dev, stream):
+        positions, token_seq, slots, cu_tokens = (
+            torch.empty(n, dtype=dtype, device=dev) if t is None else t
+            for _, t, dtype, n in outs)
+        if B == 0:
+            positions.zero_(), token_seq.fill_(-1), slots.fill_(-1), cu_tokens.zero_()
+            return positions, token_seq, slots, cu_tokens
+        st = lib.decode_attn_plan_blocks(
+            B, int(block_size), block_table.shape[1], int(num_blocks), N, free_list.shape[0],
+            old_p, new_p, table_p, list_p, count_p, positions.data_ptr(), token_seq.data_ptr(),
+            slots.data_ptr(), cu_tokens.data_ptr(), _ptr(dev_status),
+            _raw_stream(torch, dev, stream))
+    _check("decode_attn_plan_blocks", st)
+    return positions, token_seq, slots, cu_tokens
+
+
+def decode_attn_q4_page_bytes(block_size, head_dim, group) -> int:
+    """Bytes of a page of one kv head of a cache held in 4 bits: the last dimension of its
+    pool, uint8 [num_blocks, Hkv, bytes]."""
+    n = int(load_library().decode_attn_q4_page_bytes(int(block_size), int(head_dim), int(group)))
+    if n == 0:
+        raise DecodeAttnError("decode_attn_q4_page_bytes", DA_ERR_UNSUPPORTED,
+                              "block_size a power of two in [8, 256], head_dim 64, 128 or 256, group "
+                              "32, 64 or 128 and at most head_dim")
+    return n
+
+
+def _q4_pool(torch, pool, dev, D, group):
+    """(pages, kv heads, rows of a page) of a pool in 4 bits."""
+    if not _plain(pool, torch.uint8, dev, 3):
+        _req(pool, "pool", torch.uint8, dev, 3)
+    NB, Hkv, nbytes = pool.shape
+    group = int(group)
+    per = D + 8 * (D // group) if group > 0 else 0  # bytes of a row of keys and one of values
+    if group not in (32, 64, 128) or group > D:
+        raise DecodeAttnError("group", DA_ERR_UNSUPPORTED,
+                              f"group must be 32, 64 or 128 and at most head_dim {D}, got {group}")
+    if nbytes % per != 0:
+        raise ValueError(f"pool pages of {nbytes} bytes do not hold rows of head_dim {D} and group "
+                         f"{group}")
+    return NB, Hkv, nbytes // per
+
+
+def decode_attn_append_paged_q4(k_new, v_new, positions, block_table, pool, freqs=None, *, group,
+                                token_seq=None, q=None, norm=False, q_weight=None, k_weight=None,
+                                weight_offset=0.0, eps=1e-6, interleaved=False, q_out=None,
+                                dev_status=None, stream=None):
+    """decode_attn_append_paged_rope into a cache held in 4 bits: pool uint8
+    [num_blocks, Hkv, decode_attn_q4_page_bytes(block_size, D, group)], in place.
+    The keys, normed (with ``norm``) and rotated (with freqs) on the way, and the
+    values are quantised in groups of ``group`` neighbours: zero = f16(min), scale =
+    f16((max - min) / 15), codes 0..15.  Returns q_out f32 [N, Hq, D], or None without q."""
+    torch = _torch()
+    lib = _lib or load_library()
+    kind = _rope_kind(torch, k_new)
+    dtype, dev, i32 = k_new.dtype, k_new.device, torch.int32
+    ks, kt, kh = _req_rows(k_new, "k_new", dtype, dev)
+    vs, vt, vh = _req_rows(v_new, "v_new", dtype, dev)
+    qs, qt, qh = _NO_ROWS if q is None else _req_rows(q, "q", dtype, dev)
+    N, Hkv, D = ks
+    rd, fp = 0, None
+    if freqs is not None:
+        fp = _ints(torch, "freqs", freqs, dev, 1, torch.int64)
+        rd = 2 * freqs.shape[0]
+    r = DaRopeParams(kind, rd, 1 if interleaved else 0, 1 if norm else 0, eps, weight_offset,
+                     qt, qh, kt, kh, vt, vh, fp,
+                     _weight_ptr(torch, q_weight, "q_weight", norm, D, dev),
+                     _weight_ptr(torch, k_weight, "k_weight", norm, D, dev))
+    pos_p = _ints(torch, "positions", positions, dev, 1)
+    table_p = _ints(torch, "block_table", block_table, dev, 2)
+    NB, Hp, bs = _q4_pool(torch, pool, dev, D, group)
+    if vs != ks or Hp != Hkv or positions.shape[0] != N:
+        raise ValueError("inconsistent shapes")
+    seq_p = None
+    if token_seq is not None:
+        seq_p = _ints(torch, "token_seq", token_seq, dev, 1)
+        if token_seq.shape[0] != N:
+            raise ValueError("inconsistent shapes")
+    Hq = Hkv
+    if q is not None:
+        Hq = qs[1]
+        if qs[0] != N or qs[2] != D:
+            raise ValueError("inconsistent shapes")
+        if q_out is not None:
+            _req(q_out, "q_out", torch.float32, dev, 3)
+            if q_out.shape != qs:
+                raise ValueError("inconsistent shapes")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if dev_status is not None:
+        _req(dev_status, "dev_status", i32, dev)
+    _check_cuda("k_new", k_new)
+    rows, columns = block_table.shape
+    p = DaParams(rows, Hq, Hkv, D, bs, columns, NB, 0, 0.0, 0.0, 0, 1)
+    with _call_guard(torch, dev, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty((N, Hq, D), dtype=torch.float32, device=dev)
+        if N == 0:
+            return q_out
+        st = lib.decode_attn_append_paged_q4(
+            ctypes.byref(p), ctypes.byref(r), int(group), N, _ptr(q), k_new.data_ptr(),
+            v_new.data_ptr(), pos_p, seq_p, table_p, _ptr(q_out), pool.data_ptr(),
+            _ptr(dev_status), _raw_stream(torch, dev, stream))
+    _check("decode_attn_append_paged_q4", st)
+    return q_out
+
+
+def decode_attn_gather_paged_q4(positions, block_table, pool, *, head_dim, group, token_seq=None,
+                                dtype=None, k_out=None, v_out=None, dev_status=None, stream=None):
+    """The cached keys and values of tokens as rows: (k, v), [N, Hkv, head_dim]
+    each, of dtype float16 (the default), bfloat16 or float32.  positions i32 [N],
+    token_seq i32 [N] and block_table as for decode_attn_append_paged_q4; rows of
+    padding tokens (token_seq < 0) and of those that dev_status flags are zero."""
+    torch = _torch()
+    lib = _lib or load_library()
+    if not isinstance(pool, torch.Tensor):
+        raise TypeError("pool must be a torch.Tensor")
+    if dtype is None:
+        dtype = getattr(k_out if v_out is None else v_out, "dtype", torch.float16)
+    if not _ROPE_TYPES:
+        _ROPE_TYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    kind = _ROPE_TYPES.get(dtype)
+    if kind is None:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    dev, D = pool.device, int(head_dim)
+    NB, Hkv, bs = _q4_pool(torch, pool, dev, D, group)
+    pos_p = _ints(torch, "positions", positions, dev, 1)
+    table_p = _ints(torch, "block_table", block_table, dev, 2)
+    N = positions.shape[0]
+    seq_p = None
+    if token_seq is not None:
+        seq_p = _ints(torch, "token_seq", token_seq, dev, 1)
+        if token_seq.shape[0] != N:
+            raise ValueError("inconsistent shapes")
+    shape = (N, Hkv, D)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            _req(t, name, dtype, dev, 3)
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if dev_status is not None:
+        _req(dev_status, "dev_status", torch.int32, dev)
+    _check_cuda("pool", pool)
+    rows, columns = block_table.shape
+    p = DaParams(rows, Hkv, Hkv, D, bs, columns, NB, 0, 0.0, 0.0, 0, 1)
+    with _call_guard(torch, dev, stream):
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=dev)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dtype, device=dev)
+        if N == 0:
+            return k_out, v_out
+        st = lib.decode_attn_gather_paged_q4(
+            ctypes.byref(p), int(group), N, kind, pos_p, seq_p, table_p, pool.data_ptr(),
+            k_out.data_ptr(), v_out.data_ptr(), _ptr(dev_status), _raw_stream(torch, dev, stream))
+    _check("decode_attn_gather_paged_q4", st)
+    return k_out, v_out
+
+
+def decode_attn_paged_q4_workspace_size(params: DaParams, q_len: int) -> int:
+    return int(load_library().decode_attn_paged_q4_workspace_size(ctypes.byref(params),
+                                                                  int(q_len)))
+
+
+def decode_attn_paged_q4(q, pool, block_table, seq_lens, q_pos=None, *, group, scale=0.0,
+                         softcap=0.0, sliding_window=0, causal=True, max_seq_len=0, out=None,
+                         lse=None, workspace="auto", dev_status=None, stream=None):
+    """decode_attn_paged (q [B, Hq, D]) or decode_attn_paged_multi (q [B, T, Hq, D])
+    over a cache held in 4 bits (decode_attn_append_paged_q4's pool and group).
+    Returns (out, lse).
+
+    ``workspace``: "auto" (the call's own, from torch's allocator on the call's
+    stream; a captured call's in its graph's memory), None (whole units per CTA) or a
+    caller-owned uint8 tensor of decode_attn_paged_q4_workspace_size bytes (any
+    content)."""
+    torch = _torch()
+    lib = _lib or load_library()
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be a tensor of 3 or 4 dims")
+    dev, i32, shape = q.device, torch.int32, q.shape
+    if not _plain(q, torch.float32, dev, len(shape)):
+        _req(q, "q", torch.float32, dev)
+    B, Hq, D = shape[0], shape[-2], shape[-1]
+    T = shape[1] if len(shape) == 4 else 1
+    NB, Hkv, bs = _q4_pool(torch, pool, dev, D, group)
+    table_p = _ints(torch, "block_table", block_table, dev, 2)
+    lens_p = _ints(torch, "seq_lens", seq_lens, dev, 1)
+    rows, columns = block_table.shape
+    if rows != B or seq_lens.shape[0] != B:
+        raise ValueError("inconsistent shapes")
+    pos_p = None
+    if q_pos is not None:
+        pos_p = _ints(torch, "q_pos", q_pos, dev, 1)
+        if q_pos.shape[0] != B:
+            raise ValueError("inconsistent shapes")
+    for name, t, s in (("out", out, shape), ("lse", lse, shape[:-1])):
+        if t is not None:
+            _req(t, name, torch.float32, dev)
+            if t.shape != s:
+                raise ValueError("inconsistent shapes")
+    if dev_status is not None:
+        _req(dev_status, "dev_status", i32, dev)
+    auto = isinstance(workspace, str) and workspace == "auto"
+    if not auto and workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise ValueError("workspace must be \"auto\", None or a uint8 tensor")
+        _req(workspace, "workspace", torch.uint8, dev)
+    _check_cuda("q", q)
+    params = DaParams(B, Hq, Hkv, D, bs, columns, NB, max_seq_len, scale, softcap, sliding_window,
+                      1 if causal else 0)
+    ref = ctypes.byref(params)
+    with _call_guard(torch, dev, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        if B == 0:
+            return out, lse
+        if auto:
+            nbytes = lib.decode_attn_paged_q4_workspace_size(ref, T)
+            # this call's alone: its kernels hand over through it
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        st = lib.decode_attn_paged_q4(
+            ref, int(group), T, q.data_ptr(), pool.data_ptr(), table_p, lens_p, pos_p,
+            out.data_ptr(), lse.data_ptr(), _ptr(workspace),
+            0 if workspace is None else workspace.numel(), _ptr(dev_status),
+            _raw_stream(torch, dev, stream))
+    _check("decode_attn_paged_q4", st)
     return out, lse

@@ -1,0 +1,199 @@
+// q4.cu — the cache in 4 bits as rows again: cached tokens to f32, f16 or bf16.
+//
+// A value is scale * code + zero (q4.cuh), worked out in f32 by one fused multiply-add and rounded once
+// to the rows' type; f16 rows saturate at 65504, which a code's rounding may pass by half a step.
+// A thread takes eight codes, one word, so that a warp's loads and its 16- or 32-byte stores
+// cover whole sectors; a CTA looks its tokens' pages up once.  HBM bounds long calls.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/decode_attn.h"
+#include "launch.h"
+#include "ptx.cuh"
+#include "q4.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokens = 16;  // of a CTA
+
+struct GatherArgs {
+  const int32_t* positions;
+  const int32_t* token_seq;
+  const int32_t* block_table;
+  const uint8_t* pool;
+  void* k_out;
+  void* v_out;
+  int N, tokens, Hkv, group;
+  int batch, log2_bs, max_blocks, num_blocks;
+  long long page_bytes;
+  int32_t* dev_status;
+};
+
+template <typename T>
+__device__ __forceinline__ void store_row8(T* p, const float (&x)[8]) {
+  if constexpr (std::is_same<T, float>::value) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __half>::value) {
+        w[i] = da::pack_half2(fmaxf(fminf(x[2 * i], 65504.f), -65504.f),
+                              fmaxf(fminf(x[2 * i + 1], 65504.f), -65504.f));
+        // fminf and fmaxf drop a NaN
+        if (x[2 * i] != x[2 * i]) w[i] |= 0x7fffu;
+        if (x[2 * i + 1] != x[2 * i + 1]) w[i] |= 0x7fff0000u;
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
+  __shared__ long long place[kTokens];  // row of the pool, negative: none
+  const int n0 = blockIdx.x * a.tokens, tokens = min(a.tokens, a.N - n0);
+  da::let_next_grid_start();
+  da::wait_for_grid_before();
+  if ((int)threadIdx.x < tokens) {
+    const int n = n0 + threadIdx.x, seq = a.token_seq ? a.token_seq[n] : n;
+    long long row = -1;
+    int flag = 0;
+    if (seq >= a.batch) {
+      flag = DA_DEV_BAD_SEQ;
+    } else if (seq >= 0) {
+      const int pos = a.positions[n];
+      if (pos < 0 || (pos >> a.log2_bs) >= a.max_blocks) {
+        flag = DA_DEV_BAD_SEQ_LEN;
+      } else {
+        const int blk = a.block_table[(long long)seq * a.max_blocks + (pos >> a.log2_bs)];
+        if (blk < 0 || blk >= a.num_blocks)
+          flag = DA_DEV_BAD_BLOCK;
+        else
+          row = ((long long)blk << a.log2_bs) + (pos & ((1 << a.log2_bs) - 1));
+      }
+    }
+    place[threadIdx.x] = row;
+    if (flag && a.dev_status) atomicOr(a.dev_status, flag);
+  }
+  __syncthreads();
+  constexpr int C = D / 8;  // words of a row
+  const int bs = 1 << a.log2_bs, per = a.Hkv * C, ng = D / a.group;
+  for (int i = threadIdx.x; i < tokens * per; i += kThreads) {
+    const int t = i / per, h = (i - t * per) / C, c = i % C;
+    const long long row = place[t];
+    float k[8] = {}, v[8] = {};
+    if (row >= 0) {
+      const int r = (int)(row & (bs - 1));
+      const uint8_t* page = a.pool + ((row >> a.log2_bs) * a.Hkv + h) * a.page_bytes;
+      const int piece = (c / 4) ^ da::piece_xor<D>(r);
+      const uint8_t* at = page + r * (D / 2) + 16 * piece + c % 4 * 4;
+      const uint32_t kc = *reinterpret_cast<const uint32_t*>(at);
+      const uint32_t vc = *reinterpret_cast<const uint32_t*>(at + bs * (D / 2));
+      const uint32_t* par = reinterpret_cast<const uint32_t*>(page + bs * D) + r * ng + c * 8 / a.group;
+      const uint32_t kw = par[0], vw = par[bs * ng];
+      const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&kw));
+      const float2 vp = __half22float2(*reinterpret_cast<const __half2*>(&vw));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        k[j] = fmaf((float)(kc >> (4 * j) & 15u), kp.x, kp.y);
+        v[j] = fmaf((float)(vc >> (4 * j) & 15u), vp.x, vp.y);
+      }
+    }
+    const long long to = ((long long)(n0 + t) * a.Hkv + h) * D + c * 8;
+    store_row8(static_cast<T*>(a.k_out) + to, k);
+    store_row8(static_cast<T*>(a.v_out) + to, v);
+  }
+}
+
+template <typename T>
+cudaError_t launch_gather(const GatherArgs& a, int D, cudaStream_t s) {
+  const int grid = (a.N + a.tokens - 1) / a.tokens;
+  return da::launch_early(D == 64    ? gather_kernel<T, 64>
+                          : D == 128 ? gather_kernel<T, 128>
+                                     : gather_kernel<T, 256>,
+                          grid, kThreads, 0, s, a);
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+}  // namespace
+
+namespace da {
+
+int check_q4(const da_params* p, int group) {
+  if (!p || group <= 0) return DA_ERR_INVALID;
+  const int bs = p->block_size, D = p->head_dim;
+  if (bs <= 0 || D <= 0) return DA_ERR_INVALID;
+  if (bs < 8 || bs > 256 || (bs & (bs - 1)) != 0) return DA_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128 && D != 256) return DA_ERR_UNSUPPORTED;
+  return q4_group_ok(group, D) ? DA_OK : DA_ERR_UNSUPPORTED;
+}
+
+}  // namespace da
+
+extern "C" {
+
+size_t decode_attn_q4_page_bytes(int32_t block_size, int32_t head_dim, int32_t group) {
+  da_params p = {};
+  p.block_size = block_size;
+  p.head_dim = head_dim;
+  if (da::check_q4(&p, group) != DA_OK) return 0;
+  return (size_t)da::q4_page_bytes(block_size, head_dim, group);
+}
+
+int decode_attn_gather_paged_q4(const da_params* p, int32_t group, int32_t num_tokens, int32_t type,
+                                const int32_t* positions, const int32_t* token_seq,
+                                const int32_t* block_table, const uint8_t* pool, void* k_out,
+                                void* v_out, int32_t* dev_status, void* stream) {
+  int st = da::check_append_params(p);
+  if (st == DA_OK) st = da::check_q4(p, group);
+  if (st != DA_OK) return st;
+  if (type != DA_TYPE_F32 && type != DA_TYPE_F16 && type != DA_TYPE_BF16) return DA_ERR_INVALID;
+  if (num_tokens < 0 || (!token_seq && num_tokens != p->batch)) return DA_ERR_INVALID;
+  if (!positions || !block_table || !pool || !k_out || !v_out) return DA_ERR_INVALID;
+  if (!aligned(pool, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(positions, 4) ||
+      !aligned(block_table, 4) || (token_seq && !aligned(token_seq, 4)) ||
+      (dev_status && !aligned(dev_status, 4)))
+    return DA_ERR_INVALID;
+  if (p->num_kv_heads > 4096) return DA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return DA_OK;
+  int sms = 0;
+  st = da::device_sms(&sms);
+  if (st != DA_OK) return st;
+  GatherArgs a = {};
+  a.positions = positions;
+  a.token_seq = token_seq;
+  a.block_table = block_table;
+  a.pool = pool;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.N = num_tokens;
+  // short calls: a token a CTA as long as there are processors for them
+  a.tokens = (num_tokens - 1) / (sms * 8) + 1;
+  if (a.tokens > kTokens) a.tokens = kTokens;
+  a.Hkv = p->num_kv_heads;
+  a.group = group;
+  a.batch = p->batch;
+  while ((1 << a.log2_bs) < p->block_size) ++a.log2_bs;
+  a.max_blocks = p->max_blocks_per_seq;
+  a.num_blocks = p->num_blocks;
+  a.page_bytes = da::q4_page_bytes(p->block_size, p->head_dim, group);
+  a.dev_status = dev_status;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t err = type == DA_TYPE_F32   ? launch_gather<float>(a, p->head_dim, s)
+                          : type == DA_TYPE_F16 ? launch_gather<__half>(a, p->head_dim, s)
+                                                : launch_gather<__nv_bfloat16>(a, p->head_dim, s);
+  return err == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -33,14 +33,20 @@
 #include "../../include/decode_attn.h"
 #include "launch.h"
 #include "ptx.cuh"
+#include "q4.cuh"
 
 namespace {
+
+// What a launch does with its rows: norm and rotation alone, or an append to f16 pages or to
+// pages in 4 bits.
+enum { kNormRope = 0, kAppend = 1, kAppendQ4 = 2 };
 
 constexpr int kRopeThreads = 256;
 // Resident CTAs of an SM (64 registers a thread; 3 and 5, the latter spilling,
 // measured 83 and 93-98 us against 79 on 16,381 tokens x 40 heads x 128).
 constexpr int kRopeCtas = 4;
 constexpr int kMaxTokens = 12;  // of a CTA
+constexpr int rope_ctas(int mode) { return mode == kAppendQ4 ? 3 : kRopeCtas; }
 
 struct RopeArgs {
   const void* q;
@@ -66,6 +72,10 @@ struct RopeArgs {
   uint16_t* v_pool;
   int batch, bs, max_blocks, num_blocks;
   int32_t* dev_status;
+  // append in 4 bits
+  uint8_t* q4_pool;
+  int log2_bs, group;
+  long long page_bytes;
 };
 
 // Eight values of type T as they lie in memory.
@@ -157,8 +167,58 @@ __device__ __forceinline__ long long cache_row(const RopeArgs& a, int n, int& fl
   return (long long)blk * a.bs + pos % a.bs;
 }
 
-template <typename T, int D, bool IL, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const RopeArgs a) {
+// Minimum and maximum that a NaN wins.
+__device__ __forceinline__ float min_nan(float x, float y) {
+  float z;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+
+// Least and largest of eight values.
+__device__ __forceinline__ float2 extent8(const float (&x)[8]) {
+  float2 e = make_float2(x[0], x[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) e = make_float2(min_nan(e.x, x[i]), max_nan(e.y, x[i]));
+  return e;
+}
+
+// Scale and zero of a group with this extent, as they are stored and as f32.  The extent is
+// taken to f16's range first, so that both are finite but for a NaN.
+struct Q4Param {
+  uint32_t word;
+  float scale, zero;
+};
+__device__ __forceinline__ Q4Param q4_param(float2 e) {
+  const float lo = max_nan(min_nan(e.x, 65504.f), -65504.f);
+  const float hi = max_nan(min_nan(e.y, 65504.f), -65504.f);
+  const __half z = __float2half_rn(lo), s = __float2half_rn(__fdiv_rn(hi - lo, 15.f));
+  Q4Param p;
+  p.word = (uint32_t)__half_as_ushort(s) | (uint32_t)__half_as_ushort(z) << 16;
+  p.scale = __half2float(s);
+  p.zero = __half2float(z);
+  return p;
+}
+
+// Eight codes: round((x - zero) / scale), ties to even, within 0..15; 0 without a scale.
+__device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], const Q4Param& p) {
+  if (!(p.scale > 0.f)) return 0;
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float c = fminf(fmaxf(rintf(__fdiv_rn(x[i] - p.zero, p.scale)), 0.f), 15.f);
+    w |= (uint32_t)c << (4 * i);
+  }
+  return w;
+}
+
+template <typename T, int D, bool IL, int MODE>
+__global__ void __launch_bounds__(kRopeThreads, rope_ctas(MODE)) rope_kernel(const RopeArgs a) {
+  constexpr bool APPEND = MODE != kNormRope;
   constexpr int TPR = D / 16;                 // threads of a row
   constexpr int RPI = kRopeThreads / TPR;     // rows of a round
   // cosine and sine of pairs 2j and 2j + 1 of chunk c at [j][c]: a row's threads read
@@ -167,6 +227,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
   __shared__ float4 cs[kMaxTokens][4][TPR];
   __shared__ long long place[kMaxTokens];     // append: row of the pool, or one of:
   constexpr long long kDropped = -1, kPadding = -2;
+  // append in 4 bits: extents of the chunks of the rows in work
+  __shared__ float4 extent[MODE == kAppendQ4 ? RPI : 1][D / 16];
   const int n0 = blockIdx.x * a.tokens, tokens = min(a.tokens, a.N - n0);
   const int c = threadIdx.x % TPR;
   const int nrot = a.rd / 16;  // chunk pairs that are rotated
@@ -251,7 +313,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
         }
       }
     }
-    if (r >= rows) continue;
+    if (MODE != kAppendQ4 && r >= rows) continue;
     if (rot && cur.kind < 2) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -266,6 +328,41 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
     }
     long long row = 0;
     if constexpr (APPEND) row = place[cur.t];
+    if constexpr (MODE == kAppendQ4) {
+      // A group's chunks are in several threads, in an order that the rotation gives: each puts
+      // its two chunks' extents down, and takes those of the groups that they belong to.
+      float2* ext = reinterpret_cast<float2*>(extent[threadIdx.x / TPR]);
+      __syncwarp();
+      ext[lo / 8] = extent8(x[0]);
+      ext[hi / 8] = extent8(x[1]);
+      __syncwarp();
+      const bool kept = r < rows && cur.kind != 0 && row >= 0;
+      uint8_t* page = nullptr;
+      int t = 0, words = 0;
+      if (kept) {
+        t = (int)(row & (a.bs - 1));
+        page = a.q4_pool + ((row >> a.log2_bs) * a.Hkv + cur.h) * a.page_bytes;
+        words = D / a.group;  // params of a row
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int d = half ? hi : lo, g = d & -a.group;
+        float2 e = make_float2(INFINITY, -INFINITY);
+        for (int i = 0; i < a.group / 16; ++i) {
+          const float4 two = extent[threadIdx.x / TPR][g / 16 + i];
+          e = make_float2(min_nan(e.x, min_nan(two.x, two.z)), max_nan(e.y, max_nan(two.y, two.w)));
+        }
+        if (!kept) continue;
+        const Q4Param p = q4_param(e);
+        uint8_t* codes = page + (cur.kind == 2 ? a.bs * (D / 2) : 0) + t * (D / 2);
+        const int piece = (d / 32) ^ da::piece_xor<D>(t);
+        *reinterpret_cast<uint32_t*>(codes + 16 * piece + d % 32 / 2) = q4_codes(x[half], p);
+        if (d == g)
+          reinterpret_cast<uint32_t*>(page + a.bs * D)[((cur.kind == 2 ? a.bs : 0) + t) * words +
+                                                       g / a.group] = p.word;
+      }
+      if (cur.kind != 0 || r >= rows) continue;
+    }
     if (cur.kind == 0) {
       if (APPEND && row == kPadding) continue;
       float* dst = a.q_out + ((long long)(n0 + cur.t) * a.Hq + cur.h) * D;
@@ -273,7 +370,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
       store8(dst + hi, x[1], a.wide_out);
     } else {
       uint16_t* dst;
-      if constexpr (APPEND) {
+      if constexpr (MODE == kAppendQ4) {
+        continue;  // done above
+      } else if constexpr (APPEND) {
         if (row < 0) continue;
         dst = (cur.kind == 2 ? a.v_pool : a.k_pool) + (row * a.Hkv + cur.h) * D;
       } else {
@@ -285,38 +384,38 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
   }
 }
 
-template <typename T, int D, bool APPEND>
+template <typename T, int D, int MODE>
 cudaError_t launch_rope_d(const RopeArgs& a, int il, cudaStream_t s) {
   const int grid = (a.N + a.tokens - 1) / a.tokens;
-  return da::launch_early(il ? rope_kernel<T, D, true, APPEND> : rope_kernel<T, D, false, APPEND>,
+  return da::launch_early(il ? rope_kernel<T, D, true, MODE> : rope_kernel<T, D, false, MODE>,
                           grid, kRopeThreads, 0, s, a);
 }
 
-template <typename T, bool APPEND>
+template <typename T, int MODE>
 cudaError_t launch_rope_t(const RopeArgs& a, int D, int il, cudaStream_t s) {
-  if (D == 64) return launch_rope_d<T, 64, APPEND>(a, il, s);
-  if (D == 128) return launch_rope_d<T, 128, APPEND>(a, il, s);
-  return launch_rope_d<T, 256, APPEND>(a, il, s);
+  if (D == 64) return launch_rope_d<T, 64, MODE>(a, il, s);
+  if (D == 128) return launch_rope_d<T, 128, MODE>(a, il, s);
+  return launch_rope_d<T, 256, MODE>(a, il, s);
 }
 
-template <bool APPEND>
+template <int MODE>
 int launch_rope(RopeArgs& a, const da_rope_params* r, int D, int num_tokens, void* stream) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   a.N = num_tokens;
-  a.heads = a.Hq + a.Hk + (APPEND ? a.Hkv : 0);
+  a.heads = a.Hq + a.Hk + (MODE != kNormRope ? a.Hkv : 0);
   a.inv_heads = (0x100000000ULL + a.heads - 1) / a.heads;
   // Tokens of a CTA: the fewest waves of CTAs that hold them, and so many that these waves are
   // filled but for what rounding to whole tokens leaves (12,287 tokens: 11 each, 1117 of 1216 places).
   int sms = 0;
   const int st = da::device_sms(&sms);
   if (st != DA_OK) return st;
-  const int wave = sms * kRopeCtas;  // CTAs that run at once
+  const int wave = sms * rope_ctas(MODE);  // CTAs that run at once
   const int waves = (num_tokens - 1) / (wave * kMaxTokens) + 1;
   a.tokens = (num_tokens - 1) / (wave * waves) + 1;
   const cudaError_t err =
-      r->type == DA_TYPE_F32   ? launch_rope_t<float, APPEND>(a, D, r->interleaved, s)
-      : r->type == DA_TYPE_F16 ? launch_rope_t<__half, APPEND>(a, D, r->interleaved, s)
-                               : launch_rope_t<__nv_bfloat16, APPEND>(a, D, r->interleaved, s);
+      r->type == DA_TYPE_F32   ? launch_rope_t<float, MODE>(a, D, r->interleaved, s)
+      : r->type == DA_TYPE_F16 ? launch_rope_t<__half, MODE>(a, D, r->interleaved, s)
+                               : launch_rope_t<__nv_bfloat16, MODE>(a, D, r->interleaved, s);
   return err == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
@@ -375,6 +474,46 @@ void fill_args(RopeArgs& a, const da_rope_params* r, const void* q, const void* 
   a.wide_out = aligned(q_out, 32);
 }
 
+// Checks of an append, and its arguments but for where it writes (k_to, v_to are only checked).
+int append_args(RopeArgs& a, const da_params* p, const da_rope_params* r, int32_t num_tokens,
+                const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                const int32_t* token_seq, const int32_t* block_table, float* q_out,
+                int32_t* dev_status, const void* k_to, const void* v_to) {
+  int st = da::check_append_params(p);
+  if (st != DA_OK) return st;
+  st = check_rope(r, p->head_dim);
+  if (st != DA_OK) return st;
+  if (num_tokens < 0 || (!token_seq && num_tokens != p->batch)) return DA_ERR_INVALID;
+  if (!k_new || !v_new || !positions || !block_table || !k_to || !v_to) return DA_ERR_INVALID;
+  if ((q == nullptr) != (q_out == nullptr)) return DA_ERR_INVALID;
+  if (!aligned(k_to, 16) || !aligned(v_to, 16) || !aligned(positions, 4) ||
+      !aligned(block_table, 4) || (token_seq && !aligned(token_seq, 4)) ||
+      (dev_status && !aligned(dev_status, 4)) || (q_out && !aligned(q_out, 16)))
+    return DA_ERR_INVALID;
+  const int esize = r->type == DA_TYPE_F32 ? 4 : 2;
+  st = check_rows(k_new, r->k_token_stride, r->k_head_stride, esize, num_tokens, p->num_kv_heads);
+  if (st != DA_OK) return st;
+  st = check_rows(v_new, r->v_token_stride, r->v_head_stride, esize, num_tokens, p->num_kv_heads);
+  if (st != DA_OK) return st;
+  if (q) {
+    st = check_rows(q, r->q_token_stride, r->q_head_stride, esize, num_tokens, p->num_q_heads);
+    if (st != DA_OK) return st;
+  }
+  if ((long long)(q ? p->num_q_heads : 0) + 2LL * p->num_kv_heads > 4096)
+    return DA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return DA_OK;
+  fill_args(a, r, q, k_new, positions, p->num_q_heads, p->num_kv_heads, q_out);
+  a.v = v_new;
+  a.token_seq = token_seq;
+  a.block_table = block_table;
+  a.batch = p->batch;
+  a.bs = p->block_size;
+  a.max_blocks = p->max_blocks_per_seq;
+  a.num_blocks = p->num_blocks;
+  a.dev_status = dev_status;
+  return DA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -422,7 +561,7 @@ int decode_attn_qk_norm_rope(const da_rope_params* r, int32_t num_tokens, int32_
   RopeArgs a = {};
   fill_args(a, r, q, k, positions, num_q_heads, num_kv_heads, q_out);
   a.k_out = k_out;
-  return launch_rope<false>(a, r, head_dim, num_tokens, stream);
+  return launch_rope<kNormRope>(a, r, head_dim, num_tokens, stream);
 }
 
 int decode_attn_append_paged_rope(const da_params* p, const da_rope_params* r, int32_t num_tokens,
@@ -430,42 +569,32 @@ int decode_attn_append_paged_rope(const da_params* p, const da_rope_params* r, i
                                   const int32_t* positions, const int32_t* token_seq,
                                   const int32_t* block_table, float* q_out, uint16_t* k_pool,
                                   uint16_t* v_pool, int32_t* dev_status, void* stream) {
-  int st = da::check_append_params(p);
-  if (st != DA_OK) return st;
-  st = check_rope(r, p->head_dim);
-  if (st != DA_OK) return st;
-  if (num_tokens < 0 || (!token_seq && num_tokens != p->batch)) return DA_ERR_INVALID;
-  if (!k_new || !v_new || !positions || !block_table || !k_pool || !v_pool) return DA_ERR_INVALID;
-  if ((q == nullptr) != (q_out == nullptr)) return DA_ERR_INVALID;
-  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(positions, 4) ||
-      !aligned(block_table, 4) || (token_seq && !aligned(token_seq, 4)) ||
-      (dev_status && !aligned(dev_status, 4)) || (q_out && !aligned(q_out, 16)))
-    return DA_ERR_INVALID;
-  const int esize = r->type == DA_TYPE_F32 ? 4 : 2;
-  st = check_rows(k_new, r->k_token_stride, r->k_head_stride, esize, num_tokens, p->num_kv_heads);
-  if (st != DA_OK) return st;
-  st = check_rows(v_new, r->v_token_stride, r->v_head_stride, esize, num_tokens, p->num_kv_heads);
-  if (st != DA_OK) return st;
-  if (q) {
-    st = check_rows(q, r->q_token_stride, r->q_head_stride, esize, num_tokens, p->num_q_heads);
-    if (st != DA_OK) return st;
-  }
-  if ((long long)(q ? p->num_q_heads : 0) + 2LL * p->num_kv_heads > 4096)
-    return DA_ERR_UNSUPPORTED;
-  if (num_tokens == 0) return DA_OK;
   RopeArgs a = {};
-  fill_args(a, r, q, k_new, positions, p->num_q_heads, p->num_kv_heads, q_out);
-  a.v = v_new;
-  a.token_seq = token_seq;
-  a.block_table = block_table;
+  const int st = append_args(a, p, r, num_tokens, q, k_new, v_new, positions, token_seq,
+                             block_table, q_out, dev_status, k_pool, v_pool);
+  if (st != DA_OK || num_tokens == 0) return st;
   a.k_pool = k_pool;
   a.v_pool = v_pool;
-  a.batch = p->batch;
-  a.bs = p->block_size;
-  a.max_blocks = p->max_blocks_per_seq;
-  a.num_blocks = p->num_blocks;
-  a.dev_status = dev_status;
-  return launch_rope<true>(a, r, p->head_dim, num_tokens, stream);
+  return launch_rope<kAppend>(a, r, p->head_dim, num_tokens, stream);
+}
+
+int decode_attn_append_paged_q4(const da_params* p, const da_rope_params* r, int32_t group,
+                                int32_t num_tokens, const void* q, const void* k_new,
+                                const void* v_new, const int32_t* positions,
+                                const int32_t* token_seq, const int32_t* block_table,
+                                float* q_out, uint8_t* pool, int32_t* dev_status, void* stream) {
+  int st = da::check_append_params(p);
+  if (st == DA_OK) st = da::check_q4(p, group);
+  if (st != DA_OK) return st;
+  RopeArgs a = {};
+  st = append_args(a, p, r, num_tokens, q, k_new, v_new, positions, token_seq, block_table, q_out,
+                   dev_status, pool, pool);
+  if (st != DA_OK || num_tokens == 0) return st;
+  a.q4_pool = pool;
+  a.group = group;
+  while ((1 << a.log2_bs) < p->block_size) ++a.log2_bs;
+  a.page_bytes = da::q4_page_bytes(p->block_size, p->head_dim, group);
+  return launch_rope<kAppendQ4>(a, r, p->head_dim, num_tokens, stream);
 }
 
 }  // extern "C"
