@@ -558,13 +558,14 @@ int decode_attn_gather_paged_q4(const da_params* p, int32_t group, int32_t num_t
  * bits and sum in f32.  A query row with a value that is not finite comes out
  * as NaN (where it sees a key).  out must not overlap q (DA_ERR_INVALID).
  * workspace: device scratch of decode_attn_paged_q4_workspace_size(p, q_len)
- * bytes, 256-byte aligned, of any content, for long sequences to be split across
- * CTAs; NULL with 0 bytes runs whole units per CTA.  Calls that overlap on the GPU
- * must not share it; calls of one stream may, also from several threads.
- * Everything else as for decode_attn_paged.  DA_ERR_UNSUPPORTED also where a
- * launch's query rows (q_len * num_q_heads * 1024) or its key tiles
- * (ceil(max_blocks_per_seq * block_size / 64) * num_kv_heads * 1024 *
- * ceil(q_len * num_q_heads / num_kv_heads / 8)) would not count in 31 bits.
+ * bytes, 256-byte aligned, of any content (parts of sequences that several
+ * warps share); calls that overlap on the GPU must not share it.  Calls of one
+ * stream may, also from several threads.  p->max_seq_len is not used.
+ * Everything else as for decode_attn_paged.  DA_ERR_UNSUPPORTED also where one
+ * sequence's query rows (q_len * num_q_heads) or key tiles
+ *   (max_blocks_per_seq * block_size * head_dim / 4096 + 2) * num_kv_heads *
+ *   ceil(q_len * num_q_heads / num_kv_heads / 8)
+ * would not count in 31 bits.
  */
 size_t decode_attn_paged_q4_workspace_size(const da_params* p, int32_t q_len);
 int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const float* q,

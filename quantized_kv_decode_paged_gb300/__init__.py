@@ -1395,9 +1395,8 @@ def decode_attn_paged_q4(q, pool, block_table, seq_lens, q_pos=None, *, group, s
     Returns (out, lse).
 
     ``workspace``: "auto" (the call's own, from torch's allocator on the call's
-    stream; a captured call's in its graph's memory), None (whole units per CTA) or a
-    caller-owned uint8 tensor of decode_attn_paged_q4_workspace_size bytes (any
-    content)."""
+    stream; a captured call's in its graph's memory) or a caller-owned uint8
+    tensor of decode_attn_paged_q4_workspace_size bytes (any content)."""
     torch = _torch()
     lib = _lib or load_library()
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
@@ -1426,9 +1425,9 @@ def decode_attn_paged_q4(q, pool, block_table, seq_lens, q_pos=None, *, group, s
     if dev_status is not None:
         _req(dev_status, "dev_status", i32, dev)
     auto = isinstance(workspace, str) and workspace == "auto"
-    if not auto and workspace is not None:
+    if not auto:
         if not isinstance(workspace, torch.Tensor):
-            raise ValueError("workspace must be \"auto\", None or a uint8 tensor")
+            raise ValueError("workspace must be \"auto\" or a uint8 tensor")
         _req(workspace, "workspace", torch.uint8, dev)
     _check_cuda("q", q)
     params = DaParams(B, Hq, Hkv, D, bs, columns, NB, max_seq_len, scale, softcap, sliding_window,
@@ -1447,8 +1446,7 @@ def decode_attn_paged_q4(q, pool, block_table, seq_lens, q_pos=None, *, group, s
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         st = lib.decode_attn_paged_q4(
             ref, int(group), T, q.data_ptr(), pool.data_ptr(), table_p, lens_p, pos_p,
-            out.data_ptr(), lse.data_ptr(), _ptr(workspace),
-            0 if workspace is None else workspace.numel(), _ptr(dev_status),
-            _raw_stream(torch, dev, stream))
+            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _ptr(dev_status), _raw_stream(torch, dev, stream))
     _check("decode_attn_paged_q4", st)
     return out, lse

@@ -22,20 +22,22 @@
 // f16's smallest step at m.  mma.sync adds with truncation, so a sum takes at most kChain steps and is then
 // added up in f32.
 //
-// Work.  A unit is (sequence, kv head, up to 64 query rows: query tokens x heads of the kv head), a tile 128
-// of its keys.  The tiles of all units are cut into equal shares, one a CTA; a unit that two CTAs share
-// leaves its parts' states in the workspace, which q4_merge_kernel adds up.  A producer warp copies pages (one
-// bulk copy a page of a head, which holds codes and scales of keys and values) into a ring of tiles;
-// eight consumer warps take 16 keys x 8 rows at a time: S^T = K Q^T and O^T += V^T P^T with
-// mma.m16n8k16, keys and value columns as M, so that 8 rows of Q fill N.  The row order of the
-// 16 keys (tau below) is such that the fragments of K by ldmatrix and of V by its transposing byte form meet
-// in one layout and no bank twice.
+// Work.  A unit is (sequence, kv head, up to 32 query rows: query tokens x heads of the kv head), a tile 16
+// to 64 of its keys (4 to 5 KB of codes, scales and zeros).  The tiles of all units stand in one row that is cut
+// into equal shares, one a warp (or one for the two or four warps that take a unit's groups of 8 rows): a
+// warp copies its tiles (a bulk copy a page of a head, which holds codes and scales of keys and values) into a
+// ring of its own, waits for them and works them off, and nothing of it waits for another warp.  32 keys (D =
+// 256: 16) x 8 rows at a time: S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16, keys and value columns as M,
+// so that 8 rows of Q fill N.  A unit that ends in another share than it began in leaves its parts'
+// states in the workspace; q4_merge_kernel adds them up.  The row order of the 16 keys (tau below) is such that the
+// fragments of K by ldmatrix and of V by its transposing byte form meet in one layout and no bank twice.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/decode_attn.h"
 #include "launch.h"
@@ -44,15 +46,10 @@
 
 namespace {
 
-constexpr int kWarps = 8;               // consumer warps
-constexpr int kThreads = 32 * (kWarps + 4);  // and a warpgroup of which one warp copies
-// Registers of a thread of the two kinds: 2 * 232 + 40 = 3 * 168, what the launch has.
-constexpr int kConsumerRegs = 232, kProducerRegs = 40;
-constexpr int kTok = 16 * kWarps;       // keys of a tile
 constexpr int kRows = 8;                // query rows of a warp
-constexpr int kMaxGroups = kWarps;      // groups of kRows rows of a unit
+constexpr int kMaxGroups = 4;           // groups of kRows rows of a unit
 constexpr int kMaxBatch = 1024;         // sequences of a launch
-constexpr int kChain = 4;               // steps of 16 keys between f32 additions
+constexpr int kChainKeys = 256;         // keys of a warp between f32 additions
 constexpr float kShift = 10.f, kSlack = 5.f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -67,16 +64,16 @@ struct Q4Params {
   int32_t* dev_status;
   int B, T, G, R, Hq, Hkv, log2_bs, max_blocks, num_blocks, window, causal;
   int groups, blocks;  // row groups of a unit (a power of two), units of a kv head
-  int units;           // of the batch; stages of the ring
-  int split, stages, log2_eb;  // eb: rows of a page's piece in a tile, min(block size, kTok)
+  int log2_eb;         // rows of a page's piece in a tile, min(block size, tile)
+  int shares;          // of the launch
   float qscale, softcap2, softcap_inv;
   long long page_bytes;
   unsigned long long wait_ns;
   int test_skip_arm;
   // workspace
-  int4* desc;      // [CTAs] of the unit that is cut at the CTA's end: b (or -1), unit, slot, last CTA
-  float2* part_ml;  // [CTAs][2][groups * 8]: reference and sum
-  float* part_o;    // [CTAs][2][groups * 8][D]
+  int* pre;         // [B + 1] tiles of the sequences before each
+  float2* part_ml;  // [shares][2][groups * 8]: reference and sum
+  float* part_o;    // [shares][2][groups * 8][D]
 };
 
 // ------------------------------------------------------------------ what a sequence sees
@@ -86,6 +83,7 @@ struct Seq {
   int tile0, tiles;
 };
 
+template <int TOK>
 __device__ __forceinline__ int seq_info(const Q4Params& p, int b, Seq& s) {
   int flags = 0;
   const long long cap = (long long)p.max_blocks << p.log2_bs;
@@ -107,8 +105,8 @@ __device__ __forceinline__ int seq_info(const Q4Params& p, int b, Seq& s) {
   s.lo = (int)lo;
   s.hi = (int)hi;
   s.qp = (int)(qp < 0x7fff0000 ? qp : 0x7fff0000);  // past every key and window alike
-  s.tile0 = (int)(lo / kTok);
-  s.tiles = hi > lo ? (int)((hi + kTok - 1) / kTok) - s.tile0 : 0;
+  s.tile0 = (int)(lo / TOK);
+  s.tiles = hi > lo ? (int)((hi + TOK - 1) / TOK) - s.tile0 : 0;
   return flags;
 }
 
@@ -120,68 +118,19 @@ __device__ __forceinline__ void row_keys(const Q4Params& p, const Seq& s, int t,
   if (s.tiles == 0) hi = lo;
 }
 
-__device__ __forceinline__ int share_start(int cta, int total, int grid) {
-  return (int)((long long)cta * total / grid);
-}
-
-// A CTA's part of a unit.
-struct Seg {
-  int b, kv, block;  // block of row groups
-  int i0, i1;        // tiles [i0, i1) of the sequence's
-  int slot;          // -1: the whole unit; else its place among the CTA's states
-};
-
-struct Walk {
-  int g, end, n, b;  // next tile and end of the share, segments so far, last sequence
-  int upb;           // units of a sequence
-};
-
-struct Shared {
-  uint64_t full[16], empty[16];
-  uint32_t bad[16];  // pages of a stage's tile that are outside the pool
-  float2 ml[kWarps][kRows];
-  int warp_sum[kThreads / 32];
-  int abort, flags;
-};
-
-// Next segment of this CTA; false at its end.  pre: tiles of the sequences before each.
-__device__ __forceinline__ bool next_seg(const Q4Params& p, const int* pre, Walk& w, Seg& s) {
-  int unit;
-  if (p.split) {
-    if (w.g >= w.end) return false;
-    while ((long long)pre[w.b + 1] * w.upb <= w.g) ++w.b;
-    const int nt = pre[w.b + 1] - pre[w.b], rel = w.g - pre[w.b] * w.upb;
-    unit = rel / nt;
-    s.i0 = rel - unit * nt;
-    s.i1 = min(nt, s.i0 + (w.end - w.g));
-    s.slot = s.i0 == 0 && s.i1 == nt ? -1 : w.n ? 1 : 0;
-    w.g += s.i1 - s.i0;
-    s.b = w.b;
-  } else {
-    const int u = blockIdx.x + w.n * gridDim.x;
-    if (u >= p.units) return false;
-    s.b = u / w.upb;
-    unit = u - s.b * w.upb;
-    s.i0 = 0;
-    s.i1 = -1;  // all of the sequence's
-    s.slot = -1;
+// ------------------------------------------------------------------ shares
+// Of `total` tiles share i has [start(i), start(i + 1)); with fewer tiles than shares the last ones have none.
+struct Shares {
+  int total, n;
+  __device__ __forceinline__ Shares(int tiles, int shares)
+      : total(tiles), n(tiles < shares ? tiles : shares) {}
+  __device__ __forceinline__ int start(int i) const { return (int)((long long)i * total / n); }
+  __device__ __forceinline__ int of(int tile) const {  // whose it is
+    int i = (int)((long long)tile * n / total);
+    while (i + 1 < n && start(i + 1) <= tile) ++i;
+    return i;
   }
-  ++w.n;
-  s.kv = unit / p.blocks;
-  s.block = unit - s.kv * p.blocks;
-  return true;
-}
-
-// ------------------------------------------------------------------ waits
-// A wait that runs out sets the abort flag: later waits return at once, no more copies are made, and
-// every warp runs its loops to the end on whatever shared memory holds.
-__device__ __forceinline__ bool wait_for(const Q4Params& p, Shared& sh, uint64_t* bar,
-                                         uint32_t parity) {
-  if (*(volatile int*)&sh.abort) return false;
-  if (da::mbar_wait(bar, parity, &sh.abort, p.wait_ns)) return true;
-  *(volatile int*)&sh.abort = 1;
-  return false;
-}
+};
 
 // ------------------------------------------------------------------ arithmetic
 // cap * tanh(y) in base-2 units: below |y| = 1/2 the polynomial of prefix_attn.cu's cap_near, above it
@@ -219,57 +168,114 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w, bool high) {
   return z;
 }
 
+// As mma_f16_16816, free to move among what surrounds it.
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The first of a sum.
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Untiled bulk copy to a shared-memory address (16-byte aligned both, size % 16 == 0).
+__device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(to),
+      "l"(from), "r"(bytes), "r"(da::smem_u32(bar))
+      : "memory");
+}
+
+// NG params of a row side by side in shared memory.
+template <int NG>
+__device__ __forceinline__ void load_params(uint32_t at, uint32_t (&w)[NG]) {
+  if constexpr (NG == 1) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+  } else if constexpr (NG == 2) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < NG / 4; ++i)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "r"(at + 16 * i)
+                   : "memory");
+  }
+}
+
 template <int D, int NG>
 struct Geo {
-  static constexpr int P = D / 32;       // 16-byte pieces of a row
-  static constexpr int GP = P / NG;      // pieces of a group
-  static constexpr int RB = D / 2;       // bytes of a row's codes
-  static constexpr int ROW = D + 8 * NG;  // bytes of a key's and a value's row
-  static constexpr int STAGE = kTok * ROW;
-  static constexpr bool QREG = D <= 128;  // Q's fragments in registers, else in shared memory
-  static constexpr int COL = D + 4;       // floats between rows of a state in shared memory
-  static constexpr int QBYTES = QREG ? 0 : kMaxGroups * P * 2 * 512;
-  static constexpr int OBYTES = kWarps * kRows * COL * 4;
-  static constexpr int UNION = QBYTES > OBYTES ? QBYTES : OBYTES;
+  static constexpr int P = D / 32;         // 16-byte pieces of a row
+  static constexpr int GP = P / NG;        // pieces of a group
+  static constexpr int RB = D / 2;         // bytes of a row's codes
+  static constexpr int ROW = D + 8 * NG;   // bytes of a key's and a value's row
+  static constexpr int TOK = 4096 / D;     // keys of a tile
+  static constexpr int LOG2_TOK = D == 64 ? 6 : D == 128 ? 5 : 4;
+  static constexpr int H = D == 256 ? 1 : 2;  // MMA tiles of 16 keys that are worked off together
+  static constexpr int STAGE = TOK * ROW;
+  // D = 256 has twice the accumulators, and states of twice the size
+  static constexpr int WARPS = D == 256 ? 8 : 12;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr bool QREG = D <= 128;   // Q's fragments in registers, else in shared memory
+  static constexpr int COL = D + 4;        // floats between rows of a state in shared memory
+  static constexpr int STATE = kRows * COL * 4;
+  static constexpr int QBYTES = QREG ? 0 : P * 2 * 512;
+  static constexpr int kMost = 227 * 1024 - 2048;  // dynamic shared memory, Shared beside it
+  static constexpr int FIT = (kMost - (kMaxBatch + 1) * 4) / WARPS - STATE - QBYTES;
+  static constexpr int STAGES = FIT / STAGE < 4 ? FIT / STAGE : 4;  // of a warp's ring
+  static constexpr int SMEM = WARPS * (STAGES * STAGE + STATE + QBYTES);
+  static_assert(STAGES >= 2, "a warp's ring has two stages at least");
+};
+
+template <int WARPS, int STAGES>
+struct Shared {
+  uint64_t full[WARPS][STAGES];
+  uint32_t bad[WARPS][STAGES];  // pages of a tile that are outside the pool
+  int warp_sum[WARPS];
 };
 
 template <int D, int NG>
-__global__ void __launch_bounds__(kThreads, 1) q4_kernel(const __grid_constant__ Q4Params p) {
+__global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
+    q4_kernel(const __grid_constant__ Q4Params p) {
   using g_ = Geo<D, NG>;
-  constexpr int P = g_::P, GP = g_::GP, RB = g_::RB, MT = 2 * P;
+  constexpr int P = g_::P, GP = g_::GP, RB = g_::RB, MT = 2 * P, H = g_::H, TOK = g_::TOK;
+  constexpr int STAGES = g_::STAGES;
   extern __shared__ __align__(1024) uint8_t dyn[];
-  __shared__ Shared sh;
-  uint8_t* ring = dyn;
-  uint8_t* scratch = dyn + (size_t)p.stages * g_::STAGE;  // Q's fragments, states
-  int* pre = reinterpret_cast<int*>(scratch + g_::UNION);
+  __shared__ Shared<g_::WARPS, STAGES> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = da::smem_u32(dyn) + warp * (STAGES * g_::STAGE);
+  float* state = reinterpret_cast<float*>(dyn + g_::WARPS * STAGES * g_::STAGE + warp * g_::STATE);
+  uint4* qfrag = reinterpret_cast<uint4*>(
+      dyn + g_::WARPS * (STAGES * g_::STAGE + g_::STATE) + warp * g_::QBYTES);
+  int* pre = reinterpret_cast<int*>(dyn + g_::SMEM);
   const int eb = 1 << p.log2_eb, bs = 1 << p.log2_bs;
   const int rec = eb * g_::ROW;  // bytes of a page's piece in a tile
+  const int upb = p.Hkv * p.blocks;  // units of a sequence
 
-  if (tid == 0) {
-    sh.abort = sh.flags = 0;
-    for (int i = 0; i < p.stages; ++i) {
-      da::mbar_init(&sh.full[i], 1);
-      da::mbar_init(&sh.empty[i], kWarps);
-    }
-    da::fence_mbarrier_init();
-  }
+  if (lane < STAGES) da::mbar_init(&sh.full[warp][lane], 1);
+  da::fence_mbarrier_init();
   da::wait_for_grid_before();
   da::let_next_grid_start();
 
-  Walk walk;
-  walk.upb = p.Hkv * p.blocks;
-  walk.n = 0;
-  walk.g = walk.end = walk.b = 0;
-  int total = 0, shares = 0;  // tiles, CTAs that have some: at least one each
-  if (p.split) {
-    // tiles of the sequences before each
-    const int per = (p.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.B);
+  // ------------------------------------------------ tiles of the sequences before each
+  int total = 0;
+  {
+    const int per = (p.B + g_::THREADS - 1) / g_::THREADS, b0 = min(tid * per, p.B);
     const int b1 = min(b0 + per, p.B);
     int mine = 0, bad = 0;
     for (int b = b0; b < b1; ++b) {
       Seq s;
-      bad |= seq_info(p, b, s);
+      bad |= seq_info<TOK>(p, b, s);
       pre[b + 1] = s.tiles;
       mine += s.tiles;
     }
@@ -284,240 +290,277 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kernel(const __grid_constant__
     __syncthreads();
     int run = upto - mine;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < g_::WARPS; ++i) {
       if (i < warp) run += sh.warp_sum[i];
       total += sh.warp_sum[i];
     }
-    for (int b = b0; b < b1; ++b) run += pre[b + 1], pre[b + 1] = run;
-    if (tid == 0) pre[0] = 0;
-    total *= walk.upb;
-    __syncthreads();
-    shares = min((int)gridDim.x, total);
-    if ((int)blockIdx.x < shares) {
-      walk.g = share_start(blockIdx.x, total, shares);
-      walk.end = share_start(blockIdx.x + 1, total, shares);
-      int lo = 0, hi = p.B;  // the sequence that holds the first tile
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if ((long long)pre[mid] * walk.upb <= walk.g) lo = mid;
-        else hi = mid;
-      }
-      walk.b = lo;
+    for (int b = b0; b < b1; ++b) {
+      run += pre[b + 1];
+      pre[b + 1] = run;
+      if (blockIdx.x == 0) p.pre[b + 1] = run;
     }
-  } else {
+    if (tid == 0) {
+      pre[0] = 0;
+      if (blockIdx.x == 0) p.pre[0] = 0;
+    }
     __syncthreads();
   }
+  // From here on a warp is by itself.  Its row group of the units, its share of the tiles.
+  const int slots = g_::WARPS / p.groups, rg = warp / slots;
+  const int share = blockIdx.x * slots + (warp - rg * slots);
+  const Shares shares(total * upb, p.shares);
+  if (share >= shares.n) return;
+  int tile = shares.start(share), segs = 0;
+  const int tile_end = shares.start(share + 1);
+  int seq = 0;  // the sequence that holds the first tile
+  for (int hi = p.B; hi - seq > 1;) {
+    const int mid = (seq + hi) / 2;
+    if ((long long)pre[mid] * upb <= tile) seq = mid;
+    else hi = mid;
+  }
 
-  if (warp >= kWarps) {
-    // ---------------------------------------------------------------- producer
-    da::setmaxnreg_dec<kProducerRegs>();
-    if (warp == kWarps) {
-    Seg sg;
-    int stage = 0, round = 0;
-    bool skip = p.test_skip_arm && blockIdx.x == 0;
-    const int pieces = kTok >> p.log2_eb;
-    bool went = true;
-    while (went && next_seg(p, pre, walk, sg)) {
-      Seq s;
-      const int bad = seq_info(p, sg.b, s);
-      if (!p.split && bad && lane == 0 && p.dev_status) atomicOr(p.dev_status, bad);
-      const int end = sg.i1 < 0 ? s.tiles : sg.i1;
-      auto block_id = [&](int i) {  // of this lane's piece of tile i; -1: not read, -2: outside
-        const int k = (s.tile0 + i) * kTok + (lane << p.log2_eb);
-        if (i >= end || lane >= pieces || k >= s.hi || k + eb <= s.lo) return -1;
-        const int id = p.table[(long long)sg.b * p.max_blocks + (k >> p.log2_bs)];
-        return id >= 0 && id < p.num_blocks ? id : -2;
-      };
-      int id = block_id(sg.i0);
-      for (int i = sg.i0; i < end; ++i) {
-        const int now = id;
-        id = block_id(i + 1);
-        const uint32_t bad_pages = __ballot_sync(0xffffffffu, now == -2);
-        const uint32_t pages = __ballot_sync(0xffffffffu, now >= 0);
-        if (bad_pages && lane == 0 && p.dev_status) atomicOr(p.dev_status, DA_DEV_BAD_BLOCK);
-        if (round > 0)
-          went = __all_sync(0xffffffffu, wait_for(p, sh, &sh.empty[stage], (round - 1) & 1));
-        if (!went) break;
-        if (!skip) {
-          if (lane == 0) {
-            sh.bad[stage] = bad_pages;
-            da::mbar_arrive_expect_tx(&sh.full[stage], __popc(pages) * rec);
-          }
-          __syncwarp();
-          if (now >= 0) {
-            uint8_t* to = ring + (size_t)stage * g_::STAGE + lane * rec;
-            const uint8_t* from = p.pool + ((long long)now * p.Hkv + sg.kv) * p.page_bytes;
-            if (bs <= kTok) {
-              da::bulk_load(to, from, rec, &sh.full[stage]);
-            } else {  // part of a page: codes and params of its rows from r on
-              const int r = ((s.tile0 + i) * kTok) & (bs - 1);
-              da::bulk_load(to, from + r * RB, eb * RB, &sh.full[stage]);
-              da::bulk_load(to + eb * RB, from + (bs + r) * RB, eb * RB, &sh.full[stage]);
-              const uint8_t* par = from + bs * D;
-              da::bulk_load(to + eb * D, par + r * 4 * NG, eb * 4 * NG, &sh.full[stage]);
-              da::bulk_load(to + eb * (D + 4 * NG), par + (bs + r) * 4 * NG, eb * 4 * NG,
-                            &sh.full[stage]);
-            }
-          }
-        }
-        skip = false;
-        if (++stage == p.stages) stage = 0, ++round;
+  // A unit's part.
+  struct Part {
+    Seq s;
+    int b, kv, block;
+    int i0, n;  // its first tile, of the sequence's; tiles
+    int slot;   // -1: the whole unit; else the place of its state among the share's
+  };
+  auto next_part = [&](Part& a) {
+    if (tile >= tile_end) return false;
+    while ((long long)pre[seq + 1] * upb <= tile) ++seq;
+    const int nt = pre[seq + 1] - pre[seq], rel = tile - pre[seq] * upb, unit = rel / nt;
+    a.b = seq;
+    a.kv = unit / p.blocks;
+    a.block = unit - a.kv * p.blocks;
+    a.i0 = rel - unit * nt;
+    a.n = min(nt - a.i0, tile_end - tile);
+    a.slot = a.n == nt ? -1 : segs ? 1 : 0;
+    seq_info<TOK>(p, seq, a.s);
+    tile += a.n;
+    ++segs;
+    return true;
+  };
+
+  // ------------------------------------------------ copies
+  // Block ids are loaded 32 at a time, lane by lane: piece lane % pieces of tile lane / pieces of a batch of
+  // tiles, a batch ahead of the copies; addresses and masks are worked out once a batch.
+  const int log2_pieces = g_::LOG2_TOK - p.log2_eb;
+  const int batch = 32 >> log2_pieces, my_piece = lane & ((1 << log2_pieces) - 1);
+  const int my_tile = lane >> log2_pieces;
+  const uint32_t those = (2u << ((1 << log2_pieces) - 1)) - 1;  // pieces of a tile
+  int id_next = -1;  // of this lane's piece in the next batch; -1: not read, -2: outside the pool
+  const uint8_t* from = nullptr;      // of this lane's piece in this batch, nullptr: not copied
+  uint32_t pages = 0, bad_pages = 0;  // of this batch: lanes with one to copy, with one outside the pool
+  auto block_id = [&](const Part& a, int n) {
+    const int k = (a.s.tile0 + a.i0 + n) * TOK + (my_piece << p.log2_eb);
+    if (n >= a.n || k >= a.s.hi || k + eb <= a.s.lo) return -1;
+    const int x = p.table[(long long)a.b * p.max_blocks + (k >> p.log2_bs)];
+    return x >= 0 && x < p.num_blocks ? x : -2;
+  };
+  auto take_batch = [&](const Part& a, int n) {  // from tile n of the part on
+    const int id = id_next;
+    id_next = block_id(a, n + batch + my_tile);
+    bad_pages = __ballot_sync(0xffffffffu, id == -2);
+    pages = __ballot_sync(0xffffffffu, id >= 0);
+    if (bad_pages && lane == 0 && p.dev_status) atomicOr(p.dev_status, DA_DEV_BAD_BLOCK);
+    from = p.pool + ((long long)max(id, 0) * p.Hkv + a.kv) * p.page_bytes;
+    if (bs > TOK)  // tiles are parts of a page, and every one starts at a multiple of TOK in it
+      from += (((a.s.tile0 + a.i0 + n + my_tile) * TOK) & (bs - 1)) * RB;
+    if (id < 0) from = nullptr;
+  };
+  int put = 0, got = 0;  // stage of the next copy, of the next tile to work off
+  uint32_t parity = 0;   // of the phase of `got`
+  bool skip = p.test_skip_arm && blockIdx.x == 0 && warp == 0;
+  // stages that are being copied; the phase of each one's last copy, of the next round's
+  uint32_t flying = 0, phases = 0, put_phase = 0;
+  auto copy = [&](const Part& a, int n) {  // tile n of the part
+    const int j = n & (batch - 1);
+    if (j == 0) take_batch(a, n);
+    const uint32_t copied = pages >> (j << log2_pieces) & those;
+    uint64_t* bar = &sh.full[warp][put];
+    if (!skip) {
+      if (lane == 0) {
+        sh.bad[warp][put] = bad_pages >> (j << log2_pieces) & those;
+        da::mbar_arrive_expect_tx(bar, __popc(copied) * rec);
       }
-    }
-    // After an abort: what was copied has to land before its memory is given back.
-    if (!went || *(volatile int*)&sh.abort) {
-      for (int i = 0; i < p.stages; ++i) {
-        const int rounds = round + (i < stage ? 1 : 0);  // of this stage
-        const bool unarmed = p.test_skip_arm && blockIdx.x == 0 && i == 0 && rounds == 1;
-        if (rounds > 0 && !unarmed) da::mbar_wait(&sh.full[i], (rounds - 1) & 1, nullptr, p.wait_ns);
+      __syncwarp();
+      const uint32_t to = ring + put * g_::STAGE;
+      if (bs <= TOK) {
+        if (my_tile == j && from) bulk_copy(to + my_piece * rec, from, rec, bar);
+      } else if (copied && lane == j) {  // codes and params of its rows
+        const int r = ((a.s.tile0 + a.i0 + n) * TOK) & (bs - 1);
+        bulk_copy(to, from, TOK * RB, bar);
+        bulk_copy(to + TOK * RB, from + bs * RB, TOK * RB, bar);
+        const uint8_t* par = from - r * RB + bs * D + r * 4 * NG;
+        bulk_copy(to + TOK * D, par, TOK * 4 * NG, bar);
+        bulk_copy(to + TOK * (D + 4 * NG), par + bs * 4 * NG, TOK * 4 * NG, bar);
       }
+      flying |= 1u << put;
+      phases = (phases & ~(1u << put)) | put_phase << put;
     }
-    __syncwarp();
-    }
-  } else {
-    // ---------------------------------------------------------------- consumers
-    da::setmaxnreg_inc<kConsumerRegs>();
-    const int g = lane >> 2, c = lane & 3;
-    // key of the 16 that row i of the MMA holds: tau(i) = i, tau(8 + i) = 8 + (i ^ 4).  Row j of V's
-    // 16 x 16 bytes is key pi(j), which makes its bytes 4c .. 4c + 3 the keys of the MMA's k = 2c, 2c + 8, 2c + 1, 2c + 9.
-    const int key_a = g, key_b = 8 + (g ^ 4);
-    auto row_at = [&](int t) { return t * RB + (eb == 8 && t >= 8 ? rec - 8 * RB : 0); };
-    auto par_at = [&](int t) { return t * 4 * NG + (eb == 8 && t >= 8 ? rec - 8 * 4 * NG : 0); };
-    uint32_t k_lane, v_lane;  // byte offsets of this lane's rows from the 16 keys' first
+    skip = false;
+    if (++put == STAGES) put = 0, put_phase ^= 1;
+  };
+
+  const int g = lane >> 2, c = lane & 3;
+  // key of the 16 that row i of the MMA holds: tau(i) = i, tau(8 + i) = 8 + (i ^ 4).  Row j of V's
+  // 16 x 16 bytes is key pi(j), which makes its bytes 4c .. 4c + 3 the keys of the MMA's k = 2c, 2c + 8,
+  // 2c + 1, 2c + 9.
+  const int key_a = g, key_b = 8 + (g ^ 4);
+  auto row_at = [&](int t) { return t * RB + (eb == 8 && t >= 8 ? rec - 8 * RB : 0); };
+  auto par_at = [&](int t) { return t * 4 * NG + (eb == 8 && t >= 8 ? rec - 8 * 4 * NG : 0); };
+  uint32_t k_lane, v_lane;  // byte offsets of this lane's rows from the 16 keys' first
+  {
+    const int j = lane & 7, t = lane & 8 ? 8 + (j ^ 4) : j;
+    k_lane = row_at(t) + (((lane >> 4) ^ da::piece_xor<D>(t)) << 4);
+    const int i = lane & 15, cc = i >> 2, w = i & 3;
+    const int row = 2 * cc + (w >> 1);  // of tau's first half, or (odd w) of its second
+    const int u = w & 1 ? 8 + (row ^ 4) : row;
+    v_lane = row_at(u) + (((lane >> 4) ^ da::piece_xor<D>(u)) << 4);
+  }
+  const int par_a = par_at(key_a), par_b = par_at(key_b);
+  auto state_at = [&](int i, int j) {  // piece i, rows 2g (+ 16) of it and their neighbours
+    return reinterpret_cast<float2*>(state + (2 * c + (j & 1)) * g_::COL + 32 * i + 2 * g +
+                                     (j & 2 ? 16 : 0));
+  };
+
+  bool abort = false;  // a wait ran out: no more waits and copies, the loops go on over what memory holds
+  Part a;
+  while (next_part(a)) {
+    id_next = block_id(a, my_tile);
+    if (!abort)
+      for (int n = 0; n < STAGES && n < a.n; ++n) copy(a, n);
+    const int row0 = (a.block * p.groups + rg) * kRows;  // first query row of the warp
+    // ------------------------------------------------ Q: row g, dims 32 p + 8 c ..
+    uint32_t qf[g_::QREG ? P * 2 : 1][4];  // hi of k = 2c.. and 2c + 8.., lo of the same
+    float2 f, qs[NG];                      // factors and group sums of columns 2c, 2c + 1
+    int lo[2], hi[2];
     {
-      const int j = lane & 7, t = lane & 8 ? 8 + (j ^ 4) : j;
-      k_lane = row_at(t) + (((lane >> 4) ^ da::piece_xor<D>(t)) << 4);
-      const int i = lane & 15, cc = i >> 2, w = i & 3;
-      const int row = 2 * cc + (w >> 1);  // of tau's first half, or (odd w) of its second
-      const int u = w & 1 ? 8 + (row ^ 4) : row;
-      v_lane = row_at(u) + (((lane >> 4) ^ da::piece_xor<D>(u)) << 4);
-    }
-    const int par_a = par_at(key_a), par_b = par_at(key_b);
-    const int rg = warp & (p.groups - 1), slot0 = warp / p.groups, slots = kWarps / p.groups;
-    const uint32_t ring_u32 = da::smem_u32(ring);
-    float* state = reinterpret_cast<float*>(scratch);
-    uint4* qfrag = reinterpret_cast<uint4*>(scratch) + (size_t)rg * P * 2 * 32;
-    int stage = 0, round = 0;
-    Seg sg;
-    while (next_seg(p, pre, walk, sg)) {
-      Seq s;
-      seq_info(p, sg.b, s);
-      const int end = sg.i1 < 0 ? s.tiles : sg.i1;
-      const int row0 = (sg.block * p.groups + rg) * kRows;  // first query row of the warp
-      // ------------------------------------------------ Q: row g, dims 32 p + 8 c ..
-      uint32_t qf[g_::QREG ? P * 2 : 1][4];  // hi of k = 2c.. and 2c + 8.., lo of the same
-      float f[2], qs[NG][2];                 // factors and group sums of columns 2c, 2c + 1
-      int lo[2], hi[2];
-      {
-        const int r = row0 + g;
-        float x[P][8];
-        float most = 0.f;
+      const int r = row0 + g;
+      float x[P][8];
+      float most = 0.f;
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          if (r < p.R) {
-            const int t = r / p.G, h = sg.kv * p.G + (r - t * p.G);
-            const float4* src = reinterpret_cast<const float4*>(
-                p.q + (((long long)sg.b * p.T + t) * p.Hq + h) * D + 32 * i + 8 * c);
-            const float4 a = src[0], b = src[1];
-            x[i][0] = a.x, x[i][1] = a.y, x[i][2] = a.z, x[i][3] = a.w;
-            x[i][4] = b.x, x[i][5] = b.y, x[i][6] = b.z, x[i][7] = b.w;
-          } else {
+      for (int i = 0; i < P; ++i) {
+        if (r < p.R) {
+          const int t = r / p.G, h = a.kv * p.G + (r - t * p.G);
+          const float4* src = reinterpret_cast<const float4*>(
+              p.q + (((long long)a.b * p.T + t) * p.Hq + h) * D + 32 * i + 8 * c);
+          const float4 y0 = src[0], y1 = src[1];
+          x[i][0] = y0.x, x[i][1] = y0.y, x[i][2] = y0.z, x[i][3] = y0.w;
+          x[i][4] = y1.x, x[i][5] = y1.y, x[i][6] = y1.z, x[i][7] = y1.w;
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) most = max_nan(most, fabsf(x[i][j]));
-        }
-        most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        const bool finite = most < INFINITY;
-        // most < 2^e, e at least -100
-        int e = (int)(__float_as_uint(most) >> 23) - 126;
-        e = max(e, -100);
-        const float up = finite ? __uint_as_float((uint32_t)(14 - e + 127) << 23) : 0.f;
-        float back = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * p.qscale;
-        if (!finite) back = __uint_as_float(0x7fc00000u);
-        float sum[NG] = {};
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            x[i][j] = finite ? x[i][j] * up : 0.f;
-            sum[i / GP] += x[i][j];
-          }
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {  // low nibbles of a byte, high ones
-            uint4 w;
-            da::split_half2(x[i][o], x[i][o + 4], w.x, w.z);
-            da::split_half2(x[i][o + 2], x[i][o + 6], w.y, w.w);
-            if constexpr (g_::QREG) {
-              qf[2 * i + o][0] = w.x, qf[2 * i + o][1] = w.y;
-              qf[2 * i + o][2] = w.z, qf[2 * i + o][3] = w.w;
-            } else {
-              qfrag[(2 * i + o) * 32 + lane] = w;  // warps of the same rows write the same
-            }
-          }
+          for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
         }
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 1);
-          sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 2);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          f[j] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + j));
-#pragma unroll
-          for (int n = 0; n < NG; ++n)
-            qs[n][j] = __shfl_sync(0xffffffffu, sum[n], 4 * (2 * c + j)) * f[j];
-          row_keys(p, s, (row0 + 2 * c + j) / p.G, lo[j], hi[j]);
-        }
-        __syncwarp();
+        for (int j = 0; j < 8; ++j) most = max_nan(most, fabsf(x[i][j]));
       }
-      // keys that every row sees
-      int all_lo, all_hi, unused;
-      row_keys(p, s, p.T - 1, all_lo, unused);
-      row_keys(p, s, 0, unused, all_hi);
-
-      float o[MT][4] = {}, acc[MT][4] = {};
-      float zero_sum[NG][2] = {}, l[2] = {}, m[2] = {-INFINITY, -INFINITY};
-      int chain = 0;
-      for (int i = sg.i0; i < end; ++i) {
-        wait_for(p, sh, &sh.full[stage], round & 1);
-        const uint32_t bad = sh.bad[stage];
-        const uint32_t base = ring_u32 + stage * g_::STAGE;
-        for (int step = slot0; step < kTok / 16; step += slots) {
-          const int tok = 16 * step, key0 = (s.tile0 + i) * kTok + tok;
-          if (key0 >= s.hi || key0 + 16 <= s.lo) continue;
-          const int piece = tok >> p.log2_eb, r0 = tok & (eb - 1);
-          const uint32_t at = base + piece * rec;
-          // -------------------------------------------- scores
-          uint32_t kw[P][2];
+      most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      const bool finite = most < INFINITY;
+      // most < 2^e, e at least -100
+      int e = (int)(__float_as_uint(most) >> 23) - 126;
+      e = max(e, -100);
+      const float up = finite ? __uint_as_float((uint32_t)(14 - e + 127) << 23) : 0.f;
+      float back = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * p.qscale;
+      if (!finite) back = __uint_as_float(0x7fc00000u);
+      float sum[NG] = {};
 #pragma unroll
-          for (int i2 = 0; i2 < P / 2; ++i2)
-            da::ldsm_x4((at + r0 * RB + k_lane) ^ (i2 << 5), kw[2 * i2][0], kw[2 * i2][1],
-                        kw[2 * i2 + 1][0], kw[2 * i2 + 1][1]);
-          const uint8_t* par = ring + (size_t)stage * g_::STAGE + piece * rec + eb * D + r0 * 4 * NG;
-          uint32_t kp[2][NG], vp[2][NG];
+      for (int i = 0; i < P; ++i) {
 #pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            kp[0][n] = *reinterpret_cast<const uint32_t*>(par + par_a + 4 * n);
-            kp[1][n] = *reinterpret_cast<const uint32_t*>(par + par_b + 4 * n);
-            vp[0][n] = *reinterpret_cast<const uint32_t*>(par + eb * 4 * NG + par_a + 4 * n);
-            vp[1][n] = *reinterpret_cast<const uint32_t*>(par + eb * 4 * NG + par_b + 4 * n);
+        for (int j = 0; j < 8; ++j) {
+          x[i][j] = finite ? x[i][j] * up : 0.f;
+          sum[i / GP] += x[i][j];
+        }
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {  // low nibbles of a byte, high ones
+          uint4 w;
+          da::split_half2(x[i][o], x[i][o + 4], w.x, w.z);
+          da::split_half2(x[i][o + 2], x[i][o + 6], w.y, w.w);
+          if constexpr (g_::QREG) {
+            qf[2 * i + o][0] = w.x, qf[2 * i + o][1] = w.y;
+            qf[2 * i + o][2] = w.z, qf[2 * i + o][3] = w.w;
+          } else {
+            qfrag[(2 * i + o) * 32 + lane] = w;  // warps of the same rows write the same
           }
-          float x[4];  // keys a, a, b, b; columns 2c, 2c + 1
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 1);
+        sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 2);
+      }
+      f.x = __shfl_sync(0xffffffffu, back, 8 * c);
+      f.y = __shfl_sync(0xffffffffu, back, 8 * c + 4);
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        qs[n].x = __shfl_sync(0xffffffffu, sum[n], 8 * c) * f.x;
+        qs[n].y = __shfl_sync(0xffffffffu, sum[n], 8 * c + 4) * f.y;
+      }
+      f.x *= 0x1p9f, f.y *= 0x1p9f;  // the codes come times 2^-9
+#pragma unroll
+      for (int j = 0; j < 2; ++j) row_keys(p, a.s, (row0 + 2 * c + j) / p.G, lo[j], hi[j]);
+      __syncwarp();
+    }
+    // keys that every row sees
+    int all_lo, all_hi, unused;
+    row_keys(p, a.s, p.T - 1, all_lo, unused);
+    row_keys(p, a.s, 0, unused, all_hi);
+
+
+    float acc[MT][4] = {};
+    float2 zero_sum[NG] = {}, l = {}, m = make_float2(-INFINITY, -INFINITY);
+    // what has left acc lies in `state`, to be multiplied by `due`
+    float2 due = make_float2(1.f, 1.f);
+    bool kept = false;
+    int chain = 0;
+    for (int n = 0; n < a.n; ++n) {
+      if (!abort) {
+        if (da::mbar_wait(&sh.full[warp][got], parity, nullptr, p.wait_ns)) flying &= ~(1u << got);
+        else abort = true;
+        abort = __any_sync(0xffffffffu, abort);
+      }
+      const uint32_t bad = sh.bad[warp][got];
+      const uint32_t base = ring + got * g_::STAGE;
+      const int first = (a.s.tile0 + a.i0 + n) * TOK;
+#pragma unroll 1
+      for (int tok = 0; tok < TOK; tok += 16 * H) {
+        const int key0 = first + tok;
+        if (key0 >= a.s.hi || key0 + 16 * H <= a.s.lo) continue;
+        auto work = [&](auto masked) {
+          constexpr bool PART = decltype(masked)::value;
+          uint32_t at[H], par[H];  // first row and first param of the page's piece
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            const int t = tok + 16 * h, r0 = t & (eb - 1);
+            const uint32_t page = base + (t >> p.log2_eb) * rec;
+            at[h] = page + r0 * RB;
+            par[h] = page + eb * D + r0 * 4 * NG;
+          }
+          uint32_t kw[H][P][2], kp[H][2][NG], vp[H][2][NG];
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+#pragma unroll
+            for (int i2 = 0; i2 < P / 2; ++i2)
+              da::ldsm_x4((at[h] + k_lane) ^ (i2 << 5), kw[h][2 * i2][0], kw[h][2 * i2][1],
+                          kw[h][2 * i2 + 1][0], kw[h][2 * i2 + 1][1]);
+            load_params<NG>(par[h] + par_a, kp[h][0]);
+            load_params<NG>(par[h] + par_b, kp[h][1]);
+            load_params<NG>(par[h] + eb * 4 * NG + par_a, vp[h][0]);
+            load_params<NG>(par[h] + eb * 4 * NG + par_b, vp[h][1]);
+          }
+          // -------------------------------------------- scores
+          float2 x[H][2];  // of keys a and b; columns 2c, 2c + 1
           {
-            float u[4] = {}, z[4] = {};
+            float2 u[H][2], z[H][2];
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-              float ah[4] = {}, al[4] = {};
+              float ah[H][4], al[H][4];
 #pragma unroll
               for (int i2 = n * GP; i2 < (n + 1) * GP; ++i2) {
-                const uint32_t a0 = kw[i2][0], a1 = kw[i2][1], b0 = a0 >> 8, b1 = a1 >> 8;
 #pragma unroll
                 for (int o2 = 0; o2 < 2; ++o2) {
-                  const uint32_t f0 = codes2(a0, o2), f1 = codes2(a1, o2);
-                  const uint32_t f2 = codes2(b0, o2), f3 = codes2(b1, o2);
                   uint32_t q0, q1, q2, q3;
                   if constexpr (g_::QREG) {
                     q0 = qf[2 * i2 + o2][0], q1 = qf[2 * i2 + o2][1];
@@ -526,275 +569,319 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kernel(const __grid_constant__
                     const uint4 w = qfrag[(2 * i2 + o2) * 32 + lane];
                     q0 = w.x, q1 = w.y, q2 = w.z, q3 = w.w;
                   }
-                  da::mma_f16_16816(ah, f0, f1, f2, f3, q0, q1);
-                  da::mma_f16_16816(al, f0, f1, f2, f3, q2, q3);
+#pragma unroll
+                  for (int h = 0; h < H; ++h) {
+                    const uint32_t a0 = kw[h][i2][0], a1 = kw[h][i2][1];
+                    const uint32_t f0 = codes2(a0, o2), f1 = codes2(a1, o2);
+                    const uint32_t f2 = codes2(a0 >> 8, o2), f3 = codes2(a1 >> 8, o2);
+                    if (i2 == n * GP && o2 == 0) {
+                      mma_first(ah[h], f0, f1, f2, f3, q0, q1);
+                      mma_first(al[h], f0, f1, f2, f3, q2, q3);
+                    } else {
+                      mma(ah[h], f0, f1, f2, f3, q0, q1);
+                      mma(al[h], f0, f1, f2, f3, q2, q3);
+                    }
+                  }
                 }
               }
-              const float sa = half_lo(kp[0][n]) * 0x1p9f, sb = half_lo(kp[1][n]) * 0x1p9f;
-              const float za = fmaf(sa, 0x1p-6f, half_hi(kp[0][n]));
-              const float zb = fmaf(sb, 0x1p-6f, half_hi(kp[1][n]));
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                u[j] = fmaf(ah[j] + al[j], sa, u[j]);
-                u[2 + j] = fmaf(ah[2 + j] + al[2 + j], sb, u[2 + j]);
-                z[j] = fmaf(za, qs[n][j], z[j]);
-                z[2 + j] = fmaf(zb, qs[n][j], z[2 + j]);
-              }
+              for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float sk = half_lo(kp[h][k][n]);
+                  const float zk = fmaf(8.f, sk, half_hi(kp[h][k][n]));
+                  const float2 t = da::add2(make_float2(ah[h][2 * k], ah[h][2 * k + 1]),
+                                            make_float2(al[h][2 * k], al[h][2 * k + 1]));
+                  if (n == 0) {
+                    u[h][k] = make_float2(t.x * sk, t.y * sk);
+                    z[h][k] = make_float2(zk * qs[n].x, zk * qs[n].y);
+                  } else {
+                    u[h][k] = make_float2(fmaf(t.x, sk, u[h][k].x), fmaf(t.y, sk, u[h][k].y));
+                    z[h][k] = make_float2(fmaf(zk, qs[n].x, z[h][k].x),
+                                          fmaf(zk, qs[n].y, z[h][k].y));
+                  }
+                }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = fmaf(u[j], f[j & 1], z[j]);
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) x[h][k] = da::fma2(u[h][k], f, z[h][k]);
           }
+          uint32_t vw[H][P][2];
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i2 = 0; i2 < P / 2; ++i2)
+              da::ldsm_b8_x2_trans((at[h] + eb * RB + v_lane) ^ (i2 << 5), vw[h][2 * i2][0],
+                                   vw[h][2 * i2][1], vw[h][2 * i2 + 1][0], vw[h][2 * i2 + 1][1]);
           if (p.softcap2 > 0.f) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = soft_cap(x[j] * p.softcap_inv, p.softcap2);
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                x[h][k].x = soft_cap(x[h][k].x * p.softcap_inv, p.softcap2);
+                x[h][k].y = soft_cap(x[h][k].y * p.softcap_inv, p.softcap2);
+              }
           }
           // -------------------------------------------- masks
-          const bool part = key0 < all_lo || key0 + 16 > all_hi || bad;
-          uint32_t seen = 15u;
-          if (part) {
-            seen = 0;
+          uint32_t seen = 0;
+          if constexpr (PART) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int t = j < 2 ? key_a : key_b, k = key0 + t;
+            for (int j = 0; j < 4 * H; ++j) {
+              const int t = 16 * (j / 4) + (j % 4 < 2 ? key_a : key_b), k = key0 + t;
+              float2& y = x[j / 4][j % 4 / 2];
               if (k >= lo[j & 1] && k < hi[j & 1] && !(bad >> ((tok + t) >> p.log2_eb) & 1))
                 seen |= 1u << j;
               else
-                x[j] = -INFINITY;
+                (j & 1 ? y.y : y.x) = -INFINITY;
             }
           }
-          // -------------------------------------------- reference and weights
-          int ea = 0, eb2 = 0;  // largest value scale, as f16 bits
+          // -------------------------------------------- reference
+          float2 top = make_float2(-INFINITY, -INFINITY);  // a NaN score leaves it alone
 #pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            ea = max(ea, (int)(vp[0][n] & 0x7fffu));
-            eb2 = max(eb2, (int)(vp[1][n] & 0x7fffu));
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t most = vp[h][k][0] & 0x7fffu;
+#pragma unroll
+              for (int n = 1; n < NG; ++n) most = max(most, vp[h][k][n] & 0x7fffu);
+              // exponent of the key's largest value scale: the scale is less than 2^e
+              const float e = __uint_as_float(most >> 10 | 0x4b000000u) - (8388608.f + 14.f);
+              top.x = fmaxf(top.x, x[h][k].x + e);
+              top.y = fmaxf(top.y, x[h][k].y + e);
+            }
+          if (__any_sync(0xffffffffu, top.x > m.x + kSlack || top.y > m.y + kSlack)) {
+            float2 by;
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+              top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, off));
+              top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, off));
+            }
+            top.x = fmaxf(top.x, m.x), top.y = fmaxf(top.y, m.y);
+            by.x = top.x == m.x ? 1.f : da::ex2_ftz(m.x - top.x);
+            by.y = top.y == m.y ? 1.f : da::ex2_ftz(m.y - top.y);
+            m = top;
+            l = da::mul2(l, by);
+            due = da::mul2(due, by);
+#pragma unroll
+            for (int n = 0; n < NG; ++n) zero_sum[n] = da::mul2(zero_sum[n], by);
+#pragma unroll
+            for (int i2 = 0; i2 < MT; ++i2) {
+              acc[i2][0] *= by.x, acc[i2][1] *= by.y;
+              acc[i2][2] *= by.x, acc[i2][3] *= by.y;
+            }
           }
-          const float fa = (float)((ea >> 10) - 14), fb = (float)((eb2 >> 10) - 14);
-          const bool out_of = x[0] + fa > m[0] + kSlack || x[1] + fa > m[1] + kSlack ||
-                              x[2] + fb > m[0] + kSlack || x[3] + fb > m[1] + kSlack;
-          if (__any_sync(0xffffffffu, out_of)) {
+          // -------------------------------------------- weights
+          {
+            const float2 up = make_float2(kShift - m.x, kShift - m.y);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float n = fmaxf(x[j] + fa, x[2 + j] + fb);
+            for (int h = 0; h < H; ++h)
 #pragma unroll
-              for (int off = 4; off < 32; off <<= 1)
-                n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, off));
-              n = fmaxf(n, m[j]);
-              const float by = n == m[j] ? 1.f : da::ex2_ftz(m[j] - n);
-              m[j] = n;
-              l[j] *= by;
-#pragma unroll
-              for (int i2 = 0; i2 < NG; ++i2) zero_sum[i2][j] *= by;
-#pragma unroll
-              for (int i2 = 0; i2 < MT; ++i2) {
-                o[i2][j] *= by, o[i2][2 + j] *= by;
-                acc[i2][j] *= by, acc[i2][2 + j] *= by;
+              for (int k = 0; k < 2; ++k) {
+                float2 y = da::add2(x[h][k], up);
+                y.x = da::ex2_ftz(y.x), y.y = da::ex2_ftz(y.y);
+                if constexpr (PART) {
+                  if (!(seen >> (4 * h + 2 * k) & 1)) y.x = 0.f;
+                  if (!(seen >> (4 * h + 2 * k) & 2)) y.y = 0.f;
+                }
+                x[h][k] = y;
+                l = da::add2(l, y);
               }
-            }
-          }
-          float w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            w[j] = da::ex2_ftz(x[j] + (kShift - m[j & 1]));
-            if (part && !(seen >> j & 1)) w[j] = 0.f;
-            l[j & 1] += w[j];
           }
           // -------------------------------------------- values
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
-            const float sa = half_lo(vp[0][n]), sb = half_lo(vp[1][n]);
-            const float za = fmaf(8.f, sa, half_hi(vp[0][n])), zb = fmaf(8.f, sb, half_hi(vp[1][n]));
-            float ws[4] = {w[0] * sa, w[1] * sa, w[2] * sb, w[3] * sb};
-            float wz[4] = {w[0] * za, w[1] * za, w[2] * zb, w[3] * zb};
-            if (part) {  // a key that is not seen may have any scale and zero
+            uint32_t ph[H][2], pl[H][2];  // P^T: the two terms
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (!(seen >> j & 1)) ws[j] = wz[j] = 0.f;
-            }
+            for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) zero_sum[n][j] += wz[j] + wz[2 + j];
-            uint32_t h0, h1, l0, l1;
-            da::split_half2(ws[0], ws[1], h0, l0);
-            da::split_half2(ws[2], ws[3], h1, l1);
-            h0 = da::movmatrix_trans(h0), h1 = da::movmatrix_trans(h1);
-            l0 = da::movmatrix_trans(l0), l1 = da::movmatrix_trans(l1);
-#pragma unroll
-            for (int i2 = n * GP; i2 < (n + 1) * GP; ++i2) {
-              // pieces come in pairs: lanes 16 to 31 address the odd one
-              uint32_t r0_, r1_, r2_, r3_;
-              da::ldsm_b8_x2_trans((at + (eb + r0) * RB + v_lane) ^ (i2 / 2 << 5), r0_, r1_, r2_, r3_);
-              const uint32_t a0 = i2 & 1 ? r2_ : r0_, a1 = i2 & 1 ? r3_ : r1_;
-              const uint32_t b0 = a0 >> 8, b1 = a1 >> 8;
-#pragma unroll
-              for (int o2 = 0; o2 < 2; ++o2) {
-                const uint32_t f0 = codes2(a0, o2), f1 = codes2(a1, o2);
-                const uint32_t f2 = codes2(b0, o2), f3 = codes2(b1, o2);
-                da::mma_f16_16816(acc[2 * i2 + o2], f0, f1, f2, f3, h0, h1);
-                da::mma_f16_16816(acc[2 * i2 + o2], f0, f1, f2, f3, l0, l1);
+              for (int k = 0; k < 2; ++k) {
+                const float sv = half_lo(vp[h][k][n]);
+                const float zv = fmaf(8.f, sv, half_hi(vp[h][k][n]));
+                float2 w = make_float2(x[h][k].x * sv, x[h][k].y * sv);
+                if constexpr (PART) {  // a key that is not seen may have any scale and zero
+                  const bool on0 = seen >> (4 * h + 2 * k) & 1, on1 = seen >> (4 * h + 2 * k) & 2;
+                  w = make_float2(on0 ? w.x : 0.f, on1 ? w.y : 0.f);
+                  zero_sum[n].x += on0 ? x[h][k].x * zv : 0.f;
+                  zero_sum[n].y += on1 ? x[h][k].y * zv : 0.f;
+                } else {
+                  zero_sum[n].x = fmaf(x[h][k].x, zv, zero_sum[n].x);
+                  zero_sum[n].y = fmaf(x[h][k].y, zv, zero_sum[n].y);
+                }
+                da::split_half2(w.x, w.y, ph[h][k], pl[h][k]);
+                ph[h][k] = da::movmatrix_trans(ph[h][k]);
+                pl[h][k] = da::movmatrix_trans(pl[h][k]);
               }
-            }
+            // two pieces' products of one term, then of the other: each waits for none before it
+            constexpr int PP = GP > 1 ? 2 : 1;
+#pragma unroll
+            for (int i2 = n * GP; i2 < (n + 1) * GP; i2 += PP)
+#pragma unroll
+              for (int h = 0; h < H; ++h) {
+                uint32_t fr[2 * PP][4];
+#pragma unroll
+                for (int k = 0; k < 2 * PP; ++k) {
+                  const uint32_t a0 = vw[h][i2 + k / 2][0], a1 = vw[h][i2 + k / 2][1];
+                  fr[k][0] = codes2(a0, k & 1), fr[k][1] = codes2(a1, k & 1);
+                  fr[k][2] = codes2(a0 >> 8, k & 1), fr[k][3] = codes2(a1 >> 8, k & 1);
+                  mma(acc[2 * i2 + k], fr[k][0], fr[k][1], fr[k][2], fr[k][3], ph[h][0], ph[h][1]);
+                }
+#pragma unroll
+                for (int k = 0; k < 2 * PP; ++k)
+                  mma(acc[2 * i2 + k], fr[k][0], fr[k][1], fr[k][2], fr[k][3], pl[h][0], pl[h][1]);
+              }
           }
-          if (++chain == kChain) {
-            chain = 0;
+        };
+        if (key0 < all_lo || key0 + 16 * H > all_hi || bad) work(std::true_type());
+        else work(std::false_type());
+      }
+      __syncwarp();  // the stage is read
+      if (++got == STAGES) got = 0, parity ^= 1;
+      if (n + STAGES < a.n && !abort) copy(a, n + STAGES);
+      if (++chain == kChainKeys / TOK && n + 1 < a.n) {
+        const float2 d0 = make_float2(due.x, due.x), d1 = make_float2(due.y, due.y);
 #pragma unroll
-            for (int i2 = 0; i2 < MT; ++i2)
+        for (int i = 0; i < P; ++i)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) o[i2][j] += acc[i2][j], acc[i2][j] = 0.f;
+          for (int j = 0; j < 4; ++j) {
+            float2 v = make_float2(acc[2 * i][j], acc[2 * i + 1][j]);
+            if (kept) v = da::fma2(*state_at(i, j), j & 1 ? d1 : d0, v);
+            *state_at(i, j) = v;
+            acc[2 * i][j] = acc[2 * i + 1][j] = 0.f;
           }
-        }
-        __syncwarp();
-        if (lane == 0) da::mbar_arrive(&sh.empty[stage]);
-        if (++stage == p.stages) stage = 0, ++round;
-      }
-      // ------------------------------------------------ the warps' states to one
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          l[j] += __shfl_xor_sync(0xffffffffu, l[j], off);
-#pragma unroll
-          for (int n = 0; n < NG; ++n)
-            zero_sum[n][j] += __shfl_xor_sync(0xffffffffu, zero_sum[n][j], off);
-        }
-      }
-      if (!g_::QREG) da::named_bar_sync(1, 32 * kWarps);  // Q's fragments are read
-      if (g == 0) {
-        sh.ml[warp][2 * c] = make_float2(m[0], l[0]);
-        sh.ml[warp][2 * c + 1] = make_float2(m[1], l[1]);
-      }
-#pragma unroll
-      for (int i2 = 0; i2 < P; ++i2) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // row of V: 32 i2 + 2 g (+ 16): low nibble and high one side by side
-          const float z = zero_sum[i2 / GP][j & 1];
-          float2 v;
-          v.x = fmaf(o[2 * i2][j] + acc[2 * i2][j], 0x1p9f, z);
-          v.y = fmaf(o[2 * i2 + 1][j] + acc[2 * i2 + 1][j], 0x1p9f, z);
-          *reinterpret_cast<float2*>(state + (warp * kRows + 2 * c + (j & 1)) * g_::COL + 32 * i2 +
-                                     2 * g + (j & 2 ? 16 : 0)) = v;
-        }
-      }
-      da::named_bar_sync(1, 32 * kWarps);
-      for (int i = tid; i < p.groups * kRows * (D / 4); i += 32 * kWarps) {
-        const int row = i / (D / 4), d = i % (D / 4) * 4, grp = row / kRows, col = row % kRows;
-        const int r = sg.block * p.groups * kRows + row;
-        if (r >= p.R) continue;
-        float top = -INFINITY;
-        for (int w = grp; w < kWarps; w += p.groups) top = fmaxf(top, sh.ml[w][col].x);
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        float tl = 0.f;
-        for (int w = grp; w < kWarps; w += p.groups) {
-          const float2 ml = sh.ml[w][col];
-          const float by = ml.x == top ? 1.f : da::ex2_ftz(ml.x - top);
-          const float4 v = *reinterpret_cast<const float4*>(state + (w * kRows + col) * g_::COL + d);
-          sum.x = fmaf(by, v.x, sum.x), sum.y = fmaf(by, v.y, sum.y);
-          sum.z = fmaf(by, v.z, sum.z), sum.w = fmaf(by, v.w, sum.w);
-          tl = fmaf(by, ml.y, tl);
-        }
-        if (sg.slot < 0) {
-          const int t = r / p.G, h = sg.kv * p.G + (r - t * p.G);
-          const long long to = ((long long)sg.b * p.T + t) * p.Hq + h;
-          const float inv = tl == 0.f ? 0.f : 1.f / tl;
-          *reinterpret_cast<float4*>(p.out + to * D + d) =
-              make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-          if (d == 0 && p.lse)
-            p.lse[to] = tl == 0.f ? -INFINITY : (top - kShift + log2f(tl)) * kLn2;
-        } else {
-          const long long to = (long long)(blockIdx.x * 2 + sg.slot) * p.groups * kRows + row;
-          *reinterpret_cast<float4*>(p.part_o + to * D + d) = sum;
-          if (d == 0) p.part_ml[to] = make_float2(top, tl);
-        }
-      }
-      da::named_bar_sync(1, 32 * kWarps);  // the states are read
-    }
-    if (p.split) {
-      // the unit that is cut at this CTA's end, if it starts here: who has its parts
-      if (tid == 0) {
-        int4 d = make_int4(-1, 0, 0, 0);
-        if (walk.n > 0 && sg.slot >= 0 && sg.i0 == 0) {
-          const int nt = pre[sg.b + 1] - pre[sg.b];
-          const int last = pre[sg.b] * walk.upb + (sg.kv * p.blocks + sg.block + 1) * nt - 1;
-          // the CTA whose share holds tile `last`
-          int cta = (int)(((long long)last * shares) / total);
-          while (cta + 1 < shares && share_start(cta + 1, total, shares) <= last) ++cta;
-          d = make_int4(sg.b, sg.kv * p.blocks + sg.block, sg.slot, cta);
-        }
-        p.desc[blockIdx.x] = d;
-      }
-      // sequences without a key to see
-      for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        if (pre[b + 1] != pre[b]) continue;
-        const long long rows = (long long)p.T * p.Hq;
-        float4* to = reinterpret_cast<float4*>(p.out + b * rows * D);
-        for (long long i = tid; i < rows * (D / 4); i += 32 * kWarps)
-          to[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.lse)
-          for (long long i = tid; i < rows; i += 32 * kWarps) p.lse[b * rows + i] = -INFINITY;
+        due = make_float2(1.f, 1.f);
+        kept = true;
+        chain = 0;
       }
     }
+    // ------------------------------------------------ the part's state
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      l.x += __shfl_xor_sync(0xffffffffu, l.x, off);
+      l.y += __shfl_xor_sync(0xffffffffu, l.y, off);
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        zero_sum[n].x += __shfl_xor_sync(0xffffffffu, zero_sum[n].x, off);
+        zero_sum[n].y += __shfl_xor_sync(0xffffffffu, zero_sum[n].y, off);
+      }
+    }
+    float* to[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // rows of columns 2c, 2c + 1
+      const int r = row0 + 2 * c + j;
+      const float mj = j ? m.y : m.x, lj = j ? l.y : l.x;
+      to[j] = nullptr;
+      if (r >= p.R) continue;
+      if (a.slot < 0) {
+        const int t = r / p.G, h = a.kv * p.G + (r - t * p.G);
+        const long long row = ((long long)a.b * p.T + t) * p.Hq + h;
+        to[j] = p.out + row * D;
+        if (g == 0 && p.lse) p.lse[row] = lj == 0.f ? -INFINITY : (mj - kShift + log2f(lj)) * kLn2;
+      } else {
+        const long long row = ((long long)share * 2 + a.slot) * p.groups * kRows + rg * kRows + 2 * c + j;
+        to[j] = p.part_o + row * D;
+        if (g == 0) p.part_ml[row] = make_float2(mj, lj);
+      }
+    }
+    const float2 by = a.slot < 0 ? make_float2(l.x == 0.f ? 0.f : 1.f / l.x, l.y == 0.f ? 0.f : 1.f / l.y)
+                                 : make_float2(1.f, 1.f);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float2 v = make_float2(acc[2 * i][j], acc[2 * i + 1][j]);
+        const float d = j & 1 ? due.y : due.x, f = j & 1 ? by.y : by.x;
+        if (kept) v = da::fma2(*state_at(i, j), make_float2(d, d), v);
+        const float z = j & 1 ? zero_sum[i / GP].y : zero_sum[i / GP].x;
+        v = da::fma2(v, make_float2(0x1p9f, 0x1p9f), make_float2(z, z));
+        if (to[j & 1])
+          *reinterpret_cast<float2*>(to[j & 1] + 32 * i + 2 * g + (j & 2 ? 16 : 0)) =
+              make_float2(v.x * f, v.y * f);
+      }
   }
-  __syncthreads();
-  if (tid == 0 && sh.abort && p.dev_status) atomicOr(p.dev_status, DA_DEV_TIMEOUT);
+  // What is being copied has to land before its memory is given back: only after an abort is there any.
+  if (abort && lane == 0) {
+    if (p.dev_status) atomicOr(p.dev_status, DA_DEV_TIMEOUT);
+    for (int i = 0; i < STAGES; ++i)
+      if (flying >> i & 1) da::mbar_wait(&sh.full[warp][i], phases >> i & 1, nullptr, p.wait_ns);
+  }
 }
 
-// Adds up the states of a unit that CTAs share: block (i, y) rows 2y, 2y + 1 of the unit that starts in CTA
-// i's share and is cut at its end.
-constexpr int kMergeThreads = 128, kMergeRows = 2, kMaxParts = 1024;
+// Adds up the states of units that several shares hold, a warp an output row; rows of sequences without a key
+// to see are written here too.
+constexpr int kMergeWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) q4_merge_kernel(const __grid_constant__ Q4Params p) {
-  __shared__ float by[kMergeRows][kMaxParts];
-  __shared__ float2 ml[kMergeRows];
+__global__ void __launch_bounds__(32 * kMergeWarps) q4_merge_kernel(const __grid_constant__ Q4Params p) {
+  constexpr int V = D / 32;  // values of a lane, side by side
+  using Vec = typename std::conditional<V == 2, float2, float4>::type;
+  constexpr int N = V == 8 ? 2 : 1;  // vectors of a lane, 128 values apart
   da::wait_for_grid_before();
   da::let_next_grid_start();
-  const int4 d = p.desc[blockIdx.x];
-  if (d.x < 0) return;
-  const int rows = p.groups * kRows, parts = d.w - blockIdx.x + 1;
-  const int kv = d.y / p.blocks, block = d.y - kv * p.blocks;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  // place of part i of row r: the first one is in the slot that d names, the others in slot 0
-  auto place = [&](int i, int r) {
-    return (long long)((blockIdx.x + i) * 2 + (i ? 0 : d.z)) * rows + blockIdx.y * kMergeRows + r;
+  const int lane = threadIdx.x % 32;
+  const long long row = (long long)blockIdx.x * kMergeWarps + threadIdx.x / 32;
+  if (row >= (long long)p.B * p.T * p.Hq) return;
+  const int b = (int)(row / (p.T * p.Hq)), th = (int)(row - (long long)b * p.T * p.Hq);
+  const int t = th / p.Hq, h = th - t * p.Hq, kv = h / p.G, r = t * p.G + (h - kv * p.G);
+  const int pre0 = p.pre[b], nt = p.pre[b + 1] - pre0, all = p.pre[p.B], upb = p.Hkv * p.blocks;
+  Vec* out = reinterpret_cast<Vec*>(p.out + row * D) + lane;
+  if (nt == 0) {
+    for (int i = 0; i < N; ++i) out[32 * i] = Vec{};
+    if (lane == 0 && p.lse) p.lse[row] = -INFINITY;
+    return;
+  }
+  const int unit_rows = p.groups * kRows, block = r / unit_rows;
+  const Shares shares(all * upb, p.shares);
+  const int u0 = pre0 * upb + (kv * p.blocks + block) * nt, u1 = u0 + nt;
+  const int s0 = shares.of(u0), s1 = shares.of(u1 - 1);
+  if (s0 == s1) return;  // whole
+  // the first part is its share's first one if the unit starts there, the others are their shares' first
+  const int slot0 = shares.start(s0) == u0 ? 0 : 1;
+  auto place = [&](int s) {
+    return ((long long)s * 2 + (s == s0 ? slot0 : 0)) * unit_rows + (r - block * unit_rows);
   };
-  if (warp < kMergeRows) {
-    float top = -INFINITY, l = 0.f;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_ml[place(i, warp)].x);
-    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    for (int i = lane; i < parts; i += 32) {
-      const float2 x = p.part_ml[place(i, warp)];
-      const float f = x.x == top ? 1.f : da::ex2_ftz(x.x - top);
-      by[warp][i] = f;
-      l = fmaf(f, x.y, l);
+  float top = -INFINITY, l = 0.f;
+  for (int s = s0 + lane; s <= s1; s += 32) top = fmaxf(top, p.part_ml[place(s)].x);
+  for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  float sum[N][V / N] = {};
+  for (int base = s0; base <= s1; base += 32) {
+    float mine = 0.f;
+    if (base + lane <= s1) {
+      const float2 x = p.part_ml[place(base + lane)];
+      mine = x.x == top ? 1.f : da::ex2_ftz(x.x - top);
+      l = fmaf(mine, x.y, l);
     }
-    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    if (lane == 0) ml[warp] = make_float2(top, l);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kMergeRows * D / 4; i += kMergeThreads) {
-    const int r = i / (D / 4), col = i % (D / 4) * 4;
-    const int row = block * rows + blockIdx.y * kMergeRows + r;
-    if (row >= p.R) continue;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int n = min(32, s1 - base + 1);
 #pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + place(k, r) * D + col);
-      const float f = by[r][k];
-      sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
-      sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
+    for (int k = 0; k < n; ++k) {
+      const float f = __shfl_sync(0xffffffffu, mine, k);
+      const Vec* src = reinterpret_cast<const Vec*>(p.part_o + place(base + k) * D) + lane;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const Vec v = src[32 * i];
+        const float* y = reinterpret_cast<const float*>(&v);
+#pragma unroll
+        for (int j = 0; j < V / N; ++j) sum[i][j] = fmaf(f, y[j], sum[i][j]);
+      }
     }
-    const float l = ml[r].y, inv = l == 0.f ? 0.f : 1.f / l;
-    const int t = row / p.G, h = kv * p.G + (row - t * p.G);
-    const long long to = ((long long)d.x * p.T + t) * p.Hq + h;
-    *reinterpret_cast<float4*>(p.out + to * D + col) =
-        make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-    if (col == 0 && p.lse)
-      p.lse[to] = l == 0.f ? -INFINITY : (ml[r].x - kShift + log2f(l)) * kLn2;
   }
+  for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    Vec v;
+    float* y = reinterpret_cast<float*>(&v);
+#pragma unroll
+    for (int j = 0; j < V / N; ++j) y[j] = sum[i][j] * inv;
+    out[32 * i] = v;
+  }
+  if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (top - kShift + log2f(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int warps_of(int D) { return D == 256 ? Geo<256, 2>::WARPS : Geo<128, 1>::WARPS; }
 
 struct Shape {
   int groups, blocks, chunk;  // row groups of a unit, units of a kv head, sequences of a launch
@@ -806,15 +893,17 @@ int check(const da_params* p, int group, int q_len, Shape& s) {
   if (st != DA_OK) return st;
   if (q_len < 1) return DA_ERR_INVALID;
   const long long cap = (long long)p->max_blocks_per_seq * p->block_size;
-  const long long rows = (long long)q_len * (p->num_q_heads / p->num_kv_heads);
-  if (cap > 0x7fffffffLL - 1024 || rows > 0x7fffffffLL - 1024) return DA_ERR_UNSUPPORTED;
+  const long long all_rows = (long long)q_len * p->num_q_heads;
+  const long long rows = all_rows / p->num_kv_heads;
+  if (cap > 0x7fffffffLL - 1024 || all_rows > 0x7fffffffLL - 1024) return DA_ERR_UNSUPPORTED;
   const long long groups = (rows + kRows - 1) / kRows;
   s.groups = 1;
   while (s.groups < groups && s.groups < kMaxGroups) s.groups *= 2;
   const long long blocks = (groups + s.groups - 1) / s.groups;
-  // tiles of a launch count in 31 bits
-  const long long tiles = (cap / kTok + 2) * p->num_kv_heads * blocks;
-  const long long most = (0x7fffffffLL - 1024) / tiles;
+  // tiles and rows of a launch count in 31 bits
+  const long long tiles = (cap / (4096 / p->head_dim) + 2) * p->num_kv_heads * blocks;
+  long long most = (0x7fffffffLL - 4096) / tiles;
+  if (most > 0x7fffffffLL / all_rows) most = 0x7fffffffLL / all_rows;
   if (most < 1) return DA_ERR_UNSUPPORTED;
   s.blocks = (int)blocks;
   s.chunk = (int)(most < kMaxBatch ? most : kMaxBatch);
@@ -822,14 +911,15 @@ int check(const da_params* p, int group, int q_len, Shape& s) {
 }
 
 struct Layout {
-  size_t desc, ml, o, total;
+  size_t pre, ml, o, total;
 };
-Layout layout(int sms, int groups, int D) {
+Layout layout(int sms, int D) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   Layout w;
-  const size_t rows = (size_t)sms * 2 * groups * kRows;
-  w.desc = 0;
-  w.ml = up(sizeof(int4) * sms);
+  // a share has `groups` warps and as many groups of rows
+  const size_t rows = (size_t)sms * warps_of(D) * 2 * kRows;
+  w.pre = 0;
+  w.ml = up((kMaxBatch + 1) * sizeof(int));
   w.o = w.ml + up(rows * sizeof(float2));
   w.total = w.o + up(rows * D * sizeof(float));
   return w;
@@ -838,27 +928,18 @@ Layout layout(int sms, int groups, int D) {
 template <int D, int NG>
 cudaError_t launch(Q4Params& k, int grid, cudaStream_t s) {
   using g_ = Geo<D, NG>;
-  constexpr int kMost = 227 * 1024 - 2048;  // dynamic shared memory, Shared beside it
-  const int pre = k.split ? (k.B + 1) * 4 : 0;
-  int stages = (kMost - g_::UNION - pre) / g_::STAGE;
-  if (stages > 16) stages = 16;
-  k.stages = stages;
-  const int smem = stages * g_::STAGE + g_::UNION + pre;
+  static_assert(sizeof(Shared<g_::WARPS, g_::STAGES>) <= 2048, "more than a processor's shared memory");
   cudaError_t err = cudaFuncSetAttribute(q4_kernel<D, NG>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, g_::kMost);
   if (err != cudaSuccess) return err;
-  err = da::launch_early(q4_kernel<D, NG>, grid, kThreads, smem, s, k);
-  if (err != cudaSuccess || !k.split) return err;
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, k.groups * kRows / kMergeRows);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = s;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q4_merge_kernel<D>, k);
+  k.log2_eb = 0;
+  while ((2 << k.log2_eb) <= g_::TOK && k.log2_eb < k.log2_bs) ++k.log2_eb;
+  k.shares = grid * (g_::WARPS / k.groups);
+  err = da::launch_early(q4_kernel<D, NG>, grid, g_::THREADS, g_::SMEM + (k.B + 1) * 4, s, k);
+  if (err != cudaSuccess) return err;
+  const long long rows = (long long)k.B * k.T * k.Hq;
+  return da::launch_early(q4_merge_kernel<D>, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps),
+                          32 * kMergeWarps, 0, s, k);
 }
 
 cudaError_t launch(Q4Params& k, int D, int group, int grid, cudaStream_t s) {
@@ -888,7 +969,7 @@ size_t decode_attn_paged_q4_workspace_size(const da_params* p, int32_t q_len) {
   Shape s;
   int sms = 0;
   if (check(p, da::kQ4MinGroup, q_len, s) != DA_OK || da::device_sms(&sms) != DA_OK) return 0;
-  return layout(sms, s.groups, p->head_dim).total;
+  return layout(sms, p->head_dim).total;
 }
 
 int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const float* q,
@@ -913,9 +994,8 @@ int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const
   int sms = 0;
   st = da::device_sms(&sms);
   if (st != DA_OK) return st;
-  const Layout w = layout(sms, shape.groups, p->head_dim);
-  if (workspace && workspace_bytes < w.total) return DA_ERR_WORKSPACE;
-  if (sms > kMaxParts) return DA_ERR_UNSUPPORTED;
+  const Layout w = layout(sms, p->head_dim);
+  if (!workspace || workspace_bytes < w.total) return DA_ERR_WORKSPACE;
   Q4Params k = {};
   k.pool = pool;
   k.dev_status = dev_status;
@@ -925,8 +1005,6 @@ int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const
   k.Hq = p->num_q_heads;
   k.Hkv = p->num_kv_heads;
   while ((1 << k.log2_bs) < p->block_size) ++k.log2_bs;
-  const int eb = p->block_size < kTok ? p->block_size : kTok;
-  while ((1 << k.log2_eb) < eb) ++k.log2_eb;
   k.max_blocks = p->max_blocks_per_seq;
   k.num_blocks = p->num_blocks;
   k.window = p->sliding_window;
@@ -939,12 +1017,10 @@ int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const
   k.page_bytes = da::q4_page_bytes(p->block_size, p->head_dim, group);
   k.wait_ns = da::wait_limit();
   k.test_skip_arm = da::skip_first_arm();
-  if (workspace) {
-    char* ws = static_cast<char*>(workspace);
-    k.desc = reinterpret_cast<int4*>(ws + w.desc);
-    k.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-    k.part_o = reinterpret_cast<float*>(ws + w.o);
-  }
+  char* ws = static_cast<char*>(workspace);
+  k.pre = reinterpret_cast<int*>(ws + w.pre);
+  k.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  k.part_o = reinterpret_cast<float*>(ws + w.o);
   const long long row = (long long)q_len * p->num_q_heads;
   const std::lock_guard<std::mutex> unbroken(workspace_mutex(workspace));
   for (int b0 = 0; b0 < p->batch; b0 += shape.chunk) {
@@ -955,11 +1031,7 @@ int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const
     k.table = block_table + (long long)b0 * k.max_blocks;
     k.seq_lens = seq_lens + b0;
     k.q_pos = q_pos ? q_pos + b0 : nullptr;
-    k.units = k.B * k.Hkv * k.blocks;
-    // Short sequences run whole: a cut unit costs a second kernel.
-    k.split = workspace && !(p->max_seq_len > 0 && p->max_seq_len <= 512 && k.units <= 2 * sms);
-    const int grid = k.split || k.units > sms ? sms : k.units;
-    if (launch(k, p->head_dim, group, grid, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    if (launch(k, p->head_dim, group, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
       return DA_ERR_CUDA;
   }
   return DA_OK;

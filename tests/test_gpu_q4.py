@@ -317,6 +317,22 @@ def test_long_axes(D, L):
     Case(5, 2, 2, D, 32, 256, [L // 2, 3, L // 3]).check()
 
 
+@pytest.mark.parametrize("D,group,T,B", [(64, 64, 1, 300), (128, 32, 1, 300), (128, 128, 4, 300),
+                                         (256, 128, 1, 300), (256, 32, 3, 150), (256, 64, 17, 60)])
+def test_many_tiles_a_processor(D, group, T, B):
+    """Shares of many tiles and of several units: every buffer is used again and again, by
+    whoever comes first.  The sequences' tables name a few pages over and over."""
+    c = Case(15, 4, 2, D, group, 32, [2048], T=T)
+    r = c.r
+    c.lens = r.integers(1500, 2049, B).astype(np.int32)
+    c.table = r.integers(0, c.cache.NB, (B, 64)).astype(np.int32)
+    c.q = r.standard_normal((B,) + c.q.shape[1:]).astype(np.float32)
+    got = c.run()
+    c.check(got)
+    again = c.run()
+    assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1])
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("window", [1, 15, 100, 4000])
 @pytest.mark.parametrize("T", [1, 3])
@@ -485,8 +501,8 @@ def test_errors_are_those_of_f32(D, group, T, L):
 
 
 def test_workspaces_and_repeats():
-    """Bit for bit the same twice, with a workspace of any content; without one; too small
-    ones are refused; rows behind the last sequence are left alone."""
+    """Bit for bit the same twice, with a workspace of any content; too small ones are
+    refused; rows behind the last sequence are left alone."""
     import torch
     c = Case(20, 8, 2, 128, 64, 16, [9000, 40, 0, 3000, 700])
     args = c.args()
@@ -501,8 +517,7 @@ def test_workspaces_and_repeats():
         qk.decode_attn_paged_q4(*args, group=64, workspace=ws, out=out[:5], lse=lse[:5])
         assert torch.equal(out[:5], a[0]) and torch.equal(lse[:5], a[1])
         assert bool((out[5:] == 7).all()) and bool((lse[5:] == 7).all())
-    b = qk.decode_attn_paged_q4(*args, group=64, workspace=None)
-    c.check((b[0].cpu().numpy(), b[1].cpu().numpy(), 0))
+    c.check((a[0].cpu().numpy(), a[1].cpu().numpy(), 0))
     with pytest.raises(qk.DecodeAttnError) as e:
         qk.decode_attn_paged_q4(*args, group=64, workspace=ws[:n - 1])
     assert e.value.status == qk.DA_ERR_WORKSPACE

@@ -104,6 +104,7 @@ def test_attention_rejects_bad_params(lib, kw, status):
     ptrs = [FAKE] * 4 + [None, ctypes.c_void_p(0x10000 + 16), None]
     assert call(good, ptrs=ptrs) == qk.DA_ERR_INVALID
     assert call(_params(batch=0)) == qk.DA_OK
+    assert call(good) in (qk.DA_ERR_WORKSPACE, qk.DA_ERR_CUDA)  # none given (or no device to ask)
 
 
 def test_append_and_gather_reject_bad_arguments(lib):
@@ -202,7 +203,7 @@ def test_binding_refuses_before_the_device(lib):
                      (dict(block_table=torch.zeros(3, 4, dtype=i32)), ValueError),
                      (dict(q_pos=torch.zeros(3, dtype=i32)), ValueError),
                      (dict(out=torch.zeros(2, 8, 128)), ValueError), (dict(lse=torch.zeros(2, 4)), ValueError),
-                     (dict(workspace=3), ValueError), ({}, ValueError)):
+                     (dict(workspace=3), ValueError), (dict(workspace=None), ValueError), ({}, ValueError)):
         with pytest.raises(exc):
             _cpu_attend(**bad)
     for name in ("pool", "block_table", "seq_lens", "q_pos", "out", "lse", "dev_status"):
