@@ -68,8 +68,7 @@ struct Q4Params {
   int shares;          // of the launch
   float qscale, softcap2, softcap_inv;
   long long page_bytes;
-  unsigned long long wait_ns;
-  int test_skip_arm;
+  uint32_t stride;     // bytes from a page to the next: below 2^32
   // workspace
   int* pre;         // [B + 1] tiles of the sequences before each
   float2* part_ml;  // [shares][2][groups * 8]: reference and sum
@@ -186,14 +185,9 @@ __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Untiled bulk copy to a shared-memory address (16-byte aligned both, size % 16 == 0).
-__device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(to),
-      "l"(from), "r"(bytes), "r"(da::smem_u32(bar))
-      : "memory");
+// 16 bytes to shared memory, past L1, with the next ones' line to L2.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 
 // NG params of a row side by side in shared memory.
@@ -222,13 +216,13 @@ struct Geo {
   static constexpr int TOK = 4096 / D;     // keys of a tile
   static constexpr int LOG2_TOK = D == 64 ? 6 : D == 128 ? 5 : 4;
   static constexpr int H = D == 256 ? 1 : 2;  // MMA tiles of 16 keys that are worked off together
-  static constexpr int STAGE = TOK * ROW;
+  static constexpr int STAGE = TOK * ROW;  // codes of keys, of values, params of keys, of values
+  static constexpr int CODES = TOK * RB;
   // D = 256 has twice the accumulators, and states of twice the size
   static constexpr int WARPS = D == 256 ? 8 : 12;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr bool QREG = D <= 128;   // Q's fragments in registers, else in shared memory
-  static constexpr int COL = D + 4;        // floats between rows of a state in shared memory
-  static constexpr int STATE = kRows * COL * 4;
+  static constexpr int STATE = kRows * D * 4;  // sums of a warp in shared memory
   static constexpr int QBYTES = QREG ? 0 : P * 2 * 512;
   static constexpr int kMost = 227 * 1024 - 2048;  // dynamic shared memory, Shared beside it
   static constexpr int FIT = (kMost - (kMaxBatch + 1) * 4) / WARPS - STATE - QBYTES;
@@ -239,7 +233,6 @@ struct Geo {
 
 template <int WARPS, int STAGES>
 struct Shared {
-  uint64_t full[WARPS][STAGES];
   uint32_t bad[WARPS][STAGES];  // pages of a tile that are outside the pool
   int warp_sum[WARPS];
 };
@@ -259,11 +252,8 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
       dyn + g_::WARPS * (STAGES * g_::STAGE + g_::STATE) + warp * g_::QBYTES);
   int* pre = reinterpret_cast<int*>(dyn + g_::SMEM);
   const int eb = 1 << p.log2_eb, bs = 1 << p.log2_bs;
-  const int rec = eb * g_::ROW;  // bytes of a page's piece in a tile
   const int upb = p.Hkv * p.blocks;  // units of a sequence
 
-  if (lane < STAGES) da::mbar_init(&sh.full[warp][lane], 1);
-  da::fence_mbarrier_init();
   da::wait_for_grid_before();
   da::let_next_grid_start();
 
@@ -325,6 +315,7 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
     int b, kv, block;
     int i0, n;  // its first tile, of the sequence's; tiles
     int slot;   // -1: the whole unit; else the place of its state among the share's
+    const uint8_t* base;  // this lane's 16 bytes of page 0 of the kv head
   };
   auto next_part = [&](Part& a) {
     if (tile >= tile_end) return false;
@@ -336,6 +327,7 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
     a.i0 = rel - unit * nt;
     a.n = min(nt - a.i0, tile_end - tile);
     a.slot = a.n == nt ? -1 : segs ? 1 : 0;
+    a.base = p.pool + a.kv * p.page_bytes + 16 * lane;
     seq_info<TOK>(p, seq, a.s);
     tile += a.n;
     ++segs;
@@ -344,63 +336,69 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
 
   // ------------------------------------------------ copies
   // Block ids are loaded 32 at a time, lane by lane: piece lane % pieces of tile lane / pieces of a batch of
-  // tiles, a batch ahead of the copies; addresses and masks are worked out once a batch.
+  // tiles, a batch ahead of the copies.
   const int log2_pieces = g_::LOG2_TOK - p.log2_eb;
-  const int batch = 32 >> log2_pieces, my_piece = lane & ((1 << log2_pieces) - 1);
-  const int my_tile = lane >> log2_pieces;
-  const uint32_t those = (2u << ((1 << log2_pieces) - 1)) - 1;  // pieces of a tile
-  int id_next = -1;  // of this lane's piece in the next batch; -1: not read, -2: outside the pool
-  const uint8_t* from = nullptr;      // of this lane's piece in this batch, nullptr: not copied
-  uint32_t pages = 0, bad_pages = 0;  // of this batch: lanes with one to copy, with one outside the pool
+  const int batch = 32 >> log2_pieces, my_tile = lane >> log2_pieces;
+  const int my_piece = lane & ((1 << log2_pieces) - 1);
+  int id = -1, id_next = -1;  // of this lane's piece in this batch and the next; -1: not read, -2: outside
+  uint32_t bad_pages = 0;     // of this batch: lanes with a piece outside the pool
   auto block_id = [&](const Part& a, int n) {
     const int k = (a.s.tile0 + a.i0 + n) * TOK + (my_piece << p.log2_eb);
     if (n >= a.n || k >= a.s.hi || k + eb <= a.s.lo) return -1;
     const int x = p.table[(long long)a.b * p.max_blocks + (k >> p.log2_bs)];
     return x >= 0 && x < p.num_blocks ? x : -2;
   };
-  auto take_batch = [&](const Part& a, int n) {  // from tile n of the part on
-    const int id = id_next;
-    id_next = block_id(a, n + batch + my_tile);
-    bad_pages = __ballot_sync(0xffffffffu, id == -2);
-    pages = __ballot_sync(0xffffffffu, id >= 0);
-    if (bad_pages && lane == 0 && p.dev_status) atomicOr(p.dev_status, DA_DEV_BAD_BLOCK);
-    from = p.pool + ((long long)max(id, 0) * p.Hkv + a.kv) * p.page_bytes;
-    if (bs > TOK)  // tiles are parts of a page, and every one starts at a multiple of TOK in it
-      from += (((a.s.tile0 + a.i0 + n + my_tile) * TOK) & (bs - 1)) * RB;
-    if (id < 0) from = nullptr;
-  };
   int put = 0, got = 0;  // stage of the next copy, of the next tile to work off
-  uint32_t parity = 0;   // of the phase of `got`
-  bool skip = p.test_skip_arm && blockIdx.x == 0 && warp == 0;
-  // stages that are being copied; the phase of each one's last copy, of the next round's
-  uint32_t flying = 0, phases = 0, put_phase = 0;
-  auto copy = [&](const Part& a, int n) {  // tile n of the part
-    const int j = n & (batch - 1);
-    if (j == 0) take_batch(a, n);
-    const uint32_t copied = pages >> (j << log2_pieces) & those;
-    uint64_t* bar = &sh.full[warp][put];
-    if (!skip) {
-      if (lane == 0) {
-        sh.bad[warp][put] = bad_pages >> (j << log2_pieces) & those;
-        da::mbar_arrive_expect_tx(bar, __popc(copied) * rec);
+  // Tile n of the part, and a group of copies to wait for in any case.  (Bulk copies with barriers, which lanes
+  // issue for themselves one by one, took 1100 cycles a tile of a warp's time.)
+  auto copy = [&](const Part& a, int n) {
+    if (n < a.n) {
+      const int j = n & (batch - 1);
+      if (j == 0) {
+        id = id_next;
+        id_next = block_id(a, n + batch + my_tile);
+        bad_pages = __ballot_sync(0xffffffffu, id == -2);
+        if (bad_pages && lane == 0 && p.dev_status) atomicOr(p.dev_status, DA_DEV_BAD_BLOCK);
       }
-      __syncwarp();
-      const uint32_t to = ring + put * g_::STAGE;
-      if (bs <= TOK) {
-        if (my_tile == j && from) bulk_copy(to + my_piece * rec, from, rec, bar);
-      } else if (copied && lane == j) {  // codes and params of its rows
-        const int r = ((a.s.tile0 + a.i0 + n) * TOK) & (bs - 1);
-        bulk_copy(to, from, TOK * RB, bar);
-        bulk_copy(to + TOK * RB, from + bs * RB, TOK * RB, bar);
-        const uint8_t* par = from - r * RB + bs * D + r * 4 * NG;
-        bulk_copy(to + TOK * D, par, TOK * 4 * NG, bar);
-        bulk_copy(to + TOK * (D + 4 * NG), par + bs * 4 * NG, TOK * 4 * NG, bar);
-      }
-      flying |= 1u << put;
-      phases = (phases & ~(1u << put)) | put_phase << put;
+      const uint32_t those = (2u << ((1 << log2_pieces) - 1)) - 1;  // pieces of a tile
+      if (lane == 0) sh.bad[warp][put] = bad_pages >> (j << log2_pieces) & those;
+      const uint32_t to = ring + put * g_::STAGE + 16 * lane;
+      auto pieces = [&](auto rows) {  // of `rows` keys each
+        constexpr int EB = decltype(rows)::value, PAR = EB * 4 * NG;  // keys' params, values' params
+#pragma unroll
+        for (int i = 0; i < TOK / EB; ++i) {
+          const int x = __shfl_sync(0xffffffffu, id, j * (TOK / EB) + i);
+          if (x < 0) continue;
+          const uint8_t* k = a.base + (unsigned long long)(uint32_t)x * p.stride;
+          if (EB == TOK && bs > TOK)  // a part of a page: from this row on
+            k += (((a.s.tile0 + a.i0 + n) * TOK) & (bs - 1)) * RB;
+          const uint8_t* v = k + bs * RB;
+          const uint32_t dst = to + i * EB * RB;
+#pragma unroll
+          for (int at = 0; at < EB * RB; at += 512)
+            if (EB * RB >= 512 || 16 * lane < EB * RB) {
+              copy16(dst + at, k + at);
+              copy16(dst + g_::CODES + at, v + at);
+            }
+          const uint8_t* par = k + bs * D - 16 * lane;  // of the piece's keys
+          if (EB == TOK && bs > TOK) par -= (((a.s.tile0 + a.i0 + n) * TOK) & (bs - 1)) * (RB - 4 * NG);
+          const uint32_t pdst = to - 16 * lane + 2 * g_::CODES + i * PAR;
+          if constexpr (PAR <= 256) {  // both in one go
+            const int v2 = lane / (PAR / 16), off = lane % (PAR / 16) * 16;
+            if (lane < PAR / 8) copy16(pdst + v2 * TOK * 4 * NG + off, par + v2 * bs * 4 * NG + off);
+          } else if (16 * lane < PAR) {
+            copy16(pdst + 16 * lane, par + 16 * lane);
+            copy16(pdst + TOK * 4 * NG + 16 * lane, par + bs * 4 * NG + 16 * lane);
+          }
+        }
+      };
+      if (eb == TOK) pieces(std::integral_constant<int, TOK>());
+      else if (eb == 8) pieces(std::integral_constant<int, 8>());
+      else if (eb == 16) pieces(std::integral_constant<int, 16>());
+      else if constexpr (TOK == 64) pieces(std::integral_constant<int, 32>());
     }
-    skip = false;
-    if (++put == STAGES) put = 0, put_phase ^= 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++put == STAGES) put = 0;
   };
 
   const int g = lane >> 2, c = lane & 3;
@@ -408,29 +406,23 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
   // 16 x 16 bytes is key pi(j), which makes its bytes 4c .. 4c + 3 the keys of the MMA's k = 2c, 2c + 8,
   // 2c + 1, 2c + 9.
   const int key_a = g, key_b = 8 + (g ^ 4);
-  auto row_at = [&](int t) { return t * RB + (eb == 8 && t >= 8 ? rec - 8 * RB : 0); };
-  auto par_at = [&](int t) { return t * 4 * NG + (eb == 8 && t >= 8 ? rec - 8 * 4 * NG : 0); };
   uint32_t k_lane, v_lane;  // byte offsets of this lane's rows from the 16 keys' first
   {
     const int j = lane & 7, t = lane & 8 ? 8 + (j ^ 4) : j;
-    k_lane = row_at(t) + (((lane >> 4) ^ da::piece_xor<D>(t)) << 4);
+    k_lane = t * RB + (((lane >> 4) ^ da::piece_xor<D>(t)) << 4);
     const int i = lane & 15, cc = i >> 2, w = i & 3;
     const int row = 2 * cc + (w >> 1);  // of tau's first half, or (odd w) of its second
     const int u = w & 1 ? 8 + (row ^ 4) : row;
-    v_lane = row_at(u) + (((lane >> 4) ^ da::piece_xor<D>(u)) << 4);
+    v_lane = g_::CODES + u * RB + (((lane >> 4) ^ da::piece_xor<D>(u)) << 4);
   }
-  const int par_a = par_at(key_a), par_b = par_at(key_b);
-  auto state_at = [&](int i, int j) {  // piece i, rows 2g (+ 16) of it and their neighbours
-    return reinterpret_cast<float2*>(state + (2 * c + (j & 1)) * g_::COL + 32 * i + 2 * g +
-                                     (j & 2 ? 16 : 0));
-  };
+  // a lane's sums, accumulator i
+  auto state_at = [&](int i) { return reinterpret_cast<float4*>(state) + 32 * i + lane; };
 
-  bool abort = false;  // a wait ran out: no more waits and copies, the loops go on over what memory holds
   Part a;
   while (next_part(a)) {
     id_next = block_id(a, my_tile);
-    if (!abort)
-      for (int n = 0; n < STAGES && n < a.n; ++n) copy(a, n);
+#pragma unroll 1
+    for (int n = 0; n < STAGES; ++n) copy(a, n);
     const int row0 = (a.block * p.groups + rg) * kRows;  // first query row of the warp
     // ------------------------------------------------ Q: row g, dims 32 p + 8 c ..
     uint32_t qf[g_::QREG ? P * 2 : 1][4];  // hi of k = 2c.. and 2c + 8.., lo of the same
@@ -516,11 +508,8 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
     bool kept = false;
     int chain = 0;
     for (int n = 0; n < a.n; ++n) {
-      if (!abort) {
-        if (da::mbar_wait(&sh.full[warp][got], parity, nullptr, p.wait_ns)) flying &= ~(1u << got);
-        else abort = true;
-        abort = __any_sync(0xffffffffu, abort);
-      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+      __syncwarp();
       const uint32_t bad = sh.bad[warp][got];
       const uint32_t base = ring + got * g_::STAGE;
       const int first = (a.s.tile0 + a.i0 + n) * TOK;
@@ -530,25 +519,19 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
         if (key0 >= a.s.hi || key0 + 16 * H <= a.s.lo) continue;
         auto work = [&](auto masked) {
           constexpr bool PART = decltype(masked)::value;
-          uint32_t at[H], par[H];  // first row and first param of the page's piece
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            const int t = tok + 16 * h, r0 = t & (eb - 1);
-            const uint32_t page = base + (t >> p.log2_eb) * rec;
-            at[h] = page + r0 * RB;
-            par[h] = page + eb * D + r0 * 4 * NG;
-          }
+          const uint32_t at = base + tok * RB;  // the first of the keys
+          const uint32_t par = base + 2 * g_::CODES + tok * 4 * NG;
           uint32_t kw[H][P][2], kp[H][2][NG], vp[H][2][NG];
 #pragma unroll
           for (int h = 0; h < H; ++h) {
 #pragma unroll
             for (int i2 = 0; i2 < P / 2; ++i2)
-              da::ldsm_x4((at[h] + k_lane) ^ (i2 << 5), kw[h][2 * i2][0], kw[h][2 * i2][1],
+              da::ldsm_x4((at + h * 16 * RB + k_lane) ^ (i2 << 5), kw[h][2 * i2][0], kw[h][2 * i2][1],
                           kw[h][2 * i2 + 1][0], kw[h][2 * i2 + 1][1]);
-            load_params<NG>(par[h] + par_a, kp[h][0]);
-            load_params<NG>(par[h] + par_b, kp[h][1]);
-            load_params<NG>(par[h] + eb * 4 * NG + par_a, vp[h][0]);
-            load_params<NG>(par[h] + eb * 4 * NG + par_b, vp[h][1]);
+            load_params<NG>(par + (16 * h + key_a) * 4 * NG, kp[h][0]);
+            load_params<NG>(par + (16 * h + key_b) * 4 * NG, kp[h][1]);
+            load_params<NG>(par + (TOK + 16 * h + key_a) * 4 * NG, vp[h][0]);
+            load_params<NG>(par + (TOK + 16 * h + key_b) * 4 * NG, vp[h][1]);
           }
           // -------------------------------------------- scores
           float2 x[H][2];  // of keys a and b; columns 2c, 2c + 1
@@ -612,7 +595,7 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
           for (int h = 0; h < H; ++h)
 #pragma unroll
             for (int i2 = 0; i2 < P / 2; ++i2)
-              da::ldsm_b8_x2_trans((at[h] + eb * RB + v_lane) ^ (i2 << 5), vw[h][2 * i2][0],
+              da::ldsm_b8_x2_trans((at + h * 16 * RB + v_lane) ^ (i2 << 5), vw[h][2 * i2][0],
                                    vw[h][2 * i2][1], vw[h][2 * i2 + 1][0], vw[h][2 * i2 + 1][1]);
           if (p.softcap2 > 0.f) {
 #pragma unroll
@@ -736,19 +719,20 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
         else work(std::false_type());
       }
       __syncwarp();  // the stage is read
-      if (++got == STAGES) got = 0, parity ^= 1;
-      if (n + STAGES < a.n && !abort) copy(a, n + STAGES);
+      if (++got == STAGES) got = 0;
+      copy(a, n + STAGES);
       if (++chain == kChainKeys / TOK && n + 1 < a.n) {
-        const float2 d0 = make_float2(due.x, due.x), d1 = make_float2(due.y, due.y);
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float2 v = make_float2(acc[2 * i][j], acc[2 * i + 1][j]);
-            if (kept) v = da::fma2(*state_at(i, j), j & 1 ? d1 : d0, v);
-            *state_at(i, j) = v;
-            acc[2 * i][j] = acc[2 * i + 1][j] = 0.f;
+        for (int i = 0; i < MT; ++i) {
+          float4 v = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+          if (kept) {
+            const float4 y = *state_at(i);
+            v = make_float4(fmaf(y.x, due.x, v.x), fmaf(y.y, due.y, v.y), fmaf(y.z, due.x, v.z),
+                            fmaf(y.w, due.y, v.w));
           }
+          *state_at(i) = v;
+          acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        }
         due = make_float2(1.f, 1.f);
         kept = true;
         chain = 0;
@@ -785,25 +769,26 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
     }
     const float2 by = a.slot < 0 ? make_float2(l.x == 0.f ? 0.f : 1.f / l.x, l.y == 0.f ? 0.f : 1.f / l.y)
                                  : make_float2(1.f, 1.f);
+    if (kept) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const float4 y = *state_at(i);
+        acc[i][0] = fmaf(y.x, due.x, acc[i][0]), acc[i][1] = fmaf(y.y, due.y, acc[i][1]);
+        acc[i][2] = fmaf(y.z, due.x, acc[i][2]), acc[i][3] = fmaf(y.w, due.y, acc[i][3]);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float2 v = make_float2(acc[2 * i][j], acc[2 * i + 1][j]);
-        const float d = j & 1 ? due.y : due.x, f = j & 1 ? by.y : by.x;
-        if (kept) v = da::fma2(*state_at(i, j), make_float2(d, d), v);
+        const float f = j & 1 ? by.y : by.x;
         const float z = j & 1 ? zero_sum[i / GP].y : zero_sum[i / GP].x;
         v = da::fma2(v, make_float2(0x1p9f, 0x1p9f), make_float2(z, z));
         if (to[j & 1])
           *reinterpret_cast<float2*>(to[j & 1] + 32 * i + 2 * g + (j & 2 ? 16 : 0)) =
               make_float2(v.x * f, v.y * f);
       }
-  }
-  // What is being copied has to land before its memory is given back: only after an abort is there any.
-  if (abort && lane == 0) {
-    if (p.dev_status) atomicOr(p.dev_status, DA_DEV_TIMEOUT);
-    for (int i = 0; i < STAGES; ++i)
-      if (flying >> i & 1) da::mbar_wait(&sh.full[warp][i], phases >> i & 1, nullptr, p.wait_ns);
   }
 }
 
@@ -896,6 +881,8 @@ int check(const da_params* p, int group, int q_len, Shape& s) {
   const long long all_rows = (long long)q_len * p->num_q_heads;
   const long long rows = all_rows / p->num_kv_heads;
   if (cap > 0x7fffffffLL - 1024 || all_rows > 0x7fffffffLL - 1024) return DA_ERR_UNSUPPORTED;
+  if (da::q4_page_bytes(p->block_size, p->head_dim, group) * p->num_kv_heads > 0xffffffffLL)
+    return DA_ERR_UNSUPPORTED;
   const long long groups = (rows + kRows - 1) / kRows;
   s.groups = 1;
   while (s.groups < groups && s.groups < kMaxGroups) s.groups *= 2;
@@ -1015,8 +1002,7 @@ int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const
   k.softcap2 = p->softcap > 0.f ? p->softcap * 1.4426950408889634f : 0.f;
   k.softcap_inv = k.softcap2 > 0.f ? (float)(1.0 / (double)k.softcap2) : 0.f;
   k.page_bytes = da::q4_page_bytes(p->block_size, p->head_dim, group);
-  k.wait_ns = da::wait_limit();
-  k.test_skip_arm = da::skip_first_arm();
+  k.stride = (uint32_t)(k.page_bytes * p->num_kv_heads);
   char* ws = static_cast<char*>(workspace);
   k.pre = reinterpret_cast<int*>(ws + w.pre);
   k.part_ml = reinterpret_cast<float2*>(ws + w.ml);
