@@ -777,7 +777,7 @@ class _NoCall:
     def norm_rope(*args):
         return NotImplemented
 
-    append = prefix = norm_rope
+    append = prefix = append_q4 = gather_q4 = attend_q4 = plan = norm_rope
 
 
 def _load_call():
@@ -797,6 +797,10 @@ def _load_call():
                 module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                     lib.decode_attn_qk_norm_rope, lib.decode_attn_append_paged_rope,
                     lib.decode_attn_paged_prefix, lib.decode_attn_paged_prefix_workspace_size)))
+                module.bind_q4(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                    lib.decode_attn_append_paged_q4, lib.decode_attn_gather_paged_q4,
+                    lib.decode_attn_paged_q4, lib.decode_attn_paged_q4_workspace_size,
+                    lib.decode_attn_plan_blocks)))
             except ImportError as e:
                 warnings.warn("the norm, append and shared-prefix calls go through Python, slower: "
                               f"no {path} (quantized_kv_decode_paged_gb300.build() makes it): {e}",
@@ -1198,6 +1202,13 @@ def decode_attn_plan_blocks(old_lens, new_lens, block_table, free_list, free_cou
     length, page or count is out of range, nothing is changed, every token is
     padding, cu_tokens is zero and dev_status says why (DEV_NO_BLOCKS,
     DEV_TOKEN_OVERFLOW, DEV_BAD_SEQ_LEN, DEV_BAD_BLOCK, DEV_BAD_FREE_LIST)."""
+    if stream is None and positions is token_seq is slots is cu_tokens is None:
+        y = (_call or _load_call()).plan(old_lens, new_lens, block_table, free_list, free_count,
+                                         block_size, num_blocks, max_tokens, dev_status)
+        if type(y) is tuple:
+            return y
+        if y is not NotImplemented:
+            _check("decode_attn_plan_blocks", y)
     torch = _torch()
     lib = _lib or load_library()
     if not isinstance(old_lens, torch.Tensor):
@@ -1275,6 +1286,14 @@ def decode_attn_append_paged_q4(k_new, v_new, positions, block_table, pool, freq
     The keys, normed (with ``norm``) and rotated (with freqs) on the way, and the
     values are quantised in groups of ``group`` neighbours: zero = f16(min), scale =
     f16((max - min) / 15), codes 0..15.  Returns q_out f32 [N, Hq, D], or None without q."""
+    if stream is None:
+        y = (_call or _load_call()).append_q4(k_new, v_new, positions, block_table, pool, freqs,
+                                              group, token_seq, q, norm, q_weight, k_weight,
+                                              weight_offset, eps, interleaved, q_out, dev_status)
+        if type(y) is int:
+            _check("decode_attn_append_paged_q4", y)
+        if y is not NotImplemented:
+            return y
     torch = _torch()
     lib = _lib or load_library()
     kind = _rope_kind(torch, k_new)
@@ -1336,6 +1355,13 @@ def decode_attn_gather_paged_q4(positions, block_table, pool, *, head_dim, group
     each, of dtype float16 (the default), bfloat16 or float32.  positions i32 [N],
     token_seq i32 [N] and block_table as for decode_attn_append_paged_q4; rows of
     padding tokens (token_seq < 0) and of those that dev_status flags are zero."""
+    if stream is None and dtype is k_out is v_out is None:
+        y = (_call or _load_call()).gather_q4(positions, block_table, pool, head_dim, group,
+                                              token_seq, dev_status)
+        if type(y) is tuple:
+            return y
+        if y is not NotImplemented:
+            _check("decode_attn_gather_paged_q4", y)
     torch = _torch()
     lib = _lib or load_library()
     if not isinstance(pool, torch.Tensor):
@@ -1397,6 +1423,14 @@ def decode_attn_paged_q4(q, pool, block_table, seq_lens, q_pos=None, *, group, s
     ``workspace``: "auto" (the call's own, from torch's allocator on the call's
     stream; a captured call's in its graph's memory) or a caller-owned uint8
     tensor of decode_attn_paged_q4_workspace_size bytes (any content)."""
+    if stream is None and isinstance(workspace, str) and workspace == "auto":
+        y = (_call or _load_call()).attend_q4(q, pool, block_table, seq_lens, q_pos, group, scale,
+                                              softcap, sliding_window, causal, max_seq_len, out,
+                                              lse, dev_status)
+        if type(y) is tuple:
+            return y
+        if y is not NotImplemented:
+            _check("decode_attn_paged_q4", y)
     torch = _torch()
     lib = _lib or load_library()
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):

@@ -1,5 +1,5 @@
-// call.cpp — the Python module decode_attn_call: the common case of the norm, append and
-// shared-prefix calls from torch tensors to the C entry points.
+// call.cpp — the Python module decode_attn_call: the common case of the norm, append,
+// shared-prefix, 4-bit cache and block plan calls from torch tensors to the C entry points.
 //
 // A decode step's calls take a few us on the GPU, and their marshalling in Python (attribute reads,
 // a ctypes structure, two torch.empty) takes longer on the host of a GB300.  us a call in a loop,
@@ -30,6 +30,11 @@ decltype(&decode_attn_qk_norm_rope) norm_rope_fn;
 decltype(&decode_attn_append_paged_rope) append_fn;
 decltype(&decode_attn_paged_prefix) prefix_fn;
 decltype(&decode_attn_paged_prefix_workspace_size) prefix_ws_fn;
+decltype(&decode_attn_append_paged_q4) append_q4_fn;
+decltype(&decode_attn_gather_paged_q4) gather_q4_fn;
+decltype(&decode_attn_paged_q4) attend_q4_fn;
+decltype(&decode_attn_paged_q4_workspace_size) attend_q4_ws_fn;
+decltype(&decode_attn_plan_blocks) plan_fn;
 
 struct NotTaken {};  // thrown where the call is not the common case
 
@@ -282,9 +287,159 @@ PyObject* prefix(PyObject* const* a) {
   return pair(out.object(), lse.object());
 }
 
+// Geometry of a pool in 4 bits: uint8 [pages, Hkv, bytes].
+uint8_t* q4_pool(const at::Tensor& pool, int64_t d, int64_t group, int dev, da_params& p) {
+  auto* at = static_cast<uint8_t*>(plain(pool, at::kByte, dev, 3));
+  need((group == 32 || group == 64 || group == 128) && group <= d && d % group == 0);
+  const int64_t row = d + 8 * (d / group), bytes = pool.size(2);
+  need(bytes > 0 && bytes % row == 0);
+  p.num_blocks = i32(pool.size(0));
+  p.num_kv_heads = i32(pool.size(1));
+  p.head_dim = i32(d);
+  p.block_size = i32(bytes / row);
+  p.causal = 1;
+  return at;
+}
+
+// k_new, v_new, positions, block_table, pool, freqs, group, token_seq, q, norm, q_weight, k_weight,
+// weight_offset, eps, interleaved, q_out, dev_status
+PyObject* append_q4(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0]);
+  const int dev = device(x);
+  const at::ScalarType type = x.scalar_type();
+  const bool has_q = a[8] != Py_None;
+  const Rows k(x, type, dev), v(tensor(a[1]), type, dev);
+  const Rows q = has_q ? Rows(tensor(a[8]), type, dev) : Rows();
+  need(v.n == k.n && v.h == k.h && v.d == k.d);
+  need(has_q ? q.n == k.n && q.d == k.d : a[15] == Py_None);
+  const at::Tensor &pos = tensor(a[2]), &table = tensor(a[3]);
+  const auto* pos_p = static_cast<const int32_t*>(plain(pos, at::kInt, dev, 1));
+  const auto* table_p = static_cast<const int32_t*>(plain(table, at::kInt, dev, 2));
+  const int64_t group = integer(a[6]);
+  da_params p = {};
+  uint8_t* pool = q4_pool(tensor(a[4]), k.d, group, dev, p);
+  need(p.num_kv_heads == k.h && pos.size(0) == k.n);
+  const auto* seq = static_cast<const int32_t*>(plain_or_null(a[7], at::kInt, dev, 1));
+  need(!seq || tensor(a[7]).size(0) == k.n);
+  auto* status = static_cast<int32_t*>(plain_or_null(a[16], at::kInt, dev, -1));
+  const da_rope_params r =
+      rope_params(type, k.d, dev, a[5], a[9], a[10], a[11], a[12], a[13], a[14], q, k, v);
+  p.batch = i32(table.size(0));
+  p.num_q_heads = i32(has_q ? q.h : k.h);
+  p.max_blocks_per_seq = i32(table.size(1));
+  Output qo;
+  if (has_q) qo = Output(a[15], {q.n, q.h, q.d}, at::kFloat, dev);
+  const int st = append_q4_fn(&p, &r, i32(group), i32(k.n), q.p, k.p, v.p, pos_p, seq, table_p,
+                              static_cast<float*>(qo.p), pool, status, stream_of(dev));
+  if (st != DA_OK) return PyLong_FromLong(st);
+  return qo.object();
+}
+
+// positions, block_table, pool, head_dim, group, token_seq, dev_status: f16 rows of its own
+PyObject* gather_q4(PyObject* const* a) {
+  const at::Tensor& pool_t = tensor(a[2]);
+  const int dev = device(pool_t);
+  const at::Tensor &pos = tensor(a[0]), &table = tensor(a[1]);
+  const auto* pos_p = static_cast<const int32_t*>(plain(pos, at::kInt, dev, 1));
+  const auto* table_p = static_cast<const int32_t*>(plain(table, at::kInt, dev, 2));
+  const int64_t d = integer(a[3]), group = integer(a[4]), n = pos.size(0);
+  need(d > 0 && n > 0);
+  da_params p = {};
+  const uint8_t* pool = q4_pool(pool_t, d, group, dev, p);
+  const auto* seq = static_cast<const int32_t*>(plain_or_null(a[5], at::kInt, dev, 1));
+  need(!seq || tensor(a[5]).size(0) == n);
+  auto* status = static_cast<int32_t*>(plain_or_null(a[6], at::kInt, dev, -1));
+  p.batch = i32(table.size(0));
+  p.num_q_heads = p.num_kv_heads;
+  p.max_blocks_per_seq = i32(table.size(1));
+  Output k(Py_None, {n, p.num_kv_heads, d}, at::kHalf, dev);
+  Output v(Py_None, {n, p.num_kv_heads, d}, at::kHalf, dev);
+  const int st = gather_q4_fn(&p, i32(group), i32(n), DA_TYPE_F16, pos_p, seq, table_p, pool, k.p,
+                              v.p, status, stream_of(dev));
+  if (st != DA_OK) return PyLong_FromLong(st);
+  return pair(k.object(), v.object());
+}
+
+// q, pool, block_table, seq_lens, q_pos, group, scale, softcap, sliding_window, causal, max_seq_len,
+// out, lse, dev_status
+PyObject* attend_q4(PyObject* const* a) {
+  const at::Tensor& q = tensor(a[0]);
+  const int dev = device(q);
+  // captured calls go through Python
+  need(c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None);
+  need(q.dim() == 3 || q.dim() == 4);
+  const at::Tensor &table = tensor(a[2]), &lens = tensor(a[3]);
+  const int64_t B = q.size(0), T = q.dim() == 4 ? q.size(1) : 1, Hq = q.size(-2), D = q.size(-1);
+  const auto* qp = static_cast<const float*>(plain(q, at::kFloat, dev, (int)q.dim()));
+  const auto* tp = static_cast<const int32_t*>(plain(table, at::kInt, dev, 2));
+  const auto* lp = static_cast<const int32_t*>(plain(lens, at::kInt, dev, 1));
+  const int64_t group = integer(a[5]);
+  da_params p = {};
+  need(D > 0);
+  const uint8_t* pool = q4_pool(tensor(a[1]), D, group, dev, p);
+  need(B > 0 && table.size(0) == B && lens.size(0) == B);
+  const auto* pos = static_cast<const int32_t*>(plain_or_null(a[4], at::kInt, dev, 1));
+  need(!pos || tensor(a[4]).size(0) == B);
+  auto* status = static_cast<int32_t*>(plain_or_null(a[13], at::kInt, dev, -1));
+  p.batch = i32(B);
+  p.num_q_heads = i32(Hq);
+  p.max_blocks_per_seq = i32(table.size(1));
+  p.max_seq_len = i32(integer(a[10]));
+  p.scale = real(a[6]);
+  p.softcap = real(a[7]);
+  p.sliding_window = i32(integer(a[8]));
+  p.causal = truth(a[9]);
+  const size_t bytes = attend_q4_ws_fn(&p, i32(T));
+  need(bytes > 0);
+  Output out(a[11], q.sizes(), at::kFloat, dev);
+  Output lse(a[12], q.sizes().slice(0, q.dim() - 1), at::kFloat, dev);
+  const at::Tensor ws = empty({(int64_t)bytes}, at::kByte, dev);  // the call's own, as in Python
+  const int st = attend_q4_fn(&p, i32(group), i32(T), qp, pool, tp, lp, pos,
+                              static_cast<float*>(out.p), static_cast<float*>(lse.p),
+                              ws.data_ptr(), bytes, status, stream_of(dev));
+  if (st != DA_OK) return PyLong_FromLong(st);
+  return pair(out.object(), lse.object());
+}
+
+// old_lens, new_lens, block_table, free_list, free_count, block_size, num_blocks, max_tokens,
+// dev_status: outputs of its own
+PyObject* plan(PyObject* const* a) {
+  const at::Tensor& old_lens = tensor(a[0]);
+  const int dev = device(old_lens);
+  const at::Tensor &new_lens = tensor(a[1]), &table = tensor(a[2]), &list = tensor(a[3]),
+                   &count = tensor(a[4]);
+  auto ints = [&](const at::Tensor& t, int dims) {
+    return static_cast<int32_t*>(plain(t, at::kInt, dev, dims));
+  };
+  auto *op = ints(old_lens, 1), *np = ints(new_lens, 1), *tp = ints(table, 2), *lp = ints(list, 1),
+       *cp = ints(count, 1);
+  const int64_t B = old_lens.size(0), n = integer(a[7]);
+  need(B > 0 && n >= 0 && new_lens.size(0) == B && table.size(0) == B && count.size(0) == 1);
+  auto* status = static_cast<int32_t*>(plain_or_null(a[8], at::kInt, dev, -1));
+  const int32_t bs = i32(integer(a[5])), nb = i32(integer(a[6]));
+  at::Tensor out[4] = {empty({n}, at::kInt, dev), empty({n}, at::kInt, dev),
+                       empty({n}, at::kLong, dev), empty({B + 1}, at::kInt, dev)};
+  const int st = plan_fn(i32(B), bs, i32(table.size(1)), nb, i32(n), i32(list.size(0)), op, np, tp,
+                         lp, cp, static_cast<int32_t*>(out[0].data_ptr()),
+                         static_cast<int32_t*>(out[1].data_ptr()),
+                         static_cast<int64_t*>(out[2].data_ptr()),
+                         static_cast<int32_t*>(out[3].data_ptr()), status, stream_of(dev));
+  if (st != DA_OK) return PyLong_FromLong(st);
+  PyObject* t = PyTuple_New(4);
+  for (int i = 0; t && i < 4; ++i) {
+    PyObject* o = THPVariable_Wrap(std::move(out[i]));
+    if (!o) {
+      Py_DECREF(t);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(t, i, o);
+  }
+  return t;
+}
+
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != N || !norm_rope_fn) {
+  if (n != N || !norm_rope_fn || !plan_fn) {
     PyErr_SetString(PyExc_TypeError, "wrong number of arguments, or bind() was not called");
     return nullptr;
   }
@@ -317,6 +472,29 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// Addresses of decode_attn_append_paged_q4, _gather_paged_q4, _paged_q4, the latter's workspace size and
+// of decode_attn_plan_blocks.
+PyObject* bind_q4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 5) {
+    PyErr_SetString(PyExc_TypeError, "five addresses are needed");
+    return nullptr;
+  }
+  void* f[5];
+  for (int i = 0; i < 5; ++i) {
+    f[i] = PyLong_AsVoidPtr(args[i]);
+    if (!f[i]) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
+      return nullptr;
+    }
+  }
+  append_q4_fn = reinterpret_cast<decltype(append_q4_fn)>(f[0]);
+  gather_q4_fn = reinterpret_cast<decltype(gather_q4_fn)>(f[1]);
+  attend_q4_fn = reinterpret_cast<decltype(attend_q4_fn)>(f[2]);
+  attend_q4_ws_fn = reinterpret_cast<decltype(attend_q4_ws_fn)>(f[3]);
+  plan_fn = reinterpret_cast<decltype(plan_fn)>(f[4]);
+  Py_RETURN_NONE;
+}
+
 template <typename F>
 PyCFunction method(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -327,6 +505,11 @@ PyMethodDef methods[] = {
     {"norm_rope", method(entry<norm_rope, 12>), METH_FASTCALL, nullptr},
     {"append", method(entry<append, 17>), METH_FASTCALL, nullptr},
     {"prefix", method(entry<prefix, 16>), METH_FASTCALL, nullptr},
+    {"bind_q4", method(bind_q4), METH_FASTCALL, nullptr},
+    {"append_q4", method(entry<append_q4, 17>), METH_FASTCALL, nullptr},
+    {"gather_q4", method(entry<gather_q4, 7>), METH_FASTCALL, nullptr},
+    {"attend_q4", method(entry<attend_q4, 14>), METH_FASTCALL, nullptr},
+    {"plan", method(entry<plan, 9>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "decode_attn_call", nullptr, -1, methods,

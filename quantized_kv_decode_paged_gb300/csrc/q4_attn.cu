@@ -237,7 +237,9 @@ struct Shared {
   int warp_sum[WARPS];
 };
 
-template <int D, int NG>
+// PACK: at most four query rows a unit, whose two terms share one MMA operand: rows 0 to 3 of N are the first
+// terms, 4 to 7 the second ones, so that half the MMAs do.
+template <int D, int NG, bool PACK>
 __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
     q4_kernel(const __grid_constant__ Q4Params p) {
   using g_ = Geo<D, NG>;
@@ -402,6 +404,7 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
   };
 
   const int g = lane >> 2, c = lane & 3;
+  const int col = PACK ? 2 * (c & 1) : 2 * c;  // query row of the lane's first column, of kRows
   // key of the 16 that row i of the MMA holds: tau(i) = i, tau(8 + i) = 8 + (i ^ 4).  Row j of V's
   // 16 x 16 bytes is key pi(j), which makes its bytes 4c .. 4c + 3 the keys of the MMA's k = 2c, 2c + 8,
   // 2c + 1, 2c + 9.
@@ -420,18 +423,11 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
 
   Part a;
   while (next_part(a)) {
-    id_next = block_id(a, my_tile);
-#pragma unroll 1
-    for (int n = 0; n < STAGES; ++n) copy(a, n);
     const int row0 = (a.block * p.groups + rg) * kRows;  // first query row of the warp
     // ------------------------------------------------ Q: row g, dims 32 p + 8 c ..
-    uint32_t qf[g_::QREG ? P * 2 : 1][4];  // hi of k = 2c.. and 2c + 8.., lo of the same
-    float2 f, qs[NG];                      // factors and group sums of columns 2c, 2c + 1
-    int lo[2], hi[2];
+    float x[P][8];
     {
-      const int r = row0 + g;
-      float x[P][8];
-      float most = 0.f;
+      const int r = row0 + (PACK ? g & 3 : g);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         if (r < p.R) {
@@ -445,9 +441,21 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
         }
+      }
+    }
+    id_next = block_id(a, my_tile);
+#pragma unroll 1
+    for (int n = 0; n < STAGES; ++n) copy(a, n);
+    constexpr int QW = PACK ? 2 : 4;  // words of a fragment: k = 2c.. and 2c + 8.. of the first term, the second
+    uint32_t qf[g_::QREG ? P * 2 : 1][QW];
+    float2 f, qs[NG];  // factors and group sums of the lane's columns
+    int lo[2], hi[2];
+    {
+      float most = 0.f;
+#pragma unroll
+      for (int i = 0; i < P; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) most = max_nan(most, fabsf(x[i][j]));
-      }
       most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 2));
       const bool finite = most < INFINITY;
@@ -470,9 +478,12 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
           uint4 w;
           da::split_half2(x[i][o], x[i][o + 4], w.x, w.z);
           da::split_half2(x[i][o + 2], x[i][o + 6], w.y, w.w);
+          if (PACK && g >= 4) w.x = w.z, w.y = w.w;
           if constexpr (g_::QREG) {
             qf[2 * i + o][0] = w.x, qf[2 * i + o][1] = w.y;
-            qf[2 * i + o][2] = w.z, qf[2 * i + o][3] = w.w;
+            if constexpr (!PACK) qf[2 * i + o][2] = w.z, qf[2 * i + o][3] = w.w;
+          } else if constexpr (PACK) {
+            reinterpret_cast<uint2*>(qfrag)[(2 * i + o) * 32 + lane] = make_uint2(w.x, w.y);
           } else {
             qfrag[(2 * i + o) * 32 + lane] = w;  // warps of the same rows write the same
           }
@@ -483,16 +494,16 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
         sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 1);
         sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 2);
       }
-      f.x = __shfl_sync(0xffffffffu, back, 8 * c);
-      f.y = __shfl_sync(0xffffffffu, back, 8 * c + 4);
+      f.x = __shfl_sync(0xffffffffu, back, 4 * col);
+      f.y = __shfl_sync(0xffffffffu, back, 4 * col + 4);
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        qs[n].x = __shfl_sync(0xffffffffu, sum[n], 8 * c) * f.x;
-        qs[n].y = __shfl_sync(0xffffffffu, sum[n], 8 * c + 4) * f.y;
+        qs[n].x = __shfl_sync(0xffffffffu, sum[n], 4 * col) * f.x;
+        qs[n].y = __shfl_sync(0xffffffffu, sum[n], 4 * col + 4) * f.y;
       }
       f.x *= 0x1p9f, f.y *= 0x1p9f;  // the codes come times 2^-9
 #pragma unroll
-      for (int j = 0; j < 2; ++j) row_keys(p, a.s, (row0 + 2 * c + j) / p.G, lo[j], hi[j]);
+      for (int j = 0; j < 2; ++j) row_keys(p, a.s, (row0 + col + j) / p.G, lo[j], hi[j]);
       __syncwarp();
     }
     // keys that every row sees
@@ -539,15 +550,20 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
             float2 u[H][2], z[H][2];
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-              float ah[H][4], al[H][4];
+              float ah[H][4];
+                [[maybe_unused]] float al[H][4];
 #pragma unroll
               for (int i2 = n * GP; i2 < (n + 1) * GP; ++i2) {
 #pragma unroll
                 for (int o2 = 0; o2 < 2; ++o2) {
-                  uint32_t q0, q1, q2, q3;
+                  uint32_t q0, q1;
+                    [[maybe_unused]] uint32_t q2 = 0, q3 = 0;
                   if constexpr (g_::QREG) {
                     q0 = qf[2 * i2 + o2][0], q1 = qf[2 * i2 + o2][1];
-                    q2 = qf[2 * i2 + o2][2], q3 = qf[2 * i2 + o2][3];
+                    if constexpr (!PACK) q2 = qf[2 * i2 + o2][2], q3 = qf[2 * i2 + o2][3];
+                  } else if constexpr (PACK) {
+                    const uint2 w = reinterpret_cast<const uint2*>(qfrag)[(2 * i2 + o2) * 32 + lane];
+                    q0 = w.x, q1 = w.y;
                   } else {
                     const uint4 w = qfrag[(2 * i2 + o2) * 32 + lane];
                     q0 = w.x, q1 = w.y, q2 = w.z, q3 = w.w;
@@ -559,10 +575,10 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
                     const uint32_t f2 = codes2(a0 >> 8, o2), f3 = codes2(a1 >> 8, o2);
                     if (i2 == n * GP && o2 == 0) {
                       mma_first(ah[h], f0, f1, f2, f3, q0, q1);
-                      mma_first(al[h], f0, f1, f2, f3, q2, q3);
+                      if constexpr (!PACK) mma_first(al[h], f0, f1, f2, f3, q2, q3);
                     } else {
                       mma(ah[h], f0, f1, f2, f3, q0, q1);
-                      mma(al[h], f0, f1, f2, f3, q2, q3);
+                      if constexpr (!PACK) mma(al[h], f0, f1, f2, f3, q2, q3);
                     }
                   }
                 }
@@ -573,8 +589,11 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
                 for (int k = 0; k < 2; ++k) {
                   const float sk = half_lo(kp[h][k][n]);
                   const float zk = fmaf(8.f, sk, half_hi(kp[h][k][n]));
-                  const float2 t = da::add2(make_float2(ah[h][2 * k], ah[h][2 * k + 1]),
-                                            make_float2(al[h][2 * k], al[h][2 * k + 1]));
+                  float2 t = make_float2(ah[h][2 * k], ah[h][2 * k + 1]);
+if constexpr (PACK)
+  t = da::add2(t, make_float2(__shfl_xor_sync(0xffffffffu, t.x, 2), __shfl_xor_sync(0xffffffffu, t.y, 2)));
+else
+  t = da::add2(t, make_float2(al[h][2 * k], al[h][2 * k + 1]));
                   if (n == 0) {
                     u[h][k] = make_float2(t.x * sk, t.y * sk);
                     z[h][k] = make_float2(zk * qs[n].x, zk * qs[n].y);
@@ -692,8 +711,9 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
                   zero_sum[n].y = fmaf(x[h][k].y, zv, zero_sum[n].y);
                 }
                 da::split_half2(w.x, w.y, ph[h][k], pl[h][k]);
+                  if (PACK && c >= 2) ph[h][k] = pl[h][k];
                 ph[h][k] = da::movmatrix_trans(ph[h][k]);
-                pl[h][k] = da::movmatrix_trans(pl[h][k]);
+                if constexpr (!PACK) pl[h][k] = da::movmatrix_trans(pl[h][k]);
               }
             // two pieces' products of one term, then of the other: each waits for none before it
             constexpr int PP = GP > 1 ? 2 : 1;
@@ -709,9 +729,11 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
                   fr[k][2] = codes2(a0 >> 8, k & 1), fr[k][3] = codes2(a1 >> 8, k & 1);
                   mma(acc[2 * i2 + k], fr[k][0], fr[k][1], fr[k][2], fr[k][3], ph[h][0], ph[h][1]);
                 }
+if constexpr (!PACK) {
 #pragma unroll
                 for (int k = 0; k < 2 * PP; ++k)
                   mma(acc[2 * i2 + k], fr[k][0], fr[k][1], fr[k][2], fr[k][3], pl[h][0], pl[h][1]);
+}
               }
           }
         };
@@ -751,18 +773,18 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
     }
     float* to[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {  // rows of columns 2c, 2c + 1
-      const int r = row0 + 2 * c + j;
+    for (int j = 0; j < 2; ++j) {  // rows of the lane's columns
+      const int r = row0 + col + j;
       const float mj = j ? m.y : m.x, lj = j ? l.y : l.x;
       to[j] = nullptr;
-      if (r >= p.R) continue;
+      if (r >= p.R || (PACK && c >= 2)) continue;
       if (a.slot < 0) {
         const int t = r / p.G, h = a.kv * p.G + (r - t * p.G);
         const long long row = ((long long)a.b * p.T + t) * p.Hq + h;
         to[j] = p.out + row * D;
         if (g == 0 && p.lse) p.lse[row] = lj == 0.f ? -INFINITY : (mj - kShift + log2f(lj)) * kLn2;
       } else {
-        const long long row = ((long long)share * 2 + a.slot) * p.groups * kRows + rg * kRows + 2 * c + j;
+        const long long row = ((long long)share * 2 + a.slot) * p.groups * kRows + rg * kRows + col + j;
         to[j] = p.part_o + row * D;
         if (g == 0) p.part_ml[row] = make_float2(mj, lj);
       }
@@ -776,6 +798,12 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
         acc[i][0] = fmaf(y.x, due.x, acc[i][0]), acc[i][1] = fmaf(y.y, due.y, acc[i][1]);
         acc[i][2] = fmaf(y.z, due.x, acc[i][2]), acc[i][3] = fmaf(y.w, due.y, acc[i][3]);
       }
+    }
+    if constexpr (PACK) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], 2);
     }
 #pragma unroll
     for (int i = 0; i < P; ++i)
@@ -912,21 +940,26 @@ Layout layout(int sms, int D) {
   return w;
 }
 
-template <int D, int NG>
+template <int D, int NG, bool PACK>
 cudaError_t launch(Q4Params& k, int grid, cudaStream_t s) {
   using g_ = Geo<D, NG>;
   static_assert(sizeof(Shared<g_::WARPS, g_::STAGES>) <= 2048, "more than a processor's shared memory");
-  cudaError_t err = cudaFuncSetAttribute(q4_kernel<D, NG>,
+  cudaError_t err = cudaFuncSetAttribute(q4_kernel<D, NG, PACK>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, g_::kMost);
   if (err != cudaSuccess) return err;
   k.log2_eb = 0;
   while ((2 << k.log2_eb) <= g_::TOK && k.log2_eb < k.log2_bs) ++k.log2_eb;
   k.shares = grid * (g_::WARPS / k.groups);
-  err = da::launch_early(q4_kernel<D, NG>, grid, g_::THREADS, g_::SMEM + (k.B + 1) * 4, s, k);
+  err = da::launch_early(q4_kernel<D, NG, PACK>, grid, g_::THREADS, g_::SMEM + (k.B + 1) * 4, s, k);
   if (err != cudaSuccess) return err;
   const long long rows = (long long)k.B * k.T * k.Hq;
   return da::launch_early(q4_merge_kernel<D>, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps),
                           32 * kMergeWarps, 0, s, k);
+}
+
+template <int D, int NG>
+cudaError_t launch(Q4Params& k, int grid, cudaStream_t s) {
+  return k.R <= 4 ? launch<D, NG, true>(k, grid, s) : launch<D, NG, false>(k, grid, s);
 }
 
 cudaError_t launch(Q4Params& k, int D, int group, int grid, cudaStream_t s) {
