@@ -28,6 +28,11 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kCluster = 8;        // CTAs of a large call
 constexpr int kMaxBatch = 16384;   // three sums of each in shared memory
+constexpr int kKeptBatch = 10240;  // both lengths too
+// A warp takes up to 32 * kRun entries side by side: most are the request's that the one before was, and need no
+// search, and their loads are under way together (a call that takes 101,000 pages back and places 20,000 tokens:
+// 42 us with one entry at a time).
+constexpr int kRun = 8;
 
 struct PlanArgs {
   int B, log2_bs, max_blocks, num_blocks, max_tokens, free_capacity, ctas;
@@ -66,6 +71,11 @@ __device__ __forceinline__ int find(const int* sum, int B, int i) {
   return lo;
 }
 
+// The same where b is the request of an earlier entry.
+__device__ __forceinline__ int find_from(const int* sum, int B, int i, int b) {
+  return sum[b + 1] > i ? b : find(sum, B, i);
+}
+
 __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
   extern __shared__ int smem[];
   __shared__ Sums warp_sums[kThreads / 32];
@@ -74,6 +84,10 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
   int* cu = smem;                // [B + 1] tokens before request b
   int* taken = cu + a.B + 1;     // pages taken before it
   int* given = taken + a.B + 1;  // pages given back before it
+  const bool keep = a.B <= kKeptBatch;
+  int* kept = given + a.B + 1;  // [2][B] lengths before and after
+  const int* old_lens = keep ? kept : a.old_lens;
+  const int* new_lens = keep ? kept + a.B : a.new_lens;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
   const int bs = 1 << a.log2_bs;
   const long long cap = (long long)a.max_blocks << a.log2_bs;
@@ -84,9 +98,16 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
   // the sums: a thread has `per` requests side by side
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  if (keep) {
+    for (int b = tid; b < a.B; b += kThreads) {
+      kept[b] = a.old_lens[b];
+      kept[a.B + b] = a.new_lens[b];
+    }
+    __syncthreads();
+  }
   int bad = 0;
   auto of = [&](int b) {
-    const long long o = a.old_lens[b], n = a.new_lens[b];
+    const long long o = old_lens[b], n = new_lens[b];
     if (o < 0 || n < 0 || o > cap || n > cap) {
       bad |= DA_DEV_BAD_SEQ_LEN;
       return Sums{0, 0, 0};
@@ -145,15 +166,29 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
   const int T = (int)all.taken, R = (int)all.given, N = (int)all.tokens;
   const int F = (int)count, left = (int)left64;
   auto pages = [&](int len) { return (len + bs - 1) >> a.log2_bs; };
-  // table entry of page i of those given back
-  auto given_at = [&](int i) {
-    const int b = find(given, a.B, i);
-    return (long long)b * a.max_blocks + pages(a.new_lens[b]) + (i - given[b]);
+  // table entry of page i of those given back; b: the request of an earlier one, and this one's
+  auto given_at = [&](int i, int& b) {
+    b = find_from(given, a.B, i, b);
+    return (long long)b * a.max_blocks + pages(new_lens[b]) + (i - given[b]);
   };
   // the page that entry k of those taken gets
-  auto taken_page = [&](int k) {
+  auto taken_page = [&](int k, int& b) {
     const int i = left + k;
-    return i < F ? a.free_list[i] : a.table[given_at(i - F)];
+    return i < F ? a.free_list[i] : a.table[given_at(i - F, b)];
+  };
+  // each entry of `count` once: use(i, load(i)), the loads of a run before the first use
+  auto each = [&](int count, auto load, auto use) {
+    const int run = min(kRun, (count + step - 1) / step);
+    for (int i0 = (rank * (kThreads / 32) + warp) * (32 * run) + lane; i0 - lane < count;
+         i0 += step * run) {
+      decltype(load(0)) x[kRun];
+#pragma unroll
+      for (int u = 0; u < kRun; ++u)
+        if (u < run && i0 + 32 * u < count) x[u] = load(i0 + 32 * u);
+#pragma unroll
+      for (int u = 0; u < kRun; ++u)
+        if (u < run && i0 + 32 * u < count) use(i0 + 32 * u, x[u]);
+    }
   };
   auto is_page = [&](int id) { return id >= 0 && id < a.num_blocks; };
 
@@ -161,13 +196,16 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
   if (sound) {
     // all that is read from table and stack: pages given back, pages taken, last pages that grow
     bad = 0;
-    for (int i = first; i < R; i += step)
-      if (!is_page(a.table[given_at(i)])) bad |= DA_DEV_BAD_BLOCK;
+    int g = 0;
+    each(R, [&](int i) { return a.table[given_at(i, g)]; },
+         [&](int, int id) {
+           if (!is_page(id)) bad |= DA_DEV_BAD_BLOCK;
+         });
     for (int i = left + first; i < F; i += step)
       if (!is_page(a.free_list[i])) bad |= DA_DEV_BAD_FREE_LIST;
     for (int b = first; b < a.B; b += step) {
-      const int o = a.old_lens[b];
-      if (a.new_lens[b] > o && (o & (bs - 1)) &&
+      const int o = old_lens[b];
+      if (new_lens[b] > o && (o & (bs - 1)) &&
           !is_page(a.table[(long long)b * a.max_blocks + (o >> a.log2_bs)]))
         bad |= DA_DEV_BAD_BLOCK;
     }
@@ -186,35 +224,54 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
     for (int b = first; b <= a.B; b += step) a.cu[b] = 0;
     if (first == 0 && a.dev_status) atomicOr(a.dev_status, found);
   } else {
-    for (int k = first; k < T; k += step) {
-      const int b = find(taken, a.B, k);
-      a.table[(long long)b * a.max_blocks + pages(a.old_lens[b]) + (k - taken[b])] = taken_page(k);
-    }
-    for (int n = first; n < a.max_tokens; n += step) {
-      if (n >= N) {
-        a.positions[n] = 0;
-        a.token_seq[n] = -1;
-        a.slots[n] = -1;
-        continue;
-      }
-      const int b = find(cu, a.B, n), o = a.old_lens[b];
-      const int pos = o + (n - cu[b]), page = pos >> a.log2_bs, held = pages(o);
-      const int id = page < held ? a.table[(long long)b * a.max_blocks + page]
-                                 : taken_page(taken[b] + page - held);
-      a.positions[n] = pos;
-      a.token_seq[n] = b;
-      a.slots[n] = ((long long)id << a.log2_bs) + (pos & (bs - 1));
-    }
-    for (int b = first; b <= a.B; b += step) a.cu[b] = cu[b];
+    int g = 0, t = 0;
+    each(T, [&](int k) { return taken_page(k, g); },
+         [&](int k, int id) {
+           t = find_from(taken, a.B, k, t);
+           a.table[(long long)t * a.max_blocks + pages(old_lens[t]) + (k - taken[t])] = id;
+         });
+    struct Token {
+      int seq, pos, id;
+    };
+    int b = 0;
+    g = 0;
+    each(a.max_tokens,
+         [&](int n) {
+           Token x = {-1, 0, -1};
+           if (n < N) {
+             x.seq = b = find_from(cu, a.B, n, b);
+             const int o = old_lens[b], held = pages(o);
+             x.pos = o + (n - cu[b]);
+             const int page = x.pos >> a.log2_bs;
+             x.id = page < held ? a.table[(long long)b * a.max_blocks + page]
+                                : taken_page(taken[b] + page - held, g);
+           }
+           return x;
+         },
+         [&](int n, const Token& x) {
+           a.positions[n] = x.pos;
+           a.token_seq[n] = x.seq;
+           a.slots[n] = x.seq < 0 ? -1 : ((long long)x.id << a.log2_bs) + (x.pos & (bs - 1));
+         });
+    for (int i = first; i <= a.B; i += step) a.cu[i] = cu[i];
   }
   // every CTA is past its reads of entries that change now (and of the others' flags)
   cluster.sync();
   if (found) return;
-  for (int i = first; i < R; i += step) {
-    const long long at = given_at(i);
-    if (F + i < left) a.free_list[F + i] = a.table[at];
-    a.table[at] = -1;
-  }
+  struct Entry {
+    long long at;
+    int id;
+  };
+  int g = 0;
+  each(R,
+       [&](int i) {
+         const long long at = given_at(i, g);
+         return Entry{at, F + i < left ? a.table[at] : -1};
+       },
+       [&](int i, const Entry& x) {
+         if (F + i < left) a.free_list[F + i] = x.id;
+         a.table[x.at] = -1;
+       });
   if (first == 0) *a.free_count = left;
 }
 
@@ -237,7 +294,7 @@ extern "C" int decode_attn_plan_blocks(int32_t batch, int32_t block_size,
     return DA_ERR_UNSUPPORTED;
   if ((long long)num_blocks * block_size > 0x7fffffffLL ||
       (long long)max_blocks_per_seq * block_size > 0x7fffffffLL || batch > kMaxBatch ||
-      max_tokens > 0x7fffffff - (1 << 20) || free_capacity > 0x7fffffff - (1 << 20))
+      max_tokens > 0x7fffffff - (1 << 21) || free_capacity > 0x7fffffff - (1 << 21))
     return DA_ERR_UNSUPPORTED;
   if (!old_lens || !new_lens || !block_table || !free_count || !cu_tokens ||
       (free_capacity > 0 && !free_list) ||
@@ -268,10 +325,13 @@ extern "C" int decode_attn_plan_blocks(int32_t batch, int32_t block_size,
   a.dev_status = dev_status;
   // one CTA where its threads have at most a token or a request each
   a.ctas = batch <= kThreads && max_tokens <= kThreads ? 1 : kCluster;
-  const size_t smem = 3 * sizeof(int) * ((size_t)batch + 1);
+  const size_t smem = 3 * sizeof(int) * ((size_t)batch + 1) +
+                      (batch <= kKeptBatch ? 2 * sizeof(int) * (size_t)batch : 0);
+  constexpr size_t kMost = 5 * sizeof(int) * kKeptBatch + 64;
+  static_assert(kMost >= 3 * sizeof(int) * (kMaxBatch + 1) && kMost <= 226 * 1024, "shared memory");
   if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           3 * sizeof(int) * (kMaxBatch + 1)) != cudaSuccess)
+      cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) !=
+          cudaSuccess)
     return DA_ERR_CUDA;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;

@@ -19,7 +19,10 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 16;  // of a CTA
+constexpr int kTokens = 128;  // of a CTA
+// Words of eight codes of keys and values that a thread has in work at once: 40,003 tokens x 8 heads x 128 to
+// f16 took 59 us with one.
+constexpr int kAtOnce = 4;
 
 struct GatherArgs {
   const int32_t* positions;
@@ -29,6 +32,7 @@ struct GatherArgs {
   void* k_out;
   void* v_out;
   int N, tokens, Hkv, group;
+  uint64_t inv_heads;  // ceil(2^32 / Hkv): r / Hkv = r * inv_heads >> 32, r < 2^16
   int batch, log2_bs, max_blocks, num_blocks;
   long long page_bytes;
   int32_t* dev_status;
@@ -56,6 +60,11 @@ __device__ __forceinline__ void store_row8(T* p, const float (&x)[8]) {
     }
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+// Code j of a word: the last bits of 2^23 + code (the conversion instruction runs at a quarter of the rate).
+__device__ __forceinline__ float code(uint32_t w, int j) {
+  return __uint_as_float((w >> (4 * j) & 15u) | 0x4b000000u) - 8388608.f;
 }
 
 template <typename T, int D>
@@ -87,37 +96,50 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
   }
   __syncthreads();
   constexpr int C = D / 8;  // words of a row
-  const int bs = 1 << a.log2_bs, per = a.Hkv * C, ng = D / a.group;
-  for (int i = threadIdx.x; i < tokens * per; i += kThreads) {
-    const int t = i / per, h = (i - t * per) / C, c = i % C;
-    const long long row = place[t];
-    float k[8] = {}, v[8] = {};
-    if (row >= 0) {
-      const int r = (int)(row & (bs - 1));
-      const uint8_t* page = a.pool + ((row >> a.log2_bs) * a.Hkv + h) * a.page_bytes;
-      const int piece = (c / 4) ^ da::piece_xor<D>(r);
-      const uint8_t* at = page + r * (D / 2) + 16 * piece + c % 4 * 4;
-      const uint32_t kc = *reinterpret_cast<const uint32_t*>(at);
-      const uint32_t vc = *reinterpret_cast<const uint32_t*>(at + bs * (D / 2));
-      const uint32_t* par = reinterpret_cast<const uint32_t*>(page + bs * D) + r * ng + c * 8 / a.group;
-      const uint32_t kw = par[0], vw = par[bs * ng];
-      const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&kw));
-      const float2 vp = __half22float2(*reinterpret_cast<const __half2*>(&vw));
+  const int bs = 1 << a.log2_bs, ng = D / a.group, items = tokens * a.Hkv * C;
+  for (int i0 = threadIdx.x; i0 < items; i0 += kAtOnce * kThreads) {
+    uint32_t kc[kAtOnce], vc[kAtOnce], kw[kAtOnce], vw[kAtOnce];
+    bool have[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        k[j] = fmaf((float)(kc >> (4 * j) & 15u), kp.x, kp.y);
-        v[j] = fmaf((float)(vc >> (4 * j) & 15u), vp.x, vp.y);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kThreads, c = i % C, r = i / C;
+      const int t = (int)(((uint64_t)r * a.inv_heads) >> 32), h = r - t * a.Hkv;
+      const long long row = i < items ? place[t] : -1;
+      have[u] = row >= 0;
+      kc[u] = vc[u] = kw[u] = vw[u] = 0;  // codes, scales and zeros of nothing: zeros
+      if (have[u]) {
+        const int n = (int)(row & (bs - 1));
+        const uint8_t* page = a.pool + ((row >> a.log2_bs) * a.Hkv + h) * a.page_bytes;
+        const uint8_t* at = page + n * (D / 2) + 16 * ((c / 4) ^ da::piece_xor<D>(n)) + c % 4 * 4;
+        kc[u] = __ldg(reinterpret_cast<const uint32_t*>(at));
+        vc[u] = __ldg(reinterpret_cast<const uint32_t*>(at + bs * (D / 2)));
+        const uint32_t* par = reinterpret_cast<const uint32_t*>(page + bs * D) + n * ng + c * 8 / a.group;
+        kw[u] = __ldg(par);
+        vw[u] = __ldg(par + bs * ng);
       }
     }
-    const long long to = ((long long)(n0 + t) * a.Hkv + h) * D + c * 8;
-    store_row8(static_cast<T*>(a.k_out) + to, k);
-    store_row8(static_cast<T*>(a.v_out) + to, v);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= items) break;
+      const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&kw[u]));
+      const float2 vp = __half22float2(*reinterpret_cast<const __half2*>(&vw[u]));
+      float k[8], v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        k[j] = fmaf(code(kc[u], j), kp.x, kp.y);
+        v[j] = fmaf(code(vc[u], j), vp.x, vp.y);
+      }
+      const long long to = (long long)n0 * a.Hkv * D + (long long)i * 8;
+      store_row8(static_cast<T*>(a.k_out) + to, k);
+      store_row8(static_cast<T*>(a.v_out) + to, v);
+    }
   }
 }
 
 template <typename T>
 cudaError_t launch_gather(const GatherArgs& a, int D, cudaStream_t s) {
-  const int grid = (a.N + a.tokens - 1) / a.tokens;
+  const int grid = (a.N - 1) / a.tokens + 1;
   return da::launch_early(D == 64    ? gather_kernel<T, 64>
                           : D == 128 ? gather_kernel<T, 128>
                                      : gather_kernel<T, 256>,
@@ -178,10 +200,13 @@ int decode_attn_gather_paged_q4(const da_params* p, int32_t group, int32_t num_t
   a.k_out = k_out;
   a.v_out = v_out;
   a.N = num_tokens;
-  // short calls: a token a CTA as long as there are processors for them
-  a.tokens = (num_tokens - 1) / (sms * 8) + 1;
+  // Tokens of a CTA: so many that one wave of CTAs, four a processor, has them all where kTokens allow that (a
+  // CTA looks its tokens up first, 2 us that others do not hide), and rows of a CTA below 2^16.
+  a.tokens = (num_tokens - 1) / (sms * 4) + 1;
   if (a.tokens > kTokens) a.tokens = kTokens;
+  if (a.tokens > 65535 / p->num_kv_heads) a.tokens = 65535 / p->num_kv_heads;
   a.Hkv = p->num_kv_heads;
+  a.inv_heads = (0x100000000ULL + a.Hkv - 1) / a.Hkv;
   a.group = group;
   a.batch = p->batch;
   while ((1 << a.log2_bs) < p->block_size) ++a.log2_bs;
