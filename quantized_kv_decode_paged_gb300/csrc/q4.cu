@@ -1,7 +1,7 @@
 // q4.cu — the cache in 4 bits as rows again: cached tokens to f32, f16 or bf16.
 //
-// A value is scale * code + zero (q4.cuh), worked out in f32 by one fused multiply-add and rounded once
-// to the rows' type; f16 rows saturate at 65504, which a code's rounding may pass by half a step.
+// A value is scale * code + zero (q4.cuh), one fused multiply-add: in f16 for f16 rows, in f32 and rounded to bf16
+// for those.  f16 rows saturate at 65504, which a code's rounding may pass by half a step.
 // A thread takes eight codes, one word, so that a warp's loads and its 16- or 32-byte stores
 // cover whole sectors; a CTA looks its tokens' pages up once.  HBM bounds long calls.
 #include <cuda_bf16.h>
@@ -20,8 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTokens = 128;  // of a CTA
-// Words of eight codes of keys and values that a thread has in work at once: 40,003 tokens x 8 heads x 128 to
-// f16 took 59 us with one.
+// Words of eight codes of keys and values that a thread has in work at once.
 constexpr int kAtOnce = 4;
 
 struct GatherArgs {
@@ -38,44 +37,61 @@ struct GatherArgs {
   int32_t* dev_status;
 };
 
+// Eight values of a word of codes and its param {scale, zero}, stored.
 template <typename T>
-__device__ __forceinline__ void store_row8(T* p, const float (&x)[8]) {
-  if constexpr (std::is_same<T, float>::value) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    uint32_t w[4];
+__device__ __forceinline__ void store_values(T* p, uint32_t codes, uint32_t param) {
+  if constexpr (std::is_same<T, __half>::value) {
+    // In pairs of f16: 1024 + code less 1024, times the scale, plus the zero, with one rounding; then to f16's range
+    // (a NaN stays).  (Through f32, 40,003 tokens x 8 heads x 128 took 58 us, bound by the instructions.)
+    uint32_t s2, z2, v[4];
+    asm("prmt.b32 %0, %1, %1, 0x1010;" : "=r"(s2) : "r"(param));
+    asm("prmt.b32 %0, %1, %1, 0x3232;" : "=r"(z2) : "r"(param));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (std::is_same<T, __half>::value) {
-        w[i] = da::pack_half2(fmaxf(fminf(x[2 * i], 65504.f), -65504.f),
-                              fmaxf(fminf(x[2 * i + 1], 65504.f), -65504.f));
-        // fminf and fmaxf drop a NaN
-        if (x[2 * i] != x[2 * i]) w[i] |= 0x7fffu;
-        if (x[2 * i + 1] != x[2 * i + 1]) w[i] |= 0x7fff0000u;
-      } else {
+    for (int i = 0; i < 4; ++i) {  // codes i and i + 4
+      asm("{\n\t.reg .b32 c;\n\tadd.rn.f16x2 c, %1, %2;\n\tfma.rn.f16x2 %0, c, %3, %4;\n\t"
+          "min.NaN.f16x2 %0, %0, %5;\n\tmax.NaN.f16x2 %0, %0, %6;\n\t}"
+          : "=r"(v[i])
+          : "r"((codes >> (4 * i) & 0x000f000fu) | 0x64006400u), "r"(0xe400e400u), "r"(s2), "r"(z2),
+            "r"(0x7bff7bffu), "r"(0xfbfffbffu));
+    }
+    uint4 w;
+    w.x = __byte_perm(v[0], v[1], 0x5410), w.y = __byte_perm(v[2], v[3], 0x5410);
+    w.z = __byte_perm(v[0], v[1], 0x7632), w.w = __byte_perm(v[2], v[3], 0x7632);
+    *reinterpret_cast<uint4*>(p) = w;
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&param));
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)  // a code is the last bits of 2^23 + code
+      x[j] = fmaf(__uint_as_float((codes >> (4 * j) & 15u) | 0x4b000000u) - 8388608.f, f.x, f.y);
+    if constexpr (std::is_same<T, float>::value) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-}
-
-// Code j of a word: the last bits of 2^23 + code (the conversion instruction runs at a quarter of the rate).
-__device__ __forceinline__ float code(uint32_t w, int j) {
-  return __uint_as_float((w >> (4 * j) & 15u) | 0x4b000000u) - 8388608.f;
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
-  __shared__ long long place[kTokens];  // row of the pool, negative: none
+  struct Place {
+    const uint8_t* page;  // of kv head 0
+    int row;              // of the page; -1: none
+  };
+  __shared__ Place place[kTokens];
   const int n0 = blockIdx.x * a.tokens, tokens = min(a.tokens, a.N - n0);
   da::let_next_grid_start();
   da::wait_for_grid_before();
   if ((int)threadIdx.x < tokens) {
     const int n = n0 + threadIdx.x, seq = a.token_seq ? a.token_seq[n] : n;
-    long long row = -1;
+    Place x = {a.pool, -1};
     int flag = 0;
     if (seq >= a.batch) {
       flag = DA_DEV_BAD_SEQ;
@@ -88,32 +104,33 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
         if (blk < 0 || blk >= a.num_blocks)
           flag = DA_DEV_BAD_BLOCK;
         else
-          row = ((long long)blk << a.log2_bs) + (pos & ((1 << a.log2_bs) - 1));
+          x = {a.pool + (long long)blk * a.Hkv * a.page_bytes, pos & ((1 << a.log2_bs) - 1)};
       }
     }
-    place[threadIdx.x] = row;
+    place[threadIdx.x] = x;
     if (flag && a.dev_status) atomicOr(a.dev_status, flag);
   }
   __syncthreads();
   constexpr int C = D / 8;  // words of a row
   const int bs = 1 << a.log2_bs, ng = D / a.group, items = tokens * a.Hkv * C;
+  const int log2_group = 31 - __clz(a.group);
   for (int i0 = threadIdx.x; i0 < items; i0 += kAtOnce * kThreads) {
     uint32_t kc[kAtOnce], vc[kAtOnce], kw[kAtOnce], vw[kAtOnce];
-    bool have[kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const int i = i0 + u * kThreads, c = i % C, r = i / C;
       const int t = (int)(((uint64_t)r * a.inv_heads) >> 32), h = r - t * a.Hkv;
-      const long long row = i < items ? place[t] : -1;
-      have[u] = row >= 0;
       kc[u] = vc[u] = kw[u] = vw[u] = 0;  // codes, scales and zeros of nothing: zeros
-      if (have[u]) {
-        const int n = (int)(row & (bs - 1));
-        const uint8_t* page = a.pool + ((row >> a.log2_bs) * a.Hkv + h) * a.page_bytes;
-        const uint8_t* at = page + n * (D / 2) + 16 * ((c / 4) ^ da::piece_xor<D>(n)) + c % 4 * 4;
+      if (i >= items) continue;
+      const Place x = place[t];
+      if (x.row >= 0) {
+        const uint8_t* page = x.page + (long long)h * a.page_bytes;
+        const uint8_t* at =
+            page + (x.row * (D / 2) + 16 * ((c / 4) ^ da::piece_xor<D>(x.row)) + c % 4 * 4);
         kc[u] = __ldg(reinterpret_cast<const uint32_t*>(at));
         vc[u] = __ldg(reinterpret_cast<const uint32_t*>(at + bs * (D / 2)));
-        const uint32_t* par = reinterpret_cast<const uint32_t*>(page + bs * D) + n * ng + c * 8 / a.group;
+        const uint32_t* par = reinterpret_cast<const uint32_t*>(
+            page + (bs * D + (x.row * ng + (c * 8 >> log2_group)) * 4));
         kw[u] = __ldg(par);
         vw[u] = __ldg(par + bs * ng);
       }
@@ -122,17 +139,9 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
     for (int u = 0; u < kAtOnce; ++u) {
       const int i = i0 + u * kThreads;
       if (i >= items) break;
-      const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&kw[u]));
-      const float2 vp = __half22float2(*reinterpret_cast<const __half2*>(&vw[u]));
-      float k[8], v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        k[j] = fmaf(code(kc[u], j), kp.x, kp.y);
-        v[j] = fmaf(code(vc[u], j), vp.x, vp.y);
-      }
       const long long to = (long long)n0 * a.Hkv * D + (long long)i * 8;
-      store_row8(static_cast<T*>(a.k_out) + to, k);
-      store_row8(static_cast<T*>(a.v_out) + to, v);
+      store_values(static_cast<T*>(a.k_out) + to, kc[u], kw[u]);
+      store_values(static_cast<T*>(a.v_out) + to, vc[u], vw[u]);
     }
   }
 }
