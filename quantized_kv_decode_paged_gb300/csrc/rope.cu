@@ -211,19 +211,22 @@ __device__ __forceinline__ Q4Param q4_param(float2 e) {
 // x 16 rows x 128 took 58 us.)
 __device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], const Q4Param& p) {
   if (!(p.scale > 0.f)) return 0;
-  constexpr float kInt = 12582912.f;  // 1.5 * 2^23: added to a small number, its last bits are the number's nearest integer
+  // 1.5 * 2^23: added to a small number, its last bits are the number's nearest integer
+  const float2 kInt = make_float2(12582912.f, 12582912.f), kBack = make_float2(-12582912.f, -12582912.f);
+  const float2 minus = make_float2(-p.zero, -p.zero), inv = make_float2(p.inv, p.inv);
   uint32_t w = 0;
-  bool near = false;
+  float far = 0.f;  // from the nearest integer
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float q = fminf(fmaxf((x[i] - p.zero) * p.inv, 0.f), 15.f);
-    const float t = q + kInt, off = fabsf(q - (t - kInt));
-    near |= off > 0.5f - 1e-4f;
-    w = w * 16 + __float_as_uint(t);
+  for (int i = 6; i >= 0; i -= 2) {
+    float2 q = da::mul2(da::add2(make_float2(x[i], x[i + 1]), minus), inv);
+    q = make_float2(fminf(fmaxf(q.x, 0.f), 15.f), fminf(fmaxf(q.y, 0.f), 15.f));
+    const float2 t = da::add2(q, kInt), c = da::add2(t, kBack);
+    far = fmaxf(far, fmaxf(fabsf(q.x - c.x), fabsf(q.y - c.y)));
+    w = (w * 16 + __float_as_uint(t.y)) * 16 + __float_as_uint(t.x);
   }
   // the numbers' upper bits, 0x4b400000, in every one of the eight places
   w -= 0x4b400000u * 0x11111111u;
-  if (near) {
+  if (far > 0.5f - 1e-4f) {
     w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
