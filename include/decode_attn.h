@@ -493,7 +493,10 @@ int decode_attn_paged_prefix(const da_params* p, int32_t q_len, int32_t prefix_l
  * cu_tokens[B].
  * The buffers must not overlap.  batch <= 16384; block_size a power of two in
  * [8, 256].  max_tokens may be 0 (the three token arrays may then be NULL), but
- * a request that gains tokens then overflows.
+ * a request that gains tokens then overflows.  With batch 0 and max_tokens 0 nothing
+ * is done.  DA_ERR_UNSUPPORTED where num_blocks * block_size or max_blocks_per_seq *
+ * block_size does not count in 31 bits, or max_tokens or free_capacity is above
+ * 2^31 - 2^21.
  */
 int decode_attn_plan_blocks(int32_t batch, int32_t block_size, int32_t max_blocks_per_seq,
                             int32_t num_blocks, int32_t max_tokens, int32_t free_capacity,
@@ -560,12 +563,14 @@ int decode_attn_gather_paged_q4(const da_params* p, int32_t group, int32_t num_t
  * workspace: device scratch of decode_attn_paged_q4_workspace_size(p, q_len)
  * bytes, 256-byte aligned, of any content (parts of sequences that several
  * warps share); calls that overlap on the GPU must not share it.  Calls of one
- * stream may, also from several threads.  p->max_seq_len is not used.
+ * stream may, also from several threads.  p->max_seq_len is not used, nor is
+ * da_tuning: nothing in the kernel waits for another part of it.
  * Everything else as for decode_attn_paged.  DA_ERR_UNSUPPORTED also where one
  * sequence's query rows (q_len * num_q_heads) or key tiles
  *   (max_blocks_per_seq * block_size * head_dim / 4096 + 2) * num_kv_heads *
  *   ceil(q_len * num_q_heads / num_kv_heads / 8)
- * would not count in 31 bits.
+ * would not count in 31 bits, or a page's records of all kv heads not in 32 bits
+ * of bytes.
  */
 size_t decode_attn_paged_q4_workspace_size(const da_params* p, int32_t q_len);
 int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const float* q,

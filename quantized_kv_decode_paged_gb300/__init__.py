@@ -802,7 +802,8 @@ def _load_call():
                     lib.decode_attn_paged_q4, lib.decode_attn_paged_q4_workspace_size,
                     lib.decode_attn_plan_blocks)))
             except ImportError as e:
-                warnings.warn("the norm, append and shared-prefix calls go through Python, slower: "
+                warnings.warn("the norm, append, shared-prefix, 4-bit cache and block plan calls go "
+                              "through Python, slower: "
                               f"no {path} (quantized_kv_decode_paged_gb300.build() makes it): {e}",
                               RuntimeWarning)
                 module = _NoCall
@@ -1418,7 +1419,7 @@ def decode_attn_paged_q4(q, pool, block_table, seq_lens, q_pos=None, *, group, s
                          lse=None, workspace="auto", dev_status=None, stream=None):
     """decode_attn_paged (q [B, Hq, D]) or decode_attn_paged_multi (q [B, T, Hq, D])
     over a cache held in 4 bits (decode_attn_append_paged_q4's pool and group).
-    Returns (out, lse).
+    Returns (out, lse).  max_seq_len is taken for the other calls' sake and not used.
 
     ``workspace``: "auto" (the call's own, from torch's allocator on the call's
     stream; a captured call's in its graph's memory) or a caller-owned uint8

@@ -833,8 +833,6 @@ size_t workspace_ticket_bytes() {
 
 int check_paged(const da_params* p) { return check_params(p, false); }
 float base2_scale(const da_params* p) { return effective_qscale(p); }
-unsigned long long wait_limit() { return wait_limit_ns(); }
-int skip_first_arm() { return test_skip_arm(); }
 
 }  // namespace da
 

@@ -4,7 +4,8 @@
 // A decode step's calls take a few us on the GPU, and their marshalling in Python (attribute reads,
 // a ctypes structure, two torch.empty) takes longer on the host of a GB300.  us a call in a loop,
 // Python and here: norm and rotation of one token 20 and 7, the append of one 13 and 3, of 32 with
-// their queries 27 and 7, a shared-prefix decode of 2 sequences 29 and 12.  A call is
+// their queries 27 and 7, a shared-prefix decode of 2 sequences 29 and 12, a decode of 2 over a cache in 4
+// bits 29 and 11, the append of a token and its read-back 29 and 8, a gather of 333 tokens 16 and 5.  A call is
 // taken when everything is as the kernels need it: plain tensors of one device, the
 // current one, sizes that fit together, for the shared prefix no capture.  Anything
 // else is answered with NotImplemented, and the caller's checks in Python name what is wrong or do

@@ -15,11 +15,9 @@ int check_append_params(const da_params* p);
 int check_q4(const da_params* p, int group);
 
 // Validation of da_params as the paged decode entry points do it; the score scale in base-2
-// units; the tuning's time limit of a wait; the test hook (api.cu).
+// units (api.cu).
 int check_paged(const da_params* p);
 float base2_scale(const da_params* p);
-unsigned long long wait_limit();
-int skip_first_arm();
 
 // SM count of the current device (api.cu); a status.
 int device_sms(int* sms_out);

@@ -6,8 +6,8 @@
 // Code d of a row is nibble d % 2 of byte d / 2; a param is a word, f16 scale below f16 zero; a value is
 // scale * code + zero.  The 16-byte pieces (32 codes) of row t lie permuted, piece c at place
 // c ^ piece_xor<D>(t): eight neighbouring rows then have any one piece in eight different
-// 16-byte columns of shared memory's 128, and a record is copied there as it lies, by one bulk
-// copy, and read without bank conflicts.
+// 16-byte columns of shared memory's 128, and a record is copied there as it lies and read without
+// bank conflicts.
 #pragma once
 
 #include <stdint.h>

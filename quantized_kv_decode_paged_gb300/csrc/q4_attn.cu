@@ -19,18 +19,25 @@
 // to 2^14.  A weight times the value scale stays inside f16: the reference m of a row is
 // taken over s_t + e_t, e_t the exponent of the key's largest value scale, and p_t = 2^(s_t - m + 10), so
 // p_t scale_tg is at most 2^15 (m moves when some s_t + e_t passes it by 5), and lies 34 powers of two above
-// f16's smallest step at m.  mma.sync adds with truncation, so a sum takes at most kChain steps and is then
-// added up in f32.
+// f16's smallest step at m.  mma.sync adds with truncation, so a sum takes kChainKeys keys at most and is
+// then added up in f32.
 //
 // Work.  A unit is (sequence, kv head, up to 32 query rows: query tokens x heads of the kv head), a tile 16
-// to 64 of its keys (4 to 5 KB of codes, scales and zeros).  The tiles of all units stand in one row that is cut
+// to 64 of its keys (4 to 6 KB of codes, scales and zeros).  The tiles of all units stand in one row that is cut
 // into equal shares, one a warp (or one for the two or four warps that take a unit's groups of 8 rows): a
-// warp copies its tiles (a bulk copy a page of a head, which holds codes and scales of keys and values) into a
-// ring of its own, waits for them and works them off, and nothing of it waits for another warp.  32 keys (D =
-// 256: 16) x 8 rows at a time: S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16, keys and value columns as M,
-// so that 8 rows of Q fill N.  A unit that ends in another share than it began in leaves its parts'
-// states in the workspace; q4_merge_kernel adds them up.  The row order of the 16 keys (tau below) is such that the
-// fragments of K by ldmatrix and of V by its transposing byte form meet in one layout and no bank twice.
+// warp copies its tiles into a ring of its own, 16 bytes a lane at a time (codes and scales of keys and values
+// lie side by side in a page of a head), waits for them and works them off, and nothing of it waits for another
+// warp.  32 keys (D = 256: 16) x 8 rows at a time: S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16, keys
+// and value columns as M, so that 8 rows of Q fill N.  A unit that ends in another share than it began in
+// leaves its parts' states in the workspace; q4_merge_kernel adds them up.  The row order of the 16 keys (tau
+// below) is such that the fragments of K by ldmatrix and of V by its transposing byte form meet in one layout and
+// no bank twice.
+//
+// Measured (one GB300): 128 sequences of 2048 to 24,000 keys, 8 kv heads, 32 query heads, D = 128: 334 us for
+// 1.26 GB, 56% of the copy bandwidth.  The copies alone take 215 us, without any matrix product 272 us less 153:
+// the matrix products and what makes their operands share the issue slots and add up, the copies
+// hide for the most part.  Splitting by CTA with a common ring and producer warps took 515 us, by warp with
+// bulk copies 381 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -49,7 +56,9 @@ namespace {
 constexpr int kRows = 8;                // query rows of a warp
 constexpr int kMaxGroups = 4;           // groups of kRows rows of a unit
 constexpr int kMaxBatch = 1024;         // sequences of a launch
-constexpr int kChainKeys = 256;         // keys of a warp between f32 additions
+// Keys of a warp between f32 additions.  128 sequences of 2048 to 24,000 keys: 326 us and an error of 2.6e-6 with
+// 256, 328 and 1.7e-6 with 128, 334 and 1.3e-6 with 64, which is f32's own, 345 and 1.3e-6 with 32.
+constexpr int kChainKeys = 64;
 constexpr float kShift = 10.f, kSlack = 5.f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -103,7 +112,7 @@ __device__ __forceinline__ int seq_info(const Q4Params& p, int b, Seq& s) {
   s.len = (int)len;
   s.lo = (int)lo;
   s.hi = (int)hi;
-  s.qp = (int)(qp < 0x7fff0000 ? qp : 0x7fff0000);  // past every key and window alike
+  s.qp = (int)qp;
   s.tile0 = (int)(lo / TOK);
   s.tiles = hi > lo ? (int)((hi + TOK - 1) / TOK) - s.tile0 : 0;
   return flags;
@@ -112,7 +121,8 @@ __device__ __forceinline__ int seq_info(const Q4Params& p, int b, Seq& s) {
 // Keys [lo, hi) that query token t sees.
 __device__ __forceinline__ void row_keys(const Q4Params& p, const Seq& s, int t, int& lo, int& hi) {
   const long long qp = (long long)s.qp + t;
-  lo = p.window > 0 && qp >= p.window ? (int)(qp - p.window + 1) : 0;
+  const long long first = p.window > 0 && qp >= p.window ? qp - p.window + 1 : 0;
+  lo = (int)(first < 0x7fffffff ? first : 0x7fffffff);  // past every key
   hi = p.causal && qp + 1 < s.len ? (int)(qp + 1) : s.len;
   if (s.tiles == 0) hi = lo;
 }
@@ -511,7 +521,6 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
     row_keys(p, a.s, p.T - 1, all_lo, unused);
     row_keys(p, a.s, 0, unused, all_hi);
 
-
     float acc[MT][4] = {};
     float2 zero_sum[NG] = {}, l = {}, m = make_float2(-INFINITY, -INFINITY);
     // what has left acc lies in `state`, to be multiplied by `due`
@@ -551,13 +560,13 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
               float ah[H][4];
-                [[maybe_unused]] float al[H][4];
+              [[maybe_unused]] float al[H][4];
 #pragma unroll
               for (int i2 = n * GP; i2 < (n + 1) * GP; ++i2) {
 #pragma unroll
                 for (int o2 = 0; o2 < 2; ++o2) {
                   uint32_t q0, q1;
-                    [[maybe_unused]] uint32_t q2 = 0, q3 = 0;
+                  [[maybe_unused]] uint32_t q2 = 0, q3 = 0;
                   if constexpr (g_::QREG) {
                     q0 = qf[2 * i2 + o2][0], q1 = qf[2 * i2 + o2][1];
                     if constexpr (!PACK) q2 = qf[2 * i2 + o2][2], q3 = qf[2 * i2 + o2][3];
@@ -590,10 +599,11 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
                   const float sk = half_lo(kp[h][k][n]);
                   const float zk = fmaf(8.f, sk, half_hi(kp[h][k][n]));
                   float2 t = make_float2(ah[h][2 * k], ah[h][2 * k + 1]);
-if constexpr (PACK)
-  t = da::add2(t, make_float2(__shfl_xor_sync(0xffffffffu, t.x, 2), __shfl_xor_sync(0xffffffffu, t.y, 2)));
-else
-  t = da::add2(t, make_float2(al[h][2 * k], al[h][2 * k + 1]));
+                  if constexpr (PACK)
+                    t = da::add2(t, make_float2(__shfl_xor_sync(0xffffffffu, t.x, 2),
+                                                __shfl_xor_sync(0xffffffffu, t.y, 2)));
+                  else
+                    t = da::add2(t, make_float2(al[h][2 * k], al[h][2 * k + 1]));
                   if (n == 0) {
                     u[h][k] = make_float2(t.x * sk, t.y * sk);
                     z[h][k] = make_float2(zk * qs[n].x, zk * qs[n].y);
@@ -711,7 +721,7 @@ else
                   zero_sum[n].y = fmaf(x[h][k].y, zv, zero_sum[n].y);
                 }
                 da::split_half2(w.x, w.y, ph[h][k], pl[h][k]);
-                  if (PACK && c >= 2) ph[h][k] = pl[h][k];
+                if (PACK && c >= 2) ph[h][k] = pl[h][k];
                 ph[h][k] = da::movmatrix_trans(ph[h][k]);
                 if constexpr (!PACK) pl[h][k] = da::movmatrix_trans(pl[h][k]);
               }
@@ -729,11 +739,11 @@ else
                   fr[k][2] = codes2(a0 >> 8, k & 1), fr[k][3] = codes2(a1 >> 8, k & 1);
                   mma(acc[2 * i2 + k], fr[k][0], fr[k][1], fr[k][2], fr[k][3], ph[h][0], ph[h][1]);
                 }
-if constexpr (!PACK) {
+                if constexpr (!PACK) {
 #pragma unroll
-                for (int k = 0; k < 2 * PP; ++k)
-                  mma(acc[2 * i2 + k], fr[k][0], fr[k][1], fr[k][2], fr[k][3], pl[h][0], pl[h][1]);
-}
+                  for (int k = 0; k < 2 * PP; ++k)
+                    mma(acc[2 * i2 + k], fr[k][0], fr[k][1], fr[k][2], fr[k][3], pl[h][0], pl[h][1]);
+                }
               }
           }
         };

@@ -362,6 +362,18 @@ def test_query_positions(causal, T):
     c.check(flags=qk.DEV_BAD_QPOS)
 
 
+@pytest.mark.parametrize("T", [1, 4])
+def test_query_positions_up_to_the_last(T):
+    """Positions and windows whose sums pass 2^31: a window's first key is key 0, inside the
+    sequence, or past every key."""
+    far = 2 ** 31 - 1
+    c = Case(16, 8, 2, 64, 32, 16, [300, 200, 300, 77, 300], T=T)
+    c.q_pos = np.array([far, far - 1, far - 2, far - 150, 299], np.int32)
+    for window in (0, 1, 2, far - 150, far - 3, far):
+        c.kw = dict(sliding_window=window)
+        c.check()
+
+
 def test_bad_pages_and_lengths_are_masked_and_flagged():
     c = Case(9, 8, 2, 128, 64, 16, [300, 200, 100, 50])
     c.table[0, 3], c.table[1, 0], c.table[2, 6] = -1, c.cache.NB, 2 ** 31 - 1
@@ -647,6 +659,91 @@ def test_pool_past_four_giga_bytes():
 
 
 # ------------------------------------------------------------------ together
+def test_calls_behind_one_another():
+    """Append, read back and decode over and over without a wait between: each sees what
+    the one before it wrote (a kernel may be set up while the one before it still runs)."""
+    import torch
+    B, Hq, H, D, group, bs, steps = 40, 8, 2, 128, 32, 16, 30
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    x = torch.randn((steps, B, Hq + 2 * H, D), generator=g, device="cuda")
+    table = torch.randperm(4 * B, generator=g, device="cuda").int().view(B, 4)
+    shape = (4 * B, H, qk.decode_attn_q4_page_bytes(bs, D, group))
+    runs = []
+    for wait in (True, False):
+        pool = torch.zeros(shape, dtype=torch.uint8, device="cuda")
+        got = []
+        for i in range(steps):
+            pos = torch.full((B,), i, dtype=torch.int32, device="cuda")
+            lens = pos + 1
+            k, v = x[i, :, Hq:Hq + H], x[i, :, Hq + H:]
+            calls = (lambda: qk.decode_attn_append_paged_q4(k, v, pos, table, pool, group=group,
+                                                            q=x[i, :, :Hq]),
+                     lambda: qk.decode_attn_gather_paged_q4(pos, table, pool, head_dim=D, group=group),
+                     lambda: qk.decode_attn_paged_q4(got[-2], pool, table, lens, group=group))
+            for call in calls:
+                if wait:
+                    torch.cuda.synchronize()
+                got.append(call())
+        torch.cuda.synchronize()
+        runs.append([t for y in got for t in (y if isinstance(y, tuple) else (y,))])
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+@pytest.mark.parametrize("what", ["append", "gather"])
+def test_cache_calls_in_two_graphs(what):
+    """Captured on streams of their own, replayed in turn with new inputs in place."""
+    import torch
+    N, H, D, group, bs = 50, 3, 64, 64, 8
+    r = np.random.default_rng(91)
+    runs = []
+    for i in range(2):
+        x = torch.zeros((N, 2 * H, D), device="cuda")
+        pos = torch.zeros(N, dtype=torch.int32, device="cuda")
+        table = _t(r.permutation(N * 2).astype(np.int32).reshape(N, 2))
+        pool = torch.zeros((N * 2, H, qk.decode_attn_q4_page_bytes(bs, D, group)), dtype=torch.uint8,
+                           device="cuda")
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+
+        def call(x=x, pos=pos, table=table, pool=pool):
+            if what == "append":
+                return qk.decode_attn_append_paged_q4(x[:, :H], x[:, H:], pos, table, pool, group=group)
+            return qk.decode_attn_gather_paged_q4(pos, table, pool, head_dim=D, group=group)
+
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            call()
+            with torch.cuda.graph(g, stream=s):
+                out = call()
+        runs.append((x, pos, table, pool, s, g, out))
+    for _ in range(3):
+        for x, pos, table, pool, s, g, out in runs:
+            x.copy_(_t(r.standard_normal(x.shape).astype(np.float32)))
+            pos.copy_(_t(r.integers(0, 16, N).astype(np.int32)))
+            if what == "gather":
+                pool.copy_(_t(Cache(N * 2, H, bs, D, group).fill(r).bytes()))
+            else:
+                pool.zero_()
+        torch.cuda.synchronize()
+        for x, pos, table, pool, s, g, out in runs:
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for x, pos, table, pool, s, g, out in runs:
+            c = Cache.of_bytes(pool.cpu().numpy(), bs, D, group)
+            p, t = pos.cpu().numpy(), table.cpu().numpy()
+            for n in range(N):
+                at = (t[n, p[n] // bs], slice(None), p[n] % bs)
+                for j in range(2):
+                    if what == "append":
+                        want = quantised(_np(x)[n, j * H:(j + 1) * H], group)
+                        for a, b in zip((c.codes, c.scale, c.zero), want):
+                            assert np.array_equal(a[j][at], b)
+                    else:
+                        ref = c.values()[j][at]
+                        assert (np.abs(_np(out[j])[n] - ref) <= 2.0 ** -11 * np.abs(ref) + 2.0 ** -25).all()
+
+
 @pytest.mark.parametrize("T", [1, 3])
 def test_a_serving_run(T):
     """Prompts, then steps: lengths planned, tokens appended (keys and queries rotated), attended,
