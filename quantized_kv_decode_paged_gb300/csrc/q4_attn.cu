@@ -19,7 +19,7 @@
 // to 2^14.  A weight times the value scale stays inside f16: the reference m of a row is
 // taken over s_t + e_t, e_t the exponent of the key's largest value scale, and p_t = 2^(s_t - m + 10), so
 // p_t scale_tg is at most 2^15 (m moves when some s_t + e_t passes it by 5), and lies 34 powers of two above
-// f16's smallest step at m.  mma.sync adds with truncation, so a sum takes kChainKeys keys at most and is
+// f16's smallest step at m.  mma.sync adds with truncation, so a sum takes chain_keys keys at most and is
 // then added up in f32.
 //
 // Work.  A unit is (sequence, kv head, up to 32 query rows: query tokens x heads of the kv head), a tile 16
@@ -56,9 +56,11 @@ namespace {
 constexpr int kRows = 8;                // query rows of a warp
 constexpr int kMaxGroups = 4;           // groups of kRows rows of a unit
 constexpr int kMaxBatch = 1024;         // sequences of a launch
-// Keys of a warp between f32 additions.  128 sequences of 2048 to 24,000 keys: 326 us and an error of 2.6e-6 with
-// 256, 328 and 1.7e-6 with 128, 334 and 1.3e-6 with 64, which is f32's own, 345 and 1.3e-6 with 32.
-constexpr int kChainKeys = 64;
+// Keys of a warp between f32 additions.  With 8 rows a product, whose sums take both terms, 128 sequences of 2048
+// to 24,000 keys: 326 us and an error of 2.6e-6 with 256, 328 and 1.7e-6 with 128, 334 and 1.3e-6 with 64, which
+// is f32's own, 345 and 1.3e-6 with 32.  With 4 rows and a sum a term, 24 sequences of 20,000 to 40,000 keys: 172
+// us and 7.7e-7 with 256, 177 and 9e-7 with 64.
+constexpr int chain_keys(bool pack) { return pack ? 256 : 64; }
 constexpr float kShift = 10.f, kSlack = 5.f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
       __syncwarp();  // the stage is read
       if (++got == STAGES) got = 0;
       copy(a, n + STAGES);
-      if (++chain == kChainKeys / TOK && n + 1 < a.n) {
+      if (++chain == chain_keys(PACK) / TOK && n + 1 < a.n) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           float4 v = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
