@@ -11,7 +11,7 @@
 // sincospif; the quarter turns swap and negate what comes back.  (The whole angle rounded to
 // f32 is off by 2^-25 of half a turn, 9.4e-8, which the small one of sine and cosine shows.)
 //
-// A CTA takes up to kMaxTokens tokens: their rd/2 cosines and sines are computed once
+// A CTA takes up to max_tokens tokens: their rd/2 cosines and sines are computed once
 // into shared memory and serve all the tokens' heads.  D/16 threads take a row, each
 // two 8-value chunks that hold both halves of its 8 pairs: (8c, rd/2 + 8c) or, interleaved,
 // (16c, 16c + 8); the chunks past the rotated part pair up without rotation.
@@ -21,7 +21,7 @@
 // Measured (GB300): 16,381 tokens x (32 + 8) heads x 128 from bf16, 470 MB in 74 us, 6.3 TB/s (77.5 to
 // 78.3 us a call in a loop); an append of 12,287 tokens x 8 heads x 128 of keys and values, 101 MB in
 // 17.8 us a call over the same inputs, 21.6 over changing ones; 128 tokens x 72 heads 4.7 us a call in
-// a graph.  In 4 bits those 12,287 tokens take 37 us, bound by the instructions (extents of the groups, the
+// a graph.  In 4 bits those 12,287 tokens take 34 us, bound by the instructions (extents of the groups, the
 // codes): 67 MB.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,8 +47,11 @@ constexpr int kRopeThreads = 256;
 // measured 83 and 93-98 us against 79 on 16,381 tokens x 40 heads x 128).
 constexpr int kRopeCtas = 4;
 constexpr int kMaxTokens = 12;  // of a CTA
-// In 4 bits more registers are live: 12,287 tokens with their read-back 48 us with three CTAs, 52 with four
-// (which spill) and 53 with two.
+// In 4 bits a row takes twice as long, and a CTA's first loads (positions, pages) are better shared by many: those
+// 12,287 tokens 44 us with 28, 45 with 20 or 14, 48 with 12.
+constexpr int max_tokens(int mode) { return mode == kAppendQ4 ? 28 : kMaxTokens; }
+// In 4 bits more registers are live: 12,287 tokens with their read-back, 12 a CTA, 48 us with three CTAs, 52 with
+// four (which spill) and 53 with two.
 constexpr int rope_ctas(int mode) { return mode == kAppendQ4 ? 3 : kRopeCtas; }
 
 struct RopeArgs {
@@ -248,8 +251,8 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(MODE)) rope_kernel(con
   // cosine and sine of pairs 2j and 2j + 1 of chunk c at [j][c]: a row's threads read
   // neighbouring 16 bytes (in the order of the pairs, four of them met in one bank: 92 us against
   // 83 on the case above)
-  __shared__ float4 cs[kMaxTokens][4][TPR];
-  __shared__ long long place[kMaxTokens];     // append: row of the pool, or one of:
+  __shared__ float4 cs[max_tokens(MODE)][4][TPR];
+  __shared__ long long place[max_tokens(MODE)];     // append: row of the pool, or one of:
   constexpr long long kDropped = -1, kPadding = -2;
   // append in 4 bits: extents of the chunks of the rows in work
   __shared__ float4 extent[MODE == kAppendQ4 ? RPI : 1][D / 16];
@@ -452,7 +455,7 @@ int launch_rope(RopeArgs& a, const da_rope_params* r, int D, int num_tokens, voi
   const int st = da::device_sms(&sms);
   if (st != DA_OK) return st;
   const int wave = sms * rope_ctas(MODE);  // CTAs that run at once
-  const int waves = (num_tokens - 1) / (wave * kMaxTokens) + 1;
+  const int waves = (num_tokens - 1) / (wave * max_tokens(MODE)) + 1;
   a.tokens = (num_tokens - 1) / (wave * waves) + 1;
   const cudaError_t err =
       r->type == DA_TYPE_F32   ? launch_rope_t<float, MODE>(a, D, r->interleaved, s)
