@@ -65,7 +65,7 @@ struct RopeArgs {
   const int32_t* positions;
   int N, tokens;            // tokens; tokens of a CTA
   int heads;                // rows of a token: q, k and (append) v heads
-  uint64_t inv_heads;       // ceil(2^32 / heads): r / heads = r * inv_heads >> 32, r < 2^16
+  uint64_t inv_heads;       // ceil(2^32 / heads): r / heads = r * inv_heads >> 32, r < 2^20
   int Hq, Hk, Hkv, rd, norm;  // Hq, Hk: 0 where q or k is not given
   float eps, woff;
   float* q_out;
@@ -80,7 +80,7 @@ struct RopeArgs {
   int32_t* dev_status;
   // append in 4 bits
   uint8_t* q4_pool;
-  int log2_bs, group;
+  int log2_bs, log2_group;
   long long page_bytes;
 };
 
@@ -212,8 +212,9 @@ __device__ __forceinline__ Q4Param q4_param(float2 e) {
 }
 
 // Eight codes: round((x - zero) / scale), ties to even, within 0..15; 0 without a scale.  The quotient by
-// the reciprocal is off by 16 * 2^-21 at most, so it says the code of any value that is not that near to the
-// middle between two; where one is (a value in 5000), the eight are divided.  (Divided always, 12,287 tokens
+// the reciprocal (good to 2^-22, its product to 2^-24) is off from the rounded one by 15.5 * 1.5 * 2^-22 at most, 6e-6, so
+// it says the code of any value that is not that near to the middle between two; where one is (a value in
+// 50,000), the eight are divided.  (Divided always, 12,287 tokens
 // x 16 rows x 128 took 58 us.)
 __device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], const Q4Param& p) {
   if (!(p.scale > 0.f)) return 0;
@@ -232,7 +233,7 @@ __device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], const Q4Param&
   }
   // the numbers' upper bits, 0x4b400000, in every one of the eight places
   w -= 0x4b400000u * 0x11111111u;
-  if (far > 0.5f - 1e-4f) {
+  if (far > 0.5f - 1e-5f) {
     w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -277,9 +278,10 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(MODE)) rope_kernel(con
     x.kind = x.h < a.Hq ? 0 : x.h < a.Hq + a.Hk ? 1 : 2;
     x.h -= x.kind == 0 ? 0 : x.kind == 1 ? a.Hq : a.Hq + a.Hk;
     const long long n = n0 + x.t;
-    const T* src = x.kind == 0   ? static_cast<const T*>(a.q) + n * a.q_ts + x.h * a.q_hs
-                   : x.kind == 1 ? static_cast<const T*>(a.k) + n * a.k_ts + x.h * a.k_hs
-                                 : static_cast<const T*>(a.v) + n * a.v_ts + x.h * a.v_hs;
+    const void* from = x.kind == 0 ? a.q : x.kind == 1 ? a.k : a.v;
+    const long long ts = x.kind == 0 ? a.q_ts : x.kind == 1 ? a.k_ts : a.v_ts;
+    const long long hs = x.kind == 0 ? a.q_hs : x.kind == 1 ? a.k_hs : a.v_hs;
+    const T* src = static_cast<const T*>(from) + n * ts + x.h * hs;
     x.lo = load8(src + lo);
     x.hi = load8(src + hi);
     return x;
@@ -304,7 +306,10 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(MODE)) rope_kernel(con
       int flag;
       bool pad;
       const long long row = cache_row(a, n0 + threadIdx.x, flag, pad);
-      place[threadIdx.x] = pad ? kPadding : flag ? kDropped : row;
+      long long at = row;
+      if constexpr (MODE == kAppendQ4)  // its page's first byte, and its row there
+        at = ((row >> a.log2_bs) * a.Hkv * a.page_bytes) << 8 | (row & (a.bs - 1));
+      place[threadIdx.x] = pad ? kPadding : flag ? kDropped : at;
       if (flag && a.dev_status) atomicOr(a.dev_status, flag);
     }
   }
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(MODE)) rope_kernel(con
         const float2 e = extent8(x[1]);
         if (side_by_side) {
           own = make_float2(min_nan(own.x, e.x), max_nan(own.y, e.y));
-          for (int by = 1; by < a.group / 16; by <<= 1)
+          for (int by = 1; by < 1 << (a.log2_group - 4); by <<= 1)
             own = make_float2(min_nan(own.x, __shfl_xor_sync(0xffffffffu, own.x, by)),
                               max_nan(own.y, __shfl_xor_sync(0xffffffffu, own.y, by)));
         } else {
@@ -380,17 +385,17 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(MODE)) rope_kernel(con
       uint8_t* page = nullptr;
       int t = 0, words = 0;
       if (kept) {
-        t = (int)(row & (a.bs - 1));
-        page = a.q4_pool + ((row >> a.log2_bs) * a.Hkv + cur.h) * a.page_bytes;
-        words = D / a.group;  // params of a row
+        t = (int)(row & 255);
+        page = a.q4_pool + (row >> 8) + cur.h * (int)a.page_bytes;
+        words = D >> a.log2_group;  // params of a row
       }
       Q4Param p;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int d = half ? hi : lo, g = d & -a.group;
+        const int d = half ? hi : lo, g = d & -(1 << a.log2_group);
         if (!side_by_side) {
           float2 e = make_float2(INFINITY, -INFINITY);
-          for (int i = 0; i < a.group / 16; ++i) {
+          for (int i = 0; i < 1 << (a.log2_group - 4); ++i) {
             const float4 two = extent[threadIdx.x / TPR][g / 16 + i];
             e = make_float2(min_nan(e.x, min_nan(two.x, two.z)), max_nan(e.y, max_nan(two.y, two.w)));
           }
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(MODE)) rope_kernel(con
         *reinterpret_cast<uint32_t*>(codes + 16 * piece + d % 32 / 2) = q4_codes(x[half], p);
         if (d == g)
           reinterpret_cast<uint32_t*>(page + a.bs * D)[((cur.kind == 2 ? a.bs : 0) + t) * words +
-                                                       g / a.group] = p.word;
+                                                       (g >> a.log2_group)] = p.word;
       }
       if (cur.kind != 0 || r >= rows) continue;
     }
@@ -636,7 +641,7 @@ int decode_attn_append_paged_q4(const da_params* p, const da_rope_params* r, int
                    dev_status, pool, pool);
   if (st != DA_OK || num_tokens == 0) return st;
   a.q4_pool = pool;
-  a.group = group;
+  while ((1 << a.log2_group) < group) ++a.log2_group;
   while ((1 << a.log2_bs) < p->block_size) ++a.log2_bs;
   a.page_bytes = da::q4_page_bytes(p->block_size, p->head_dim, group);
   return launch_rope<kAppendQ4>(a, r, p->head_dim, num_tokens, stream);
