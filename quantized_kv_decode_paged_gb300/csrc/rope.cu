@@ -21,8 +21,8 @@
 // Measured (GB300): 16,381 tokens x (32 + 8) heads x 128 from bf16, 470 MB in 74 us, 6.3 TB/s (77.5 to
 // 78.3 us a call in a loop); an append of 12,287 tokens x 8 heads x 128 of keys and values, 101 MB in
 // 17.8 us a call over the same inputs, 21.6 over changing ones; 128 tokens x 72 heads 4.7 us a call in
-// a graph.  In 4 bits those 12,287 tokens take 34 us, bound by the instructions (extents of the groups, the
-// codes): 67 MB.
+// a graph.  In 4 bits those 12,287 tokens take 31 us with cold caches, bound by the instructions (extents of
+// the groups, codes): 64 MB.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -50,8 +50,8 @@ constexpr int kMaxTokens = 12;  // of a CTA
 // In 4 bits a row takes twice as long, and a CTA's first loads (positions, pages) are better shared by many: those
 // 12,287 tokens 44 us with 28, 45 with 20 or 14, 48 with 12.
 constexpr int max_tokens(int mode) { return mode == kAppendQ4 ? 28 : kMaxTokens; }
-// In 4 bits more registers are live: 12,287 tokens with their read-back, 12 a CTA, 48 us with three CTAs, 52 with
-// four (which spill) and 53 with two.
+// In 4 bits more registers are live: 12,287 tokens x 8 heads x 128 with their read-back 40 us with three CTAs, 47
+// with four (which spill) and 44 with two.
 constexpr int rope_ctas(int mode) { return mode == kAppendQ4 ? 3 : kRopeCtas; }
 
 struct RopeArgs {
@@ -215,7 +215,7 @@ __device__ __forceinline__ Q4Param q4_param(float2 e) {
 // the reciprocal (good to 2^-22, its product to 2^-24) is off from the rounded one by 15.5 * 1.5 * 2^-22 at most, 6e-6, so
 // it says the code of any value that is not that near to the middle between two; where one is (a value in
 // 50,000), the eight are divided.  (Divided always, 12,287 tokens
-// x 16 rows x 128 took 58 us.)
+// x 16 rows x 128 took 58 us, where this took 39.)
 __device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], const Q4Param& p) {
   if (!(p.scale > 0.f)) return 0;
   // 1.5 * 2^23: added to a small number, its last bits are the number's nearest integer
