@@ -343,6 +343,20 @@ def test_sliding_windows(D, window, T):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,Hq,H", [(2, 2, 1), (4, 2, 2), (17, 4, 2), (40, 1, 1)])
+@pytest.mark.parametrize("window", [1, 5, 40])
+def test_query_tokens_behind_windows(D, T, Hq, H, window):
+    """Rows of a unit that see different keys, some none of a tile that others see."""
+    c = Case(17, Hq, H, D, 32, 8, [300, 3, 41, 0, T], T=T)
+    c.kw = dict(sliding_window=window)
+    c.check()
+    c.q_pos = np.array([350, 0, 20, 5, 10 ** 6], np.int32)
+    for causal in (True, False):
+        c.kw = dict(sliding_window=window, causal=causal)
+        c.check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("softcap,scale,q_scale", [(50.0, 0.0, 1.0), (2.0, 0.0, 4.0), (30.0, 1.0, 3.0),
                                                    (0.0, 0.3, 1.0), (1e-3, 0.0, 1.0)])
 def test_softcap_and_scale(D, softcap, scale, q_scale):
