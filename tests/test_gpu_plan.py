@@ -247,6 +247,35 @@ def test_outputs_streams_and_graph_replay():
         old = new
 
 
+def test_a_large_call_in_a_graph():
+    """A cluster's launch, captured and replayed: there and back, many times."""
+    import torch
+    r = np.random.default_rng(7)
+    B, bs, mb, NB = 1500, 16, 10, 9000
+    old, new = r.integers(0, 80, B), r.integers(0, 80, B)
+    table, free, count = _state(r, old, bs, mb, NB)
+    N = 40000
+    want = plan(old, new, table, free, count, bs, NB, N)
+    assert want[0] == 0
+    tt, tf, tc = _t(table), _t(free), _t(np.array([count], np.int32))
+    told, tnew = _t(old.astype(np.int32)), _t(new.astype(np.int32))
+    kw = dict(block_size=bs, num_blocks=NB, max_tokens=N)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(g, stream=s):
+            outs = qk.decode_attn_plan_blocks(told, tnew, tt, tf, tc, **kw)
+            kept = [t.clone() for t in (tt, tf, tc)]
+            qk.decode_attn_plan_blocks(tnew, told, tt, tf, tc, **kw)
+        for _ in range(5):
+            g.replay()
+    torch.cuda.synchronize()
+    _same((0, kept[0].cpu().numpy(), kept[1].cpu().numpy(), int(kept[2].item()),
+           *[o.cpu().numpy() for o in outs]), want)
+    assert np.array_equal(tt.cpu().numpy(), table) and int(tc.item()) == count
+    assert np.array_equal(tf.cpu().numpy()[:count], free[:count])
+
+
 def test_no_requests_and_no_tokens():
     import torch
     z = torch.zeros(0, dtype=torch.int32, device="cuda")
