@@ -568,7 +568,7 @@ int decode_attn_gather_paged_q4(const da_params* p, int32_t group, int32_t num_t
  * Everything else as for decode_attn_paged.  DA_ERR_UNSUPPORTED also where one
  * sequence's query rows (q_len * num_q_heads) or key tiles
  *   (max_blocks_per_seq * block_size * head_dim / 4096 + 2) * num_kv_heads *
- *   ceil(q_len * num_q_heads / num_kv_heads / 8)
+ *   ceil(q_len * num_q_heads / num_kv_heads / 32)
  * would not count in 31 bits, or a page's records of all kv heads not in 32 bits
  * of bytes.
  */

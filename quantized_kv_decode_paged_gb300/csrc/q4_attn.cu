@@ -22,9 +22,9 @@
 // f16's smallest step at m.  mma.sync adds with truncation, so a sum takes chain_keys keys at most and is
 // then added up in f32.
 //
-// Work.  A unit is (sequence, kv head, up to 32 query rows: query tokens x heads of the kv head), a tile 16
+// Work.  A unit is (sequence, kv head, up to 64 query rows: query tokens x heads of the kv head), a tile 16
 // to 64 of its keys (4 to 6 KB of codes, scales and zeros).  The tiles of all units stand in one row that is cut
-// into equal shares, one a warp (or one for the two or four warps that take a unit's groups of 8 rows): a
+// into equal shares, one a warp (or one for the two or four warps that take a unit's rows, 8 or 16 each): a
 // warp copies its tiles into a ring of its own, 16 bytes a lane at a time (codes and scales of keys and values
 // lie side by side in a page of a head), waits for them and works them off, and nothing of it waits for another
 // warp.  32 keys (D = 256: 16) x 8 rows at a time: S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16, keys
@@ -53,8 +53,8 @@
 
 namespace {
 
-constexpr int kRows = 8;                // query rows of a warp
-constexpr int kMaxGroups = 4;           // groups of kRows rows of a unit
+constexpr int kRows = 8;                // query rows of a group: N of a product
+constexpr int kMaxWarps = 4;            // warps of a unit
 constexpr int kMaxBatch = 1024;         // sequences of a launch
 // Keys of a warp between f32 additions.  With 8 rows a product, whose sums take both terms, 128 sequences of 2048
 // to 24,000 keys: 326 us and an error of 2.6e-6 with 256, 328 and 1.7e-6 with 128, 334 and 1.3e-6 with 64, which
@@ -74,7 +74,8 @@ struct Q4Params {
   float* lse;
   int32_t* dev_status;
   int B, T, G, R, Hq, Hkv, log2_bs, max_blocks, num_blocks, window, causal;
-  int groups, blocks;  // row groups of a unit (a power of two), units of a kv head
+  int warps, blocks;   // warps of a unit (a power of two), units of a kv head
+  int unit_rows;       // query rows of a unit
   int log2_eb;         // rows of a page's piece in a tile, min(block size, tile)
   int shares;          // of the launch
   float qscale, softcap2, softcap_inv;
@@ -82,8 +83,8 @@ struct Q4Params {
   uint32_t stride;     // bytes from a page to the next: below 2^32
   // workspace
   int* pre;         // [B + 1] tiles of the sequences before each
-  float2* part_ml;  // [shares][2][groups * 8]: reference and sum
-  float* part_o;    // [shares][2][groups * 8][D]
+  float2* part_ml;  // [shares][2][unit_rows]: reference and sum
+  float* part_o;    // [shares][2][unit_rows][D]
 };
 
 // ------------------------------------------------------------------ what a sequence sees
@@ -225,23 +226,25 @@ __device__ __forceinline__ void load_params(uint32_t at, uint32_t (&w)[NG]) {
   }
 }
 
-template <int D, int NG>
+// ROWS: query rows of a warp, 4, 8 or 16.
+template <int D, int NG, int ROWS>
 struct Geo {
+  static constexpr int RG = ROWS == 16 ? 2 : 1;  // groups of kRows rows
+  static constexpr bool BIG = D == 256 || (D == 128 && RG == 2);  // sums fill the registers
   static constexpr int P = D / 32;         // 16-byte pieces of a row
   static constexpr int GP = P / NG;        // pieces of a group
   static constexpr int RB = D / 2;         // bytes of a row's codes
   static constexpr int ROW = D + 8 * NG;   // bytes of a key's and a value's row
   static constexpr int TOK = 4096 / D;     // keys of a tile
   static constexpr int LOG2_TOK = D == 64 ? 6 : D == 128 ? 5 : 4;
-  static constexpr int H = D == 256 ? 1 : 2;  // MMA tiles of 16 keys that are worked off together
+  static constexpr int H = BIG ? 1 : 2;    // MMA tiles of 16 keys that are worked off together
   static constexpr int STAGE = TOK * ROW;  // codes of keys, of values, params of keys, of values
   static constexpr int CODES = TOK * RB;
-  // D = 256 has twice the accumulators, and states of twice the size
-  static constexpr int WARPS = D == 256 ? 8 : 12;
+  static constexpr int WARPS = BIG ? 8 : 12;
   static constexpr int THREADS = 32 * WARPS;
-  static constexpr bool QREG = D <= 128;   // Q's fragments in registers, else in shared memory
-  static constexpr int STATE = kRows * D * 4;  // sums of a warp in shared memory
-  static constexpr int QBYTES = QREG ? 0 : P * 2 * 512;
+  static constexpr bool QREG = !BIG;       // Q's fragments in registers, else in shared memory
+  static constexpr int STATE = RG * kRows * D * 4;  // sums of a warp in shared memory
+  static constexpr int QBYTES = QREG ? 0 : RG * P * 2 * 512;
   static constexpr int kMost = 227 * 1024 - 2048;  // dynamic shared memory, Shared beside it
   static constexpr int FIT = (kMost - (kMaxBatch + 1) * 4) / WARPS - STATE - QBYTES;
   static constexpr int STAGES = FIT / STAGE < 4 ? FIT / STAGE : 4;  // of a warp's ring
@@ -255,12 +258,15 @@ struct Shared {
   int warp_sum[WARPS];
 };
 
-// PACK: at most four query rows a unit, whose two terms share one MMA operand: rows 0 to 3 of N are the first
-// terms, 4 to 7 the second ones, so that half the MMAs do.
-template <int D, int NG, bool PACK>
-__global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
+// ROWS 4 (PACK): at most four query rows a unit, whose two terms share one MMA operand: rows 0 to 3 of N are the first
+// terms, 4 to 7 the second ones, so that half the MMAs do.  ROWS 16: two groups of
+// rows share the operands that are made of the codes.
+template <int D, int NG, int ROWS>
+__global__ void __launch_bounds__(Geo<D, NG, ROWS>::THREADS, 1)
     q4_kernel(const __grid_constant__ Q4Params p) {
-  using g_ = Geo<D, NG>;
+  using g_ = Geo<D, NG, ROWS>;
+  constexpr bool PACK = ROWS == 4;
+  constexpr int RG = g_::RG, WROWS = RG * kRows;  // rows of a warp, of which PACK uses four
   constexpr int P = g_::P, GP = g_::GP, RB = g_::RB, MT = 2 * P, H = g_::H, TOK = g_::TOK;
   constexpr int STAGES = g_::STAGES;
   extern __shared__ __align__(1024) uint8_t dyn[];
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
     __syncthreads();
   }
   // From here on a warp is by itself.  Its row group of the units, its share of the tiles.
-  const int slots = g_::WARPS / p.groups, rg = warp / slots;
+  const int slots = g_::WARPS / p.warps, rg = warp / slots;
   const int share = blockIdx.x * slots + (warp - rg * slots);
   const Shares shares(total * upb, p.shares);
   if (share >= shares.n) return;
@@ -441,23 +447,25 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
 
   Part a;
   while (next_part(a)) {
-    const int row0 = (a.block * p.groups + rg) * kRows;  // first query row of the warp
-    // ------------------------------------------------ Q: row g, dims 32 p + 8 c ..
-    float x[P][8];
-    {
-      const int r = row0 + (PACK ? g & 3 : g);
+    const int row0 = (a.block * p.warps + rg) * WROWS;  // first query row of the warp
+    // ------------------------------------------------ Q: row g of a group, dims 32 p + 8 c ..
+    float x[RG][P][8];
+#pragma unroll
+    for (int gr = 0; gr < RG; ++gr) {
+      const int r = row0 + kRows * gr + (PACK ? g & 3 : g);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
+        float (&y)[8] = x[gr][i];
         if (r < p.R) {
           const int t = r / p.G, h = a.kv * p.G + (r - t * p.G);
           const float4* src = reinterpret_cast<const float4*>(
               p.q + (((long long)a.b * p.T + t) * p.Hq + h) * D + 32 * i + 8 * c);
           const float4 y0 = src[0], y1 = src[1];
-          x[i][0] = y0.x, x[i][1] = y0.y, x[i][2] = y0.z, x[i][3] = y0.w;
-          x[i][4] = y1.x, x[i][5] = y1.y, x[i][6] = y1.z, x[i][7] = y1.w;
+          y[0] = y0.x, y[1] = y0.y, y[2] = y0.z, y[3] = y0.w;
+          y[4] = y1.x, y[5] = y1.y, y[6] = y1.z, y[7] = y1.w;
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+          for (int j = 0; j < 8; ++j) y[j] = 0.f;
         }
       }
     }
@@ -465,15 +473,16 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
 #pragma unroll 1
     for (int n = 0; n < STAGES; ++n) copy(a, n);
     constexpr int QW = PACK ? 2 : 4;  // words of a fragment: k = 2c.. and 2c + 8.. of the first term, the second
-    uint32_t qf[g_::QREG ? P * 2 : 1][QW];
-    float2 f, qs[NG];  // factors and group sums of the lane's columns
-    int lo[2], hi[2];
-    {
+    uint32_t qf[g_::QREG ? RG * P * 2 : 1][QW];
+    float2 f[RG], qs[RG][NG];  // factors and group sums of the lane's columns
+    int lo[RG][2], hi[RG][2];
+#pragma unroll
+    for (int gr = 0; gr < RG; ++gr) {
       float most = 0.f;
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) most = max_nan(most, fabsf(x[i][j]));
+        for (int j = 0; j < 8; ++j) most = max_nan(most, fabsf(x[gr][i][j]));
       most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 2));
       const bool finite = most < INFINITY;
@@ -486,24 +495,26 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
       float sum[NG] = {};
 #pragma unroll
       for (int i = 0; i < P; ++i) {
+        float (&y)[8] = x[gr][i];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          x[i][j] = finite ? x[i][j] * up : 0.f;
-          sum[i / GP] += x[i][j];
+          y[j] = finite ? y[j] * up : 0.f;
+          sum[i / GP] += y[j];
         }
 #pragma unroll
         for (int o = 0; o < 2; ++o) {  // low nibbles of a byte, high ones
           uint4 w;
-          da::split_half2(x[i][o], x[i][o + 4], w.x, w.z);
-          da::split_half2(x[i][o + 2], x[i][o + 6], w.y, w.w);
+          da::split_half2(y[o], y[o + 4], w.x, w.z);
+          da::split_half2(y[o + 2], y[o + 6], w.y, w.w);
           if (PACK && g >= 4) w.x = w.z, w.y = w.w;
+          const int at = gr * P * 2 + 2 * i + o;
           if constexpr (g_::QREG) {
-            qf[2 * i + o][0] = w.x, qf[2 * i + o][1] = w.y;
-            if constexpr (!PACK) qf[2 * i + o][2] = w.z, qf[2 * i + o][3] = w.w;
+            qf[at][0] = w.x, qf[at][1] = w.y;
+            if constexpr (!PACK) qf[at][2] = w.z, qf[at][3] = w.w;
           } else if constexpr (PACK) {
-            reinterpret_cast<uint2*>(qfrag)[(2 * i + o) * 32 + lane] = make_uint2(w.x, w.y);
+            reinterpret_cast<uint2*>(qfrag)[at * 32 + lane] = make_uint2(w.x, w.y);
           } else {
-            qfrag[(2 * i + o) * 32 + lane] = w;  // warps of the same rows write the same
+            qfrag[at * 32 + lane] = w;  // warps of the same rows write the same
           }
         }
       }
@@ -512,27 +523,31 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
         sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 1);
         sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 2);
       }
-      f.x = __shfl_sync(0xffffffffu, back, 4 * col);
-      f.y = __shfl_sync(0xffffffffu, back, 4 * col + 4);
+      f[gr].x = __shfl_sync(0xffffffffu, back, 4 * col);
+      f[gr].y = __shfl_sync(0xffffffffu, back, 4 * col + 4);
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        qs[n].x = __shfl_sync(0xffffffffu, sum[n], 4 * col) * f.x;
-        qs[n].y = __shfl_sync(0xffffffffu, sum[n], 4 * col + 4) * f.y;
+        qs[gr][n].x = __shfl_sync(0xffffffffu, sum[n], 4 * col) * f[gr].x;
+        qs[gr][n].y = __shfl_sync(0xffffffffu, sum[n], 4 * col + 4) * f[gr].y;
       }
-      f.x *= 0x1p9f, f.y *= 0x1p9f;  // the codes come times 2^-9
+      f[gr].x *= 0x1p9f, f[gr].y *= 0x1p9f;  // the codes come times 2^-9
 #pragma unroll
-      for (int j = 0; j < 2; ++j) row_keys(p, a.s, (row0 + col + j) / p.G, lo[j], hi[j]);
-      __syncwarp();
+      for (int j = 0; j < 2; ++j)
+        row_keys(p, a.s, (row0 + kRows * gr + col + j) / p.G, lo[gr][j], hi[gr][j]);
     }
+    __syncwarp();
     // keys that every row sees
     int all_lo, all_hi, unused;
     row_keys(p, a.s, p.T - 1, all_lo, unused);
     row_keys(p, a.s, 0, unused, all_hi);
 
-    float acc[MT][4] = {};
-    float2 zero_sum[NG] = {}, l = {}, m = make_float2(-INFINITY, -INFINITY);
-    // what has left acc lies in `state`, to be multiplied by `due`
-    float2 due = make_float2(1.f, 1.f);
+    float acc[RG][MT][4] = {};
+    float2 zero_sum[RG][NG] = {}, l[RG] = {}, m[RG], due[RG];
+#pragma unroll
+    for (int gr = 0; gr < RG; ++gr) {
+      m[gr] = make_float2(-INFINITY, -INFINITY);
+      due[gr] = make_float2(1.f, 1.f);  // what has left acc lies in `state`, to be multiplied by this
+    }
     bool kept = false;
     int chain = 0;
     for (int n = 0; n < a.n; ++n) {
@@ -562,40 +577,47 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
             load_params<NG>(par + (TOK + 16 * h + key_b) * 4 * NG, vp[h][1]);
           }
           // -------------------------------------------- scores
-          float2 x[H][2];  // of keys a and b; columns 2c, 2c + 1
+          float2 x[RG][H][2];  // of keys a and b; columns 2c, 2c + 1
           {
-            float2 u[H][2], z[H][2];
+            float2 u[RG][H][2], z[RG][H][2];
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-              float ah[H][4];
-              [[maybe_unused]] float al[H][4];
+              float ah[RG][H][4];
+              [[maybe_unused]] float al[RG][H][4];
 #pragma unroll
               for (int i2 = n * GP; i2 < (n + 1) * GP; ++i2) {
 #pragma unroll
                 for (int o2 = 0; o2 < 2; ++o2) {
-                  uint32_t q0, q1;
-                  [[maybe_unused]] uint32_t q2 = 0, q3 = 0;
-                  if constexpr (g_::QREG) {
-                    q0 = qf[2 * i2 + o2][0], q1 = qf[2 * i2 + o2][1];
-                    if constexpr (!PACK) q2 = qf[2 * i2 + o2][2], q3 = qf[2 * i2 + o2][3];
-                  } else if constexpr (PACK) {
-                    const uint2 w = reinterpret_cast<const uint2*>(qfrag)[(2 * i2 + o2) * 32 + lane];
-                    q0 = w.x, q1 = w.y;
-                  } else {
-                    const uint4 w = qfrag[(2 * i2 + o2) * 32 + lane];
-                    q0 = w.x, q1 = w.y, q2 = w.z, q3 = w.w;
+                  uint32_t q[RG][4];
+#pragma unroll
+                  for (int gr = 0; gr < RG; ++gr) {
+                    const int at = gr * P * 2 + 2 * i2 + o2;
+                    q[gr][2] = q[gr][3] = 0;
+                    if constexpr (g_::QREG) {
+                      q[gr][0] = qf[at][0], q[gr][1] = qf[at][1];
+                      if constexpr (!PACK) q[gr][2] = qf[at][2], q[gr][3] = qf[at][3];
+                    } else if constexpr (PACK) {
+                      const uint2 w = reinterpret_cast<const uint2*>(qfrag)[at * 32 + lane];
+                      q[gr][0] = w.x, q[gr][1] = w.y;
+                    } else {
+                      const uint4 w = qfrag[at * 32 + lane];
+                      q[gr][0] = w.x, q[gr][1] = w.y, q[gr][2] = w.z, q[gr][3] = w.w;
+                    }
                   }
 #pragma unroll
                   for (int h = 0; h < H; ++h) {
                     const uint32_t a0 = kw[h][i2][0], a1 = kw[h][i2][1];
                     const uint32_t f0 = codes2(a0, o2), f1 = codes2(a1, o2);
                     const uint32_t f2 = codes2(a0 >> 8, o2), f3 = codes2(a1 >> 8, o2);
-                    if (i2 == n * GP && o2 == 0) {
-                      mma_first(ah[h], f0, f1, f2, f3, q0, q1);
-                      if constexpr (!PACK) mma_first(al[h], f0, f1, f2, f3, q2, q3);
-                    } else {
-                      mma(ah[h], f0, f1, f2, f3, q0, q1);
-                      if constexpr (!PACK) mma(al[h], f0, f1, f2, f3, q2, q3);
+#pragma unroll
+                    for (int gr = 0; gr < RG; ++gr) {
+                      if (i2 == n * GP && o2 == 0) {
+                        mma_first(ah[gr][h], f0, f1, f2, f3, q[gr][0], q[gr][1]);
+                        if constexpr (!PACK) mma_first(al[gr][h], f0, f1, f2, f3, q[gr][2], q[gr][3]);
+                      } else {
+                        mma(ah[gr][h], f0, f1, f2, f3, q[gr][0], q[gr][1]);
+                        if constexpr (!PACK) mma(al[gr][h], f0, f1, f2, f3, q[gr][2], q[gr][3]);
+                      }
                     }
                   }
                 }
@@ -606,26 +628,31 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
                 for (int k = 0; k < 2; ++k) {
                   const float sk = half_lo(kp[h][k][n]);
                   const float zk = fmaf(8.f, sk, half_hi(kp[h][k][n]));
-                  float2 t = make_float2(ah[h][2 * k], ah[h][2 * k + 1]);
-                  if constexpr (PACK)
-                    t = da::add2(t, make_float2(__shfl_xor_sync(0xffffffffu, t.x, 2),
-                                                __shfl_xor_sync(0xffffffffu, t.y, 2)));
-                  else
-                    t = da::add2(t, make_float2(al[h][2 * k], al[h][2 * k + 1]));
-                  if (n == 0) {
-                    u[h][k] = make_float2(t.x * sk, t.y * sk);
-                    z[h][k] = make_float2(zk * qs[n].x, zk * qs[n].y);
-                  } else {
-                    u[h][k] = make_float2(fmaf(t.x, sk, u[h][k].x), fmaf(t.y, sk, u[h][k].y));
-                    z[h][k] = make_float2(fmaf(zk, qs[n].x, z[h][k].x),
-                                          fmaf(zk, qs[n].y, z[h][k].y));
+#pragma unroll
+                  for (int gr = 0; gr < RG; ++gr) {
+                    float2 t = make_float2(ah[gr][h][2 * k], ah[gr][h][2 * k + 1]);
+                    if constexpr (PACK)
+                      t = da::add2(t, make_float2(__shfl_xor_sync(0xffffffffu, t.x, 2),
+                                                  __shfl_xor_sync(0xffffffffu, t.y, 2)));
+                    else
+                      t = da::add2(t, make_float2(al[gr][h][2 * k], al[gr][h][2 * k + 1]));
+                    float2 &uu = u[gr][h][k], &zz = z[gr][h][k];
+                    if (n == 0) {
+                      uu = make_float2(t.x * sk, t.y * sk);
+                      zz = make_float2(zk * qs[gr][n].x, zk * qs[gr][n].y);
+                    } else {
+                      uu = make_float2(fmaf(t.x, sk, uu.x), fmaf(t.y, sk, uu.y));
+                      zz = make_float2(fmaf(zk, qs[gr][n].x, zz.x), fmaf(zk, qs[gr][n].y, zz.y));
+                    }
                   }
                 }
             }
 #pragma unroll
-            for (int h = 0; h < H; ++h)
+            for (int gr = 0; gr < RG; ++gr)
 #pragma unroll
-              for (int k = 0; k < 2; ++k) x[h][k] = da::fma2(u[h][k], f, z[h][k]);
+              for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) x[gr][h][k] = da::fma2(u[gr][h][k], f[gr], z[gr][h][k]);
           }
           uint32_t vw[H][P][2];
 #pragma unroll
@@ -636,28 +663,35 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
                                    vw[h][2 * i2][1], vw[h][2 * i2 + 1][0], vw[h][2 * i2 + 1][1]);
           if (p.softcap2 > 0.f) {
 #pragma unroll
-            for (int h = 0; h < H; ++h)
+            for (int gr = 0; gr < RG; ++gr)
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                x[h][k].x = soft_cap(x[h][k].x * p.softcap_inv, p.softcap2);
-                x[h][k].y = soft_cap(x[h][k].y * p.softcap_inv, p.softcap2);
-              }
+              for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  float2& y = x[gr][h][k];
+                  y.x = soft_cap(y.x * p.softcap_inv, p.softcap2);
+                  y.y = soft_cap(y.y * p.softcap_inv, p.softcap2);
+                }
           }
           // -------------------------------------------- masks
-          uint32_t seen = 0;
+          uint32_t seen[RG] = {};
           if constexpr (PART) {
 #pragma unroll
-            for (int j = 0; j < 4 * H; ++j) {
-              const int t = 16 * (j / 4) + (j % 4 < 2 ? key_a : key_b), k = key0 + t;
-              float2& y = x[j / 4][j % 4 / 2];
-              if (k >= lo[j & 1] && k < hi[j & 1] && !(bad >> ((tok + t) >> p.log2_eb) & 1))
-                seen |= 1u << j;
-              else
-                (j & 1 ? y.y : y.x) = -INFINITY;
-            }
+            for (int gr = 0; gr < RG; ++gr)
+#pragma unroll
+              for (int j = 0; j < 4 * H; ++j) {
+                const int t = 16 * (j / 4) + (j % 4 < 2 ? key_a : key_b), k = key0 + t;
+                float2& y = x[gr][j / 4][j % 4 / 2];
+                if (k >= lo[gr][j & 1] && k < hi[gr][j & 1] && !(bad >> ((tok + t) >> p.log2_eb) & 1))
+                  seen[gr] |= 1u << j;
+                else
+                  (j & 1 ? y.y : y.x) = -INFINITY;
+              }
           }
           // -------------------------------------------- reference
-          float2 top = make_float2(-INFINITY, -INFINITY);  // a NaN score leaves it alone
+          float2 top[RG];  // a NaN score leaves it alone
+#pragma unroll
+          for (int gr = 0; gr < RG; ++gr) top[gr] = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
           for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -667,71 +701,87 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
               for (int n = 1; n < NG; ++n) most = max(most, vp[h][k][n] & 0x7fffu);
               // exponent of the key's largest value scale: the scale is less than 2^e
               const float e = __uint_as_float(most >> 10 | 0x4b000000u) - (8388608.f + 14.f);
-              top.x = fmaxf(top.x, x[h][k].x + e);
-              top.y = fmaxf(top.y, x[h][k].y + e);
+#pragma unroll
+              for (int gr = 0; gr < RG; ++gr) {
+                top[gr].x = fmaxf(top[gr].x, x[gr][h][k].x + e);
+                top[gr].y = fmaxf(top[gr].y, x[gr][h][k].y + e);
+              }
             }
-          if (__any_sync(0xffffffffu, top.x > m.x + kSlack || top.y > m.y + kSlack)) {
-            float2 by;
+          bool past = false;
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-              top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, off));
-              top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, off));
-            }
-            top.x = fmaxf(top.x, m.x), top.y = fmaxf(top.y, m.y);
-            by.x = top.x == m.x ? 1.f : da::ex2_ftz(m.x - top.x);
-            by.y = top.y == m.y ? 1.f : da::ex2_ftz(m.y - top.y);
-            m = top;
-            l = da::mul2(l, by);
-            due = da::mul2(due, by);
+          for (int gr = 0; gr < RG; ++gr)
+            past |= top[gr].x > m[gr].x + kSlack || top[gr].y > m[gr].y + kSlack;
+          if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
-            for (int n = 0; n < NG; ++n) zero_sum[n] = da::mul2(zero_sum[n], by);
+            for (int gr = 0; gr < RG; ++gr) {
+              float2 by, t = top[gr];
 #pragma unroll
-            for (int i2 = 0; i2 < MT; ++i2) {
-              acc[i2][0] *= by.x, acc[i2][1] *= by.y;
-              acc[i2][2] *= by.x, acc[i2][3] *= by.y;
+              for (int off = 4; off < 32; off <<= 1) {
+                t.x = fmaxf(t.x, __shfl_xor_sync(0xffffffffu, t.x, off));
+                t.y = fmaxf(t.y, __shfl_xor_sync(0xffffffffu, t.y, off));
+              }
+              t.x = fmaxf(t.x, m[gr].x), t.y = fmaxf(t.y, m[gr].y);
+              by.x = t.x == m[gr].x ? 1.f : da::ex2_ftz(m[gr].x - t.x);
+              by.y = t.y == m[gr].y ? 1.f : da::ex2_ftz(m[gr].y - t.y);
+              m[gr] = t;
+              l[gr] = da::mul2(l[gr], by);
+              due[gr] = da::mul2(due[gr], by);
+#pragma unroll
+              for (int n = 0; n < NG; ++n) zero_sum[gr][n] = da::mul2(zero_sum[gr][n], by);
+#pragma unroll
+              for (int i2 = 0; i2 < MT; ++i2) {
+                acc[gr][i2][0] *= by.x, acc[gr][i2][1] *= by.y;
+                acc[gr][i2][2] *= by.x, acc[gr][i2][3] *= by.y;
+              }
             }
           }
           // -------------------------------------------- weights
-          {
-            const float2 up = make_float2(kShift - m.x, kShift - m.y);
+#pragma unroll
+          for (int gr = 0; gr < RG; ++gr) {
+            const float2 up = make_float2(kShift - m[gr].x, kShift - m[gr].y);
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                float2 y = da::add2(x[h][k], up);
+                float2 y = da::add2(x[gr][h][k], up);
                 y.x = da::ex2_ftz(y.x), y.y = da::ex2_ftz(y.y);
                 if constexpr (PART) {
-                  if (!(seen >> (4 * h + 2 * k) & 1)) y.x = 0.f;
-                  if (!(seen >> (4 * h + 2 * k) & 2)) y.y = 0.f;
+                  if (!(seen[gr] >> (4 * h + 2 * k) & 1)) y.x = 0.f;
+                  if (!(seen[gr] >> (4 * h + 2 * k) & 2)) y.y = 0.f;
                 }
-                x[h][k] = y;
-                l = da::add2(l, y);
+                x[gr][h][k] = y;
+                l[gr] = da::add2(l[gr], y);
               }
           }
           // -------------------------------------------- values
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
-            uint32_t ph[H][2], pl[H][2];  // P^T: the two terms
+            uint32_t ph[RG][H][2], pl[RG][H][2];  // P^T: the two terms
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const float sv = half_lo(vp[h][k][n]);
                 const float zv = fmaf(8.f, sv, half_hi(vp[h][k][n]));
-                float2 w = make_float2(x[h][k].x * sv, x[h][k].y * sv);
-                if constexpr (PART) {  // a key that is not seen may have any scale and zero
-                  const bool on0 = seen >> (4 * h + 2 * k) & 1, on1 = seen >> (4 * h + 2 * k) & 2;
-                  w = make_float2(on0 ? w.x : 0.f, on1 ? w.y : 0.f);
-                  zero_sum[n].x += on0 ? x[h][k].x * zv : 0.f;
-                  zero_sum[n].y += on1 ? x[h][k].y * zv : 0.f;
-                } else {
-                  zero_sum[n].x = fmaf(x[h][k].x, zv, zero_sum[n].x);
-                  zero_sum[n].y = fmaf(x[h][k].y, zv, zero_sum[n].y);
+#pragma unroll
+                for (int gr = 0; gr < RG; ++gr) {
+                  const float2 y = x[gr][h][k];
+                  float2 &zs = zero_sum[gr][n], w = make_float2(y.x * sv, y.y * sv);
+                  if constexpr (PART) {  // a key that is not seen may have any scale and zero
+                    const bool on0 = seen[gr] >> (4 * h + 2 * k) & 1, on1 = seen[gr] >> (4 * h + 2 * k) & 2;
+                    w = make_float2(on0 ? w.x : 0.f, on1 ? w.y : 0.f);
+                    zs.x += on0 ? y.x * zv : 0.f;
+                    zs.y += on1 ? y.y * zv : 0.f;
+                  } else {
+                    zs.x = fmaf(y.x, zv, zs.x);
+                    zs.y = fmaf(y.y, zv, zs.y);
+                  }
+                  uint32_t &hi_t = ph[gr][h][k], &lo_t = pl[gr][h][k];
+                  da::split_half2(w.x, w.y, hi_t, lo_t);
+                  if (PACK && c >= 2) hi_t = lo_t;
+                  hi_t = da::movmatrix_trans(hi_t);
+                  if constexpr (!PACK) lo_t = da::movmatrix_trans(lo_t);
                 }
-                da::split_half2(w.x, w.y, ph[h][k], pl[h][k]);
-                if (PACK && c >= 2) ph[h][k] = pl[h][k];
-                ph[h][k] = da::movmatrix_trans(ph[h][k]);
-                if constexpr (!PACK) pl[h][k] = da::movmatrix_trans(pl[h][k]);
               }
             // two pieces' products of one term, then of the other: each waits for none before it
             constexpr int PP = GP > 1 ? 2 : 1;
@@ -745,12 +795,18 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
                   const uint32_t a0 = vw[h][i2 + k / 2][0], a1 = vw[h][i2 + k / 2][1];
                   fr[k][0] = codes2(a0, k & 1), fr[k][1] = codes2(a1, k & 1);
                   fr[k][2] = codes2(a0 >> 8, k & 1), fr[k][3] = codes2(a1 >> 8, k & 1);
-                  mma(acc[2 * i2 + k], fr[k][0], fr[k][1], fr[k][2], fr[k][3], ph[h][0], ph[h][1]);
+#pragma unroll
+                  for (int gr = 0; gr < RG; ++gr)
+                    mma(acc[gr][2 * i2 + k], fr[k][0], fr[k][1], fr[k][2], fr[k][3], ph[gr][h][0],
+                        ph[gr][h][1]);
                 }
                 if constexpr (!PACK) {
 #pragma unroll
                   for (int k = 0; k < 2 * PP; ++k)
-                    mma(acc[2 * i2 + k], fr[k][0], fr[k][1], fr[k][2], fr[k][3], pl[h][0], pl[h][1]);
+#pragma unroll
+                    for (int gr = 0; gr < RG; ++gr)
+                      mma(acc[gr][2 * i2 + k], fr[k][0], fr[k][1], fr[k][2], fr[k][3], pl[gr][h][0],
+                          pl[gr][h][1]);
                 }
               }
           }
@@ -763,78 +819,91 @@ __global__ void __launch_bounds__(Geo<D, NG>::THREADS, 1)
       copy(a, n + STAGES);
       if (++chain == chain_keys(PACK) / TOK && n + 1 < a.n) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          float4 v = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-          if (kept) {
-            const float4 y = *state_at(i);
-            v = make_float4(fmaf(y.x, due.x, v.x), fmaf(y.y, due.y, v.y), fmaf(y.z, due.x, v.z),
-                            fmaf(y.w, due.y, v.w));
+        for (int gr = 0; gr < RG; ++gr) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            float (&y)[4] = acc[gr][i];
+            float4 v = make_float4(y[0], y[1], y[2], y[3]), *at = state_at(gr * MT + i);
+            if (kept) {
+              const float4 w = *at;
+              const float2 d = due[gr];
+              v = make_float4(fmaf(w.x, d.x, v.x), fmaf(w.y, d.y, v.y), fmaf(w.z, d.x, v.z),
+                              fmaf(w.w, d.y, v.w));
+            }
+            *at = v;
+            y[0] = y[1] = y[2] = y[3] = 0.f;
           }
-          *state_at(i) = v;
-          acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+          due[gr] = make_float2(1.f, 1.f);
         }
-        due = make_float2(1.f, 1.f);
         kept = true;
         chain = 0;
       }
     }
     // ------------------------------------------------ the part's state
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      l.x += __shfl_xor_sync(0xffffffffu, l.x, off);
-      l.y += __shfl_xor_sync(0xffffffffu, l.y, off);
+    for (int gr = 0; gr < RG; ++gr) {
+      float2 sum = l[gr], zs[NG];
 #pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        zero_sum[n].x += __shfl_xor_sync(0xffffffffu, zero_sum[n].x, off);
-        zero_sum[n].y += __shfl_xor_sync(0xffffffffu, zero_sum[n].y, off);
+      for (int n = 0; n < NG; ++n) zs[n] = zero_sum[gr][n];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        sum.x += __shfl_xor_sync(0xffffffffu, sum.x, off);
+        sum.y += __shfl_xor_sync(0xffffffffu, sum.y, off);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          zs[n].x += __shfl_xor_sync(0xffffffffu, zs[n].x, off);
+          zs[n].y += __shfl_xor_sync(0xffffffffu, zs[n].y, off);
+        }
       }
-    }
-    float* to[2];
+      float* to[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {  // rows of the lane's columns
-      const int r = row0 + col + j;
-      const float mj = j ? m.y : m.x, lj = j ? l.y : l.x;
-      to[j] = nullptr;
-      if (r >= p.R || (PACK && c >= 2)) continue;
-      if (a.slot < 0) {
-        const int t = r / p.G, h = a.kv * p.G + (r - t * p.G);
-        const long long row = ((long long)a.b * p.T + t) * p.Hq + h;
-        to[j] = p.out + row * D;
-        if (g == 0 && p.lse) p.lse[row] = lj == 0.f ? -INFINITY : (mj - kShift + log2f(lj)) * kLn2;
-      } else {
-        const long long row = ((long long)share * 2 + a.slot) * p.groups * kRows + rg * kRows + col + j;
-        to[j] = p.part_o + row * D;
-        if (g == 0) p.part_ml[row] = make_float2(mj, lj);
+      for (int j = 0; j < 2; ++j) {  // rows of the lane's columns
+        const int own = kRows * gr + col + j, r = row0 + own;
+        const float mj = j ? m[gr].y : m[gr].x, lj = j ? sum.y : sum.x;
+        to[j] = nullptr;
+        if (r >= p.R || (PACK && c >= 2)) continue;
+        if (a.slot < 0) {
+          const int t = r / p.G, h = a.kv * p.G + (r - t * p.G);
+          const long long row = ((long long)a.b * p.T + t) * p.Hq + h;
+          to[j] = p.out + row * D;
+          if (g == 0 && p.lse) p.lse[row] = lj == 0.f ? -INFINITY : (mj - kShift + log2f(lj)) * kLn2;
+        } else {
+          const long long row = ((long long)share * 2 + a.slot) * p.unit_rows + rg * WROWS + own;
+          to[j] = p.part_o + row * D;
+          if (g == 0) p.part_ml[row] = make_float2(mj, lj);
+        }
       }
-    }
-    const float2 by = a.slot < 0 ? make_float2(l.x == 0.f ? 0.f : 1.f / l.x, l.y == 0.f ? 0.f : 1.f / l.y)
-                                 : make_float2(1.f, 1.f);
-    if (kept) {
+      const float2 by = a.slot < 0 ? make_float2(sum.x == 0.f ? 0.f : 1.f / sum.x,
+                                                 sum.y == 0.f ? 0.f : 1.f / sum.y)
+                                   : make_float2(1.f, 1.f);
+      if (kept) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const float4 y = *state_at(i);
-        acc[i][0] = fmaf(y.x, due.x, acc[i][0]), acc[i][1] = fmaf(y.y, due.y, acc[i][1]);
-        acc[i][2] = fmaf(y.z, due.x, acc[i][2]), acc[i][3] = fmaf(y.w, due.y, acc[i][3]);
+        for (int i = 0; i < MT; ++i) {
+          const float4 w = *state_at(gr * MT + i);
+          const float2 d = due[gr];
+          float (&y)[4] = acc[gr][i];
+          y[0] = fmaf(w.x, d.x, y[0]), y[1] = fmaf(w.y, d.y, y[1]);
+          y[2] = fmaf(w.z, d.x, y[2]), y[3] = fmaf(w.w, d.y, y[3]);
+        }
       }
-    }
-    if constexpr (PACK) {
+      if constexpr (PACK) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], 2);
-    }
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 v = make_float2(acc[2 * i][j], acc[2 * i + 1][j]);
-        const float f = j & 1 ? by.y : by.x;
-        const float z = j & 1 ? zero_sum[i / GP].y : zero_sum[i / GP].x;
-        v = da::fma2(v, make_float2(0x1p9f, 0x1p9f), make_float2(z, z));
-        if (to[j & 1])
-          *reinterpret_cast<float2*>(to[j & 1] + 32 * i + 2 * g + (j & 2 ? 16 : 0)) =
-              make_float2(v.x * f, v.y * f);
+          for (int j = 0; j < 4; ++j) acc[gr][i][j] += __shfl_xor_sync(0xffffffffu, acc[gr][i][j], 2);
       }
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 v = make_float2(acc[gr][2 * i][j], acc[gr][2 * i + 1][j]);
+          const float k = j & 1 ? by.y : by.x, z = j & 1 ? zs[i / GP].y : zs[i / GP].x;
+          v = da::fma2(v, make_float2(0x1p9f, 0x1p9f), make_float2(z, z));
+          if (to[j & 1])
+            *reinterpret_cast<float2*>(to[j & 1] + 32 * i + 2 * g + (j & 2 ? 16 : 0)) =
+                make_float2(v.x * k, v.y * k);
+        }
+    }
   }
 }
 
@@ -861,7 +930,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) q4_merge_kernel(const __grid
     if (lane == 0 && p.lse) p.lse[row] = -INFINITY;
     return;
   }
-  const int unit_rows = p.groups * kRows, block = r / unit_rows;
+  const int unit_rows = p.unit_rows, block = r / unit_rows;
   const Shares shares(all * upb, p.shares);
   const int u0 = pre0 * upb + (kv * p.blocks + block) * nt, u1 = u0 + nt;
   const int s0 = shares.of(u0), s1 = shares.of(u1 - 1);
@@ -934,11 +1003,34 @@ __global__ void __launch_bounds__(32 * kMergeWarps) q4_merge_kernel(const __grid
 // ------------------------------------------------------------------ host
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-int warps_of(int D) { return D == 256 ? Geo<256, 2>::WARPS : Geo<128, 1>::WARPS; }
+int warps_of(int D, int rows) {
+  return D == 256                ? Geo<256, 2, 8>::WARPS
+         : D == 128 && rows == 16 ? Geo<128, 1, 16>::WARPS
+                                  : Geo<128, 1, 8>::WARPS;
+}
 
 struct Shape {
-  int groups, blocks, chunk;  // row groups of a unit, units of a kv head, sequences of a launch
+  int rows, warps;    // query rows of a warp, warps of a unit
+  int blocks, chunk;  // units of a kv head, sequences of a launch
 };
+
+void set_rows(Shape& s, long long rows, int of_warp) {
+  const long long n = of_warp < kRows ? kRows : of_warp, warps = (rows + n - 1) / n;
+  s.rows = of_warp;
+  s.warps = 1;
+  while (s.warps < warps && s.warps < kMaxWarps) s.warps *= 2;
+  s.blocks = (int)((warps + s.warps - 1) / s.warps);
+}
+
+// 16 rows a warp take less work in all, but leave fewer shares with more latency each: they are for many heads
+// with room for long sequences.  D = 128, 16 rows, us with 16 and 8: 512 heads of 2048 to 24,000 keys 283 and 326, 160 of
+// 8500 98 and 109, 800 of 100 to 600 49 and 46, 48 of 1000 to 9000 48 and 41.
+void choose_rows(const da_params* p, int q_len, int sms, Shape& s) {
+  const long long rows = (long long)q_len * p->num_q_heads / p->num_kv_heads;
+  if (rows > 8 && p->head_dim <= 128 && (long long)p->batch * p->num_kv_heads >= sms &&
+      (long long)p->max_blocks_per_seq * p->block_size >= 1024)
+    set_rows(s, rows, 16);
+}
 
 int check(const da_params* p, int group, int q_len, Shape& s) {
   int st = da::check_paged(p);
@@ -951,16 +1043,12 @@ int check(const da_params* p, int group, int q_len, Shape& s) {
   if (cap > 0x7fffffffLL - 1024 || all_rows > 0x7fffffffLL - 1024) return DA_ERR_UNSUPPORTED;
   if (da::q4_page_bytes(p->block_size, p->head_dim, group) * p->num_kv_heads > 0xffffffffLL)
     return DA_ERR_UNSUPPORTED;
-  const long long groups = (rows + kRows - 1) / kRows;
-  s.groups = 1;
-  while (s.groups < groups && s.groups < kMaxGroups) s.groups *= 2;
-  const long long blocks = (groups + s.groups - 1) / s.groups;
+  set_rows(s, rows, rows <= 4 ? 4 : 8);
   // tiles and rows of a launch count in 31 bits
-  const long long tiles = (cap / (4096 / p->head_dim) + 2) * p->num_kv_heads * blocks;
+  const long long tiles = (cap / (4096 / p->head_dim) + 2) * p->num_kv_heads * s.blocks;
   long long most = (0x7fffffffLL - 4096) / tiles;
   if (most > 0x7fffffffLL / all_rows) most = 0x7fffffffLL / all_rows;
   if (most < 1) return DA_ERR_UNSUPPORTED;
-  s.blocks = (int)blocks;
   s.chunk = (int)(most < kMaxBatch ? most : kMaxBatch);
   return DA_OK;
 }
@@ -968,11 +1056,11 @@ int check(const da_params* p, int group, int q_len, Shape& s) {
 struct Layout {
   size_t pre, ml, o, total;
 };
-Layout layout(int sms, int D) {
+Layout layout(int sms, int D, int wrows) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   Layout w;
-  // a share has `groups` warps and as many groups of rows
-  const size_t rows = (size_t)sms * warps_of(D) * 2 * kRows;
+  // two states of each warp's rows
+  const size_t rows = (size_t)sms * warps_of(D, wrows) * 2 * (wrows < kRows ? kRows : wrows);
   w.pre = 0;
   w.ml = up((kMaxBatch + 1) * sizeof(int));
   w.o = w.ml + up(rows * sizeof(float2));
@@ -980,17 +1068,17 @@ Layout layout(int sms, int D) {
   return w;
 }
 
-template <int D, int NG, bool PACK>
-cudaError_t launch(Q4Params& k, int grid, cudaStream_t s) {
-  using g_ = Geo<D, NG>;
+template <int D, int NG, int ROWS>
+cudaError_t launch_rows(Q4Params& k, int grid, cudaStream_t s) {
+  using g_ = Geo<D, NG, ROWS>;
   static_assert(sizeof(Shared<g_::WARPS, g_::STAGES>) <= 2048, "more than a processor's shared memory");
-  cudaError_t err = cudaFuncSetAttribute(q4_kernel<D, NG, PACK>,
+  cudaError_t err = cudaFuncSetAttribute(q4_kernel<D, NG, ROWS>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, g_::kMost);
   if (err != cudaSuccess) return err;
   k.log2_eb = 0;
   while ((2 << k.log2_eb) <= g_::TOK && k.log2_eb < k.log2_bs) ++k.log2_eb;
-  k.shares = grid * (g_::WARPS / k.groups);
-  err = da::launch_early(q4_kernel<D, NG, PACK>, grid, g_::THREADS, g_::SMEM + (k.B + 1) * 4, s, k);
+  k.shares = grid * (g_::WARPS / k.warps);
+  err = da::launch_early(q4_kernel<D, NG, ROWS>, grid, g_::THREADS, g_::SMEM + (k.B + 1) * 4, s, k);
   if (err != cudaSuccess) return err;
   const long long rows = (long long)k.B * k.T * k.Hq;
   return da::launch_early(q4_merge_kernel<D>, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps),
@@ -998,20 +1086,22 @@ cudaError_t launch(Q4Params& k, int grid, cudaStream_t s) {
 }
 
 template <int D, int NG>
-cudaError_t launch(Q4Params& k, int grid, cudaStream_t s) {
-  return k.R <= 4 ? launch<D, NG, true>(k, grid, s) : launch<D, NG, false>(k, grid, s);
+cudaError_t launch(Q4Params& k, int rows, int grid, cudaStream_t s) {
+  if constexpr (D <= 128)
+    if (rows == 16) return launch_rows<D, NG, 16>(k, grid, s);
+  return rows == 4 ? launch_rows<D, NG, 4>(k, grid, s) : launch_rows<D, NG, 8>(k, grid, s);
 }
 
-cudaError_t launch(Q4Params& k, int D, int group, int grid, cudaStream_t s) {
+cudaError_t launch(Q4Params& k, int D, int group, int rows, int grid, cudaStream_t s) {
   switch (D * 1000 + group) {
-    case 64032: return launch<64, 2>(k, grid, s);
-    case 64064: return launch<64, 1>(k, grid, s);
-    case 128032: return launch<128, 4>(k, grid, s);
-    case 128064: return launch<128, 2>(k, grid, s);
-    case 128128: return launch<128, 1>(k, grid, s);
-    case 256032: return launch<256, 8>(k, grid, s);
-    case 256064: return launch<256, 4>(k, grid, s);
-    default: return launch<256, 2>(k, grid, s);
+    case 64032: return launch<64, 2>(k, rows, grid, s);
+    case 64064: return launch<64, 1>(k, rows, grid, s);
+    case 128032: return launch<128, 4>(k, rows, grid, s);
+    case 128064: return launch<128, 2>(k, rows, grid, s);
+    case 128128: return launch<128, 1>(k, rows, grid, s);
+    case 256032: return launch<256, 8>(k, rows, grid, s);
+    case 256064: return launch<256, 4>(k, rows, grid, s);
+    default: return launch<256, 2>(k, rows, grid, s);
   }
 }
 
@@ -1029,7 +1119,8 @@ size_t decode_attn_paged_q4_workspace_size(const da_params* p, int32_t q_len) {
   Shape s;
   int sms = 0;
   if (check(p, da::kQ4MinGroup, q_len, s) != DA_OK || da::device_sms(&sms) != DA_OK) return 0;
-  return layout(sms, p->head_dim).total;
+  choose_rows(p, q_len, sms, s);
+  return layout(sms, p->head_dim, s.rows).total;
 }
 
 int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const float* q,
@@ -1054,7 +1145,8 @@ int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const
   int sms = 0;
   st = da::device_sms(&sms);
   if (st != DA_OK) return st;
-  const Layout w = layout(sms, p->head_dim);
+  choose_rows(p, q_len, sms, shape);
+  const Layout w = layout(sms, p->head_dim, shape.rows);
   if (!workspace || workspace_bytes < w.total) return DA_ERR_WORKSPACE;
   Q4Params k = {};
   k.pool = pool;
@@ -1069,8 +1161,9 @@ int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const
   k.num_blocks = p->num_blocks;
   k.window = p->sliding_window;
   k.causal = p->causal;
-  k.groups = shape.groups;
+  k.warps = shape.warps;
   k.blocks = shape.blocks;
+  k.unit_rows = shape.warps * (shape.rows < kRows ? kRows : shape.rows);
   k.qscale = da::base2_scale(p);
   k.softcap2 = p->softcap > 0.f ? p->softcap * 1.4426950408889634f : 0.f;
   k.softcap_inv = k.softcap2 > 0.f ? (float)(1.0 / (double)k.softcap2) : 0.f;
@@ -1090,7 +1183,7 @@ int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const
     k.table = block_table + (long long)b0 * k.max_blocks;
     k.seq_lens = seq_lens + b0;
     k.q_pos = q_pos ? q_pos + b0 : nullptr;
-    if (launch(k, p->head_dim, group, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    if (launch(k, p->head_dim, group, shape.rows, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
       return DA_ERR_CUDA;
   }
   return DA_OK;

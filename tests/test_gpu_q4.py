@@ -342,6 +342,25 @@ def test_sliding_windows(D, window, T):
     c.check()
 
 
+@pytest.mark.parametrize("D,group", FORMATS)
+@pytest.mark.parametrize("T,Hq,H", [(1, 36, 4), (2, 32, 4), (5, 20, 4), (9, 32, 4), (16, 40, 4)])
+@pytest.mark.parametrize("window,causal", [(0, True), (70, True), (200, False)])
+def test_many_rows_of_many_heads(D, group, T, Hq, H, window, causal):
+    """9 to 160 rows a kv head in a batch large enough for warps of 16 rows, tables with room
+    for 1024 keys and more; lengths from none on."""
+    c = Case(18, Hq, H, D, group, 16, [0, 1, T, 15, 16, 17, 63, 64, 65, 300, 1024, 700, 33], T=T)
+    pick = np.arange(44) % 13
+    pick[13:] = pick[13:][::-1]
+    c.lens, c.table, c.q = c.lens[pick], c.table[pick], c.q[pick]
+    c.q = c.q + np.float32(0.01) * np.arange(44, dtype=np.float32).reshape((44,) + (1,) * (c.q.ndim - 1))
+    c.kw = dict(sliding_window=window, causal=causal)
+    c.check()
+    c.cache.scale[1, c.table[10, 3], 1, 5, -1] = np.nan  # in one value group of one key
+    out, lse, _ = c.run()
+    ro, _, _ = c.want()
+    assert np.array_equal(np.isnan(out), np.isnan(ro)) and np.isfinite(lse[10]).all()
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("T,Hq,H", [(2, 2, 1), (4, 2, 2), (17, 4, 2), (40, 1, 1)])
 @pytest.mark.parametrize("window", [1, 5, 40])
