@@ -562,7 +562,8 @@ int decode_attn_gather_paged_q4(const da_params* p, int32_t group, int32_t num_t
  * as NaN (where it sees a key).  out must not overlap q (DA_ERR_INVALID).
  * workspace: device scratch of decode_attn_paged_q4_workspace_size(p, q_len)
  * bytes, 256-byte aligned, of any content (parts of sequences that several
- * warps share); calls that overlap on the GPU must not share it.  Calls of one
+ * warps share; one that serves a batch, q_len and max_blocks_per_seq serves smaller
+ * ones too); calls that overlap on the GPU must not share it.  Calls of one
  * stream may, also from several threads.  p->max_seq_len is not used, nor is
  * da_tuning: nothing in the kernel waits for another part of it.
  * Everything else as for decode_attn_paged.  DA_ERR_UNSUPPORTED also where one

@@ -571,6 +571,25 @@ def test_workspaces_and_repeats():
     assert e.value.status == qk.DA_ERR_INVALID
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_workspace_serves_smaller_calls(D):
+    """Its size never falls as batch, query tokens or room grow; a call of few rows in the
+    workspace of a large one."""
+    import torch
+    size = lambda B, T, mb: qk.decode_attn_paged_q4_workspace_size(  # noqa: E731
+        qk.DaParams(B, 16, 4, D, 16, mb, 64, 0, 0.0, 0.0, 0, 1), T)
+    axes = ((1, 30, 40, 2000), (1, 2, 3, 5, 40), (1, 63, 64, 4000))
+    for mb in axes[2]:
+        for T in axes[1]:
+            for B in axes[0]:
+                n = size(B, T, mb)
+                assert n > 0 and all(size(B2, T2, mb2) <= n for B2 in axes[0] if B2 <= B
+                                     for T2 in axes[1] if T2 <= T for mb2 in axes[2] if mb2 <= mb)
+    ws = torch.empty(size(2000, 40, 4000), dtype=torch.uint8, device="cuda")
+    c = Case(23, 16, 4, D, 64, 16, [700, 3, 90])
+    c.check(c.run(workspace=ws))
+
+
 def test_a_length_past_the_bound_is_still_right():
     """max_seq_len sizes the launch only."""
     c = Case(21, 8, 2, 128, 64, 16, [5000, 40, 900])
