@@ -33,6 +33,7 @@ constexpr int kThreads = 1024;
 constexpr int kCluster = 16;
 constexpr int kMaxBatch = 16384;   // three sums of each in shared memory
 constexpr int kKeptBatch = 10240;  // both lengths too
+constexpr size_t kOwnShared = 1024;  // at most, of shared memory that the kernel declares
 // A warp takes up to 32 * kRun entries side by side: most are the request's that the one before was, and need no
 // search, and their loads are under way together (the same call, with 8 CTAs: 42 us with one entry at a time).
 constexpr int kRun = 8;
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
   extern __shared__ int smem[];
   __shared__ Sums warp_sums[kThreads / 32];
   __shared__ int flags, flags_found;  // of lengths and counts; of what table and stack hold
+  static_assert(sizeof(warp_sums) + 2 * sizeof(int) + 16 <= kOwnShared, "shared memory");
   cg::cluster_group cluster = cg::this_cluster();
   int* cu = smem;                // [B + 1] tokens before request b
   int* taken = cu + a.B + 1;     // pages taken before it
@@ -355,8 +357,10 @@ extern "C" int decode_attn_plan_blocks(int32_t batch, int32_t block_size,
   const size_t smem = 3 * sizeof(int) * ((size_t)batch + 1) +
                       (batch <= kKeptBatch ? 2 * sizeof(int) * (size_t)batch : 0);
   constexpr size_t kMost = 5 * sizeof(int) * kKeptBatch + 64;
-  static_assert(kMost >= 3 * sizeof(int) * (kMaxBatch + 1) && kMost <= 226 * 1024, "shared memory");
-  if (smem > 48 * 1024 &&
+  static_assert(kMost >= 3 * sizeof(int) * (kMaxBatch + 1) && kMost + kOwnShared <= 227 * 1024,
+                "shared memory");
+  // what a kernel has without being allowed more, its own included
+  if (smem + kOwnShared > 48 * 1024 &&
       cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) !=
           cudaSuccess)
     return DA_ERR_CUDA;

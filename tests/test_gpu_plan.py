@@ -1,5 +1,9 @@
 """Pages and places of requests on the GPU against a loop on the host: every
 table entry, free page, position and slot has to match."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -289,3 +293,20 @@ def test_no_requests_and_no_tokens():
     args = (np.array([20]), np.array([3]), np.array([[2, 1]], np.int32), np.array([0, 9], np.int32),
             1, 16, 4, 0)
     _same(_run(*args), plan(*args))
+
+
+def test_shared_memory_up_to_and_past_the_default(tmp_path):
+    """A process's first calls, from 2417 requests on (48,352 bytes of sums and lengths beside the
+    kernel's own; past 48 KB a kernel has to be allowed to have them), none larger before."""
+    code = ("import numpy as np, test_gpu_plan as t\n"
+            "r = np.random.default_rng(8)\n"
+            "for B in (2417, 2418, 2440, 2457, 2458):\n"
+            "    old, new = r.integers(0, 60, B), r.integers(0, 60, B)\n"
+            "    table, free, count = t._state(r, old, 16, 4, 4 * B)\n"
+            "    args = (old, new, table, free, count, 16, 4 * B, 60 * B)\n"
+            "    t._same(t._run(*args), t.plan(*args))\n")
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = {**os.environ, "PYTHONPATH": os.pathsep.join([here, os.path.dirname(here)])}
+    ran = subprocess.run([sys.executable, "-c", code], env=env, cwd=tmp_path, capture_output=True,
+                         text=True, timeout=300)
+    assert ran.returncode == 0, ran.stderr[-2000:]
