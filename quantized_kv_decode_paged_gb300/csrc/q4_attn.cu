@@ -63,6 +63,9 @@ constexpr int kMaxBatch = 1024;         // sequences of a launch
 constexpr int chain_keys(bool pack) { return pack ? 256 : 64; }
 constexpr float kShift = 10.f, kSlack = 5.f;
 constexpr float kLn2 = 0.6931471805599453f;
+// The reference of a row before its first key of weight: finite, so that scores of -inf (below f32's range) that
+// come before it weigh 0 and not 2^(-inf + inf).
+constexpr float kLeast = -3.402823466e38f;
 
 struct Q4Params {
   const float* q;
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(Geo<D, NG, ROWS>::THREADS, 1)
     float2 zero_sum[RG][NG] = {}, l[RG] = {}, m[RG], due[RG];
 #pragma unroll
     for (int gr = 0; gr < RG; ++gr) {
-      m[gr] = make_float2(-INFINITY, -INFINITY);
+      m[gr] = make_float2(kLeast, kLeast);
       due[gr] = make_float2(1.f, 1.f);  // what has left acc lies in `state`, to be multiplied by this
     }
     bool kept = false;

@@ -481,6 +481,29 @@ def test_query_values_of_any_size(D):
     d.check()
 
 
+@pytest.mark.parametrize("D,group", FORMATS)
+@pytest.mark.parametrize("B,T,Hq,H", [(3, 1, 4, 2), (3, 1, 16, 2), (48, 3, 16, 4)])
+@pytest.mark.parametrize("window", [0, 300])
+def test_scores_below_f32(D, group, B, T, Hq, H, window):
+    """Keys whose scores are below f32's range have no weight, also those that come first: their
+    rows are all -1000, the other keys 0, every q_d 10^36.  The others' scores are 0, exactly, and
+    count alike: the bounds are those of q = 0."""
+    c = Case(24, Hq, H, D, group, 16, [1, 40, 200, 1040, 5000], T=T)
+    pick = np.arange(B) % 3 + 2
+    c.lens, c.table, c.q = c.lens[pick], c.table[pick], np.zeros((B,) + c.q.shape[1:], np.float32)
+    c.cache.codes[0], c.cache.scale[0], c.cache.zero[0] = 0, 0, -1000
+    for b in range(B):
+        for t in range(c.lens[b] - 90, c.lens[b] - T + 1):  # every query token sees some
+            c.cache.zero[0, c.table[b, t // 16], :, t % 16] = 0
+    c.kw = dict(sliding_window=window)
+    bo, bl = c.bounds()
+    c.q[:] = 1e36
+    out, lse, flags = c.run()
+    ro, rl, _ = c.want()
+    assert flags == 0 and (np.abs(out - ro) <= bo).all()
+    assert (np.abs(lse - rl) <= bl + 2.0 ** -23 * np.abs(rl)).all()
+
+
 @pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (128, 128), (256, 128)])
 @pytest.mark.parametrize("s", [2.0 ** -20, 2.0 ** -10, 1.0, 4096.0])
 def test_value_scales_of_any_size(D, group, s):
