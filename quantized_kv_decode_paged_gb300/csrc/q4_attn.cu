@@ -1168,8 +1168,10 @@ int decode_attn_paged_q4(const da_params* p, int32_t group, int32_t q_len, const
   k.blocks = shape.blocks;
   k.unit_rows = shape.warps * (shape.rows < kRows ? kRows : shape.rows);
   k.qscale = da::base2_scale(p);
-  k.softcap2 = p->softcap > 0.f ? p->softcap * 1.4426950408889634f : 0.f;
-  k.softcap_inv = k.softcap2 > 0.f ? (float)(1.0 / (double)k.softcap2) : 0.f;
+  // cap and reciprocal are finite for the largest and the least caps too: a score of 0 stays 0
+  constexpr float kMostF32 = 3.402823466e38f;
+  k.softcap2 = fminf(p->softcap * 1.4426950408889634f, kMostF32);
+  k.softcap_inv = k.softcap2 > 0.f ? (float)fmin(1.0 / (double)k.softcap2, kMostF32) : 0.f;
   k.page_bytes = da::q4_page_bytes(p->block_size, p->head_dim, group);
   k.stride = (uint32_t)(k.page_bytes * p->num_kv_heads);
   char* ws = static_cast<char*>(workspace);

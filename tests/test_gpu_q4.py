@@ -504,6 +504,30 @@ def test_scores_below_f32(D, group, B, T, Hq, H, window):
     assert (np.abs(lse - rl) <= bl + 2.0 ** -23 * np.abs(rl)).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_softcap_below_normal_numbers(D):
+    """cap * tanh(s / cap) of the least caps is 0 to any accuracy, also for s = 0."""
+    c = Case(25, 8, 2, D, 32, 16, [300, 33])
+    c.q[:, :2] = 0
+    for cap in (1e-37, 1e-39, 1e-40, 1e-45):
+        c.kw = dict(softcap=cap)
+        c.check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_softcap_past_every_score(D):
+    """A cap near f32's largest number changes nothing.  s / cap is off by half of f32's least step,
+    2^-150, which comes back times a cap below 2^128: 2^-22 of a score in units of log 2."""
+    c = Case(27, 8, 2, D, 32, 16, [300, 33])
+    bo, bl = c.bounds()
+    vmag = (8 * c.cache.scale[1] + np.abs(c.cache.zero[1] + 8 * c.cache.scale[1])).max()
+    for cap in (1e37, 2e38, 3.4e38):
+        out, lse, _ = c.run(softcap=cap)
+        ro, rl, _ = c.want()
+        assert (np.abs(out - ro) <= bo + 2 * 2.0 ** -22 * vmag).all()
+        assert (np.abs(lse - rl) <= bl + 2.0 ** -22 + 2.0 ** -23 * np.abs(rl)).all()
+
+
 @pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (128, 128), (256, 128)])
 @pytest.mark.parametrize("s", [2.0 ** -20, 2.0 ** -10, 1.0, 4096.0])
 def test_value_scales_of_any_size(D, group, s):
