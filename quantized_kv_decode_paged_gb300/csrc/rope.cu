@@ -278,10 +278,17 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(MODE)) rope_kernel(con
     x.kind = x.h < a.Hq ? 0 : x.h < a.Hq + a.Hk ? 1 : 2;
     x.h -= x.kind == 0 ? 0 : x.kind == 1 ? a.Hq : a.Hq + a.Hk;
     const long long n = n0 + x.t;
-    const void* from = x.kind == 0 ? a.q : x.kind == 1 ? a.k : a.v;
-    const long long ts = x.kind == 0 ? a.q_ts : x.kind == 1 ? a.k_ts : a.v_ts;
-    const long long hs = x.kind == 0 ? a.q_hs : x.kind == 1 ? a.k_hs : a.v_hs;
-    const T* src = static_cast<const T*>(from) + n * ts + x.h * hs;
+    const T* src;
+    if constexpr (MODE == kAppendQ4) {
+      const void* from = x.kind == 0 ? a.q : x.kind == 1 ? a.k : a.v;
+      const long long ts = x.kind == 0 ? a.q_ts : x.kind == 1 ? a.k_ts : a.v_ts;
+      const long long hs = x.kind == 0 ? a.q_hs : x.kind == 1 ? a.k_hs : a.v_hs;
+      src = static_cast<const T*>(from) + n * ts + x.h * hs;
+    } else {  // an address of each: with selected terms the f32 norm and rotation spills 24 bytes more, 41 for 28.8 us
+      src = x.kind == 0   ? static_cast<const T*>(a.q) + n * a.q_ts + x.h * a.q_hs
+            : x.kind == 1 ? static_cast<const T*>(a.k) + n * a.k_ts + x.h * a.k_hs
+                          : static_cast<const T*>(a.v) + n * a.v_ts + x.h * a.v_hs;
+    }
     x.lo = load8(src + lo);
     x.hi = load8(src + hi);
     return x;
