@@ -801,10 +801,11 @@ def _load_call():
                     lib.decode_attn_append_paged_q4, lib.decode_attn_gather_paged_q4,
                     lib.decode_attn_paged_q4, lib.decode_attn_paged_q4_workspace_size,
                     lib.decode_attn_plan_blocks)))
-            except ImportError as e:
+            except (ImportError, AttributeError, TypeError) as e:  # missing, or an older library's
                 warnings.warn("the norm, append, shared-prefix, 4-bit cache and block plan calls go "
                               "through Python, slower: "
-                              f"no {path} (quantized_kv_decode_paged_gb300.build() makes it): {e}",
+                              f"no {path} of this library "
+                              f"(quantized_kv_decode_paged_gb300.build() makes it): {e}",
                               RuntimeWarning)
                 module = _NoCall
             _call = module

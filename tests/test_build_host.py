@@ -80,3 +80,19 @@ def test_calls_without_the_module_go_through_python(tmp_path, monkeypatch):
     monkeypatch.setattr(qk, "_call", None)
     with pytest.warns(RuntimeWarning, match="through Python"):
         assert qk._load_call().prefix() is NotImplemented
+
+
+def test_calls_with_a_module_of_an_older_library_go_through_python(tmp_path, monkeypatch):
+    """One that lacks a function, or whose functions take other arguments."""
+    qk.build()
+    path = tmp_path / "module.py"
+    loader = qk.importlib.machinery.SourceFileLoader
+    monkeypatch.setattr(qk.importlib.machinery, "ExtensionFileLoader",
+                        lambda name, _: loader(name, str(path)))
+    for text in ("def bind(*a): pass\n", "def bind(): pass\ndef bind_q4(*a): pass\n"):
+        path.write_text(text)
+        monkeypatch.setattr(qk, "_call", None)
+        with pytest.warns(RuntimeWarning, match="through Python"):
+            with pytest.raises(ValueError, match="CUDA device"):
+                qk.decode_attn_qk_norm_rope(torch.zeros(1, 1, 64), None, None, None)
+        assert qk._load_call().plan() is NotImplemented
