@@ -420,6 +420,28 @@ def test_bad_pages_and_lengths_are_masked_and_flagged():
     d.check(d.run(max_seq_len=0), flags=qk.DEV_BAD_SEQ_LEN)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bs", [8, 16, 64, 256])
+@pytest.mark.parametrize("B,T,Hq,H", [(4, 1, 8, 2), (4, 1, 16, 2), (40, 4, 16, 4)])
+@pytest.mark.parametrize("window", [0, 333])
+def test_bad_pages_of_every_place_in_a_tile(D, bs, B, T, Hq, H, window):
+    """Units of 4, 8 and 16 rows, tiles of many pages and pages of many tiles: pages outside the
+    pool first, last and inside of a tile, side by side, before the window and as the last
+    one of a sequence."""
+    c = Case(26, Hq, H, D, 32, bs, [1100, 700, 1024, 801], T=T)
+    pick = np.arange(B) % 4
+    c.lens, c.table = c.lens[pick], c.table[pick]
+    c.q = c.r.standard_normal((B,) + c.q.shape[1:]).astype(np.float32)
+    for b in range(B):
+        n = -(-int(c.lens[b]) // bs)
+        some = [(b // 4 + k) % n for k in (0, 5, 6, n - 1)] + c.r.integers(0, n, 1 + n // 9).tolist()
+        c.table[b, some[b % 2:]] = c.r.choice([-1, c.cache.NB, 2 ** 31 - 1, -2 ** 31])
+    c.kw = dict(sliding_window=window)
+    c.check(flags=qk.DEV_BAD_BLOCK)
+    c.table[:B // 2] = -1  # sequences without a single page
+    c.check(flags=qk.DEV_BAD_BLOCK)
+
+
 @pytest.mark.parametrize("D,group", FORMATS)
 @pytest.mark.parametrize("poison", [np.nan, np.inf, -np.inf])
 def test_nonfinite_scales_in_masked_places(D, group, poison):
