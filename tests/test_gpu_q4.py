@@ -237,6 +237,41 @@ def test_append_with_norm_and_rotation(dtype, D, rd, group, il):
             assert (np.abs(vals[i][at] - rows[n]) <= tol).all()
 
 
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16", "float32"])
+@pytest.mark.parametrize("D,rd,group", [(64, 64, 32), (64, 16, 64), (128, 128, 32), (128, 128, 128),
+                                        (128, 96, 64), (256, 256, 128), (256, 96, 32), (256, 16, 64)])
+@pytest.mark.parametrize("il", [False, True])
+@pytest.mark.parametrize("norm,kind", [(True, "normal"), (False, "wide"), (False, "past"), (True, "nan")])
+def test_append_of_rotated_keys_bit_for_bit(dtype, D, rd, group, il, norm, kind):
+    """The f32 rows that the norm and rotation give, quantised as the format defines it, whichever
+    threads hold a group's values; a NaN's group and no other."""
+    import torch
+    rng = np.random.default_rng(D + rd + group)
+    N, H, bs = 333, 2, 16
+    rows = _rows(rng, (N, 2 * H, D), kind)
+    if kind == "nan":
+        rows[::7, :, D // 3] = np.nan
+    x = torch.from_numpy(rows).cuda().to(getattr(torch, dtype))
+    k, v = x[:, :H], x[:, H:]
+    pos = rng.integers(0, 64, N).astype(np.int32)
+    table = rng.permutation(N * 4).astype(np.int32).reshape(N, 4)
+    f = qk.decode_attn_rope_freqs(rd)
+    w = _t((1 + 0.1 * rng.standard_normal(D)).astype(np.float32)) if norm else None
+    pool = torch.zeros((N * 4, H, qk.decode_attn_q4_page_bytes(bs, D, group)), dtype=torch.uint8,
+                       device="cuda")
+    qk.decode_attn_append_paged_q4(k, v, _t(pos), _t(table), pool, f, group=group, norm=norm,
+                                   k_weight=w, interleaved=il)
+    y, _ = qk.decode_attn_qk_norm_rope(k, None, _t(pos), f, norm=norm, q_weight=w, interleaved=il)
+    c = Cache.of_bytes(pool.cpu().numpy(), bs, D, group)
+    at = (table[np.arange(N), pos // bs], slice(None), pos % bs)
+    for i, ref in enumerate((y, v)):
+        codes, scale, zero = quantised(_np(ref), group)
+        assert np.array_equal(c.scale[i][at], scale, equal_nan=True)
+        assert np.array_equal(c.zero[i][at], zero, equal_nan=True)
+        assert np.array_equal(c.codes[i][at], codes)
+    assert kind == "past" or np.isnan(c.scale).any() == (kind == "nan")
+
+
 def test_append_keeps_nan_where_it_is():
     """A NaN makes its own group NaN, keys and values, and no other."""
     import torch
