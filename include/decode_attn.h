@@ -491,6 +491,10 @@ int decode_attn_paged_prefix(const da_params* p, int32_t q_len, int32_t prefix_l
  * (DA_DEV_BAD_FREE_LIST), table, list and count stay as they are, every token is
  * padding and cu_tokens is zero.  A caller sees that without dev_status by
  * cu_tokens[B].
+ * A page stands in one place: in the part of one row that its request's length
+ * covers, or among the free ones.  The call counts no holders: a page that several
+ * rows name (the prefix of decode_attn_paged_prefix) would be given back with the
+ * first of them that ends, while the others still read it.
  * The buffers must not overlap.  batch <= 16384; block_size a power of two in
  * [8, 256].  max_tokens may be 0 (the three token arrays may then be NULL), but
  * a request that gains tokens then overflows.  With batch 0 and max_tokens 0 nothing

@@ -1200,6 +1200,9 @@ def decode_attn_plan_blocks(old_lens, new_lens, block_table, free_list, free_cou
     i32 [B + 1]): every new token's position, request and page * block_size + row, requests
     in order, padding (0, -1, -1) behind them, and the tokens before each request.
 
+    A page belongs to one request, or is free.  Holders are not counted: one that
+    several rows name (a shared prefix) would become free with the first that ends.
+
     All or nothing: where free pages or max_tokens do not suffice, or a
     length, page or count is out of range, nothing is changed, every token is
     padding, cu_tokens is zero and dev_status says why (DEV_NO_BLOCKS,
