@@ -84,7 +84,8 @@ def _build_call() -> None:
     try:
         _compile_call(call_path())
     except Exception as e:
-        warnings.warn(f"the norm, append and shared-prefix calls go through Python, slower: {e}",
+        warnings.warn("the norm, append, shared-prefix, 4-bit cache and block plan calls go "
+                      f"through Python, slower: {e}",
                       RuntimeWarning)
 
 

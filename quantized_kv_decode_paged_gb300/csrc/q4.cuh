@@ -20,7 +20,6 @@ inline bool q4_group_ok(int group, int D) {
   return (group == 32 || group == 64 || group == 128) && group <= D;
 }
 
-__host__ __device__ constexpr int q4_row_bytes(int D) { return D / 2; }
 __host__ __device__ constexpr long long q4_page_bytes(int bs, int D, int group) {
   return (long long)bs * (D + 8 * (D / group));
 }

@@ -23,7 +23,7 @@
 // then added up in f32.
 //
 // Work.  A unit is (sequence, kv head, up to 64 query rows: query tokens x heads of the kv head), a tile 16
-// to 64 of its keys (4 to 6 KB of codes, scales and zeros).  The tiles of all units stand in one row that is cut
+// to 64 of its keys (4.25 to 5 KB of codes, scales and zeros).  The tiles of all units stand in one row that is cut
 // into equal shares, one a warp (or one for the two or four warps that take a unit's rows, 8 or 16 each): a
 // warp copies its tiles into a ring of its own, 16 bytes a lane at a time (codes and scales of keys and values
 // lie side by side in a page of a head), waits for them and works them off, and nothing of it waits for another
@@ -33,9 +33,9 @@
 // below) is such that the fragments of K by ldmatrix and of V by its transposing byte form meet in one layout and
 // no bank twice.
 //
-// Measured (one GB300): 128 sequences of 2048 to 24,000 keys, 8 kv heads, 32 query heads, D = 128: 334 us for
-// 1.26 GB, 56% of the copy bandwidth.  The copies alone take 215 us, without any matrix product 272 us less 153:
-// the matrix products and what makes their operands share the issue slots and add up, the copies
+// Measured (one GB300): 128 sequences of 2048 to 24,000 keys, 8 kv heads, 64 query heads, D = 128: 334 us for
+// 1.26 GB, 56% of the copy bandwidth.  The copies alone take 215 us, everything but the copies 272, of which 119 are
+// left without the matrix products: these and what makes their operands add up, the copies
 // hide for the most part.  Splitting by CTA with a common ring and producer warps took 515 us, by warp with
 // bulk copies 381 us.
 #include <cuda_fp16.h>
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(Geo<D, NG, ROWS>::THREADS, 1)
           } else if constexpr (PACK) {
             reinterpret_cast<uint2*>(qfrag)[at * 32 + lane] = make_uint2(w.x, w.y);
           } else {
-            qfrag[at * 32 + lane] = w;  // warps of the same rows write the same
+            qfrag[at * 32 + lane] = w;  // read back by this lane alone
           }
         }
       }
@@ -1027,7 +1027,10 @@ void set_rows(Shape& s, long long rows, int of_warp) {
 
 // 16 rows a warp take less work in all, but leave fewer shares with more latency each: they are for many heads
 // with room for long sequences.  D = 128, 16 rows, us with 16 and 8: 512 heads of 2048 to 24,000 keys 283 and 326, 160 of
-// 8500 98 and 109, 800 of 100 to 600 49 and 46, 48 of 1000 to 9000 48 and 41.
+// 8500 98 and 109, 800 of 100 to 600 49 and 46, 48 of 1000 to 9000 48 and 41.  D = 64, groups of 32 and 64 (the first
+// spills 144 bytes with 16 rows): 512 heads of 2048 to 24,000 keys 216 and 245, 174 and 207; 192 of 1000 to 9000 53 and
+// 51, 45 and 45; 800 of 100 to 600 43 and 37, 37 and 34.  The room stands for the lengths, which the host does not
+// know: short sequences in large tables take the longer form.
 void choose_rows(const da_params* p, int q_len, int sms, Shape& s) {
   const long long rows = (long long)q_len * p->num_q_heads / p->num_kv_heads;
   if (rows > 8 && p->head_dim <= 128 && (long long)p->batch * p->num_kv_heads >= sms &&
